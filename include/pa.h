@@ -54,7 +54,7 @@ enum pa_status {
     PA_ERR_INVALID = 1,     /* bad shape, null pointer, misalignment, ... */
     PA_ERR_UNSUPPORTED = 2, /* valid but not built: head_dim, block_size, group size, device */
     PA_ERR_CUDA = 3,        /* a CUDA runtime call failed (launch, copy, malloc) */
-    PA_ERR_WORKSPACE = 4    /* the decode workspace is smaller than the call needs */
+    PA_ERR_WORKSPACE = 4    /* the workspace is smaller than the call needs */
 };
 
 /* Bits that kernels OR into *dev_status. */
@@ -64,7 +64,7 @@ enum pa_device_status {
     PA_DEV_BAD_BLOCK = 4,     /* block_tables entry outside [0, num_blocks) */
     PA_DEV_BAD_LENGTH = 8,    /* cu_seqlens / context_lens inconsistent or too long */
     PA_DEV_TIMEOUT = 16,      /* a bounded wait inside a kernel gave up */
-    PA_DEV_WORKSPACE = 32     /* more decode chunks than the workspace holds */
+    PA_DEV_WORKSPACE = 32     /* the batch needs more than the workspace holds */
 };
 
 /*
@@ -449,6 +449,141 @@ int pa_decode_i8(const void *q, const pa_cache_i8_t *cache, int layer,
                  const int32_t *context_lens, int num_seqs, int n_heads, int n_kv_heads,
                  int head_dim, float scale, void *workspace, size_t workspace_bytes, void *out,
                  int32_t *dev_status, pa_stream_t stream);
+
+/*
+ * A 4-bit KV cache.  The page ("Meta Llama source deep-dive", 8.4) lists
+ * int8 and int4 caches without a scheme; this library's: every (token, KV
+ * head) row of head_dim fp16 values (K after RoPE, V as given) is cut into
+ * groups of 32, and a group x stands in the cache as
+ *     m   = min_i x_i                                        (fp16)
+ *     s   = fl32((max_i x_i - m) / 15) rounded up to fp16    (0 if all equal)
+ *     c_i = clamp(rint(fl32(fl32(x_i - m) / s)), 0, 15)      (ties to even; 0 if s = 0)
+ * which stands for m + s * c_i, within s / 2 of x_i.  A group with a NaN or an
+ * infinity stores s = m = NaN (0x7fff) and c = 0: its 32 values read as NaN.
+ *
+ * Layout: [layers][num_blocks][n_kv_heads][2 (K, V)][tile], a tile being one
+ * block of 16 tokens of one KV head: 8 d bytes of codes, then 32 G fp16
+ * parameters, d = head_dim, G = d / 32; 10 d bytes in all (5 bits a value).
+ * With j the token's row of the block and x = 32 g + y the value's index, the
+ * code is the nibble (low nibble first) number
+ *     K   y % 2  of byte  j d/2 + (y / 8) 4 G + 4 g + (y % 8) / 2
+ *     V   y % 2  of byte  2 (2 (G (4 (8 (j / 8) + y / 4) + (j % 8) / 2) + g) + j % 2)
+ *                         + (y % 4) / 2
+ * and the parameters, counted in fp16 from the end of the codes, are
+ *     s, K and V   place  4 (G ((j % 8) / 2) + g) + 2 (j / 8) + j % 2
+ *     m, K         place  16 G + G j + g
+ *     m, V         place  16 G + (the place of s)
+ * (the order in which the decode kernel's threads take them as tensor-core
+ * operands).  A decode step reads 1.25 d bytes per (token, KV head) instead
+ * of 4 d.
+ */
+typedef struct {
+    uint8_t *base;        /* device pointer to the first tile, 256-byte aligned */
+    int32_t layers;
+    int32_t num_blocks;
+    int32_t block_size;   /* 16 */
+    int32_t n_kv_heads;
+    int32_t head_dim;     /* 64 or 128 */
+    int32_t owns;         /* 1 if pa_alloc_cache_i4 allocated it */
+} pa_cache_i4_t;
+
+/* Bytes of the pool: layers * num_blocks * n_kv_heads * 20 * head_dim
+ * (block_size 16).  0 for non-positive arguments. */
+size_t pa_cache_i4_bytes(int layers, int num_blocks, int block_size, int n_kv_heads,
+                         int head_dim);
+/* As pa_alloc_cache, for the 4-bit pool (device_base 256-byte aligned, at
+ * least pa_cache_i4_bytes(...) bytes, or NULL to allocate). */
+int pa_alloc_cache_i4(pa_cache_i4_t *out, int layers, int num_blocks, int block_size,
+                      int n_kv_heads, int head_dim, void *device_base);
+int pa_free_cache_i4(pa_cache_i4_t *cache);
+
+/*
+ * pa_rope_kv_write into the 4-bit pool: Q is rotated exactly as by
+ * pa_rope_kv_write, and each new token's K (rotated, rounded to fp16) and V
+ * rows are quantised as above into their slot.  K and V are read only: unlike
+ * pa_rope_kv_write, K is not rotated in place (the rotated row would only be
+ * of use in the cache).
+ *   q      device fp16 [num_tokens][n_heads][head_dim]
+ *   q_out  device fp16, the rotated Q: q itself (in place) or a buffer that
+ *          does not overlap q, k or v
+ * Every other argument, the results and the device-side checks are those of
+ * pa_rope_kv_write: a bad position leaves the token's q_out row and slot as
+ * they were.  Two tokens of one call must not share a slot (its codes and
+ * parameters would be a mix of both).
+ */
+int pa_rope_kv_write_i4(const void *q, void *q_out, const void *k, const void *v,
+                        const int32_t *positions, const int32_t *slot_mapping, int num_tokens,
+                        int n_heads, int n_kv_heads, int head_dim, const void *rope_table,
+                        int max_positions, const pa_cache_i4_t *cache, int layer,
+                        int32_t *dev_status, pa_stream_t stream);
+
+/*
+ * Reads rows of the 4-bit pool back as fp16: for every sequence s, its tokens
+ * first_tokens[s] .. first_tokens[s] + lengths[s] - 1, located through
+ * block_tables[s], go to rows row_starts[s] .. of k_out and v_out, as
+ * m + s * c (computed in fp32) rounded to the nearest fp16, saturated at
+ * +-65504 (the step's rounding up can carry a group's top past it).
+ *   block_tables  device int32 [num_seqs][max_blocks_per_seq]
+ *   lengths       device int32 [num_seqs]; 0 reads nothing
+ *   first_tokens  device int32 [num_seqs], or NULL for 0
+ *   row_starts    device int32 [num_seqs]; the sequences' row ranges must not
+ *                 overlap
+ *   k_out, v_out  device fp16 [total_rows][n_kv_heads][head_dim], either of
+ *                 them NULL to leave it out; rows no sequence names stay as
+ *                 they were
+ * A sequence whose length or first token is negative, whose tokens pass
+ * max_blocks_per_seq * 16 or whose rows pass total_rows sets
+ * PA_DEV_BAD_LENGTH and is left out; a block id outside the pool sets
+ * PA_DEV_BAD_BLOCK and its rows stay as they were.  num_seqs <= 4096.
+ * With row_starts multiples of 16 the outputs are the K and V planes of a
+ * one-layer fp16 pool of total_rows / 16 blocks (swapping a sequence out of,
+ * or a prefix into, a pa_cache_t).
+ */
+int pa_kv_read_i4(const pa_cache_i4_t *cache, int layer, const int32_t *block_tables,
+                  int max_blocks_per_seq, const int32_t *lengths, const int32_t *first_tokens,
+                  const int32_t *row_starts, int num_seqs, int total_rows, int n_kv_heads,
+                  int head_dim, void *k_out, void *v_out, int32_t *dev_status,
+                  pa_stream_t stream);
+
+/*
+ * pa_decode against the 4-bit pool, K and V standing for m + s * c.  Scores,
+ * softmax statistics and sums are fp32; each probability is rounded to fp16
+ * once, times its group's step.  Arguments, results and checks are those of
+ * pa_decode except the workspace, whose size is
+ * pa_decode_i4_workspace_bytes(...); it too is 256-byte aligned, zeroed
+ * before its first use, left ready for the next call, and serves one call at
+ * a time (two streams, or two captured graphs that may run together, take
+ * one each).
+ */
+size_t pa_decode_i4_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads, int head_dim);
+int pa_decode_i4(const void *q, const pa_cache_i4_t *cache, int layer,
+                 const int32_t *block_tables, int max_blocks_per_seq,
+                 const int32_t *context_lens, int num_seqs, int n_heads, int n_kv_heads,
+                 int head_dim, float scale, void *workspace, size_t workspace_bytes, void *out,
+                 int32_t *dev_status, pa_stream_t stream);
+
+/*
+ * pa_prefill_varlen against the 4-bit pool: each key and value is the fp16
+ * row that pa_kv_read_i4 gives (for the new tokens too, which must already
+ * have been written by pa_rope_kv_write_i4, so a later decode step sees the
+ * same context).  The rows the batch sees are read back into the workspace
+ * once, as a scratch fp16 pool, and the tensor-core kernel of
+ * pa_prefill_varlen runs over that.
+ *   workspace  device, 256-byte aligned, contents undefined before and after:
+ *              pa_prefill_i4_workspace_bytes(scratch_blocks, ...) bytes, where
+ *              scratch_blocks >= sum_s ceil(L_k(s) / 16); sequences that no
+ *              longer fit set PA_DEV_WORKSPACE and their rows of out are
+ *              undefined.  One call at a time per workspace.
+ * Arguments, results and checks otherwise as pa_prefill_varlen.
+ */
+size_t pa_prefill_i4_workspace_bytes(int scratch_blocks, int num_seqs, int max_blocks_per_seq,
+                                     int n_kv_heads, int head_dim);
+int pa_prefill_varlen_i4(const void *q, int total_q, const pa_cache_i4_t *cache, int layer,
+                         const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                         const int32_t *block_tables, int max_blocks_per_seq, int num_seqs,
+                         int max_seqlen_q, int n_heads, int n_kv_heads, int head_dim, float scale,
+                         void *workspace, size_t workspace_bytes, void *out, int32_t *dev_status,
+                         pa_stream_t stream);
 
 /* Human-readable text of a pa_status code. */
 const char *pa_strerror(int code);

@@ -344,3 +344,119 @@ def attention_decode_i8(q16, codes, scales, layer, block_tables, context_lens,
     codes and scales stand for."""
     return attention_decode(q16, dequantize_cache_i8(codes, scales), layer, block_tables,
                             context_lens, n_heads, n_kv_heads, scale=scale, seqs=seqs)
+
+
+# ---------------------------------------------------------------------------
+# 4-bit KV cache (the quantised cache of "Meta Llama source deep-dive", 8.4;
+# the page gives no scheme, so this is the reading the CUDA path also follows)
+# ---------------------------------------------------------------------------
+#
+# Each (token, KV head) row of head_dim fp16 values (K after the pinned RoPE,
+# V as given) is cut into groups of 32; a group x stands as
+#   m   = min x (fp16),  s = fl32((max x - m) / 15) rounded up to fp16,
+#   c_i = clamp(rint(fl32(fl32(x_i - m) / s)), 0, 15), 0 where s is 0,
+# and reads back as m + s c_i.  A group with a NaN or an infinity stores
+# s = m = NaN (0x7fff) and codes 0.  Tiles: see kv_i4_places.
+
+def kv_quantize_int4(x16):
+    """Rows [..., d] -> codes uint8 [..., d], steps and least values fp16 [..., d/32]."""
+    x = np.asarray(x16, np.float16)
+    x = x.reshape(*x.shape[:-1], -1, 32).astype(np.float32)
+    odd = ~np.isfinite(x).all(axis=-1)
+    x = np.where(odd[..., None], np.float32(0), x)
+    m = x.min(axis=-1) + np.float32(0)  # -0 becomes +0
+    r = (x.max(axis=-1) - m) / np.float32(15.0)
+    s = r.astype(np.float16)
+    s = np.where(s.astype(np.float32) < r, np.nextafter(s, np.float16(np.inf)), s)
+    s32 = s.astype(np.float32)
+    safe = np.where(s32 > 0, s32, np.float32(1))
+    c = np.rint((x - m[..., None]) / safe[..., None])
+    c = np.where(s32[..., None] > 0, np.clip(c, 0, 15), 0).astype(np.uint8)
+    nan = np.uint16(0x7FFF).view(np.float16)
+    s, m = np.where(odd, nan, s), np.where(odd, nan, m.astype(np.float16))
+    return c.reshape(*np.shape(x16)), s.astype(np.float16), m.astype(np.float16)
+
+
+def kv_i4_places(d, is_v):
+    """Where a tile of 16 rows keeps things: (byte, shift) of the code of (row,
+    value) [16, d], and the fp16 index, counted from the end of the 8 d bytes of
+    codes, of the step and the least value of (row, group) [16, d/32]."""
+    G = d // 32
+    byte, shift = np.zeros((16, d), np.int64), np.zeros((16, d), np.int64)
+    step, least = np.zeros((16, G), np.int64), np.zeros((16, G), np.int64)
+    for j in range(16):
+        for g in range(G):
+            step[j, g] = 4 * (G * (j % 8 // 2) + g) + 2 * (j // 8) + j % 2
+            least[j, g] = 16 * G + (step[j, g] if is_v else G * j + g)
+            for y in range(32):
+                if is_v:
+                    unit = G * (4 * (8 * (j // 8) + y // 4) + j % 8 // 2) + g
+                    byte[j, 32 * g + y] = 2 * (2 * unit + j % 2) + y % 4 // 2
+                else:
+                    byte[j, 32 * g + y] = j * d // 2 + y // 8 * 4 * G + 4 * g + y % 8 // 2
+                shift[j, 32 * g + y] = 4 * (y % 2)
+    return byte, shift, step, least
+
+
+def new_cache_i4(layers, num_blocks, n_kv_heads, head_dim):
+    return np.zeros((layers, num_blocks, n_kv_heads, 2, 10 * head_dim), np.uint8)
+
+
+def kv_write_i4(tiles, layer: int, k16, v16, slot_mapping) -> None:
+    """Quantise token t's K and V rows and store them at slot slot_mapping[t]
+    (negative: no write)."""
+    d = tiles.shape[-1] // 10
+    for kv, x in ((0, k16), (1, v16)):
+        byte, shift, step, least = kv_i4_places(d, kv == 1)
+        codes, s, m = kv_quantize_int4(x)
+        for t, slot in enumerate(slot_mapping):
+            slot = int(slot)
+            if slot < 0:
+                continue
+            j = slot % 16
+            for h in range(x.shape[1]):
+                tile = tiles[layer, slot // 16, h, kv]
+                for y in range(d):
+                    keep = 0xF0 if shift[j, y] == 0 else 0x0F
+                    tile[byte[j, y]] = (tile[byte[j, y]] & keep) | (int(codes[t, h, y]) << shift[j, y])
+                params = tile[8 * d:].view(np.float16)
+                params[step[j]], params[least[j]] = s[t, h], m[t, h]
+
+
+def pack_cache_i4(cache16):
+    """The 4-bit form of an fp16 pool [2, L, NB, 16, Hk, d], every row quantised."""
+    two, L, NB, bs, Hk, d = cache16.shape
+    tiles = np.zeros((L, NB, Hk, 2, 10 * d), np.uint8)
+    for kv in (0, 1):
+        byte, shift, step, least = kv_i4_places(d, kv == 1)
+        codes, s, m = kv_quantize_int4(np.swapaxes(cache16[kv], 2, 3))  # [L, NB, Hk, 16, d]
+        packed = np.zeros((L, NB, Hk, 8 * d), np.uint8)
+        for nib in (0, 4):
+            at = shift == nib
+            packed[..., byte[at]] |= codes[..., at] << np.uint8(nib)
+        params = np.zeros((L, NB, Hk, d), np.float16)
+        params[..., step], params[..., least] = s, m
+        tiles[..., kv, :8 * d] = packed
+        tiles[..., kv, 8 * d:] = params.view(np.uint8)
+    return tiles
+
+
+def dequantize_cache_i4(tiles) -> np.ndarray:
+    """The float64 pool [2, L, NB, 16, Hk, d] the tiles stand for: m + s c."""
+    L, NB, Hk, two, n = tiles.shape
+    d = n // 10
+    out = np.empty((2, L, NB, 16, Hk, d))
+    for kv in (0, 1):
+        byte, shift, step, least = kv_i4_places(d, kv == 1)
+        x = np.ascontiguousarray(tiles[..., kv, :])
+        codes = (x[..., byte] >> shift) & 15
+        p = x[..., 8 * d:].view(np.float16).astype(np.float64)
+        val = np.repeat(p[..., least], 32, -1) + np.repeat(p[..., step], 32, -1) * codes
+        out[kv] = np.swapaxes(val, 2, 3)
+    return out
+
+
+def read_rows_i4(values64) -> np.ndarray:
+    """fp16 rows as the library reads them back: the values in float32 (the
+    product is exact, one rounding of the sum), saturated, rounded to fp16."""
+    return np.minimum(values64.astype(np.float32), np.float32(65504)).astype(np.float16)

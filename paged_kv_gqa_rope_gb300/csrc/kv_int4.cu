@@ -1,0 +1,502 @@
+// The 4-bit KV pool ("Meta Llama source deep-dive", 8.4: a quantised KV
+// cache; the scheme is this library's, see include/pa.h): allocation, the
+// RoPE + append kernel that quantises each appended K/V row, and the kernel
+// that reads rows back as fp16.
+#include <string.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+#include "kv_int4.cuh"
+
+namespace pa {
+namespace {
+
+struct RopeI4Args {
+    const __half *q;
+    __half *q_out;
+    const __half *k;
+    const __half *v;
+    const int32_t *positions;
+    const int32_t *slots;
+    const float2 *table;  // [max_pos][d/2] {cos, sin}
+    uint8_t *tiles;       // tile pairs of the layer
+    int64_t num_slots;
+    int32_t *status;
+    int num_tokens, n_heads, n_kv_heads, max_pos;
+};
+
+__device__ __forceinline__ __half2 as_half2(uint32_t w) {
+    return *reinterpret_cast<const __half2 *>(&w);
+}
+__device__ __forceinline__ uint32_t as_u32(__half2 h) {
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// One group's 8 values held by this lane, its other 24 by the lanes of the
+// same aligned quad: the group's step and least value and this lane's codes,
+// value i in nibble i.  Every lane of the warp takes part.
+__device__ __forceinline__ uint32_t quantise8(const uint4 x, __half &step, __half &least) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    // (min, -max) as a pair, reduced together; a NaN or an infinity shows in
+    // the exponent bits, which the minimum of a NaN would not
+    __half2 mm = __hmin2(__hmin2(as_half2(w[0]), as_half2(w[1])),
+                         __hmin2(as_half2(w[2]), as_half2(w[3])));
+    __half2 nx = __hmin2(__hmin2(__hneg2(as_half2(w[0])), __hneg2(as_half2(w[1]))),
+                         __hmin2(__hneg2(as_half2(w[2])), __hneg2(as_half2(w[3]))));
+    __half2 r = __hmin2(__lows2half2(mm, nx), __highs2half2(mm, nx));
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        odd |= (w[i] & 0x7c00u) == 0x7c00u || (w[i] & 0x7c000000u) == 0x7c000000u;
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1)
+        r = __hmin2(r, as_half2(__shfl_xor_sync(0xffffffffu, as_u32(r), o)));
+    const uint32_t quad = 0xfu << (threadIdx.x & 28);
+    odd = (__ballot_sync(0xffffffffu, odd) & quad) != 0;
+    const float lo = __low2float(r) + 0.f;  // (-0 becomes +0)
+    const float range = __fsub_rn(-__high2float(r), lo);
+    step = __float2half_ru(__fdiv_rn(range, 15.f));
+    least = __float2half_rn(lo);
+    if (odd) step = least = __ushort_as_half(0x7fff);
+    const float s = __half2float(step);
+    if (!(s > 0.f)) return 0u;
+    uint32_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __half2 h = as_half2(w[i >> 1]);
+        const float v = (i & 1) ? __high2float(h) : __low2float(h);
+        const int c = __float2int_rn(__fdiv_rn(__fsub_rn(v, lo), s));
+        codes |= (uint32_t)max(0, min(15, c)) << (4 * i);
+    }
+    return codes;
+}
+
+// One thread handles one 16-byte piece (8 fp16 values) of one head row of a
+// token, as in rope_kv_write_kernel; the four threads of a group of 32 (an
+// aligned quad of lanes) find its least and greatest value with shuffles.
+template <int D>
+__global__ void __launch_bounds__(kTokenThreads) rope_kv_write_i4_kernel(const RopeI4Args a) {
+    griddep_launch_dependents();
+    using T = I4Tile<D>;
+    constexpr int kPieces = D / 8;
+    const int H = a.n_heads, Hk = a.n_kv_heads;
+    const int rows = H + 2 * Hk;
+    const int t = (int)(blockIdx.z * gridDim.y + blockIdx.y);
+    if (t >= a.num_tokens) return;  // the whole CTA
+    const int idx = (int)(blockIdx.x * blockDim.x + threadIdx.x);
+    // Threads past the token's last row (whole quads of them) still take part
+    // in the quad's reductions; they read row 0 and write nothing.
+    const bool live = idx < rows * kPieces;
+    const int i = live ? idx : idx % kPieces;
+    const int piece = i % kPieces, row = i / kPieces;
+
+    const int pos = __ldg(a.positions + t);
+    const bool pos_ok = pos >= 0 && pos < a.max_pos;
+    const int slot = __ldg(a.slots + t);
+    if (idx == 0) {
+        if (!pos_ok)
+            report(a.status, PA_DEV_BAD_POSITION);
+        else if (slot >= a.num_slots)
+            report(a.status, PA_DEV_BAD_SLOT);
+    }
+    if (!pos_ok) return;  // the whole CTA
+    const bool write_cache = live && slot >= 0 && slot < a.num_slots;
+
+    uint4 x;
+    if (row < H + Hk) {
+        const bool is_q = row < H;
+        const __half *base = is_q ? a.q + ((int64_t)t * H + row) * D
+                                  : a.k + ((int64_t)t * Hk + (row - H)) * D;
+        const float4 *cs =
+            reinterpret_cast<const float4 *>(a.table + (int64_t)pos * (D / 2) + piece * 4);
+        // (an ordinary load: q_out may be q)
+        x = rope_rotate8(reinterpret_cast<const uint4 *>(base)[piece], __ldg(cs), __ldg(cs + 1));
+        if (is_q && live)
+            reinterpret_cast<uint4 *>(a.q_out + ((int64_t)t * H + row) * D)[piece] = x;
+    } else {
+        x = __ldg(reinterpret_cast<const uint4 *>(a.v + ((int64_t)t * Hk + (row - H - Hk)) * D) +
+                  piece);
+    }
+    __half step, least;
+    const uint32_t codes = quantise8(x, step, least);
+    if (row >= H && write_cache) {
+        const bool is_k = row < H + Hk;
+        const int h = is_k ? row - H : row - H - Hk;
+        const int j = slot % kBlockSize, g = piece >> 2, t8 = piece & 3;
+        uint8_t *tile = a.tiles + ((int64_t)(slot / kBlockSize) * Hk + h) * T::kPair;
+        if (is_k) {
+            *reinterpret_cast<uint32_t *>(tile + T::k_word(j, g, t8)) = codes;
+        } else {
+            tile += T::kBytes;
+            *reinterpret_cast<uint16_t *>(tile + T::v_half(j, g, 2 * t8)) = (uint16_t)codes;
+            *reinterpret_cast<uint16_t *>(tile + T::v_half(j, g, 2 * t8 + 1)) =
+                (uint16_t)(codes >> 16);
+        }
+        if (t8 == 0)
+            *reinterpret_cast<__half *>(tile + T::step(j, g)) = step;
+        else if (t8 == 1)
+            *reinterpret_cast<__half *>(tile + (is_k ? T::least_k(j, g) : T::least_v(j, g))) = least;
+    }
+}
+
+// ---------------------------------------------------------------- read back
+
+constexpr int kReadThreads = 256;
+constexpr int kMaxReadSeqs = 4096;
+constexpr int kMaxPrefillSeqs = 2048;  // pa_prefill_varlen's limit
+
+struct ReadI4Args {
+    const uint8_t *tiles;  // tile pairs of the layer
+    const int32_t *block_tables;
+    const int32_t *lengths;  // rows mode: [B]; scratch mode: cu_seqlens_k [B + 1]
+    const int32_t *first;    // rows mode: [B] or null
+    const int32_t *rows;     // rows mode: [B]
+    __half *k_out;
+    __half *v_out;
+    int32_t *scratch_table;  // scratch mode: [B][maxb]
+    int64_t total_rows;
+    int32_t *status;
+    int B, Hk, maxb, num_blocks;
+};
+
+// 8 codes (nibble i = value i) with their step and least value -> 8 fp16.
+__device__ __forceinline__ uint4 dequantise8(uint32_t codes, float s, float m) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // s * c is exact in fp32 (11 + 4 bits)
+        const float a = __fadd_rn(__fmul_rn(s, (float)((codes >> (8 * i)) & 15u)), m);
+        const float b = __fadd_rn(__fmul_rn(s, (float)((codes >> (8 * i + 4)) & 15u)), m);
+        // saturated from above (m is itself an fp16); a NaN stays one
+        w[i] = pack_half2(a > 65504.f ? 65504.f : a, b > 65504.f ? 65504.f : b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// kScratch false: rows of sequences to the caller's row positions.
+// kScratch true: every sequence's whole context into consecutive blocks of a
+// scratch fp16 pool, with its block table.
+template <int D, bool kScratch>
+__global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const ReadI4Args a) {
+    using T = I4Tile<D>;
+    constexpr int kPieces = D / 8;
+    extern __shared__ int64_t prefix[];  // [B + 1] blocks of the sequences before
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int s = tid; s < a.B; s += kReadThreads) {
+        int64_t n = 0;
+        const int64_t len = kScratch
+                                ? (int64_t)__ldg(a.lengths + s + 1) - __ldg(a.lengths + s)
+                                : (int64_t)__ldg(a.lengths + s);
+        const int64_t f = !kScratch && a.first ? __ldg(a.first + s) : 0;
+        const int64_t r = kScratch ? 0 : __ldg(a.rows + s);
+        const bool ok = len >= 0 && f >= 0 && f + len <= (int64_t)a.maxb * kBlockSize && r >= 0 &&
+                        (kScratch || r + len <= a.total_rows);
+        if (!ok) {
+            // (the prefill kernel reports a bad length of its own)
+            if (!kScratch && blockIdx.x == 0) report(a.status, PA_DEV_BAD_LENGTH);
+        } else if (len > 0) {
+            n = (f % kBlockSize + len + kBlockSize - 1) / kBlockSize;
+        }
+        prefix[s + 1] = n;
+    }
+    if (tid == 0) prefix[0] = 0;
+    __syncthreads();
+    if (tid < 32) {
+        int64_t carry = 0;
+        for (int base = 1; base <= a.B; base += 32) {
+            const int i = base + lane;
+            int64_t v = i <= a.B ? prefix[i] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (i <= a.B) prefix[i] = v + carry;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    __syncthreads();
+    const int64_t units = prefix[a.B];
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        int lo = 0, hi = a.B - 1;  // largest s with prefix[s] <= u
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= u)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int s = lo;
+        const int64_t f = !kScratch && a.first ? __ldg(a.first + s) : 0;
+        const int64_t len = kScratch
+                                ? (int64_t)__ldg(a.lengths + s + 1) - __ldg(a.lengths + s)
+                                : (int64_t)__ldg(a.lengths + s);
+        const int64_t b = f / kBlockSize + (u - prefix[s]);  // logical block
+        const int blk = __ldg(a.block_tables + (int64_t)s * a.maxb + b);
+        const bool blk_ok = blk >= 0 && blk < a.num_blocks;
+        // output row of the block's token 0 (it may lie before the first row)
+        int64_t row0;
+        if constexpr (kScratch) {
+            row0 = u * kBlockSize;
+            const bool fits = row0 + kBlockSize <= a.total_rows;
+            if (tid == 0) {
+                a.scratch_table[(int64_t)s * a.maxb + b] = blk_ok && fits ? (int32_t)u : -1;
+                if (!fits) report(a.status, PA_DEV_WORKSPACE);
+            }
+            if (!fits) continue;
+        } else {
+            row0 = (int64_t)__ldg(a.rows + s) + b * kBlockSize - f;
+        }
+        if (!blk_ok) {
+            if (tid == 0) report(a.status, PA_DEV_BAD_BLOCK);
+            continue;
+        }
+        const int j0 = (int)max((int64_t)0, f - b * kBlockSize);
+        const int j1 = (int)min((int64_t)kBlockSize, f + len - b * kBlockSize);
+        const uint8_t *tiles = a.tiles + (int64_t)blk * a.Hk * T::kPair;
+        for (int i = tid; i < (j1 - j0) * a.Hk * kPieces; i += kReadThreads) {
+            const int piece = i % kPieces, h = i / kPieces % a.Hk, j = j0 + i / kPieces / a.Hk;
+            const int g = piece >> 2, t8 = piece & 3;
+            const int64_t at = ((row0 + j) * a.Hk + h) * D + piece * 8;
+            const uint8_t *kt = tiles + (int64_t)h * T::kPair, *vt = kt + T::kBytes;
+            if (a.k_out) {
+                const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(kt + T::k_word(j, g, t8)));
+                const float st = __half2float(
+                    __ldg(reinterpret_cast<const __half *>(kt + T::step(j, g))));
+                const float m = __half2float(
+                    __ldg(reinterpret_cast<const __half *>(kt + T::least_k(j, g))));
+                *reinterpret_cast<uint4 *>(a.k_out + at) = dequantise8(c, st, m);
+            }
+            if (a.v_out) {
+                const uint32_t c0 = __ldg(
+                    reinterpret_cast<const uint16_t *>(vt + T::v_half(j, g, 2 * t8)));
+                const uint32_t c1 = __ldg(
+                    reinterpret_cast<const uint16_t *>(vt + T::v_half(j, g, 2 * t8 + 1)));
+                const float st = __half2float(
+                    __ldg(reinterpret_cast<const __half *>(vt + T::step(j, g))));
+                const float m = __half2float(
+                    __ldg(reinterpret_cast<const __half *>(vt + T::least_v(j, g))));
+                *reinterpret_cast<uint4 *>(a.v_out + at) = dequantise8(c0 | c1 << 16, st, m);
+            }
+        }
+    }
+}
+
+template <int D, bool kScratch>
+int launch_read(const ReadI4Args &a, cudaStream_t st) {
+    const int sms = sm_count();
+    if (sms < 1) return PA_ERR_CUDA;
+    const size_t smem = (size_t)(a.B + 1) * sizeof(int64_t);
+    kv_read_i4_kernel<D, kScratch><<<sms * 8, kReadThreads, smem, st>>>(a);
+    return launch_status();
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" size_t pa_cache_i4_bytes(int layers, int num_blocks, int block_size, int n_kv_heads,
+                                    int head_dim) {
+    if (layers <= 0 || num_blocks <= 0 || block_size <= 0 || n_kv_heads <= 0 || head_dim <= 0)
+        return 0;
+    // 5 bits a value, K and V
+    return (size_t)layers * num_blocks * block_size * n_kv_heads * head_dim / 4 * 5;
+}
+
+extern "C" int pa_alloc_cache_i4(pa_cache_i4_t *out, int layers, int num_blocks, int block_size,
+                                 int n_kv_heads, int head_dim, void *device_base) {
+    if (!out) return PA_ERR_INVALID;
+    memset(out, 0, sizeof(*out));
+    const size_t bytes = pa_cache_i4_bytes(layers, num_blocks, block_size, n_kv_heads, head_dim);
+    if (bytes == 0) return PA_ERR_INVALID;
+    if ((int64_t)num_blocks * block_size > INT32_MAX) return PA_ERR_INVALID;
+    if (block_size != kBlockSize || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
+    if (device_base && (reinterpret_cast<uintptr_t>(device_base) & 255u)) return PA_ERR_INVALID;
+    void *base = device_base;
+    if (!base) {
+        if (cudaMalloc(&base, bytes) != cudaSuccess) {
+            cudaGetLastError();
+            return PA_ERR_CUDA;
+        }
+        out->owns = 1;
+    }
+    out->base = static_cast<uint8_t *>(base);
+    out->layers = layers;
+    out->num_blocks = num_blocks;
+    out->block_size = block_size;
+    out->n_kv_heads = n_kv_heads;
+    out->head_dim = head_dim;
+    return PA_OK;
+}
+
+extern "C" int pa_free_cache_i4(pa_cache_i4_t *cache) {
+    if (!cache) return PA_ERR_INVALID;
+    int rc = PA_OK;
+    if (cache->owns && cache->base && cudaFree(cache->base) != cudaSuccess) rc = PA_ERR_CUDA;
+    memset(cache, 0, sizeof(*cache));
+    return rc;
+}
+
+extern "C" int pa_rope_kv_write_i4(const void *q, void *q_out, const void *k, const void *v,
+                                   const int32_t *positions, const int32_t *slot_mapping,
+                                   int num_tokens, int n_heads, int n_kv_heads, int head_dim,
+                                   const void *rope_table, int max_positions,
+                                   const pa_cache_i4_t *cache, int layer, int32_t *dev_status,
+                                   pa_stream_t stream) {
+    if (num_tokens < 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0 ||
+        max_positions <= 0)
+        return PA_ERR_INVALID;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (!cache_i4_ok(cache, layer, n_kv_heads, head_dim)) return PA_ERR_INVALID;
+    if (num_tokens == 0) return PA_OK;
+    if (!q || !q_out || !k || !v || !positions || !slot_mapping || !rope_table)
+        return PA_ERR_INVALID;
+    if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) ||
+        !aligned16(rope_table))
+        return PA_ERR_INVALID;
+    if ((int64_t)num_tokens * ((int64_t)n_heads + 2 * (int64_t)n_kv_heads) * (head_dim / 8) >
+        (int64_t)1 << 40)
+        return PA_ERR_INVALID;
+    // q_out is q or lies apart from every input
+    const int64_t qb = (int64_t)num_tokens * n_heads * head_dim * 2;
+    const int64_t kb = (int64_t)num_tokens * n_kv_heads * head_dim * 2;
+    const uintptr_t o = reinterpret_cast<uintptr_t>(q_out);
+    auto apart = [&](const void *p, int64_t n) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(p);
+        return x + (uintptr_t)n <= o || o + (uintptr_t)qb <= x;
+    };
+    if ((q_out != q && !apart(q, qb)) || !apart(k, kb) || !apart(v, kb)) return PA_ERR_INVALID;
+
+    RopeI4Args a;
+    a.q = static_cast<const __half *>(q);
+    a.q_out = static_cast<__half *>(q_out);
+    a.k = static_cast<const __half *>(k);
+    a.v = static_cast<const __half *>(v);
+    a.positions = positions;
+    a.slots = slot_mapping;
+    a.table = static_cast<const float2 *>(rope_table);
+    a.tiles = cache_i4_layer(cache, layer);
+    a.num_slots = (int64_t)cache->num_blocks * kBlockSize;
+    a.status = dev_status;
+    a.num_tokens = num_tokens;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.max_pos = max_positions;
+    const dim3 grid = token_grid(num_tokens, (n_heads + 2 * n_kv_heads) * (head_dim / 8));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (head_dim == 128)
+        rope_kv_write_i4_kernel<128><<<grid, kTokenThreads, 0, st>>>(a);
+    else
+        rope_kv_write_i4_kernel<64><<<grid, kTokenThreads, 0, st>>>(a);
+    return launch_status();
+}
+
+extern "C" int pa_kv_read_i4(const pa_cache_i4_t *cache, int layer, const int32_t *block_tables,
+                             int max_blocks_per_seq, const int32_t *lengths,
+                             const int32_t *first_tokens, const int32_t *row_starts, int num_seqs,
+                             int total_rows, int n_kv_heads, int head_dim, void *k_out,
+                             void *v_out, int32_t *dev_status, pa_stream_t stream) {
+    if (num_seqs < 0 || total_rows < 0 || n_kv_heads <= 0 || max_blocks_per_seq <= 0 ||
+        max_blocks_per_seq > kMaxBlocksPerSeq)
+        return PA_ERR_INVALID;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (num_seqs > kMaxReadSeqs) return PA_ERR_UNSUPPORTED;
+    if (!cache_i4_ok(cache, layer, n_kv_heads, head_dim)) return PA_ERR_INVALID;
+    if (num_seqs == 0) return PA_OK;
+    if (!block_tables || !lengths || !row_starts) return PA_ERR_INVALID;
+    if (!aligned16(k_out) || !aligned16(v_out)) return PA_ERR_INVALID;
+    if (!k_out && !v_out) return PA_OK;
+
+    ReadI4Args a = {};
+    a.tiles = cache_i4_layer(cache, layer);
+    a.block_tables = block_tables;
+    a.lengths = lengths;
+    a.first = first_tokens;
+    a.rows = row_starts;
+    a.k_out = static_cast<__half *>(k_out);
+    a.v_out = static_cast<__half *>(v_out);
+    a.total_rows = total_rows;
+    a.status = dev_status;
+    a.B = num_seqs;
+    a.Hk = n_kv_heads;
+    a.maxb = max_blocks_per_seq;
+    a.num_blocks = cache->num_blocks;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return head_dim == 128 ? launch_read<128, false>(a, st) : launch_read<64, false>(a, st);
+}
+
+// ---------------------------------------------------------------- prefill
+
+namespace pa {
+namespace {
+
+size_t scratch_table_bytes(int num_seqs, int maxb) {
+    return ((size_t)num_seqs * maxb * sizeof(int32_t) + 255) & ~(size_t)255;
+}
+size_t scratch_block_bytes(int Hk, int d) { return (size_t)kBlockSize * Hk * d * 2 * 2; }
+
+}  // namespace
+}  // namespace pa
+
+extern "C" size_t pa_prefill_i4_workspace_bytes(int scratch_blocks, int num_seqs,
+                                                int max_blocks_per_seq, int n_kv_heads,
+                                                int head_dim) {
+    if (scratch_blocks <= 0 || num_seqs <= 0 || max_blocks_per_seq <= 0 || n_kv_heads <= 0 ||
+        head_dim <= 0)
+        return 0;
+    return scratch_table_bytes(num_seqs, max_blocks_per_seq) +
+           (size_t)scratch_blocks * scratch_block_bytes(n_kv_heads, head_dim);
+}
+
+extern "C" int pa_prefill_varlen_i4(const void *q, int total_q, const pa_cache_i4_t *cache,
+                                    int layer, const int32_t *cu_seqlens_q,
+                                    const int32_t *cu_seqlens_k, const int32_t *block_tables,
+                                    int max_blocks_per_seq, int num_seqs, int max_seqlen_q,
+                                    int n_heads, int n_kv_heads, int head_dim, float scale,
+                                    void *workspace, size_t workspace_bytes, void *out,
+                                    int32_t *dev_status, pa_stream_t stream) {
+    if (n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0 || num_seqs < 0 ||
+        total_q < 0 || max_seqlen_q < 0 || max_blocks_per_seq <= 0 ||
+        max_blocks_per_seq > kMaxBlocksPerSeq || !(scale >= 0.f))
+        return PA_ERR_INVALID;
+    if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (num_seqs > kMaxPrefillSeqs) return PA_ERR_UNSUPPORTED;
+    if (!cache_i4_ok(cache, layer, n_kv_heads, head_dim)) return PA_ERR_INVALID;
+    if (num_seqs == 0 || max_seqlen_q == 0 || total_q == 0) return PA_OK;
+    if (!q || !out || !cu_seqlens_q || !cu_seqlens_k || !block_tables || !workspace)
+        return PA_ERR_INVALID;
+    if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return PA_ERR_INVALID;
+    const size_t tab = scratch_table_bytes(num_seqs, max_blocks_per_seq);
+    const size_t per_block = scratch_block_bytes(n_kv_heads, head_dim);
+    if (workspace_bytes < tab + per_block) return PA_ERR_WORKSPACE;
+    size_t blocks = (workspace_bytes - tab) / per_block;
+    if (blocks > (size_t)(INT32_MAX / kBlockSize)) blocks = INT32_MAX / kBlockSize;
+
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    pa_cache_t pool;
+    int rc = pa_alloc_cache(&pool, 1, (int)blocks, kBlockSize, n_kv_heads, head_dim, ws + tab);
+    if (rc != PA_OK) return rc;
+    ReadI4Args a = {};
+    a.tiles = cache_i4_layer(cache, layer);
+    a.block_tables = block_tables;
+    a.lengths = cu_seqlens_k;
+    a.k_out = cache_plane(&pool, 0, 0);
+    a.v_out = cache_plane(&pool, 1, 0);
+    a.scratch_table = reinterpret_cast<int32_t *>(ws);
+    a.total_rows = (int64_t)blocks * kBlockSize;
+    a.status = dev_status;
+    a.B = num_seqs;
+    a.Hk = n_kv_heads;
+    a.maxb = max_blocks_per_seq;
+    a.num_blocks = cache->num_blocks;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    rc = head_dim == 128 ? launch_read<128, true>(a, st) : launch_read<64, true>(a, st);
+    if (rc != PA_OK) return rc;
+    return pa_prefill_varlen(q, total_q, &pool, 0, cu_seqlens_q, cu_seqlens_k,
+                             a.scratch_table, max_blocks_per_seq, num_seqs, max_seqlen_q, n_heads,
+                             n_kv_heads, head_dim, scale, out, dev_status, stream);
+}

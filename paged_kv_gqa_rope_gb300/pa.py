@@ -32,6 +32,9 @@ EXPORTS = (
     "pa_bm_num_tokens", "pa_bm_block_table", "pa_bm_free", "pa_selftest_wait_timeout",
     "pa_cache_i8_bytes", "pa_alloc_cache_i8", "pa_free_cache_i8", "pa_rope_kv_write_i8",
     "pa_decode_i8",
+    "pa_cache_i4_bytes", "pa_alloc_cache_i4", "pa_free_cache_i4", "pa_rope_kv_write_i4",
+    "pa_kv_read_i4", "pa_decode_i4_workspace_bytes", "pa_decode_i4",
+    "pa_prefill_i4_workspace_bytes", "pa_prefill_varlen_i4",
 )
 
 
@@ -48,6 +51,13 @@ class PaCacheI8(ctypes.Structure):
                 ("layers", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
                 ("block_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("owns", ctypes.c_int32)]
+
+
+class PaCacheI4(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("layers", ctypes.c_int32),
+                ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("owns", ctypes.c_int32)]
 
 
 class PAError(RuntimeError):
@@ -111,6 +121,20 @@ _SIGS = {
                                    ctypes.POINTER(PaCacheI8), _i32, _vp, _vp]),
     "pa_decode_i8": (_i32, [_vp, ctypes.POINTER(PaCacheI8), _i32, _vp, _i32, _vp, _i32, _i32,
                             _i32, _i32, ctypes.c_float, _vp, _sz, _vp, _vp, _vp]),
+    "pa_cache_i4_bytes": (_sz, [_i32] * 5),
+    "pa_alloc_cache_i4": (_i32, [ctypes.POINTER(PaCacheI4)] + [_i32] * 5 + [_vp]),
+    "pa_free_cache_i4": (_i32, [ctypes.POINTER(PaCacheI4)]),
+    "pa_rope_kv_write_i4": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp,
+                                   _i32, ctypes.POINTER(PaCacheI4), _i32, _vp, _vp]),
+    "pa_kv_read_i4": (_i32, [ctypes.POINTER(PaCacheI4), _i32, _vp, _i32, _vp, _vp, _vp, _i32,
+                             _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "pa_decode_i4_workspace_bytes": (_sz, [_i32] * 4),
+    "pa_decode_i4": (_i32, [_vp, ctypes.POINTER(PaCacheI4), _i32, _vp, _i32, _vp, _i32, _i32,
+                            _i32, _i32, ctypes.c_float, _vp, _sz, _vp, _vp, _vp]),
+    "pa_prefill_i4_workspace_bytes": (_sz, [_i32] * 5),
+    "pa_prefill_varlen_i4": (_i32, [_vp, _i32, ctypes.POINTER(PaCacheI4), _i32, _vp, _vp, _vp,
+                                    _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _sz,
+                                    _vp, _vp, _vp]),
     "pa_strerror": (ctypes.c_char_p, [_i32]),
     "pa_check_device": (_i32, []),
 }
@@ -565,4 +589,141 @@ def decode_i8(q, cache: CacheI8, block_tables, context_lens, workspace, n_kv_hea
         _p(q), ctypes.byref(cache.desc), layer, _p(block_tables), block_tables.shape[1],
         _p(context_lens), B, H, n_kv_heads, d, float(scale), _p(workspace), workspace.numel(),
         _p(out), _p(status), _stream(stream)))
+    return out
+
+
+class CacheI4:
+    """The 4-bit pool: ``tiles`` uint8 [layers, num_blocks, n_kv_heads, 2 (K, V),
+    10 * head_dim] (the tile's layout is in include/pa.h), a view of ``buffer``,
+    the torch allocation the library wraps.  `buffer` takes a caller's own: a
+    contiguous CUDA uint8 tensor of at least cache_i4_bytes(...) elements,
+    256-byte aligned."""
+
+    def __init__(self, layers, num_blocks, n_kv_heads, head_dim, block_size=16, device="cuda",
+                 buffer=None):
+        self.desc = PaCacheI4()
+        n = cache_i4_bytes(layers, num_blocks, block_size, n_kv_heads, head_dim)
+        if n == 0:
+            raise ValueError("bad 4-bit cache shape")
+        if buffer is None:
+            buffer = torch.empty(n, dtype=torch.uint8, device=device)
+        elif _dev(buffer, torch.uint8, "buffer", (None,)).numel() < n:
+            raise ValueError(f"buffer holds {buffer.numel()} bytes, the pool needs {n}")
+        self.buffer = buffer
+        _check("pa_alloc_cache_i4", lib().pa_alloc_cache_i4(
+            ctypes.byref(self.desc), layers, num_blocks, block_size, n_kv_heads, head_dim,
+            _p(buffer)))
+        self.tiles = buffer[:n].view(layers, num_blocks, n_kv_heads, 2, 10 * head_dim)
+
+
+def cache_i4_bytes(layers, num_blocks, block_size, n_kv_heads, head_dim) -> int:
+    return lib().pa_cache_i4_bytes(layers, num_blocks, block_size, n_kv_heads, head_dim)
+
+
+def _call_on(name, stream, tensors, *args):
+    """lib().<name>(*args, stream) with the tensors' device current, on `stream`
+    or that device's current stream.  All tensors must be on one device."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"{name}: tensors on {dev}, stream on {stream.device}")
+    if dev.index == torch.cuda.current_device():
+        _check(name, getattr(lib(), name)(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(name, getattr(lib(), name)(*args, _stream(stream)))
+
+
+def rope_kv_write_i4(q, k, v, positions, slot_mapping, table, cache: CacheI4, layer=0,
+                     q_out=None, status=None, stream=None):
+    """pa_rope_kv_write_i4: rotates Q (in place, or into `q_out`) and appends the
+    quantised rotated K and V (both left as they are).  Returns the rotated Q."""
+    T, H, Hk, d = _rope_args(q, k, v, positions, slot_mapping, table, status)
+    q_out = q if q_out is None else _out(q_out, q, "q_out")
+    _call_on("pa_rope_kv_write_i4", stream,
+             (q, k, v, positions, slot_mapping, table, cache.buffer, q_out, status),
+             _p(q), _p(q_out), _p(k), _p(v), _p(positions), _p(slot_mapping), T, H, Hk, d,
+             _p(table), table.shape[0], ctypes.byref(cache.desc), layer, _p(status))
+    return q_out
+
+
+def kv_read_i4(cache: CacheI4, block_tables, lengths, row_starts, k_out=None, v_out=None,
+               first_tokens=None, layer=0, status=None, stream=None):
+    """pa_kv_read_i4: tokens first_tokens[s] .. + lengths[s] - 1 of every sequence
+    (from its first token by default) as fp16 into rows row_starts[s] .. of k_out
+    and v_out [rows, n_kv_heads, head_dim] (None: not read).  Returns (k_out, v_out)."""
+    _dev(block_tables, torch.int32, "block_tables", (None, None))
+    B = block_tables.shape[0]
+    _table_width(block_tables)
+    _dev(lengths, torch.int32, "lengths", (B,))
+    _dev(row_starts, torch.int32, "row_starts", (B,))
+    _opt(first_tokens, torch.int32, "first_tokens", (B,))
+    _opt(status, torch.int32, "status", (1,))
+    Hk, d = cache.desc.n_kv_heads, cache.desc.head_dim
+    _opt(k_out, torch.float16, "k_out", (None, Hk, d))
+    _opt(v_out, torch.float16, "v_out", (None, Hk, d))
+    rows = [t.shape[0] for t in (k_out, v_out) if t is not None]
+    if len(rows) == 2 and rows[0] != rows[1]:
+        raise ValueError(f"k_out has {rows[0]} rows, v_out {rows[1]}")
+    total = rows[0] if rows else 0
+    if total > 2**31 - 1:
+        raise ValueError(f"{total} output rows: they must stay within int32")
+    _call_on("pa_kv_read_i4", stream,
+             (block_tables, lengths, row_starts, cache.buffer, k_out, v_out, first_tokens, status),
+             ctypes.byref(cache.desc), layer, _p(block_tables), block_tables.shape[1],
+             _p(lengths), _p(first_tokens), _p(row_starts), B, total, Hk, d, _p(k_out),
+             _p(v_out), _p(status))
+    return k_out, v_out
+
+
+def decode_i4_workspace(num_seqs, n_heads, n_kv_heads, head_dim, device="cuda"):
+    """A zeroed workspace for pa_decode_i4 (its counters must start at zero)."""
+    return torch.zeros(lib().pa_decode_i4_workspace_bytes(num_seqs, n_heads, n_kv_heads, head_dim),
+                       dtype=torch.uint8, device=device)
+
+
+def decode_i4(q, cache: CacheI4, block_tables, context_lens, workspace, n_kv_heads, layer=0,
+              scale=0.0, out=None, status=None, stream=None):
+    B, H, d = _decode_args(q, block_tables, context_lens, workspace, status)
+    out = _out(out, q)
+    _call_on("pa_decode_i4", stream,
+             (q, block_tables, context_lens, workspace, cache.buffer, out, status),
+             _p(q), ctypes.byref(cache.desc), layer, _p(block_tables), block_tables.shape[1],
+             _p(context_lens), B, H, n_kv_heads, d, float(scale), _p(workspace),
+             workspace.numel(), _p(out), _p(status))
+    return out
+
+
+def prefill_i4_workspace(scratch_blocks, num_seqs, max_blocks_per_seq, n_kv_heads, head_dim,
+                         device="cuda"):
+    """A workspace for pa_prefill_varlen_i4 batches whose sequences' contexts
+    take at most `scratch_blocks` blocks of 16 tokens together."""
+    n = lib().pa_prefill_i4_workspace_bytes(scratch_blocks, num_seqs, max_blocks_per_seq,
+                                            n_kv_heads, head_dim)
+    if n == 0:
+        raise ValueError("bad 4-bit prefill workspace shape")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def prefill_varlen_i4(q, cache: CacheI4, cu_seqlens_q, cu_seqlens_k, block_tables, max_seqlen_q,
+                      n_kv_heads, workspace, layer=0, scale=0.0, out=None, status=None,
+                      stream=None):
+    """pa_prefill_varlen_i4: varlen causal prefill over the 4-bit pool."""
+    _dev(q, torch.float16, "q", (None, None, None))
+    T, H, d = q.shape
+    _dev(cu_seqlens_q, torch.int32, "cu_seqlens_q", (None,))
+    B = cu_seqlens_q.shape[0] - 1
+    _dev(cu_seqlens_k, torch.int32, "cu_seqlens_k", (B + 1,))
+    _dev(block_tables, torch.int32, "block_tables", (B, None))
+    _table_width(block_tables)
+    _dev(workspace, torch.uint8, "workspace", (None,))
+    _opt(status, torch.int32, "status", (1,))
+    out = _out(out, q)
+    _call_on("pa_prefill_varlen_i4", stream,
+             (q, cu_seqlens_q, cu_seqlens_k, block_tables, workspace, cache.buffer, out, status),
+             _p(q), T, ctypes.byref(cache.desc), layer, _p(cu_seqlens_q), _p(cu_seqlens_k),
+             _p(block_tables), block_tables.shape[1], B, int(max_seqlen_q), H, n_kv_heads, d,
+             float(scale), _p(workspace), workspace.numel(), _p(out), _p(status))
     return out
