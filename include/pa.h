@@ -459,7 +459,7 @@ int pa_decode_i8(const void *q, const pa_cache_i8_t *cache, int layer,
  *     s   = fl32((max_i x_i - m) / 15) rounded up to fp16    (0 if all equal)
  *     c_i = clamp(rint(fl32(fl32(x_i - m) / s)), 0, 15)      (ties to even; 0 if s = 0)
  * which stands for m + s * c_i, within s / 2 of x_i.  A group with a NaN or an
- * infinity stores s = m = NaN (0x7fff) and c = 0: its 32 values read as NaN.
+ * infinity stores m = NaN (0x7fff), s = 0 and c = 0: its 32 values read as NaN.
  *
  * Layout: [layers][num_blocks][n_kv_heads][2 (K, V)][tile], a tile being one
  * block of 16 tokens of one KV head: 8 d bytes of codes, then 32 G fp16

@@ -356,7 +356,7 @@ def attention_decode_i8(q16, codes, scales, layer, block_tables, context_lens,
 #   m   = min x (fp16),  s = fl32((max x - m) / 15) rounded up to fp16,
 #   c_i = clamp(rint(fl32(fl32(x_i - m) / s)), 0, 15), 0 where s is 0,
 # and reads back as m + s c_i.  A group with a NaN or an infinity stores
-# s = m = NaN (0x7fff) and codes 0.  Tiles: see kv_i4_places.
+# m = NaN (0x7fff), s = 0 and codes 0.  Tiles: see kv_i4_places.
 
 def kv_quantize_int4(x16):
     """Rows [..., d] -> codes uint8 [..., d], steps and least values fp16 [..., d/32]."""
@@ -373,7 +373,7 @@ def kv_quantize_int4(x16):
     c = np.rint((x - m[..., None]) / safe[..., None])
     c = np.where(s32[..., None] > 0, np.clip(c, 0, 15), 0).astype(np.uint8)
     nan = np.uint16(0x7FFF).view(np.float16)
-    s, m = np.where(odd, nan, s), np.where(odd, nan, m.astype(np.float16))
+    s, m = np.where(odd, np.float16(0), s), np.where(odd, nan, m.astype(np.float16))
     return c.reshape(*np.shape(x16)), s.astype(np.float16), m.astype(np.float16)
 
 

@@ -2,10 +2,39 @@
 // pa_cache_i4_t): out = softmax(scale q K^T) V with K and V standing for
 // m + s c.
 //
-// One CTA per (sequence, KV head); its warps take the blocks in turn.  A lane
-// holds one half of one token's K row for the scores of the g heads, then a
-// few columns of O for P V; the running maximum and sum of the softmax are
-// per warp and head, and the warps' results are joined at the end.
+// Work decomposition.  The blocks of all (sequence, KV head) pairs, each pair
+// followed by kPairCost units for its fixed cost, laid end to end, form one
+// line of W units, cut into equal ranges, one per WARP of a persistent grid
+// (one CTA of 16 warps per SM).  A warp streams its range by itself: lane 0
+// brings block tiles (K and V of one KV head, 20 d contiguous bytes: one bulk
+// copy) into the warp's own ring of shared memory, so no warp waits for
+// another until the end.  A pair that lies within one range is finished by
+// its warp; the pieces of a pair cut between warps are joined by the CTA once
+// all its warps are done, and a pair cut between CTAs by the CTA whose record
+// of it arrives last.  Every join sums in the order of the line, so the
+// result does not depend on who arrives when.
+//
+// Arithmetic, on warp-level MMAs (the g heads that share the KV head are the
+// M = 16 rows of Q and the N = 8 columns of P^T, so each code is unpacked once
+// for the whole group):
+//   - A code is used as the fp16 whose low bits it is: c 2^-24 (or 16 c 2^-24
+//     for every other one, taken out of the other operand), exact, for one
+//     logic operation per two codes.
+//   - q k = sum over groups of  s (q . c) + m (sum of q): per group of 32 the
+//     product of fp16 q and codes, scaled in fp32 by s; the second term one
+//     MMA more, with the sums of q as the sum of two fp16.  q enters scaled by
+//     a power of two to [2^9, 2^10), so nothing of it underflows.
+//   - p v = sum over keys of  (p s)(c - 8) + p (m + 8 s): p s is rounded to
+//     fp16 once (the one rounding of this kernel that shows, as P's in the
+//     fp16 kernel); c - 8 rather than c, and the centre rather than the least
+//     value, keep both terms as small as the values themselves, so the
+//     rounding is not magnified by their cancelling.  c - 8 is the product
+//     with c and, from the same rounded operand, 8 times its sum (one MMA a
+//     group, row g of one accumulator tile).
+//   - The running maximum is raised only when a score passes it by kLazy
+//     (in log2), so P <= 2^kLazy and O is rarely rescaled.
+#include <mutex>
+
 #include "common.cuh"
 #include "internal.h"
 #include "kv_int4.cuh"
@@ -14,111 +43,731 @@ namespace pa {
 namespace {
 
 constexpr int kMaxSeqs = 4096;
-constexpr int kGroupPad = 8;
-constexpr int kWarps = 8;
+constexpr int kGroupPad = 8;  // Q heads per KV head, padded
+constexpr int kWarps = 16;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxGrid = 152;  // CTAs the workspace has records for
+constexpr int kPairCost = 2;   // units of the line for a pair's fixed cost
+constexpr int kMinUnits = 4;   // least units of a warp's range
+constexpr int kSeqStep = 4;    // sequences per entry of the prefix table
+constexpr float kLazy = 2.f;
+constexpr float kNoMax = -1e30f;  // running maximum before the first score
+
+template <int D>
+constexpr int kRing = D == 128 ? 5 : 10;  // block tiles in a warp's ring
 
 struct DecodeI4Args {
-    const __half *q;
-    const uint8_t *tiles;
-    const int32_t *block_tables;
-    const int32_t *context_lens;
-    __half *out;
+    const __half *q;              // [B][H][D]
+    const uint8_t *tiles;         // tile pairs of the layer
+    const int32_t *block_tables;  // [B][maxb]
+    const int32_t *context_lens;  // [B]
+    __half *out;                  // [B][H][D]
+    int32_t *counters;            // [B][Hk] arrivals (zero between calls)
+    float *rec;                   // [grid][2][8][D + 2] O, then max, sum
+    float *lead;                  // [grid][kWarps][8][D] O of a warp's first piece
     int32_t *status;
-    float scale_log2;
+    float scale_log2;             // scale * log2(e)
     int B, H, Hk, g, maxb, num_blocks;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) decode_i4_kernel(const DecodeI4Args a) {
-    using T = I4Tile<D>;
-    constexpr int kCols = D / 32;
-    __shared__ float sm_q[kGroupPad][D];
-    __shared__ float sm_o[kWarps][kGroupPad][D];
-    __shared__ float sm_m[kWarps][kGroupPad], sm_l[kWarps][kGroupPad];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int kvh = blockIdx.x % a.Hk, s = blockIdx.x / a.Hk;
-    const int ctx = __ldg(a.context_lens + s);
-    if (ctx < 1 || ctx > a.maxb * kBlockSize) {
-        if (tid == 0 && kvh == 0) report(a.status, PA_DEV_BAD_LENGTH);
-        return;
+__device__ __forceinline__ int blocks_of(int ctx, int maxb) {
+    return ctx >= 1 && ctx <= maxb * kBlockSize ? (ctx + kBlockSize - 1) / kBlockSize : 0;
+}
+
+// A pair on the line: its blocks are the units [start, start + nblk).
+struct Pair {
+    int64_t start;
+    int s, kvh, nblk, ctx;
+
+    __device__ __forceinline__ void load(const DecodeI4Args &a) {
+        ctx = __ldg(a.context_lens + s);
+        nblk = blocks_of(ctx, a.maxb);
     }
-    for (int i = tid; i < a.g * D; i += kWarps * 32)
-        sm_q[i / D][i % D] =
-            __half2float(a.q[((int64_t)s * a.H + kvh * a.g) * D + i]) * a.scale_log2;
-    __syncthreads();
-    float m[kGroupPad], l[kGroupPad], o[kGroupPad][kCols];
-    for (int h = 0; h < kGroupPad; ++h) {
-        m[h] = -INFINITY;
-        l[h] = 0.f;
-        for (int c = 0; c < kCols; ++c) o[h][c] = 0.f;
-    }
-    const int nblk = (ctx + kBlockSize - 1) / kBlockSize;
-    const int j = lane & 15, half = lane >> 4;
-    for (int b = warp; b < nblk; b += kWarps) {
-        const int blk = __ldg(a.block_tables + (int64_t)s * a.maxb + b);
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (lane == 0) report(a.status, PA_DEV_BAD_BLOCK);
-            continue;
+    // The pair that holds unit pos (pos < W): prefix[i] = units before sequence kSeqStep i.
+    __device__ __forceinline__ void find(int64_t pos, const int64_t *prefix,
+                                         const DecodeI4Args &a) {
+        int lo = 0, hi = (a.B - 1) / kSeqStep;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= pos)
+                lo = mid;
+            else
+                hi = mid - 1;
         }
-        const uint8_t *kt = a.tiles + ((int64_t)blk * a.Hk + kvh) * T::kPair, *vt = kt + T::kBytes;
-        const bool live = b * kBlockSize + j < ctx;
-        float x[kGroupPad] = {};
-        for (int gr = half * (T::kGroups / 2); gr < (half + 1) * (T::kGroups / 2); ++gr) {
-            const float st = __half2float(*(const __half *)(kt + T::step(j, gr)));
-            const float ls = __half2float(*(const __half *)(kt + T::least_k(j, gr)));
-            for (int t = 0; t < 4; ++t) {
-                const uint32_t w = *(const uint32_t *)(kt + T::k_word(j, gr, t));
-                for (int i = 0; i < 8; ++i) {
-                    const float k = ls + st * (float)((w >> (4 * i)) & 15u);
-                    for (int h = 0; h < a.g; ++h) x[h] += k * sm_q[h][32 * gr + 8 * t + i];
+        start = prefix[lo];
+        s = lo * kSeqStep;
+        while (true) {
+            load(a);
+            const int64_t n = nblk ? (int64_t)(nblk + kPairCost) * a.Hk : 0;
+            if (pos < start + n) break;
+            start += n;
+            ++s;
+        }
+        kvh = (int)((pos - start) / (nblk + kPairCost));
+        start += (int64_t)kvh * (nblk + kPairCost);
+    }
+    // The next pair; only called while it starts before W.
+    __device__ __forceinline__ void next(const DecodeI4Args &a) {
+        start += nblk + kPairCost;
+        if (++kvh < a.Hk) return;
+        kvh = 0;
+        do {
+            ++s;
+            load(a);
+        } while (nblk == 0);
+    }
+};
+
+// Cuts of the line: the first unit of range w of A, and the range that holds a unit.
+__device__ __forceinline__ int64_t range_start(int64_t W, int w, int A) { return W * w / A; }
+__device__ __forceinline__ int range_of(int64_t unit, int64_t W, int A) {
+    return (int)(((unit + 1) * A + W - 1) / W) - 1;
+}
+
+__device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void *src, uint32_t bytes,
+                                               uint64_t *bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(pol)
+        : "memory");
+}
+
+// D(16x8, f32) += A(16x8, f16, row) * B(8x8, f16, col); rows 8-15 of A are zero.
+__device__ __forceinline__ void mma_1688_top(float (&c)[4], uint32_t a0, uint32_t b0) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6},"
+        " {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(0u), "r"(b0));
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// The two fp16 of a word as a pair of fp32.
+__device__ __forceinline__ uint64_t f2_of_half2(uint32_t w) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return f2_pack(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t half2_of_f2(uint64_t v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return pack_half2(lo, hi);
+}
+
+// G consecutive words (G = 4 or 2), 4 G-byte aligned.
+template <int G>
+__device__ __forceinline__ void ld_words(uint32_t (&w)[G], uint32_t addr) {
+    if constexpr (G == 4) {
+        const uint4 x = ld_shared_v4(addr);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else {
+        const uint2 x = ld_shared_v2(addr);
+        w[0] = x.x, w[1] = x.y;
+    }
+}
+
+// One warp's state of the softmax over the keys it has seen of one pair.
+// Lane = 4 r + t (r = 0..7, t = 0..3).  Head r: m, l (this lane's keys only)
+// and the Q fragments; heads 2 t, 2 t + 1: the accumulators of O^T, rows
+// (values of V) 32 grp + 4 r + n:
+//   o[2 grp][0..1] n = 0, [2..3] n = 1; o[2 grp + 1][0..1] n = 2, [2..3] n = 3,
+// in units of 2^-24 (n even) and 2^-20 (n odd), and row grp of z: what every
+// value of group grp gets on top.
+template <int D>
+struct State {
+    static constexpr int G = D / 32;
+    uint32_t qa[2 * G][2];  // A fragments of Q, two k steps a group (rows 0-7; 8-15 are zero)
+    uint32_t qsum;          // A fragment of the groups' sums of q, high and low parts
+    float qs;               // scores -> log2 units
+    float m, l;
+    float o[2 * G][4], z[4];
+
+    __device__ __forceinline__ void begin(const DecodeI4Args &a, const Pair &p, int lane) {
+        const int r = lane >> 2, t = lane & 3;
+        uint4 x[G];
+        const uint4 *row = reinterpret_cast<const uint4 *>(
+            a.q + ((int64_t)p.s * a.H + p.kvh * a.g + (r < a.g ? r : 0)) * D);
+        __half2 big = __float2half2_rn(0.f);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            x[i] = r < a.g ? row[4 * i + t] : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                big = __hmax2(big, __habs2(*reinterpret_cast<const __half2 *>(&w[k])));
+        }
+        float amax = fmaxf(__low2float(big), __high2float(big));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // 2^(9 - floor(log2 amax)) and its inverse
+        const int e = __float_as_int(amax) >> 23;
+        const bool fine = amax > 0.f && amax <= 65504.f;
+        const float up = fine ? __int_as_float((263 - e) << 23) : 1.f;
+        qs = a.scale_log2 * 0x1p24f * (fine ? __int_as_float((e - 9) << 23) : 1.f);
+        float sum[G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+                f[2 * k] = y.x * up;
+                f[2 * k + 1] = y.y * up;
+            }
+            // codes 0, 4 | 2, 6 at weight 1; codes 1, 5 | 3, 7 at weight 16
+            qa[2 * i][0] = pack_half2(f[0], f[4]);
+            qa[2 * i][1] = pack_half2(f[2], f[6]);
+            qa[2 * i + 1][0] = pack_half2(f[1] * 0.0625f, f[5] * 0.0625f);
+            qa[2 * i + 1][1] = pack_half2(f[3] * 0.0625f, f[7] * 0.0625f);
+            sum[i] = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+        }
+        // k = 0 .. G - 1 the high parts, G .. 2 G - 1 the low parts
+        qsum = 0;
+#pragma unroll
+        for (int i = 0; i < G; i += 2) {
+            const __half h0 = __float2half_rn(sum[i]), h1 = __float2half_rn(sum[i + 1]);
+            const __half2 hi = __halves2half2(h0, h1);
+            if (t == i / 2) qsum = *reinterpret_cast<const uint32_t *>(&hi);
+            if (t == (G + i) / 2)
+                qsum = pack_half2(sum[i] - __half2float(h0), sum[i + 1] - __half2float(h1));
+        }
+        m = kNoMax;
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        z[0] = z[1] = z[2] = z[3] = 0.f;
+    }
+
+    // NB consecutive blocks: their tile pairs at addr[i] in shared memory and
+    // the number of tokens of each that count (16, less in the pair's last
+    // block, 0 for a block that was not loaded).
+    template <int NB>
+    __device__ __forceinline__ void blocks(const uint32_t (&addr)[NB], const int (&valid)[NB],
+                                           int lane) {
+        const int r = lane >> 2, t = lane & 3;
+        using T = I4Tile<D>;
+        // scores of head r, keys 8 h + 2 t and + 1 of each block
+        uint64_t x[NB][2];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const uint32_t par = addr[i] + T::kCodes;
+            uint32_t st[2][G];  // steps: [.][2 grp % G + half]: groups 0..G/2-1, then the rest
+            ld_words<G>(st[0], par + t * (8 * G));
+            ld_words<G>(st[1], par + t * (8 * G) + 4 * G);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int j = 8 * h + r;
+                uint32_t w[G];
+                ld_words<G>(w, addr[i] + j * (D / 2) + t * (4 * G));
+                const uint32_t ls = ld_shared_u32(par + 2 * (16 * G + G * j) +
+                                                  (G == 4 ? (t & 1) * 4 : 0));
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_1688_top(c, qsum, ls);
+                uint64_t acc = f2_pack(c[0] * 0x1p-24f, c[1] * 0x1p-24f);
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) {
+                    const uint32_t v = w[gr], u = v >> 8;
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint32_t a0[4] = {qa[2 * gr][0], 0u, qa[2 * gr][1], 0u};
+                    const uint32_t a1[4] = {qa[2 * gr + 1][0], 0u, qa[2 * gr + 1][1], 0u};
+                    mma_16816(d, a0, v & 0x000f000fu, u & 0x000f000fu);
+                    mma_16816(d, a1, v & 0x00f000f0u, u & 0x00f000f0u);
+                    const uint32_t sw = st[gr / (G / 2)][2 * (gr % (G / 2)) + h];
+                    acc = f2_fma(f2_pack(d[0], d[1]), f2_of_half2(sw), acc);
+                }
+                x[i][h] = f2_mul(acc, f2_pack(qs, qs));
+            }
+            if (valid[i] < kBlockSize) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float lo, hi;
+                    f2_unpack(x[i][h], lo, hi);
+                    if (8 * h + 2 * t >= valid[i]) lo = -INFINITY;
+                    if (8 * h + 2 * t + 1 >= valid[i]) hi = -INFINITY;
+                    x[i][h] = f2_pack(lo, hi);
                 }
             }
         }
-        for (int h = 0; h < a.g; ++h) {
-            x[h] += __shfl_xor_sync(0xffffffffu, x[h], 16);
-            if (!live) x[h] = -INFINITY;
-            float bm = x[h];
-            for (int f = 8; f >= 1; f >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, f));
-            const float mn = fmaxf(m[h], bm), al = ex2(m[h] - mn);
-            m[h] = mn;
-            x[h] = ex2(x[h] - mn);
-            l[h] = l[h] * al + (half == 0 ? x[h] : 0.f);
-            for (int c = 0; c < kCols; ++c) o[h][c] *= al;
+        float top = -INFINITY;
+        float y[NB][4];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            f2_unpack(x[i][0], y[i][0], y[i][1]);
+            f2_unpack(x[i][1], y[i][2], y[i][3]);
+            top = fmaxf(fmax3(top, y[i][0], y[i][1]), fmaxf(y[i][2], y[i][3]));
         }
-        for (int t = 0; t < kBlockSize && b * kBlockSize + t < ctx; ++t) {
-            float v[kCols];
-            for (int c = 0; c < kCols; ++c) {  // columns 32 c + lane
-                const float st = __half2float(*(const __half *)(vt + T::step(t, c)));
-                const float ls = __half2float(*(const __half *)(vt + T::least_v(t, c)));
-                const uint32_t w = *(const uint16_t *)(vt + T::v_half(t, c, lane >> 2));
-                v[c] = ls + st * (float)((w >> (4 * (lane & 3))) & 15u);
+        if (__any_sync(0xffffffffu, top > m + kLazy)) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float n = top > m + kLazy ? top : m;
+            const float f = ex2(m - n);
+            m = n;
+            l *= f;
+            const float f0 = __shfl_sync(0xffffffffu, f, 8 * t);
+            const float f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+#pragma unroll
+            for (int k = 0; k < 2 * G; ++k) {
+                o[k][0] *= f0;
+                o[k][1] *= f1;
+                o[k][2] *= f0;
+                o[k][3] *= f1;
             }
-            for (int h = 0; h < a.g; ++h) {
-                const float p = __shfl_sync(0xffffffffu, x[h], t);
-                for (int c = 0; c < kCols; ++c) o[h][c] += p * v[c];
+            z[0] *= f0;
+            z[1] *= f1;
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const uint32_t vt = addr[i] + T::kBytes, par = vt + T::kCodes;
+            float p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[k] = ex2(y[i][k] - m);
+            l += (p[0] + p[1]) + (p[2] + p[3]);
+            uint32_t st[2][G];
+            ld_words<G>(st[0], par + t * (8 * G));
+            ld_words<G>(st[1], par + t * (8 * G) + 4 * G);
+            // row r % G of the centre's operand: m + 8 s of keys 2 t, + 1, + 8, + 9
+            const int row = 8 * (G * t + (r & (G - 1)));
+            const uint2 ls = ld_shared_v2(par + 32 * G + row), ss = ld_shared_v2(par + row);
+            const __half2 eight = __float2half2_rn(8.f);
+            const __half2 z0 = __hfma2(*reinterpret_cast<const __half2 *>(&ss.x), eight,
+                                       *reinterpret_cast<const __half2 *>(&ls.x));
+            const __half2 z1 = __hfma2(*reinterpret_cast<const __half2 *>(&ss.y), eight,
+                                       *reinterpret_cast<const __half2 *>(&ls.y));
+            uint32_t za[4] = {*reinterpret_cast<const uint32_t *>(&z0), 0u,
+                              *reinterpret_cast<const uint32_t *>(&z1), 0u};
+            uint32_t w0[G], w1[G];  // word grp: keys 2 t (low half), 2 t + 1; then + 8
+            ld_words<G>(w0, vt + lane * (4 * G));
+            ld_words<G>(w1, vt + lane * (4 * G) + 4 * D);
+            if (valid[i] < kBlockSize) {
+                // parameters of tokens that do not count may be anything, NaN included
+                const uint32_t k0 = (2 * t < valid[i] ? 0x0000ffffu : 0u) |
+                                    (2 * t + 1 < valid[i] ? 0xffff0000u : 0u);
+                const uint32_t k1 = (2 * t + 8 < valid[i] ? 0x0000ffffu : 0u) |
+                                    (2 * t + 9 < valid[i] ? 0xffff0000u : 0u);
+#pragma unroll
+                for (int k = 0; k < G; ++k) {
+                    st[0][k] &= (k & 1) ? k1 : k0;
+                    st[1][k] &= (k & 1) ? k1 : k0;
+                }
+                za[0] &= k0;
+                za[2] &= k1;
+            }
+            mma_16816(z, za, pack_half2(p[0], p[1]), pack_half2(p[2], p[3]));
+            const uint64_t p01 = f2_pack(p[0], p[1]), p23 = f2_pack(p[2], p[3]);
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                const uint32_t *sw = &st[gr / (G / 2)][2 * (gr % (G / 2))];
+                const uint32_t b0 = half2_of_f2(f2_mul(p01, f2_of_half2(sw[0])));
+                const uint32_t b1 = half2_of_f2(f2_mul(p23, f2_of_half2(sw[1])));
+                const uint32_t u0 = w0[gr] >> 8, u1 = w1[gr] >> 8;
+                const uint32_t a0[4] = {w0[gr] & 0x000f000fu, w0[gr] & 0x00f000f0u,
+                                        w1[gr] & 0x000f000fu, w1[gr] & 0x00f000f0u};
+                const uint32_t a1[4] = {u0 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x000f000fu,
+                                        u1 & 0x00f000f0u};
+                mma_16816(o[2 * gr], a0, b0, b1);
+                mma_16816(o[2 * gr + 1], a1, b0, b1);
+                const uint32_t e = r == gr ? 0xc800c800u : 0u;  // -8 in row gr
+                const uint32_t ea[4] = {e, 0u, e, 0u};
+                mma_16816(z, ea, b0, b1);
             }
         }
     }
-    for (int h = 0; h < a.g; ++h) {
-        for (int f = 16; f >= 1; f >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], f);
-        if (lane == 0) {
-            sm_m[warp][h] = m[h];
-            sm_l[warp][h] = l[h];
+
+    // l over all keys; O of heads 2 t + (0, 1): v[grp][head][n], values 32 grp + 4 r + n.
+    __device__ __forceinline__ void end(float (&v)[G][2][4], int lane) {
+        const int t = lane & 3;
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float zz = __shfl_sync(0xffffffffu, z[h], 4 * gr + t);
+                v[gr][h][0] = fmaf(o[2 * gr][h], 0x1p24f, zz);
+                v[gr][h][1] = fmaf(o[2 * gr][2 + h], 0x1p20f, zz);
+                v[gr][h][2] = fmaf(o[2 * gr + 1][h], 0x1p24f, zz);
+                v[gr][h][3] = fmaf(o[2 * gr + 1][2 + h], 0x1p20f, zz);
+            }
         }
-        for (int c = 0; c < kCols; ++c) sm_o[warp][h][32 * c + lane] = o[h][c];
+    }
+};
+
+// What a warp leaves of a pair that it does not finish by itself.
+struct Piece {
+    int64_t start;  // the pair's first unit; -1: none
+    int s, kvh, nblk, pad;
+};
+
+template <int D>
+struct Smem {
+    alignas(128) uint8_t ring[kWarps][kRing<D>][20 * D];
+    uint64_t full[kWarps][kRing<D>];
+    float m[2 * kWarps][kGroupPad], l[2 * kWarps][kGroupPad];
+    Piece piece[2 * kWarps];  // 2 w: the warp's first, begun by another; 2 w + 1: its last
+    int last[2];
+    int64_t prefix[kMaxSeqs / kSeqStep + 1];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Args a) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
+    constexpr int R = kRing<D>, G = D / 32;
+    static_assert(sizeof(sm.ring[0]) >= kGroupPad * D * sizeof(float), "a piece's O fits the ring");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = blockIdx.x;
+
+    // -------- units of every kSeqStep sequences and their prefix sums
+    const int entries = (a.B + kSeqStep - 1) / kSeqStep;
+    for (int i = tid; i < entries; i += kThreads) {
+        int64_t n = 0;
+        for (int s = i * kSeqStep; s < min(a.B, (i + 1) * kSeqStep); ++s) {
+            const int nblk = blocks_of(__ldg(a.context_lens + s), a.maxb);
+            if (nblk)
+                n += (int64_t)(nblk + kPairCost) * a.Hk;
+            else if (cta == 0)
+                report(a.status, PA_DEV_BAD_LENGTH);
+        }
+        sm.prefix[i + 1] = n;
+    }
+    if (tid < 2 * kWarps) sm.piece[tid].start = -1;
+    if (lane < R) mbar_init(&sm.full[warp][lane], 1);
+    if (tid == 0) sm.prefix[0] = 0;
+    fence_barrier_init();
+    __syncthreads();
+    if (warp == 0) {
+        int64_t carry = 0;
+        for (int base = 1; base <= entries; base += 32) {
+            const int i = base + lane;
+            int64_t v = i <= entries ? sm.prefix[i] : 0;
+#pragma unroll
+            for (int f = 1; f < 32; f <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, v, f);
+                if (lane >= f) v += u;
+            }
+            if (i <= entries) sm.prefix[i] = v + carry;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
     }
     __syncthreads();
-    for (int i = tid; i < a.g * D; i += kWarps * 32) {
-        const int h = i / D, d = i % D;
-        float M = -INFINITY, L = 0.f, O = 0.f;
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][h]);
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = M == -INFINITY ? 0.f : ex2(sm_m[w][h] - M);
-            L += f * sm_l[w][h];
-            O += f * sm_o[w][h][d];
+    // Everything above read only call metadata; Q and the pool may still be
+    // being written by the kernel before this one.
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t W = sm.prefix[entries];
+    if (W == 0) return;
+    const int A = (int)min((int64_t)gridDim.x * kWarps, (W + kMinUnits - 1) / kMinUnits);
+    if (cta * kWarps >= A) return;
+    const int me = cta * kWarps + warp;
+
+    if (me < A) {
+        const int64_t begin = range_start(W, me, A), end = range_start(W, me + 1, A);
+        const uint64_t pol = [] {
+            uint64_t p;
+            asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+            return p;
+        }();
+        Pair cur;  // the pair being attended to
+        cur.find(begin, sm.prefix, a);
+        Pair nxt = cur;               // the pair being loaded
+        int64_t nxt_pos = begin;      // its first unit in the range
+        int ib = 0, ie = 0;           // its next block to load, and the end of them
+        int chunk = 0;                // block of lane 0's entry
+        int entry = 0, entry2 = 0;    // block ids chunk + lane, chunk + 32 + lane
+        bool more = true;
+        uint32_t phase = 0, loaded = 0;  // per ring slot: parity to wait for; a copy was issued
+        bool dead = false;               // a wait gave up
+        int put = 0, get = 0;            // ring slots
+
+        auto open = [&]() {  // blocks of nxt in [nxt_pos, end)
+            ib = (int)min((int64_t)nxt.nblk, nxt_pos - nxt.start);
+            ie = (int)min((int64_t)nxt.nblk, end - nxt.start);
+            chunk = ib;
+            const int32_t *row = a.block_tables + (int64_t)nxt.s * a.maxb;
+            entry = ib + lane < ie ? __ldg(row + ib + lane) : 0;
+            entry2 = ib + 32 + lane < ie ? __ldg(row + ib + 32 + lane) : 0;
+        };
+        auto issue = [&]() {  // the next block of the range into slot `put`
+            while (more && ib >= ie) {
+                nxt_pos = nxt.start + nxt.nblk + kPairCost;
+                if (nxt_pos >= end) {
+                    more = false;
+                } else {
+                    nxt.next(a);
+                    open();
+                }
+            }
+            if (!more) return;
+            if (ib == chunk + 32) {
+                chunk = ib;
+                entry = entry2;
+                entry2 = ib + 32 + lane < ie
+                             ? __ldg(a.block_tables + (int64_t)nxt.s * a.maxb + ib + 32 + lane)
+                             : 0;
+            }
+            const int blk = __shfl_sync(0xffffffffu, entry, ib - chunk);
+            const bool ok = blk >= 0 && blk < a.num_blocks && !dead;
+            if (ok) {
+                loaded |= 1u << put;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sm.full[warp][put], 20 * D);
+                    bulk_load_hint(smem_u32(sm.ring[warp][put]),
+                                   a.tiles + ((int64_t)blk * a.Hk + nxt.kvh) * (20 * D), 20 * D,
+                                   &sm.full[warp][put], pol);
+                }
+            } else {
+                loaded &= ~(1u << put);
+                if (!dead && lane == 0) report(a.status, PA_DEV_BAD_BLOCK);
+            }
+            ++ib;
+            put = put + 1 == R ? 0 : put + 1;
+        };
+        // Waits for slot `get`; whether it holds a block.
+        auto take = [&]() -> bool {
+            const uint32_t bit = 1u << get;
+            bool ok = (loaded & bit) != 0;
+            if (ok) {
+                ok = mbar_wait(&sm.full[warp][get], (phase & bit) != 0);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    // counted as empty from here on; the copies in flight are
+                    // waited for at the end
+                    if (lane == 0) report(a.status, PA_DEV_TIMEOUT);
+                    dead = true;
+                } else {
+                    phase ^= bit;
+                    loaded &= ~bit;
+                }
+            }
+            get = get + 1 == R ? 0 : get + 1;
+            return ok;
+        };
+
+        open();
+        for (int i = 0; i < R; ++i) issue();
+        State<D> st;
+        for (int64_t pos = begin; pos < end;) {
+            const int b0 = (int)min((int64_t)cur.nblk, pos - cur.start);
+            const int b1 = (int)min((int64_t)cur.nblk, end - cur.start);
+            if (b0 < b1) {
+                st.begin(a, cur, lane);
+                int b = b0;
+                for (; b + 2 <= b1; b += 2) {
+                    const uint32_t at0 = smem_u32(sm.ring[warp][get]);
+                    const bool ok0 = !dead && take();
+                    const uint32_t at1 = smem_u32(sm.ring[warp][get]);
+                    const bool ok1 = !dead && take();
+                    const uint32_t addr[2] = {at0, at1};
+                    const int valid[2] = {ok0 ? kBlockSize : 0,
+                                          ok1 ? min(kBlockSize, cur.ctx - (b + 1) * kBlockSize) : 0};
+                    st.template blocks<2>(addr, valid, lane);
+                    __syncwarp();  // every lane has read the two slots
+                    if (!dead) {
+                        issue();
+                        issue();
+                    }
+                }
+                if (b < b1) {
+                    const uint32_t addr[1] = {smem_u32(sm.ring[warp][get])};
+                    const bool ok = !dead && take();
+                    const int valid[1] = {ok ? min(kBlockSize, cur.ctx - b * kBlockSize) : 0};
+                    st.template blocks<1>(addr, valid, lane);
+                    __syncwarp();
+                    if (!dead) issue();
+                }
+                float v[G][2][4];
+                st.end(v, lane);
+                const int r = lane >> 2, t = lane & 3;
+                if (b0 == 0 && b1 == cur.nblk) {  // the whole pair
+                    const float l0 = __shfl_sync(0xffffffffu, st.l, 8 * t);
+                    const float l1 = __shfl_sync(0xffffffffu, st.l, 8 * t + 4);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float l = h ? l1 : l0;
+                        const float inv = l != 0.f ? 1.f / l : 0.f;
+                        if (2 * t + h < a.g) {
+                            __half *row = a.out + ((int64_t)cur.s * a.H + cur.kvh * a.g + 2 * t + h) * D;
+#pragma unroll
+                            for (int gr = 0; gr < G; ++gr)
+                                *reinterpret_cast<uint2 *>(row + 32 * gr + 4 * r) =
+                                    make_uint2(pack_half2(v[gr][h][0] * inv, v[gr][h][1] * inv),
+                                               pack_half2(v[gr][h][2] * inv, v[gr][h][3] * inv));
+                        }
+                    }
+                } else {
+                    // A pair that ends in this range leaves its O in the
+                    // workspace (the ring still streams); one that goes on, the
+                    // warp's last, in the ring, which is empty by then.
+                    const int k = b1 == cur.nblk ? 0 : 1;
+                    float *dst = k == 0 ? a.lead + (int64_t)me * kGroupPad * D
+                                        : reinterpret_cast<float *>(sm.ring[warp]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (2 * t + h < a.g)
+#pragma unroll
+                            for (int gr = 0; gr < G; ++gr)
+                                *reinterpret_cast<float4 *>(dst + (2 * t + h) * D + 32 * gr + 4 * r) =
+                                    make_float4(v[gr][h][0], v[gr][h][1], v[gr][h][2], v[gr][h][3]);
+                    if (t == 0) {
+                        sm.m[2 * warp + k][r] = st.m;
+                        sm.l[2 * warp + k][r] = st.l;
+                    }
+                    if (lane == 0) {
+                        Piece &p = sm.piece[2 * warp + k];
+                        p.start = cur.start;
+                        p.s = cur.s;
+                        p.kvh = cur.kvh;
+                        p.nblk = cur.nblk;
+                    }
+                }
+            }
+            pos = cur.start + cur.nblk + kPairCost;
+            if (pos < end) cur.next(a);
         }
-        a.out[((int64_t)s * a.H + kvh * a.g) * D + i] = __float2half_rn(L > 0.f ? O / L : 0.f);
+        if (dead)  // leave no copy in flight
+            for (int i = 0; i < R; ++i)
+                if (loaded >> i & 1) mbar_wait(&sm.full[warp][i], (phase >> i) & 1);
     }
+    __syncthreads();
+
+    // -------- pairs cut between warps, in the order of the line
+    const int c0 = cta * kWarps, c1 = min(A, c0 + kWarps);
+    const int64_t cta_begin = range_start(W, c0, A), cta_end = range_start(W, c1, A);
+    constexpr int kRec = D + 2;
+    auto record = [&](int c, int slot, int h) -> float * {
+        return a.rec + (((int64_t)c * 2 + slot) * kGroupPad + h) * kRec;
+    };
+    int cut[2] = {-1, -1};  // pieces that name the pairs cut between CTAs, by record slot
+    for (int i = 0; i < 2 * kWarps;) {
+        const Piece p = sm.piece[i];
+        if (p.start < 0) {
+            ++i;
+            continue;
+        }
+        int e = i + 1;
+        while (e < 2 * kWarps && (sm.piece[e].start < 0 || sm.piece[e].start == p.start)) ++e;
+        const bool whole = p.start >= cta_begin && p.start + p.nblk <= cta_end;
+        const int slot = p.start < cta_begin ? 0 : 1;
+        if (!whole) cut[slot] = i;
+        for (int x = tid; x < a.g * D; x += kThreads) {
+            const int h = x / D, d = x - h * D;
+            float M = kNoMax;
+            for (int k = i; k < e; ++k)
+                if (sm.piece[k].start >= 0) M = fmaxf(M, sm.m[k][h]);
+            float L = 0.f, O = 0.f;
+            for (int k = i; k < e; ++k) {
+                if (sm.piece[k].start < 0) continue;
+                const float f = ex2(sm.m[k][h] - M);
+                const float v = (k & 1)
+                                    ? reinterpret_cast<const float *>(sm.ring[k >> 1])[x]
+                                    : __ldcg(a.lead + (int64_t)(c0 + (k >> 1)) * kGroupPad * D + x);
+                L = __fmaf_rn(f, sm.l[k][h], L);
+                O = __fmaf_rn(f, v, O);
+            }
+            if (whole) {
+                a.out[((int64_t)p.s * a.H + p.kvh * a.g) * D + x] =
+                    __float2half_rn(L != 0.f ? O / L : 0.f);
+            } else {
+                float *rec = record(cta, slot, h);
+                rec[d] = O;
+                if (d == 0) {
+                    rec[D] = M;
+                    rec[D + 1] = L;
+                }
+            }
+        }
+        i = e;
+    }
+    if (cut[0] < 0 && cut[1] < 0) return;  // the same for every thread
+    // -------- pairs cut between CTAs: the last of their records to arrive joins them
+    __syncthreads();
+    if (lane == 0 && warp < 2) {
+        int last = 0;
+        if (cut[warp] >= 0) {
+            const Piece p = sm.piece[cut[warp]];
+            const int first = range_of(p.start, W, A) / kWarps;
+            const int n = range_of(p.start + p.nblk - 1, W, A) / kWarps - first + 1;
+            __threadfence();
+            last = atomicAdd(a.counters + p.s * a.Hk + p.kvh, 1) == n - 1;
+            if (last) __threadfence();
+        }
+        sm.last[warp] = last;
+    }
+    __syncthreads();
+    for (int slot = 0; slot < 2; ++slot) {
+        if (!sm.last[slot]) continue;
+        const Piece p = sm.piece[cut[slot]];
+        const int first = range_of(p.start, W, A) / kWarps;
+        const int n = range_of(p.start + p.nblk - 1, W, A) / kWarps - first + 1;
+        for (int x = tid; x < a.g * D; x += kThreads) {
+            const int h = x / D, d = x - h * D;
+            // only the pair's first CTA holds it as its last (slot 1)
+            const int64_t fb = range_start(W, first * kWarps, A);
+            const int s0 = p.start < fb ? 0 : 1;
+            float M = kNoMax;
+            for (int k = 0; k < n; ++k) M = fmaxf(M, __ldcg(record(first + k, k ? 0 : s0, h) + D));
+            float L = 0.f, O = 0.f;
+#pragma unroll 4
+            for (int k = 0; k < n; ++k) {
+                const float *rec = record(first + k, k ? 0 : s0, h);
+                const float f = ex2(__ldcg(rec + D) - M);
+                L = __fmaf_rn(f, __ldcg(rec + D + 1), L);
+                O = __fmaf_rn(f, __ldcg(rec + d), O);
+            }
+            a.out[((int64_t)p.s * a.H + p.kvh * a.g) * D + x] =
+                __float2half_rn(L != 0.f ? O / L : 0.f);
+        }
+        if (tid == 0) a.counters[p.s * a.Hk + p.kvh] = 0;
+    }
+}
+
+size_t counters_bytes(int B, int Hk) {
+    return ((size_t)B * Hk * sizeof(int32_t) + 255) & ~(size_t)255;
+}
+size_t records_bytes(int D) {
+    return ((size_t)kMaxGrid * 2 * kGroupPad * (D + 2) * sizeof(float) + 255) & ~(size_t)255;
+}
+
+template <int D>
+int launch_decode_i4(const DecodeI4Args &a, cudaStream_t st) {
+    constexpr size_t smem = sizeof(Smem<D>);
+    static std::mutex mu;
+    static bool attr_set[64] = {false};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PA_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!attr_set[dev]) {
+            if (cudaFuncSetAttribute(decode_i4_kernel<D>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)smem) != cudaSuccess) {
+                cudaGetLastError();
+                return PA_ERR_CUDA;
+            }
+            attr_set[dev] = true;
+        }
+    }
+    // One CTA per SM, fewer when the tables' width bounds the work below that.
+    const int64_t most = (int64_t)a.B * a.Hk * ((int64_t)a.maxb + kPairCost);
+    const int64_t ctas = (most + kMinUnits * kWarps - 1) / (kMinUnits * kWarps);
+    int grid = sm_count();
+    if (grid > kMaxGrid) grid = kMaxGrid;
+    if (grid > ctas) grid = (int)ctas;
+    if (grid < 1) return PA_ERR_CUDA;
+    launch_dependent(decode_i4_kernel<D>, dim3(grid), dim3(kThreads), smem, st, a);
+    return launch_status();
 }
 
 }  // namespace
@@ -129,7 +778,8 @@ using namespace pa;
 extern "C" size_t pa_decode_i4_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads,
                                                int head_dim) {
     if (num_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0) return 0;
-    return 256;
+    return counters_bytes(num_seqs, n_kv_heads) + records_bytes(head_dim) +
+           (size_t)kMaxGrid * kWarps * kGroupPad * head_dim * sizeof(float);
 }
 
 extern "C" int pa_decode_i4(const void *q, const pa_cache_i4_t *cache, int layer,
@@ -157,6 +807,11 @@ extern "C" int pa_decode_i4(const void *q, const pa_cache_i4_t *cache, int layer
     a.block_tables = block_tables;
     a.context_lens = context_lens;
     a.out = static_cast<__half *>(out);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.counters = reinterpret_cast<int32_t *>(ws);
+    ws += counters_bytes(num_seqs, n_kv_heads);
+    a.rec = reinterpret_cast<float *>(ws);
+    a.lead = reinterpret_cast<float *>(ws + records_bytes(head_dim));
     a.status = dev_status;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.B = num_seqs;
@@ -166,9 +821,5 @@ extern "C" int pa_decode_i4(const void *q, const pa_cache_i4_t *cache, int layer
     a.maxb = max_blocks_per_seq;
     a.num_blocks = cache->num_blocks;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (head_dim == 128)
-        decode_i4_kernel<128><<<num_seqs * n_kv_heads, kWarps * 32, 0, st>>>(a);
-    else
-        decode_i4_kernel<64><<<num_seqs * n_kv_heads, kWarps * 32, 0, st>>>(a);
-    return launch_status();
+    return head_dim == 128 ? launch_decode_i4<128>(a, st) : launch_decode_i4<64>(a, st);
 }

@@ -59,7 +59,10 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 x, __half &step, __hal
     const float range = __fsub_rn(-__high2float(r), lo);
     step = __float2half_ru(__fdiv_rn(range, 15.f));
     least = __float2half_rn(lo);
-    if (odd) step = least = __ushort_as_half(0x7fff);
+    if (odd) {
+        step = __ushort_as_half(0);
+        least = __ushort_as_half(0x7fff);
+    }
     const float s = __half2float(step);
     if (!(s > 0.f)) return 0u;
     uint32_t codes = 0;

@@ -361,7 +361,7 @@ def test_decode_nan_stays_in_its_group():
     q, tiles, bt, ctx = decode_case(36, 8, 2, 128, [100, 100])
     _, _, step, least = orc.kv_i4_places(128, True)
     v = tiles[0, bt[0, 2], 1, 1, 8 * 128:].view(np.float16)
-    v[step[5, 2]] = v[least[5, 2]] = np.nan
+    v[step[5, 2]], v[least[5, 2]] = 0, np.nan
     got = run_decode(q, tiles, bt, ctx, 2).float().cpu().numpy()
     nan = np.zeros((2, 8, 128), bool)
     nan[0, 4:, 64:96] = True

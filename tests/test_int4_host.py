@@ -39,8 +39,8 @@ def test_constant_and_non_finite_groups():
     x[2, 3] = np.nan
     c, s, m = orc.kv_quantize_int4(x)
     assert (c == 0).all() and s[0].tolist() == [0, 0] and m[0].tolist() == [5, 5]
-    assert np.isnan(s[1, 1]) and np.isnan(m[1, 1]) and s[1, 0] == 0
-    assert np.isnan(s[2, 0]) and np.isnan(m[2, 0]) and m[2, 1] == 5
+    assert s[1, 1] == 0 and np.isnan(m[1, 1]) and m[1, 0] == 5
+    assert s[2, 0] == 0 and np.isnan(m[2, 0]) and m[2, 1] == 5
     x = np.zeros((1, 32), np.float16)
     x[0, :2] = [-65504, 65504]  # the widest range: the step is finite, the top saturates
     c, s, m = orc.kv_quantize_int4(x)
