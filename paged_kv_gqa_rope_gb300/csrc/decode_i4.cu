@@ -44,7 +44,7 @@ namespace {
 
 constexpr int kMaxSeqs = 4096;
 constexpr int kGroupPad = 8;  // Q heads per KV head, padded
-constexpr int kWarps = 16;
+constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxGrid = 152;  // CTAs the workspace has records for
 constexpr int kPairCost = 2;   // units of the line for a pair's fixed cost
@@ -54,7 +54,7 @@ constexpr float kLazy = 2.f;
 constexpr float kNoMax = -1e30f;  // running maximum before the first score
 
 template <int D>
-constexpr int kRing = D == 128 ? 5 : 10;  // block tiles in a warp's ring
+constexpr int kStages = D == 128 ? 3 : 6;  // stages of a warp's ring, two blocks each
 
 struct DecodeI4Args {
     const __half *q;              // [B][H][D]
@@ -63,7 +63,7 @@ struct DecodeI4Args {
     const int32_t *context_lens;  // [B]
     __half *out;                  // [B][H][D]
     int32_t *counters;            // [B][Hk] arrivals (zero between calls)
-    float *rec;                   // [grid][2][8][D + 2] O, then max, sum
+    float *rec;                   // [grid][2][8][D + 4] O, then max, sum
     float *lead;                  // [grid][kWarps][8][D] O of a warp's first piece
     int32_t *status;
     float scale_log2;             // scale * log2(e)
@@ -83,19 +83,12 @@ struct Pair {
         ctx = __ldg(a.context_lens + s);
         nblk = blocks_of(ctx, a.maxb);
     }
-    // The pair that holds unit pos (pos < W): prefix[i] = units before sequence kSeqStep i.
-    __device__ __forceinline__ void find(int64_t pos, const int64_t *prefix,
+    // The pair that holds unit pos: `first`, at most kSeqStep sequences, starts
+    // at unit `from` <= pos and holds it.
+    __device__ __forceinline__ void find(int64_t pos, int first, int64_t from,
                                          const DecodeI4Args &a) {
-        int lo = 0, hi = (a.B - 1) / kSeqStep;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (prefix[mid] <= pos)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        start = prefix[lo];
-        s = lo * kSeqStep;
+        start = from;
+        s = first;
         while (true) {
             load(a);
             const int64_t n = nblk ? (int64_t)(nblk + kPairCost) * a.Hk : 0;
@@ -133,13 +126,23 @@ __device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void *src, ui
         : "memory");
 }
 
-// D(16x8, f32) += A(16x8, f16, row) * B(8x8, f16, col); rows 8-15 of A are zero.
-__device__ __forceinline__ void mma_1688_top(float (&c)[4], uint32_t a0, uint32_t b0) {
+// D(16x8, f32) = A(16x8, f16, row) * B(8x8, f16, col)
+__device__ __forceinline__ void mma_1688_zero(float (&d)[4], uint32_t a0, uint32_t a1,
+                                              uint32_t b0) {
     asm volatile(
         "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6},"
-        " {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(0u), "r"(b0));
+        " {%7, %7, %7, %7};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+}
+// D(16x8, f32) = A(16x16, f16, row) * B(16x8, f16, col)
+__device__ __forceinline__ void mma_16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+        " {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
@@ -180,16 +183,20 @@ __device__ __forceinline__ void ld_words(uint32_t (&w)[G], uint32_t addr) {
 // and the Q fragments; heads 2 t, 2 t + 1: the accumulators of O^T, rows
 // (values of V) 32 grp + 4 r + n:
 //   o[2 grp][0..1] n = 0, [2..3] n = 1; o[2 grp + 1][0..1] n = 2, [2..3] n = 3,
-// in units of 2^-24 (n even) and 2^-20 (n odd), and row grp of z: what every
-// value of group grp gets on top.
+// in units of 2^-24 (n even) and 2^-20 (n odd); row grp of z: the sum of p times
+// the centre of group grp; e[grp]: -8 times the sum of its p s.
 template <int D>
 struct State {
     static constexpr int G = D / 32;
-    uint32_t qa[2 * G][2];  // A fragments of Q, two k steps a group (rows 0-7; 8-15 are zero)
+    // A fragments of Q: rows 0-7 are the heads with a group's codes of weight 1,
+    // rows 8-15 the heads with its codes of weight 16 (each multiplied by both
+    // kinds of codes; half of either product is not used)
+    uint32_t qa[G][4];
     uint32_t qsum;          // A fragment of the groups' sums of q, high and low parts
     float qs;               // scores -> log2 units
     float m, l;
     float o[2 * G][4], z[4];
+    uint64_t e[G];
 
     __device__ __forceinline__ void begin(const DecodeI4Args &a, const Pair &p, int lane) {
         const int r = lane >> 2, t = lane & 3;
@@ -209,10 +216,10 @@ struct State {
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         // 2^(9 - floor(log2 amax)) and its inverse
-        const int e = __float_as_int(amax) >> 23;
+        const int ex = __float_as_int(amax) >> 23;
         const bool fine = amax > 0.f && amax <= 65504.f;
-        const float up = fine ? __int_as_float((263 - e) << 23) : 1.f;
-        qs = a.scale_log2 * 0x1p24f * (fine ? __int_as_float((e - 9) << 23) : 1.f);
+        const float up = fine ? __int_as_float((263 - ex) << 23) : 1.f;
+        qs = a.scale_log2 * 0x1p24f * (fine ? __int_as_float((ex - 9) << 23) : 1.f);
         float sum[G];
 #pragma unroll
         for (int i = 0; i < G; ++i) {
@@ -225,10 +232,10 @@ struct State {
                 f[2 * k + 1] = y.y * up;
             }
             // codes 0, 4 | 2, 6 at weight 1; codes 1, 5 | 3, 7 at weight 16
-            qa[2 * i][0] = pack_half2(f[0], f[4]);
-            qa[2 * i][1] = pack_half2(f[2], f[6]);
-            qa[2 * i + 1][0] = pack_half2(f[1] * 0.0625f, f[5] * 0.0625f);
-            qa[2 * i + 1][1] = pack_half2(f[3] * 0.0625f, f[7] * 0.0625f);
+            qa[i][0] = pack_half2(f[0], f[4]);
+            qa[i][2] = pack_half2(f[2], f[6]);
+            qa[i][1] = pack_half2(f[1] * 0.0625f, f[5] * 0.0625f);
+            qa[i][3] = pack_half2(f[3] * 0.0625f, f[7] * 0.0625f);
             sum[i] = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
             sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
             sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
@@ -248,22 +255,23 @@ struct State {
 #pragma unroll
         for (int i = 0; i < 2 * G; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         z[0] = z[1] = z[2] = z[3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < G; ++i) e[i] = f2_pack(0.f, 0.f);
     }
 
-    // NB consecutive blocks: their tile pairs at addr[i] in shared memory and
-    // the number of tokens of each that count (16, less in the pair's last
-    // block, 0 for a block that was not loaded).
-    template <int NB>
-    __device__ __forceinline__ void blocks(const uint32_t (&addr)[NB], const int (&valid)[NB],
-                                           int lane) {
+    // NB consecutive blocks, their tile pairs at addr[i] in shared memory.  With
+    // kTail, only the first `valid` tokens of the (one) block count.
+    template <int NB, bool kTail>
+    __device__ __forceinline__ void blocks(const uint32_t (&addr)[NB], int valid, int lane) {
+        static_assert(NB == 1 || !kTail, "");
         const int r = lane >> 2, t = lane & 3;
         using T = I4Tile<D>;
         // scores of head r, keys 8 h + 2 t and + 1 of each block
-        uint64_t x[NB][2];
+        float y[NB][4];
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             const uint32_t par = addr[i] + T::kCodes;
-            uint32_t st[2][G];  // steps: [.][2 grp % G + half]: groups 0..G/2-1, then the rest
+            uint32_t st[2][G];  // steps: word 2 grp + h of the two
             ld_words<G>(st[0], par + t * (8 * G));
             ld_words<G>(st[1], par + t * (8 * G) + 4 * G);
 #pragma unroll
@@ -273,41 +281,31 @@ struct State {
                 ld_words<G>(w, addr[i] + j * (D / 2) + t * (4 * G));
                 const uint32_t ls = ld_shared_u32(par + 2 * (16 * G + G * j) +
                                                   (G == 4 ? (t & 1) * 4 : 0));
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_1688_top(c, qsum, ls);
-                uint64_t acc = f2_pack(c[0] * 0x1p-24f, c[1] * 0x1p-24f);
+                float c[4];
+                mma_1688_zero(c, qsum, qsum, ls);
+                uint64_t acc = f2_mul(f2_pack(c[0], c[1]), f2_pack(0x1p-24f, 0x1p-24f));
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr) {
                     const uint32_t v = w[gr], u = v >> 8;
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    const uint32_t a0[4] = {qa[2 * gr][0], 0u, qa[2 * gr][1], 0u};
-                    const uint32_t a1[4] = {qa[2 * gr + 1][0], 0u, qa[2 * gr + 1][1], 0u};
-                    mma_16816(d, a0, v & 0x000f000fu, u & 0x000f000fu);
-                    mma_16816(d, a1, v & 0x00f000f0u, u & 0x00f000f0u);
-                    const uint32_t sw = st[gr / (G / 2)][2 * (gr % (G / 2)) + h];
-                    acc = f2_fma(f2_pack(d[0], d[1]), f2_of_half2(sw), acc);
+                    float d0[4], d1[4];
+                    mma_16816_zero(d0, qa[gr], v & 0x000f000fu, u & 0x000f000fu);
+                    mma_16816_zero(d1, qa[gr], v & 0x00f000f0u, u & 0x00f000f0u);
+                    const uint64_t sw = f2_of_half2(st[gr / (G / 2)][2 * (gr % (G / 2)) + h]);
+                    acc = f2_fma(f2_pack(d0[0], d0[1]), sw, acc);
+                    acc = f2_fma(f2_pack(d1[2], d1[3]), sw, acc);
                 }
-                x[i][h] = f2_mul(acc, f2_pack(qs, qs));
+                f2_unpack(f2_mul(acc, f2_pack(qs, qs)), y[i][2 * h], y[i][2 * h + 1]);
             }
-            if (valid[i] < kBlockSize) {
+            if (kTail) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float lo, hi;
-                    f2_unpack(x[i][h], lo, hi);
-                    if (8 * h + 2 * t >= valid[i]) lo = -INFINITY;
-                    if (8 * h + 2 * t + 1 >= valid[i]) hi = -INFINITY;
-                    x[i][h] = f2_pack(lo, hi);
-                }
+                for (int k = 0; k < 4; ++k)
+                    if (8 * (k >> 1) + 2 * t + (k & 1) >= valid) y[i][k] = -INFINITY;
             }
         }
         float top = -INFINITY;
-        float y[NB][4];
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            f2_unpack(x[i][0], y[i][0], y[i][1]);
-            f2_unpack(x[i][1], y[i][2], y[i][3]);
-            top = fmaxf(fmax3(top, y[i][0], y[i][1]), fmaxf(y[i][2], y[i][3]));
-        }
+        for (int i = 0; i < NB; ++i)
+            top = fmax3(fmax3(top, y[i][0], y[i][1]), y[i][2], y[i][3]);
         if (__any_sync(0xffffffffu, top > m + kLazy)) {
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -326,6 +324,8 @@ struct State {
             }
             z[0] *= f0;
             z[1] *= f1;
+#pragma unroll
+            for (int k = 0; k < G; ++k) e[k] = f2_mul(e[k], f2_pack(f0, f1));
         }
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
@@ -345,27 +345,31 @@ struct State {
                                        *reinterpret_cast<const __half2 *>(&ls.x));
             const __half2 z1 = __hfma2(*reinterpret_cast<const __half2 *>(&ss.y), eight,
                                        *reinterpret_cast<const __half2 *>(&ls.y));
-            uint32_t za[4] = {*reinterpret_cast<const uint32_t *>(&z0), 0u,
-                              *reinterpret_cast<const uint32_t *>(&z1), 0u};
+            uint32_t za[2] = {*reinterpret_cast<const uint32_t *>(&z0),
+                              *reinterpret_cast<const uint32_t *>(&z1)};
             uint32_t w0[G], w1[G];  // word grp: keys 2 t (low half), 2 t + 1; then + 8
             ld_words<G>(w0, vt + lane * (4 * G));
             ld_words<G>(w1, vt + lane * (4 * G) + 4 * D);
-            if (valid[i] < kBlockSize) {
+            if (kTail) {
                 // parameters of tokens that do not count may be anything, NaN included
-                const uint32_t k0 = (2 * t < valid[i] ? 0x0000ffffu : 0u) |
-                                    (2 * t + 1 < valid[i] ? 0xffff0000u : 0u);
-                const uint32_t k1 = (2 * t + 8 < valid[i] ? 0x0000ffffu : 0u) |
-                                    (2 * t + 9 < valid[i] ? 0xffff0000u : 0u);
+                const uint32_t k0 = (2 * t < valid ? 0x0000ffffu : 0u) |
+                                    (2 * t + 1 < valid ? 0xffff0000u : 0u);
+                const uint32_t k1 = (2 * t + 8 < valid ? 0x0000ffffu : 0u) |
+                                    (2 * t + 9 < valid ? 0xffff0000u : 0u);
 #pragma unroll
                 for (int k = 0; k < G; ++k) {
                     st[0][k] &= (k & 1) ? k1 : k0;
                     st[1][k] &= (k & 1) ? k1 : k0;
                 }
                 za[0] &= k0;
-                za[2] &= k1;
+                za[1] &= k1;
             }
-            mma_16816(z, za, pack_half2(p[0], p[1]), pack_half2(p[2], p[3]));
+            {  // (rows 8-15 of the operand and of z are not used)
+                const uint32_t a4[4] = {za[0], za[0], za[1], za[1]};
+                mma_16816(z, a4, pack_half2(p[0], p[1]), pack_half2(p[2], p[3]));
+            }
             const uint64_t p01 = f2_pack(p[0], p[1]), p23 = f2_pack(p[2], p[3]);
+            const uint32_t eights[4] = {0xc800c800u, 0xc800c800u, 0xc800c800u, 0xc800c800u};
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
                 const uint32_t *sw = &st[gr / (G / 2)][2 * (gr % (G / 2))];
@@ -378,9 +382,9 @@ struct State {
                                         u1 & 0x00f000f0u};
                 mma_16816(o[2 * gr], a0, b0, b1);
                 mma_16816(o[2 * gr + 1], a1, b0, b1);
-                const uint32_t e = r == gr ? 0xc800c800u : 0u;  // -8 in row gr
-                const uint32_t ea[4] = {e, 0u, e, 0u};
-                mma_16816(z, ea, b0, b1);
+                float d[4];
+                mma_16816_zero(d, eights, b0, b1);
+                e[gr] = f2_add(e[gr], f2_pack(d[0], d[1]));
             }
         }
     }
@@ -392,9 +396,11 @@ struct State {
         l += __shfl_xor_sync(0xffffffffu, l, 2);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
+            float es[2];
+            f2_unpack(e[gr], es[0], es[1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float zz = __shfl_sync(0xffffffffu, z[h], 4 * gr + t);
+                const float zz = __shfl_sync(0xffffffffu, z[h], 4 * gr + t) + es[h];
                 v[gr][h][0] = fmaf(o[2 * gr][h], 0x1p24f, zz);
                 v[gr][h][1] = fmaf(o[2 * gr][2 + h], 0x1p20f, zz);
                 v[gr][h][2] = fmaf(o[2 * gr + 1][h], 0x1p24f, zz);
@@ -406,67 +412,175 @@ struct State {
 
 // What a warp leaves of a pair that it does not finish by itself.
 struct Piece {
-    int64_t start;  // the pair's first unit; -1: none
+    int64_t start;  // the pair's first unit; negative (its own for each piece): none
     int s, kvh, nblk, pad;
 };
 
 template <int D>
 struct Smem {
-    alignas(128) uint8_t ring[kWarps][kRing<D>][20 * D];
-    uint64_t full[kWarps][kRing<D>];
+    alignas(128) uint8_t ring[kWarps][kStages<D>][2 * 20 * D];
+    uint64_t full[kWarps][kStages<D>];
     float m[2 * kWarps][kGroupPad], l[2 * kWarps][kGroupPad];
     Piece piece[2 * kWarps];  // 2 w: the warp's first, begun by another; 2 w + 1: its last
-    int last[2];
+    int flag[4];              // per record slot: this CTA closes the pair; was the last to arrive
     int64_t prefix[kMaxSeqs / kSeqStep + 1];
 };
+
+// A row (one head) of partial results: D / 32 columns a lane, from column lane D / 32.
+template <int D>
+struct Row {
+    static constexpr int N = D / 32;
+    float o[N], m, l;
+
+    __device__ __forceinline__ void add(float f, const float (&v)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = __fmaf_rn(f, v[i], o[i]);
+    }
+    __device__ __forceinline__ void store_out(__half *row, int lane) const {
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        if constexpr (N == 4)
+            *reinterpret_cast<uint2 *>(row + lane * 4) =
+                make_uint2(pack_half2(o[0] * inv, o[1] * inv), pack_half2(o[2] * inv, o[3] * inv));
+        else
+            *reinterpret_cast<uint32_t *>(row + lane * 2) = pack_half2(o[0] * inv, o[1] * inv);
+    }
+};
+// N consecutive floats that another CTA or warp may have written.
+template <int N>
+__device__ __forceinline__ void load_cols(float (&v)[N], const float *p) {
+    if constexpr (N == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4 *>(p));
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2 *>(p));
+        v[0] = x.x, v[1] = x.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_cols(float *p, const float (&v)[N]) {
+    if constexpr (N == 4)
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+        *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int f = 16; f; f >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, f));
+    return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int f = 16; f; f >>= 1) x += __shfl_xor_sync(0xffffffffu, x, f);
+    return x;
+}
+
+// One head's row of a pair cut between CTAs first .. first + n - 1, from their
+// records; the row of CTA first + own (none if own < 0) is `mine` instead.
+template <int D>
+__device__ __forceinline__ Row<D> join_records(const DecodeI4Args &a, int first, int n, int h,
+                                               int own, const Row<D> &mine, int lane) {
+    constexpr int N = Row<D>::N;
+    // the first CTA holds the pair as its last (slot 1), the others as their first
+    auto rec = [&](int k) {
+        return a.rec + (((int64_t)(first + k) * 2 + (k == 0)) * kGroupPad + h) * (D + 4);
+    };
+    float M = kNoMax;
+    for (int k = lane; k < n; k += 32)
+        M = fmaxf(M, k == own ? mine.m : __ldcg(rec(k) + D));
+    M = warp_max(M);
+    Row<D> r;
+    r.m = M;
+    r.l = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.o[i] = 0.f;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        float f = 0.f, l = 0.f;
+        if (k0 + lane < n) {
+            const bool me = k0 + lane == own;
+            f = ex2((me ? mine.m : __ldcg(rec(k0 + lane) + D)) - M);
+            l = me ? mine.l : __ldcg(rec(k0 + lane) + D + 1);
+        }
+        r.l += warp_sum(f * l);
+        const int c = min(32, n - k0);
+#pragma unroll 4
+        for (int k = 0; k < c; ++k) {
+            float v[N];
+            load_cols<N>(v, rec(k0 + k) + lane * N);  // (own record: in bounds, not used)
+            if (k0 + k == own)
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = mine.o[i];
+            r.add(__shfl_sync(0xffffffffu, f, k), v);
+        }
+    }
+    return r;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Args a) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Smem<D> &sm = *reinterpret_cast<Smem<D> *>(smem_raw);
-    constexpr int R = kRing<D>, G = D / 32;
+    constexpr int R = kStages<D>, G = D / 32, kPairBytes = 20 * D;
     static_assert(sizeof(sm.ring[0]) >= kGroupPad * D * sizeof(float), "a piece's O fits the ring");
+    static_assert(2 * kWarps <= 32, "a lane for each piece");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x;
 
-    // -------- units of every kSeqStep sequences and their prefix sums
+    // -------- the line: units of all sequences, and where ranges begin.  Up to
+    // 128 sequences every warp keeps the prefix sums in its lanes (lane i: the
+    // units before sequence i * per); more go through shared memory.
+    const bool few = a.B <= 32 * kSeqStep;
     const int entries = (a.B + kSeqStep - 1) / kSeqStep;
-    for (int i = tid; i < entries; i += kThreads) {
+    auto units_of = [&](int first) {
         int64_t n = 0;
-        for (int s = i * kSeqStep; s < min(a.B, (i + 1) * kSeqStep); ++s) {
-            const int nblk = blocks_of(__ldg(a.context_lens + s), a.maxb);
-            if (nblk)
-                n += (int64_t)(nblk + kPairCost) * a.Hk;
-            else if (cta == 0)
-                report(a.status, PA_DEV_BAD_LENGTH);
-        }
-        sm.prefix[i + 1] = n;
-    }
-    if (tid < 2 * kWarps) sm.piece[tid].start = -1;
-    if (lane < R) mbar_init(&sm.full[warp][lane], 1);
-    if (tid == 0) sm.prefix[0] = 0;
-    fence_barrier_init();
-    __syncthreads();
-    if (warp == 0) {
-        int64_t carry = 0;
-        for (int base = 1; base <= entries; base += 32) {
-            const int i = base + lane;
-            int64_t v = i <= entries ? sm.prefix[i] : 0;
 #pragma unroll
-            for (int f = 1; f < 32; f <<= 1) {
-                const int64_t u = __shfl_up_sync(0xffffffffu, v, f);
-                if (lane >= f) v += u;
-            }
-            if (i <= entries) sm.prefix[i] = v + carry;
-            carry += __shfl_sync(0xffffffffu, v, 31);
+        for (int k = 0; k < kSeqStep; ++k) {
+            const int s = first + k;
+            const int ctx = s < a.B ? __ldg(a.context_lens + s) : 1;
+            const int nblk = blocks_of(ctx, a.maxb);
+            if (s < a.B && nblk == 0 && cta == 0 && (!few || warp == 0))
+                report(a.status, PA_DEV_BAD_LENGTH);
+            n += s < a.B && nblk ? nblk + kPairCost : 0;
         }
+        return n * a.Hk;
+    };
+    auto scan = [&](int64_t v) {  // inclusive, over the warp
+#pragma unroll
+        for (int f = 1; f < 32; f <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, v, f);
+            if (lane >= f) v += u;
+        }
+        return v;
+    };
+    if (tid < 2 * kWarps) sm.piece[tid].start = -1 - tid;
+    if (lane < R) mbar_init(&sm.full[warp][lane], 1);
+    fence_barrier_init();
+    int64_t W, before = 0;  // few: units before sequence lane * kSeqStep
+    if (few) {
+        const int64_t mine = units_of(lane * kSeqStep);
+        const int64_t upto = scan(mine);
+        before = upto - mine;
+        W = __shfl_sync(0xffffffffu, upto, 31);
+        __syncwarp();
+    } else {
+        for (int i = tid; i < entries; i += kThreads) sm.prefix[i + 1] = units_of(i * kSeqStep);
+        if (tid == 0) sm.prefix[0] = 0;
+        __syncthreads();
+        if (warp == 0) {
+            int64_t carry = 0;
+            for (int base = 1; base <= entries; base += 32) {
+                const int i = base + lane;
+                const int64_t v = scan(i <= entries ? sm.prefix[i] : 0);
+                if (i <= entries) sm.prefix[i] = v + carry;
+                carry += __shfl_sync(0xffffffffu, v, 31);
+            }
+        }
+        __syncthreads();
+        W = sm.prefix[entries];
     }
-    __syncthreads();
     // Everything above read only call metadata; Q and the pool may still be
     // being written by the kernel before this one.
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t W = sm.prefix[entries];
     if (W == 0) return;
     const int A = (int)min((int64_t)gridDim.x * kWarps, (W + kMinUnits - 1) / kMinUnits);
     if (cta * kWarps >= A) return;
@@ -480,82 +594,90 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
             return p;
         }();
         Pair cur;  // the pair being attended to
-        cur.find(begin, sm.prefix, a);
-        Pair nxt = cur;               // the pair being loaded
-        int64_t nxt_pos = begin;      // its first unit in the range
-        int ib = 0, ie = 0;           // its next block to load, and the end of them
-        int chunk = 0;                // block of lane 0's entry
-        int entry = 0, entry2 = 0;    // block ids chunk + lane, chunk + 32 + lane
-        bool more = true;
-        uint32_t phase = 0, loaded = 0;  // per ring slot: parity to wait for; a copy was issued
-        bool dead = false;               // a wait gave up
-        int put = 0, get = 0;            // ring slots
+        if (few) {
+            const uint32_t le = __ballot_sync(0xffffffffu, before <= begin && lane < entries);
+            const int i = 31 - __clz(le);
+            cur.find(begin, i * kSeqStep, __shfl_sync(0xffffffffu, before, i), a);
+        } else {
+            int lo = 0, hi = entries - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (sm.prefix[mid] <= begin)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            cur.find(begin, lo * kSeqStep, sm.prefix[lo], a);
+        }
+        Pair nxt = cur;  // the pair being loaded
+        int ib, ie;      // its next block to load, and the end of those in the range
+        int chunk;       // block of lane 0's entry
+        int entry, entry2;  // block ids of blocks chunk + lane, chunk + 32 + lane
+        const uint32_t block_stride = (uint32_t)a.Hk * kPairBytes;
+        const uint8_t *tiles;  // of nxt's KV head
+        const uint32_t ring = smem_u32(sm.ring[warp]);
+        uint64_t *const full = sm.full[warp];
 
-        auto open = [&]() {  // blocks of nxt in [nxt_pos, end)
-            ib = (int)min((int64_t)nxt.nblk, nxt_pos - nxt.start);
+        auto open = [&](int64_t pos) {  // blocks of nxt in [pos, end)
+            ib = (int)min((int64_t)nxt.nblk, pos - nxt.start);
             ie = (int)min((int64_t)nxt.nblk, end - nxt.start);
             chunk = ib;
             const int32_t *row = a.block_tables + (int64_t)nxt.s * a.maxb;
             entry = ib + lane < ie ? __ldg(row + ib + lane) : 0;
             entry2 = ib + 32 + lane < ie ? __ldg(row + ib + 32 + lane) : 0;
+            tiles = a.tiles + nxt.kvh * kPairBytes;
         };
-        auto issue = [&]() {  // the next block of the range into slot `put`
-            while (more && ib >= ie) {
-                nxt_pos = nxt.start + nxt.nblk + kPairCost;
-                if (nxt_pos >= end) {
-                    more = false;
-                } else {
-                    nxt.next(a);
-                    open();
-                }
+        // A stage takes the next two blocks of the range, or a pair's last one;
+        // lane i loads block i.  `put` and `get` run round the ring; every
+        // stage's barrier completes one phase per use (a block that cannot be
+        // loaded brings no bytes and is marked), so its parity turns when `get`
+        // comes round.
+        int put = 0, get = 0, held = 0;
+        uint32_t parity = 0, bad = 0;  // bad: bit 2 stage + block
+        bool dead = false;             // a wait gave up: nothing more is loaded or waited for
+        auto issue = [&]() {
+            while (ib >= ie) {
+                const int64_t pos = nxt.start + nxt.nblk + kPairCost;
+                if (pos >= end) return;
+                nxt.next(a);
+                open(pos);
             }
-            if (!more) return;
-            if (ib == chunk + 32) {
+            if (ib == chunk + 32) {  // (chunks and stages both begin at the pair's first block)
                 chunk = ib;
                 entry = entry2;
                 entry2 = ib + 32 + lane < ie
                              ? __ldg(a.block_tables + (int64_t)nxt.s * a.maxb + ib + 32 + lane)
                              : 0;
             }
-            const int blk = __shfl_sync(0xffffffffu, entry, ib - chunk);
-            const bool ok = blk >= 0 && blk < a.num_blocks && !dead;
-            if (ok) {
-                loaded |= 1u << put;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&sm.full[warp][put], 20 * D);
-                    bulk_load_hint(smem_u32(sm.ring[warp][put]),
-                                   a.tiles + ((int64_t)blk * a.Hk + nxt.kvh) * (20 * D), 20 * D,
-                                   &sm.full[warp][put], pol);
-                }
-            } else {
-                loaded &= ~(1u << put);
-                if (!dead && lane == 0) report(a.status, PA_DEV_BAD_BLOCK);
+            const int blk = __shfl_sync(0xffffffffu, entry, (ib - chunk + lane) & 31);
+            const bool mine = lane < 2 && ib + lane < ie;
+            const bool ok = mine && (unsigned)blk < (unsigned)a.num_blocks;
+            const uint32_t oks = __ballot_sync(0xffffffffu, ok);
+            if (lane == 0) {
+                if (oks)
+                    mbar_arrive_expect_tx(&full[put], oks == 3 ? 2 * kPairBytes : kPairBytes);
+                else
+                    mbar_arrive(&full[put]);
             }
-            ++ib;
+            if (ok)
+                bulk_load_hint(ring + (2 * put + lane) * kPairBytes,
+                               tiles + (uint64_t)(uint32_t)blk * block_stride, kPairBytes,
+                               &full[put], pol);
+            if (oks != (ib + 1 < ie ? 3u : 1u)) {
+                if (mine && !ok) report(a.status, PA_DEV_BAD_BLOCK);
+                bad |= (oks ^ (ib + 1 < ie ? 3u : 1u)) << (2 * put);
+            }
+            ib += 2;
+            ++held;
             put = put + 1 == R ? 0 : put + 1;
         };
-        // Waits for slot `get`; whether it holds a block.
-        auto take = [&]() -> bool {
-            const uint32_t bit = 1u << get;
-            bool ok = (loaded & bit) != 0;
-            if (ok) {
-                ok = mbar_wait(&sm.full[warp][get], (phase & bit) != 0);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) {
-                    // counted as empty from here on; the copies in flight are
-                    // waited for at the end
-                    if (lane == 0) report(a.status, PA_DEV_TIMEOUT);
-                    dead = true;
-                } else {
-                    phase ^= bit;
-                    loaded &= ~bit;
-                }
-            }
+        auto next_stage = [&]() {
+            --held;
             get = get + 1 == R ? 0 : get + 1;
-            return ok;
+            parity ^= get == 0;
         };
 
-        open();
+        open(begin);
         for (int i = 0; i < R; ++i) issue();
         State<D> st;
         for (int64_t pos = begin; pos < end;) {
@@ -563,29 +685,32 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
             const int b1 = (int)min((int64_t)cur.nblk, end - cur.start);
             if (b0 < b1) {
                 st.begin(a, cur, lane);
-                int b = b0;
-                for (; b + 2 <= b1; b += 2) {
-                    const uint32_t at0 = smem_u32(sm.ring[warp][get]);
-                    const bool ok0 = !dead && take();
-                    const uint32_t at1 = smem_u32(sm.ring[warp][get]);
-                    const bool ok1 = !dead && take();
-                    const uint32_t addr[2] = {at0, at1};
-                    const int valid[2] = {ok0 ? kBlockSize : 0,
-                                          ok1 ? min(kBlockSize, cur.ctx - (b + 1) * kBlockSize) : 0};
-                    st.template blocks<2>(addr, valid, lane);
-                    __syncwarp();  // every lane has read the two slots
-                    if (!dead) {
-                        issue();
-                        issue();
+                // blocks whose tokens all count
+                const int full_end = min(b1, cur.ctx / kBlockSize);
+                for (int b = b0; b < b1 && !dead; b += 2) {
+                    const bool ok = mbar_wait(&full[get], parity);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        if (lane == 0) report(a.status, PA_DEV_TIMEOUT);
+                        dead = true;
+                        break;
                     }
-                }
-                if (b < b1) {
-                    const uint32_t addr[1] = {smem_u32(sm.ring[warp][get])};
-                    const bool ok = !dead && take();
-                    const int valid[1] = {ok ? min(kBlockSize, cur.ctx - b * kBlockSize) : 0};
-                    st.template blocks<1>(addr, valid, lane);
-                    __syncwarp();
-                    if (!dead) issue();
+                    const uint32_t at = ring + get * (2 * kPairBytes);
+                    if (b + 2 <= full_end && bad == 0) {
+                        const uint32_t addr[2] = {at, at + kPairBytes};
+                        st.template blocks<2, false>(addr, kBlockSize, lane);
+                    } else {
+                        for (int i = 0; i < 2 && b + i < b1; ++i) {
+                            const uint32_t addr[1] = {at + i * kPairBytes}, bit = 1u << (2 * get + i);
+                            st.template blocks<1, true>(
+                                addr,
+                                (bad & bit) ? 0 : min(kBlockSize, cur.ctx - (b + i) * kBlockSize),
+                                lane);
+                            bad &= ~bit;
+                        }
+                    }
+                    next_stage();
+                    __syncwarp();  // every lane has read the stage
+                    issue();
                 }
                 float v[G][2][4];
                 st.end(v, lane);
@@ -636,100 +761,122 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
             pos = cur.start + cur.nblk + kPairCost;
             if (pos < end) cur.next(a);
         }
-        if (dead)  // leave no copy in flight
-            for (int i = 0; i < R; ++i)
-                if (loaded >> i & 1) mbar_wait(&sm.full[warp][i], (phase >> i) & 1);
+        for (; held > 0; next_stage()) mbar_wait(&full[get], parity);  // (dead only)
     }
     __syncthreads();
 
-    // -------- pairs cut between warps, in the order of the line
+    // -------- pairs cut between warps.  In every warp, lane k speaks for piece
+    // k (in the order of the line) and knows the pieces of the same pair.
     const int c0 = cta * kWarps, c1 = min(A, c0 + kWarps);
     const int64_t cta_begin = range_start(W, c0, A), cta_end = range_start(W, c1, A);
-    constexpr int kRec = D + 2;
-    auto record = [&](int c, int slot, int h) -> float * {
-        return a.rec + (((int64_t)c * 2 + slot) * kGroupPad + h) * kRec;
-    };
-    int cut[2] = {-1, -1};  // pieces that name the pairs cut between CTAs, by record slot
-    for (int i = 0; i < 2 * kWarps;) {
-        const Piece p = sm.piece[i];
-        if (p.start < 0) {
-            ++i;
-            continue;
+    Piece p;
+    p.start = -1 - lane;
+    p.s = p.kvh = p.nblk = 0;
+    if (lane < 2 * kWarps) p = sm.piece[lane];
+    const uint32_t same = __match_any_sync(0xffffffffu, (unsigned long long)p.start);
+    const uint32_t heads = __ballot_sync(0xffffffffu, p.start >= 0 && lane == __ffs(same) - 1);
+    if (heads == 0) return;  // the same for every warp
+    // A pair cut between CTAs, by this CTA's record slot: 0 if it began before
+    // the CTA's range, else 1; `first` and `n`, the CTAs that hold it.
+    const bool cut = (heads >> lane & 1) && (p.start < cta_begin || p.start + p.nblk > cta_end);
+    const int slot = p.start < cta_begin ? 0 : 1;
+    int first = 0, n = 1;
+    if (cut) {
+        first = range_of(p.start, W, A) / kWarps;
+        n = range_of(p.start + p.nblk - 1, W, A) / kWarps - first + 1;
+    }
+    const uint32_t cuts = __ballot_sync(0xffffffffu, cut);
+    if (cuts) {
+        // If the others' records have all arrived, this CTA closes the pair and
+        // needs neither record nor arrival of its own.
+        if (warp == 0 && cut) {
+            int seen;
+            asm volatile("ld.acquire.gpu.global.s32 %0, [%1];"
+                         : "=r"(seen)
+                         : "l"(a.counters + p.s * a.Hk + p.kvh)
+                         : "memory");
+            sm.flag[slot] = seen == n - 1;
+            if (seen == n - 1) a.counters[p.s * a.Hk + p.kvh] = 0;
         }
-        int e = i + 1;
-        while (e < 2 * kWarps && (sm.piece[e].start < 0 || sm.piece[e].start == p.start)) ++e;
-        const bool whole = p.start >= cta_begin && p.start + p.nblk <= cta_end;
-        const int slot = p.start < cta_begin ? 0 : 1;
-        if (!whole) cut[slot] = i;
-        for (int x = tid; x < a.g * D; x += kThreads) {
-            const int h = x / D, d = x - h * D;
-            float M = kNoMax;
-            for (int k = i; k < e; ++k)
-                if (sm.piece[k].start >= 0) M = fmaxf(M, sm.m[k][h]);
-            float L = 0.f, O = 0.f;
-            for (int k = i; k < e; ++k) {
-                if (sm.piece[k].start < 0) continue;
-                const float f = ex2(sm.m[k][h] - M);
-                const float v = (k & 1)
-                                    ? reinterpret_cast<const float *>(sm.ring[k >> 1])[x]
-                                    : __ldcg(a.lead + (int64_t)(c0 + (k >> 1)) * kGroupPad * D + x);
-                L = __fmaf_rn(f, sm.l[k][h], L);
-                O = __fmaf_rn(f, v, O);
-            }
-            if (whole) {
-                a.out[((int64_t)p.s * a.H + p.kvh * a.g) * D + x] =
-                    __float2half_rn(L != 0.f ? O / L : 0.f);
+        __syncthreads();
+    }
+    constexpr int N = Row<D>::N;
+    const int rows = __popc(heads) * a.g;
+    for (int x = warp; x < rows; x += kWarps) {
+        const int h = x % a.g;
+        uint32_t rest = heads;
+        for (int k = x / a.g; k > 0; --k) rest &= rest - 1;
+        const int lead = __ffs(rest) - 1;
+        const uint32_t members = __shfl_sync(0xffffffffu, same, lead);
+        const bool in = members >> lane & 1;
+        const float pm = in ? sm.m[lane][h] : kNoMax;
+        Row<D> r;
+        r.m = warp_max(pm);
+        const float f = in ? ex2(pm - r.m) : 0.f;
+        r.l = warp_sum(in ? f * sm.l[lane][h] : 0.f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) r.o[i] = 0.f;
+        for (uint32_t left = members; left; left &= left - 1) {
+            const int k = __ffs(left) - 1;
+            const float *o = (k & 1) ? reinterpret_cast<const float *>(sm.ring[k >> 1])
+                                     : a.lead + (int64_t)(c0 + (k >> 1)) * kGroupPad * D;
+            float v[N];
+            if (k & 1) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = o[h * D + lane * N + i];
             } else {
-                float *rec = record(cta, slot, h);
-                rec[d] = O;
-                if (d == 0) {
-                    rec[D] = M;
-                    rec[D + 1] = L;
+                load_cols<N>(v, o + h * D + lane * N);
+            }
+            r.add(__shfl_sync(0xffffffffu, f, k), v);
+        }
+        const int ps = __shfl_sync(0xffffffffu, p.s, lead);
+        const int pk = __shfl_sync(0xffffffffu, p.kvh, lead);
+        if (cuts >> lead & 1) {
+            const int sl = __shfl_sync(0xffffffffu, slot, lead);
+            const int pf = __shfl_sync(0xffffffffu, first, lead);
+            const int pn = __shfl_sync(0xffffffffu, n, lead);
+            if (!sm.flag[sl]) {
+                float *rec = a.rec + (((int64_t)cta * 2 + sl) * kGroupPad + h) * (D + 4);
+                store_cols<N>(rec + lane * N, r.o);
+                if (lane == 0) {
+                    rec[D] = r.m;
+                    rec[D + 1] = r.l;
                 }
+                continue;
             }
+            r = join_records<D>(a, pf, pn, h, cta - pf, r, lane);
         }
-        i = e;
+        r.store_out(a.out + ((int64_t)ps * a.H + pk * a.g + h) * D, lane);
     }
-    if (cut[0] < 0 && cut[1] < 0) return;  // the same for every thread
-    // -------- pairs cut between CTAs: the last of their records to arrive joins them
+    if (!cuts) return;
+    // -------- arrivals: the last CTA to arrive joins the records
     __syncthreads();
-    if (lane == 0 && warp < 2) {
+    if (warp == 0 && cut) {
         int last = 0;
-        if (cut[warp] >= 0) {
-            const Piece p = sm.piece[cut[warp]];
-            const int first = range_of(p.start, W, A) / kWarps;
-            const int n = range_of(p.start + p.nblk - 1, W, A) / kWarps - first + 1;
+        if (!sm.flag[slot]) {
             __threadfence();
-            last = atomicAdd(a.counters + p.s * a.Hk + p.kvh, 1) == n - 1;
-            if (last) __threadfence();
+            int32_t *counter = a.counters + p.s * a.Hk + p.kvh;
+            last = atomicAdd(counter, 1) == n - 1;
+            if (last) {
+                __threadfence();
+                *counter = 0;
+            }
         }
-        sm.last[warp] = last;
+        sm.flag[2 + slot] = last;
     }
     __syncthreads();
-    for (int slot = 0; slot < 2; ++slot) {
-        if (!sm.last[slot]) continue;
-        const Piece p = sm.piece[cut[slot]];
-        const int first = range_of(p.start, W, A) / kWarps;
-        const int n = range_of(p.start + p.nblk - 1, W, A) / kWarps - first + 1;
-        for (int x = tid; x < a.g * D; x += kThreads) {
-            const int h = x / D, d = x - h * D;
-            // only the pair's first CTA holds it as its last (slot 1)
-            const int64_t fb = range_start(W, first * kWarps, A);
-            const int s0 = p.start < fb ? 0 : 1;
-            float M = kNoMax;
-            for (int k = 0; k < n; ++k) M = fmaxf(M, __ldcg(record(first + k, k ? 0 : s0, h) + D));
-            float L = 0.f, O = 0.f;
-#pragma unroll 4
-            for (int k = 0; k < n; ++k) {
-                const float *rec = record(first + k, k ? 0 : s0, h);
-                const float f = ex2(__ldcg(rec + D) - M);
-                L = __fmaf_rn(f, __ldcg(rec + D + 1), L);
-                O = __fmaf_rn(f, __ldcg(rec + d), O);
-            }
-            a.out[((int64_t)p.s * a.H + p.kvh * a.g) * D + x] =
-                __float2half_rn(L != 0.f ? O / L : 0.f);
+    for (uint32_t left = cuts; left; left &= left - 1) {
+        const int lead = __ffs(left) - 1;
+        if (!sm.flag[2 + __shfl_sync(0xffffffffu, slot, lead)]) continue;
+        const int ps = __shfl_sync(0xffffffffu, p.s, lead);
+        const int pk = __shfl_sync(0xffffffffu, p.kvh, lead);
+        const int pf = __shfl_sync(0xffffffffu, first, lead);
+        const int pn = __shfl_sync(0xffffffffu, n, lead);
+        for (int h = warp; h < a.g; h += kWarps) {
+            const Row<D> none = {};
+            join_records<D>(a, pf, pn, h, -1, none, lane)
+                .store_out(a.out + ((int64_t)ps * a.H + pk * a.g + h) * D, lane);
         }
-        if (tid == 0) a.counters[p.s * a.Hk + p.kvh] = 0;
     }
 }
 
@@ -737,7 +884,7 @@ size_t counters_bytes(int B, int Hk) {
     return ((size_t)B * Hk * sizeof(int32_t) + 255) & ~(size_t)255;
 }
 size_t records_bytes(int D) {
-    return ((size_t)kMaxGrid * 2 * kGroupPad * (D + 2) * sizeof(float) + 255) & ~(size_t)255;
+    return ((size_t)kMaxGrid * 2 * kGroupPad * (D + 4) * sizeof(float) + 255) & ~(size_t)255;
 }
 
 template <int D>
@@ -793,6 +940,7 @@ extern "C" int pa_decode_i4(const void *q, const pa_cache_i4_t *cache, int layer
         return PA_ERR_INVALID;
     if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
     if (n_heads / n_kv_heads > kGroupPad || num_seqs > kMaxSeqs) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)n_kv_heads * head_dim * 20 > INT32_MAX) return PA_ERR_UNSUPPORTED;  // a block's bytes
     if (!cache_i4_ok(cache, layer, n_kv_heads, head_dim)) return PA_ERR_INVALID;
     if (num_seqs == 0) return PA_OK;
     if (!q || !block_tables || !context_lens || !out || !workspace) return PA_ERR_INVALID;
