@@ -5,10 +5,10 @@
 // Work decomposition.  The blocks of all (sequence, KV head) pairs, each pair
 // followed by kPairCost units for its fixed cost, laid end to end, form one
 // line of W units, cut into equal ranges, one per WARP of a persistent grid
-// (one CTA of 16 warps per SM).  A warp streams its range by itself: lane 0
-// brings block tiles (K and V of one KV head, 20 d contiguous bytes: one bulk
-// copy) into the warp's own ring of shared memory, so no warp waits for
-// another until the end.  A pair that lies within one range is finished by
+// (one CTA of 12 warps per SM).  A warp streams its range by itself into its
+// own ring of shared memory (K and V of one block and KV head are 20 d
+// contiguous bytes, which its lanes bring by 16-byte asynchronous copies), so
+// no warp waits for another until the end.  A pair that lies within one range is finished by
 // its warp; the pieces of a pair cut between warps are joined by the CTA once
 // all its warps are done, and a pair cut between CTAs by the CTA whose record
 // of it arrives last.  Every join sums in the order of the line, so the
@@ -117,38 +117,41 @@ __device__ __forceinline__ int range_of(int64_t unit, int64_t W, int A) {
     return (int)(((unit + 1) * A + W - 1) / W) - 1;
 }
 
-__device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void *src, uint32_t bytes,
-                                               uint64_t *bar, uint64_t pol) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(pol)
-        : "memory");
+// 16-byte asynchronous copy global -> shared through L2 only, 16 zero bytes
+// instead if !ok.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok, uint64_t pol) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+                 "l"(src), "r"(ok ? 16 : 0), "l"(pol)
+                 : "memory");
 }
 
 // D(16x8, f32) = A(16x8, f16, row) * B(8x8, f16, col)
 __device__ __forceinline__ void mma_1688_zero(float (&d)[4], uint32_t a0, uint32_t a1,
                                               uint32_t b0) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6},"
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6},"
         " {%7, %7, %7, %7};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
+// (mma_16816 without volatile: the compiler may move it among the others)
+__device__ __forceinline__ void mma_add(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+        " {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 // D(16x8, f32) = A(16x16, f16, row) * B(16x8, f16, col)
 __device__ __forceinline__ void mma_16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                                uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
         " {%8, %9}, {%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
 }
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     uint64_t d;
@@ -166,14 +169,14 @@ __device__ __forceinline__ uint32_t half2_of_f2(uint64_t v) {
     return pack_half2(lo, hi);
 }
 
-// G consecutive words (G = 4 or 2), 4 G-byte aligned.
+// G consecutive words (G = 4 or 2) of shared memory, 4 G-byte aligned.
 template <int G>
-__device__ __forceinline__ void ld_words(uint32_t (&w)[G], uint32_t addr) {
+__device__ __forceinline__ void ld_words(uint32_t (&w)[G], const uint8_t *p) {
     if constexpr (G == 4) {
-        const uint4 x = ld_shared_v4(addr);
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
         w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
     } else {
-        const uint2 x = ld_shared_v2(addr);
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
         w[0] = x.x, w[1] = x.y;
     }
 }
@@ -259,48 +262,56 @@ struct State {
         for (int i = 0; i < G; ++i) e[i] = f2_pack(0.f, 0.f);
     }
 
-    // NB consecutive blocks, their tile pairs at addr[i] in shared memory.  With
+    // NB consecutive blocks, their tile pairs at `tiles` in shared memory.  With
     // kTail, only the first `valid` tokens of the (one) block count.
     template <int NB, bool kTail>
-    __device__ __forceinline__ void blocks(const uint32_t (&addr)[NB], int valid, int lane) {
+    __device__ __forceinline__ void blocks(const uint8_t *tiles, int valid, int lane) {
         static_assert(NB == 1 || !kTail, "");
         const int r = lane >> 2, t = lane & 3;
         using T = I4Tile<D>;
-        // scores of head r, keys 8 h + 2 t and + 1 of each block
+        // scores of head r, keys 8 h + 2 t and + 1 of each block: chain c = 2 block + h
+        constexpr int C = 2 * NB;
+        uint32_t w[C][G], st[NB][2][G];  // st: steps, word 2 grp + h
+        uint64_t acc[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const uint8_t *kt = tiles + (c >> 1) * T::kPair;
+            ld_words<G>(w[c], kt + (8 * (c & 1) + r) * (D / 2) + t * (4 * G));
+            ld_words<G>(st[c >> 1][c & 1], kt + T::kCodes + t * (8 * G) + (c & 1) * 4 * G);
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const uint8_t *kt = tiles + (c >> 1) * T::kPair;
+            const uint32_t ls = *reinterpret_cast<const uint32_t *>(
+                kt + T::kCodes + 2 * (16 * G + G * (8 * (c & 1) + r)) +
+                (G == 4 ? (t & 1) * 4 : 0));
+            float d[4];
+            mma_1688_zero(d, qsum, qsum, ls);
+            acc[c] = f2_mul(f2_pack(d[0], d[1]), f2_pack(0x1p-24f, 0x1p-24f));
+        }
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const uint32_t v = w[c][gr], u = v >> 8;
+                float d0[4], d1[4];
+                mma_16816_zero(d0, qa[gr], v & 0x000f000fu, u & 0x000f000fu);
+                mma_16816_zero(d1, qa[gr], v & 0x00f000f0u, u & 0x00f000f0u);
+                const uint64_t sw =
+                    f2_of_half2(st[c >> 1][gr / (G / 2)][2 * (gr % (G / 2)) + (c & 1)]);
+                acc[c] = f2_fma(f2_pack(d0[0], d0[1]), sw, acc[c]);
+                acc[c] = f2_fma(f2_pack(d1[2], d1[3]), sw, acc[c]);
+            }
+        }
         float y[NB][4];
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const uint32_t par = addr[i] + T::kCodes;
-            uint32_t st[2][G];  // steps: word 2 grp + h of the two
-            ld_words<G>(st[0], par + t * (8 * G));
-            ld_words<G>(st[1], par + t * (8 * G) + 4 * G);
+        for (int c = 0; c < C; ++c)
+            f2_unpack(f2_mul(acc[c], f2_pack(qs, qs)), y[c >> 1][2 * (c & 1)],
+                      y[c >> 1][2 * (c & 1) + 1]);
+        if (kTail) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int j = 8 * h + r;
-                uint32_t w[G];
-                ld_words<G>(w, addr[i] + j * (D / 2) + t * (4 * G));
-                const uint32_t ls = ld_shared_u32(par + 2 * (16 * G + G * j) +
-                                                  (G == 4 ? (t & 1) * 4 : 0));
-                float c[4];
-                mma_1688_zero(c, qsum, qsum, ls);
-                uint64_t acc = f2_mul(f2_pack(c[0], c[1]), f2_pack(0x1p-24f, 0x1p-24f));
-#pragma unroll
-                for (int gr = 0; gr < G; ++gr) {
-                    const uint32_t v = w[gr], u = v >> 8;
-                    float d0[4], d1[4];
-                    mma_16816_zero(d0, qa[gr], v & 0x000f000fu, u & 0x000f000fu);
-                    mma_16816_zero(d1, qa[gr], v & 0x00f000f0u, u & 0x00f000f0u);
-                    const uint64_t sw = f2_of_half2(st[gr / (G / 2)][2 * (gr % (G / 2)) + h]);
-                    acc = f2_fma(f2_pack(d0[0], d0[1]), sw, acc);
-                    acc = f2_fma(f2_pack(d1[2], d1[3]), sw, acc);
-                }
-                f2_unpack(f2_mul(acc, f2_pack(qs, qs)), y[i][2 * h], y[i][2 * h + 1]);
-            }
-            if (kTail) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (8 * (k >> 1) + 2 * t + (k & 1) >= valid) y[i][k] = -INFINITY;
-            }
+            for (int k = 0; k < 4; ++k)
+                if (8 * (k >> 1) + 2 * t + (k & 1) >= valid) y[0][k] = -INFINITY;
         }
         float top = -INFINITY;
 #pragma unroll
@@ -329,7 +340,7 @@ struct State {
         }
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const uint32_t vt = addr[i] + T::kBytes, par = vt + T::kCodes;
+            const uint8_t *vt = tiles + i * T::kPair + T::kBytes, *par = vt + T::kCodes;
             float p[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) p[k] = ex2(y[i][k] - m);
@@ -339,7 +350,8 @@ struct State {
             ld_words<G>(st[1], par + t * (8 * G) + 4 * G);
             // row r % G of the centre's operand: m + 8 s of keys 2 t, + 1, + 8, + 9
             const int row = 8 * (G * t + (r & (G - 1)));
-            const uint2 ls = ld_shared_v2(par + 32 * G + row), ss = ld_shared_v2(par + row);
+            const uint2 ls = *reinterpret_cast<const uint2 *>(par + 32 * G + row);
+            const uint2 ss = *reinterpret_cast<const uint2 *>(par + row);
             const __half2 eight = __float2half2_rn(8.f);
             const __half2 z0 = __hfma2(*reinterpret_cast<const __half2 *>(&ss.x), eight,
                                        *reinterpret_cast<const __half2 *>(&ls.x));
@@ -366,7 +378,7 @@ struct State {
             }
             {  // (rows 8-15 of the operand and of z are not used)
                 const uint32_t a4[4] = {za[0], za[0], za[1], za[1]};
-                mma_16816(z, a4, pack_half2(p[0], p[1]), pack_half2(p[2], p[3]));
+                mma_add(z, a4, pack_half2(p[0], p[1]), pack_half2(p[2], p[3]));
             }
             const uint64_t p01 = f2_pack(p[0], p[1]), p23 = f2_pack(p[2], p[3]);
             const uint32_t eights[4] = {0xc800c800u, 0xc800c800u, 0xc800c800u, 0xc800c800u};
@@ -380,8 +392,8 @@ struct State {
                                         w1[gr] & 0x000f000fu, w1[gr] & 0x00f000f0u};
                 const uint32_t a1[4] = {u0 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x000f000fu,
                                         u1 & 0x00f000f0u};
-                mma_16816(o[2 * gr], a0, b0, b1);
-                mma_16816(o[2 * gr + 1], a1, b0, b1);
+                mma_add(o[2 * gr], a0, b0, b1);
+                mma_add(o[2 * gr + 1], a1, b0, b1);
                 float d[4];
                 mma_16816_zero(d, eights, b0, b1);
                 e[gr] = f2_add(e[gr], f2_pack(d[0], d[1]));
@@ -419,7 +431,6 @@ struct Piece {
 template <int D>
 struct Smem {
     alignas(128) uint8_t ring[kWarps][kStages<D>][2 * 20 * D];
-    uint64_t full[kWarps][kStages<D>];
     float m[2 * kWarps][kGroupPad], l[2 * kWarps][kGroupPad];
     Piece piece[2 * kWarps];  // 2 w: the warp's first, begun by another; 2 w + 1: its last
     int flag[4];              // per record slot: this CTA closes the pair; was the last to arrive
@@ -552,15 +563,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
         return v;
     };
     if (tid < 2 * kWarps) sm.piece[tid].start = -1 - tid;
-    if (lane < R) mbar_init(&sm.full[warp][lane], 1);
-    fence_barrier_init();
     int64_t W, before = 0;  // few: units before sequence lane * kSeqStep
     if (few) {
         const int64_t mine = units_of(lane * kSeqStep);
         const int64_t upto = scan(mine);
         before = upto - mine;
         W = __shfl_sync(0xffffffffu, upto, 31);
-        __syncwarp();
     } else {
         for (int i = tid; i < entries; i += kThreads) sm.prefix[i + 1] = units_of(i * kSeqStep);
         if (tid == 0) sm.prefix[0] = 0;
@@ -616,7 +624,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
         const uint32_t block_stride = (uint32_t)a.Hk * kPairBytes;
         const uint8_t *tiles;  // of nxt's KV head
         const uint32_t ring = smem_u32(sm.ring[warp]);
-        uint64_t *const full = sm.full[warp];
 
         auto open = [&](int64_t pos) {  // blocks of nxt in [pos, end)
             ib = (int)min((int64_t)nxt.nblk, pos - nxt.start);
@@ -627,18 +634,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
             entry2 = ib + 32 + lane < ie ? __ldg(row + ib + 32 + lane) : 0;
             tiles = a.tiles + nxt.kvh * kPairBytes;
         };
-        // A stage takes the next two blocks of the range, or a pair's last one;
-        // lane i loads block i.  `put` and `get` run round the ring; every
-        // stage's barrier completes one phase per use (a block that cannot be
-        // loaded brings no bytes and is marked), so its parity turns when `get`
-        // comes round.
-        int put = 0, get = 0, held = 0;
-        uint32_t parity = 0, bad = 0;  // bad: bit 2 stage + block
-        bool dead = false;             // a wait gave up: nothing more is loaded or waited for
+        // A stage takes the next two blocks of the range, or a pair's last one
+        // (a block that cannot be loaded is zero and marked); each is one group
+        // of copies, so that of the R stages in flight the oldest has landed
+        // when at most R - 1 groups are outstanding.
+        int put = 0, get = 0;
+        uint32_t bad = 0;  // bit 2 stage + block
         auto issue = [&]() {
             while (ib >= ie) {
                 const int64_t pos = nxt.start + nxt.nblk + kPairCost;
-                if (pos >= end) return;
+                if (pos >= end) {
+                    cp_async_commit();
+                    return;
+                }
                 nxt.next(a);
                 open(pos);
             }
@@ -649,32 +657,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
                              ? __ldg(a.block_tables + (int64_t)nxt.s * a.maxb + ib + 32 + lane)
                              : 0;
             }
-            const int blk = __shfl_sync(0xffffffffu, entry, (ib - chunk + lane) & 31);
-            const bool mine = lane < 2 && ib + lane < ie;
-            const bool ok = mine && (unsigned)blk < (unsigned)a.num_blocks;
-            const uint32_t oks = __ballot_sync(0xffffffffu, ok);
-            if (lane == 0) {
-                if (oks)
-                    mbar_arrive_expect_tx(&full[put], oks == 3 ? 2 * kPairBytes : kPairBytes);
-                else
-                    mbar_arrive(&full[put]);
+            const uint32_t dst = ring + put * (2 * kPairBytes) + lane * 16;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (i == 1 && ib + 1 >= ie) break;
+                const int blk = __shfl_sync(0xffffffffu, entry, ib - chunk + i);
+                const bool ok = (unsigned)blk < (unsigned)a.num_blocks;
+                const uint8_t *src =
+                    tiles + (uint64_t)(uint32_t)(ok ? blk : 0) * block_stride + lane * 16;
+                if (!ok) {
+                    if (lane == 0) report(a.status, PA_DEV_BAD_BLOCK);
+                    bad |= 1u << (2 * put + i);
+                }
+#pragma unroll
+                for (int k = 0; k < kPairBytes; k += 512)
+                    if (k + 512 <= kPairBytes || lane * 16 < kPairBytes - k)
+                        cp_async16(dst + i * kPairBytes + k, src + k, ok, pol);
             }
-            if (ok)
-                bulk_load_hint(ring + (2 * put + lane) * kPairBytes,
-                               tiles + (uint64_t)(uint32_t)blk * block_stride, kPairBytes,
-                               &full[put], pol);
-            if (oks != (ib + 1 < ie ? 3u : 1u)) {
-                if (mine && !ok) report(a.status, PA_DEV_BAD_BLOCK);
-                bad |= (oks ^ (ib + 1 < ie ? 3u : 1u)) << (2 * put);
-            }
+            cp_async_commit();
             ib += 2;
-            ++held;
             put = put + 1 == R ? 0 : put + 1;
-        };
-        auto next_stage = [&]() {
-            --held;
-            get = get + 1 == R ? 0 : get + 1;
-            parity ^= get == 0;
         };
 
         open(begin);
@@ -687,28 +689,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
                 st.begin(a, cur, lane);
                 // blocks whose tokens all count
                 const int full_end = min(b1, cur.ctx / kBlockSize);
-                for (int b = b0; b < b1 && !dead; b += 2) {
-                    const bool ok = mbar_wait(&full[get], parity);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        if (lane == 0) report(a.status, PA_DEV_TIMEOUT);
-                        dead = true;
-                        break;
-                    }
-                    const uint32_t at = ring + get * (2 * kPairBytes);
+                for (int b = b0; b < b1; b += 2) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
+                    __syncwarp();  // every lane's copies of the stage have landed
+                    const uint8_t *at = sm.ring[warp][get];
                     if (b + 2 <= full_end && bad == 0) {
-                        const uint32_t addr[2] = {at, at + kPairBytes};
-                        st.template blocks<2, false>(addr, kBlockSize, lane);
+                        st.template blocks<2, false>(at, kBlockSize, lane);
                     } else {
                         for (int i = 0; i < 2 && b + i < b1; ++i) {
-                            const uint32_t addr[1] = {at + i * kPairBytes}, bit = 1u << (2 * get + i);
+                            const uint32_t bit = 1u << (2 * get + i);
                             st.template blocks<1, true>(
-                                addr,
+                                at + i * kPairBytes,
                                 (bad & bit) ? 0 : min(kBlockSize, cur.ctx - (b + i) * kBlockSize),
                                 lane);
                             bad &= ~bit;
                         }
                     }
-                    next_stage();
+                    get = get + 1 == R ? 0 : get + 1;
                     __syncwarp();  // every lane has read the stage
                     issue();
                 }
@@ -761,7 +758,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
             pos = cur.start + cur.nblk + kPairCost;
             if (pos < end) cur.next(a);
         }
-        for (; held > 0; next_stage()) mbar_wait(&full[get], parity);  // (dead only)
     }
     __syncthreads();
 
