@@ -117,11 +117,10 @@ __device__ __forceinline__ int range_of(int64_t unit, int64_t W, int A) {
     return (int)(((unit + 1) * A + W - 1) / W) - 1;
 }
 
-// 16-byte asynchronous copy global -> shared through L2 only, 16 zero bytes
-// instead if !ok.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok, uint64_t pol) {
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
-                 "l"(src), "r"(ok ? 16 : 0), "l"(pol)
+// 16-byte asynchronous copy global -> shared through L2 only.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint64_t pol) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(src), "l"(pol)
                  : "memory");
 }
 
@@ -622,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
         int chunk;       // block of lane 0's entry
         int entry, entry2;  // block ids of blocks chunk + lane, chunk + 32 + lane
         const uint32_t block_stride = (uint32_t)a.Hk * kPairBytes;
-        const uint8_t *tiles;  // of nxt's KV head
+        const uint8_t *tiles;  // of nxt's KV head, this lane's first 16 bytes
         const uint32_t ring = smem_u32(sm.ring[warp]);
 
         auto open = [&](int64_t pos) {  // blocks of nxt in [pos, end)
@@ -632,10 +631,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
             const int32_t *row = a.block_tables + (int64_t)nxt.s * a.maxb;
             entry = ib + lane < ie ? __ldg(row + ib + lane) : 0;
             entry2 = ib + 32 + lane < ie ? __ldg(row + ib + 32 + lane) : 0;
-            tiles = a.tiles + nxt.kvh * kPairBytes;
+            tiles = a.tiles + nxt.kvh * kPairBytes + lane * 16;
         };
         // A stage takes the next two blocks of the range, or a pair's last one
-        // (a block that cannot be loaded is zero and marked); each is one group
+        // (a block that cannot be loaded is left out and marked); each is one group
         // of copies, so that of the R stages in flight the oldest has landed
         // when at most R - 1 groups are outstanding.
         int put = 0, get = 0;
@@ -662,17 +661,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
             for (int i = 0; i < 2; ++i) {
                 if (i == 1 && ib + 1 >= ie) break;
                 const int blk = __shfl_sync(0xffffffffu, entry, ib - chunk + i);
-                const bool ok = (unsigned)blk < (unsigned)a.num_blocks;
-                const uint8_t *src =
-                    tiles + (uint64_t)(uint32_t)(ok ? blk : 0) * block_stride + lane * 16;
-                if (!ok) {
+                if ((unsigned)blk < (unsigned)a.num_blocks) {
+                    const uint8_t *src = tiles + (uint64_t)(uint32_t)blk * block_stride;
+#pragma unroll
+                    for (int k = 0; k < kPairBytes; k += 512)
+                        if (k + 512 <= kPairBytes || lane * 16 < kPairBytes - k)
+                            cp_async16(dst + i * kPairBytes + k, src + k, pol);
+                } else {
                     if (lane == 0) report(a.status, PA_DEV_BAD_BLOCK);
                     bad |= 1u << (2 * put + i);
                 }
-#pragma unroll
-                for (int k = 0; k < kPairBytes; k += 512)
-                    if (k + 512 <= kPairBytes || lane * 16 < kPairBytes - k)
-                        cp_async16(dst + i * kPairBytes + k, src + k, ok, pol);
             }
             cp_async_commit();
             ib += 2;
