@@ -622,7 +622,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
         int entry, entry2;  // block ids of blocks chunk + lane, chunk + 32 + lane
         const uint32_t block_stride = (uint32_t)a.Hk * kPairBytes;
         const uint8_t *tiles;  // of nxt's KV head, this lane's first 16 bytes
-        const uint32_t ring = smem_u32(sm.ring[warp]);
 
         auto open = [&](int64_t pos) {  // blocks of nxt in [pos, end)
             ib = (int)min((int64_t)nxt.nblk, pos - nxt.start);
@@ -637,48 +636,57 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
         // (a block that cannot be loaded is left out and marked); each is one group
         // of copies, so that of the R stages in flight the oldest has landed
         // when at most R - 1 groups are outstanding.
-        int put = 0, get = 0;
         uint32_t bad = 0;  // bit 2 stage + block
-        auto issue = [&]() {
-            while (ib >= ie) {
-                const int64_t pos = nxt.start + nxt.nblk + kPairCost;
-                if (pos >= end) {
-                    cp_async_commit();
-                    return;
+        auto copy = [&](uint8_t *dst, int blk) {
+            const uint8_t *src = tiles + (uint64_t)(uint32_t)blk * block_stride;
+            const uint32_t to = smem_u32(dst) + lane * 16;
+#pragma unroll
+            for (int k = 0; k < kPairBytes; k += 512)
+                if (k + 512 <= kPairBytes || lane * 16 < kPairBytes - k)
+                    cp_async16(to + k, src + k, pol);
+        };
+        auto issue = [&](uint8_t *dst, int stage) {
+            if (ib + 2 > min(ie, chunk + 32)) {
+                while (ib >= ie) {
+                    const int64_t pos = nxt.start + nxt.nblk + kPairCost;
+                    if (pos >= end) {
+                        cp_async_commit();
+                        return;
+                    }
+                    nxt.next(a);
+                    open(pos);
                 }
-                nxt.next(a);
-                open(pos);
+                if (ib == chunk + 32) {  // (chunks and stages both begin at the pair's first block)
+                    chunk = ib;
+                    entry = entry2;
+                    entry2 = ib + 32 + lane < ie
+                                 ? __ldg(a.block_tables + (int64_t)nxt.s * a.maxb + ib + 32 + lane)
+                                 : 0;
+                }
             }
-            if (ib == chunk + 32) {  // (chunks and stages both begin at the pair's first block)
-                chunk = ib;
-                entry = entry2;
-                entry2 = ib + 32 + lane < ie
-                             ? __ldg(a.block_tables + (int64_t)nxt.s * a.maxb + ib + 32 + lane)
-                             : 0;
-            }
-            const uint32_t dst = ring + put * (2 * kPairBytes) + lane * 16;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (i == 1 && ib + 1 >= ie) break;
-                const int blk = __shfl_sync(0xffffffffu, entry, ib - chunk + i);
-                if ((unsigned)blk < (unsigned)a.num_blocks) {
-                    const uint8_t *src = tiles + (uint64_t)(uint32_t)blk * block_stride;
-#pragma unroll
-                    for (int k = 0; k < kPairBytes; k += 512)
-                        if (k + 512 <= kPairBytes || lane * 16 < kPairBytes - k)
-                            cp_async16(dst + i * kPairBytes + k, src + k, pol);
-                } else {
-                    if (lane == 0) report(a.status, PA_DEV_BAD_BLOCK);
-                    bad |= 1u << (2 * put + i);
+            const int blk0 = __shfl_sync(0xffffffffu, entry, ib - chunk);
+            const int blk1 = __shfl_sync(0xffffffffu, entry, (ib - chunk + 1) & 31);
+            if (ib + 1 < ie && max((unsigned)blk0, (unsigned)blk1) < (unsigned)a.num_blocks) {
+                copy(dst, blk0);
+                copy(dst + kPairBytes, blk1);
+            } else {
+                for (int i = 0; i < 2 && ib + i < ie; ++i) {
+                    const int blk = i ? blk1 : blk0;
+                    if ((unsigned)blk < (unsigned)a.num_blocks) {
+                        copy(dst + i * kPairBytes, blk);
+                    } else {
+                        if (lane == 0) report(a.status, PA_DEV_BAD_BLOCK);
+                        bad |= 1u << (2 * stage + i);
+                    }
                 }
             }
             cp_async_commit();
             ib += 2;
-            put = put + 1 == R ? 0 : put + 1;
         };
 
         open(begin);
-        for (int i = 0; i < R; ++i) issue();
+        for (int i = 0; i < R; ++i) issue(sm.ring[warp][i], i);
+        int get = 0;
         State<D> st;
         for (int64_t pos = begin; pos < end;) {
             const int b0 = (int)min((int64_t)cur.nblk, pos - cur.start);
@@ -690,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
                 for (int b = b0; b < b1; b += 2) {
                     asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory");
                     __syncwarp();  // every lane's copies of the stage have landed
-                    const uint8_t *at = sm.ring[warp][get];
+                    uint8_t *at = sm.ring[warp][get];
                     if (b + 2 <= full_end && bad == 0) {
                         st.template blocks<2, false>(at, kBlockSize, lane);
                     } else {
@@ -703,9 +711,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
                             bad &= ~bit;
                         }
                     }
-                    get = get + 1 == R ? 0 : get + 1;
                     __syncwarp();  // every lane has read the stage
-                    issue();
+                    issue(at, get);
+                    get = get + 1 == R ? 0 : get + 1;
                 }
                 float v[G][2][4];
                 st.end(v, lane);
