@@ -62,7 +62,7 @@ struct DecodeI4Args {
     const int32_t *block_tables;  // [B][maxb]
     const int32_t *context_lens;  // [B]
     __half *out;                  // [B][H][D]
-    int32_t *counters;            // [B][Hk] arrivals (zero between calls)
+    int32_t *counters;            // [B][H] arrivals (zero between calls)
     float *rec;                   // [grid][2][8][D + 4] O, then max, sum
     float *lead;                  // [grid][kWarps][8][D] O of a warp's first piece
     int32_t *status;
@@ -72,6 +72,11 @@ struct DecodeI4Args {
 
 __device__ __forceinline__ int blocks_of(int ctx, int maxb) {
     return ctx >= 1 && ctx <= maxb * kBlockSize ? (ctx + kBlockSize - 1) / kBlockSize : 0;
+}
+
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // both >= 0, b > 0
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
 }
 
 // A pair on the line: its blocks are the units [start, start + nblk).
@@ -96,7 +101,7 @@ struct Pair {
             start += n;
             ++s;
         }
-        kvh = (int)((pos - start) / (nblk + kPairCost));
+        kvh = (int)divide(pos - start, nblk + kPairCost);
         start += (int64_t)kvh * (nblk + kPairCost);
     }
     // The next pair; only called while it starts before W.
@@ -111,11 +116,19 @@ struct Pair {
     }
 };
 
-// Cuts of the line: the first unit of range w of A, and the range that holds a unit.
-__device__ __forceinline__ int64_t range_start(int64_t W, int w, int A) { return W * w / A; }
-__device__ __forceinline__ int range_of(int64_t unit, int64_t W, int A) {
-    return (int)(((unit + 1) * A + W - 1) / W) - 1;
-}
+// The line cut into A ranges of `per` units, the first `more` of them one longer.
+struct Cuts {
+    int64_t per, more;
+    __device__ __forceinline__ Cuts(int64_t W, int A) {
+        per = divide(W, A);
+        more = W - per * A;
+    }
+    __device__ __forceinline__ int64_t start(int w) const { return per * w + min((int64_t)w, more); }
+    __device__ __forceinline__ int range_of(int64_t unit) const {
+        const int64_t longer = more * (per + 1);
+        return (int)(unit < longer ? divide(unit, per + 1) : more + divide(unit - longer, per));
+    }
+};
 
 // 16-byte asynchronous copy global -> shared through L2 only.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint64_t pol) {
@@ -432,7 +445,6 @@ struct Smem {
     alignas(128) uint8_t ring[kWarps][kStages<D>][2 * 20 * D];
     float m[2 * kWarps][kGroupPad], l[2 * kWarps][kGroupPad];
     Piece piece[2 * kWarps];  // 2 w: the warp's first, begun by another; 2 w + 1: its last
-    int flag[4];              // per record slot: this CTA closes the pair; was the last to arrive
     int64_t prefix[kMaxSeqs / kSeqStep + 1];
 };
 
@@ -592,9 +604,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
     const int A = (int)min((int64_t)gridDim.x * kWarps, (W + kMinUnits - 1) / kMinUnits);
     if (cta * kWarps >= A) return;
     const int me = cta * kWarps + warp;
+    const Cuts cuts(W, A);
 
     if (me < A) {
-        const int64_t begin = range_start(W, me, A), end = range_start(W, me + 1, A);
+        const int64_t begin = cuts.start(me), end = cuts.start(me + 1);
         const uint64_t pol = [] {
             uint64_t p;
             asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -685,14 +698,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
         };
 
         open(begin);
-        for (int i = 0; i < R; ++i) issue(sm.ring[warp][i], i);
+        // The first stage alone before Q is asked for, so that every warp's first
+        // blocks arrive ahead of the later stages' (28 MB over all warps).
+        issue(sm.ring[warp][0], 0);
         int get = 0;
+        bool primed = false;
         State<D> st;
         for (int64_t pos = begin; pos < end;) {
             const int b0 = (int)min((int64_t)cur.nblk, pos - cur.start);
             const int b1 = (int)min((int64_t)cur.nblk, end - cur.start);
             if (b0 < b1) {
                 st.begin(a, cur, lane);
+                if (!primed) {
+                    for (int i = 1; i < R; ++i) issue(sm.ring[warp][i], i);
+                    primed = true;
+                }
                 // blocks whose tokens all count
                 const int full_end = min(b1, cur.ctx / kBlockSize);
                 for (int b = b0; b < b1; b += 2) {
@@ -770,46 +790,40 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
     // -------- pairs cut between warps.  In every warp, lane k speaks for piece
     // k (in the order of the line) and knows the pieces of the same pair.
     const int c0 = cta * kWarps, c1 = min(A, c0 + kWarps);
-    const int64_t cta_begin = range_start(W, c0, A), cta_end = range_start(W, c1, A);
+    const int64_t cta_begin = cuts.start(c0), cta_end = cuts.start(c1);
     Piece p;
     p.start = -1 - lane;
     p.s = p.kvh = p.nblk = 0;
     if (lane < 2 * kWarps) p = sm.piece[lane];
     const uint32_t same = __match_any_sync(0xffffffffu, (unsigned long long)p.start);
     const uint32_t heads = __ballot_sync(0xffffffffu, p.start >= 0 && lane == __ffs(same) - 1);
-    if (heads == 0) return;  // the same for every warp
-    // A pair cut between CTAs, by this CTA's record slot: 0 if it began before
-    // the CTA's range, else 1; `first` and `n`, the CTAs that hold it.
-    const bool cut = (heads >> lane & 1) && (p.start < cta_begin || p.start + p.nblk > cta_end);
-    const int slot = p.start < cta_begin ? 0 : 1;
-    int first = 0, n = 1;
-    if (cut) {
-        first = range_of(p.start, W, A) / kWarps;
-        n = range_of(p.start + p.nblk - 1, W, A) / kWarps - first + 1;
-    }
-    const uint32_t cuts = __ballot_sync(0xffffffffu, cut);
-    if (cuts) {
-        // If the others' records have all arrived, this CTA closes the pair and
-        // needs neither record nor arrival of its own.
-        if (warp == 0 && cut) {
-            int seen;
-            asm volatile("ld.acquire.gpu.global.s32 %0, [%1];"
-                         : "=r"(seen)
-                         : "l"(a.counters + p.s * a.Hk + p.kvh)
-                         : "memory");
-            sm.flag[slot] = seen == n - 1;
-            if (seen == n - 1) a.counters[p.s * a.Hk + p.kvh] = 0;
-        }
-        __syncthreads();
-    }
     constexpr int N = Row<D>::N;
     const int rows = __popc(heads) * a.g;
-    for (int x = warp; x < rows; x += kWarps) {
+    for (int x = warp; x < rows; x += kWarps) {  // a row (one head) per warp
         const int h = x % a.g;
         uint32_t rest = heads;
         for (int k = x / a.g; k > 0; --k) rest &= rest - 1;
         const int lead = __ffs(rest) - 1;
         const uint32_t members = __shfl_sync(0xffffffffu, same, lead);
+        const int64_t start = __shfl_sync(0xffffffffu, p.start, lead);
+        const int nblk = __shfl_sync(0xffffffffu, p.nblk, lead);
+        const int qrow = __shfl_sync(0xffffffffu, p.s, lead) * a.H +
+                         __shfl_sync(0xffffffffu, p.kvh, lead) * a.g + h;
+        // A row cut between CTAs: each leaves a record of it (slot 0 if the pair
+        // began before the CTA's range, else 1) and arrives on the row's counter;
+        // the last joins the records.  If the others' have all arrived already,
+        // this CTA needs neither record nor arrival of its own.
+        const bool cut = start < cta_begin || start + nblk > cta_end;
+        int first = 0, n = 1, seen = 0;
+        if (cut) {
+            first = cuts.range_of(start) / kWarps;
+            n = cuts.range_of(start + nblk - 1) / kWarps - first + 1;
+            if (lane == 0)
+                asm volatile("ld.acquire.gpu.global.s32 %0, [%1];"
+                             : "=r"(seen)
+                             : "l"(a.counters + qrow)
+                             : "memory");
+        }
         const bool in = members >> lane & 1;
         const float pm = in ? sm.m[lane][h] : kNoMax;
         Row<D> r;
@@ -831,63 +845,40 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
             }
             r.add(__shfl_sync(0xffffffffu, f, k), v);
         }
-        const int ps = __shfl_sync(0xffffffffu, p.s, lead);
-        const int pk = __shfl_sync(0xffffffffu, p.kvh, lead);
-        if (cuts >> lead & 1) {
-            const int sl = __shfl_sync(0xffffffffu, slot, lead);
-            const int pf = __shfl_sync(0xffffffffu, first, lead);
-            const int pn = __shfl_sync(0xffffffffu, n, lead);
-            if (!sm.flag[sl]) {
-                float *rec = a.rec + (((int64_t)cta * 2 + sl) * kGroupPad + h) * (D + 4);
+        if (cut) {
+            int own = cta - first;
+            if (__shfl_sync(0xffffffffu, seen, 0) != n - 1) {
+                float *rec =
+                    a.rec +
+                    (((int64_t)cta * 2 + (start >= cta_begin)) * kGroupPad + h) * (D + 4);
                 store_cols<N>(rec + lane * N, r.o);
                 if (lane == 0) {
                     rec[D] = r.m;
                     rec[D + 1] = r.l;
                 }
-                continue;
+                __syncwarp();
+                if (lane == 0) {
+                    __threadfence();
+                    seen = atomicAdd(a.counters + qrow, 1);
+                    __threadfence();
+                }
+                if (__shfl_sync(0xffffffffu, seen, 0) != n - 1) continue;
+                own = -1;
             }
-            r = join_records<D>(a, pf, pn, h, cta - pf, r, lane);
+            __syncwarp();
+            r = join_records<D>(a, first, n, h, own, r, lane);
+            if (lane == 0) a.counters[qrow] = 0;
         }
-        r.store_out(a.out + ((int64_t)ps * a.H + pk * a.g + h) * D, lane);
-    }
-    if (!cuts) return;
-    // -------- arrivals: the last CTA to arrive joins the records
-    __syncthreads();
-    if (warp == 0 && cut) {
-        int last = 0;
-        if (!sm.flag[slot]) {
-            __threadfence();
-            int32_t *counter = a.counters + p.s * a.Hk + p.kvh;
-            last = atomicAdd(counter, 1) == n - 1;
-            if (last) {
-                __threadfence();
-                *counter = 0;
-            }
-        }
-        sm.flag[2 + slot] = last;
-    }
-    __syncthreads();
-    for (uint32_t left = cuts; left; left &= left - 1) {
-        const int lead = __ffs(left) - 1;
-        if (!sm.flag[2 + __shfl_sync(0xffffffffu, slot, lead)]) continue;
-        const int ps = __shfl_sync(0xffffffffu, p.s, lead);
-        const int pk = __shfl_sync(0xffffffffu, p.kvh, lead);
-        const int pf = __shfl_sync(0xffffffffu, first, lead);
-        const int pn = __shfl_sync(0xffffffffu, n, lead);
-        for (int h = warp; h < a.g; h += kWarps) {
-            const Row<D> none = {};
-            join_records<D>(a, pf, pn, h, -1, none, lane)
-                .store_out(a.out + ((int64_t)ps * a.H + pk * a.g + h) * D, lane);
-        }
+        r.store_out(a.out + (int64_t)qrow * D, lane);
     }
 }
 
-size_t counters_bytes(int B, int Hk) {
-    return ((size_t)B * Hk * sizeof(int32_t) + 255) & ~(size_t)255;
-}
-size_t records_bytes(int D) {
-    return ((size_t)kMaxGrid * 2 * kGroupPad * (D + 4) * sizeof(float) + 255) & ~(size_t)255;
-}
+// The workspace: records, first pieces, counters.  The counters must stay zero
+// between calls of any shape, so they lie behind areas whose sizes no shape
+// changes (head_dim 128's).
+constexpr size_t kRecBytes = (size_t)kMaxGrid * 2 * kGroupPad * (128 + 4) * sizeof(float);
+constexpr size_t kLeadBytes = (size_t)kMaxGrid * kWarps * kGroupPad * 128 * sizeof(float);
+static_assert(kRecBytes % 256 == 0 && kLeadBytes % 256 == 0, "");
 
 template <int D>
 int launch_decode_i4(const DecodeI4Args &a, cudaStream_t st) {
@@ -927,8 +918,7 @@ using namespace pa;
 extern "C" size_t pa_decode_i4_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads,
                                                int head_dim) {
     if (num_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0) return 0;
-    return counters_bytes(num_seqs, n_kv_heads) + records_bytes(head_dim) +
-           (size_t)kMaxGrid * kWarps * kGroupPad * head_dim * sizeof(float);
+    return kRecBytes + kLeadBytes + (size_t)num_seqs * n_heads * sizeof(int32_t);
 }
 
 extern "C" int pa_decode_i4(const void *q, const pa_cache_i4_t *cache, int layer,
@@ -958,10 +948,9 @@ extern "C" int pa_decode_i4(const void *q, const pa_cache_i4_t *cache, int layer
     a.context_lens = context_lens;
     a.out = static_cast<__half *>(out);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    a.counters = reinterpret_cast<int32_t *>(ws);
-    ws += counters_bytes(num_seqs, n_kv_heads);
     a.rec = reinterpret_cast<float *>(ws);
-    a.lead = reinterpret_cast<float *>(ws + records_bytes(head_dim));
+    a.lead = reinterpret_cast<float *>(ws + kRecBytes);
+    a.counters = reinterpret_cast<int32_t *>(ws + kRecBytes + kLeadBytes);
     a.status = dev_status;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.B = num_seqs;
