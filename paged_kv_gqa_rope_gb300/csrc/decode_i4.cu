@@ -506,32 +506,48 @@ __device__ __forceinline__ Row<D> join_records(const DecodeI4Args &a, int first,
     auto rec = [&](int k) {
         return a.rec + (((int64_t)(first + k) * 2 + (k == 0)) * kGroupPad + h) * (D + 4);
     };
-    float M = kNoMax;
-    for (int k = lane; k < n; k += 32)
-        M = fmaxf(M, k == own ? mine.m : __ldcg(rec(k) + D));
-    M = warp_max(M);
+    // Up to 32 records, a lane for each: their (max, sum) and the O of the first
+    // eight are asked for together, so that a short join waits once.
+    constexpr int kBatch = 8;
     Row<D> r;
-    r.m = M;
+    r.m = kNoMax;
     r.l = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) r.o[i] = 0.f;
     for (int k0 = 0; k0 < n; k0 += 32) {
-        float f = 0.f, l = 0.f;
-        if (k0 + lane < n) {
-            const bool me = k0 + lane == own;
-            f = ex2((me ? mine.m : __ldcg(rec(k0 + lane) + D)) - M);
-            l = me ? mine.l : __ldcg(rec(k0 + lane) + D + 1);
-        }
-        r.l += warp_sum(f * l);
         const int c = min(32, n - k0);
-#pragma unroll 4
-        for (int k = 0; k < c; ++k) {
-            float v[N];
-            load_cols<N>(v, rec(k0 + k) + lane * N);  // (own record: in bounds, not used)
-            if (k0 + k == own)
+        float m = kNoMax, l = 0.f;
+        if (lane < c) {
+            m = __ldcg(rec(k0 + lane) + D);  // (own record: in bounds, not used)
+            l = __ldcg(rec(k0 + lane) + D + 1);
+        }
+        float v[kBatch][N];
+        auto ask = [&](int j) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) v[i] = mine.o[i];
-            r.add(__shfl_sync(0xffffffffu, f, k), v);
+            for (int i = 0; i < kBatch; ++i)
+                load_cols<N>(v[i], rec(k0 + min(j + i, c - 1)) + lane * N);
+        };
+        ask(0);
+        if (k0 + lane == own) {
+            m = mine.m;
+            l = mine.l;
+        }
+        const float M = fmaxf(r.m, warp_max(m)), old = ex2(r.m - M);
+        const float f = lane < c ? ex2(m - M) : 0.f;
+        r.m = M;
+        r.l = r.l * old + warp_sum(f * l);
+#pragma unroll
+        for (int i = 0; i < N; ++i) r.o[i] *= old;
+        for (int j = 0; j < c; j += kBatch) {
+            if (j) ask(j);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (j + i >= c) break;
+                if (k0 + j + i == own)
+#pragma unroll
+                    for (int d = 0; d < N; ++d) v[i][d] = mine.o[d];
+                r.add(__shfl_sync(0xffffffffu, f, j + i), v[i]);
+            }
         }
     }
     return r;
@@ -800,9 +816,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
     constexpr int N = Row<D>::N;
     const int rows = __popc(heads) * a.g;
     for (int x = warp; x < rows; x += kWarps) {  // a row (one head) per warp
+        // the last pair's rows, then the others': those cut between CTAs, the
+        // last pair and the first, are the ones that another CTA may wait for
         const int h = x % a.g;
+        int which = x / a.g - 1;
+        if (which < 0) which = __popc(heads) - 1;
         uint32_t rest = heads;
-        for (int k = x / a.g; k > 0; --k) rest &= rest - 1;
+        for (int k = which; k > 0; --k) rest &= rest - 1;
         const int lead = __ffs(rest) - 1;
         const uint32_t members = __shfl_sync(0xffffffffu, same, lead);
         const int64_t start = __shfl_sync(0xffffffffu, p.start, lead);
@@ -814,6 +834,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
         // the last joins the records.  If the others' have all arrived already,
         // this CTA needs neither record nor arrival of its own.
         const bool cut = start < cta_begin || start + nblk > cta_end;
+        // A piece in the workspace (the members' last, if any) is asked for
+        // before the counter is read, whose acquire holds up later loads.
+        const int tail = 31 - __clz(members);
+        float v[N];
+        if (!(tail & 1))
+            load_cols<N>(v, a.lead + ((int64_t)(c0 + (tail >> 1)) * kGroupPad + h) * D + lane * N);
         int first = 0, n = 1, seen = 0;
         if (cut) {
             first = cuts.range_of(start) / kWarps;
@@ -832,19 +858,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
         r.l = warp_sum(in ? f * sm.l[lane][h] : 0.f);
 #pragma unroll
         for (int i = 0; i < N; ++i) r.o[i] = 0.f;
-        for (uint32_t left = members; left; left &= left - 1) {
+        for (uint32_t left = members & 0xaaaaaaaau; left; left &= left - 1) {
             const int k = __ffs(left) - 1;
-            const float *o = (k & 1) ? reinterpret_cast<const float *>(sm.ring[k >> 1])
-                                     : a.lead + (int64_t)(c0 + (k >> 1)) * kGroupPad * D;
-            float v[N];
-            if (k & 1) {
+            const float *o = reinterpret_cast<const float *>(sm.ring[k >> 1]);
+            float w[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) v[i] = o[h * D + lane * N + i];
-            } else {
-                load_cols<N>(v, o + h * D + lane * N);
-            }
-            r.add(__shfl_sync(0xffffffffu, f, k), v);
+            for (int i = 0; i < N; ++i) w[i] = o[h * D + lane * N + i];
+            r.add(__shfl_sync(0xffffffffu, f, k), w);
         }
+        if (!(tail & 1)) r.add(__shfl_sync(0xffffffffu, f, tail), v);
         if (cut) {
             int own = cta - first;
             if (__shfl_sync(0xffffffffu, seen, 0) != n - 1) {
