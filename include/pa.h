@@ -521,8 +521,8 @@ int pa_rope_kv_write_i4(const void *q, void *q_out, const void *k, const void *v
  * Reads rows of the 4-bit pool back as fp16: for every sequence s, its tokens
  * first_tokens[s] .. first_tokens[s] + lengths[s] - 1, located through
  * block_tables[s], go to rows row_starts[s] .. of k_out and v_out, as
- * m + s * c (computed in fp32) rounded to the nearest fp16, saturated at
- * +-65504 (the step's rounding up can carry a group's top past it).
+ * m + s * c rounded once to the nearest fp16, saturated at 65504 (the step's
+ * rounding up can carry a group's top past it).
  *   block_tables  device int32 [num_seqs][max_blocks_per_seq]
  *   lengths       device int32 [num_seqs]; 0 reads nothing
  *   first_tokens  device int32 [num_seqs], or NULL for 0

@@ -457,6 +457,6 @@ def dequantize_cache_i4(tiles) -> np.ndarray:
 
 
 def read_rows_i4(values64) -> np.ndarray:
-    """fp16 rows as the library reads them back: the values in float32 (the
-    product is exact, one rounding of the sum), saturated, rounded to fp16."""
-    return np.minimum(values64.astype(np.float32), np.float32(65504)).astype(np.float16)
+    """fp16 rows as the library reads them back: the value (exact in float64)
+    saturated and rounded once to fp16."""
+    return np.minimum(values64, 65504).astype(np.float16)

@@ -4,7 +4,7 @@
 // that reads rows back as fp16.
 #include <string.h>
 
-#include <mutex>
+#include <algorithm>
 
 #include "common.cuh"
 #include "internal.h"
@@ -24,7 +24,7 @@ struct RopeI4Args {
     uint8_t *tiles;       // tile pairs of the layer
     int64_t num_slots;
     int32_t *status;
-    int num_tokens, n_heads, n_kv_heads, max_pos;
+    int num_tokens, n_heads, n_kv_heads, max_pos, rows_per_cta;
 };
 
 __device__ __forceinline__ __half2 as_half2(uint32_t w) {
@@ -65,88 +65,125 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 x, __half &step, __hal
     }
     const float s = __half2float(step);
     if (!(s > 0.f)) return 0u;
-    uint32_t codes = 0;
+    // rint((v - lo) / s): the quotient by a reciprocal, which is within 2^-17 of
+    // the divided one, unless that leaves the rounding open (then by division).
+    // Adding 1.5 2^23 rounds to an integer, ties to even; the quotient is at
+    // most 15 (1 + 2^-22), since s is not below the range's fifteenth.
+    constexpr float kRint = 12582912.f;
+    const float inv = __frcp_rn(s);
+    float c[8];
+    bool open = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const __half2 h = as_half2(w[i >> 1]);
-        const float v = (i & 1) ? __high2float(h) : __low2float(h);
-        const int c = __float2int_rn(__fdiv_rn(__fsub_rn(v, lo), s));
-        codes |= (uint32_t)max(0, min(15, c)) << (4 * i);
+        const float q = __fsub_rn((i & 1) ? __high2float(h) : __low2float(h), lo) * inv;
+        c[i] = __fsub_rn(__fadd_rn(q, kRint), kRint);
+        open |= fabsf(q - c[i]) > 0.4999f;
     }
-    return codes;
+    if (open) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __half2 h = as_half2(w[i >> 1]);
+            c[i] = rintf(__fdiv_rn(
+                __fsub_rn((i & 1) ? __high2float(h) : __low2float(h), lo), s));
+        }
+    }
+    // four codes as one integer below 2^16 (exact), twice
+    const float a = fmaf(fmaf(fmaf(c[3], 16.f, c[2]), 16.f, c[1]), 16.f, c[0]);
+    const float b = fmaf(fmaf(fmaf(c[7], 16.f, c[6]), 16.f, c[5]), 16.f, c[4]);
+    return __byte_perm(__float_as_uint(a + 8388608.f), __float_as_uint(b + 8388608.f), 0x5410);
 }
 
-// One thread handles one 16-byte piece (8 fp16 values) of one head row of a
-// token, as in rope_kv_write_kernel; the four threads of a group of 32 (an
-// aligned quad of lanes) find its least and greatest value with shuffles.
+// A CTA takes tokens blockIdx.x, + gridDim.x, ..., of each the rows of its
+// blockIdx.y, kRows of them at a time in kUnroll rounds whose loads are issued
+// together; a thread keeps to one 16-byte piece (8 values) of the rows, so that
+// it needs one set of cosines and sines a token.  The four threads of a group
+// of 32 (an aligned quad of lanes) find its least and greatest value with
+// shuffles.  Bound by HBM: Q, K and V in, Q and the codes out.
+constexpr int kUnroll = 4;
+
 template <int D>
-__global__ void __launch_bounds__(kTokenThreads) rope_kv_write_i4_kernel(const RopeI4Args a) {
+__global__ void __launch_bounds__(kTokenThreads, 4) rope_kv_write_i4_kernel(const RopeI4Args a) {
     griddep_launch_dependents();
     using T = I4Tile<D>;
-    constexpr int kPieces = D / 8;
-    const int H = a.n_heads, Hk = a.n_kv_heads;
-    const int rows = H + 2 * Hk;
-    const int t = (int)(blockIdx.z * gridDim.y + blockIdx.y);
-    if (t >= a.num_tokens) return;  // the whole CTA
-    const int idx = (int)(blockIdx.x * blockDim.x + threadIdx.x);
-    // Threads past the token's last row (whole quads of them) still take part
-    // in the quad's reductions; they read row 0 and write nothing.
-    const bool live = idx < rows * kPieces;
-    const int i = live ? idx : idx % kPieces;
-    const int piece = i % kPieces, row = i / kPieces;
-
-    const int pos = __ldg(a.positions + t);
-    const bool pos_ok = pos >= 0 && pos < a.max_pos;
-    const int slot = __ldg(a.slots + t);
-    if (idx == 0) {
-        if (!pos_ok)
-            report(a.status, PA_DEV_BAD_POSITION);
-        else if (slot >= a.num_slots)
-            report(a.status, PA_DEV_BAD_SLOT);
-    }
-    if (!pos_ok) return;  // the whole CTA
-    const bool write_cache = live && slot >= 0 && slot < a.num_slots;
-
-    uint4 x;
-    if (row < H + Hk) {
-        const bool is_q = row < H;
-        const __half *base = is_q ? a.q + ((int64_t)t * H + row) * D
-                                  : a.k + ((int64_t)t * Hk + (row - H)) * D;
+    constexpr int kPieces = D / 8, kRows = kTokenThreads / kPieces;
+    const int H = a.n_heads, Hk = a.n_kv_heads, rows = H + 2 * Hk;
+    const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces;
+    const int g = piece >> 2, t8 = piece & 3;
+    const int row_begin = (int)blockIdx.y * a.rows_per_cta;
+    const int row_end = min(rows, row_begin + a.rows_per_cta);
+    for (int t = (int)blockIdx.x; t < a.num_tokens; t += (int)gridDim.x) {
+        const int pos = __ldg(a.positions + t);
+        const int slot = __ldg(a.slots + t);
+        const bool pos_ok = pos >= 0 && pos < a.max_pos;
+        if (threadIdx.x == 0 && blockIdx.y == 0) {
+            if (!pos_ok)
+                report(a.status, PA_DEV_BAD_POSITION);
+            else if (slot >= a.num_slots)
+                report(a.status, PA_DEV_BAD_SLOT);
+        }
+        if (!pos_ok) continue;
+        const bool write_cache = slot >= 0 && slot < a.num_slots;
         const float4 *cs =
             reinterpret_cast<const float4 *>(a.table + (int64_t)pos * (D / 2) + piece * 4);
-        // (an ordinary load: q_out may be q)
-        x = rope_rotate8(reinterpret_cast<const uint4 *>(base)[piece], __ldg(cs), __ldg(cs + 1));
-        if (is_q && live)
-            reinterpret_cast<uint4 *>(a.q_out + ((int64_t)t * H + row) * D)[piece] = x;
-    } else {
-        x = __ldg(reinterpret_cast<const uint4 *>(a.v + ((int64_t)t * Hk + (row - H - Hk)) * D) +
-                  piece);
-    }
-    __half step, least;
-    const uint32_t codes = quantise8(x, step, least);
-    if (row >= H && write_cache) {
-        const bool is_k = row < H + Hk;
-        const int h = is_k ? row - H : row - H - Hk;
-        const int j = slot % kBlockSize, g = piece >> 2, t8 = piece & 3;
-        uint8_t *tile = a.tiles + ((int64_t)(slot / kBlockSize) * Hk + h) * T::kPair;
-        if (is_k) {
-            *reinterpret_cast<uint32_t *>(tile + T::k_word(j, g, t8)) = codes;
-        } else {
-            tile += T::kBytes;
-            *reinterpret_cast<uint16_t *>(tile + T::v_half(j, g, 2 * t8)) = (uint16_t)codes;
-            *reinterpret_cast<uint16_t *>(tile + T::v_half(j, g, 2 * t8 + 1)) =
-                (uint16_t)(codes >> 16);
+        const float4 cs0 = __ldg(cs), cs1 = __ldg(cs + 1);
+        const uint4 *q = reinterpret_cast<const uint4 *>(a.q + (int64_t)t * H * D) + piece;
+        uint4 *q_out = reinterpret_cast<uint4 *>(a.q_out + (int64_t)t * H * D) + piece;
+        const uint4 *k = reinterpret_cast<const uint4 *>(a.k + (int64_t)t * Hk * D) + piece;
+        const uint4 *v = reinterpret_cast<const uint4 *>(a.v + (int64_t)t * Hk * D) + piece;
+        uint8_t *tiles = a.tiles + (int64_t)(slot / kBlockSize) * Hk * T::kPair;
+        const int j = slot % kBlockSize;
+        for (int base = row_begin + sub; base - sub < row_end; base += kRows * kUnroll) {
+            uint4 x[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int row = base + u * kRows;
+                x[u] = make_uint4(0, 0, 0, 0);
+                if (row < row_end)  // (Q by an ordinary load: q_out may be q)
+                    x[u] = row < H        ? q[row * kPieces]
+                           : row < H + Hk ? __ldg(k + (row - H) * kPieces)
+                                          : __ldg(v + (row - H - Hk) * kPieces);
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int row = base + u * kRows;
+                if (row < H + Hk) x[u] = rope_rotate8(x[u], cs0, cs1);
+                if (row < min(H, row_end)) q_out[row * kPieces] = x[u];
+                // the whole warp, if one of its rows is a K or V row
+                const bool kv = row >= H && row < row_end;
+                if (!__any_sync(0xffffffffu, kv)) continue;
+                __half step, least;
+                const uint32_t codes = quantise8(x[u], step, least);
+                if (!kv || !write_cache) continue;
+                const bool is_k = row < H + Hk;
+                uint8_t *tile = tiles + (int64_t)(is_k ? row - H : row - H - Hk) * T::kPair;
+                if (is_k) {
+                    *reinterpret_cast<uint32_t *>(tile + T::k_word(j, g, t8)) = codes;
+                } else {
+                    tile += T::kBytes;
+                    *reinterpret_cast<uint16_t *>(tile + T::v_half(j, g, 2 * t8)) = (uint16_t)codes;
+                    *reinterpret_cast<uint16_t *>(tile + T::v_half(j, g, 2 * t8 + 1)) =
+                        (uint16_t)(codes >> 16);
+                }
+                if (t8 == 0)
+                    *reinterpret_cast<__half *>(tile + T::step(j, g)) = step;
+                else if (t8 == 1)
+                    *reinterpret_cast<__half *>(
+                        tile + (is_k ? T::least_k(j, g) : T::least_v(j, g))) = least;
+            }
         }
-        if (t8 == 0)
-            *reinterpret_cast<__half *>(tile + T::step(j, g)) = step;
-        else if (t8 == 1)
-            *reinterpret_cast<__half *>(tile + (is_k ? T::least_k(j, g) : T::least_v(j, g))) = least;
     }
 }
 
 // ---------------------------------------------------------------- read back
 
+// A warp takes one block of one KV head (a K and a V tile) at a time, its lanes
+// the words of codes in the order they are stored, so that every load is a
+// whole line; the 8 values of a word leave as one 16-byte store, four lanes
+// side by side for 64 bytes of a row.  Bound by HBM: 1.25 d bytes read and 4 d
+// written per (token, KV head).
 constexpr int kReadThreads = 256;
+constexpr int kReadCtas = 4;  // per SM
 constexpr int kMaxReadSeqs = 4096;
 constexpr int kMaxPrefillSeqs = 2048;  // pa_prefill_varlen's limit
 
@@ -164,18 +201,101 @@ struct ReadI4Args {
     int B, Hk, maxb, num_blocks;
 };
 
-// 8 codes (nibble i = value i) with their step and least value -> 8 fp16.
-__device__ __forceinline__ uint4 dequantise8(uint32_t codes, float s, float m) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        // s * c is exact in fp32 (11 + 4 bits)
-        const float a = __fadd_rn(__fmul_rn(s, (float)((codes >> (8 * i)) & 15u)), m);
-        const float b = __fadd_rn(__fmul_rn(s, (float)((codes >> (8 * i + 4)) & 15u)), m);
-        // saturated from above (m is itself an fp16); a NaN stays one
-        w[i] = pack_half2(a > 65504.f ? 65504.f : a, b > 65504.f ? 65504.f : b);
+// 8 codes (nibble i = value i) with their step and least value (each twice) ->
+// 8 fp16, m + s c rounded once.  The codes are the low mantissa bits of 1024
+// (of every other one 16 times as large); the fused multiply-add rounds once.
+__device__ __forceinline__ uint4 dequantise8(uint32_t codes, uint32_t s, uint32_t m) {
+    const __half2 top = __float2half2_rn(65504.f);
+    auto value = [&](uint32_t w, bool high) {
+        const uint32_t x = (w & (high ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;
+        const __half2 c = high ? __hfma2(as_half2(x), __float2half2_rn(0.0625f),
+                                         __float2half2_rn(-64.f))
+                               : __hadd2(as_half2(x), __float2half2_rn(-1024.f));
+        return as_u32(__hmin2_nan(__hfma2(as_half2(s), c, as_half2(m)), top));
+    };
+    const uint32_t a = value(codes, false), b = value(codes, true);  // 0, 4 | 1, 5
+    const uint32_t c = value(codes >> 8, false), d = value(codes >> 8, true);  // 2, 6 | 3, 7
+    return make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410),
+                      __byte_perm(a, b, 0x7632), __byte_perm(c, d, 0x7632));
+}
+
+// G words of 32 bits, 4 G-byte aligned, read once.
+template <int G>
+__device__ __forceinline__ void read_words(uint32_t (&w)[G], const uint8_t *p) {
+    if constexpr (G == 4) {
+        const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(p));
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else {
+        const uint2 x = __ldcs(reinterpret_cast<const uint2 *>(p));
+        w[0] = x.x, w[1] = x.y;
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One K tile: rows j0 .. j1 - 1 to `out` (row 0 of the block), rows `stride` halves apart.
+template <int D>
+__device__ __forceinline__ void read_k(const uint8_t *tile, __half *out, int64_t stride, int j0,
+                                       int j1, int lane) {
+    using T = I4Tile<D>;
+    constexpr int G = T::kGroups;
+    const int r = lane >> 2, t = lane & 3;
+    uint32_t w[2][G], st[2][G], ls[2][G / 2];  // rows r and r + 8
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        read_words<G>(w[h], tile + T::k_word(r + 8 * h, 0, t));
+        // steps of rows 2 (r / 2) + (0, 1, 8, 9), group after group
+        read_words<G>(st[h], tile + T::step(r & 6, 0) + 4 * G * h);
+        if constexpr (G == 4) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(tile + T::least_k(r + 8 * h, 0));
+            ls[h][0] = x.x, ls[h][1] = x.y;
+        } else {
+            ls[h][0] = *reinterpret_cast<const uint32_t *>(tile + T::least_k(r + 8 * h, 0));
+        }
+    }
+    const uint32_t pick = (r & 1) ? 0x3232u : 0x1010u;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = r + 8 * h;
+            const uint32_t s = __byte_perm(st[g / (G / 2)][2 * (g % (G / 2)) + h], 0u, pick);
+            const uint32_t m = __byte_perm(ls[h][g / 2], 0u, (g & 1) ? 0x3232u : 0x1010u);
+            if (j >= j0 && j < j1)
+                __stcs(reinterpret_cast<uint4 *>(out + j * stride + 32 * g + 8 * t),
+                       dequantise8(w[h][g], s, m));
+        }
+}
+
+// One V tile, likewise.  Lane = (half h of the rows, t, i): rows 8 h + 2 t and + 1,
+// values 32 g + 8 i .. + 7.
+template <int D>
+__device__ __forceinline__ void read_v(const uint8_t *tile, __half *out, int64_t stride, int j0,
+                                       int j1, int lane) {
+    using T = I4Tile<D>;
+    constexpr int G = T::kGroups;
+    const int i = lane & 3, t = (lane >> 2) & 3, h = lane >> 4;
+    const int j = 8 * h + 2 * t;
+    uint32_t w0[G], w1[G], st[2][G], ls[2][G];
+    read_words<G>(w0, tile + T::v_half(j, 0, 2 * i));
+    read_words<G>(w1, tile + T::v_half(j, 0, 2 * i + 1));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        read_words<G>(st[k], tile + T::step(2 * t, 0) + 4 * G * k);
+        read_words<G>(ls[k], tile + T::least_v(2 * t, 0) + 4 * G * k);
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        // words 2 g + h: rows j and j + 1
+        const uint32_t *sp = &st[g / (G / 2)][2 * (g % (G / 2))];
+        const uint32_t *mp = &ls[g / (G / 2)][2 * (g % (G / 2))];
+        const uint32_t sw = h ? sp[1] : sp[0], mw = h ? mp[1] : mp[0];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (j + k >= j0 && j + k < j1)
+                __stcs(reinterpret_cast<uint4 *>(out + (j + k) * stride + 32 * g + 8 * i),
+                       dequantise8(__byte_perm(w0[g], w1[g], k ? 0x7632 : 0x5410),
+                                   __byte_perm(sw, 0u, k ? 0x3232 : 0x1010),
+                                   __byte_perm(mw, 0u, k ? 0x3232 : 0x1010)));
+    }
 }
 
 // kScratch false: rows of sequences to the caller's row positions.
@@ -184,7 +304,6 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t codes, float s, float m) {
 template <int D, bool kScratch>
 __global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const ReadI4Args a) {
     using T = I4Tile<D>;
-    constexpr int kPieces = D / 8;
     extern __shared__ int64_t prefix[];  // [B + 1] blocks of the sequences before
     const int tid = threadIdx.x, lane = tid & 31;
     for (int s = tid; s < a.B; s += kReadThreads) {
@@ -222,7 +341,13 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const ReadI4Ar
     }
     __syncthreads();
     const int64_t units = prefix[a.B];
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    // warps take (block, head) pairs, the heads of a block side by side
+    const int64_t items = units * a.Hk;
+    const int64_t warps = (int64_t)gridDim.x * (kReadThreads / 32);
+    const int64_t stride = (int64_t)a.Hk * D;
+    for (int64_t x = (int64_t)blockIdx.x * (kReadThreads / 32) + (tid >> 5); x < items; x += warps) {
+        const int64_t u = (x >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)a.Hk) : x / a.Hk;
+        const int h = (int)(x - u * a.Hk);
         int lo = 0, hi = a.B - 1;  // largest s with prefix[s] <= u
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -244,7 +369,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const ReadI4Ar
         if constexpr (kScratch) {
             row0 = u * kBlockSize;
             const bool fits = row0 + kBlockSize <= a.total_rows;
-            if (tid == 0) {
+            if (h == 0 && lane == 0) {
                 a.scratch_table[(int64_t)s * a.maxb + b] = blk_ok && fits ? (int32_t)u : -1;
                 if (!fits) report(a.status, PA_DEV_WORKSPACE);
             }
@@ -253,37 +378,15 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const ReadI4Ar
             row0 = (int64_t)__ldg(a.rows + s) + b * kBlockSize - f;
         }
         if (!blk_ok) {
-            if (tid == 0) report(a.status, PA_DEV_BAD_BLOCK);
+            if (h == 0 && lane == 0) report(a.status, PA_DEV_BAD_BLOCK);
             continue;
         }
         const int j0 = (int)max((int64_t)0, f - b * kBlockSize);
         const int j1 = (int)min((int64_t)kBlockSize, f + len - b * kBlockSize);
-        const uint8_t *tiles = a.tiles + (int64_t)blk * a.Hk * T::kPair;
-        for (int i = tid; i < (j1 - j0) * a.Hk * kPieces; i += kReadThreads) {
-            const int piece = i % kPieces, h = i / kPieces % a.Hk, j = j0 + i / kPieces / a.Hk;
-            const int g = piece >> 2, t8 = piece & 3;
-            const int64_t at = ((row0 + j) * a.Hk + h) * D + piece * 8;
-            const uint8_t *kt = tiles + (int64_t)h * T::kPair, *vt = kt + T::kBytes;
-            if (a.k_out) {
-                const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(kt + T::k_word(j, g, t8)));
-                const float st = __half2float(
-                    __ldg(reinterpret_cast<const __half *>(kt + T::step(j, g))));
-                const float m = __half2float(
-                    __ldg(reinterpret_cast<const __half *>(kt + T::least_k(j, g))));
-                *reinterpret_cast<uint4 *>(a.k_out + at) = dequantise8(c, st, m);
-            }
-            if (a.v_out) {
-                const uint32_t c0 = __ldg(
-                    reinterpret_cast<const uint16_t *>(vt + T::v_half(j, g, 2 * t8)));
-                const uint32_t c1 = __ldg(
-                    reinterpret_cast<const uint16_t *>(vt + T::v_half(j, g, 2 * t8 + 1)));
-                const float st = __half2float(
-                    __ldg(reinterpret_cast<const __half *>(vt + T::step(j, g))));
-                const float m = __half2float(
-                    __ldg(reinterpret_cast<const __half *>(vt + T::least_v(j, g))));
-                *reinterpret_cast<uint4 *>(a.v_out + at) = dequantise8(c0 | c1 << 16, st, m);
-            }
-        }
+        const uint8_t *tile = a.tiles + ((int64_t)blk * a.Hk + h) * T::kPair;
+        const int64_t at = row0 * stride + (int64_t)h * D;
+        if (a.k_out) read_k<D>(tile, a.k_out + at, stride, j0, j1, lane);
+        if (a.v_out) read_v<D>(tile + T::kBytes, a.v_out + at, stride, j0, j1, lane);
     }
 }
 
@@ -292,7 +395,7 @@ int launch_read(const ReadI4Args &a, cudaStream_t st) {
     const int sms = sm_count();
     if (sms < 1) return PA_ERR_CUDA;
     const size_t smem = (size_t)(a.B + 1) * sizeof(int64_t);
-    kv_read_i4_kernel<D, kScratch><<<sms * 8, kReadThreads, smem, st>>>(a);
+    kv_read_i4_kernel<D, kScratch><<<sms * kReadCtas, kReadThreads, smem, st>>>(a);
     return launch_status();
 }
 
@@ -388,7 +491,15 @@ extern "C" int pa_rope_kv_write_i4(const void *q, void *q_out, const void *k, co
     a.n_heads = n_heads;
     a.n_kv_heads = n_kv_heads;
     a.max_pos = max_positions;
-    const dim3 grid = token_grid(num_tokens, (n_heads + 2 * n_kv_heads) * (head_dim / 8));
+    // Four CTAs per SM; with fewer tokens than that, a token's rows are spread
+    // over several CTAs, down to one round of rows each.
+    const int sms = sm_count();
+    if (sms < 1) return PA_ERR_CUDA;
+    const int rows = n_heads + 2 * n_kv_heads, round = kTokenThreads / (head_dim / 8);
+    const int rounds = (rows + round - 1) / round;
+    const int split = std::max(1, std::min(rounds, sms * 4 / num_tokens));
+    a.rows_per_cta = (rounds + split - 1) / split * round;
+    const dim3 grid(std::min(num_tokens, sms * 4), (rows + a.rows_per_cta - 1) / a.rows_per_cta);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (head_dim == 128)
         rope_kv_write_i4_kernel<128><<<grid, kTokenThreads, 0, st>>>(a);
