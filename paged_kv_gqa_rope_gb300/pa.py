@@ -620,32 +620,74 @@ def cache_i4_bytes(layers, num_blocks, block_size, n_kv_heads, head_dim) -> int:
     return lib().pa_cache_i4_bytes(layers, num_blocks, block_size, n_kv_heads, head_dim)
 
 
-def _call_on(name, stream, tensors, *args):
-    """lib().<name>(*args, stream) with the tensors' device current, on `stream`
-    or that device's current stream.  All tensors must be on one device."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"{name}: tensors on {dev}, stream on {stream.device}")
-    if dev.index == torch.cuda.current_device():
-        _check(name, getattr(lib(), name)(*args, _stream(stream)))
+# The 4-bit entry points check their tensors with `_on` and pass addresses as
+# plain integers: a call is a few microseconds of Python, as much as its kernel
+# takes on a small batch.
+
+def _on(dev, t, dtype, name, shape):
+    """The address of a contiguous CUDA tensor of `dtype` and exactly `shape`
+    (None entries free) on device number `dev`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous CUDA {dtype} tensor")
+    got = t.shape
+    if got != shape:
+        _check_shape(t, shape, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's device is cuda:{dev}")
+    return t.data_ptr()
+
+
+def _call_on(dev, name, stream, *args):
+    """lib().<name>(*args, stream) with device `dev` current, on `stream` or that
+    device's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"{name}: tensors on cuda:{dev}, stream on {stream.device}")
+    fn = getattr(_lib or lib(), name)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
-            _check(name, getattr(lib(), name)(*args, _stream(stream)))
+            rc = fn(*args, stream.cuda_stream)
+    if rc != PA_OK:
+        raise PAError(name, rc)
+
+
+def _cache_i4(dev, cache):
+    if cache.buffer.get_device() != dev:
+        raise ValueError(f"the cache is on {cache.buffer.device}, the call's device is cuda:{dev}")
+    return ctypes.byref(cache.desc)
+
+
+def _query(q, name="q"):
+    """Device number and sizes of a query tensor [rows, heads, head_dim]."""
+    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3):
+        raise TypeError(f"{name} must be a contiguous CUDA torch.float16 tensor of three dimensions")
+    return q.get_device(), q.shape
+
+
+def _status_i4(dev, status):
+    return None if status is None else _on(dev, status, torch.int32, "status", (1,))
 
 
 def rope_kv_write_i4(q, k, v, positions, slot_mapping, table, cache: CacheI4, layer=0,
                      q_out=None, status=None, stream=None):
     """pa_rope_kv_write_i4: rotates Q (in place, or into `q_out`) and appends the
     quantised rotated K and V (both left as they are).  Returns the rotated Q."""
-    T, H, Hk, d = _rope_args(q, k, v, positions, slot_mapping, table, status)
-    q_out = q if q_out is None else _out(q_out, q, "q_out")
-    _call_on("pa_rope_kv_write_i4", stream,
-             (q, k, v, positions, slot_mapping, table, cache.buffer, q_out, status),
-             _p(q), _p(q_out), _p(k), _p(v), _p(positions), _p(slot_mapping), T, H, Hk, d,
-             _p(table), table.shape[0], ctypes.byref(cache.desc), layer, _p(status))
+    dev, (T, H, d) = _query(q)
+    Hk = _query(k, "k")[1][1]
+    if q_out is None:
+        q_out = q
+    _call_on(dev, "pa_rope_kv_write_i4", stream,
+             _on(dev, q, torch.float16, "q", (T, H, d)),
+             _on(dev, q_out, torch.float16, "q_out", (T, H, d)),
+             _on(dev, k, torch.float16, "k", (T, Hk, d)),
+             _on(dev, v, torch.float16, "v", (T, Hk, d)),
+             _on(dev, positions, torch.int32, "positions", (T,)),
+             _on(dev, slot_mapping, torch.int32, "slot_mapping", (T,)), T, H, Hk, d,
+             _on(dev, table, torch.float32, "table", (None, d // 2, 2)), table.shape[0],
+             _cache_i4(dev, cache), layer, _status_i4(dev, status))
     return q_out
 
 
@@ -654,27 +696,26 @@ def kv_read_i4(cache: CacheI4, block_tables, lengths, row_starts, k_out=None, v_
     """pa_kv_read_i4: tokens first_tokens[s] .. + lengths[s] - 1 of every sequence
     (from its first token by default) as fp16 into rows row_starts[s] .. of k_out
     and v_out [rows, n_kv_heads, head_dim] (None: not read).  Returns (k_out, v_out)."""
-    _dev(block_tables, torch.int32, "block_tables", (None, None))
+    dev = cache.buffer.get_device()
+    tables = _on(dev, block_tables, torch.int32, "block_tables", (None, None))
     B = block_tables.shape[0]
-    _table_width(block_tables)
-    _dev(lengths, torch.int32, "lengths", (B,))
-    _dev(row_starts, torch.int32, "row_starts", (B,))
-    _opt(first_tokens, torch.int32, "first_tokens", (B,))
-    _opt(status, torch.int32, "status", (1,))
     Hk, d = cache.desc.n_kv_heads, cache.desc.head_dim
-    _opt(k_out, torch.float16, "k_out", (None, Hk, d))
-    _opt(v_out, torch.float16, "v_out", (None, Hk, d))
-    rows = [t.shape[0] for t in (k_out, v_out) if t is not None]
-    if len(rows) == 2 and rows[0] != rows[1]:
-        raise ValueError(f"k_out has {rows[0]} rows, v_out {rows[1]}")
-    total = rows[0] if rows else 0
-    if total > 2**31 - 1:
-        raise ValueError(f"{total} output rows: they must stay within int32")
-    _call_on("pa_kv_read_i4", stream,
-             (block_tables, lengths, row_starts, cache.buffer, k_out, v_out, first_tokens, status),
-             ctypes.byref(cache.desc), layer, _p(block_tables), block_tables.shape[1],
-             _p(lengths), _p(first_tokens), _p(row_starts), B, total, Hk, d, _p(k_out),
-             _p(v_out), _p(status))
+    rows = 0
+    if k_out is not None:
+        rows = k_out.shape[0]
+        _on(dev, k_out, torch.float16, "k_out", (None, Hk, d))
+    if v_out is not None:
+        _on(dev, v_out, torch.float16, "v_out", (rows if k_out is not None else None, Hk, d))
+        rows = v_out.shape[0]
+    if rows > 2**31 - 1:
+        raise ValueError(f"{rows} output rows: they must stay within int32")
+    _call_on(dev, "pa_kv_read_i4", stream, ctypes.byref(cache.desc), layer, tables,
+             _table_width(block_tables), _on(dev, lengths, torch.int32, "lengths", (B,)),
+             None if first_tokens is None else
+             _on(dev, first_tokens, torch.int32, "first_tokens", (B,)),
+             _on(dev, row_starts, torch.int32, "row_starts", (B,)), B, rows, Hk, d,
+             None if k_out is None else k_out.data_ptr(),
+             None if v_out is None else v_out.data_ptr(), _status_i4(dev, status))
     return k_out, v_out
 
 
@@ -686,13 +727,16 @@ def decode_i4_workspace(num_seqs, n_heads, n_kv_heads, head_dim, device="cuda"):
 
 def decode_i4(q, cache: CacheI4, block_tables, context_lens, workspace, n_kv_heads, layer=0,
               scale=0.0, out=None, status=None, stream=None):
-    B, H, d = _decode_args(q, block_tables, context_lens, workspace, status)
-    out = _out(out, q)
-    _call_on("pa_decode_i4", stream,
-             (q, block_tables, context_lens, workspace, cache.buffer, out, status),
-             _p(q), ctypes.byref(cache.desc), layer, _p(block_tables), block_tables.shape[1],
-             _p(context_lens), B, H, n_kv_heads, d, float(scale), _p(workspace),
-             workspace.numel(), _p(out), _p(status))
+    dev, (B, H, d) = _query(q)
+    if out is None:
+        out = torch.empty_like(q)
+    _call_on(dev, "pa_decode_i4", stream, _on(dev, q, torch.float16, "q", (B, H, d)),
+             _cache_i4(dev, cache), layer,
+             _on(dev, block_tables, torch.int32, "block_tables", (B, None)),
+             _table_width(block_tables),
+             _on(dev, context_lens, torch.int32, "context_lens", (B,)), B, H, n_kv_heads, d,
+             scale, _on(dev, workspace, torch.uint8, "workspace", (None,)), workspace.numel(),
+             _on(dev, out, torch.float16, "out", (B, H, d)), _status_i4(dev, status))
     return out
 
 
@@ -711,19 +755,16 @@ def prefill_varlen_i4(q, cache: CacheI4, cu_seqlens_q, cu_seqlens_k, block_table
                       n_kv_heads, workspace, layer=0, scale=0.0, out=None, status=None,
                       stream=None):
     """pa_prefill_varlen_i4: varlen causal prefill over the 4-bit pool."""
-    _dev(q, torch.float16, "q", (None, None, None))
-    T, H, d = q.shape
-    _dev(cu_seqlens_q, torch.int32, "cu_seqlens_q", (None,))
-    B = cu_seqlens_q.shape[0] - 1
-    _dev(cu_seqlens_k, torch.int32, "cu_seqlens_k", (B + 1,))
-    _dev(block_tables, torch.int32, "block_tables", (B, None))
-    _table_width(block_tables)
-    _dev(workspace, torch.uint8, "workspace", (None,))
-    _opt(status, torch.int32, "status", (1,))
-    out = _out(out, q)
-    _call_on("pa_prefill_varlen_i4", stream,
-             (q, cu_seqlens_q, cu_seqlens_k, block_tables, workspace, cache.buffer, out, status),
-             _p(q), T, ctypes.byref(cache.desc), layer, _p(cu_seqlens_q), _p(cu_seqlens_k),
-             _p(block_tables), block_tables.shape[1], B, int(max_seqlen_q), H, n_kv_heads, d,
-             float(scale), _p(workspace), workspace.numel(), _p(out), _p(status))
+    dev, (T, H, d) = _query(q)
+    if out is None:
+        out = torch.empty_like(q)
+    tables = _on(dev, block_tables, torch.int32, "block_tables", (None, None))
+    B = block_tables.shape[0]
+    _call_on(dev, "pa_prefill_varlen_i4", stream, _on(dev, q, torch.float16, "q", (T, H, d)), T,
+             _cache_i4(dev, cache), layer,
+             _on(dev, cu_seqlens_q, torch.int32, "cu_seqlens_q", (B + 1,)),
+             _on(dev, cu_seqlens_k, torch.int32, "cu_seqlens_k", (B + 1,)), tables,
+             _table_width(block_tables), B, int(max_seqlen_q), H, n_kv_heads, d, scale,
+             _on(dev, workspace, torch.uint8, "workspace", (None,)), workspace.numel(),
+             _on(dev, out, torch.float16, "out", (T, H, d)), _status_i4(dev, status))
     return out
