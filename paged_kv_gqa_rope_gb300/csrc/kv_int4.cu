@@ -231,8 +231,17 @@ __device__ __forceinline__ void read_words(uint32_t (&w)[G], const uint8_t *p) {
     }
 }
 
+// 8 values of an output row; kKeep: the next kernel reads them, so they stay in L2.
+template <bool kKeep>
+__device__ __forceinline__ void store_row(__half *p, const uint4 &x) {
+    if constexpr (kKeep)
+        *reinterpret_cast<uint4 *>(p) = x;
+    else
+        __stcs(reinterpret_cast<uint4 *>(p), x);
+}
+
 // One K tile: rows j0 .. j1 - 1 to `out` (row 0 of the block), rows `stride` halves apart.
-template <int D>
+template <int D, bool kKeep>
 __device__ __forceinline__ void read_k(const uint8_t *tile, __half *out, int64_t stride, int j0,
                                        int j1, int lane) {
     using T = I4Tile<D>;
@@ -260,14 +269,13 @@ __device__ __forceinline__ void read_k(const uint8_t *tile, __half *out, int64_t
             const uint32_t s = __byte_perm(st[g / (G / 2)][2 * (g % (G / 2)) + h], 0u, pick);
             const uint32_t m = __byte_perm(ls[h][g / 2], 0u, (g & 1) ? 0x3232u : 0x1010u);
             if (j >= j0 && j < j1)
-                __stcs(reinterpret_cast<uint4 *>(out + j * stride + 32 * g + 8 * t),
-                       dequantise8(w[h][g], s, m));
+                store_row<kKeep>(out + j * stride + 32 * g + 8 * t, dequantise8(w[h][g], s, m));
         }
 }
 
 // One V tile, likewise.  Lane = (half h of the rows, t, i): rows 8 h + 2 t and + 1,
 // values 32 g + 8 i .. + 7.
-template <int D>
+template <int D, bool kKeep>
 __device__ __forceinline__ void read_v(const uint8_t *tile, __half *out, int64_t stride, int j0,
                                        int j1, int lane) {
     using T = I4Tile<D>;
@@ -291,10 +299,10 @@ __device__ __forceinline__ void read_v(const uint8_t *tile, __half *out, int64_t
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             if (j + k >= j0 && j + k < j1)
-                __stcs(reinterpret_cast<uint4 *>(out + (j + k) * stride + 32 * g + 8 * i),
-                       dequantise8(__byte_perm(w0[g], w1[g], k ? 0x7632 : 0x5410),
-                                   __byte_perm(sw, 0u, k ? 0x3232 : 0x1010),
-                                   __byte_perm(mw, 0u, k ? 0x3232 : 0x1010)));
+                store_row<kKeep>(out + (j + k) * stride + 32 * g + 8 * i,
+                                 dequantise8(__byte_perm(w0[g], w1[g], k ? 0x7632 : 0x5410),
+                                             __byte_perm(sw, 0u, k ? 0x3232 : 0x1010),
+                                             __byte_perm(mw, 0u, k ? 0x3232 : 0x1010)));
     }
 }
 
@@ -385,8 +393,8 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const ReadI4Ar
         const int j1 = (int)min((int64_t)kBlockSize, f + len - b * kBlockSize);
         const uint8_t *tile = a.tiles + ((int64_t)blk * a.Hk + h) * T::kPair;
         const int64_t at = row0 * stride + (int64_t)h * D;
-        if (a.k_out) read_k<D>(tile, a.k_out + at, stride, j0, j1, lane);
-        if (a.v_out) read_v<D>(tile + T::kBytes, a.v_out + at, stride, j0, j1, lane);
+        if (a.k_out) read_k<D, kScratch>(tile, a.k_out + at, stride, j0, j1, lane);
+        if (a.v_out) read_v<D, kScratch>(tile + T::kBytes, a.v_out + at, stride, j0, j1, lane);
     }
 }
 
