@@ -880,9 +880,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    __threadfence();
+                    asm volatile("fence.acq_rel.gpu;" ::: "memory");
                     seen = atomicAdd(a.counters + qrow, 1);
-                    __threadfence();
+                    asm volatile("fence.acq_rel.gpu;" ::: "memory");
                 }
                 if (__shfl_sync(0xffffffffu, seen, 0) != n - 1) continue;
                 own = -1;
