@@ -34,53 +34,62 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // One group's 8 values held by this lane, its other 24 by the lanes of the
 // same aligned quad: the group's step and least value and this lane's codes,
 // value i in nibble i.  Every lane of the warp takes part.
 __device__ __forceinline__ uint32_t quantise8(const uint4 x, __half &step, __half &least) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    // (min, -max) as a pair, reduced together; a NaN or an infinity shows in
-    // the exponent bits, which the minimum of a NaN would not
-    __half2 mm = __hmin2(__hmin2(as_half2(w[0]), as_half2(w[1])),
-                         __hmin2(as_half2(w[2]), as_half2(w[3])));
-    __half2 nx = __hmin2(__hmin2(__hneg2(as_half2(w[0])), __hneg2(as_half2(w[1]))),
-                         __hmin2(__hneg2(as_half2(w[2])), __hneg2(as_half2(w[3]))));
-    __half2 r = __hmin2(__lows2half2(mm, nx), __highs2half2(mm, nx));
-    bool odd = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        odd |= (w[i] & 0x7c00u) == 0x7c00u || (w[i] & 0x7c000000u) == 0x7c000000u;
+    // (min, -max) as a pair, reduced together; a NaN stays one
+    const __half2 mn = __hmin2_nan(__hmin2_nan(as_half2(w[0]), as_half2(w[1])),
+                                   __hmin2_nan(as_half2(w[2]), as_half2(w[3])));
+    const __half2 mx = __hneg2(__hmax2_nan(__hmax2_nan(as_half2(w[0]), as_half2(w[1])),
+                                           __hmax2_nan(as_half2(w[2]), as_half2(w[3]))));
+    __half2 r = __hmin2_nan(__lows2half2(mn, mx), __highs2half2(mn, mx));
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1)
-        r = __hmin2(r, as_half2(__shfl_xor_sync(0xffffffffu, as_u32(r), o)));
-    const uint32_t quad = 0xfu << (threadIdx.x & 28);
-    odd = (__ballot_sync(0xffffffffu, odd) & quad) != 0;
+        r = __hmin2_nan(r, as_half2(__shfl_xor_sync(0xffffffffu, as_u32(r), o)));
     const float lo = __low2float(r) + 0.f;  // (-0 becomes +0)
     const float range = __fsub_rn(-__high2float(r), lo);
-    step = __float2half_ru(__fdiv_rn(range, 15.f));
+    // The range's fifteenth rounded up to fp16: the nearest fp16 of a product
+    // that is within 2^-22 of it, or the next one if 15 times that (exact) falls
+    // short of the range.
+    __half s16 = __float2half_rn(range * (1.f / 15.f));
+    if (15.f * __half2float(s16) < range) s16 = __ushort_as_half(__half_as_ushort(s16) + 1);
+    step = s16;
     least = __float2half_rn(lo);
-    if (odd) {
+    if (!(range <= 131008.f)) {  // a NaN or an infinity among them
         step = __ushort_as_half(0);
         least = __ushort_as_half(0x7fff);
     }
     const float s = __half2float(step);
     if (!(s > 0.f)) return 0u;
-    // rint((v - lo) / s): the quotient by a reciprocal, which is within 2^-17 of
-    // the divided one, unless that leaves the rounding open (then by division).
-    // Adding 1.5 2^23 rounds to an integer, ties to even; the quotient is at
-    // most 15 (1 + 2^-22), since s is not below the range's fifteenth.
+    // rint((v - lo) / s): the quotient by an approximate reciprocal, which is
+    // within 2^-16 of the divided one, unless that leaves the rounding open
+    // (then by division).  Adding 1.5 2^23 rounds to an integer, ties to even;
+    // the quotient is at most 15 (1 + 2^-21), since 15 s is not below the range.
     constexpr float kRint = 12582912.f;
-    const float inv = __frcp_rn(s);
-    float c[8];
-    bool open = false;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const uint64_t lo2 = f2_pack(-lo, -lo), inv2 = f2_pack(inv, inv);
+    const uint64_t rint2 = f2_pack(kRint, kRint), back2 = f2_pack(-kRint, -kRint);
+    float c[8], off = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const __half2 h = as_half2(w[i >> 1]);
-        const float q = __fsub_rn((i & 1) ? __high2float(h) : __low2float(h), lo) * inv;
-        c[i] = __fsub_rn(__fadd_rn(q, kRint), kRint);
-        open |= fabsf(q - c[i]) > 0.4999f;
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = __half22float2(as_half2(w[i]));
+        const uint64_t q = f2_mul(f2_add(f2_pack(v.x, v.y), lo2), inv2);
+        const uint64_t n = f2_add(f2_add(q, rint2), back2);
+        f2_unpack(n, c[2 * i], c[2 * i + 1]);
+        float q0, q1;
+        f2_unpack(q, q0, q1);
+        off = fmaxf(off, fmaxf(fabsf(q0 - c[2 * i]), fabsf(q1 - c[2 * i + 1])));
     }
-    if (open) {
+    if (off > 0.4999f) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const __half2 h = as_half2(w[i >> 1]);
