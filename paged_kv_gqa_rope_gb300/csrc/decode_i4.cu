@@ -437,7 +437,9 @@ struct State {
 // What a warp leaves of a pair that it does not finish by itself.
 struct Piece {
     int64_t start;  // the pair's first unit; negative (its own for each piece): none
-    int s, kvh, nblk, pad;
+    int row;        // the pair's first row of the output
+    int first, n;   // the CTAs that hold the pair, if there are several (n = 0: only this one)
+    int pad;
 };
 
 template <int D>
@@ -621,6 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
     if (cta * kWarps >= A) return;
     const int me = cta * kWarps + warp;
     const Cuts cuts(W, A);
+    const int c0 = cta * kWarps;
+    const int64_t cta_begin = cuts.start(c0), cta_end = cuts.start(min(A, c0 + kWarps));
 
     if (me < A) {
         const int64_t begin = cuts.start(me), end = cuts.start(me + 1);
@@ -789,11 +793,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
                         sm.l[2 * warp + k][r] = st.l;
                     }
                     if (lane == 0) {
-                        Piece &p = sm.piece[2 * warp + k];
+                        Piece p;
                         p.start = cur.start;
-                        p.s = cur.s;
-                        p.kvh = cur.kvh;
-                        p.nblk = cur.nblk;
+                        p.row = cur.s * a.H + cur.kvh * a.g;
+                        p.first = p.n = p.pad = 0;
+                        if (cur.start < cta_begin || cur.start + cur.nblk > cta_end) {
+                            p.first = cuts.range_of(cur.start) / kWarps;
+                            p.n = cuts.range_of(cur.start + cur.nblk - 1) / kWarps - p.first + 1;
+                        }
+                        sm.piece[2 * warp + k] = p;
                     }
                 }
             }
@@ -805,11 +813,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
 
     // -------- pairs cut between warps.  In every warp, lane k speaks for piece
     // k (in the order of the line) and knows the pieces of the same pair.
-    const int c0 = cta * kWarps, c1 = min(A, c0 + kWarps);
-    const int64_t cta_begin = cuts.start(c0), cta_end = cuts.start(c1);
     Piece p;
     p.start = -1 - lane;
-    p.s = p.kvh = p.nblk = 0;
+    p.row = p.first = p.n = 0;
     if (lane < 2 * kWarps) p = sm.piece[lane];
     const uint32_t same = __match_any_sync(0xffffffffu, (unsigned long long)p.start);
     const uint32_t heads = __ballot_sync(0xffffffffu, p.start >= 0 && lane == __ffs(same) - 1);
@@ -825,31 +831,24 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
         for (int k = which; k > 0; --k) rest &= rest - 1;
         const int lead = __ffs(rest) - 1;
         const uint32_t members = __shfl_sync(0xffffffffu, same, lead);
-        const int64_t start = __shfl_sync(0xffffffffu, p.start, lead);
-        const int nblk = __shfl_sync(0xffffffffu, p.nblk, lead);
-        const int qrow = __shfl_sync(0xffffffffu, p.s, lead) * a.H +
-                         __shfl_sync(0xffffffffu, p.kvh, lead) * a.g + h;
-        // A row cut between CTAs: each leaves a record of it (slot 0 if the pair
-        // began before the CTA's range, else 1) and arrives on the row's counter;
-        // the last joins the records.  If the others' have all arrived already,
-        // this CTA needs neither record nor arrival of its own.
-        const bool cut = start < cta_begin || start + nblk > cta_end;
-        // A piece in the workspace (the members' last, if any) is asked for
-        // before the counter is read, whose acquire holds up later loads.
+        const int qrow = __shfl_sync(0xffffffffu, p.row, lead) + h;
+        // A row cut between CTAs: each leaves a record of it (slot 1 the pair's
+        // first CTA, whose last pair it is, slot 0 the others) and arrives on the
+        // row's counter; the last joins the records.  If the others' have all
+        // arrived already, this CTA needs neither record nor arrival of its own.
+        const int first = __shfl_sync(0xffffffffu, p.first, lead);
+        const int n = __shfl_sync(0xffffffffu, p.n, lead);
+        // A piece in the workspace (the members' last, if any) is asked for first.
         const int tail = 31 - __clz(members);
         float v[N];
         if (!(tail & 1))
             load_cols<N>(v, a.lead + ((int64_t)(c0 + (tail >> 1)) * kGroupPad + h) * D + lane * N);
-        int first = 0, n = 1, seen = 0;
-        if (cut) {
-            first = cuts.range_of(start) / kWarps;
-            n = cuts.range_of(start + nblk - 1) / kWarps - first + 1;
-            if (lane == 0)
-                asm volatile("ld.acquire.gpu.global.s32 %0, [%1];"
-                             : "=r"(seen)
-                             : "l"(a.counters + qrow)
-                             : "memory");
-        }
+        int seen = 0;
+        if (n && lane == 0)
+            asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];"
+                         : "=r"(seen)
+                         : "l"(a.counters + qrow)
+                         : "memory");
         const bool in = members >> lane & 1;
         const float pm = in ? sm.m[lane][h] : kNoMax;
         Row<D> r;
@@ -867,12 +866,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
             r.add(__shfl_sync(0xffffffffu, f, k), w);
         }
         if (!(tail & 1)) r.add(__shfl_sync(0xffffffffu, f, tail), v);
-        if (cut) {
+        if (n) {
             int own = cta - first;
             if (__shfl_sync(0xffffffffu, seen, 0) != n - 1) {
                 float *rec =
-                    a.rec +
-                    (((int64_t)cta * 2 + (start >= cta_begin)) * kGroupPad + h) * (D + 4);
+                    a.rec + (((int64_t)cta * 2 + (own == 0)) * kGroupPad + h) * (D + 4);
                 store_cols<N>(rec + lane * N, r.o);
                 if (lane == 0) {
                     rec[D] = r.m;
@@ -886,6 +884,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
                 }
                 if (__shfl_sync(0xffffffffu, seen, 0) != n - 1) continue;
                 own = -1;
+            } else {
+                asm volatile("fence.acq_rel.gpu;" ::: "memory");
             }
             __syncwarp();
             r = join_records<D>(a, first, n, h, own, r, lane);
