@@ -438,6 +438,56 @@ def test_decode_two_streams_at_once():
         assert torch.equal(out, w)
 
 
+def test_decode_4096_sequences():
+    rng = np.random.default_rng(57)
+    ctxs = rng.integers(1, 40, 4096)
+    ctxs[:5] = [1, 16, 17, 700, 1]
+    check_decode(*decode_case(57, 2, 1, 64, ctxs), 1)
+
+
+@pytest.mark.parametrize("H,Hk,d", [(32, 8, 128), (8, 2, 64)])
+def test_pool_past_32_bits(H, Hk, d):
+    """Blocks whose bytes lie past 2^32 (and 2^33) of the pool, in a layer past the
+    first: append, read back, prefill and decode."""
+    rng = np.random.default_rng(58)
+    NB = 9_000_000_000 // (2 * Hk * 20 * d)
+    cache = pa.CacheI4(2, NB, Hk, d)
+    assert cache.buffer.numel() > 2**33
+    bt = np.array([[NB - 1, 3, NB - 2, NB // 2], [NB - 5, NB - 4, 0, NB - 3]], np.int32)
+    n = np.array([60, 33], np.int32)
+    md = pa.prepare_prefill([0, 0], n, bt)
+    q, k, v = (normal16(rng, 93, h, d) for h in (H, Hk, Hk))
+    qd, status = dev(q), pa.new_status()
+    pa.rope_kv_write_i4(qd, dev(k), dev(v), dev(md["positions"]), dev(md["slot_mapping"]),
+                        pa.rope_table(64, d), cache, layer=1, status=status)
+    # the same rows in a small pool, on the host
+    small = np.where(bt >= 0, np.arange(8).reshape(2, 4), -1).astype(np.int32)
+    md2 = pa.prepare_prefill([0, 0], n, small)
+    tiles = orc.new_cache_i4(1, 8, Hk, d)
+    q_rot = orc.rope_pinned(q, md["positions"], d)
+    orc.kv_write_i4(tiles, 0, orc.rope_pinned(k, md["positions"], d), v, md2["slot_mapping"])
+    assert np.array_equal(cache.tiles[1][torch.from_numpy(bt.reshape(-1)).cuda().long()].cpu().numpy()
+                          [:4].reshape(4, -1)[:3], tiles[0, :3].reshape(3, -1))
+    ko, vo = (torch.empty(93, Hk, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    pa.kv_read_i4(cache, dev(bt), dev(n), dev(np.array([0, 60], np.int32)), ko, vo, layer=1,
+                  status=status)
+    vals = orc.read_rows_i4(orc.dequantize_cache_i4(tiles))[:, 0].reshape(2, 2, 64, Hk, d)
+    for kv, got in enumerate((ko, vo)):
+        want = np.concatenate([vals[kv, s][:m] for s, m in enumerate(n)])
+        assert np.array_equal(bits(got), bits(want))
+    ws = pa.prefill_i4_workspace(8, 2, 4, Hk, d)
+    out = pa.prefill_varlen_i4(qd, cache, dev(md["cu_seqlens_q"]), dev(md["cu_seqlens_k"]), dev(bt),
+                               60, Hk, ws, layer=1, status=status)
+    assert_attention_close(out, prefill_want(q_rot, tiles, small,
+                                             (md["cu_seqlens_q"], md["cu_seqlens_k"]), Hk))
+    last = q_rot[[59, 92]]
+    got = pa.decode_i4(dev(last), cache, dev(bt), dev(n), pa.decode_i4_workspace(2, H, Hk, d), Hk,
+                       layer=1, status=status)
+    want, tol = decode_want(last, tiles, 0, small, n, Hk)
+    assert (np.abs(got.cpu().numpy() - want) <= tol).all()
+    assert int(status.item()) == 0
+
+
 # ------------------------------------------------------------------ prefill
 
 def prefill_case(seed, H, Hk, d, past, new, layers=1):
