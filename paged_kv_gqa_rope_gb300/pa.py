@@ -621,20 +621,28 @@ def cache_i4_bytes(layers, num_blocks, block_size, n_kv_heads, head_dim) -> int:
 
 
 # The 4-bit entry points check their tensors with `_on` and pass addresses as
-# plain integers: a call is a few microseconds of Python, as much as its kernel
-# takes on a small batch.
+# plain integers: on a small batch the Python of a call takes longer than its
+# kernel.
 
-def _on(dev, t, dtype, name, shape):
-    """The address of a contiguous CUDA tensor of `dtype` and exactly `shape`
-    (None entries free) on device number `dev`."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
-        raise TypeError(f"{name} must be a contiguous CUDA {dtype} tensor")
-    got = t.shape
-    if got != shape:
-        _check_shape(t, shape, name)
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's device is cuda:{dev}")
-    return t.data_ptr()
+def _on(dev, t, dtype, name, *shape):
+    """The address of a contiguous CUDA tensor of `dtype` and exactly `shape` on
+    device number `dev`."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name, shape)
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's device is cuda:{dev}")
+
+
+def _sizes(t, n, name):
+    """The n sizes of a CUDA tensor."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {n} dimensions")
+    return t.shape
 
 
 def _call_on(dev, name, stream, *args):
@@ -660,33 +668,26 @@ def _cache_i4(dev, cache):
     return ctypes.byref(cache.desc)
 
 
-def _query(q, name="q"):
-    """Device number and sizes of a query tensor [rows, heads, head_dim]."""
-    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3):
-        raise TypeError(f"{name} must be a contiguous CUDA torch.float16 tensor of three dimensions")
-    return q.get_device(), q.shape
-
-
 def _status_i4(dev, status):
-    return None if status is None else _on(dev, status, torch.int32, "status", (1,))
+    return None if status is None else _on(dev, status, torch.int32, "status", 1)
 
 
 def rope_kv_write_i4(q, k, v, positions, slot_mapping, table, cache: CacheI4, layer=0,
                      q_out=None, status=None, stream=None):
     """pa_rope_kv_write_i4: rotates Q (in place, or into `q_out`) and appends the
     quantised rotated K and V (both left as they are).  Returns the rotated Q."""
-    dev, (T, H, d) = _query(q)
-    Hk = _query(k, "k")[1][1]
+    T, H, d = _sizes(q, 3, "q")
+    Hk = _sizes(k, 3, "k")[1]
+    rows = _sizes(table, 3, "table")[0]
+    dev = q.get_device()
     if q_out is None:
         q_out = q
-    _call_on(dev, "pa_rope_kv_write_i4", stream,
-             _on(dev, q, torch.float16, "q", (T, H, d)),
-             _on(dev, q_out, torch.float16, "q_out", (T, H, d)),
-             _on(dev, k, torch.float16, "k", (T, Hk, d)),
-             _on(dev, v, torch.float16, "v", (T, Hk, d)),
-             _on(dev, positions, torch.int32, "positions", (T,)),
-             _on(dev, slot_mapping, torch.int32, "slot_mapping", (T,)), T, H, Hk, d,
-             _on(dev, table, torch.float32, "table", (None, d // 2, 2)), table.shape[0],
+    _call_on(dev, "pa_rope_kv_write_i4", stream, _on(dev, q, torch.float16, "q", T, H, d),
+             _on(dev, q_out, torch.float16, "q_out", T, H, d),
+             _on(dev, k, torch.float16, "k", T, Hk, d), _on(dev, v, torch.float16, "v", T, Hk, d),
+             _on(dev, positions, torch.int32, "positions", T),
+             _on(dev, slot_mapping, torch.int32, "slot_mapping", T), T, H, Hk, d,
+             _on(dev, table, torch.float32, "table", rows, d // 2, 2), rows,
              _cache_i4(dev, cache), layer, _status_i4(dev, status))
     return q_out
 
@@ -696,26 +697,22 @@ def kv_read_i4(cache: CacheI4, block_tables, lengths, row_starts, k_out=None, v_
     """pa_kv_read_i4: tokens first_tokens[s] .. + lengths[s] - 1 of every sequence
     (from its first token by default) as fp16 into rows row_starts[s] .. of k_out
     and v_out [rows, n_kv_heads, head_dim] (None: not read).  Returns (k_out, v_out)."""
+    B, width = _sizes(block_tables, 2, "block_tables")
     dev = cache.buffer.get_device()
-    tables = _on(dev, block_tables, torch.int32, "block_tables", (None, None))
-    B = block_tables.shape[0]
     Hk, d = cache.desc.n_kv_heads, cache.desc.head_dim
-    rows = 0
-    if k_out is not None:
-        rows = k_out.shape[0]
-        _on(dev, k_out, torch.float16, "k_out", (None, Hk, d))
-    if v_out is not None:
-        _on(dev, v_out, torch.float16, "v_out", (rows if k_out is not None else None, Hk, d))
-        rows = v_out.shape[0]
+    out = k_out if k_out is not None else v_out
+    rows = 0 if out is None else _sizes(out, 3, "k_out" if out is k_out else "v_out")[0]
     if rows > 2**31 - 1:
         raise ValueError(f"{rows} output rows: they must stay within int32")
-    _call_on(dev, "pa_kv_read_i4", stream, ctypes.byref(cache.desc), layer, tables,
-             _table_width(block_tables), _on(dev, lengths, torch.int32, "lengths", (B,)),
+    _call_on(dev, "pa_kv_read_i4", stream, ctypes.byref(cache.desc), layer,
+             _on(dev, block_tables, torch.int32, "block_tables", B, width),
+             _table_width(block_tables), _on(dev, lengths, torch.int32, "lengths", B),
              None if first_tokens is None else
-             _on(dev, first_tokens, torch.int32, "first_tokens", (B,)),
-             _on(dev, row_starts, torch.int32, "row_starts", (B,)), B, rows, Hk, d,
-             None if k_out is None else k_out.data_ptr(),
-             None if v_out is None else v_out.data_ptr(), _status_i4(dev, status))
+             _on(dev, first_tokens, torch.int32, "first_tokens", B),
+             _on(dev, row_starts, torch.int32, "row_starts", B), B, rows, Hk, d,
+             None if k_out is None else _on(dev, k_out, torch.float16, "k_out", rows, Hk, d),
+             None if v_out is None else _on(dev, v_out, torch.float16, "v_out", rows, Hk, d),
+             _status_i4(dev, status))
     return k_out, v_out
 
 
@@ -727,16 +724,18 @@ def decode_i4_workspace(num_seqs, n_heads, n_kv_heads, head_dim, device="cuda"):
 
 def decode_i4(q, cache: CacheI4, block_tables, context_lens, workspace, n_kv_heads, layer=0,
               scale=0.0, out=None, status=None, stream=None):
-    dev, (B, H, d) = _query(q)
+    B, H, d = _sizes(q, 3, "q")
+    width = _sizes(block_tables, 2, "block_tables")[1]
+    nbytes = _sizes(workspace, 1, "workspace")[0]
+    dev = q.get_device()
     if out is None:
         out = torch.empty_like(q)
-    _call_on(dev, "pa_decode_i4", stream, _on(dev, q, torch.float16, "q", (B, H, d)),
+    _call_on(dev, "pa_decode_i4", stream, _on(dev, q, torch.float16, "q", B, H, d),
              _cache_i4(dev, cache), layer,
-             _on(dev, block_tables, torch.int32, "block_tables", (B, None)),
-             _table_width(block_tables),
-             _on(dev, context_lens, torch.int32, "context_lens", (B,)), B, H, n_kv_heads, d,
-             scale, _on(dev, workspace, torch.uint8, "workspace", (None,)), workspace.numel(),
-             _on(dev, out, torch.float16, "out", (B, H, d)), _status_i4(dev, status))
+             _on(dev, block_tables, torch.int32, "block_tables", B, width),
+             _table_width(block_tables), _on(dev, context_lens, torch.int32, "context_lens", B), B,
+             H, n_kv_heads, d, scale, _on(dev, workspace, torch.uint8, "workspace", nbytes), nbytes,
+             _on(dev, out, torch.float16, "out", B, H, d), _status_i4(dev, status))
     return out
 
 
@@ -755,16 +754,18 @@ def prefill_varlen_i4(q, cache: CacheI4, cu_seqlens_q, cu_seqlens_k, block_table
                       n_kv_heads, workspace, layer=0, scale=0.0, out=None, status=None,
                       stream=None):
     """pa_prefill_varlen_i4: varlen causal prefill over the 4-bit pool."""
-    dev, (T, H, d) = _query(q)
+    T, H, d = _sizes(q, 3, "q")
+    B, width = _sizes(block_tables, 2, "block_tables")
+    nbytes = _sizes(workspace, 1, "workspace")[0]
+    dev = q.get_device()
     if out is None:
         out = torch.empty_like(q)
-    tables = _on(dev, block_tables, torch.int32, "block_tables", (None, None))
-    B = block_tables.shape[0]
-    _call_on(dev, "pa_prefill_varlen_i4", stream, _on(dev, q, torch.float16, "q", (T, H, d)), T,
+    _call_on(dev, "pa_prefill_varlen_i4", stream, _on(dev, q, torch.float16, "q", T, H, d), T,
              _cache_i4(dev, cache), layer,
-             _on(dev, cu_seqlens_q, torch.int32, "cu_seqlens_q", (B + 1,)),
-             _on(dev, cu_seqlens_k, torch.int32, "cu_seqlens_k", (B + 1,)), tables,
+             _on(dev, cu_seqlens_q, torch.int32, "cu_seqlens_q", B + 1),
+             _on(dev, cu_seqlens_k, torch.int32, "cu_seqlens_k", B + 1),
+             _on(dev, block_tables, torch.int32, "block_tables", B, width),
              _table_width(block_tables), B, int(max_seqlen_q), H, n_kv_heads, d, scale,
-             _on(dev, workspace, torch.uint8, "workspace", (None,)), workspace.numel(),
-             _on(dev, out, torch.float16, "out", (T, H, d)), _status_i4(dev, status))
+             _on(dev, workspace, torch.uint8, "workspace", nbytes), nbytes,
+             _on(dev, out, torch.float16, "out", T, H, d), _status_i4(dev, status))
     return out
