@@ -170,15 +170,18 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// The two fp16 of a word as a pair of fp32.
-__device__ __forceinline__ uint64_t f2_of_half2(uint32_t w) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-    return f2_pack(f.x, f.y);
+// (hi + lo) s of two fp16 pairs, rounded to fp16 (lo s, far below it, before).
+__device__ __forceinline__ uint32_t times(uint32_t hi, uint32_t lo, uint32_t s) {
+    const __half2 x = *reinterpret_cast<const __half2 *>(&s);
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&hi), x,
+                              __hmul2(*reinterpret_cast<const __half2 *>(&lo), x));
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
-__device__ __forceinline__ uint32_t half2_of_f2(uint64_t v) {
-    float lo, hi;
-    f2_unpack(v, lo, hi);
-    return pack_half2(lo, hi);
+// (movmatrix_trans without volatile)
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 // G consecutive words (G = 4 or 2) of shared memory, 4 G-byte aligned.
@@ -194,22 +197,19 @@ __device__ __forceinline__ void ld_words(uint32_t (&w)[G], const uint8_t *p) {
 }
 
 // One warp's state of the softmax over the keys it has seen of one pair.
-// Lane = 4 r + t (r = 0..7, t = 0..3).  Head r: m, l (this lane's keys only)
-// and the Q fragments; heads 2 t, 2 t + 1: the accumulators of O^T, rows
-// (values of V) 32 grp + 4 r + n:
+// Lane = 4 r + t (r = 0..7, t = 0..3).  Head r: the Q fragments; heads 2 t, 2 t + 1:
+// the scores of keys r and r + 8 of a block, m, l (this lane's keys only) and the
+// accumulators of O^T, rows (values of V) 32 grp + 4 r + n:
 //   o[2 grp][0..1] n = 0, [2..3] n = 1; o[2 grp + 1][0..1] n = 2, [2..3] n = 3,
 // in units of 2^-24 (n even) and 2^-20 (n odd); row grp of z: the sum of p times
 // the centre of group grp; e[grp]: -8 times the sum of its p s.
 template <int D>
 struct State {
     static constexpr int G = D / 32;
-    // A fragments of Q: rows 0-7 are the heads with a group's codes of weight 1,
-    // rows 8-15 the heads with its codes of weight 16 (each multiplied by both
-    // kinds of codes; half of either product is not used)
-    uint32_t qa[G][4];
-    uint32_t qsum;          // A fragment of the groups' sums of q, high and low parts
-    float qs;               // scores -> log2 units
-    float m, l;
+    uint32_t qb[G][4];  // B fragments of Q^T: a group's codes of weight 1, then of weight 16
+    uint32_t qsum;      // B fragment of the groups' sums of q, high and low parts
+    float qs[2];        // scores -> log2 units
+    float m[2], l[2];
     float o[2 * G][4], z[4];
     uint64_t e[G];
 
@@ -234,7 +234,9 @@ struct State {
         const int ex = __float_as_int(amax) >> 23;
         const bool fine = amax > 0.f && amax <= 65504.f;
         const float up = fine ? __int_as_float((263 - ex) << 23) : 1.f;
-        qs = a.scale_log2 * 0x1p24f * (fine ? __int_as_float((ex - 9) << 23) : 1.f);
+        const float down = a.scale_log2 * 0x1p24f * (fine ? __int_as_float((ex - 9) << 23) : 1.f);
+        qs[0] = __shfl_sync(0xffffffffu, down, 8 * t);
+        qs[1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
         float sum[G];
 #pragma unroll
         for (int i = 0; i < G; ++i) {
@@ -247,10 +249,10 @@ struct State {
                 f[2 * k + 1] = y.y * up;
             }
             // codes 0, 4 | 2, 6 at weight 1; codes 1, 5 | 3, 7 at weight 16
-            qa[i][0] = pack_half2(f[0], f[4]);
-            qa[i][2] = pack_half2(f[2], f[6]);
-            qa[i][1] = pack_half2(f[1] * 0.0625f, f[5] * 0.0625f);
-            qa[i][3] = pack_half2(f[3] * 0.0625f, f[7] * 0.0625f);
+            qb[i][0] = pack_half2(f[0], f[4]);
+            qb[i][1] = pack_half2(f[2], f[6]);
+            qb[i][2] = pack_half2(f[1] * 0.0625f, f[5] * 0.0625f);
+            qb[i][3] = pack_half2(f[3] * 0.0625f, f[7] * 0.0625f);
             sum[i] = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
             sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
             sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
@@ -265,8 +267,8 @@ struct State {
             if (t == (G + i) / 2)
                 qsum = pack_half2(sum[i] - __half2float(h0), sum[i + 1] - __half2float(h1));
         }
-        m = kNoMax;
-        l = 0.f;
+        m[0] = m[1] = kNoMax;
+        l[0] = l[1] = 0.f;
 #pragma unroll
         for (int i = 0; i < 2 * G; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         z[0] = z[1] = z[2] = z[3] = 0.f;
@@ -281,82 +283,97 @@ struct State {
         static_assert(NB == 1 || !kTail, "");
         const int r = lane >> 2, t = lane & 3;
         using T = I4Tile<D>;
-        // scores of head r, keys 8 h + 2 t and + 1 of each block: chain c = 2 block + h
-        constexpr int C = 2 * NB;
-        uint32_t w[C][G], st[NB][2][G];  // st: steps, word 2 grp + h
-        uint64_t acc[C];
+        // scores of keys r (y[.][0..1]: heads 2 t, 2 t + 1) and r + 8 (y[.][2..3])
+        float y[NB][4];
+        uint32_t w[NB][2][G];
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const uint8_t *kt = tiles + (c >> 1) * T::kPair;
-            ld_words<G>(w[c], kt + (8 * (c & 1) + r) * (D / 2) + t * (4 * G));
-            ld_words<G>(st[c >> 1][c & 1], kt + T::kCodes + t * (8 * G) + (c & 1) * 4 * G);
-        }
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const uint8_t *kt = tiles + (c >> 1) * T::kPair;
-            const uint32_t ls = *reinterpret_cast<const uint32_t *>(
-                kt + T::kCodes + 2 * (16 * G + G * (8 * (c & 1) + r)) +
-                (G == 4 ? (t & 1) * 4 : 0));
+            for (int h = 0; h < 2; ++h)
+                ld_words<G>(w[i][h],
+                            tiles + i * T::kPair + (8 * h + r) * (D / 2) + t * (4 * G));
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const uint8_t *par = tiles + i * T::kPair + T::kCodes + 2 * (16 * G + G * r) +
+                                 (G == 4 ? (t & 1) * 4 : 0);
             float d[4];
-            mma_1688_zero(d, qsum, qsum, ls);
-            acc[c] = f2_mul(f2_pack(d[0], d[1]), f2_pack(0x1p-24f, 0x1p-24f));
+            mma_1688_zero(d, *reinterpret_cast<const uint32_t *>(par),
+                          *reinterpret_cast<const uint32_t *>(par + 16 * G), qsum);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[i][k] = d[k] * 0x1p-24f;
         }
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const uint32_t v = w[c][gr], u = v >> 8;
-                float d0[4], d1[4];
-                mma_16816_zero(d0, qa[gr], v & 0x000f000fu, u & 0x000f000fu);
-                mma_16816_zero(d1, qa[gr], v & 0x00f000f0u, u & 0x00f000f0u);
-                const uint64_t sw =
-                    f2_of_half2(st[c >> 1][gr / (G / 2)][2 * (gr % (G / 2)) + (c & 1)]);
-                acc[c] = f2_fma(f2_pack(d0[0], d0[1]), sw, acc[c]);
-                acc[c] = f2_fma(f2_pack(d1[2], d1[3]), sw, acc[c]);
+            for (int i = 0; i < NB; ++i) {
+                const uint32_t v0 = w[i][0][gr], v1 = w[i][1][gr], u0 = v0 >> 8, u1 = v1 >> 8;
+                const uint32_t a0[4] = {v0 & 0x000f000fu, v1 & 0x000f000fu, u0 & 0x000f000fu,
+                                        u1 & 0x000f000fu};
+                const uint32_t a1[4] = {v0 & 0x00f000f0u, v1 & 0x00f000f0u, u0 & 0x00f000f0u,
+                                        u1 & 0x00f000f0u};
+                float d[4];
+                mma_16816_zero(d, a0, qb[gr][0], qb[gr][1]);
+                mma_add(d, a1, qb[gr][2], qb[gr][3]);
+                const __half *st = reinterpret_cast<const __half *>(
+                    tiles + i * T::kPair + T::kCodes + 8 * (G * (r >> 1) + gr) + 2 * (r & 1));
+                const float s0 = __half2float(st[0]), s1 = __half2float(st[2]);
+                y[i][0] = fmaf(d[0], s0, y[i][0]);
+                y[i][1] = fmaf(d[1], s0, y[i][1]);
+                y[i][2] = fmaf(d[2], s1, y[i][2]);
+                y[i][3] = fmaf(d[3], s1, y[i][3]);
             }
         }
-        float y[NB][4];
+        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-            f2_unpack(f2_mul(acc[c], f2_pack(qs, qs)), y[c >> 1][2 * (c & 1)],
-                      y[c >> 1][2 * (c & 1) + 1]);
-        if (kTail) {
+        for (int i = 0; i < NB; ++i) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (8 * (k >> 1) + 2 * t + (k & 1) >= valid) y[0][k] = -INFINITY;
+            for (int k = 0; k < 4; ++k) {
+                y[i][k] *= qs[k & 1];
+                if (kTail && r + 8 * (k >> 1) >= valid) y[i][k] = -INFINITY;
+            }
+            top[0] = fmax3(top[0], y[i][0], y[i][2]);
+            top[1] = fmax3(top[1], y[i][1], y[i][3]);
         }
-        float top = -INFINITY;
+        if (__any_sync(0xffffffffu, top[0] > m[0] + kLazy || top[1] > m[1] + kLazy)) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-            top = fmax3(fmax3(top, y[i][0], y[i][1]), y[i][2], y[i][3]);
-        if (__any_sync(0xffffffffu, top > m + kLazy)) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float n = top > m + kLazy ? top : m;
-            const float f = ex2(m - n);
-            m = n;
-            l *= f;
-            const float f0 = __shfl_sync(0xffffffffu, f, 8 * t);
-            const float f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int f = 4; f < 32; f <<= 1)
+                    top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], f));
+                const float n = top[k] > m[k] + kLazy ? top[k] : m[k];
+                const float f = ex2(m[k] - n);
+                m[k] = n;
+                l[k] *= f;
+                top[k] = f;
+            }
 #pragma unroll
             for (int k = 0; k < 2 * G; ++k) {
-                o[k][0] *= f0;
-                o[k][1] *= f1;
-                o[k][2] *= f0;
-                o[k][3] *= f1;
+                o[k][0] *= top[0];
+                o[k][1] *= top[1];
+                o[k][2] *= top[0];
+                o[k][3] *= top[1];
             }
-            z[0] *= f0;
-            z[1] *= f1;
+            z[0] *= top[0];
+            z[1] *= top[1];
 #pragma unroll
-            for (int k = 0; k < G; ++k) e[k] = f2_mul(e[k], f2_pack(f0, f1));
+            for (int k = 0; k < G; ++k) e[k] = f2_mul(e[k], f2_pack(top[0], top[1]));
         }
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             const uint8_t *vt = tiles + i * T::kPair + T::kBytes, *par = vt + T::kCodes;
-            float p[4];
+            // p as the sum of two fp16 (so that its product with a step is rounded
+            // once), transposed to head r, keys 2 t, + 1 ([0]), + 8, + 9 ([1])
+            uint32_t hi[2], lo[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) p[k] = ex2(y[i][k] - m);
-            l += (p[0] + p[1]) + (p[2] + p[3]);
+            for (int k = 0; k < 2; ++k) {
+                const float p0 = ex2(y[i][2 * k] - m[0]), p1 = ex2(y[i][2 * k + 1] - m[1]);
+                l[0] += p0;
+                l[1] += p1;
+                const uint32_t x = pack_half2(p0, p1);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+                hi[k] = transpose8(x);
+                lo[k] = transpose8(pack_half2(p0 - f.x, p1 - f.y));
+            }
             uint32_t st[2][G];
             ld_words<G>(st[0], par + t * (8 * G));
             ld_words<G>(st[1], par + t * (8 * G) + 4 * G);
@@ -390,15 +407,13 @@ struct State {
             }
             {  // (rows 8-15 of the operand and of z are not used)
                 const uint32_t a4[4] = {za[0], za[0], za[1], za[1]};
-                mma_add(z, a4, pack_half2(p[0], p[1]), pack_half2(p[2], p[3]));
+                mma_add(z, a4, hi[0], hi[1]);
             }
-            const uint64_t p01 = f2_pack(p[0], p[1]), p23 = f2_pack(p[2], p[3]);
             const uint32_t eights[4] = {0xc800c800u, 0xc800c800u, 0xc800c800u, 0xc800c800u};
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
                 const uint32_t *sw = &st[gr / (G / 2)][2 * (gr % (G / 2))];
-                const uint32_t b0 = half2_of_f2(f2_mul(p01, f2_of_half2(sw[0])));
-                const uint32_t b1 = half2_of_f2(f2_mul(p23, f2_of_half2(sw[1])));
+                const uint32_t b0 = times(hi[0], lo[0], sw[0]), b1 = times(hi[1], lo[1], sw[1]);
                 const uint32_t u0 = w0[gr] >> 8, u1 = w1[gr] >> 8;
                 const uint32_t a0[4] = {w0[gr] & 0x000f000fu, w0[gr] & 0x00f000f0u,
                                         w1[gr] & 0x000f000fu, w1[gr] & 0x00f000f0u};
@@ -416,8 +431,10 @@ struct State {
     // l over all keys; O of heads 2 t + (0, 1): v[grp][head][n], values 32 grp + 4 r + n.
     __device__ __forceinline__ void end(float (&v)[G][2][4], int lane) {
         const int t = lane & 3;
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int f = 4; f < 32; f <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], f);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
             float es[2];
@@ -759,12 +776,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
                 st.end(v, lane);
                 const int r = lane >> 2, t = lane & 3;
                 if (b0 == 0 && b1 == cur.nblk) {  // the whole pair
-                    const float l0 = __shfl_sync(0xffffffffu, st.l, 8 * t);
-                    const float l1 = __shfl_sync(0xffffffffu, st.l, 8 * t + 4);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float l = h ? l1 : l0;
-                        const float inv = l != 0.f ? 1.f / l : 0.f;
+                        const float inv = st.l[h] != 0.f ? 1.f / st.l[h] : 0.f;
                         if (2 * t + h < a.g) {
                             __half *row = a.out + ((int64_t)cur.s * a.H + cur.kvh * a.g + 2 * t + h) * D;
 #pragma unroll
@@ -788,9 +802,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
                             for (int gr = 0; gr < G; ++gr)
                                 *reinterpret_cast<float4 *>(dst + (2 * t + h) * D + 32 * gr + 4 * r) =
                                     make_float4(v[gr][h][0], v[gr][h][1], v[gr][h][2], v[gr][h][3]);
-                    if (t == 0) {
-                        sm.m[2 * warp + k][r] = st.m;
-                        sm.l[2 * warp + k][r] = st.l;
+                    if (r == 0) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            sm.m[2 * warp + k][2 * t + h] = st.m[h];
+                            sm.l[2 * warp + k][2 * t + h] = st.l[h];
+                        }
                     }
                     if (lane == 0) {
                         Piece p;
