@@ -276,64 +276,49 @@ struct State {
         for (int i = 0; i < G; ++i) e[i] = f2_pack(0.f, 0.f);
     }
 
-    // NB consecutive blocks, their tile pairs at `tiles` in shared memory.  With
-    // kTail, only the first `valid` tokens of the (one) block count.
-    template <int NB, bool kTail>
-    __device__ __forceinline__ void blocks(const uint8_t *tiles, int valid, int lane) {
-        static_assert(NB == 1 || !kTail, "");
+    // One block, its tile pair at `kt` in shared memory.  With kTail, only its
+    // first `valid` tokens count.
+    template <bool kTail>
+    __device__ __forceinline__ void block(const uint8_t *kt, int valid, int lane) {
         const int r = lane >> 2, t = lane & 3;
         using T = I4Tile<D>;
-        // scores of keys r (y[.][0..1]: heads 2 t, 2 t + 1) and r + 8 (y[.][2..3])
-        float y[NB][4];
-        uint32_t w[NB][2][G];
+        // scores of keys r (y[0..1]: heads 2 t, 2 t + 1) and r + 8 (y[2..3])
+        float y[4];
+        uint32_t w[2][G];
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                ld_words<G>(w[i][h],
-                            tiles + i * T::kPair + (8 * h + r) * (D / 2) + t * (4 * G));
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const uint8_t *par = tiles + i * T::kPair + T::kCodes + 2 * (16 * G + G * r) +
-                                 (G == 4 ? (t & 1) * 4 : 0);
+        for (int h = 0; h < 2; ++h) ld_words<G>(w[h], kt + (8 * h + r) * (D / 2) + t * (4 * G));
+        {
+            const uint8_t *par = kt + T::kCodes + 2 * (16 * G + G * r) + (G == 4 ? (t & 1) * 4 : 0);
             float d[4];
             mma_1688_zero(d, *reinterpret_cast<const uint32_t *>(par),
                           *reinterpret_cast<const uint32_t *>(par + 16 * G), qsum);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[i][k] = d[k] * 0x1p-24f;
+            for (int k = 0; k < 4; ++k) y[k] = d[k] * 0x1p-24f;
         }
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const uint32_t v0 = w[i][0][gr], v1 = w[i][1][gr], u0 = v0 >> 8, u1 = v1 >> 8;
-                const uint32_t a0[4] = {v0 & 0x000f000fu, v1 & 0x000f000fu, u0 & 0x000f000fu,
-                                        u1 & 0x000f000fu};
-                const uint32_t a1[4] = {v0 & 0x00f000f0u, v1 & 0x00f000f0u, u0 & 0x00f000f0u,
-                                        u1 & 0x00f000f0u};
-                float d[4];
-                mma_16816_zero(d, a0, qb[gr][0], qb[gr][1]);
-                mma_add(d, a1, qb[gr][2], qb[gr][3]);
-                const __half *st = reinterpret_cast<const __half *>(
-                    tiles + i * T::kPair + T::kCodes + 8 * (G * (r >> 1) + gr) + 2 * (r & 1));
-                const float s0 = __half2float(st[0]), s1 = __half2float(st[2]);
-                y[i][0] = fmaf(d[0], s0, y[i][0]);
-                y[i][1] = fmaf(d[1], s0, y[i][1]);
-                y[i][2] = fmaf(d[2], s1, y[i][2]);
-                y[i][3] = fmaf(d[3], s1, y[i][3]);
-            }
+            const uint32_t v0 = w[0][gr], v1 = w[1][gr], u0 = v0 >> 8, u1 = v1 >> 8;
+            const uint32_t a0[4] = {v0 & 0x000f000fu, v1 & 0x000f000fu, u0 & 0x000f000fu,
+                                    u1 & 0x000f000fu};
+            const uint32_t a1[4] = {v0 & 0x00f000f0u, v1 & 0x00f000f0u, u0 & 0x00f000f0u,
+                                    u1 & 0x00f000f0u};
+            float d[4];
+            mma_16816_zero(d, a0, qb[gr][0], qb[gr][1]);
+            mma_add(d, a1, qb[gr][2], qb[gr][3]);
+            const __half *st = reinterpret_cast<const __half *>(
+                kt + T::kCodes + 8 * (G * (r >> 1) + gr) + 2 * (r & 1));
+            const float s0 = __half2float(st[0]), s1 = __half2float(st[2]);
+            y[0] = fmaf(d[0], s0, y[0]);
+            y[1] = fmaf(d[1], s0, y[1]);
+            y[2] = fmaf(d[2], s1, y[2]);
+            y[3] = fmaf(d[3], s1, y[3]);
         }
-        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                y[i][k] *= qs[k & 1];
-                if (kTail && r + 8 * (k >> 1) >= valid) y[i][k] = -INFINITY;
-            }
-            top[0] = fmax3(top[0], y[i][0], y[i][2]);
-            top[1] = fmax3(top[1], y[i][1], y[i][3]);
+        for (int k = 0; k < 4; ++k) {
+            y[k] *= qs[k & 1];
+            if (kTail && r + 8 * (k >> 1) >= valid) y[k] = -INFINITY;
         }
+        float top[2] = {fmaxf(y[0], y[2]), fmaxf(y[1], y[3])};
         if (__any_sync(0xffffffffu, top[0] > m[0] + kLazy || top[1] > m[1] + kLazy)) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -358,73 +343,70 @@ struct State {
 #pragma unroll
             for (int k = 0; k < G; ++k) e[k] = f2_mul(e[k], f2_pack(top[0], top[1]));
         }
+        const uint8_t *vt = kt + T::kBytes, *par = vt + T::kCodes;
+        // p as the sum of two fp16 (so that its product with a step is rounded
+        // once), transposed to head r, keys 2 t, + 1 ([0]), + 8, + 9 ([1])
+        uint32_t hi[2], lo[2];
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const uint8_t *vt = tiles + i * T::kPair + T::kBytes, *par = vt + T::kCodes;
-            // p as the sum of two fp16 (so that its product with a step is rounded
-            // once), transposed to head r, keys 2 t, + 1 ([0]), + 8, + 9 ([1])
-            uint32_t hi[2], lo[2];
+        for (int k = 0; k < 2; ++k) {
+            const float p0 = ex2(y[2 * k] - m[0]), p1 = ex2(y[2 * k + 1] - m[1]);
+            l[0] += p0;
+            l[1] += p1;
+            const uint32_t x = pack_half2(p0, p1);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+            hi[k] = transpose8(x);
+            lo[k] = transpose8(pack_half2(p0 - f.x, p1 - f.y));
+        }
+        uint32_t st[2][G];
+        ld_words<G>(st[0], par + t * (8 * G));
+        ld_words<G>(st[1], par + t * (8 * G) + 4 * G);
+        // row r % G of the centre's operand: m + 8 s of keys 2 t, + 1, + 8, + 9
+        const int row = 8 * (G * t + (r & (G - 1)));
+        const uint2 ls = *reinterpret_cast<const uint2 *>(par + 32 * G + row);
+        const uint2 ss = *reinterpret_cast<const uint2 *>(par + row);
+        const __half2 eight = __float2half2_rn(8.f);
+        const __half2 z0 = __hfma2(*reinterpret_cast<const __half2 *>(&ss.x), eight,
+                                   *reinterpret_cast<const __half2 *>(&ls.x));
+        const __half2 z1 = __hfma2(*reinterpret_cast<const __half2 *>(&ss.y), eight,
+                                   *reinterpret_cast<const __half2 *>(&ls.y));
+        uint32_t za[2] = {*reinterpret_cast<const uint32_t *>(&z0),
+                          *reinterpret_cast<const uint32_t *>(&z1)};
+        uint32_t w0[G], w1[G];  // word grp: keys 2 t (low half), 2 t + 1; then + 8
+        ld_words<G>(w0, vt + lane * (4 * G));
+        ld_words<G>(w1, vt + lane * (4 * G) + 4 * D);
+        if (kTail) {
+            // parameters of tokens that do not count may be anything, NaN included
+            const uint32_t k0 = (2 * t < valid ? 0x0000ffffu : 0u) |
+                                (2 * t + 1 < valid ? 0xffff0000u : 0u);
+            const uint32_t k1 = (2 * t + 8 < valid ? 0x0000ffffu : 0u) |
+                                (2 * t + 9 < valid ? 0xffff0000u : 0u);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float p0 = ex2(y[i][2 * k] - m[0]), p1 = ex2(y[i][2 * k + 1] - m[1]);
-                l[0] += p0;
-                l[1] += p1;
-                const uint32_t x = pack_half2(p0, p1);
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-                hi[k] = transpose8(x);
-                lo[k] = transpose8(pack_half2(p0 - f.x, p1 - f.y));
+            for (int k = 0; k < G; ++k) {
+                st[0][k] &= (k & 1) ? k1 : k0;
+                st[1][k] &= (k & 1) ? k1 : k0;
             }
-            uint32_t st[2][G];
-            ld_words<G>(st[0], par + t * (8 * G));
-            ld_words<G>(st[1], par + t * (8 * G) + 4 * G);
-            // row r % G of the centre's operand: m + 8 s of keys 2 t, + 1, + 8, + 9
-            const int row = 8 * (G * t + (r & (G - 1)));
-            const uint2 ls = *reinterpret_cast<const uint2 *>(par + 32 * G + row);
-            const uint2 ss = *reinterpret_cast<const uint2 *>(par + row);
-            const __half2 eight = __float2half2_rn(8.f);
-            const __half2 z0 = __hfma2(*reinterpret_cast<const __half2 *>(&ss.x), eight,
-                                       *reinterpret_cast<const __half2 *>(&ls.x));
-            const __half2 z1 = __hfma2(*reinterpret_cast<const __half2 *>(&ss.y), eight,
-                                       *reinterpret_cast<const __half2 *>(&ls.y));
-            uint32_t za[2] = {*reinterpret_cast<const uint32_t *>(&z0),
-                              *reinterpret_cast<const uint32_t *>(&z1)};
-            uint32_t w0[G], w1[G];  // word grp: keys 2 t (low half), 2 t + 1; then + 8
-            ld_words<G>(w0, vt + lane * (4 * G));
-            ld_words<G>(w1, vt + lane * (4 * G) + 4 * D);
-            if (kTail) {
-                // parameters of tokens that do not count may be anything, NaN included
-                const uint32_t k0 = (2 * t < valid ? 0x0000ffffu : 0u) |
-                                    (2 * t + 1 < valid ? 0xffff0000u : 0u);
-                const uint32_t k1 = (2 * t + 8 < valid ? 0x0000ffffu : 0u) |
-                                    (2 * t + 9 < valid ? 0xffff0000u : 0u);
+            za[0] &= k0;
+            za[1] &= k1;
+        }
+        {  // (rows 8-15 of the operand and of z are not used)
+            const uint32_t a4[4] = {za[0], za[0], za[1], za[1]};
+            mma_add(z, a4, hi[0], hi[1]);
+        }
+        const uint32_t eights[4] = {0xc800c800u, 0xc800c800u, 0xc800c800u, 0xc800c800u};
 #pragma unroll
-                for (int k = 0; k < G; ++k) {
-                    st[0][k] &= (k & 1) ? k1 : k0;
-                    st[1][k] &= (k & 1) ? k1 : k0;
-                }
-                za[0] &= k0;
-                za[1] &= k1;
-            }
-            {  // (rows 8-15 of the operand and of z are not used)
-                const uint32_t a4[4] = {za[0], za[0], za[1], za[1]};
-                mma_add(z, a4, hi[0], hi[1]);
-            }
-            const uint32_t eights[4] = {0xc800c800u, 0xc800c800u, 0xc800c800u, 0xc800c800u};
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                const uint32_t *sw = &st[gr / (G / 2)][2 * (gr % (G / 2))];
-                const uint32_t b0 = times(hi[0], lo[0], sw[0]), b1 = times(hi[1], lo[1], sw[1]);
-                const uint32_t u0 = w0[gr] >> 8, u1 = w1[gr] >> 8;
-                const uint32_t a0[4] = {w0[gr] & 0x000f000fu, w0[gr] & 0x00f000f0u,
-                                        w1[gr] & 0x000f000fu, w1[gr] & 0x00f000f0u};
-                const uint32_t a1[4] = {u0 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x000f000fu,
-                                        u1 & 0x00f000f0u};
-                mma_add(o[2 * gr], a0, b0, b1);
-                mma_add(o[2 * gr + 1], a1, b0, b1);
-                float d[4];
-                mma_16816_zero(d, eights, b0, b1);
-                e[gr] = f2_add(e[gr], f2_pack(d[0], d[1]));
-            }
+        for (int gr = 0; gr < G; ++gr) {
+            const uint32_t *sw = &st[gr / (G / 2)][2 * (gr % (G / 2))];
+            const uint32_t b0 = times(hi[0], lo[0], sw[0]), b1 = times(hi[1], lo[1], sw[1]);
+            const uint32_t u0 = w0[gr] >> 8, u1 = w1[gr] >> 8;
+            const uint32_t a0[4] = {w0[gr] & 0x000f000fu, w0[gr] & 0x00f000f0u,
+                                    w1[gr] & 0x000f000fu, w1[gr] & 0x00f000f0u};
+            const uint32_t a1[4] = {u0 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x000f000fu,
+                                    u1 & 0x00f000f0u};
+            mma_add(o[2 * gr], a0, b0, b1);
+            mma_add(o[2 * gr + 1], a1, b0, b1);
+            float d[4];
+            mma_16816_zero(d, eights, b0, b1);
+            e[gr] = f2_add(e[gr], f2_pack(d[0], d[1]));
         }
     }
 
@@ -757,11 +739,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
                     __syncwarp();  // every lane's copies of the stage have landed
                     uint8_t *at = sm.ring[warp][get];
                     if (b + 2 <= full_end && bad == 0) {
-                        st.template blocks<2, false>(at, kBlockSize, lane);
+                        st.template block<false>(at, kBlockSize, lane);
+                        st.template block<false>(at + kPairBytes, kBlockSize, lane);
                     } else {
                         for (int i = 0; i < 2 && b + i < b1; ++i) {
                             const uint32_t bit = 1u << (2 * get + i);
-                            st.template blocks<1, true>(
+                            st.template block<true>(
                                 at + i * kPairBytes,
                                 (bad & bit) ? 0 : min(kBlockSize, cur.ctx - (b + i) * kBlockSize),
                                 lane);
