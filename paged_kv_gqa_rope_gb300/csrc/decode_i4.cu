@@ -30,7 +30,12 @@
 //     value, keep both terms as small as the values themselves, so the
 //     rounding is not magnified by their cancelling.  c - 8 is the product
 //     with c and, from the same rounded operand, 8 times its sum (one MMA a
-//     group, row g of one accumulator tile).
+//     group; making c - 8 itself, one packed add for each two codes, was
+//     slower: 77.9 against 75.4 us on 32 x 32 heads of 2049 keys).
+//     Every other block enters as -(p s)(15 - c) and 7 times the sum instead:
+//     the tensor core truncates its sums, and with c alone they grow to many
+//     times the result (a warp's 575 blocks of even weights: 4.6e-3 off).  For
+//     the same reason the sums of p s and of the centres are added up outside.
 //   - The running maximum is raised only when a score passes it by kLazy
 //     (in log2), so P <= 2^kLazy and O is rarely rescaled.
 #include <mutex>
@@ -173,9 +178,12 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// (hi + lo) s of two fp16 pairs, rounded to fp16 (lo s, far below it, before).
+// (hi + lo) s of two fp16 pairs, or its negative, rounded to fp16 (lo s, far
+// below it, before).
+template <bool kNegative>
 __device__ __forceinline__ uint32_t times(uint32_t hi, uint32_t lo, uint32_t s) {
-    const __half2 x = *reinterpret_cast<const __half2 *>(&s);
+    __half2 x = *reinterpret_cast<const __half2 *>(&s);
+    if (kNegative) x = __hneg2(x);
     const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&hi), x,
                               __hmul2(*reinterpret_cast<const __half2 *>(&lo), x));
     return *reinterpret_cast<const uint32_t *>(&r);
@@ -205,7 +213,7 @@ __device__ __forceinline__ void ld_words(uint32_t (&w)[G], const uint8_t *p) {
 // accumulators of O^T, rows (values of V) 32 grp + 4 r + n:
 //   o[2 grp][0..1] n = 0, [2..3] n = 1; o[2 grp + 1][0..1] n = 2, [2..3] n = 3,
 // in units of 2^-24 (n even) and 2^-20 (n odd); row grp of z: the sum of p times
-// the centre of group grp; e[grp]: -8 times the sum of its p s.
+// the centre of group grp; e[grp]: -8 (or 7) times the sum of its p s.
 template <int D>
 struct State {
     static constexpr int G = D / 32;
@@ -213,8 +221,8 @@ struct State {
     uint32_t qsum;      // B fragment of the groups' sums of q, high and low parts
     float qs[2];        // scores -> log2 units
     float m[2], l[2];
-    float o[2 * G][4], z[4];
-    uint64_t e[G];
+    float o[2 * G][4];
+    uint64_t z, e[G];
 
     __device__ __forceinline__ void begin(const DecodeI4Args &a, const Pair &p, int lane) {
         const int r = lane >> 2, t = lane & 3;
@@ -274,14 +282,14 @@ struct State {
         l[0] = l[1] = 0.f;
 #pragma unroll
         for (int i = 0; i < 2 * G; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        z[0] = z[1] = z[2] = z[3] = 0.f;
+        z = f2_pack(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < G; ++i) e[i] = f2_pack(0.f, 0.f);
     }
 
     // One block, its tile pair at `kt` in shared memory.  With kTail, only its
-    // first `valid` tokens count.
-    template <bool kTail>
+    // first `valid` tokens count; kFlip: V's codes enter as 15 - c.
+    template <bool kTail, bool kFlip>
     __device__ __forceinline__ void block(const uint8_t *kt, int valid, int lane) {
         const int r = lane >> 2, t = lane & 3;
         using T = I4Tile<D>;
@@ -341,10 +349,10 @@ struct State {
                 o[k][2] *= top[0];
                 o[k][3] *= top[1];
             }
-            z[0] *= top[0];
-            z[1] *= top[1];
+            const uint64_t both = f2_pack(top[0], top[1]);
+            z = f2_mul(z, both);
 #pragma unroll
-            for (int k = 0; k < G; ++k) e[k] = f2_mul(e[k], f2_pack(top[0], top[1]));
+            for (int k = 0; k < G; ++k) e[k] = f2_mul(e[k], both);
         }
         const uint8_t *vt = kt + T::kBytes, *par = vt + T::kCodes;
         // p as the sum of two fp16 (so that its product with a step is rounded
@@ -391,24 +399,30 @@ struct State {
             za[0] &= k0;
             za[1] &= k1;
         }
-        {  // (rows 8-15 of the operand and of z are not used)
+        {  // (rows 8-15 of the operand and the product are not used)
             const uint32_t a4[4] = {za[0], za[0], za[1], za[1]};
-            mma_add(z, a4, hi[0], hi[1]);
+            float d[4];
+            mma_16816_zero(d, a4, hi[0], hi[1]);
+            z = f2_add(z, f2_pack(d[0], d[1]));
         }
-        const uint32_t eights[4] = {0xc800c800u, 0xc800c800u, 0xc800c800u, 0xc800c800u};
+        // -8, or -7 beside the negated p s
+        constexpr uint32_t kOff = kFlip ? 0xc700c700u : 0xc800c800u;
+        const uint32_t off[4] = {kOff, kOff, kOff, kOff};
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
             const uint32_t *sw = &st[gr / (G / 2)][2 * (gr % (G / 2))];
-            const uint32_t b0 = times(hi[0], lo[0], sw[0]), b1 = times(hi[1], lo[1], sw[1]);
-            const uint32_t u0 = w0[gr] >> 8, u1 = w1[gr] >> 8;
-            const uint32_t a0[4] = {w0[gr] & 0x000f000fu, w0[gr] & 0x00f000f0u,
-                                    w1[gr] & 0x000f000fu, w1[gr] & 0x00f000f0u};
+            const uint32_t b0 = times<kFlip>(hi[0], lo[0], sw[0]);
+            const uint32_t b1 = times<kFlip>(hi[1], lo[1], sw[1]);
+            const uint32_t v0 = kFlip ? ~w0[gr] : w0[gr], v1 = kFlip ? ~w1[gr] : w1[gr];
+            const uint32_t u0 = v0 >> 8, u1 = v1 >> 8;
+            const uint32_t a0[4] = {v0 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x000f000fu,
+                                    v1 & 0x00f000f0u};
             const uint32_t a1[4] = {u0 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x000f000fu,
                                     u1 & 0x00f000f0u};
             mma_add(o[2 * gr], a0, b0, b1);
             mma_add(o[2 * gr + 1], a1, b0, b1);
             float d[4];
-            mma_16816_zero(d, eights, b0, b1);
+            mma_16816_zero(d, off, b0, b1);
             e[gr] = f2_add(e[gr], f2_pack(d[0], d[1]));
         }
     }
@@ -422,11 +436,12 @@ struct State {
             for (int f = 4; f < 32; f <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], f);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
-            float es[2];
+            float es[2], zs[2];
             f2_unpack(e[gr], es[0], es[1]);
+            f2_unpack(z, zs[0], zs[1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float zz = __shfl_sync(0xffffffffu, z[h], 4 * gr + t) + es[h];
+                const float zz = __shfl_sync(0xffffffffu, zs[h], 4 * gr + t) + es[h];
                 v[gr][h][0] = fmaf(o[2 * gr][h], 0x1p24f, zz);
                 v[gr][h][1] = fmaf(o[2 * gr][2 + h], 0x1p20f, zz);
                 v[gr][h][2] = fmaf(o[2 * gr + 1][h], 0x1p24f, zz);
@@ -742,12 +757,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
                     __syncwarp();  // every lane's copies of the stage have landed
                     uint8_t *at = sm.ring[warp][get];
                     if (b + 2 <= full_end && bad == 0) {
-                        st.template block<false>(at, kBlockSize, lane);
-                        st.template block<false>(at + kPairBytes, kBlockSize, lane);
+                        st.template block<false, false>(at, kBlockSize, lane);
+                        st.template block<false, true>(at + kPairBytes, kBlockSize, lane);
                     } else {
                         for (int i = 0; i < 2 && b + i < b1; ++i) {
                             const uint32_t bit = 1u << (2 * get + i);
-                            st.template block<true>(
+                            st.template block<true, false>(
                                 at + i * kPairBytes,
                                 (bad & bit) ? 0 : min(kBlockSize, cur.ctx - (b + i) * kBlockSize),
                                 lane);
