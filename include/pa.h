@@ -492,7 +492,8 @@ typedef struct {
 size_t pa_cache_i4_bytes(int layers, int num_blocks, int block_size, int n_kv_heads,
                          int head_dim);
 /* As pa_alloc_cache, for the 4-bit pool (device_base 256-byte aligned, at
- * least pa_cache_i4_bytes(...) bytes, or NULL to allocate). */
+ * least pa_cache_i4_bytes(...) bytes, or NULL to allocate); also
+ * PA_ERR_UNSUPPORTED for a block of more than INT32_MAX bytes. */
 int pa_alloc_cache_i4(pa_cache_i4_t *out, int layers, int num_blocks, int block_size,
                       int n_kv_heads, int head_dim, void *device_base);
 int pa_free_cache_i4(pa_cache_i4_t *cache);
@@ -524,7 +525,8 @@ int pa_rope_kv_write_i4(const void *q, void *q_out, const void *k, const void *v
  * m + s * c rounded once to the nearest fp16, saturated at 65504 (the step's
  * rounding up can carry a group's top past it).
  *   block_tables  device int32 [num_seqs][max_blocks_per_seq]
- *   lengths       device int32 [num_seqs]; 0 reads nothing
+ *   lengths       device int32 [num_seqs]; 0 reads nothing, whatever the
+ *                 sequence's other entries hold (a padded batch)
  *   first_tokens  device int32 [num_seqs], or NULL for 0
  *   row_starts    device int32 [num_seqs]; the sequences' row ranges must not
  *                 overlap
@@ -571,9 +573,10 @@ int pa_decode_i4(const void *q, const pa_cache_i4_t *cache, int layer,
  * pa_prefill_varlen runs over that.
  *   workspace  device, 256-byte aligned, contents undefined before and after:
  *              pa_prefill_i4_workspace_bytes(scratch_blocks, ...) bytes, where
- *              scratch_blocks >= sum_s ceil(L_k(s) / 16); sequences that no
- *              longer fit set PA_DEV_WORKSPACE and their rows of out are
- *              undefined.  One call at a time per workspace.
+ *              scratch_blocks >= sum_s ceil(L_k(s) / 16) over all sequences;
+ *              those that no longer fit set PA_DEV_WORKSPACE (and
+ *              PA_DEV_BAD_BLOCK) and their rows of out are undefined.  One
+ *              call at a time per workspace.
  * Arguments, results and checks otherwise as pa_prefill_varlen.
  */
 size_t pa_prefill_i4_workspace_bytes(int scratch_blocks, int num_seqs, int max_blocks_per_seq,

@@ -352,10 +352,12 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const ReadI4Ar
         const int64_t r = kScratch ? 0 : __ldg(a.rows + s);
         const bool ok = len >= 0 && f >= 0 && f + len <= (int64_t)a.maxb * kBlockSize && r >= 0 &&
                         (kScratch || r + len <= a.total_rows);
-        if (!ok) {
+        if (len == 0) {
+            // nothing to read, whatever the rest says (a padded batch)
+        } else if (!ok) {
             // (the prefill kernel reports a bad length of its own)
             if (!kScratch && blockIdx.x == 0) report(a.status, PA_DEV_BAD_LENGTH);
-        } else if (len > 0) {
+        } else {
             n = (f % kBlockSize + len + kBlockSize - 1) / kBlockSize;
         }
         prefix[s + 1] = n;
@@ -457,6 +459,7 @@ extern "C" int pa_alloc_cache_i4(pa_cache_i4_t *out, int layers, int num_blocks,
     if (bytes == 0) return PA_ERR_INVALID;
     if ((int64_t)num_blocks * block_size > INT32_MAX) return PA_ERR_INVALID;
     if (block_size != kBlockSize || (head_dim != 64 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)n_kv_heads * head_dim * 20 > INT32_MAX) return PA_ERR_UNSUPPORTED;
     if (device_base && (reinterpret_cast<uintptr_t>(device_base) & 255u)) return PA_ERR_INVALID;
     void *base = device_base;
     if (!base) {

@@ -52,7 +52,8 @@ def cache_of(tiles):
 
 # ------------------------------------------------------------------ write
 
-@pytest.mark.parametrize("H,Hk,d,T", [(4, 2, 64, 1), (4, 2, 64, 10), (32, 4, 64, 33),
+@pytest.mark.parametrize("H,Hk,d,T", [(1, 1, 64, 1), (1, 1, 128, 5), (33, 33, 128, 2),
+                                      (4, 2, 64, 1), (4, 2, 64, 10), (32, 4, 64, 33),
                                       (8, 1, 128, 7), (32, 8, 128, 40), (64, 8, 128, 100),
                                       (5, 5, 128, 3), (14, 2, 64, 1500), (64, 8, 128, 1300)])
 @pytest.mark.parametrize("in_place", [False, True])
@@ -196,6 +197,27 @@ def test_read_reports_bad_lengths_rows_and_blocks():
     want[56] = vals[bt[4, 1]][0]
     want[100:133] = vals[bt[3]].reshape(-1, Hk, d)[:33]
     assert np.array_equal(bits(out), bits(want))
+
+
+def test_read_padded_batch():
+    """Sequences of length 0 read nothing and report nothing, whatever their
+    other entries hold."""
+    rng = np.random.default_rng(24)
+    bt, NB = tables(rng, [20])
+    tiles = orc.pack_cache_i4(normal16(rng, 2, 1, NB, 16, 2, 64))
+    bt = np.concatenate([bt, np.full((3, 2), 1 << 30, np.int32)])
+    out, status = torch.full((25, 2, 64), 9.0).half().cuda(), pa.new_status()
+    i32 = lambda *x: dev(np.array(x, np.int32))  # noqa: E731
+    pa.kv_read_i4(cache_of(tiles), dev(bt), i32(20, 0, 0, 0), i32(2, -7, 2**31 - 1, 0), out, None,
+                  first_tokens=i32(0, -1, 2**31 - 1, 5), status=status)
+    assert int(status.item()) == 0
+    want = np.full((25, 2, 64), 9, np.float16)
+    vals = orc.read_rows_i4(orc.dequantize_cache_i4(tiles))[0, 0]
+    want[2:22] = vals[bt[0]].reshape(-1, 2, 64)[:20]
+    assert np.array_equal(bits(out), bits(want))
+    # nothing at all to read
+    pa.kv_read_i4(cache_of(tiles), dev(bt), i32(0, 0, 0, 0), i32(0, 0, 0, 0), out, out, status=status)
+    assert int(status.item()) == 0 and np.array_equal(bits(out), bits(want))
 
 
 def test_read_many_sequences():
@@ -577,6 +599,26 @@ def test_prefill_workspace_too_small_is_reported():
     assert status & pa.PA_DEV_WORKSPACE
     want = prefill_want(q, tiles, bt, cu, 2)
     assert_attention_close(out, want, rows=slice(0, 40))  # the sequence that fits
+
+
+def test_prefill_sequences_without_new_tokens():
+    """A batch in which some sequences have nothing new, or nothing at all."""
+    q, tiles, bt, cu = prefill_case(73, 8, 2, 128, [50, 0, 7, 0], [0, 33, 1, 0])
+    out, status = run_prefill(q, tiles, bt, cu, 2)
+    assert status == 0
+    assert_attention_close(out, prefill_want(q, tiles, bt, cu, 2))
+
+
+def test_prefill_reports_bad_lengths():
+    q, tiles, bt, cu = prefill_case(74, 8, 2, 128, [0, 10, 0], [40, 30, 20])
+    good = prefill_want(q, tiles, bt, cu, 2)
+    for k_of_1 in (20, bt.shape[1] * 16 + 1):  # fewer keys than queries; past the table
+        k = np.diff(cu[1])
+        k[1] = k_of_1
+        bad = np.concatenate([[0], np.cumsum(k)]).astype(np.int32)
+        out, status = run_prefill(q, tiles, bt, (cu[0], bad), 2)
+        assert status == pa.PA_DEV_BAD_LENGTH
+        assert_attention_close(out, good, rows=np.r_[0:40, 70:90])
 
 
 def test_prefill_bad_block_is_reported():

@@ -105,6 +105,7 @@ def test_descriptor(libpa):
     assert libpa.pa_alloc_cache_i4(r, 1, 10, 16, 8, 96, fake) == pa.PA_ERR_UNSUPPORTED
     assert libpa.pa_alloc_cache_i4(r, 1, 0, 16, 8, 128, fake) == pa.PA_ERR_INVALID
     assert libpa.pa_alloc_cache_i4(r, 1, 1 << 28, 16, 8, 128, fake) == pa.PA_ERR_INVALID
+    assert libpa.pa_alloc_cache_i4(r, 1, 1, 16, 1 << 20, 128, fake) == pa.PA_ERR_UNSUPPORTED
     assert libpa.pa_alloc_cache_i4(r, 1, 10, 16, 8, 128,
                                    ctypes.c_void_p(1 << 20 | 16)) == pa.PA_ERR_INVALID
 
