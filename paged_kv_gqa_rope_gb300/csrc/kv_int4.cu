@@ -118,6 +118,10 @@ constexpr int kWriteCtas = 4;  // per SM
 template <int D>
 __global__ void __launch_bounds__(kTokenThreads, kWriteCtas)
     rope_kv_write_i4_kernel(const RopeI4Args a) {
+    // Launched as a dependent; what follows may be launched once all work before
+    // this kernel is done (so a decode kernel's set-up, which reads the context
+    // lengths early, never runs beside the work that writes them).
+    griddep_wait();
     griddep_launch_dependents();
     using T = I4Tile<D>;
     constexpr int kPieces = D / 8, kRows = kTokenThreads / kPieces;  // rows of a round
@@ -341,6 +345,8 @@ __device__ __forceinline__ void read_v(const uint8_t *tile, __half *out, int64_t
 template <int D, bool kScratch>
 __global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const ReadI4Args a) {
     using T = I4Tile<D>;
+    griddep_wait();  // as in rope_kv_write_i4_kernel
+    griddep_launch_dependents();
     extern __shared__ int64_t prefix[];  // [B + 1] blocks of the sequences before
     const int tid = threadIdx.x, lane = tid & 31;
     for (int s = tid; s < a.B; s += kReadThreads) {
@@ -434,7 +440,8 @@ int launch_read(const ReadI4Args &a, cudaStream_t st) {
     const int sms = sm_count();
     if (sms < 1) return PA_ERR_CUDA;
     const size_t smem = (size_t)(a.B + 1) * sizeof(int64_t);
-    kv_read_i4_kernel<D, kScratch><<<sms * kReadCtas, kReadThreads, smem, st>>>(a);
+    launch_dependent(kv_read_i4_kernel<D, kScratch>, dim3(sms * kReadCtas), dim3(kReadThreads), smem,
+                     st, a);
     return launch_status();
 }
 
@@ -543,9 +550,9 @@ extern "C" int pa_rope_kv_write_i4(const void *q, void *q_out, const void *k, co
                     (rounds + a.rounds_per_cta - 1) / a.rounds_per_cta);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (head_dim == 128)
-        rope_kv_write_i4_kernel<128><<<grid, kTokenThreads, 0, st>>>(a);
+        launch_dependent(rope_kv_write_i4_kernel<128>, grid, dim3(kTokenThreads), 0, st, a);
     else
-        rope_kv_write_i4_kernel<64><<<grid, kTokenThreads, 0, st>>>(a);
+        launch_dependent(rope_kv_write_i4_kernel<64>, grid, dim3(kTokenThreads), 0, st, a);
     return launch_status();
 }
 
