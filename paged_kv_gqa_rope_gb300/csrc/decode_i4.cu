@@ -8,15 +8,23 @@
 // (one CTA of 12 warps per SM).  A warp streams its range by itself into its
 // own ring of shared memory (K and V of one block and KV head are 20 d
 // contiguous bytes, which its lanes bring by 16-byte asynchronous copies), so
-// no warp waits for another until the end.  A pair that lies within one range is finished by
-// its warp; the pieces of a pair cut between warps are joined by the CTA once
-// all its warps are done, and a pair cut between CTAs by the CTA whose record
-// of it arrives last.  Every join sums in the order of the line, so the
-// result does not depend on who arrives when.
+// no warp waits for another until the end.  A pair that lies within one range
+// is finished by its warp; the pieces of a pair cut between warps are joined by
+// the CTA once all its warps are done, and a pair cut between CTAs by the CTA
+// whose record of it arrives last.  Every join sums in the order of the line,
+// so the result does not depend on who arrives when.
 //
-// Arithmetic, on warp-level MMAs (the g heads that share the KV head are the
-// M = 16 rows of Q and the N = 8 columns of P^T, so each code is unpacked once
-// for the whole group):
+// Bound: HBM on paper (1.25 d bytes per token and KV head); measured, the warp
+// schedulers: about 275 warp instructions and 22 MMAs a block, 5.6 TB/s on
+// 32 x 32 heads of 2049 keys (60 us, 84 % of the copy peak; the same loads
+// without the arithmetic take 52), and on short launches the edges, about 6 us
+// to the first tiles and 5 to the joins (32 x 8 heads of 4097 keys: 38.6 us,
+// 65 %).  Time grows in proportion from 12 warps an SM to 10, and 16 warps of
+// 128 registers spill what they gain.
+//
+// Arithmetic, on warp-level MMAs (scores S^T = K Q^T and O^T = V^T P^T, the g
+// heads that share the KV head being the N = 8 columns of both, so each code
+// is unpacked once for the whole group):
 //   - A code is used as the fp16 whose low bits it is: c 2^-24 (or 16 c 2^-24
 //     for every other one, taken out of the other operand), exact, for one
 //     logic operation per two codes.
@@ -582,55 +590,44 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x;
 
-    // -------- the line: units of all sequences, and where ranges begin.  Up to
-    // 128 sequences every warp keeps the prefix sums in its lanes (lane i: the
-    // units before sequence i * per); more go through shared memory.
-    const bool few = a.B <= 32 * kSeqStep;
+    // -------- units of every kSeqStep sequences and their prefix sums
     const int entries = (a.B + kSeqStep - 1) / kSeqStep;
-    auto units_of = [&](int first) {
+    for (int i = tid; i < entries; i += kThreads) {
         int64_t n = 0;
 #pragma unroll
         for (int k = 0; k < kSeqStep; ++k) {
-            const int s = first + k;
-            const int ctx = s < a.B ? __ldg(a.context_lens + s) : 1;
-            const int nblk = blocks_of(ctx, a.maxb);
-            if (s < a.B && nblk == 0 && cta == 0 && (!few || warp == 0))
+            const int s = i * kSeqStep + k;
+            if (s >= a.B) break;
+            const int nblk = blocks_of(__ldg(a.context_lens + s), a.maxb);
+            if (nblk)
+                n += nblk + kPairCost;
+            else if (cta == 0)
                 report(a.status, PA_DEV_BAD_LENGTH);
-            n += s < a.B && nblk ? nblk + kPairCost : 0;
         }
-        return n * a.Hk;
-    };
-    auto scan = [&](int64_t v) {  // inclusive, over the warp
-#pragma unroll
-        for (int f = 1; f < 32; f <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, v, f);
-            if (lane >= f) v += u;
-        }
-        return v;
-    };
-    if (tid < 2 * kWarps) sm.piece[tid].start = -1 - tid;
-    int64_t W, before = 0;  // few: units before sequence lane * kSeqStep
-    if (few) {
-        const int64_t mine = units_of(lane * kSeqStep);
-        const int64_t upto = scan(mine);
-        before = upto - mine;
-        W = __shfl_sync(0xffffffffu, upto, 31);
-    } else {
-        for (int i = tid; i < entries; i += kThreads) sm.prefix[i + 1] = units_of(i * kSeqStep);
-        if (tid == 0) sm.prefix[0] = 0;
-        __syncthreads();
-        if (warp == 0) {
-            int64_t carry = 0;
-            for (int base = 1; base <= entries; base += 32) {
-                const int i = base + lane;
-                const int64_t v = scan(i <= entries ? sm.prefix[i] : 0);
-                if (i <= entries) sm.prefix[i] = v + carry;
-                carry += __shfl_sync(0xffffffffu, v, 31);
-            }
-        }
-        __syncthreads();
-        W = sm.prefix[entries];
+        sm.prefix[i + 1] = n * a.Hk;
     }
+    if (lane == 0) {  // (by the lane that may overwrite them)
+        sm.piece[2 * warp].start = -1 - 2 * warp;
+        sm.piece[2 * warp + 1].start = -2 - 2 * warp;
+    }
+    if (tid == 0) sm.prefix[0] = 0;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t carry = 0;
+        for (int base = 1; base <= entries; base += 32) {
+            const int i = base + lane;
+            int64_t v = i <= entries ? sm.prefix[i] : 0;
+#pragma unroll
+            for (int f = 1; f < 32; f <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, v, f);
+                if (lane >= f) v += u;
+            }
+            if (i <= entries) sm.prefix[i] = v + carry;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    __syncthreads();
+    const int64_t W = sm.prefix[entries];
     // Everything above read only call metadata; Q and the pool may still be
     // being written by the kernel before this one.
     griddep_wait();
@@ -651,12 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
             return p;
         }();
         Pair cur;  // the pair being attended to
-        if (few) {
-            const uint32_t le = __ballot_sync(0xffffffffu, before <= begin && lane < entries);
-            const int i = 31 - __clz(le);
-            cur.find(begin, i * kSeqStep, __shfl_sync(0xffffffffu, before, i), a);
-        } else {
-            int lo = 0, hi = entries - 1;
+        {
+            int lo = 0, hi = entries - 1;  // largest entry at or before `begin`
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
                 if (sm.prefix[mid] <= begin)

@@ -109,9 +109,11 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 x, __half &step, __hal
 // keeps to one 16-byte piece (8 values) of the rows, so that it needs one set
 // of cosines and sines a token.  The four threads of a group of 32 (an aligned
 // quad of lanes) find its least and greatest value with shuffles.  Bound by
-// HBM (Q, K and V in, Q and the codes out) and, on large batches, nearly as
-// much by the arithmetic: 8116 tokens of 64 + 16 heads, 300 MB, took 64 us
-// with Q, K and V rows in one loop, 57 us in two.
+// HBM (Q, K and V in, Q and the codes out) with the K and V rows' arithmetic and
+// narrow stores close behind: 8116 tokens of 64 + 16 heads, 310 MB, take 53.5 us
+// (5.8 TB/s; 63.7 with Q, K and V rows in one loop and a division a code).  Two
+// tokens a CTA, so that V's codes leave in whole words, and loads a token ahead
+// took as long.
 constexpr int kAhead = 4;
 constexpr int kWriteCtas = 4;  // per SM
 
@@ -538,13 +540,15 @@ extern "C" int pa_rope_kv_write_i4(const void *q, void *q_out, const void *k, co
     a.n_heads = n_heads;
     a.n_kv_heads = n_kv_heads;
     a.max_pos = max_positions;
-    // Four CTAs per SM; with fewer tokens than that, a token's rows are spread
-    // over several CTAs, down to one round of rows each.
+    // Four CTAs per SM.  A token's rows are spread over several CTAs, down to one
+    // round of rows each, while that leaves two per SM: 1 token of 64 + 16 heads
+    // takes 1.75 us spread and 2.27 not, 16 tokens 2.16 and 2.58, but 256 tokens
+    // 3.39 (in two) and 3.14.
     const int sms = sm_count();
     if (sms < 1) return PA_ERR_CUDA;
     const int round = kTokenThreads / (head_dim / 8);
     const int rounds = (n_heads + round - 1) / round + (2 * n_kv_heads + round - 1) / round;
-    const int split = std::max(1, std::min(rounds, sms * kWriteCtas / num_tokens));
+    const int split = std::max(1, std::min(rounds, sms * 2 / num_tokens));
     a.rounds_per_cta = (rounds + split - 1) / split;
     const dim3 grid(std::min(num_tokens, sms * kWriteCtas),
                     (rounds + a.rounds_per_cta - 1) / a.rounds_per_cta);
