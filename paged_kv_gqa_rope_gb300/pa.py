@@ -636,33 +636,45 @@ def _on(dev, t, dtype, name, *shape):
     raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's device is cuda:{dev}")
 
 
-def _sizes(t, n, name):
-    """The n sizes of a CUDA tensor."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != n:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {n} dimensions")
-    return t.shape
+def _refuse_rank(*tensors):
+    """The error of a call whose tensors' sizes could not be read: (tensor,
+    dimensions, name) of each."""
+    for t, n, name in tensors:
+        if not (isinstance(t, torch.Tensor) and t.is_cuda):
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dim() != n:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {n} dimensions")
+    raise TypeError("arguments are not CUDA tensors")
+
+
+# The handle of a device's current stream, without a Stream object around it
+# where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _call_on(dev, name, stream, *args):
     """lib().<name>(*args, stream) with device `dev` current, on `stream` or that
     device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device.index != dev:
+        handle = _raw_stream(dev)
+    elif stream.device.index == dev:
+        handle = stream.cuda_stream
+    else:
         raise ValueError(f"{name}: tensors on cuda:{dev}, stream on {stream.device}")
     fn = getattr(_lib or lib(), name)
     if dev == torch.cuda.current_device():
-        rc = fn(*args, stream.cuda_stream)
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream.cuda_stream)
+            rc = fn(*args, handle)
     if rc != PA_OK:
         raise PAError(name, rc)
 
 
 def _cache_i4(dev, cache):
+    if not isinstance(cache, CacheI4):
+        raise TypeError(f"cache must be a CacheI4, not {type(cache).__name__}")
     if cache.buffer.get_device() != dev:
         raise ValueError(f"the cache is on {cache.buffer.device}, the call's device is cuda:{dev}")
     return ctypes.byref(cache.desc)
@@ -676,10 +688,13 @@ def rope_kv_write_i4(q, k, v, positions, slot_mapping, table, cache: CacheI4, la
                      q_out=None, status=None, stream=None):
     """pa_rope_kv_write_i4: rotates Q (in place, or into `q_out`) and appends the
     quantised rotated K and V (both left as they are).  Returns the rotated Q."""
-    T, H, d = _sizes(q, 3, "q")
-    Hk = _sizes(k, 3, "k")[1]
-    rows = _sizes(table, 3, "table")[0]
-    dev = q.get_device()
+    try:
+        (T, H, d), (_, Hk, _), (rows, _, _) = q.shape, k.shape, table.shape
+        dev = q.get_device()
+        if dev < 0:  # a host tensor
+            raise ValueError
+    except (AttributeError, ValueError):
+        _refuse_rank((q, 3, "q"), (k, 3, "k"), (table, 3, "table"))
     if q_out is None:
         q_out = q
     _call_on(dev, "pa_rope_kv_write_i4", stream, _on(dev, q, torch.float16, "q", T, H, d),
@@ -697,11 +712,17 @@ def kv_read_i4(cache: CacheI4, block_tables, lengths, row_starts, k_out=None, v_
     """pa_kv_read_i4: tokens first_tokens[s] .. + lengths[s] - 1 of every sequence
     (from its first token by default) as fp16 into rows row_starts[s] .. of k_out
     and v_out [rows, n_kv_heads, head_dim] (None: not read).  Returns (k_out, v_out)."""
-    B, width = _sizes(block_tables, 2, "block_tables")
+    if not isinstance(cache, CacheI4):
+        raise TypeError(f"cache must be a CacheI4, not {type(cache).__name__}")
     dev = cache.buffer.get_device()
     Hk, d = cache.desc.n_kv_heads, cache.desc.head_dim
-    out = k_out if k_out is not None else v_out
-    rows = 0 if out is None else _sizes(out, 3, "k_out" if out is k_out else "v_out")[0]
+    out, rows = (k_out, "k_out") if k_out is not None else (v_out, "v_out"), 0
+    try:
+        B, width = block_tables.shape
+        if out[0] is not None:
+            rows, _, _ = out[0].shape
+    except (AttributeError, ValueError):
+        _refuse_rank((block_tables, 2, "block_tables"), (out[0], 3, out[1]))
     if rows > 2**31 - 1:
         raise ValueError(f"{rows} output rows: they must stay within int32")
     _call_on(dev, "pa_kv_read_i4", stream, ctypes.byref(cache.desc), layer,
@@ -724,10 +745,13 @@ def decode_i4_workspace(num_seqs, n_heads, n_kv_heads, head_dim, device="cuda"):
 
 def decode_i4(q, cache: CacheI4, block_tables, context_lens, workspace, n_kv_heads, layer=0,
               scale=0.0, out=None, status=None, stream=None):
-    B, H, d = _sizes(q, 3, "q")
-    width = _sizes(block_tables, 2, "block_tables")[1]
-    nbytes = _sizes(workspace, 1, "workspace")[0]
-    dev = q.get_device()
+    try:
+        (B, H, d), (_, width), (nbytes,) = q.shape, block_tables.shape, workspace.shape
+        dev = q.get_device()
+        if dev < 0:  # a host tensor
+            raise ValueError
+    except (AttributeError, ValueError):
+        _refuse_rank((q, 3, "q"), (block_tables, 2, "block_tables"), (workspace, 1, "workspace"))
     if out is None:
         out = torch.empty_like(q)
     _call_on(dev, "pa_decode_i4", stream, _on(dev, q, torch.float16, "q", B, H, d),
@@ -754,10 +778,13 @@ def prefill_varlen_i4(q, cache: CacheI4, cu_seqlens_q, cu_seqlens_k, block_table
                       n_kv_heads, workspace, layer=0, scale=0.0, out=None, status=None,
                       stream=None):
     """pa_prefill_varlen_i4: varlen causal prefill over the 4-bit pool."""
-    T, H, d = _sizes(q, 3, "q")
-    B, width = _sizes(block_tables, 2, "block_tables")
-    nbytes = _sizes(workspace, 1, "workspace")[0]
-    dev = q.get_device()
+    try:
+        (T, H, d), (B, width), (nbytes,) = q.shape, block_tables.shape, workspace.shape
+        dev = q.get_device()
+        if dev < 0:  # a host tensor
+            raise ValueError
+    except (AttributeError, ValueError):
+        _refuse_rank((q, 3, "q"), (block_tables, 2, "block_tables"), (workspace, 1, "workspace"))
     if out is None:
         out = torch.empty_like(q)
     _call_on(dev, "pa_prefill_varlen_i4", stream, _on(dev, q, torch.float16, "q", T, H, d), T,

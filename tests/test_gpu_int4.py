@@ -791,6 +791,31 @@ def test_binding_refuses_shapes_and_places():
     with pytest.raises(pa.PAError):
         n = pa.cache_i4_bytes(1, 4, 16, 2, 64)
         pa.CacheI4(1, 4, 2, 64, buffer=torch.empty(n + 16, dtype=torch.uint8, device="cuda")[16:])
+    table, ws = pa.rope_table(4, 64), pa.decode_i4_workspace(2, 4, 2, 64)
     with pytest.raises(TypeError):
         pa.rope_kv_write_i4(f16(1, 4, 64), f16(1, 2, 64), f16(1, 2, 64).cpu(), i32(1), i32(1),
-                            pa.rope_table(4, 64), c)
+                            table, c)
+    q, bt, ctx = f16(2, 4, 64), i32(2, 4), i32(2)
+    for bad in (q.cpu(), q.float(), None, [1], q.permute(1, 0, 2)):
+        with pytest.raises(TypeError):
+            pa.decode_i4(bad, c, bt, ctx, ws, 2)
+    for args in ((q[0], c, bt, ctx, ws, 2), (q, c, bt[0], ctx, ws, 2), (q, c, bt, ctx[:1], ws, 2),
+                 (q, c, bt[:1], ctx, ws, 2)):
+        with pytest.raises(ValueError):
+            pa.decode_i4(*args)
+    for args in ((q, c, bt.long(), ctx, ws, 2), (q, c, bt, ctx.float(), ws, 2),
+                 (q, c, bt, ctx, ws.int(), 2), (q, c, bt.cpu(), ctx, ws, 2), (q, c, bt, ctx, None, 2)):
+        with pytest.raises(TypeError):
+            pa.decode_i4(*args)
+    with pytest.raises(ValueError):
+        pa.decode_i4(q, c, bt, ctx, ws, 2, out=f16(2, 4, 128))
+    with pytest.raises(ValueError):
+        pa.decode_i4(q, c, bt, ctx, ws, 2, status=i32(2))
+    with pytest.raises(TypeError):  # a pool of another kind
+        pa.decode_i4(q, pa.CacheI8(1, 4, 2, 64), bt, ctx, ws, 2)
+    with pytest.raises(TypeError):
+        pa.kv_read_i4(c, None, ctx, ctx, f16(4, 2, 64))
+    with pytest.raises(ValueError):
+        pa.kv_read_i4(c, bt, ctx, ctx, f16(4, 128))
+    with pytest.raises(ValueError):
+        pa.prefill_varlen_i4(q, c, i32(4), i32(3), bt, 1, 2, ws)
