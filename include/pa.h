@@ -549,8 +549,9 @@ int pa_kv_read_i4(const pa_cache_i4_t *cache, int layer, const int32_t *block_ta
 
 /*
  * pa_decode against the 4-bit pool, K and V standing for m + s * c.  Scores,
- * softmax statistics and sums are fp32; each probability is rounded to fp16
- * once, times its group's step.  Arguments, results and checks are those of
+ * softmax statistics and sums are fp32; a value of V enters as
+ * (c - 8) s + (m + 8 s), and a probability times s, a probability and m + 8 s
+ * are rounded to fp16 on their way.  Arguments, results and checks are those of
  * pa_decode except the workspace, whose size is
  * pa_decode_i4_workspace_bytes(...); it too is 256-byte aligned, zeroed
  * before its first use, left ready for the next call, and serves one call at

@@ -15,11 +15,11 @@
 // so the result does not depend on who arrives when.
 //
 // Bound: HBM on paper (1.25 d bytes per token and KV head); measured, the warp
-// schedulers: about 275 warp instructions and 22 MMAs a block, 5.6 TB/s on
-// 32 x 32 heads of 2049 keys (60 us, 84 % of the copy peak; the same loads
-// without the arithmetic take 52), and on short launches the edges, about 6 us
-// to the first tiles and 5 to the joins (32 x 8 heads of 4097 keys: 38.6 us,
-// 65 %).  Time grows in proportion from 12 warps an SM to 10, and 16 warps of
+// schedulers: about 275 warp instructions and 22 MMAs a block, 5.5 TB/s on
+// 32 x 32 heads of 2049 keys (61 us, 82 % of the copy peak; the same loads
+// without the arithmetic take 53), and on short launches the edges, about 7 us
+// to the first tiles and 5 to the joins (32 x 8 heads of 4097 keys: 39.4 us,
+// 64 %).  Time grows in proportion from 12 warps an SM to 10, and 16 warps of
 // 128 registers spill what they gain.
 //
 // Arithmetic, on warp-level MMAs (scores S^T = K Q^T and O^T = V^T P^T, the g
@@ -33,13 +33,14 @@
 //     MMA more, with the sums of q as the sum of two fp16.  q enters scaled by
 //     a power of two to [2^9, 2^10), so nothing of it underflows.
 //   - p v = sum over keys of  (p s)(c - 8) + p (m + 8 s): p s is rounded to
-//     fp16 once (the one rounding of this kernel that shows, as P's in the
-//     fp16 kernel); c - 8 rather than c, and the centre rather than the least
-//     value, keep both terms as small as the values themselves, so the
-//     rounding is not magnified by their cancelling.  c - 8 is the product
-//     with c and, from the same rounded operand, 8 times its sum (one MMA a
-//     group; making c - 8 itself, one packed add for each two codes, was
-//     slower: 77.9 against 75.4 us on 32 x 32 heads of 2049 keys).
+//     fp16 once, and so are p and the centre m + 8 s for their product (the
+//     roundings of this kernel that show, as P's in the fp16 kernel); c - 8
+//     rather than c, and the centre rather than the least value, keep both
+//     terms as small as the values themselves, so the rounding is not magnified
+//     by their cancelling.  c - 8 is the product with c and, from the same
+//     rounded operand, 8 times its sum (one MMA a group; making c - 8 itself,
+//     one packed add for each two codes, was slower: 77.9 against 75.4 us on
+//     32 x 32 heads of 2049 keys).
 //     Every other block enters as -(p s)(15 - c) and 7 times the sum instead:
 //     the tensor core truncates its sums, and with c alone they grow to many
 //     times the result (a warp's 575 blocks of even weights: 4.6e-3 off).  For
@@ -590,6 +591,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x;
 
+    // The work before this kernel may still be writing the context lengths; were
+    // CTAs to read different ones, their cuts would not match.  (Reading them
+    // ahead of this wait would save 0.5 to 0.7 us a call.)
+    griddep_wait();
+
     // -------- units of every kSeqStep sequences and their prefix sums
     const int entries = (a.B + kSeqStep - 1) / kSeqStep;
     for (int i = tid; i < entries; i += kThreads) {
@@ -628,9 +634,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
     }
     __syncthreads();
     const int64_t W = sm.prefix[entries];
-    // Everything above read only call metadata; Q and the pool may still be
-    // being written by the kernel before this one.
-    griddep_wait();
     griddep_launch_dependents();
     if (W == 0) return;
     const int A = (int)min((int64_t)gridDim.x * kWarps, (W + kMinUnits - 1) / kMinUnits);

@@ -121,8 +121,8 @@ template <int D>
 __global__ void __launch_bounds__(kTokenThreads, kWriteCtas)
     rope_kv_write_i4_kernel(const RopeI4Args a) {
     // Launched as a dependent; what follows may be launched once all work before
-    // this kernel is done (so a decode kernel's set-up, which reads the context
-    // lengths early, never runs beside the work that writes them).
+    // this kernel is done (so pa_decode's set-up, which reads the context lengths
+    // ahead of its own wait, never runs beside the work that writes them).
     griddep_wait();
     griddep_launch_dependents();
     using T = I4Tile<D>;

@@ -448,6 +448,25 @@ def test_decode_on_another_stream():
         assert torch.equal(out, want)
 
 
+def test_decode_right_behind_new_lengths():
+    """Lengths written by kernels and copies directly before the call."""
+    H, Hk, d = 16, 2, 128
+    q, tiles, bt, ctx = decode_case(42, H, Hk, d, [900, 17, 3000, 333] * 4)
+    cache, qd, btd = cache_of(tiles), dev(q), dev(bt)
+    lens = [dev(c) for c in (ctx, np.maximum(ctx // 3, 1).astype(np.int32), np.ones_like(ctx))]
+    ws = pa.decode_i4_workspace(len(ctx), H, Hk, d)
+    want = [run_decode(q, cache, bt, x.cpu().numpy(), Hk) for x in lens]
+    live, got = lens[0].clone(), []
+    for i in range(60):
+        if i % 2:
+            live.copy_(lens[i % 3])
+        else:
+            torch.add(lens[i % 3], 0, out=live)
+        got.append(pa.decode_i4(qd, cache, btd, live, ws, Hk))
+    for i, x in enumerate(got):
+        assert torch.equal(x, want[i % 3])
+
+
 def test_decode_two_streams_at_once():
     """Two calls in flight together, each with its own workspace."""
     cases = [decode_case(51 + i, 64, 8, 128, [2000 + 500 * i] * 4) for i in range(2)]
