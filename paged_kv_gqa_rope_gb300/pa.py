@@ -609,6 +609,8 @@ class CacheI4:
             buffer = torch.empty(n, dtype=torch.uint8, device=device)
         elif _dev(buffer, torch.uint8, "buffer", (None,)).numel() < n:
             raise ValueError(f"buffer holds {buffer.numel()} bytes, the pool needs {n}")
+        if not buffer.is_cuda:
+            raise ValueError(f"the 4-bit pool cannot be on {buffer.device}")
         self.buffer = buffer
         _check("pa_alloc_cache_i4", lib().pa_alloc_cache_i4(
             ctypes.byref(self.desc), layers, num_blocks, block_size, n_kv_heads, head_dim,

@@ -6,6 +6,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 from oracle import reference as orc
 from paged_kv_gqa_rope_gb300 import pa
@@ -108,6 +109,13 @@ def test_descriptor(libpa):
     assert libpa.pa_alloc_cache_i4(r, 1, 1, 16, 1 << 20, 128, fake) == pa.PA_ERR_UNSUPPORTED
     assert libpa.pa_alloc_cache_i4(r, 1, 10, 16, 8, 128,
                                    ctypes.c_void_p(1 << 20 | 16)) == pa.PA_ERR_INVALID
+
+
+def test_pool_in_host_memory_is_refused(libpa):
+    with pytest.raises(ValueError):
+        pa.CacheI4(1, 4, 2, 64, device="cpu")
+    with pytest.raises(TypeError):
+        pa.CacheI4(1, 4, 2, 64, buffer=torch.empty(1 << 16, dtype=torch.uint8))
 
 
 BUF = ctypes.c_void_p(1 << 24)
