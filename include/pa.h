@@ -488,7 +488,7 @@ typedef struct {
 } pa_cache_i4_t;
 
 /* Bytes of the pool: layers * num_blocks * n_kv_heads * 20 * head_dim
- * (block_size 16).  0 for non-positive arguments. */
+ * (block_size 16).  0 for non-positive arguments and a pool past SIZE_MAX. */
 size_t pa_cache_i4_bytes(int layers, int num_blocks, int block_size, int n_kv_heads,
                          int head_dim);
 /* As pa_alloc_cache, for the 4-bit pool (device_base 256-byte aligned, at
@@ -510,7 +510,8 @@ int pa_free_cache_i4(pa_cache_i4_t *cache);
  * Every other argument, the results and the device-side checks are those of
  * pa_rope_kv_write: a bad position leaves the token's q_out row and slot as
  * they were.  Two tokens of one call must not share a slot (its codes and
- * parameters would be a mix of both).
+ * parameters would be a mix of both).  PA_ERR_UNSUPPORTED for a token's Q of
+ * more than INT32_MAX bytes.
  */
 int pa_rope_kv_write_i4(const void *q, void *q_out, const void *k, const void *v,
                         const int32_t *positions, const int32_t *slot_mapping, int num_tokens,

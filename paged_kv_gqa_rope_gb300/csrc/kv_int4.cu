@@ -456,8 +456,12 @@ extern "C" size_t pa_cache_i4_bytes(int layers, int num_blocks, int block_size, 
                                     int head_dim) {
     if (layers <= 0 || num_blocks <= 0 || block_size <= 0 || n_kv_heads <= 0 || head_dim <= 0)
         return 0;
-    // 5 bits a value, K and V
-    return (size_t)layers * num_blocks * block_size * n_kv_heads * head_dim / 4 * 5;
+    // 5 bits a value, K and V; 0 if that passes a size_t
+    size_t values = (size_t)layers * num_blocks;
+    if (__builtin_mul_overflow(values, (size_t)block_size * n_kv_heads, &values) ||
+        __builtin_mul_overflow(values, (size_t)head_dim, &values) || values > SIZE_MAX / 5 * 4)
+        return 0;
+    return values / 4 * 5;
 }
 
 extern "C" int pa_alloc_cache_i4(pa_cache_i4_t *out, int layers, int num_blocks, int block_size,
@@ -512,9 +516,10 @@ extern "C" int pa_rope_kv_write_i4(const void *q, void *q_out, const void *k, co
     if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v) ||
         !aligned16(rope_table))
         return PA_ERR_INVALID;
-    if ((int64_t)num_tokens * ((int64_t)n_heads + 2 * (int64_t)n_kv_heads) * (head_dim / 8) >
-        (int64_t)1 << 40)
+    if (num_tokens > ((int64_t)1 << 40) / (((int64_t)n_heads + 2 * (int64_t)n_kv_heads) *
+                                           (head_dim / 8)))
         return PA_ERR_INVALID;
+    if ((int64_t)n_heads * head_dim * 2 > INT32_MAX) return PA_ERR_UNSUPPORTED;  // a token's Q
     // q_out is q or lies apart from every input
     const int64_t qb = (int64_t)num_tokens * n_heads * head_dim * 2;
     const int64_t kb = (int64_t)num_tokens * n_kv_heads * head_dim * 2;

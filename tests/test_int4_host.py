@@ -81,6 +81,9 @@ def test_sizes(libpa):
     # 5/16 of the fp16 pool
     assert 16 * pa.cache_i4_bytes(3, 7, 16, 5, 128) == 5 * pa.cache_bytes(3, 7, 16, 5, 128)
     assert pa.cache_i4_bytes(80, 1 << 20, 16, 8, 128) == 80 * (1 << 20) * 8 * 2560  # past 32 bits
+    assert pa.cache_i4_bytes(1 << 30, 1 << 27, 16, 1 << 20, 64) == 0  # past 64
+    assert pa.cache_i4_bytes(1 << 30, 1 << 27, 16, 1, 4) == (1 << 61) * 5
+    assert pa.cache_i4_bytes(1 << 30, 1 << 27, 16, 1, 7) == 0  # (the values fit)
     assert libpa.pa_decode_i4_workspace_bytes(0, 8, 8, 128) == 0
     assert libpa.pa_decode_i4_workspace_bytes(32, 64, 8, 128) > 0
     assert libpa.pa_prefill_i4_workspace_bytes(0, 1, 1, 8, 128) == 0
@@ -134,6 +137,7 @@ def test_write_refusals(libpa):
 
     assert call(T=0, q=None, k=None) == pa.PA_OK
     assert call(d=96) == pa.PA_ERR_UNSUPPORTED
+    assert call(T=1, H=2**26) == pa.PA_ERR_UNSUPPORTED
     for bad in (dict(T=-1), dict(H=5), dict(Hk=4), dict(layer=1), dict(layer=-1), dict(maxpos=0),
                 dict(cache=None), dict(q=None), dict(q_out=None), dict(k=None), dict(v=None),
                 dict(pos=None), dict(slots=None), dict(table=None), dict(q=ODD), dict(q_out=ODD),
