@@ -552,12 +552,13 @@ int pa_kv_read_i4(const pa_cache_i4_t *cache, int layer, const int32_t *block_ta
  * pa_decode against the 4-bit pool, K and V standing for m + s * c.  Scores,
  * softmax statistics and sums are fp32; a value of V enters as
  * (c - 8) s + (m + 8 s), and a probability times s, a probability and m + 8 s
- * are rounded to fp16 on their way.  Arguments, results and checks are those of
- * pa_decode except the workspace, whose size is
- * pa_decode_i4_workspace_bytes(...); it too is 256-byte aligned, zeroed
- * before its first use, left ready for the next call, and serves one call at
- * a time (two streams, or two captured graphs that may run together, take
- * one each).
+ * are rounded to fp16 on their way, scaled so that the rounding is relative
+ * (2^-11) down to weights 2^-22 of the largest, whatever the size of V.
+ * Arguments, results and checks are those of pa_decode except the workspace,
+ * whose size is pa_decode_i4_workspace_bytes(...); it too is 256-byte aligned,
+ * zeroed before its first use, left ready for the next call, and serves one
+ * call at a time (two streams, or two captured graphs that may run together,
+ * take one each).
  */
 size_t pa_decode_i4_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads, int head_dim);
 int pa_decode_i4(const void *q, const pa_cache_i4_t *cache, int layer,

@@ -45,8 +45,20 @@
 //     the tensor core truncates its sums, and with c alone they grow to many
 //     times the result (a warp's 575 blocks of even weights: 4.6e-3 off).  For
 //     the same reason the sums of p s and of the centres are added up outside.
+//   - Both roundings keep fp16's 11 bits over a wide range.  p is taken 2^13 times
+//     as large (the maximum kept lies 13 below the scores', in log2; where steps
+//     pass 1, by so much less that p s fits fp16).  Steps that stay at or below
+//     2^-5 are multiplied by the power of two that brings the largest to
+//     (1/2, 1].  So p s is normal down to 2^-22 of that of the largest score and
+//     step, and below it off by at most 2^-33 of that, whatever the size of V; a
+//     larger step scales the sums down as a larger score does.  (As they come,
+//     beside one key with most of the weight the others' p s is subnormal or
+//     nothing: 32768 keys with V of std 0.02, and a value of zero that had 0.9 of
+//     the weight, came out with a relative error of 0.3.)  The small steps'
+//     products are under a branch: 32 x 8 heads of 4097 keys take 39.9 us without
+//     and 40.3 with them, 40.5 where they are always made.
 //   - The running maximum is raised only when a score passes it by kLazy
-//     (in log2), so P <= 2^kLazy and O is rarely rescaled.
+//     (in log2), so P <= 2^(13 + kLazy) and O is rarely rescaled.
 #include <mutex>
 
 #include "common.cuh"
@@ -68,6 +80,7 @@ constexpr int kPairCost = 4;
 constexpr int kMinUnits = 4;   // least units of a warp's range
 constexpr int kSeqStep = 4;    // sequences per entry of the prefix table
 constexpr float kLazy = 2.f;
+constexpr int kShift = 13;        // the maximum kept lies at most this far below the scores'
 constexpr float kNoMax = -1e30f;  // running maximum before the first score
 
 template <int D>
@@ -187,15 +200,19 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ __half2 as_half2(uint32_t w) {
+    return *reinterpret_cast<const __half2 *>(&w);
+}
+__device__ __forceinline__ uint32_t as_u32(__half2 h) {
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
 // (hi + lo) s of two fp16 pairs, or its negative, rounded to fp16 (lo s, far
 // below it, before).
 template <bool kNegative>
 __device__ __forceinline__ uint32_t times(uint32_t hi, uint32_t lo, uint32_t s) {
-    __half2 x = *reinterpret_cast<const __half2 *>(&s);
+    __half2 x = as_half2(s);
     if (kNegative) x = __hneg2(x);
-    const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&hi), x,
-                              __hmul2(*reinterpret_cast<const __half2 *>(&lo), x));
-    return *reinterpret_cast<const uint32_t *>(&r);
+    return as_u32(__hfma2(as_half2(hi), x, __hmul2(as_half2(lo), x)));
 }
 // (movmatrix_trans without volatile)
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -222,16 +239,22 @@ __device__ __forceinline__ void ld_words(uint32_t (&w)[G], const uint8_t *p) {
 // accumulators of O^T, rows (values of V) 32 grp + 4 r + n:
 //   o[2 grp][0..1] n = 0, [2..3] n = 1; o[2 grp + 1][0..1] n = 2, [2..3] n = 3,
 // in units of 2^-24 (n even) and 2^-20 (n odd); row grp of z: the sum of p times
-// the centre of group grp; e[grp]: -8 (or 7) times the sum of its p s.
+// the centre of group grp; e[grp]: -8 (or 7) times the sum of its p s.  m lies
+// room - kLazy below the maximum; lim is the power of two (as two fp16) that no
+// step so far passes, 1 for 2^-4 to 1; where it is below 1, o and e are sums of
+// p s / lim.
 template <int D>
 struct State {
     static constexpr int G = D / 32;
+    static constexpr uint32_t kLeastLim = 0x04000400u, kOneLim = 0x3c003c00u;  // 2^-14, 1
     uint32_t qb[G][4];  // B fragments of Q^T: a group's codes of weight 1, then of weight 16
     uint32_t qsum;      // B fragment of the groups' sums of q, high and low parts
     float qs[2];        // scores -> log2 units
     float m[2], l[2];
     float o[2 * G][4];
     uint64_t z, e[G];
+    uint32_t lim;
+    float room;
 
     __device__ __forceinline__ void begin(const DecodeI4Args &a, const Pair &p, int lane) {
         const int r = lane >> 2, t = lane & 3;
@@ -294,6 +317,8 @@ struct State {
         z = f2_pack(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < G; ++i) e[i] = f2_pack(0.f, 0.f);
+        lim = kLeastLim;
+        room = kShift + kLazy;
     }
 
     // One block, its tile pair at `kt` in shared memory.  With kTail, only its
@@ -339,18 +364,48 @@ struct State {
             if (kTail && r + 8 * (k >> 1) >= valid) y[k] = -INFINITY;
         }
         float top[2] = {fmaxf(y[0], y[2]), fmaxf(y[1], y[3])};
-        if (__any_sync(0xffffffffu, top[0] > m[0] + kLazy || top[1] > m[1] + kLazy)) {
+        const uint8_t *vt = kt + T::kBytes, *par = vt + T::kCodes;
+        // V's steps of keys 2 t, + 1, + 8, + 9 and group r % G
+        const int row = 8 * (G * t + (r & (G - 1)));
+        uint2 ss = *reinterpret_cast<const uint2 *>(par + row);
+        uint32_t k0 = 0, k1 = 0;
+        if (kTail) {
+            // parameters of tokens that do not count may be anything, NaN included
+            k0 = (2 * t < valid ? 0x0000ffffu : 0u) | (2 * t + 1 < valid ? 0xffff0000u : 0u);
+            k1 = (2 * t + 8 < valid ? 0x0000ffffu : 0u) | (2 * t + 9 < valid ? 0xffff0000u : 0u);
+            ss.x &= k0;
+            ss.y &= k1;
+        }
+        const uint32_t big = as_u32(__hmax2(as_half2(ss.x), as_half2(ss.y)));
+        if (__any_sync(0xffffffffu, top[0] > __fadd_rd(m[0], room) ||
+                                        top[1] > __fadd_rd(m[1], room) ||
+                                        !__hble2(as_half2(big), as_half2(lim)))) {
+            // the limits' exponents, 15 for 1
+            const int was = (int)((lim >> 10) & 31u);
+            const uint32_t most = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
+            int now = max(was, min(29, (int)((most + 0x3ffu) >> 10)));
+            if (now > 10 && now < 15) now = 15;
+            lim = (uint32_t)now * 0x04000400u;
+            const float scaled = __int_as_float((127 + min(was, 15) - min(now, 15)) << 23);
+            const float shift = (float)max(0, kShift - max(0, now - 15));
+            const float less = room - kLazy - shift;  // what the maxima kept come nearer by
+            room = shift + kLazy;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
 #pragma unroll
                 for (int f = 4; f < 32; f <<= 1)
                     top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], f));
-                const float n = top[k] > m[k] + kLazy ? top[k] : m[k];
+                // (rounded so that top - n <= room, however large the scores)
+                float n = __fadd_ru(m[k], less);
+                if (top[k] > __fadd_rd(n, room)) n = __fsub_ru(top[k], shift);
                 const float f = ex2(m[k] - n);
                 m[k] = n;
                 l[k] *= f;
                 top[k] = f;
             }
+            z = f2_mul(z, f2_pack(top[0], top[1]));
+            top[0] *= scaled;
+            top[1] *= scaled;
 #pragma unroll
             for (int k = 0; k < 2 * G; ++k) {
                 o[k][0] *= top[0];
@@ -359,11 +414,9 @@ struct State {
                 o[k][3] *= top[1];
             }
             const uint64_t both = f2_pack(top[0], top[1]);
-            z = f2_mul(z, both);
 #pragma unroll
             for (int k = 0; k < G; ++k) e[k] = f2_mul(e[k], both);
         }
-        const uint8_t *vt = kt + T::kBytes, *par = vt + T::kCodes;
         // p as the sum of two fp16 (so that its product with a step is rounded
         // once), transposed to head r, keys 2 t, + 1 ([0]), + 8, + 9 ([1])
         uint32_t hi[2], lo[2];
@@ -381,25 +434,22 @@ struct State {
         ld_words<G>(st[0], par + t * (8 * G));
         ld_words<G>(st[1], par + t * (8 * G) + 4 * G);
         // row r % G of the centre's operand: m + 8 s of keys 2 t, + 1, + 8, + 9
-        const int row = 8 * (G * t + (r & (G - 1)));
         const uint2 ls = *reinterpret_cast<const uint2 *>(par + 32 * G + row);
-        const uint2 ss = *reinterpret_cast<const uint2 *>(par + row);
         const __half2 eight = __float2half2_rn(8.f);
-        const __half2 z0 = __hfma2(*reinterpret_cast<const __half2 *>(&ss.x), eight,
-                                   *reinterpret_cast<const __half2 *>(&ls.x));
-        const __half2 z1 = __hfma2(*reinterpret_cast<const __half2 *>(&ss.y), eight,
-                                   *reinterpret_cast<const __half2 *>(&ls.y));
-        uint32_t za[2] = {*reinterpret_cast<const uint32_t *>(&z0),
-                          *reinterpret_cast<const uint32_t *>(&z1)};
+        uint32_t za[2] = {as_u32(__hfma2(as_half2(ss.x), eight, as_half2(ls.x))),
+                          as_u32(__hfma2(as_half2(ss.y), eight, as_half2(ls.y)))};
         uint32_t w0[G], w1[G];  // word grp: keys 2 t (low half), 2 t + 1; then + 8
         ld_words<G>(w0, vt + lane * (4 * G));
         ld_words<G>(w1, vt + lane * (4 * G) + 4 * D);
+        if (lim < kOneLim) {
+            const __half2 sc = as_half2(2 * kOneLim - lim);  // 1 / lim
+#pragma unroll
+            for (int k = 0; k < G; ++k) {
+                st[0][k] = as_u32(__hmul2(as_half2(st[0][k]), sc));
+                st[1][k] = as_u32(__hmul2(as_half2(st[1][k]), sc));
+            }
+        }
         if (kTail) {
-            // parameters of tokens that do not count may be anything, NaN included
-            const uint32_t k0 = (2 * t < valid ? 0x0000ffffu : 0u) |
-                                (2 * t + 1 < valid ? 0xffff0000u : 0u);
-            const uint32_t k1 = (2 * t + 8 < valid ? 0x0000ffffu : 0u) |
-                                (2 * t + 9 < valid ? 0xffff0000u : 0u);
 #pragma unroll
             for (int k = 0; k < G; ++k) {
                 st[0][k] &= (k & 1) ? k1 : k0;
@@ -439,6 +489,7 @@ struct State {
     // l over all keys; O of heads 2 t + (0, 1): v[grp][head][n], values 32 grp + 4 r + n.
     __device__ __forceinline__ void end(float (&v)[G][2][4], int lane) {
         const int t = lane & 3;
+        const float unit = __int_as_float((127 - 15 + min(15, (int)((lim >> 10) & 31u))) << 23);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -450,11 +501,11 @@ struct State {
             f2_unpack(z, zs[0], zs[1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float zz = __shfl_sync(0xffffffffu, zs[h], 4 * gr + t) + es[h];
-                v[gr][h][0] = fmaf(o[2 * gr][h], 0x1p24f, zz);
-                v[gr][h][1] = fmaf(o[2 * gr][2 + h], 0x1p20f, zz);
-                v[gr][h][2] = fmaf(o[2 * gr + 1][h], 0x1p24f, zz);
-                v[gr][h][3] = fmaf(o[2 * gr + 1][2 + h], 0x1p20f, zz);
+                const float zz = fmaf(es[h], unit, __shfl_sync(0xffffffffu, zs[h], 4 * gr + t));
+                v[gr][h][0] = fmaf(o[2 * gr][h], 0x1p24f * unit, zz);
+                v[gr][h][1] = fmaf(o[2 * gr][2 + h], 0x1p20f * unit, zz);
+                v[gr][h][2] = fmaf(o[2 * gr + 1][h], 0x1p24f * unit, zz);
+                v[gr][h][3] = fmaf(o[2 * gr + 1][2 + h], 0x1p20f * unit, zz);
             }
         }
     }
