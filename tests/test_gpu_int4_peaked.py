@@ -75,6 +75,18 @@ def attend(q, k, v, keep=None):
     return (w @ v).view(H, d), w
 
 
+def codes_and_centres(cache, table, n):
+    """|c - 8| s and |m + 8 s| [Hk, n, d] of V, and its largest step."""
+    d = cache.desc.head_dim
+    byte, shift, step, least = (torch.from_numpy(x).cuda() for x in orc.kv_i4_places(d, True))
+    x = cache.tiles[0, table.long()][:, :, 1]
+    p = x[..., 8 * d:].contiguous().view(torch.float16).double()
+    c = (x[..., byte].int() >> shift) & 15
+    s, m = (p[..., y].repeat_interleave(32, -1) for y in (step, least))
+    rows = lambda y: y.transpose(0, 1).flatten(1, 2)[:, :n]  # noqa: E731
+    return rows((c - 8).abs() * s), rows((m + 8 * s).abs()), float(rows(s).max())
+
+
 def fill(lens, Hk, d, make, seed):
     """A pool with every sequence's K and V rows as `make(rng, s, n)` gives them,
     appended without rotation; returns (cache, block tables)."""
@@ -172,6 +184,58 @@ def test_decode_relative_error(H, Hk, d, std_k, std_v, mean):
         want = attend(q[s], k, v)[0]
         err = float((got[s] - want).norm())
         assert err <= bound(want), (n, err / float(want.norm()), bound(want) / float(want.norm()))
+
+
+@pytest.mark.parametrize("std_v,mean", [(1.0, 0.0), (0.02, 0.0), (0.02, 1.0), (30.0, 0.0)])
+@pytest.mark.parametrize("H,Hk,d", [(8, 8, 128), (32, 8, 128), (64, 8, 128), (16, 8, 64), (8, 1, 64),
+                                    (8, 1, 128), (14, 2, 64), (6, 2, 128), (35, 7, 128),
+                                    (1, 1, 128), (1, 1, 64)])
+def test_decode_edge_lengths_value_by_value(H, Hk, d, std_v, mean):
+    """Every output within what its roundings can come to, a share of the weighted
+    values.  With w the weights relative to the largest:
+      - p s, p and the centre, half a step of fp16 each: 2^-11 of |c - 8| s w and
+        of |m + 8 s| w twice, and 2^-20 of both for the second order and fp32;
+      - p s below the normal range: 2^-33 of the largest step s' for each key,
+        times |c - 8| <= 8, and p there 2^-38 of the centre, which does not show;
+      - the tensor core's truncated sums of p s c, c <= 15, of up to 16 keys a
+        block: 2^-23 of at most 240 s' (w = 1) for each block of 16 keys;
+      - scores of at most 16, off by 300 roundings of 2^-24 of that: the weights
+        by 2^-12, relatively, of which half stays after the normalisation's
+        average at the very most: 2^-12 of the weighted size of V about its mean;
+      - half a step of the output."""
+    lens = [1, 2, 7, 8, 9, 15, 16, 17, 31, 32, 33, 47, 48, 49, 255, 256, 257, 1000, 4100]
+    rng = torch.Generator(device="cuda").manual_seed(H + Hk + d)
+    q = torch.randn(len(lens), H, d, device="cuda", generator=rng).half()
+
+    def make(rng, s, n):
+        k, v = (torch.randn(n, Hk, d, device="cuda", generator=rng) for _ in range(2))
+        return k, v * std_v + mean
+
+    cache, bt = fill(lens, Hk, d, make, 15)
+    got = decode(q, cache, bt, lens)
+    for s, n in enumerate(lens):
+        table = bt[s, :-(-n // 16)]
+        k, v = values(cache, table, n)
+        code, centre, top = codes_and_centres(cache, table, n)
+        want, w = attend(q[s], k, v)
+
+        def mean_of(x):
+            return (w @ x).view(H, d)
+
+        most = w.amax(-1, keepdim=True).expand(-1, -1, d).reshape(H, d)  # 1 / sum of w
+        about = mean_of(v.square()) - want.square()
+        tol = (2.0 ** -11 + 2.0 ** -20) * (mean_of(code) + 2 * mean_of(centre)) + \
+            n * top * most * (2.0 ** -30 + 2.0 ** -23 * 15) + \
+            2.0 ** -12 * about.clamp(min=0).sqrt() + step16(want) / 2
+        off = (got[s] - want).abs()
+        assert bool((off <= tol).all()), (n, float((off / tol).max()))
+        # no output, and a block left out, are seen (not beside a mean of 50 times the
+        # spread: 16 of 1000 keys move the output by 0.02 * 4 / 1000 = 8e-5, less than
+        # half a step of an fp16 output of 1, 2.4e-4)
+        assert float((want.abs() / tol).max()) > 20
+        if n > 32 and mean == 0:
+            keep = torch.arange(n, device="cuda") >= 16
+            assert bool(((attend(q[s], k, v, keep)[0] - want).abs() > tol).any()), n
 
 
 @pytest.mark.parametrize("shape", [(2, 8, 2, 128), (228, 16, 8, 64)])
