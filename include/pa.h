@@ -553,7 +553,8 @@ int pa_kv_read_i4(const pa_cache_i4_t *cache, int layer, const int32_t *block_ta
  * softmax statistics and sums are fp32; a value of V enters as
  * (c - 8) s + (m + 8 s), and a probability times s, a probability and m + 8 s
  * are rounded to fp16 on their way, scaled so that the rounding is relative
- * (2^-11) down to weights 2^-22 of the largest, whatever the size of V.
+ * (2^-11) down to weights 2^-22 of the largest, whatever the size of V.  The
+ * output is saturated at +-65504 (m + 15 s can lie past it).
  * Arguments, results and checks are those of pa_decode except the workspace,
  * whose size is pa_decode_i4_workspace_bytes(...); it too is 256-byte aligned,
  * zeroed before its first use, left ready for the next call, and serves one

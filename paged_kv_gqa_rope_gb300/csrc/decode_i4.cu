@@ -214,6 +214,12 @@ __device__ __forceinline__ uint32_t times(uint32_t hi, uint32_t lo, uint32_t s) 
     if (kNegative) x = __hneg2(x);
     return as_u32(__hfma2(as_half2(hi), x, __hmul2(as_half2(lo), x)));
 }
+// Two outputs as fp16, saturated (a value m + 15 s may lie past 65504, and the
+// roundings may carry a mean of values at the edge past it); a NaN stays one.
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
+    const __half2 top = __float2half2_rn(65504.f);
+    return as_u32(__hmax2_nan(__hmin2_nan(__floats2half2_rn(lo, hi), top), __hneg2(top)));
+}
 // (movmatrix_trans without volatile)
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -541,9 +547,9 @@ struct Row {
         const float inv = l != 0.f ? 1.f / l : 0.f;
         if constexpr (N == 4)
             *reinterpret_cast<uint2 *>(row + lane * 4) =
-                make_uint2(pack_half2(o[0] * inv, o[1] * inv), pack_half2(o[2] * inv, o[3] * inv));
+                make_uint2(pack_out(o[0] * inv, o[1] * inv), pack_out(o[2] * inv, o[3] * inv));
         else
-            *reinterpret_cast<uint32_t *>(row + lane * 2) = pack_half2(o[0] * inv, o[1] * inv);
+            *reinterpret_cast<uint32_t *>(row + lane * 2) = pack_out(o[0] * inv, o[1] * inv);
     }
 };
 // N consecutive floats that another CTA or warp may have written.
@@ -832,8 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
 #pragma unroll
                             for (int gr = 0; gr < G; ++gr)
                                 *reinterpret_cast<uint2 *>(row + 32 * gr + 4 * r) =
-                                    make_uint2(pack_half2(v[gr][h][0] * inv, v[gr][h][1] * inv),
-                                               pack_half2(v[gr][h][2] * inv, v[gr][h][3] * inv));
+                                    make_uint2(pack_out(v[gr][h][0] * inv, v[gr][h][1] * inv),
+                                               pack_out(v[gr][h][2] * inv, v[gr][h][3] * inv));
                         }
                     }
                 } else {

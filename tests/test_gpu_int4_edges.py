@@ -1,0 +1,56 @@
+"""Edges of the 4-bit cache's calls: values at the end of fp16's range."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import reference as orc
+from paged_kv_gqa_rope_gb300 import pa
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(libpa):
+    assert torch.cuda.is_available()
+    assert pa.check_device() == pa.PA_OK
+    return libpa
+
+
+def dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).cuda()
+
+
+def cache_of(tiles):
+    L, NB, Hk, _, n = tiles.shape
+    c = pa.CacheI4(L, NB, Hk, n // 10)
+    c.tiles.copy_(torch.from_numpy(tiles))
+    return c
+
+
+@pytest.mark.parametrize("n,sequences", [(1, 1), (5, 3), (40, 2), (3000, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_saturates(d, n, sequences):
+    """Finite values give finite outputs: of V rows all alike, each with -65504 and
+    65504 in every group, whose step is rounded up so that the top code stands for
+    65536 = -65504 + 15 * 8736, the output is V's row; a NaN's group stays NaN."""
+    H, Hk, NB = 4, 2, -(-n // 16)
+    rng = np.random.default_rng(3)
+    pool = rng.standard_normal((2, 1, NB, 16, Hk, d)).astype(np.float16)
+    row = np.where(np.arange(d) % 2, 65504, -65504).astype(np.float16)
+    pool[1] = row
+    pool[1, 0, 0, 0, 1, 40] = np.nan
+    tiles = orc.pack_cache_i4(pool)
+    assert orc.dequantize_cache_i4(tiles)[1, 0, 0, 0, 0].max() == 65536
+    q = rng.standard_normal((sequences, H, d)).astype(np.float16)
+    bt = dev(np.tile(np.arange(NB, dtype=np.int32), (sequences, 1)))
+    ctx = torch.full((sequences,), n, dtype=torch.int32, device="cuda")
+    ws = pa.decode_i4_workspace(sequences, H, Hk, d)
+    out = pa.decode_i4(dev(q), cache_of(tiles), bt, ctx, ws, Hk).cpu().numpy()
+    nan = np.zeros((H, d), bool)
+    nan[H // Hk:, 32:64] = True
+    assert np.array_equal(np.isnan(out), np.broadcast_to(nan, out.shape))
+    got = out.astype(np.float64)[:, ~nan]
+    want = np.broadcast_to(row.astype(np.float64), (H, d))[~nan]
+    # below the saturation, three roundings of 2^-11 of at most 8 s + |m + 8 s| = 74272
+    assert np.isfinite(got).all() and (np.abs(got - want) <= 3 * 2.0 ** -11 * 74272).all()
