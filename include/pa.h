@@ -577,8 +577,9 @@ int pa_decode_i4(const void *q, const pa_cache_i4_t *cache, int layer,
  * pa_prefill_varlen runs over that.
  *   workspace  device, 256-byte aligned, contents undefined before and after:
  *              pa_prefill_i4_workspace_bytes(scratch_blocks, ...) bytes, where
- *              scratch_blocks >= sum_s ceil(L_k(s) / 16) over all sequences;
- *              those that no longer fit set PA_DEV_WORKSPACE (and
+ *              scratch_blocks >= sum_s ceil(L_k(s) / 16) over the sequences
+ *              with new tokens (nothing of the others is read); those that no
+ *              longer fit set PA_DEV_WORKSPACE (and
  *              PA_DEV_BAD_BLOCK) and their rows of out are undefined.  One
  *              call at a time per workspace.
  * Arguments, results and checks otherwise as pa_prefill_varlen.

@@ -228,12 +228,13 @@ struct ReadI4Args {
     const int32_t *lengths;  // rows mode: [B]; scratch mode: cu_seqlens_k [B + 1]
     const int32_t *first;    // rows mode: [B] or null
     const int32_t *rows;     // rows mode: [B]
+    const int32_t *cu_q;     // scratch mode: cu_seqlens_q [B + 1]
     __half *k_out;
     __half *v_out;
     int32_t *scratch_table;  // scratch mode: [B][maxb]
     int64_t total_rows;
     int32_t *status;
-    int B, Hk, maxb, num_blocks;
+    int B, Hk, maxb, num_blocks, total_q;
 };
 
 // 8 codes (nibble i = value i) with their step and least value (each twice) ->
@@ -342,8 +343,9 @@ __device__ __forceinline__ void read_v(const uint8_t *tile, __half *out, int64_t
 }
 
 // kScratch false: rows of sequences to the caller's row positions.
-// kScratch true: every sequence's whole context into consecutive blocks of a
-// scratch fp16 pool, with its block table.
+// kScratch true: the whole context of every sequence that the prefill kernel
+// attends to (the others may be long, and have tables of another call) into
+// consecutive blocks of a scratch fp16 pool, with its block table.
 template <int D, bool kScratch>
 __global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const ReadI4Args a) {
     using T = I4Tile<D>;
@@ -358,8 +360,12 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const ReadI4Ar
                                 : (int64_t)__ldg(a.lengths + s);
         const int64_t f = !kScratch && a.first ? __ldg(a.first + s) : 0;
         const int64_t r = kScratch ? 0 : __ldg(a.rows + s);
-        const bool ok = len >= 0 && f >= 0 && f + len <= (int64_t)a.maxb * kBlockSize && r >= 0 &&
-                        (kScratch || r + len <= a.total_rows);
+        bool ok = len >= 0 && f >= 0 && f + len <= (int64_t)a.maxb * kBlockSize && r >= 0 &&
+                  (kScratch || r + len <= a.total_rows);
+        if constexpr (kScratch) {
+            const int64_t q0 = __ldg(a.cu_q + s), q1 = __ldg(a.cu_q + s + 1);
+            ok = ok && q0 >= 0 && q0 < q1 && q1 <= a.total_q && q1 - q0 <= len;
+        }
         if (len == 0) {
             // nothing to read, whatever the rest says (a padded batch)
         } else if (!ok) {
@@ -655,6 +661,8 @@ extern "C" int pa_prefill_varlen_i4(const void *q, int total_q, const pa_cache_i
     a.tiles = cache_i4_layer(cache, layer);
     a.block_tables = block_tables;
     a.lengths = cu_seqlens_k;
+    a.cu_q = cu_seqlens_q;
+    a.total_q = total_q;
     a.k_out = cache_plane(&pool, 0, 0);
     a.v_out = cache_plane(&pool, 1, 0);
     a.scratch_table = reinterpret_cast<int32_t *>(ws);

@@ -767,8 +767,9 @@ def decode_i4(q, cache: CacheI4, block_tables, context_lens, workspace, n_kv_hea
 
 def prefill_i4_workspace(scratch_blocks, num_seqs, max_blocks_per_seq, n_kv_heads, head_dim,
                          device="cuda"):
-    """A workspace for pa_prefill_varlen_i4 batches whose sequences' contexts
-    take at most `scratch_blocks` blocks of 16 tokens together."""
+    """A workspace for pa_prefill_varlen_i4 batches in which the contexts of the
+    sequences with new tokens take at most `scratch_blocks` blocks of 16 tokens
+    together."""
     n = lib().pa_prefill_i4_workspace_bytes(scratch_blocks, num_seqs, max_blocks_per_seq,
                                             n_kv_heads, head_dim)
     if n == 0:

@@ -1,4 +1,5 @@
-"""Edges of the 4-bit cache's calls: values at the end of fp16's range."""
+"""Edges of the 4-bit cache's calls: values at the end of fp16's range, sequences
+without new tokens in a prefill batch."""
 
 import numpy as np
 import pytest
@@ -6,6 +7,7 @@ import torch
 
 from oracle import reference as orc
 from paged_kv_gqa_rope_gb300 import pa
+from tests.gpu_helpers import assert_attention_close
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +56,41 @@ def test_decode_saturates(d, n, sequences):
     want = np.broadcast_to(row.astype(np.float64), (H, d))[~nan]
     # below the saturation, three roundings of 2^-11 of at most 8 s + |m + 8 s| = 74272
     assert np.isfinite(got).all() and (np.abs(got - want) <= 3 * 2.0 ** -11 * 74272).all()
+
+
+@pytest.mark.parametrize("case", ["idle", "bad table", "bad length"])
+def test_prefill_leaves_out_contexts_that_no_query_sees(case):
+    """A workspace for the sequences with new tokens is enough beside long idle
+    ones (or one refused for its length), and an idle sequence's block table is not
+    looked at."""
+    H, Hk, d = 8, 2, 64
+    rng = np.random.default_rng(5)
+    past, new = np.array([5000, 20, 0, 3000, 7]), np.array([0, 30, 17, 0, 1])
+    lens = past + new
+    need = -(-lens // 16)
+    NB = int(need.sum())
+    tiles = orc.pack_cache_i4(rng.standard_normal((2, 1, NB, 16, Hk, d)).astype(np.float16))
+    order, at = rng.permutation(NB).astype(np.int32), 0
+    bt = np.full((5, need.max()), -1, np.int32)
+    for s, n in enumerate(need):
+        bt[s, :n] = order[at:at + n]
+        at += n
+    cu_q, cu_k = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32) for x in (new, lens))
+    q = rng.standard_normal((int(new.sum()), H, d)).astype(np.float16)
+    vals = orc.read_rows_i4(orc.dequantize_cache_i4(tiles)).astype(np.float64)
+    want = orc.attention_prefill(q, vals, 0, cu_q, cu_k, bt, H, Hk)
+    used, rows, status = need[new > 0].sum(), slice(None), 0
+    if case == "bad table":
+        bt[0] = NB
+        bt[3, 1] = -1
+    if case == "bad length":  # more keys than its table has room for; nothing of it is read
+        cu_k = cu_k.copy()
+        cu_k[2:] += 16 * bt.shape[1]
+        used, rows, status = used - need[1], slice(30, None), pa.PA_DEV_BAD_LENGTH
+    ws = pa.prefill_i4_workspace(int(used), 5, bt.shape[1], Hk, d)
+    ws.fill_(0xFF)
+    got = pa.new_status()
+    out = pa.prefill_varlen_i4(dev(q), cache_of(tiles), dev(cu_q), dev(cu_k), dev(bt), 30, Hk, ws,
+                               status=got)
+    assert int(got.item()) == status
+    assert_attention_close(out, want, rows=rows)
