@@ -582,7 +582,8 @@ int pa_decode_i4(const void *q, const pa_cache_i4_t *cache, int layer,
  *              longer fit set PA_DEV_WORKSPACE (and
  *              PA_DEV_BAD_BLOCK) and their rows of out are undefined.  One
  *              call at a time per workspace.
- * Arguments, results and checks otherwise as pa_prefill_varlen.
+ * Arguments, results and checks otherwise as pa_prefill_varlen.  The size is 0
+ * for non-positive arguments and one past SIZE_MAX.
  */
 size_t pa_prefill_i4_workspace_bytes(int scratch_blocks, int num_seqs, int max_blocks_per_seq,
                                      int n_kv_heads, int head_dim);

@@ -624,8 +624,13 @@ extern "C" size_t pa_prefill_i4_workspace_bytes(int scratch_blocks, int num_seqs
     if (scratch_blocks <= 0 || num_seqs <= 0 || max_blocks_per_seq <= 0 || n_kv_heads <= 0 ||
         head_dim <= 0)
         return 0;
-    return scratch_table_bytes(num_seqs, max_blocks_per_seq) +
-           (size_t)scratch_blocks * scratch_block_bytes(n_kv_heads, head_dim);
+    // (the table's bytes and one row of a block fit a size_t; 0 if the sum does not)
+    size_t bytes;
+    if (__builtin_mul_overflow((size_t)n_kv_heads * head_dim, (size_t)kBlockSize * 4, &bytes) ||
+        __builtin_mul_overflow(bytes, (size_t)scratch_blocks, &bytes) ||
+        __builtin_add_overflow(bytes, scratch_table_bytes(num_seqs, max_blocks_per_seq), &bytes))
+        return 0;
+    return bytes;
 }
 
 extern "C" int pa_prefill_varlen_i4(const void *q, int total_q, const pa_cache_i4_t *cache,

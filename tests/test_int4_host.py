@@ -90,6 +90,17 @@ def test_sizes(libpa):
     assert libpa.pa_prefill_i4_workspace_bytes(100, 2, 30, 8, 128) >= 100 * 16 * 8 * 128 * 4 + 240
 
 
+def test_prefill_workspace_past_64_bits(libpa):
+    big = 2**31 - 1
+    size = libpa.pa_prefill_i4_workspace_bytes
+    assert size(big, 1, 1, big, 128) == 0
+    assert size(1 << 30, 1, 1, 1 << 30, 128) == 0  # 2^73: all 64 low bits are 0
+    assert size(1, big, big, big, big) == 0        # (each part fits)
+    assert size(1 << 28, 1, 1, 1 << 20, 128) == (1 << 61) + 256
+    with pytest.raises(ValueError):
+        pa.prefill_i4_workspace(1 << 30, 1, 1, 1 << 30, 128)
+
+
 def descriptor(libpa, heads=2, d=64, layers=1, blocks=10):
     c = pa.PaCacheI4()
     fake = ctypes.c_void_p(1 << 20)  # never dereferenced on the host
