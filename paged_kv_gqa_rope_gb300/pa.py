@@ -208,10 +208,19 @@ def _opt(t, dtype, name, shape):
     return None if t is None else _dev(t, dtype, name, shape)
 
 
-def _out(out, like, name="out"):
+def _out(out, like, stream=None):
     if out is None:
+        return _new_out(like, stream)
+    return _dev(out, like.dtype, "out", tuple(like.shape))
+
+
+def _new_out(like, stream):
+    """A tensor like `like` from the memory of the stream that will write it: of
+    another stream's, the work before may still be using it."""
+    if stream is None:
         return torch.empty_like(like)
-    return _dev(out, like.dtype, name, tuple(like.shape))
+    with torch.cuda.stream(stream):
+        return torch.empty_like(like)
 
 
 def check_device() -> int:
@@ -331,7 +340,7 @@ def prefill_varlen(q, cache: Cache, cu_seqlens_q, cu_seqlens_k, block_tables, ma
     _dev(block_tables, torch.int32, "block_tables", (B, None))
     _table_width(block_tables)
     _opt(status, torch.int32, "status", (1,))
-    out = _out(out, q)
+    out = _out(out, q, stream)
     _check("pa_prefill_varlen", lib().pa_prefill_varlen(
         _p(q), T, ctypes.byref(cache.desc), layer, _p(cu_seqlens_q), _p(cu_seqlens_k),
         _p(block_tables), block_tables.shape[1], B, int(max_seqlen_q), H,
@@ -351,7 +360,7 @@ def prefill_step(q, k, v, positions, slot_mapping, rope_table, cache: Cache, cu_
     _table_width(block_tables)
     if Hk != n_kv_heads:
         raise ValueError(f"k has {Hk} KV heads, n_kv_heads is {n_kv_heads}")
-    out = _out(out, q)
+    out = _out(out, q, stream)
     _check("pa_prefill_step", lib().pa_prefill_step(
         _p(q), _p(k), _p(v), _p(positions), _p(slot_mapping), _p(rope_table),
         rope_table.shape[0], ctypes.byref(cache.desc), layer, _p(cu_seqlens_q), _p(cu_seqlens_k),
@@ -385,7 +394,7 @@ def _decode_args(q, block_tables, context_lens, workspace, status):
 def decode(q, cache: Cache, block_tables, context_lens, workspace, n_kv_heads, layer=0, scale=0.0,
            out=None, status=None, stream=None):
     B, H, d = _decode_args(q, block_tables, context_lens, workspace, status)
-    out = _out(out, q)
+    out = _out(out, q, stream)
     _check("pa_decode", lib().pa_decode(
         _p(q), ctypes.byref(cache.desc), layer, _p(block_tables), block_tables.shape[1],
         _p(context_lens), B, H, n_kv_heads, d, float(scale), _p(workspace), workspace.numel(),
@@ -408,7 +417,7 @@ def decode_step(q, k, v, positions, slot_mapping, rope_table, cache: Cache, bloc
                 context_lens, workspace, n_kv_heads, layer=0, scale=0.0, out=None, status=None,
                 stream=None):
     """pa_decode_step: RoPE + append of the new tokens, then decode."""
-    out = _out(out, q)
+    out = _out(out, q, stream)
     args = _step_args(q, k, v, positions, slot_mapping, rope_table, cache, block_tables,
                       context_lens, workspace, n_kv_heads, layer, scale, out, status)
     _check("pa_decode_step", lib().pa_decode_step(*args, _stream(stream)))
@@ -584,7 +593,7 @@ def rope_kv_write_i8(q, k, v, positions, slot_mapping, table, cache: CacheI8, la
 def decode_i8(q, cache: CacheI8, block_tables, context_lens, workspace, n_kv_heads, layer=0,
               scale=0.0, out=None, status=None, stream=None):
     B, H, d = _decode_args(q, block_tables, context_lens, workspace, status)
-    out = _out(out, q)
+    out = _out(out, q, stream)
     _check("pa_decode_i8", lib().pa_decode_i8(
         _p(q), ctypes.byref(cache.desc), layer, _p(block_tables), block_tables.shape[1],
         _p(context_lens), B, H, n_kv_heads, d, float(scale), _p(workspace), workspace.numel(),
@@ -755,7 +764,7 @@ def decode_i4(q, cache: CacheI4, block_tables, context_lens, workspace, n_kv_hea
     except (AttributeError, ValueError):
         _refuse_rank((q, 3, "q"), (block_tables, 2, "block_tables"), (workspace, 1, "workspace"))
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_out(q, stream)
     _call_on(dev, "pa_decode_i4", stream, _on(dev, q, torch.float16, "q", B, H, d),
              _cache_i4(dev, cache), layer,
              _on(dev, block_tables, torch.int32, "block_tables", B, width),
@@ -789,7 +798,7 @@ def prefill_varlen_i4(q, cache: CacheI4, cu_seqlens_q, cu_seqlens_k, block_table
     except (AttributeError, ValueError):
         _refuse_rank((q, 3, "q"), (block_tables, 2, "block_tables"), (workspace, 1, "workspace"))
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_out(q, stream)
     _call_on(dev, "pa_prefill_varlen_i4", stream, _on(dev, q, torch.float16, "q", T, H, d), T,
              _cache_i4(dev, cache), layer,
              _on(dev, cu_seqlens_q, torch.int32, "cu_seqlens_q", B + 1),

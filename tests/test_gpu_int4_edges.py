@@ -1,5 +1,5 @@
 """Edges of the 4-bit cache's calls: values at the end of fp16's range, sequences
-without new tokens in a prefill batch."""
+without new tokens in a prefill batch, outputs made on a stream of the caller's."""
 
 import numpy as np
 import pytest
@@ -94,3 +94,35 @@ def test_prefill_leaves_out_contexts_that_no_query_sees(case):
                                status=got)
     assert int(got.item()) == status
     assert_attention_close(out, want, rows=rows)
+
+
+def test_outputs_belong_to_the_stream_that_writes_them():
+    """An output made by the call is not memory that was freed on the current
+    stream, where work may still be using it, when the call is given another."""
+    B, H, Hk, d = 64, 16, 2, 128
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = torch.randn(B, H, d, device="cuda").half()
+    bt = torch.arange(B, dtype=torch.int32, device="cuda")[:, None]
+    ctx, cu = torch.full((B,), 1, dtype=torch.int32, device="cuda"), i32(*range(B + 1))
+    c4, c16 = pa.CacheI4(1, B, Hk, d), pa.Cache(1, B, Hk, d)
+    c4.buffer.zero_()
+    c16.tensor.zero_()
+    ws4, ws16 = pa.decode_i4_workspace(B, H, Hk, d), pa.decode_workspace(B, H, Hk, d)
+    wsp = pa.prefill_i4_workspace(B, B, 1, Hk, d)
+    side = torch.cuda.Stream()
+    for call in (lambda: pa.decode_i4(q, c4, bt, ctx, ws4, Hk, stream=side),
+                 lambda: pa.prefill_varlen_i4(q, c4, cu, cu, bt, 1, Hk, wsp, stream=side),
+                 lambda: pa.decode(q, c16, bt, ctx, ws16, Hk, stream=side),
+                 lambda: pa.prefill_varlen(q, c16, cu, cu, bt, 1, Hk, stream=side)):
+        torch.cuda.synchronize()
+        freed = torch.empty_like(q)
+        torch.cuda.synchronize()
+        at = freed.data_ptr()
+        del freed
+        again = torch.empty_like(q)  # the allocator gives the block out again
+        assert again.data_ptr() == at
+        del again
+        out = call()
+        torch.cuda.synchronize()
+        assert out.data_ptr() != at
+        assert out.shape == q.shape and not bool(out.any())
