@@ -204,6 +204,12 @@ def _table_width(block_tables):
     return w
 
 
+def _bound(n):
+    """A bound on lengths as an int32 (a larger one would reach the library cut to
+    its low 32 bits)."""
+    return min(int(n), 2**31 - 1)
+
+
 def _opt(t, dtype, name, shape):
     return None if t is None else _dev(t, dtype, name, shape)
 
@@ -343,7 +349,7 @@ def prefill_varlen(q, cache: Cache, cu_seqlens_q, cu_seqlens_k, block_tables, ma
     out = _out(out, q, stream)
     _check("pa_prefill_varlen", lib().pa_prefill_varlen(
         _p(q), T, ctypes.byref(cache.desc), layer, _p(cu_seqlens_q), _p(cu_seqlens_k),
-        _p(block_tables), block_tables.shape[1], B, int(max_seqlen_q), H,
+        _p(block_tables), block_tables.shape[1], B, _bound(max_seqlen_q), H,
         n_kv_heads, d, float(scale), _p(out), _p(status), _stream(stream)))
     return out
 
@@ -364,7 +370,7 @@ def prefill_step(q, k, v, positions, slot_mapping, rope_table, cache: Cache, cu_
     _check("pa_prefill_step", lib().pa_prefill_step(
         _p(q), _p(k), _p(v), _p(positions), _p(slot_mapping), _p(rope_table),
         rope_table.shape[0], ctypes.byref(cache.desc), layer, _p(cu_seqlens_q), _p(cu_seqlens_k),
-        _p(block_tables), block_tables.shape[1], B, T, int(max_seqlen_q), H, n_kv_heads, d,
+        _p(block_tables), block_tables.shape[1], B, T, _bound(max_seqlen_q), H, n_kv_heads, d,
         float(scale), _p(out), _p(status), _stream(stream)))
     return out
 
@@ -804,7 +810,7 @@ def prefill_varlen_i4(q, cache: CacheI4, cu_seqlens_q, cu_seqlens_k, block_table
              _on(dev, cu_seqlens_q, torch.int32, "cu_seqlens_q", B + 1),
              _on(dev, cu_seqlens_k, torch.int32, "cu_seqlens_k", B + 1),
              _on(dev, block_tables, torch.int32, "block_tables", B, width),
-             _table_width(block_tables), B, int(max_seqlen_q), H, n_kv_heads, d, scale,
+             _table_width(block_tables), B, _bound(max_seqlen_q), H, n_kv_heads, d, scale,
              _on(dev, workspace, torch.uint8, "workspace", nbytes), nbytes,
              _on(dev, out, torch.float16, "out", T, H, d), _status_i4(dev, status))
     return out

@@ -1,5 +1,6 @@
 """Edges of the 4-bit cache's calls: values at the end of fp16's range, sequences
-without new tokens in a prefill batch, outputs made on a stream of the caller's."""
+without new tokens in a prefill batch, outputs made on a stream of the caller's, a
+length bound past 32 bits."""
 
 import numpy as np
 import pytest
@@ -126,3 +127,21 @@ def test_outputs_belong_to_the_stream_that_writes_them():
         torch.cuda.synchronize()
         assert out.data_ptr() != at
         assert out.shape == q.shape and not bool(out.any())
+
+
+@pytest.mark.parametrize("bound", [2**31 - 1, 2**32, 2**32 + 1, 2**63])
+def test_prefill_with_a_bound_past_32_bits(bound):
+    """max_seqlen_q bounds the lengths; one past int32 is no other bound, nor none."""
+    T, H, Hk, d = 20, 4, 2, 64
+    rng = np.random.default_rng(6)
+    tiles = orc.pack_cache_i4(rng.standard_normal((2, 1, 2, 16, Hk, d)).astype(np.float16))
+    q = dev(rng.standard_normal((T, H, d)).astype(np.float16))
+    cu, bt = dev(np.array([0, T], np.int32)), dev(np.array([[1, 0]], np.int32))
+    ws = pa.prefill_i4_workspace(2, 1, 2, Hk, d)
+    outs = []
+    for n in (T, bound):
+        status, out = pa.new_status(), torch.full_like(q, 7.0)
+        pa.prefill_varlen_i4(q, cache_of(tiles), cu, cu, bt, n, Hk, ws, out=out, status=status)
+        assert int(status.item()) == 0
+        outs.append(out)
+    assert torch.equal(*outs) and not bool((outs[0] == 7).all())
