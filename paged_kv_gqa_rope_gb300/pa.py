@@ -697,6 +697,13 @@ def _cache_i4(dev, cache):
     return ctypes.byref(cache.desc)
 
 
+def _layer_i4(layer):
+    """The library checks it against the pool; past int32 it would see another one."""
+    if not -2**31 <= layer < 2**31:
+        raise ValueError(f"layer {layer} is not one of the pool's")
+    return layer
+
+
 def _status_i4(dev, status):
     return None if status is None else _on(dev, status, torch.int32, "status", 1)
 
@@ -720,7 +727,7 @@ def rope_kv_write_i4(q, k, v, positions, slot_mapping, table, cache: CacheI4, la
              _on(dev, positions, torch.int32, "positions", T),
              _on(dev, slot_mapping, torch.int32, "slot_mapping", T), T, H, Hk, d,
              _on(dev, table, torch.float32, "table", rows, d // 2, 2), rows,
-             _cache_i4(dev, cache), layer, _status_i4(dev, status))
+             _cache_i4(dev, cache), _layer_i4(layer), _status_i4(dev, status))
     return q_out
 
 
@@ -742,7 +749,7 @@ def kv_read_i4(cache: CacheI4, block_tables, lengths, row_starts, k_out=None, v_
         _refuse_rank((block_tables, 2, "block_tables"), (out[0], 3, out[1]))
     if rows > 2**31 - 1:
         raise ValueError(f"{rows} output rows: they must stay within int32")
-    _call_on(dev, "pa_kv_read_i4", stream, ctypes.byref(cache.desc), layer,
+    _call_on(dev, "pa_kv_read_i4", stream, ctypes.byref(cache.desc), _layer_i4(layer),
              _on(dev, block_tables, torch.int32, "block_tables", B, width),
              _table_width(block_tables), _on(dev, lengths, torch.int32, "lengths", B),
              None if first_tokens is None else
@@ -772,7 +779,7 @@ def decode_i4(q, cache: CacheI4, block_tables, context_lens, workspace, n_kv_hea
     if out is None:
         out = _new_out(q, stream)
     _call_on(dev, "pa_decode_i4", stream, _on(dev, q, torch.float16, "q", B, H, d),
-             _cache_i4(dev, cache), layer,
+             _cache_i4(dev, cache), _layer_i4(layer),
              _on(dev, block_tables, torch.int32, "block_tables", B, width),
              _table_width(block_tables), _on(dev, context_lens, torch.int32, "context_lens", B), B,
              H, n_kv_heads, d, scale, _on(dev, workspace, torch.uint8, "workspace", nbytes), nbytes,
@@ -806,7 +813,7 @@ def prefill_varlen_i4(q, cache: CacheI4, cu_seqlens_q, cu_seqlens_k, block_table
     if out is None:
         out = _new_out(q, stream)
     _call_on(dev, "pa_prefill_varlen_i4", stream, _on(dev, q, torch.float16, "q", T, H, d), T,
-             _cache_i4(dev, cache), layer,
+             _cache_i4(dev, cache), _layer_i4(layer),
              _on(dev, cu_seqlens_q, torch.int32, "cu_seqlens_q", B + 1),
              _on(dev, cu_seqlens_k, torch.int32, "cu_seqlens_k", B + 1),
              _on(dev, block_tables, torch.int32, "block_tables", B, width),

@@ -1,6 +1,6 @@
 """Edges of the 4-bit cache's calls: values at the end of fp16's range, sequences
 without new tokens in a prefill batch, outputs made on a stream of the caller's, a
-length bound past 32 bits."""
+length bound and a layer past 32 bits."""
 
 import numpy as np
 import pytest
@@ -145,3 +145,26 @@ def test_prefill_with_a_bound_past_32_bits(bound):
         assert int(status.item()) == 0
         outs.append(out)
     assert torch.equal(*outs) and not bool((outs[0] == 7).all())
+
+
+@pytest.mark.parametrize("layer", [2**32, -2**32, 2**32 + 1, 2, -1])
+def test_a_layer_outside_the_pool_is_refused(layer):
+    """A layer past int32 is refused too, and not taken for its low 32 bits."""
+    B, H, Hk, d = 2, 4, 2, 64
+    f16 = lambda *s: torch.ones(*s, dtype=torch.float16, device="cuda")  # noqa: E731
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    c = pa.CacheI4(2, 2, Hk, d)
+    c.buffer.fill_(7)
+    q, bt, rows = f16(B, H, d), i32(0, 1)[:, None], i32(0, 16)
+    k_out = torch.full((32, Hk, d), 9.0, dtype=torch.float16, device="cuda")
+    wsd, wsp = pa.decode_i4_workspace(B, H, Hk, d), pa.prefill_i4_workspace(2, B, 1, Hk, d)
+    for call in (lambda: pa.rope_kv_write_i4(q, f16(B, Hk, d), f16(B, Hk, d), i32(0, 0), rows,
+                                             pa.rope_table(1, d), c, layer=layer),
+                 lambda: pa.kv_read_i4(c, bt, i32(1, 1), rows, k_out, layer=layer),
+                 lambda: pa.decode_i4(q, c, bt, i32(1, 1), wsd, Hk, layer=layer),
+                 lambda: pa.prefill_varlen_i4(q, c, i32(0, 1, 2), i32(0, 1, 2), bt, 1, Hk, wsp,
+                                              layer=layer)):
+        with pytest.raises((ValueError, pa.PAError)):
+            call()
+    torch.cuda.synchronize()
+    assert bool((c.buffer == 7).all()) and bool((k_out == 9).all()) and bool((q == 1).all())
