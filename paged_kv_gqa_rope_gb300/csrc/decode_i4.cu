@@ -195,17 +195,6 @@ __device__ __forceinline__ void mma_16816_zero(float (&d)[4], const uint32_t (&a
 __device__ __forceinline__ void cp_async_commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ __half2 as_half2(uint32_t w) {
-    return *reinterpret_cast<const __half2 *>(&w);
-}
-__device__ __forceinline__ uint32_t as_u32(__half2 h) {
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 // (hi + lo) s of two fp16 pairs, or its negative, rounded to fp16 (lo s, far
 // below it, before).
 template <bool kNegative>
@@ -675,20 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_i4_kernel(const DecodeI4Ar
     }
     if (tid == 0) sm.prefix[0] = 0;
     __syncthreads();
-    if (warp == 0) {
-        int64_t carry = 0;
-        for (int base = 1; base <= entries; base += 32) {
-            const int i = base + lane;
-            int64_t v = i <= entries ? sm.prefix[i] : 0;
-#pragma unroll
-            for (int f = 1; f < 32; f <<= 1) {
-                const int64_t u = __shfl_up_sync(0xffffffffu, v, f);
-                if (lane >= f) v += u;
-            }
-            if (i <= entries) sm.prefix[i] = v + carry;
-            carry += __shfl_sync(0xffffffffu, v, 31);
-        }
-    }
+    if (warp == 0) prefix_sums(sm.prefix, entries, lane);
     __syncthreads();
     const int64_t W = sm.prefix[entries];
     griddep_launch_dependents();

@@ -27,19 +27,6 @@ struct RopeI4Args {
     int num_tokens, n_heads, n_kv_heads, max_pos, rounds_per_cta;
 };
 
-__device__ __forceinline__ __half2 as_half2(uint32_t w) {
-    return *reinterpret_cast<const __half2 *>(&w);
-}
-__device__ __forceinline__ uint32_t as_u32(__half2 h) {
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // One group's 8 values held by this lane, its other 24 by the lanes of the
 // same aligned quad: the group's step and least value and this lane's codes,
 // value i in nibble i.  Every lane of the warp takes part.
@@ -378,20 +365,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_i4_kernel(const ReadI4Ar
     }
     if (tid == 0) prefix[0] = 0;
     __syncthreads();
-    if (tid < 32) {
-        int64_t carry = 0;
-        for (int base = 1; base <= a.B; base += 32) {
-            const int i = base + lane;
-            int64_t v = i <= a.B ? prefix[i] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
-            }
-            if (i <= a.B) prefix[i] = v + carry;
-            carry += __shfl_sync(0xffffffffu, v, 31);
-        }
-    }
+    if (tid < 32) prefix_sums(prefix, a.B, lane);
     __syncthreads();
     const int64_t units = prefix[a.B];
     // warps take (block, head) pairs, the heads of a block side by side

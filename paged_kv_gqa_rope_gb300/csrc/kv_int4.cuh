@@ -39,6 +39,29 @@ struct I4Tile {
     }
 };
 
+__device__ __forceinline__ __half2 as_half2(uint32_t w) {
+    return *reinterpret_cast<const __half2 *>(&w);
+}
+__device__ __forceinline__ uint32_t as_u32(__half2 h) {
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// x[1] .. x[n] become their running sums; one warp.
+__device__ __forceinline__ void prefix_sums(int64_t *x, int n, int lane) {
+    int64_t carry = 0;
+    for (int base = 1; base <= n; base += 32) {
+        const int i = base + lane;
+        int64_t v = i <= n ? x[i] : 0;
+#pragma unroll
+        for (int f = 1; f < 32; f <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, v, f);
+            if (lane >= f) v += u;
+        }
+        if (i <= n) x[i] = v + carry;
+        carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+}
+
 inline bool cache_i4_ok(const pa_cache_i4_t *c, int layer, int n_kv_heads, int head_dim) {
     return c && c->base && (reinterpret_cast<uintptr_t>(c->base) & 255u) == 0 &&
            c->block_size == kBlockSize && c->n_kv_heads == n_kv_heads &&
