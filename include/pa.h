@@ -199,7 +199,9 @@ int pa_rope_kv_write(void *q, void *k, const void *v, const int32_t *positions,
  *   scale        softmax scale; pass 0 for 1/sqrt(head_dim)
  * Built for head_dim 64 and 128, any n_heads divisible by n_kv_heads and
  * num_seqs <= 2048 (PA_ERR_UNSUPPORTED beyond); Q.K^T and P.V run on the
- * tcgen05 tensor cores with TMEM accumulators.
+ * tcgen05 tensor cores with TMEM accumulators.  A value of V that is not finite
+ * makes NaN not only of the rows that attend to it but, as 0 times NaN, of the
+ * up to 255 rows before it that are computed beside its tile of 128 keys.
  */
 int pa_prefill_varlen(const void *q, int total_q, const pa_cache_t *cache, int layer,
                       const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
@@ -570,9 +572,10 @@ int pa_decode_i4(const void *q, const pa_cache_i4_t *cache, int layer,
 
 /*
  * pa_prefill_varlen against the 4-bit pool: each key and value is the fp16
- * row that pa_kv_read_i4 gives (for the new tokens too, which must already
- * have been written by pa_rope_kv_write_i4, so a later decode step sees the
- * same context).  The rows the batch sees are read back into the workspace
+ * row that pa_kv_read_i4 gives, for the new tokens too, which must already
+ * have been written by pa_rope_kv_write_i4.  A later decode step reads the same
+ * codes as m + s * c itself; prefill sees each value rounded once more, to fp16,
+ * and saturated.  The rows the batch sees are read back into the workspace
  * once, as a scratch fp16 pool, and the tensor-core kernel of
  * pa_prefill_varlen runs over that.
  *   workspace  device, 256-byte aligned, contents undefined before and after:

@@ -14,12 +14,14 @@
 // whose record of it arrives last.  Every join sums in the order of the line,
 // so the result does not depend on who arrives when.
 //
-// Bound: HBM on paper (1.25 d bytes per token and KV head); measured, the warp
-// schedulers: about 275 warp instructions and 22 MMAs a block, 5.5 TB/s on
-// 32 x 32 heads of 2049 keys (61 us, 82 % of the copy peak; the same loads
-// without the arithmetic take 53), and on short launches the edges, about 7 us
-// to the first tiles and 5 to the joins (32 x 8 heads of 4097 keys: 39.4 us,
-// 64 %).  Time grows in proportion from 12 warps an SM to 10, and 16 warps of
+// Bound: HBM on paper (1.25 d bytes per token and KV head); measured, the
+// latency of dependent instructions at three warps a scheduler, which issue half
+// the slots (2.0 of 4 an SM; of the waits a fixed latency is the longest, then
+// the tensor and integer pipes): about 285 warp instructions and 22 MMAs a block,
+// 5.4 TB/s on 32 x 32 heads of 2049 keys (62.3 us, 81 % of the copy peak; the same
+// loads without the arithmetic take 53).  On short launches the edges, about 7 us
+// to the first tiles and 5 to the joins (32 x 8 heads of 4097 keys: 40.1 us,
+// 63 %).  Time grows in proportion from 12 warps an SM to 10, and 16 warps of
 // 128 registers spill what they gain.
 //
 // Arithmetic, on warp-level MMAs (scores S^T = K Q^T and O^T = V^T P^T, the g
@@ -53,8 +55,8 @@
 //     step, and below it off by at most 2^-33 of that, whatever the size of V; a
 //     larger step scales the sums down as a larger score does.  (As they come,
 //     beside one key with most of the weight the others' p s is subnormal or
-//     nothing: 32768 keys with V of std 0.02, and a value of zero that had 0.9 of
-//     the weight, came out with a relative error of 0.3.)  The small steps'
+//     nothing: 32768 keys with V of std 0.1, and a value of zero that had 0.9 of
+//     the weight, came out with a relative error of 0.33.)  The small steps'
 //     products are under a branch: 32 x 8 heads of 4097 keys take 39.9 us without
 //     and 40.3 with them, 40.5 where they are always made.
 //   - The running maximum is raised only when a score passes it by kLazy
@@ -74,8 +76,10 @@ constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxGrid = 152;  // CTAs the workspace has records for
 // Units of the line for a pair's fixed cost, in blocks: 64 histories of 16 to 16384
-// tokens took 49.0, 46.4, 46.6, 46.8 and 47.0 us with 2, 3, 4, 6 and 8, one history
-// of 32768 20.3, 20.2, 18.8, 19.9 and 19.8; equal histories do not care.
+// tokens took 49.0, 46.4, 46.6, 46.8 and 47.0 us with 2, 3, 4, 6 and 8, so that 3 to
+// 8 serve alike; equal histories do not care.  (One history of 32768 over 8 heads
+// took 20.3, 20.2, 18.8, 19.9 and 19.8: with 4 its 8 (2048 + 4) units happen to be 9
+// for each of the 1824 warps.)
 constexpr int kPairCost = 4;
 constexpr int kMinUnits = 4;   // least units of a warp's range
 constexpr int kSeqStep = 4;    // sequences per entry of the prefix table
