@@ -597,6 +597,207 @@ int pa_prefill_varlen_i4(const void *q, int total_q, const pa_cache_i4_t *cache,
                          void *workspace, size_t workspace_bytes, void *out, int32_t *dev_status,
                          pa_stream_t stream);
 
+/*
+ * The rotary append with another layout than pa_rope_kv_write's, over a part
+ * of the head, with Q going to a buffer of its own.  Layouts of the pairs
+ * among the first rotary_dim values x of a row, r = rotary_dim:
+ *   PA_ROPE_INTERLEAVED  (x_2i, x_2i+1), as pa_rope_kv_write
+ *   PA_ROPE_HALF         (x_i, x_(i + r/2)), i < r/2
+ * Pair i is turned by entry i of the table's row positions[t], in the
+ * arithmetic of pa_rope_kv_write; the values from rotary_dim on pass
+ * unchanged.  K (turned) and V go to slot_mapping[t] of the cache; unlike
+ * pa_rope_kv_write, k itself is left as it is.  With rotary_dim = head_dim,
+ * PA_ROPE_INTERLEAVED and q_out = q, Q and the cache come out bit for bit as
+ * pa_rope_kv_write's.
+ *   q_out       device fp16, the rotated Q: q itself (in place) or a buffer
+ *               that does not overlap q, k or v
+ *   rotary_dim  a multiple of 16 (PA_ERR_UNSUPPORTED otherwise), at most head_dim
+ *   rope_table  device float pairs {cos, sin} [max_positions][rotary_dim / 2],
+ *               16-byte aligned: pa_rope_table_init(table, max_positions,
+ *               rotary_dim, ...) or pa_rope_table_init_scaled
+ * Other arguments, results and device-side checks are those of
+ * pa_rope_kv_write: a bad position leaves the token's q_out row and slot as
+ * they were.  Two tokens of one call must not share a slot.
+ */
+enum pa_rope_layout { PA_ROPE_INTERLEAVED = 0, PA_ROPE_HALF = 1 };
+int pa_rope_kv_write_layout(const void *q, void *q_out, const void *k, const void *v,
+                            const int32_t *positions, const int32_t *slot_mapping, int num_tokens,
+                            int n_heads, int n_kv_heads, int head_dim, int layout, int rotary_dim,
+                            const void *rope_table, int max_positions, const pa_cache_t *cache,
+                            int layer, int32_t *dev_status, pa_stream_t stream);
+
+/*
+ * pa_rope_table_init with frequencies changed for contexts longer than the
+ * model was trained on.  f_i = theta^(-2i / r), r = rotary_dim, i < r / 2:
+ *   PA_ROPE_UNSCALED  f_i
+ *   PA_ROPE_LINEAR    f_i / factor (positions divided by the factor)
+ *   PA_ROPE_NTK       f_i of the base theta * factor^(r / (r - 2)): the slowest
+ *                     pair is slowed by the factor, the fastest not at all
+ *   PA_ROPE_YARN      f_i * keep_i + f_i / factor * (1 - keep_i), keep_i falling
+ *                     from 1 to 0, linearly in i, from
+ *                     floor(r ln(original_positions / (2 pi high)) / (2 ln theta)) to
+ *                     ceil (r ln(original_positions / (2 pi low )) / (2 ln theta))
+ *                     (both brought into 0 .. r - 1): pairs that turn more than
+ *                     `high` times over original_positions are kept, those that
+ *                     turn less than `low` times slowed
+ *   PA_ROPE_BANDS     the same mix with keep_i = clamp((turns_i - low) /
+ *                     (high - low), 0, 1), turns_i = original_positions f_i / (2 pi)
+ * Entries are {a cos, a sin} of m f_i, computed in double precision on the host
+ * and rounded once to float; a = attention, or, where that is 0, 1, and for
+ * PA_ROPE_YARN 0.1 ln(factor) + 1.  factor >= 1; 0 < low < high and
+ * original_positions > 0 for the last two kinds; scaling NULL is
+ * PA_ROPE_UNSCALED.  rotary_dim: a multiple of 16 up to 128
+ * (PA_ERR_UNSUPPORTED otherwise).  device_table holds
+ * pa_rope_table_bytes(max_positions, rotary_dim) bytes, 16-byte aligned.
+ * Synchronises `stream`.
+ */
+enum pa_rope_scaling_kind {
+    PA_ROPE_UNSCALED = 0,
+    PA_ROPE_LINEAR = 1,
+    PA_ROPE_NTK = 2,
+    PA_ROPE_YARN = 3,
+    PA_ROPE_BANDS = 4
+};
+typedef struct {
+    int32_t kind;               /* pa_rope_scaling_kind */
+    int32_t original_positions; /* YARN, BANDS */
+    double factor;
+    double low, high;           /* YARN, BANDS: turns over original_positions */
+    double attention;           /* 0: the kind's own */
+} pa_rope_scaling_t;
+int pa_rope_table_init_scaled(void *device_table, int max_positions, int rotary_dim, double theta,
+                              const pa_rope_scaling_t *scaling, pa_stream_t stream);
+
+/*
+ * pa_decode for sequences that share a prefix ("nano-vllm notes - Llama",
+ * scheduler.py: a prefix-cache hit makes block tables name the same blocks).
+ * Group r is sequences group_starts[r] .. group_starts[r + 1] - 1, whose block
+ * tables begin with the same shared_blocks[r] blocks.  Those blocks are read
+ * once for the whole group, all its queries against them on the tcgen05 tensor
+ * cores, the rest of each context as by pa_decode, and the parts joined by an
+ * online softmax: the results are pa_decode's up to rounding.
+ *   group_starts   device int32 [num_groups + 1], rising from 0 to num_seqs
+ *                  (empty groups allowed)
+ *   shared_blocks  device int32 [num_groups], each at most
+ *                  floor(context_lens[s] / 16) of every sequence s of the group
+ *                  (nothing but the shared blocks is allowed); 0 or a group of
+ *                  one sequence shares nothing
+ *   num_groups     1 .. 4096
+ *   workspace      pa_decode_shared_workspace_bytes(...) bytes, otherwise as
+ *                  pa_decode's: 256-byte aligned, ZEROED before its first use,
+ *                  left ready for the next call (of any shape that it is large
+ *                  enough for), one call at a time (two streams, or two captured
+ *                  graphs that may run together, take one each).  A smaller one
+ *                  gives PA_ERR_WORKSPACE.
+ * The blocks are read through the table of the group's first sequence that is
+ * in order.  A sequence whose length is out of range or shorter than its shared
+ * blocks, and every sequence of a group whose shared_blocks is out of range,
+ * sets PA_DEV_BAD_LENGTH and its output is not written; group_starts that do not
+ * rise from 0 to num_seqs leave all outputs so.  Shared blocks whose id is out
+ * of range set PA_DEV_BAD_BLOCK and drop out of the group's attention, as in
+ * pa_decode.  Other arguments, results and limits are those of pa_decode, and
+ * num_seqs * n_kv_heads <= 262144.
+ */
+size_t pa_decode_shared_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads, int head_dim);
+int pa_decode_shared(const void *q, const pa_cache_t *cache, int layer,
+                     const int32_t *block_tables, int max_blocks_per_seq,
+                     const int32_t *context_lens, int num_seqs, const int32_t *group_starts,
+                     const int32_t *shared_blocks, int num_groups, int n_heads, int n_kv_heads,
+                     int head_dim, float scale, void *workspace, size_t workspace_bytes, void *out,
+                     int32_t *dev_status, pa_stream_t stream);
+
+/*
+ * Groups for pa_decode_shared, host to host: goes through the sequences in
+ * order and puts one into the group before it while their tables' common
+ * leading full blocks save at least as many block reads as the group saves
+ * without it.  Sequences with a common prefix should stand next to each other.
+ *   block_tables   host int32 [num_seqs][max_blocks_per_seq]
+ *   context_lens   host int32 [num_seqs]
+ *   group_starts   host int32 [num_seqs + 1]  (output: num_groups + 1 of them)
+ *   shared_blocks  host int32 [num_seqs]      (output: num_groups of them)
+ *   num_groups     host int32                 (output)
+ * PA_ERR_INVALID for a length that is negative or longer than its table row
+ * (nothing is written).
+ */
+int pa_prepare_shared(int num_seqs, const int32_t *block_tables, int max_blocks_per_seq,
+                      const int32_t *context_lens, int block_size, int32_t *group_starts,
+                      int32_t *shared_blocks, int32_t *num_groups);
+
+/*
+ * pa_decode that also adds up how much attention each cached token receives
+ * (what pa_kv_evict goes by): with p[h][t] the softmax weight of token t in Q
+ * head h's row,
+ *     weights_out[s][kv][t] = weights[s][kv][t] + sum over the Q heads h of KV
+ *                             head kv of p[h][t],   t < context_lens[s].
+ *   weights      device fp32 [num_seqs][n_kv_heads][weights_stride], or NULL
+ *                for zeros
+ *   weights_out  the same shape: weights itself (in place) or a buffer that does
+ *                not overlap it.  Places from context_lens[s] on stay as they
+ *                were, so a buffer that starts as zeros is ready for the
+ *                sequence's next tokens.
+ *   weights_stride  floats between rows; a context longer than it sets
+ *                PA_DEV_BAD_LENGTH and nothing of the sequence is written
+ *   workspace    pa_decode_weights_workspace_bytes(..., score_blocks) bytes with
+ *                score_blocks >= sum_s ceil(context_lens[s] / 16): the call keeps
+ *                4 bytes a (Q head, token) between its kernels.  Sequences that
+ *                no longer fit set PA_DEV_WORKSPACE: their out is written, their
+ *                weights are not.  256-byte aligned, ZEROED before its first
+ *                use, left ready for the next call (of any shape that it is
+ *                large enough for); one call at a time.
+ * Other arguments, results, checks and limits are those of pa_decode, and
+ * num_seqs * n_kv_heads <= 262144.  The size
+ * is 0 for non-positive arguments and one past SIZE_MAX.
+ */
+size_t pa_decode_weights_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads, int head_dim,
+                                         int64_t score_blocks);
+int pa_decode_weights(const void *q, const pa_cache_t *cache, int layer,
+                      const int32_t *block_tables, int max_blocks_per_seq,
+                      const int32_t *context_lens, int num_seqs, int n_heads, int n_kv_heads,
+                      int head_dim, float scale, const float *weights, float *weights_out,
+                      int64_t weights_stride, void *workspace, size_t workspace_bytes, void *out,
+                      int32_t *dev_status, pa_stream_t stream);
+
+/*
+ * Shortens cached sequences to `budget` tokens, by weight.  Of a sequence's
+ * n = context_lens[s] tokens each KV head keeps k = min(n, budget): the first
+ * `sinks`, the last `recent` and, of the others, those of the largest weights
+ * (NaN counts as the smallest; of equal weights the earlier token stays), in
+ * their order: kept token i's K and V rows go to place i, its weight to
+ * weights_out[s][kv][i], and the weights of places k .. n - 1 become 0.
+ * Afterwards out_context_lens[s] = k.  KV heads keep different tokens, which
+ * decode and prefill do not see: keys carry their rotation, so the next token
+ * goes to slot k of the shortened sequence with the position it would have had
+ * (pass positions and slots apart to the append).
+ *   weights      device fp32 [num_seqs][n_kv_heads][weights_stride]
+ *   weights_out  weights itself (in place) or a buffer that does not overlap it
+ *                (its places from n on stay as they were)
+ *   budget       at least 1; 0 <= sinks, recent; sinks + recent <= budget
+ *   out_block_tables  device int32 [num_seqs][out_max_blocks_per_seq]: where the
+ *                kept rows go.  Entry j is either block_tables' own entry j (in
+ *                place, and the same pointer may be passed) or a block that
+ *                block_tables names nowhere, which leaves the old rows as they
+ *                are: a block that other sequences still read (a shared prefix)
+ *                has to be replaced.  No two sequences may name the same block
+ *                among the entries that receive rows.
+ *   out_context_lens  device int32 [num_seqs]; may be context_lens, unless other
+ *                layers' calls still need the old lengths
+ *   workspace    pa_kv_evict_workspace_bytes(num_seqs, n_kv_heads, budget) bytes
+ *                (a budget past max_blocks_per_seq * 16 counts as that), 256-byte
+ *                aligned, contents undefined before and after; one call at a time
+ * A length of 0 is in order (nothing moves).  One that is negative or longer than
+ * a table row, or than weights_stride, or whose k tokens pass
+ * out_max_blocks_per_seq * 16, sets PA_DEV_BAD_LENGTH and the sequence is left as
+ * it is (out_context_lens[s] too); a block id outside the pool sets
+ * PA_DEV_BAD_BLOCK and its rows do not move.  num_seqs <= 4096.
+ */
+size_t pa_kv_evict_workspace_bytes(int num_seqs, int n_kv_heads, int budget);
+int pa_kv_evict(const pa_cache_t *cache, int layer, const int32_t *block_tables,
+                int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int n_kv_heads,
+                int head_dim, const float *weights, float *weights_out, int64_t weights_stride,
+                int budget, int sinks, int recent, const int32_t *out_block_tables,
+                int out_max_blocks_per_seq, int32_t *out_context_lens, void *workspace,
+                size_t workspace_bytes, int32_t *dev_status, pa_stream_t stream);
+
 /* Human-readable text of a pa_status code. */
 const char *pa_strerror(int code);
 

@@ -460,3 +460,107 @@ def read_rows_i4(values64) -> np.ndarray:
     """fp16 rows as the library reads them back: the value (exact in float64)
     saturated and rounded once to fp16."""
     return np.minimum(values64, 65504).astype(np.float16)
+
+
+# ---------------------------------------------------------------------------
+# Long contexts: other rotary layouts and scaled tables, decode's attention
+# weights, eviction by them (a shared prefix changes nothing that is computed:
+# attention_decode is its oracle)
+# ---------------------------------------------------------------------------
+
+def rope_scaled_frequencies(rotary_dim, theta=10000.0, scaling=None, factor=1.0,
+                            original_positions=0, low=1.0, high=4.0, attention=0.0):
+    """(frequencies of the rotary_dim / 2 pairs, magnitude of the table's entries),
+    Python floats."""
+    r, n = rotary_dim, rotary_dim // 2
+    magnitude = attention or 1.0
+    if scaling == "ntk":
+        theta = theta * factor ** (r / (r - 2))
+    f = [1.0 / theta ** (2 * i / r) for i in range(n)]
+    if scaling in (None, "ntk"):
+        return f, magnitude
+    if scaling == "linear":
+        return [x / factor for x in f], magnitude
+    turns = original_positions / (2 * math.pi)
+    if scaling == "bands":
+        keep = [(turns * x - low) / (high - low) for x in f]
+    else:
+        def pair(t):  # the pair that turns t times over the original positions
+            return r * math.log(turns / t) / (2 * math.log(theta))
+        first, last = max(math.floor(pair(high)), 0), min(math.ceil(pair(low)), r - 1)
+        width = last - first if last > first else 0.001
+        keep = [1 - (i - first) / width for i in range(n)]
+        magnitude = attention or 0.1 * math.log(factor) + 1.0
+    keep = [min(max(k, 0.0), 1.0) for k in keep]
+    return [x * k + x / factor * (1 - k) for x, k in zip(f, keep)], magnitude
+
+
+def rope_scaled_table(max_positions, rotary_dim, **scaling):
+    """float32 [max_positions, rotary_dim / 2, 2] {cos, sin}, rounded once from
+    float64."""
+    f, a = rope_scaled_frequencies(rotary_dim, **scaling)
+    ang = np.arange(max_positions, dtype=np.float64)[:, None] * np.asarray(f)
+    return np.stack([a * np.cos(ang), a * np.sin(ang)], -1).astype(np.float32)
+
+
+def rope_layout_pinned(x16, positions, table, half):
+    """rope_pinned with the pairs of a layout among the first 2 * table.shape[1]
+    values, the angles from a table; the other values unchanged."""
+    x16 = np.asarray(x16, np.float16)
+    r = 2 * table.shape[1]
+    out = x16.copy()
+    a, b = (slice(0, r // 2), slice(r // 2, r)) if half else (slice(0, r, 2), slice(1, r, 2))
+    x, y = x16[..., a].astype(np.float32), x16[..., b].astype(np.float32)
+    c, s = (table[np.asarray(positions)][:, None, :, i] for i in (0, 1))
+    out[..., a] = ((x * c) - (y * s)).astype(np.float16)  # each op rounds to float32
+    out[..., b] = ((x * s) + (y * c)).astype(np.float16)
+    return out
+
+
+def decode_weights(q16, cache, layer, block_tables, context_lens, n_heads, n_kv_heads, scale=None):
+    """For every sequence, float64 [n_kv_heads, context_lens[s]]: each cached token's
+    softmax weight, summed over the Q heads of the KV head."""
+    B, H, d = q16.shape
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    out = []
+    for s in range(B):
+        n = int(context_lens[s])
+        K, _ = gather_kv(cache, layer, block_tables[s], n)
+        w = np.zeros((n_kv_heads, n))
+        for h in range(H):
+            kv = h // (H // n_kv_heads)
+            w[kv] += _softmax_rows((K[:, kv] @ q16[s, h].astype(np.float64)) * scale)
+        out.append(w)
+    return out
+
+
+def evict_keep(weights, budget, sinks, recent):
+    """Tokens kept of a (sequence, KV head) with the given weights, in order: the first
+    `sinks`, the last `recent`, and the largest of the others (NaN the smallest, of equal
+    ones the earlier), `budget` in all."""
+    n = len(weights)
+    if n <= budget:
+        return list(range(n))
+    fixed = list(range(sinks)) + list(range(n - recent, n))
+    others = sorted(range(sinks, n - recent),
+                    key=lambda t: (np.isnan(weights[t]), -weights[t] if weights[t] == weights[t] else 0, t))
+    return sorted(fixed + others[:budget - sinks - recent])
+
+
+def evict(cache, layer, block_tables, context_lens, weights, budget, sinks, recent, out_tables):
+    """In place on `cache` and `weights` [B, n_kv_heads, stride]: rows and weights of the
+    kept tokens move to the first places.  Returns the new lengths."""
+    bs = cache.shape[3]
+    old, lens = cache.copy(), np.asarray(context_lens).copy()
+    for s, n in enumerate(context_lens):
+        n = int(n)
+        for h in range(weights.shape[1]):
+            kept = evict_keep(weights[s, h, :n], budget, sinks, recent)
+            moved = weights[s, h, kept]
+            weights[s, h, :n] = 0
+            weights[s, h, :len(kept)] = moved
+            for i, t in enumerate(kept):
+                cache[:, layer, out_tables[s][i // bs], i % bs, h] = \
+                    old[:, layer, block_tables[s][t // bs], t % bs, h]
+        lens[s] = min(n, budget)
+    return lens

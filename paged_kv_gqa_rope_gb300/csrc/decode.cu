@@ -48,6 +48,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "decode_modes.cuh"
 #include "internal.h"
 
 namespace pa {
@@ -69,7 +70,18 @@ struct DecodeArgs {
     int32_t *status;
     float scale_log2;             // scale * log2(e)
     int B, H, Hk, g, maxb, num_blocks;
+    DecodeScores sc;              // Mode::kScores
+    DecodeTails tl;               // Mode::kTails
 };
+
+// What a launch leaves besides, or in the place of, the output (internal.h).
+enum class Mode { kOut, kScores, kTails };
+
+// P enters the tensor core as 2^(x - max + kPShift) in the modes other than
+// kOut, at most 2^15: fp16 then holds it with its full 11 bits down to 2^-29 of
+// the row's largest, not 2^-14, at no cost (the exponent's argument takes the
+// shift with the maximum).
+constexpr float kPShift = 15.f;
 
 // Shared memory of one ring stage.  fp16 cache: the K and V tiles of one
 // (block, KV head) as TMA writes them (128-byte swizzle).  int8 cache: the
@@ -123,7 +135,19 @@ struct Segment {
     int64_t pair_start, pair_end;
 };
 
-template <int kCost, bool kFront>
+// First block (all KV heads counted) of sequence s in the scores, or -1 and
+// PA_DEV_WORKSPACE if they do not fit.
+template <int kCost>
+__device__ __forceinline__ int64_t scores_start(const DecodeArgs &a, const int64_t *prefix,
+                                                const int32_t *lens, int s, int32_t *status) {
+    const int64_t at = prefix[s] - (int64_t)s * kCost * a.Hk;
+    const int64_t n = (int64_t)((lens[s] + kBlockSize - 1) / kBlockSize) * a.Hk;
+    if (at + n <= a.sc.capacity) return at;
+    report(status, PA_DEV_WORKSPACE);
+    return -1;
+}
+
+template <int kCost, bool kFront, bool kShared = false>
 __device__ __forceinline__ Segment segment_at(int64_t pos, int64_t end, const int64_t *prefix,
                                               int B, const int32_t *context_lens) {
     int lo = 0, hi = B - 1;  // largest s with prefix[s] <= pos
@@ -136,7 +160,7 @@ __device__ __forceinline__ Segment segment_at(int64_t pos, int64_t end, const in
     }
     Segment g;
     g.s = lo;
-    g.ctx = __ldg(context_lens + lo);
+    g.ctx = kShared ? context_lens[lo] : __ldg(context_lens + lo);  // (shared memory)
     const int nblk = (g.ctx + kBlockSize - 1) / kBlockSize;
     const int span = kCost + nblk;
     const int64_t rem = pos - prefix[lo];
@@ -275,7 +299,32 @@ __device__ __forceinline__ int ld_acquire_gpu(const int *p) {
 // sum), the row sum and the O of the head's D columns (lane = column within
 // each run of 32) accumulated in piece order, the O values of four pieces
 // loaded at a time (two for the int8 kernel, whose registers are capped).
-template <int D, bool I8>
+// One element (head h of the pair, value d) of a finished pair: O unnormalised,
+// M the maximum, L the sum of the row.
+template <int D, Mode MODE>
+__device__ __forceinline__ void emit(const DecodeArgs &a, int s, int kvh, int h, int d, float O,
+                                     float M, float L) {
+    const int64_t row = (int64_t)s * a.H + kvh * a.g + h;
+    if constexpr (MODE == Mode::kTails) {
+        float *r = a.tl.rec + row * (D + 4);
+        r[d] = O;
+        if (d == 0) {
+            r[D] = M - kPShift;
+            r[D + 1] = L;
+        }
+    } else {
+        if constexpr (MODE == Mode::kOut) {
+            a.out[row * D + d] = __float2half_rn(L > 0.f ? O / L : 0.f);
+        } else {  // (NaN stays NaN; a row whose blocks are all out of range is 0)
+            const bool none = L == 0.f;
+            a.out[row * D + d] = __float2half_rn(none ? 0.f : O / L);
+            if (d == 0)
+                a.sc.stats[row] = none ? make_float2(0.f, 0.f) : make_float2(M - kPShift, 1.f / L);
+        }
+    }
+}
+
+template <int D, bool I8, Mode MODE>
 __device__ void warp_merge_records(const DecodeArgs &a, const Segment &sg, int64_t W, int G,
                                    int lane) {
     constexpr int kRec = D + 4;
@@ -329,12 +378,16 @@ __device__ void warp_merge_records(const DecodeArgs &a, const Segment &sg, int64
         }
 #pragma unroll
         for (int rr = 0; rr < kRuns; ++rr)
-            a.out[((int64_t)sg.s * a.H + sg.kvh * a.g + h) * D + rr * 32 + lane] =
-                __float2half_rn(Lsum > 0.f ? O[rr] / Lsum : 0.f);
+            emit<D, MODE>(a, sg.s, sg.kvh, h, rr * 32 + lane, O[rr], M, Lsum);
     }
 }
 
-template <int D, int NSTAGE, bool I8>
+// The lines of the modes other than kOut: every sequence has its cost units, one
+// with no blocks (nothing behind its shared prefix, or a bad length) nothing
+// else, and `lens` in shared memory has the tokens that are the sequence's here
+// (0 for a bad length).  Blocks of all KV heads ahead of sequence s:
+// prefix[s] - s * kCost * Hk.
+template <int D, int NSTAGE, bool I8, Mode MODE>
 __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     decode_kernel(const __grid_constant__ CUtensorMap kvmap,
                   const __grid_constant__ CUtensorMap smap, const DecodeArgs a) {
@@ -363,19 +416,39 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     float *sm_pl = sm_pm + kConsumerWarps * kGroupPad;             // [4][8]  sum) per head
     int *sm_flag = reinterpret_cast<int *>(sm_pl + kConsumerWarps * kGroupPad);  // [4]
     int64_t *prefix = reinterpret_cast<int64_t *>(sm_flag + 4);    // [B + 1]
+    constexpr bool kOut = MODE == Mode::kOut;
+    int32_t *lens = reinterpret_cast<int32_t *>(prefix + a.B + 1);  // [B], not kOut
+    int32_t *skip = lens + a.B;                                     // [B], kTails
+    const int32_t *seg_lens = kOut ? a.context_lens : lens;
+    constexpr bool kShared = !kOut;  // (where the lengths are)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = a.B;
     const int cta = blockIdx.x;
 
     // -------- blocks per sequence (all KV heads) and their prefix sum
+    if constexpr (!kOut) griddep_wait();  // (the lengths may be the kernel before's)
+    if constexpr (MODE == Mode::kTails) {
+        const int bad = read_groups(a.tl.groups, a.context_lens, B, skip, lens, tid, kThreads);
+        if (bad && cta == 0 && tid == 0) report(a.status, PA_DEV_BAD_LENGTH);
+        if (cta == 0 && warp == 1) write_plan(a.tl, skip, a.Hk, a.g, B, bad == 2, lane);
+    }
     for (int s = tid; s < B; s += kThreads) {
-        const int ctx = __ldg(a.context_lens + s);
+        [[maybe_unused]] const int ctx = __ldg(a.context_lens + s);
         int64_t n = 0;
-        if (ctx >= 1 && ctx <= a.maxb * kBlockSize)
-            n = (int64_t)((ctx + kBlockSize - 1) / kBlockSize + kCost) * a.Hk;
-        else if (cta == 0)
-            report(a.status, PA_DEV_BAD_LENGTH);
+        if constexpr (kOut) {
+            if (ctx >= 1 && ctx <= a.maxb * kBlockSize)
+                n = (int64_t)((ctx + kBlockSize - 1) / kBlockSize + kCost) * a.Hk;
+            else if (cta == 0)
+                report(a.status, PA_DEV_BAD_LENGTH);
+        } else {
+            if constexpr (MODE == Mode::kScores) {
+                const bool ok = ctx >= 1 && ctx <= a.maxb * kBlockSize && ctx <= a.sc.max_len;
+                if (!ok && cta == 0) report(a.status, PA_DEV_BAD_LENGTH);
+                lens[s] = ok ? ctx : 0;
+            }
+            n = (int64_t)((lens[s] + kBlockSize - 1) / kBlockSize + kCost) * a.Hk;
+        }
         prefix[s + 1] = n;
     }
     if (tid < NSTAGE) stage_bad[tid] = 0;
@@ -406,13 +479,20 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     __syncthreads();
     // Everything above read only call metadata; Q and the cache may still be
     // being written by the RoPE/append kernel before this one.
-    griddep_wait();
+    if constexpr (kOut) griddep_wait();
     // The kernel after this one (the next step's RoPE/append, the step
     // graph's output copy) may be launched now: it waits for this grid to
     // finish before it touches memory, and this grid's CTAs are all resident
     // (one persistent wave), so its launch latency hides under this kernel.
     griddep_launch_dependents();
     const int64_t W = prefix[B];
+    if constexpr (MODE == Mode::kScores) {
+        // where the second kernel finds a sequence's scores
+        if (cta == 0)
+            for (int s = tid; s < B; s += kThreads)
+                a.sc.first[s] = lens[s] == 0 ? -1
+                                             : scores_start<kCost>(a, prefix, lens, s, a.status);
+    }
     // With fewer blocks than CTAs only the first W CTAs get a (one-block)
     // range, so that every range is non-empty and a pair cut into pieces
     // counts exactly one arrival per CTA between its first and last.
@@ -430,8 +510,9 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
         bool abort = false;
         const uint64_t pol = l2_evict_first();
         for (int64_t pos = start; pos < end && !abort;) {
-            const Segment sg = segment_at<kCost, I8>(pos, end, prefix, B, a.context_lens);
+            const Segment sg = segment_at<kCost, I8, kShared>(pos, end, prefix, B, seg_lens);
             const int32_t *row = a.block_tables + (int64_t)sg.s * a.maxb + sg.b0;
+            if constexpr (MODE == Mode::kTails) row += max(skip[sg.s], 0);
             for (int w0 = 0; w0 < sg.nb && !abort; w0 += 32) {
                 const int cnt = min(32, sg.nb - w0);
                 const int my_blk = lane < cnt ? __ldg(row + w0 + lane) : 0;
@@ -492,11 +573,17 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     constexpr int kCons = kConsumerWarps * 32;
     int gblk = 0;
     for (int64_t pos = start; pos < end;) {
-        const Segment sg = segment_at<kCost, I8>(pos, end, prefix, B, a.context_lens);
+        const Segment sg = segment_at<kCost, I8, kShared>(pos, end, prefix, B, seg_lens);
         const int s = sg.s, kvh = sg.kvh, b0 = sg.b0, nb = sg.nb, ctx = sg.ctx;
         if (nb == 0) {  // cost units alone
             pos += sg.nu;
             continue;
+        }
+        [[maybe_unused]] float *scores = nullptr;  // of the pair's first token
+        if constexpr (MODE == Mode::kScores) {
+            const int64_t at = scores_start<kCost>(a, prefix, lens, s, nullptr);
+            if (at >= 0)
+                scores = a.sc.scores + (at + (sg.pair_end - sg.pair_start) * kvh) * kBlockSize * a.g;
         }
 
         // Q^T fragments (B operand).  fp16 cache: Q[head][16kk + 2*quad + {0,1}]
@@ -685,6 +772,12 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                     pl1 = ps[1];
                 }
             } else {
+                if constexpr (MODE == Mode::kScores) {
+                    // a block out of range takes part in nothing
+                    if (bad && scores != nullptr)
+                        for (int i = lane; i < kBlockSize * a.g; i += 32)
+                            scores[(int64_t)(b0 + j) * kBlockSize * a.g + i] = -INFINITY;
+                }
                 if (!bad) {
                     const uint32_t vt = kt + L::kTileBytes;
                     float sc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -699,6 +792,27 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                     float x2 = sc[2] * a.scale_log2, x3 = sc[3] * a.scale_log2;
                     if (tok >= ctx) x0 = x1 = -INFINITY;
                     if (tok + 8 >= ctx) x2 = x3 = -INFINITY;
+                    if constexpr (MODE == Mode::kScores) {
+                        // the block's scores [16 tokens][g heads], padding tokens' too
+                        if (scores != nullptr) {
+                            float *r = scores + (int64_t)tok * a.g + h0;
+                            if ((a.g & 1) == 0) {
+                                if (h0 < a.g) {
+                                    *reinterpret_cast<float2 *>(r) = make_float2(x0, x1);
+                                    *reinterpret_cast<float2 *>(r + 8 * a.g) = make_float2(x2, x3);
+                                }
+                            } else {
+                                if (h0 < a.g) {
+                                    r[0] = x0;
+                                    r[8 * a.g] = x2;
+                                }
+                                if (h0 + 1 < a.g) {
+                                    r[1] = x1;
+                                    r[8 * a.g + 1] = x3;
+                                }
+                            }
+                        }
+                    }
                     float bm0 = fmaxf(x0, x2), bm1 = fmaxf(x1, x3);
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) {
@@ -709,10 +823,22 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                     const float al0 = ex2(m0 - mn0), al1 = ex2(m1 - mn1);
                     m0 = mn0;
                     m1 = mn1;
-                    const __half2 p01 = __floats2half2_rn(ex2(x0 - mn0), ex2(x1 - mn1));
-                    const __half2 p23 = __floats2half2_rn(ex2(x2 - mn0), ex2(x3 - mn1));
-                    l0 = l0 * al0 + __low2float(p01) + __low2float(p23);
-                    l1 = l1 * al1 + __high2float(p01) + __high2float(p23);
+                    __half2 p01, p23;
+                    if constexpr (kOut) {
+                        p01 = __floats2half2_rn(ex2(x0 - mn0), ex2(x1 - mn1));
+                        p23 = __floats2half2_rn(ex2(x2 - mn0), ex2(x3 - mn1));
+                        l0 = l0 * al0 + __low2float(p01) + __low2float(p23);
+                        l1 = l1 * al1 + __high2float(p01) + __high2float(p23);
+                    } else {
+                        // the row sum adds P before its rounding: a weight is
+                        // divided by it, and P's 2^-11 would show there
+                        const float e0 = ex2(x0 - (mn0 - kPShift)), e1 = ex2(x1 - (mn1 - kPShift));
+                        const float e2 = ex2(x2 - (mn0 - kPShift)), e3 = ex2(x3 - (mn1 - kPShift));
+                        p01 = __floats2half2_rn(e0, e1);
+                        p23 = __floats2half2_rn(e2, e3);
+                        l0 = l0 * al0 + (e0 + e2);
+                        l1 = l1 * al1 + (e1 + e3);
+                    }
                     const uint32_t pb0 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&p01));
                     const uint32_t pb1 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&p23));
                     const int vrow = (lane & 7) + (lane >> 4) * 8;
@@ -821,9 +947,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
 #pragma unroll
                 for (int wv = 0; wv < kConsumerWarps; ++wv)
                     O = __fmaf_rn(sm_m[wv * kGroupPad + h], sm_o[(wv * kGroupPad + h) * D + d], O);
-                const float Lsum = sm_l[h];
-                a.out[((int64_t)s * a.H + kvh * a.g + h) * D + d] =
-                    __float2half_rn(Lsum > 0.f ? O / Lsum : 0.f);
+                emit<D, MODE>(a, s, kvh, h, d, O, sm_l[kGroupPad + h], sm_l[h]);
             }
             named_barrier_sync(1, kCons);  // the smem merge area is free again
         } else {
@@ -867,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                             if (last) fence_acq_rel_gpu();
                         }
                         if (__shfl_sync(0xffffffffu, last, 0)) {
-                            warp_merge_records<D, I8>(a, sg, W, G, lane);
+                            warp_merge_records<D, I8, MODE>(a, sg, W, G, lane);
                             if (lane == 0) a.counters[s * a.Hk + kvh] = 0;
                         }
                     }
@@ -952,9 +1076,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                                     if (i < nrec)
                                         O = __fmaf_rn(sm_pm[i * kGroupPad + h],
                                                       i == own ? Oown : x[i][k], O);
-                                const float Lsum = sm_pl[h];
-                                a.out[((int64_t)s * a.H + kvh * a.g + h) * D + d] =
-                                    __float2half_rn(Lsum > 0.f ? O / Lsum : 0.f);
+                                emit<D, MODE>(a, s, kvh, h, d, O, sm_pl[kGroupPad + h], sm_pl[h]);
                             }
                         }
                     }
@@ -1024,9 +1146,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                                                   i == own ? oown[k]
                                                            : sm_o[(i * kGroupPad + h) * D + d],
                                                   O);
-                            const float Lsum = sm_pl[h];
-                            a.out[((int64_t)s * a.H + kvh * a.g + h) * D + d] =
-                                __float2half_rn(Lsum > 0.f ? O / Lsum : 0.f);
+                            emit<D, MODE>(a, s, kvh, h, d, O, sm_pl[kGroupPad + h], sm_pl[h]);
                         }
                     }
                 }
@@ -1049,8 +1169,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                         Lsum = __fmaf_rn(f, __ldcg(r + D + 1), Lsum);
                         O = __fmaf_rn(f, __ldcg(r + d), O);
                     }
-                    a.out[((int64_t)s * a.H + kvh * a.g + h) * D + d] =
-                        __float2half_rn(Lsum > 0.f ? O / Lsum : 0.f);
+                    emit<D, MODE>(a, s, kvh, h, d, O, M, Lsum);
                 }
                 if (tid == 0) a.counters[s * a.Hk + kvh] = 0;
             }
@@ -1060,21 +1179,22 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     }
 }
 
-template <int D, int NSTAGE, bool I8>
+template <int D, int NSTAGE, bool I8, Mode MODE = Mode::kOut>
 size_t decode_smem_bytes(int B) {
     return 1024 + (size_t)NSTAGE * Layout<D, I8>::kStageBytes +
            (size_t)NSTAGE * Layout<D, I8>::kScaleBytes + Layout<D, I8>::kQsmBytes +
            2 * NSTAGE * sizeof(uint64_t) +
            NSTAGE * sizeof(int) + (size_t)kConsumerWarps * kGroupPad * (D + 4) * sizeof(float) +
-           4 * sizeof(int) + 8 + (size_t)(B + 1) * sizeof(int64_t);
+           4 * sizeof(int) + 8 + (size_t)(B + 1) * sizeof(int64_t) +
+           (MODE == Mode::kOut ? 0 : MODE == Mode::kScores ? 1 : 2) * (size_t)B * sizeof(int32_t);
 }
 
 constexpr int kStages = 8;
 
-template <int D, int NSTAGE, bool I8>
+template <int D, int NSTAGE, bool I8, Mode MODE = Mode::kOut>
 int launch_decode_stages(const CUtensorMap &map, const CUtensorMap &smap, const DecodeArgs &a,
                          int max_grid, cudaStream_t st) {
-    const size_t smem = decode_smem_bytes<D, NSTAGE, I8>(a.B);
+    const size_t smem = decode_smem_bytes<D, NSTAGE, I8, MODE>(a.B);
     // The kernel may use up to the shared memory of kMaxSeqs sequences; the
     // limit is raised once per device.  The grid is sized from this call's
     // shared memory, so small batches get more CTAs (bytes in flight) per SM.
@@ -1085,9 +1205,9 @@ int launch_decode_stages(const CUtensorMap &map, const CUtensorMap &smap, const 
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!attr_set[dev]) {
-            if (cudaFuncSetAttribute(decode_kernel<D, NSTAGE, I8>,
+            if (cudaFuncSetAttribute(decode_kernel<D, NSTAGE, I8, MODE>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)decode_smem_bytes<D, NSTAGE, I8>(kMaxSeqs)) !=
+                                     (int)decode_smem_bytes<D, NSTAGE, I8, MODE>(kMaxSeqs)) !=
                 cudaSuccess) {
                 cudaGetLastError();
                 return PA_ERR_CUDA;
@@ -1096,7 +1216,7 @@ int launch_decode_stages(const CUtensorMap &map, const CUtensorMap &smap, const 
         }
     }
     int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_kernel<D, NSTAGE, I8>,
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_kernel<D, NSTAGE, I8, MODE>,
                                                       kThreads, smem) != cudaSuccess ||
         per_sm < 1) {
         cudaGetLastError();
@@ -1104,7 +1224,7 @@ int launch_decode_stages(const CUtensorMap &map, const CUtensorMap &smap, const 
     }
     const int grid = min(sm_count() * per_sm, max_grid);
     if (grid < 1) return PA_ERR_CUDA;
-    launch_dependent(decode_kernel<D, NSTAGE, I8>, dim3(grid), dim3(kThreads), smem, st, map, smap,
+    launch_dependent(decode_kernel<D, NSTAGE, I8, MODE>, dim3(grid), dim3(kThreads), smem, st, map, smap,
                      a);
     return launch_status();
 }
@@ -1116,6 +1236,15 @@ int launch_decode(const CUtensorMap &map, const DecodeArgs &a, int max_grid, cud
     // allows two) keep 128 KB of K/V in flight per SM; 4 stages, or 12-16
     // stages at one CTA per SM, measured slower on all decode workloads.
     return launch_decode_stages<D, kStages, false>(map, map, a, max_grid, st);
+}
+
+// (the modes other than kOut, fp16 cache)
+template <Mode MODE>
+int launch_decode_mode(const CUtensorMap &map, const DecodeArgs &a, int head_dim, int max_grid,
+                       cudaStream_t st) {
+    return head_dim == 128
+               ? launch_decode_stages<128, kStages, false, MODE>(map, map, a, max_grid, st)
+               : launch_decode_stages<64, kStages, false, MODE>(map, map, a, max_grid, st);
 }
 
 // int8 cache: a stage holds half the bytes; 8 stages at four CTAs per SM.
@@ -1138,7 +1267,6 @@ extern "C" size_t pa_decode_workspace_bytes(int num_seqs, int n_heads, int n_kv_
 }
 
 namespace pa {
-namespace {
 
 // The argument checks of pa_decode that do not involve the workspace, in
 // the order pa_decode makes them.  PA_OK with num_seqs == 0 means "nothing
@@ -1159,7 +1287,51 @@ int check_decode_args(const void *q, const pa_cache_t *cache, int layer,
     return PA_OK;
 }
 
+namespace {
+
+// A mode's launch: pa_decode's kernel arguments.
+template <Mode MODE>
+int launch_mode(const DecodeCall &c, void *workspace, const DecodeScores &sc,
+                const DecodeTails &tl) {
+    CUtensorMap map;
+    if (!make_cache_pair_map(&map, c.cache, c.layer)) return PA_ERR_CUDA;
+    const float scale = c.scale == 0.f ? 1.0f / sqrtf((float)c.head_dim) : c.scale;
+    DecodeArgs a = {};
+    a.q = static_cast<const __half *>(c.q);
+    a.block_tables = c.block_tables;
+    a.context_lens = c.context_lens;
+    a.out = static_cast<__half *>(c.out);
+    a.counters = static_cast<int32_t *>(workspace);
+    a.rec = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
+                                      (size_t)kModePairs * sizeof(int32_t));
+    a.status = c.dev_status;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.B = c.num_seqs;
+    a.H = c.n_heads;
+    a.Hk = c.n_kv_heads;
+    a.g = c.n_heads / c.n_kv_heads;
+    a.maxb = c.max_blocks_per_seq;
+    a.num_blocks = c.cache->num_blocks;
+    a.sc = sc;
+    a.tl = tl;
+    return launch_decode_mode<MODE>(map, a, c.head_dim, kMaxGrid, c.stream);
+}
+
 }  // namespace
+
+size_t mode_workspace_bytes(int head_dim) {
+    const size_t rec = cta_record_bytes(head_dim > 128 ? head_dim : 128);
+    return (size_t)kModePairs * sizeof(int32_t) + (size_t)kMaxGrid * rec;
+}
+
+int launch_decode_scores(const DecodeCall &c, void *workspace, const DecodeScores &sc) {
+    return launch_mode<Mode::kScores>(c, workspace, sc, DecodeTails{});
+}
+
+int launch_decode_tails(const DecodeCall &c, void *workspace, const DecodeTails &tl) {
+    return launch_mode<Mode::kTails>(c, workspace, DecodeScores{}, tl);
+}
+
 }  // namespace pa
 
 extern "C" int pa_decode(const void *q, const pa_cache_t *cache, int layer,
@@ -1182,7 +1354,7 @@ extern "C" int pa_decode(const void *q, const pa_cache_t *cache, int layer,
     if (!make_cache_pair_map(&map, cache, layer)) return PA_ERR_CUDA;
     if (scale == 0.f) scale = 1.0f / sqrtf((float)head_dim);
 
-    DecodeArgs a;
+    DecodeArgs a = {};
     a.q = static_cast<const __half *>(q);
     a.block_tables = block_tables;
     a.context_lens = context_lens;
@@ -1278,7 +1450,7 @@ extern "C" int pa_decode_i8(const void *q, const pa_cache_i8_t *cache, int layer
         return PA_ERR_CUDA;
     if (scale == 0.f) scale = 1.0f / sqrtf((float)head_dim);
 
-    DecodeArgs a;
+    DecodeArgs a = {};
     a.q = static_cast<const __half *>(q);
     a.block_tables = block_tables;
     a.context_lens = context_lens;

@@ -1,0 +1,134 @@
+// Decode that accumulates attention weights (pa_decode_weights).
+//
+// With x[h][t] the scaled score of Q head h and token t in log2 units,
+//     out[h]  = sum_t p[h][t] v[t],   p[h][t] = 2^(x[h][t] - m_h) / l_h,
+//     weights_out[kv head][t] = weights[kv head][t] + sum over its Q heads of p[h][t].
+// A token's p is known only once its row's last token has been seen, so the
+// decode kernel leaves the scores (fp32, 4 g bytes a (token, KV head), against
+// 4 d for its K and V row) and each row's m and 1/l behind; this kernel turns
+// them into weights.  Reading K a second time instead would cost 2 d bytes.
+//
+// Bound: L2 and HBM, 4 g + 8 bytes a (token, KV head).
+#include <algorithm>
+
+#include "decode_modes.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kWeightThreads = 256;
+
+struct WeightArgs {
+    DecodeScores sc;
+    const int32_t *context_lens;
+    const float *weights;  // nullptr: zeros
+    float *weights_out;
+    int64_t stride;
+    int H, Hk;
+};
+
+// grid (chunks of tokens, Hk, B); one thread a token at a time.
+template <int G>
+__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int h = blockIdx.y, s = blockIdx.z;
+    const int64_t first = a.sc.first[s];
+    if (first < 0) return;
+    const int n = a.context_lens[s];
+    float2 st[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) st[j] = a.sc.stats[(int64_t)s * a.H + h * G + j];
+    const float *x =
+        a.sc.scores + (first + (int64_t)((n + kBlockSize - 1) / kBlockSize) * h) * kBlockSize * G;
+    const int64_t row = ((int64_t)s * a.Hk + h) * a.stride;
+    for (int64_t t = blockIdx.x * kWeightThreads + threadIdx.x; t < n;
+         t += (int64_t)gridDim.x * kWeightThreads) {
+        float w = 0.f;
+#pragma unroll
+        for (int j = 0; j < G; ++j) w += ex2(__ldcs(x + t * G + j) - st[j].x) * st[j].y;
+        a.weights_out[row + t] = a.weights ? a.weights[row + t] + w : w;
+    }
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Workspace: the decode kernel's, the statistics, each sequence's first block, scores.
+size_t fixed_bytes(int B, int H, int D) {
+    return up256(mode_workspace_bytes(D)) + up256((size_t)B * H * sizeof(float2)) +
+           up256((size_t)B * sizeof(int64_t));
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" size_t pa_decode_weights_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads,
+                                                    int head_dim, int64_t score_blocks) {
+    if (num_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || score_blocks <= 0)
+        return 0;
+    const unsigned __int128 n = (unsigned __int128)score_blocks * kBlockSize * n_heads * 4 +
+                                fixed_bytes(num_seqs, n_heads, head_dim);
+    return n > SIZE_MAX ? 0 : (size_t)n;
+}
+
+extern "C" int pa_decode_weights(const void *q, const pa_cache_t *cache, int layer,
+                                 const int32_t *block_tables, int max_blocks_per_seq,
+                                 const int32_t *context_lens, int num_seqs, int n_heads,
+                                 int n_kv_heads, int head_dim, float scale, const float *weights,
+                                 float *weights_out, int64_t weights_stride, void *workspace,
+                                 size_t workspace_bytes, void *out, int32_t *dev_status,
+                                 pa_stream_t stream) {
+    const int rc = check_decode_args(q, cache, layer, block_tables, max_blocks_per_seq,
+                                     context_lens, num_seqs, n_heads, n_kv_heads, head_dim, scale,
+                                     out);
+    if (rc != PA_OK) return rc;
+    if (weights_stride <= 0) return PA_ERR_INVALID;
+    if (n_kv_heads > 65535 || (int64_t)num_seqs * n_kv_heads > kModePairs)
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!weights_out || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return PA_ERR_INVALID;
+    const unsigned __int128 rows = (unsigned __int128)num_seqs * n_kv_heads * weights_stride * 4;
+    if (rows > SIZE_MAX || (weights && weights_out != weights &&
+                            ranges_overlap(weights, (uint64_t)rows, weights_out, (uint64_t)rows)))
+        return PA_ERR_INVALID;
+    const size_t fixed = fixed_bytes(num_seqs, n_heads, head_dim);
+    const size_t block = (size_t)kBlockSize * n_heads * sizeof(float);  // of all KV heads
+    if (workspace_bytes < fixed + block) return PA_ERR_WORKSPACE;
+
+    uint8_t *at = static_cast<uint8_t *>(workspace);
+    const size_t dec = mode_workspace_bytes(head_dim);
+    WeightArgs w;
+    w.sc.stats = reinterpret_cast<float2 *>(at + up256(dec));
+    w.sc.first = reinterpret_cast<int64_t *>(at + up256(dec) +
+                                             up256((size_t)num_seqs * n_heads * sizeof(float2)));
+    w.sc.scores = reinterpret_cast<float *>(at + fixed);
+    w.sc.capacity = (int64_t)((workspace_bytes - fixed) / block) * n_kv_heads;
+    w.sc.max_len = (int)std::min<int64_t>(weights_stride, INT32_MAX);
+    w.context_lens = context_lens;
+    w.weights = weights;
+    w.weights_out = weights_out;
+    w.stride = weights_stride;
+    w.H = n_heads;
+    w.Hk = n_kv_heads;
+    const DecodeCall c = {q,        cache,   layer,      block_tables, max_blocks_per_seq,
+                          context_lens, num_seqs, n_heads, n_kv_heads, head_dim,
+                          scale,    out,     dev_status, static_cast<cudaStream_t>(stream)};
+    const int rc2 = launch_decode_scores(c, at, w.sc);
+    if (rc2 != PA_OK) return rc2;
+    // CTAs for the longest row the table allows, as long as they are few
+    const int64_t pairs = (int64_t)num_seqs * n_kv_heads;
+    const int64_t longest = (int64_t)max_blocks_per_seq * kBlockSize;
+    const int64_t chunks = std::min((longest + kWeightThreads - 1) / kWeightThreads,
+                                    std::max<int64_t>(1, (16 * (int64_t)sm_count() + pairs - 1) / pairs));
+    const dim3 grid((unsigned)chunks, n_kv_heads, num_seqs), block_dim(kWeightThreads);
+    switch (n_heads / n_kv_heads) {
+#define PA_CASE(G) \
+    case G: launch_dependent(weights_kernel<G>, grid, block_dim, 0, c.stream, w); break;
+        PA_CASE(1) PA_CASE(2) PA_CASE(3) PA_CASE(4) PA_CASE(5) PA_CASE(6) PA_CASE(7) PA_CASE(8)
+#undef PA_CASE
+    }
+    return launch_status();
+}

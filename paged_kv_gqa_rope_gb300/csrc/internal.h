@@ -19,6 +19,12 @@ constexpr int kBlockSize = 16;
 // max_blocks_per_seq * kBlockSize must fit in int32.
 constexpr int kMaxBlocksPerSeq = INT32_MAX / kBlockSize;
 
+// Do the na bytes from a and the nb bytes from b overlap?
+inline bool ranges_overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y ? y - x < na : x - y < nb;
+}
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline bool cache_ok(const pa_cache_t *c, int layer, int n_kv_heads, int head_dim) {

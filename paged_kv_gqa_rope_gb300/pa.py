@@ -35,6 +35,10 @@ EXPORTS = (
     "pa_cache_i4_bytes", "pa_alloc_cache_i4", "pa_free_cache_i4", "pa_rope_kv_write_i4",
     "pa_kv_read_i4", "pa_decode_i4_workspace_bytes", "pa_decode_i4",
     "pa_prefill_i4_workspace_bytes", "pa_prefill_varlen_i4",
+    "pa_rope_kv_write_layout", "pa_rope_table_init_scaled", "pa_prepare_shared",
+    "pa_decode_shared_workspace_bytes", "pa_decode_shared",
+    "pa_decode_weights_workspace_bytes", "pa_decode_weights",
+    "pa_kv_evict_workspace_bytes", "pa_kv_evict",
 )
 
 
@@ -58,6 +62,12 @@ class PaCacheI4(ctypes.Structure):
                 ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("owns", ctypes.c_int32)]
+
+
+class PaRopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("original_positions", ctypes.c_int32),
+                ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("attention", ctypes.c_double)]
 
 
 class PAError(RuntimeError):
@@ -135,6 +145,21 @@ _SIGS = {
     "pa_prefill_varlen_i4": (_i32, [_vp, _i32, ctypes.POINTER(PaCacheI4), _i32, _vp, _vp, _vp,
                                     _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _sz,
                                     _vp, _vp, _vp]),
+    "pa_rope_kv_write_layout": (_i32, [_vp] * 6 + [_i32] * 6 + [_vp, _i32, ctypes.POINTER(PaCache),
+                                                                _i32, _vp, _vp]),
+    "pa_rope_table_init_scaled": (_i32, [_vp, _i32, _i32, ctypes.c_double,
+                                         ctypes.POINTER(PaRopeScaling), _vp]),
+    "pa_prepare_shared": (_i32, [_i32, _vp, _i32, _vp, _i32, _vp, _vp, ctypes.POINTER(_i32)]),
+    "pa_decode_shared_workspace_bytes": (_sz, [_i32] * 4),
+    "pa_decode_shared": (_i32, [_vp, ctypes.POINTER(PaCache), _i32, _vp, _i32, _vp, _i32, _vp, _vp,
+                                _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _sz, _vp, _vp, _vp]),
+    "pa_decode_weights_workspace_bytes": (_sz, [_i32] * 4 + [_i64]),
+    "pa_decode_weights": (_i32, [_vp, ctypes.POINTER(PaCache), _i32, _vp, _i32, _vp, _i32, _i32,
+                                 _i32, _i32, ctypes.c_float, _vp, _vp, _i64, _vp, _sz, _vp, _vp,
+                                 _vp]),
+    "pa_kv_evict_workspace_bytes": (_sz, [_i32] * 3),
+    "pa_kv_evict": (_i32, [ctypes.POINTER(PaCache), _i32, _vp, _i32, _vp, _i32, _i32, _i32, _vp,
+                           _vp, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _sz, _vp, _vp]),
     "pa_strerror": (ctypes.c_char_p, [_i32]),
     "pa_check_device": (_i32, []),
 }
@@ -268,17 +293,21 @@ def prepare_decode(num_cached, block_tables, block_size=16):
 class Cache:
     """The block pool [2, layers, num_blocks, block_size, n_kv_heads, head_dim]
     fp16.  By default the memory is a torch tensor (``self.tensor``) that the
-    library wraps; ``library_owned=True`` lets pa_alloc_cache allocate it."""
+    library wraps; `tensor` takes a caller's own, a contiguous CUDA fp16 tensor
+    of that shape; ``library_owned=True`` lets pa_alloc_cache allocate it."""
 
     def __init__(self, layers, num_blocks, n_kv_heads, head_dim, block_size=16, device="cuda",
-                 library_owned=False):
+                 library_owned=False, tensor=None):
         self.desc = PaCache()
         self.tensor = None
+        shape = (2, layers, num_blocks, block_size, n_kv_heads, head_dim)
         if library_owned:
+            if tensor is not None:
+                raise ValueError("a library-owned pool takes no tensor")
             base = None
         else:
-            self.tensor = torch.empty((2, layers, num_blocks, block_size, n_kv_heads, head_dim),
-                                      dtype=torch.float16, device=device)
+            self.tensor = (torch.empty(shape, dtype=torch.float16, device=device)
+                           if tensor is None else _dev(tensor, torch.float16, "tensor", shape))
             base = _p(self.tensor)
         _check("pa_alloc_cache", lib().pa_alloc_cache(
             ctypes.byref(self.desc), layers, num_blocks, block_size, n_kv_heads, head_dim, base))
@@ -821,3 +850,210 @@ def prefill_varlen_i4(q, cache: CacheI4, cu_seqlens_q, cu_seqlens_k, block_table
              _on(dev, workspace, torch.uint8, "workspace", nbytes), nbytes,
              _on(dev, out, torch.float16, "out", T, H, d), _status_i4(dev, status))
     return out
+
+
+# ------------------------------------------------------------------ long contexts
+
+def _cache_f16(dev, cache):
+    """The descriptor of an fp16 pool on device number `dev` (a library-owned pool
+    names no device: it is taken to be on the call's)."""
+    if not isinstance(cache, Cache):
+        raise TypeError(f"cache must be a Cache, not {type(cache).__name__}")
+    if cache.tensor is not None and cache.tensor.get_device() != dev:
+        raise ValueError(f"the cache is on {cache.tensor.device}, the call's device is cuda:{dev}")
+    return ctypes.byref(cache.desc)
+
+
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+
+def rope_kv_write_layout(q, k, v, positions, slot_mapping, table, cache: Cache, layout, layer=0,
+                         q_out=None, status=None, stream=None):
+    """pa_rope_kv_write_layout: turns the first 2 * table.shape[1] values of every Q
+    row (in place, or into `q_out`) and of K, `layout` "interleaved" or "half", and
+    appends K and V (both left as they are).  Returns the rotated Q."""
+    try:
+        (T, H, d), (_, Hk, _), (rows, pairs, _) = q.shape, k.shape, table.shape
+        dev = q.get_device()
+        if dev < 0:  # a host tensor
+            raise ValueError
+    except (AttributeError, ValueError):
+        _refuse_rank((q, 3, "q"), (k, 3, "k"), (table, 3, "table"))
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout {layout!r} is none of {', '.join(ROPE_LAYOUTS)}")
+    if q_out is None:
+        q_out = q
+    _call_on(dev, "pa_rope_kv_write_layout", stream, _on(dev, q, torch.float16, "q", T, H, d),
+             _on(dev, q_out, torch.float16, "q_out", T, H, d),
+             _on(dev, k, torch.float16, "k", T, Hk, d), _on(dev, v, torch.float16, "v", T, Hk, d),
+             _on(dev, positions, torch.int32, "positions", T),
+             _on(dev, slot_mapping, torch.int32, "slot_mapping", T), T, H, Hk, d,
+             ROPE_LAYOUTS[layout], 2 * pairs,
+             _on(dev, table, torch.float32, "table", rows, pairs, 2), rows,
+             _cache_f16(dev, cache), _layer_i4(layer), _status_i4(dev, status))
+    return q_out
+
+
+def rope_table_scaled(max_positions, rotary_dim, theta=10000.0, scaling=None, factor=1.0,
+                      original_positions=0, low=1.0, high=None, attention=0.0, device="cuda",
+                      stream=None):
+    """pa_rope_table_init_scaled: a table [max_positions, rotary_dim / 2, 2] for
+    rope_kv_write_layout.  `scaling`: None, "linear", "ntk", "yarn" or "bands" (`low` and
+    `high` turns over `original_positions`; high is 32 for "yarn" and 4 for "bands"
+    unless given)."""
+    if scaling is not None and scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling {scaling!r} is none of {', '.join(ROPE_SCALINGS)}")
+    if lib().pa_rope_table_bytes(max_positions, rotary_dim) == 0:
+        raise ValueError("bad RoPE table shape")
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
+    t = torch.empty((max_positions, rotary_dim // 2, 2), dtype=torch.float32, device=device)
+    if not t.is_cuda:
+        raise ValueError(f"a RoPE table cannot be on {t.device}")
+    sc = PaRopeScaling(ROPE_SCALINGS.get(scaling, 0), original_positions, factor, low, high,
+                       attention)
+    _call_on(t.get_device(), "pa_rope_table_init_scaled", stream, t.data_ptr(), max_positions,
+             rotary_dim, float(theta), ctypes.byref(sc))
+    return t
+
+
+def prepare_shared(block_tables, context_lens, block_size=16):
+    """pa_prepare_shared: the groups of neighbouring sequences whose block tables begin
+    alike, as group_starts [groups + 1] and shared_blocks [groups] (numpy)."""
+    bt = np.ascontiguousarray(block_tables, np.int32)
+    ctx = np.ascontiguousarray(context_lens, np.int32)
+    if bt.ndim != 2 or ctx.shape != bt.shape[:1]:
+        raise ValueError(f"block_tables {bt.shape} and context_lens {ctx.shape} do not match")
+    B = len(ctx)
+    starts, blocks, n = np.zeros(B + 1, np.int32), np.zeros(max(B, 1), np.int32), _i32()
+    _check("pa_prepare_shared", lib().pa_prepare_shared(
+        B, _p(bt), bt.shape[1], _p(ctx), block_size, _p(starts), _p(blocks), ctypes.byref(n)))
+    return dict(group_starts=starts[:n.value + 1].copy(), shared_blocks=blocks[:n.value].copy())
+
+
+def decode_shared_workspace(num_seqs, n_heads, n_kv_heads, head_dim, device="cuda"):
+    """A zeroed workspace for pa_decode_shared (its counters must start at zero)."""
+    n = lib().pa_decode_shared_workspace_bytes(num_seqs, n_heads, n_kv_heads, head_dim)
+    if n == 0:
+        raise ValueError("bad shared decode workspace shape")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def decode_shared(q, cache: Cache, block_tables, context_lens, group_starts, shared_blocks,
+                  workspace, n_kv_heads, layer=0, scale=0.0, out=None, status=None, stream=None):
+    """pa_decode_shared: decode of sequences group_starts[r] .. group_starts[r + 1] - 1
+    that share their first shared_blocks[r] blocks, read once for the group."""
+    try:
+        (B, H, d), (_, width), (nbytes,) = q.shape, block_tables.shape, workspace.shape
+        (groups,) = shared_blocks.shape
+        dev = q.get_device()
+        if dev < 0:  # a host tensor
+            raise ValueError
+    except (AttributeError, ValueError):
+        _refuse_rank((q, 3, "q"), (block_tables, 2, "block_tables"), (workspace, 1, "workspace"),
+                     (shared_blocks, 1, "shared_blocks"))
+    if out is None:
+        out = _new_out(q, stream)
+    _call_on(dev, "pa_decode_shared", stream, _on(dev, q, torch.float16, "q", B, H, d),
+             _cache_f16(dev, cache), _layer_i4(layer),
+             _on(dev, block_tables, torch.int32, "block_tables", B, width),
+             _table_width(block_tables), _on(dev, context_lens, torch.int32, "context_lens", B), B,
+             _on(dev, group_starts, torch.int32, "group_starts", groups + 1),
+             _on(dev, shared_blocks, torch.int32, "shared_blocks", groups), groups,
+             H, n_kv_heads, d, scale, _on(dev, workspace, torch.uint8, "workspace", nbytes), nbytes,
+             _on(dev, out, torch.float16, "out", B, H, d), _status_i4(dev, status))
+    return out
+
+
+def decode_weights_workspace(num_seqs, n_heads, n_kv_heads, head_dim, score_blocks,
+                             device="cuda"):
+    """A zeroed workspace for pa_decode_weights batches whose contexts take at most
+    `score_blocks` blocks of 16 tokens together."""
+    n = lib().pa_decode_weights_workspace_bytes(num_seqs, n_heads, n_kv_heads, head_dim,
+                                                score_blocks)
+    if n == 0:
+        raise ValueError("bad weights workspace shape")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def decode_weights(q, cache: Cache, block_tables, context_lens, weights, workspace, n_kv_heads,
+                   weights_out=None, layer=0, scale=0.0, out=None, status=None, stream=None):
+    """pa_decode_weights: decode, and weights_out[s, kv head, t] = weights + the attention
+    weight of token t in the KV head's Q heads.  `weights` fp32 [B, n_kv_heads, stride]
+    is updated in place unless `weights_out` is given; None stands for zeros (weights_out
+    is then needed).  Returns (out, weights_out)."""
+    if weights_out is None:
+        weights_out = weights
+    try:
+        (B, H, d), (_, width), (nbytes,) = q.shape, block_tables.shape, workspace.shape
+        _, _, stride = weights_out.shape
+        dev = q.get_device()
+        if dev < 0:  # a host tensor
+            raise ValueError
+    except (AttributeError, ValueError):
+        _refuse_rank((q, 3, "q"), (block_tables, 2, "block_tables"), (workspace, 1, "workspace"),
+                     (weights_out, 3, "weights_out"))
+    if out is None:
+        out = _new_out(q, stream)
+    _call_on(dev, "pa_decode_weights", stream, _on(dev, q, torch.float16, "q", B, H, d),
+             _cache_f16(dev, cache), _layer_i4(layer),
+             _on(dev, block_tables, torch.int32, "block_tables", B, width),
+             _table_width(block_tables), _on(dev, context_lens, torch.int32, "context_lens", B), B,
+             H, n_kv_heads, d, scale,
+             None if weights is None else
+             _on(dev, weights, torch.float32, "weights", B, n_kv_heads, stride),
+             _on(dev, weights_out, torch.float32, "weights_out", B, n_kv_heads, stride), stride,
+             _on(dev, workspace, torch.uint8, "workspace", nbytes), nbytes,
+             _on(dev, out, torch.float16, "out", B, H, d), _status_i4(dev, status))
+    return out, weights_out
+
+
+def kv_evict_workspace(num_seqs, n_kv_heads, budget, device="cuda"):
+    """A workspace for pa_kv_evict."""
+    n = lib().pa_kv_evict_workspace_bytes(num_seqs, n_kv_heads, budget)
+    if n == 0:
+        raise ValueError("bad eviction workspace shape")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def kv_evict(cache: Cache, block_tables, context_lens, weights, budget, workspace, sinks=0,
+             recent=0, out_block_tables=None, out_context_lens=None, weights_out=None, layer=0,
+             status=None, stream=None):
+    """pa_kv_evict: every KV head keeps `budget` of a sequence's tokens, the first `sinks`,
+    the last `recent` and those of the largest weights, K and V rows and weights [B,
+    n_kv_heads, stride] moved to the first places.  Tables, lengths and weights are
+    worked on in place unless their `out` is given.  Returns (weights_out,
+    out_context_lens)."""
+    if out_block_tables is None:
+        out_block_tables = block_tables
+    if out_context_lens is None:
+        out_context_lens = context_lens
+    if weights_out is None:
+        weights_out = weights
+    try:
+        (B, width), (_, out_width), (nbytes,) = (block_tables.shape, out_block_tables.shape,
+                                                 workspace.shape)
+        _, Hk, stride = weights.shape
+        dev = weights.get_device()
+        if dev < 0:  # a host tensor
+            raise ValueError
+    except (AttributeError, ValueError):
+        _refuse_rank((block_tables, 2, "block_tables"), (out_block_tables, 2, "out_block_tables"),
+                     (workspace, 1, "workspace"), (weights, 3, "weights"))
+    desc = _cache_f16(dev, cache)
+    for name, x in (("budget", budget), ("sinks", sinks), ("recent", recent)):
+        if not -2**31 <= x < 2**31:
+            raise ValueError(f"{name} {x} does not fit int32")
+    _call_on(dev, "pa_kv_evict", stream, desc, _layer_i4(layer),
+             _on(dev, block_tables, torch.int32, "block_tables", B, width),
+             _table_width(block_tables), _on(dev, context_lens, torch.int32, "context_lens", B), B,
+             Hk, cache.desc.head_dim, _on(dev, weights, torch.float32, "weights", B, Hk, stride),
+             _on(dev, weights_out, torch.float32, "weights_out", B, Hk, stride), stride, budget,
+             sinks, recent,
+             _on(dev, out_block_tables, torch.int32, "out_block_tables", B, out_width),
+             _table_width(out_block_tables),
+             _on(dev, out_context_lens, torch.int32, "out_context_lens", B),
+             _on(dev, workspace, torch.uint8, "workspace", nbytes), nbytes,
+             _status_i4(dev, status))
+    return weights_out, out_context_lens
