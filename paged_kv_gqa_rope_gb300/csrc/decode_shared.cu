@@ -1,15 +1,15 @@
 // Decode of sequences that share a prefix (pa_decode_shared).
 #include <algorithm>
+#include <mutex>
 
 #include "decode_modes.cuh"
+#include "tcgen05.cuh"
 
 namespace pa {
 namespace {
 
 struct SharedArgs {
     const __half *q;
-    const __half *kplane;
-    const __half *vplane;
     const int32_t *block_tables;
     const int32_t *context_lens;
     __half *out;
@@ -18,78 +18,507 @@ struct SharedArgs {
     float *more;   // [G][256][D + 4]: of the piece with which a CTA's range begins inside a unit
     int32_t *status;
     float scale_log2;
-    int B, H, Hk, g, maxb, num_blocks, G;
+    int B, H, Hk, g, maxb, num_blocks, plane_k, plane_v, G;
 };
 
-constexpr int kPrefixThreads = 1024;
+// ------------------------------------------------------------------ prefixes
 
-// One piece after another of the CTA's range: four threads a query row.
+// Roles: warps 0-3 and 4-7 the softmax of stream 0 and 1 (thread = query row =
+// TMEM lane), warp 8 the TMA producer, warps 9 and 10 the MMA issuers (one thread
+// each; warp 9 owns the TMEM).
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kPrefixThreads = 11 * 32;
+constexpr int kTmemCols = 512;
+constexpr float kRescale = 8.f;   // the maximum moves only when a tile raises it by more
+constexpr float kShift = 7.f;     // P = 2^(x - m + 7) <= 2^15
+constexpr int kValidRing = 16;    // tiles whose mask of blocks is kept
+
 template <int D>
-__global__ void __launch_bounds__(kPrefixThreads) prefix_kernel(const SharedArgs a) {
-    griddep_launch_dependents();
+struct PrefixLayout {
+    static constexpr int kHalf = kPrefixTile * 128;    // 64 columns of a tile
+    static constexpr int kTileBytes = kHalf * (D / 64);
+    static constexpr int kStages = D == 128 ? 5 : 10;  // K and V tiles in turn
+    static constexpr int kRing = 2 * kTileBytes;       // behind two Q tiles
+    static constexpr int kBytes = kRing + kStages * kTileBytes;
+    // barriers and small arrays, at most 1008 bytes to the 1024-byte boundary of
+    // the tiles (the window starts 16-byte aligned)
+    static constexpr int kMisc = 512 + kValidRing * 4 + 2 * kPrefixTile * 4;
+    static constexpr size_t smem() { return kMisc + 1008 + kBytes; }
+};
+
+enum {
+    B_QFULL = 0,
+    B_QEMPTY = 1,  // both issuers: the segment's last scores done
+    B_SFULL = 2,   // per stream: a score tile written
+    B_PREADY = 4,  // per stream: its P written
+    B_OUNIT = 6,   // per stream: the segment's last P.V done
+    B_OFREE = 8,   // per stream: O read out
+    B_STATS = 10,  // stream 1's row statistics written
+    B_DRAIN = 11,  // per stream
+    B_FULL = 13,   // ring stages
+    B_EMPTY = 23,
+    B_COUNT = 33
+};
+static_assert(B_COUNT * 8 + 4 <= 512, "barrier area");
+
+__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
+// 16 consecutive 32-bit columns of this thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// The part of the CTA's range that lies in one unit.
+struct PrefixSegment {
+    PlanGroup p;
+    int kvh, member0, tiles, t0;  // first member of the unit; key tiles, first of them
+    bool pair;                    // two tiles of query rows: a stream each, else the
+                                  // streams take the key tiles in turn
+    __device__ __forceinline__ bool mine(int j, int t) const { return pair || (j & 1) == t; }
+    __device__ __forceinline__ int count(int t) const {
+        return pair ? tiles : (tiles + 1 - t) >> 1;
+    }
+};
+
+// Walks a CTA's range; every role has its own.
+struct PrefixWalk {
+    int64_t pos, end;
+    int group;
+    PrefixSegment seg;
+    __device__ __forceinline__ bool next(const SharedArgs &a) {
+        if (pos >= end) return false;
+        seg.p = a.tl.plan[group];
+        while (pos >= seg.p.start + (int64_t)seg.p.tiles * seg.p.units * a.Hk)
+            seg.p = a.tl.plan[++group];
+        const int64_t off = pos - seg.p.start;
+        const int unit = (int)(off / seg.p.tiles);
+        const int mpt = kPrefixTile / a.g;
+        seg.t0 = (int)(off - (int64_t)unit * seg.p.tiles);
+        seg.tiles = (int)min((int64_t)(seg.p.tiles - seg.t0), end - pos);
+        seg.kvh = unit / seg.p.units;
+        seg.member0 = (unit - seg.kvh * seg.p.units) * 2 * mpt;
+        seg.pair = seg.p.members - seg.member0 > mpt;
+        pos += seg.tiles;
+        return true;
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPrefixThreads, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap qmap,
+                  const __grid_constant__ CUtensorMap kvmap, const SharedArgs a) {
+    using L = PrefixLayout<D>;
+    constexpr int NS = L::kStages;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem_raw);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + B_COUNT);
+    uint32_t *valid = reinterpret_cast<uint32_t *>(smem_raw + 512);  // [kValidRing]
+    float *stats = reinterpret_cast<float *>(valid + kValidRing);    // [128] m, [128] l
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + L::kMisc + 1023) & ~static_cast<uintptr_t>(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        mbar_init(&bar[B_QFULL], 1);
+        mbar_init(&bar[B_QEMPTY], 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar[B_SFULL + i], 1);
+            mbar_init(&bar[B_PREADY + i], 128);
+            mbar_init(&bar[B_OUNIT + i], 1);
+            mbar_init(&bar[B_OFREE + i], 128);
+            mbar_init(&bar[B_DRAIN + i], 1);
+        }
+        mbar_init(&bar[B_STATS], 128);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&bar[B_FULL + i], 1);
+            mbar_init(&bar[B_EMPTY + i], 2);
+        }
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tc::alloc(tmem_slot, kTmemCols);
+        tc::relinquish();
+    }
+    if (warp == kProducerWarp && lane == 0) {
+        tma_prefetch_desc(&qmap);
+        tma_prefetch_desc(&kvmap);
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
     griddep_wait();
-    constexpr int kPart = D / 4, kRec = D + 4;
-    __shared__ __align__(16) __half ks[kBlockSize][D];
-    __shared__ __align__(16) __half vs[kBlockSize][D];
+    griddep_launch_dependents();
+    const uint32_t tmem = *tmem_slot;  // S_0 | S_1 | O_0 | O_1
     const int64_t total = a.tl.head->total;
     const int G = plan_ctas(total, a.G);
-    if ((int)blockIdx.x >= G) return;
-    const int64_t end = plan_cut(total, blockIdx.x + 1, G);
-    const int tid = threadIdx.x, local = tid >> 2, part = tid & 3;
-    const int mpt = kPrefixTile / a.g, tile = local / kPrefixTile, in = local % kPrefixTile;
-    int r = 0;
-    for (int64_t pos = plan_cut(total, blockIdx.x, G); pos < end;) {
-        PlanGroup p = a.tl.plan[r];
-        while (pos >= p.start + (int64_t)p.tiles * p.units * a.Hk) p = a.tl.plan[++r];
-        const int64_t off = pos - p.start;
-        const int unit = (int)(off / p.tiles), t0 = (int)(off % p.tiles);
-        const int nt = (int)min((int64_t)(p.tiles - t0), end - pos);
-        const int kvh = unit / p.units, u = unit % p.units;
-        const int member = u * 2 * mpt + tile * mpt + in / a.g;
-        const bool live = in < mpt * a.g && member < p.members;
-        const int64_t row = (int64_t)(p.s0 + (live ? member : 0)) * a.H + kvh * a.g + in % a.g;
-        float q[kPart], o[kPart], m = -INFINITY, l = 0.f;
-        for (int i = 0; i < kPart; ++i) {
-            q[i] = live ? __half2float(a.q[row * D + part * kPart + i]) * a.scale_log2 : 0.f;
-            o[i] = 0.f;
-        }
-        for (int b = t0 * kTileBlocks; b < min((t0 + nt) * kTileBlocks, p.blocks); ++b) {
-            const int blk = a.block_tables[(int64_t)p.lead * a.maxb + b];
-            const bool ok = blk >= 0 && blk < a.num_blocks;
-            if (!ok) {
-                if (tid == 0) report(a.status, PA_DEV_BAD_BLOCK);
-                continue;
-            }
-            __syncthreads();
-            for (int i = tid; i < kBlockSize * D; i += kPrefixThreads) {
-                const int64_t at = ((int64_t)(blk * kBlockSize + i / D) * a.Hk + kvh) * D + i % D;
-                ks[i / D][i % D] = a.kplane[at];
-                vs[i / D][i % D] = a.vplane[at];
-            }
-            __syncthreads();
-            for (int t = 0; t < kBlockSize; ++t) {
-                float x = 0.f;
-                for (int i = 0; i < kPart; ++i) x += q[i] * __half2float(ks[t][part * kPart + i]);
-                x += __shfl_xor_sync(0xffffffffu, x, 1);
-                x += __shfl_xor_sync(0xffffffffu, x, 2);
-                const float mn = fmaxf(m, x), f = ex2(m - mn), e = ex2(x - mn);
-                m = mn;
-                l = l * f + e;
-                for (int i = 0; i < kPart; ++i)
-                    o[i] = o[i] * f + e * __half2float(vs[t][part * kPart + i]);
-            }
-        }
-        if (live) {
-            float *rec = t0 == 0 ? a.first + row * kRec
-                                 : a.more + ((int64_t)blockIdx.x * 2 * kPrefixTile + local) * kRec;
-            for (int i = 0; i < kPart; ++i) rec[part * kPart + i] = o[i];
-            if (part == 0) {
-                rec[D] = m;
-                rec[D + 1] = l;
-            }
-        }
-        pos += nt;
+    PrefixWalk w;
+    w.pos = w.end = 0;
+    w.group = 0;
+    if ((int)blockIdx.x < G) {
+        w.pos = plan_cut(total, blockIdx.x, G);
+        w.end = plan_cut(total, blockIdx.x + 1, G);
     }
+    const int mpt = kPrefixTile / a.g;
+    auto s_col = [](int t) { return (uint32_t)(t * kPrefixTile); };
+    auto o_col = [](int t) { return (uint32_t)(2 * kPrefixTile + t * D); };
+
+    if (warp == kProducerWarp) {
+        // ============ producer: a segment's K and V tiles in turn, its Q tiles behind
+        // the first two (whose stages free before the Q tiles' last reader does)
+        const uint32_t q_bytes = (uint32_t)(a.g * mpt * 128 * (D / 64));
+        int ok = 1, entry = 0, segs = 0, tile = 0;
+        while (ok && w.next(a)) {
+            const PrefixSegment &sg = w.seg;
+            const int32_t *row = a.block_tables + (int64_t)sg.p.lead * a.maxb;
+            auto block_at = [&](int j) -> int {  // lane's block of key tile j, -1: none
+                const int b = (sg.t0 + j) * kTileBlocks + lane;
+                if (lane >= kTileBlocks || j >= sg.tiles || b >= sg.p.blocks) return -1;
+                const int blk = __ldg(row + b);
+                if (blk >= 0 && blk < a.num_blocks) return blk;
+                report(a.status, PA_DEV_BAD_BLOCK);
+                return -1;
+            };
+            int blk = block_at(0);
+            for (int j = 0; j < sg.tiles && ok; ++j, ++tile) {
+                const uint32_t have = __ballot_sync(0xffffffffu, blk >= 0);
+                const int next_blk = block_at(j + 1);
+                if (lane == 0) valid[tile % kValidRing] = have;
+                __syncwarp();
+                for (int kv = 0; kv < 2 && ok; ++kv, ++entry) {
+                    const int st = entry % NS;
+                    ok = mbar_wait(&bar[B_EMPTY + st], ((entry / NS) & 1) ^ 1);
+                    if (lane == 0 && ok) mbar_arrive_expect_tx(&bar[B_FULL + st], L::kTileBytes);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    // (a block that is missing comes from behind the pool: zeros)
+                    const int r0 = (blk >= 0 ? blk : a.num_blocks) * kBlockSize;
+                    if (lane < kTileBlocks)
+                        for (int hf = 0; hf < D / 64; ++hf)
+                            tma_load_5d(smem + L::kRing + st * L::kTileBytes + hf * L::kHalf +
+                                            lane * kBlockSize * 128,
+                                        &kvmap, &bar[B_FULL + st], 0, hf, sg.kvh, r0,
+                                        kv ? a.plane_v : a.plane_k);
+                }
+                blk = next_blk;
+                if (j == 0 && ok) {
+                    if (segs > 0) ok = mbar_wait(&bar[B_QEMPTY], (segs - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (lane == 0 && ok) {
+                        mbar_arrive_expect_tx(&bar[B_QFULL], q_bytes * (sg.pair ? 2 : 1));
+                        for (int t = 0; t < (sg.pair ? 2 : 1); ++t)
+                            for (int hf = 0; hf < D / 64; ++hf)
+                                tma_load_4d(smem + t * L::kTileBytes + hf * L::kHalf, &qmap,
+                                            &bar[B_QFULL], 0, hf, sg.kvh * a.g,
+                                            sg.p.s0 + sg.member0 + t * mpt);
+                    }
+                    ++segs;
+                }
+            }
+        }
+        if (lane == 0) {
+            if (!ok) report(a.status, PA_DEV_TIMEOUT);
+            // Leave no copy in flight.
+            for (int i = max(0, entry - NS); i < entry; ++i)
+                mbar_wait(&bar[B_FULL + i % NS], (i / NS) & 1);
+            if (segs > 0) mbar_wait(&bar[B_QFULL], (segs - 1) & 1);
+        }
+    } else if (warp > kProducerWarp) {
+        // ============ MMA issuers.  Per key tile: S_t = Q_t K^T, then, once the
+        // softmax has put P over it, O_t += P V (operations issued by one thread
+        // execute in order, so the next scores may be issued at once).  Every
+        // thread waits for every tile of the ring and gives it back, so that each
+        // wait by phase parity is exact.
+        const int t = warp - kMmaWarp;
+        if (lane == 0) {
+            constexpr uint32_t kIdescQK = tc::idesc_f16(kPrefixTile, kPrefixTile, false, false);
+            constexpr uint32_t kIdescPV = tc::idesc_f16(kPrefixTile, D, false, true);
+            const uint64_t dk0 = tc::smem_desc_sw128(smem_u32(smem + L::kRing), 16, 1024);
+            const uint64_t dv0 = tc::smem_desc_sw128(smem_u32(smem + L::kRing), L::kHalf, 1024);
+            bool ok = true;
+            int entry = 0, segs = 0, g = 0, un = 0;
+            while (ok && w.next(a)) {
+                const PrefixSegment &sg = w.seg;
+                const int n = sg.count(t);
+                const uint64_t dq = tc::smem_desc_sw128(
+                    smem_u32(smem + (sg.pair ? t * L::kTileBytes : 0)), 16, 1024);
+                ok = mbar_wait(&bar[B_QFULL], segs & 1);
+                ++segs;
+                if (ok && n == 0) mbar_arrive(&bar[B_QEMPTY]);
+                int done = 0;  // tiles of this stream
+                for (int j = 0; j < sg.tiles && ok; ++j, entry += 2) {
+                    const bool mine = sg.mine(j, t);
+                    const int ks = entry % NS, vs = (entry + 1) % NS;
+                    ok = mbar_wait(&bar[B_FULL + ks], (entry / NS) & 1);
+                    if (!ok) break;
+                    if (mine) {
+                        tc::fence_after();
+                        const uint64_t dk = dk0 + (uint64_t)((ks * L::kTileBytes) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t step =
+                                (uint64_t)(((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4);
+                            tc::mma_ss(tmem + s_col(t), dq + step, dk + step, kIdescQK, kk > 0);
+                        }
+                        tc::commit(&bar[B_SFULL + t]);
+                        tc::commit(&bar[B_EMPTY + ks]);
+                        if (done == n - 1) tc::commit(&bar[B_QEMPTY]);
+                    } else {
+                        mbar_arrive(&bar[B_EMPTY + ks]);
+                    }
+                    ok = mbar_wait(&bar[B_FULL + vs], ((entry + 1) / NS) & 1);
+                    if (!ok) break;
+                    if (mine) {
+                        ok = mbar_wait(&bar[B_PREADY + t], g & 1);
+                        // the last segment's O has to have been read
+                        if (ok && done == 0 && un > 0)
+                            ok = mbar_wait(&bar[B_OFREE + t], (un - 1) & 1);
+                        if (!ok) break;
+                        tc::fence_after();
+                        const uint64_t dv = dv0 + (uint64_t)((vs * L::kTileBytes) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < kPrefixTile / 16; ++kk)
+                            tc::mma_ts(tmem + o_col(t), tmem + s_col(t) + kk * 8,
+                                       dv + (uint64_t)((kk * 16 * 128) >> 4), kIdescPV,
+                                       (done > 0 || kk > 0) ? 1u : 0u);
+                        tc::commit(&bar[B_EMPTY + vs]);
+                        if (done == n - 1) tc::commit(&bar[B_OUNIT + t]);
+                        ++done;
+                        ++g;
+                    } else {
+                        mbar_arrive(&bar[B_EMPTY + vs]);
+                    }
+                }
+                if (n > 0) ++un;
+            }
+            if (!ok) report(a.status, PA_DEV_TIMEOUT);
+            // Nothing of ours may still be running when the CTA frees TMEM.
+            tc::commit(&bar[B_DRAIN + t]);
+            mbar_wait(&bar[B_DRAIN + t], 0);
+        }
+        __syncwarp();
+    } else {
+        // ============ softmax of stream t
+        const int t = warp >> 2, r = tid - t * 128;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_tmem = tmem + lane_base + s_col(t), o_tmem = tmem + lane_base + o_col(t);
+        const float sl2 = a.scale_log2;
+        const uint64_t sl2x2 = f2_pack(sl2, sl2);
+        bool ok = true;
+        int g = 0, un = 0, tile = 0, merged = 0;
+        while (ok && w.next(a)) {
+            const PrefixSegment &sg = w.seg;
+            const int n = sg.count(t);
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; i < n; ++i, ++g) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_SFULL + t], g & 1));
+                if (!ok) break;
+                tc::fence_after();
+                const uint32_t have = valid[(tile + (sg.pair ? i : 2 * i + t)) % kValidRing];
+                uint32_t s0[32], s1[32], s2[32], s3[32];
+                float x0, x1, x2, x3;
+                tc::ld32_max_issue(s_tmem, s0, x0);
+                tc::ld32_max_issue(s_tmem + 32, s1, x1);
+                tc::ld32_max_issue(s_tmem + 64, s2, x2);
+                tc::ld32_max_issue(s_tmem + 96, s3, x3);
+                tc::wait_ld(s0, s1, x0, x1);
+                tc::wait_ld(s2, s3, x2, x3);
+                if (have != (1u << kTileBlocks) - 1) {
+                    // blocks that are missing: 16 columns each
+                    auto mask = [&](uint32_t (&s)[32], float &x, int b) {
+                        x = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            if (!(have >> (b + (c >> 4)) & 1)) s[c] = __float_as_uint(-INFINITY);
+                            x = fmaxf(x, u2f(s[c]));
+                        }
+                    };
+                    mask(s0, x0, 0);
+                    mask(s1, x1, 2);
+                    mask(s2, x2, 4);
+                    mask(s3, x3, 6);
+                }
+                const float mt = fmaxf(fmax3(x0, x1, x2), x3) * sl2;
+                const bool up = mt > m + kRescale;
+                float f = 1.f;
+                if (up) {
+                    f = ex2(m - mt);  // 0 for the segment's first
+                    l *= f;
+                    m = mt;
+                }
+                if (i > 0 && __any_sync(0xffffffffu, up)) {
+                    // (these scores were issued behind the last P.V, and their
+                    // barrier tracks both: O is complete)
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o_tmem + c, o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(u2f(o[k]) * f);
+                        tc::st16(o_tmem + c, o);
+                    }
+                }
+                const float base = (m == -INFINITY ? 0.f : m) - kShift;
+                const uint64_t negm = f2_pack(-base, -base);
+                uint64_t la = 0, lb = 0;
+                auto exps = [&](const uint32_t (&s)[32], int c) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        float e0, e1, e2, e3;
+                        f2_unpack(f2_fma(f2_pack(u2f(s[2 * k]), u2f(s[2 * k + 1])), sl2x2, negm), e0, e1);
+                        f2_unpack(f2_fma(f2_pack(u2f(s[2 * k + 2]), u2f(s[2 * k + 3])), sl2x2, negm), e2, e3);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        e2 = ex2(e2);
+                        e3 = ex2(e3);
+                        la = f2_add(la, f2_pack(e0, e1));
+                        lb = f2_add(lb, f2_pack(e2, e3));
+                        p[k] = pack_half2(e0, e1);
+                        p[k + 1] = pack_half2(e2, e3);
+                    }
+                    tc::st16(s_tmem + c, p);
+                };
+                exps(s0, 0);
+                exps(s1, 16);
+                exps(s2, 32);
+                exps(s3, 48);
+                float y0, y1, y2, y3;
+                f2_unpack(la, y0, y1);
+                f2_unpack(lb, y2, y3);
+                l += (y0 + y1) + (y2 + y3);
+                tc::wait_st();
+                tc::fence_before();
+                mbar_arrive(&bar[B_PREADY + t]);
+            }
+            tile += sg.tiles;
+            if (!ok) break;
+            if (n == 0) continue;
+
+            // ---- the segment's record: m and l are of P = 2^(x - m + kShift)
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_OUNIT + t], un & 1));
+            ++un;
+            if (!ok) break;
+            tc::fence_after();
+            float f0 = 1.f, f1 = 0.f;
+            const bool both = !sg.pair && sg.tiles > 1;
+            if (both) {
+                // one tile of rows: stream 0 joins what both have of it
+                if (t == 1) {
+                    stats[r] = m;
+                    stats[kPrefixTile + r] = l;
+                    tc::fence_before();
+                    mbar_arrive(&bar[B_STATS]);
+                    continue;
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_STATS], merged & 1));
+                // (stream 1's last P.V: its thread has waited for it)
+                ++merged;
+                if (!ok) break;
+                tc::fence_after();
+                const float m1 = stats[r], l1 = stats[kPrefixTile + r];
+                const float M = fmaxf(m, m1);
+                f0 = m == -INFINITY ? 0.f : ex2(m - M);
+                f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+                l = f0 * l + f1 * l1;
+                m = M;
+            }
+            const int member = sg.member0 + (sg.pair ? t * mpt : 0) + r / a.g;
+            const bool live = r < mpt * a.g && member < sg.p.members;
+            float *rec = sg.t0 == 0
+                             ? a.first + ((int64_t)(sg.p.s0 + member) * a.H + sg.kvh * a.g + r % a.g) *
+                                             (D + 4)
+                             : a.more + ((int64_t)blockIdx.x * 2 * kPrefixTile +
+                                         (sg.pair ? t * kPrefixTile : 0) + r) *
+                                            (D + 4);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32], o1[32];
+                tc::ld32_issue(o_tmem + c, o);
+                tc::ld32_issue(both ? tmem + lane_base + o_col(1) + c : o_tmem + c, o1);
+                tc::wait_ld(o, o1);
+                if (both) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        o[k] = __float_as_uint(fmaf(f0, u2f(o[k]), f1 * u2f(o1[k])));
+                }
+                if (live) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        *reinterpret_cast<uint4 *>(rec + c + k) =
+                            make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                }
+            }
+            if (live) *reinterpret_cast<float2 *>(rec + D) = make_float2(m - kShift, l);
+            tc::fence_before();
+            mbar_arrive(&bar[B_OFREE + t]);
+            if (both) mbar_arrive(&bar[B_OFREE + 1]);
+        }
+        if (!ok && lane == 0) report(a.status, PA_DEV_TIMEOUT);
+    }
+
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == kMmaWarp) tc::dealloc(tmem, kTmemCols);
+}
+
+// 4-D fp16 map of q [B][H][D]: {64, D/64, H, B}, box {64, 1, g, 128/g}: the query
+// rows of a tile, (sequence, head) one after another.
+bool make_group_map(CUtensorMap *map, const void *base, int B, int H, int D, int g) {
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {64, (cuuint64_t)(D / 64), (cuuint64_t)H, (cuuint64_t)B};
+    cuuint64_t strides[3] = {128, (cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)g, (cuuint32_t)(kPrefixTile / g)};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(base), dims, strides,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+int launch_prefix(const SharedArgs &a, const pa_cache_t *cache, cudaStream_t st) {
+    static std::mutex mu;
+    static bool attr_set[64] = {false};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PA_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!attr_set[dev]) {
+            if (cudaFuncSetAttribute(prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)PrefixLayout<D>::smem()) != cudaSuccess) {
+                cudaGetLastError();
+                return PA_ERR_CUDA;
+            }
+            attr_set[dev] = true;
+        }
+    }
+    CUtensorMap qmap, kvmap;
+    if (!make_group_map(&qmap, a.q, a.B, a.H, D, a.g) || !make_cache_map(&kvmap, cache, 1, kBlockSize))
+        return PA_ERR_CUDA;
+    launch_dependent(prefix_kernel<D>, dim3(a.G), dim3(kPrefixThreads), PrefixLayout<D>::smem(), st,
+                     qmap, kvmap, a);
+    return launch_status();
 }
 
 constexpr int kJoinThreads = 256;
@@ -152,9 +581,8 @@ constexpr int kMaxCtas = 160;  // (152 SMs)
 size_t rows_bytes(int B, int H, int D) { return up256((size_t)B * H * (D + 4) * sizeof(float)); }
 
 template <int D>
-int launch_shared(const SharedArgs &a, cudaStream_t st) {
-    launch_dependent(prefix_kernel<D>, dim3(a.G), dim3(kPrefixThreads), 0, st, a);
-    const int rc = launch_status();
+int launch_shared(const SharedArgs &a, const pa_cache_t *cache, cudaStream_t st) {
+    const int rc = launch_prefix<D>(a, cache, st);
     if (rc != PA_OK) return rc;
     const int64_t rows = (int64_t)a.B * a.H, per = kJoinThreads / 32;
     launch_dependent(join_kernel<D>, dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinThreads),
@@ -216,8 +644,8 @@ extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int laye
     a.more = reinterpret_cast<float *>(p);
     a.tl.groups = {group_starts, shared_blocks, num_groups, max_blocks_per_seq};
     a.q = static_cast<const __half *>(q);
-    a.kplane = cache_plane(cache, 0, layer);
-    a.vplane = cache_plane(cache, 1, layer);
+    a.plane_k = layer;
+    a.plane_v = cache->layers + layer;
     a.block_tables = block_tables;
     a.context_lens = context_lens;
     a.out = static_cast<__half *>(out);
@@ -236,7 +664,7 @@ extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int laye
                           scale,    out,     dev_status, st};
     const int rc2 = launch_decode_tails(c, at, a.tl);
     if (rc2 != PA_OK) return rc2;
-    return head_dim == 128 ? launch_shared<128>(a, st) : launch_shared<64>(a, st);
+    return head_dim == 128 ? launch_shared<128>(a, cache, st) : launch_shared<64>(a, cache, st);
 }
 
 extern "C" int pa_prepare_shared(int num_seqs, const int32_t *block_tables,
