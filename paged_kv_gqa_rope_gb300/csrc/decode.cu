@@ -431,7 +431,8 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     if constexpr (MODE == Mode::kTails) {
         const int bad = read_groups(a.tl.groups, a.context_lens, B, skip, lens, tid, kThreads);
         if (bad && cta == 0 && tid == 0) report(a.status, PA_DEV_BAD_LENGTH);
-        if (cta == 0 && warp == 1) write_plan(a.tl, skip, a.Hk, a.g, B, bad == 2, lane);
+        if (warp == 1)
+            write_plan(a.tl, skip, lens, a.Hk, a.g, B, bad == 2, lane, cta, (int)gridDim.x);
     }
     for (int s = tid; s < B; s += kThreads) {
         [[maybe_unused]] const int ctx = __ldg(a.context_lens + s);

@@ -37,20 +37,35 @@ struct alignas(16) PlanGroup {
     int lead;       // sequence whose block table is read
     int units;      // units of a KV head
 };
-struct PlanHead {
-    int64_t total;  // tiles of the line
-    int n;          // groups
+// What the join needs of a sequence.
+struct alignas(16) SeqPlan {
+    int64_t start;   // line: first tile of its unit, of KV head 0
+    int64_t stride;  // tiles from a KV head's unit to the next head's
+    int tiles;       // of its unit
+    int local;       // row of its first Q head (of a KV head) in the unit
+    int state;
+    int tail;        // tokens behind the shared blocks
 };
-enum : int { kNoGroup = -1, kLeftOut = -2 };  // in seq_group
-
+enum : int { kInGroup = 0, kAlone = -1, kLeftOut = -2 };  // SeqPlan::state
+// Where a CTA's range begins: in tile t0 of unit `unit` (all KV heads counted) of
+// group `group` of the plan, and how many tiles it has.  One load, instead of a
+// search and 64-bit divisions at the start of every CTA (5.1 us to the first
+// scores with those).
+struct alignas(16) PlanCut {
+    PlanGroup p;
+    int64_t tiles;
+    int group, unit, t0, pad[3];
+};
 // Records in the place of the output, over the tokens behind the shared blocks
 // (pa_decode_shared): unnormalised O, then m and l of the row.
 struct DecodeTails {
     float *rec;  // [B][H][D + 4]
     Groups groups;
-    PlanHead *head;
-    PlanGroup *plan;     // [groups.n]
-    int32_t *seq_group;  // [B]: its place in plan, kNoGroup or kLeftOut
+    int64_t *total;   // tiles of the line
+    PlanGroup *plan;  // [groups.n]: the groups with tiles
+    SeqPlan *seqs;    // [B]
+    PlanCut *cuts;    // [G]
+    int G;            // CTAs of the prefix kernel
 };
 
 constexpr int kPrefixTile = 128;  // keys of a tile, and query rows
@@ -64,6 +79,8 @@ __device__ __forceinline__ int plan_ctas(int64_t total, int grid) {
 }
 __device__ __forceinline__ int64_t plan_cut(int64_t total, int c, int G) { return total * c / G; }
 __device__ __forceinline__ int plan_cta(int64_t t, int64_t total, int G) {
+    if (total < INT32_MAX / 1024)  // (G <= 160: the sum fits 32 bits)
+        return (int)((((uint32_t)t + 1) * (uint32_t)G + (uint32_t)total - 1) / (uint32_t)total) - 1;
     return (int)(((t + 1) * G + total - 1) / total) - 1;
 }
 
@@ -156,16 +173,23 @@ __device__ __forceinline__ int read_groups(const Groups &g, const int32_t *conte
     return __syncthreads_or(bad) != 0 ? 1 : 0;
 }
 
-// By one warp: the plan of the groups read_groups has gone over.
-__device__ __forceinline__ void write_plan(const DecodeTails &tl, const int32_t *skip, int Hk,
-                                           int g, int B, bool broken, int lane) {
-    const int per_unit = 2 * (kPrefixTile / g);
-    int64_t line = 0;
-    int count = 0;
-    if (broken)
-        for (int s = lane; s < B; s += 32) tl.seq_group[s] = kLeftOut;
-    for (int r0 = 0; r0 < tl.groups.n && !broken; r0 += 32) {
-        PlanGroup p = {};
+// The plan of the groups read_groups has gone over, by one warp of every CTA:
+// CTA 0 writes it down, CTA c the cut of the prefix kernel's CTA c.
+__device__ __forceinline__ void write_plan(const DecodeTails &tl, const int32_t *skip,
+                                           const int32_t *lens, int Hk, int g, int B, bool broken,
+                                           int lane, int cta, int ctas) {
+    const int mpt = kPrefixTile / g, per_unit = 2 * mpt;
+    const bool writes = cta == 0;
+    if (broken) {
+        if (writes) {
+            for (int s = lane; s < B; s += 32) tl.seqs[s].state = kLeftOut;
+            if (lane == 0) *tl.total = 0;
+        }
+        return;
+    }
+    // Groups r0 .. r0 + 31, one a lane, and the tiles that each has of the line.
+    auto load = [&](int r0, PlanGroup &p) -> int64_t {
+        p = PlanGroup{};
         if (r0 + lane < tl.groups.n) {
             p.s0 = __ldg(tl.groups.starts + r0 + lane);
             p.members = __ldg(tl.groups.starts + r0 + lane + 1) - p.s0;
@@ -175,29 +199,70 @@ __device__ __forceinline__ void write_plan(const DecodeTails &tl, const int32_t 
             p.tiles = (p.blocks + kTileBlocks - 1) / kTileBlocks;
             p.units = (p.members + per_unit - 1) / per_unit;
         }
-        const int64_t mine = (int64_t)p.tiles * p.units * Hk;
-        int64_t sum = mine;
+        return (int64_t)p.tiles * p.units * Hk;
+    };
+    auto scan = [&](int64_t x) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
         }
+        return x;
+    };
+    PlanGroup p;
+    int64_t line = 0;
+    int count = 0;
+    for (int r0 = 0; r0 < tl.groups.n; r0 += 32) {
+        const int64_t mine = load(r0, p), sum = scan(mine);
         p.start = line + sum - mine;
-        const uint32_t has = __ballot_sync(0xffffffffu, mine > 0);
-        const int at = mine > 0 ? count + __popc(has & ((1u << lane) - 1)) : kNoGroup;
-        if (mine > 0) tl.plan[at] = p;
-        line += __shfl_sync(0xffffffffu, sum, 31);
-        count += __popc(has);
-        for (int i = 0; i < min(32, tl.groups.n - r0); ++i) {
-            const int s0 = __shfl_sync(0xffffffffu, p.s0, i);
-            const int m = __shfl_sync(0xffffffffu, p.members, i);
-            const int id = __shfl_sync(0xffffffffu, at, i);
-            for (int s = s0 + lane; s < s0 + m; s += 32) tl.seq_group[s] = skip[s] < 0 ? kLeftOut : id;
+        if (writes) {
+            const uint32_t has = __ballot_sync(0xffffffffu, mine > 0);
+            if (mine > 0) tl.plan[count + __popc(has & ((1u << lane) - 1))] = p;
+            count += __popc(has);
+            for (int i = 0; i < min(32, tl.groups.n - r0); ++i) {
+                const int s0 = __shfl_sync(0xffffffffu, p.s0, i);
+                const int m = __shfl_sync(0xffffffffu, p.members, i);
+                SeqPlan q = {};
+                q.start = __shfl_sync(0xffffffffu, p.start, i);
+                q.tiles = __shfl_sync(0xffffffffu, p.tiles, i);
+                q.stride = (int64_t)q.tiles * __shfl_sync(0xffffffffu, p.units, i);
+                for (int s = s0 + lane; s < s0 + m; s += 32) {
+                    const int u = (s - s0) / per_unit, in = s - s0 - u * per_unit;
+                    SeqPlan x = q;
+                    x.start += (int64_t)u * x.tiles;
+                    x.local = in / mpt * kPrefixTile + in % mpt * g;
+                    x.state = skip[s] < 0 ? kLeftOut : q.tiles > 0 ? kInGroup : kAlone;
+                    x.tail = lens[s];
+                    tl.seqs[s] = x;
+                }
+            }
         }
+        line += __shfl_sync(0xffffffffu, sum, 31);
     }
-    if (lane == 0) {
-        tl.head->total = line;
-        tl.head->n = count;
+    if (writes && lane == 0) *tl.total = line;
+    // The group that holds a cut, and where the cut lies in it.
+    const int G = plan_ctas(line, tl.G);
+    for (int c = cta; c < G; c += ctas) {
+        const int64_t at = plan_cut(line, c, G);
+        int64_t before = 0;
+        int group = 0;
+        for (int r0 = 0; r0 < tl.groups.n; r0 += 32) {
+            const int64_t mine = load(r0, p), sum = scan(mine);
+            p.start = before + sum - mine;
+            const uint32_t has = __ballot_sync(0xffffffffu, mine > 0);
+            if (p.start <= at && at < p.start + mine) {
+                PlanCut cut = {};
+                cut.p = p;
+                cut.tiles = plan_cut(line, c + 1, G) - at;
+                cut.group = group + __popc(has & ((1u << lane) - 1));
+                cut.unit = (int)((at - p.start) / p.tiles);
+                cut.t0 = (int)((at - p.start) % p.tiles);
+                tl.cuts[c] = cut;
+            }
+            group += __popc(has);
+            before += __shfl_sync(0xffffffffu, sum, 31);
+            if (before > at) break;
+        }
     }
 }
 

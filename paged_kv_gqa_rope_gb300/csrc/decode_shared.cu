@@ -14,8 +14,13 @@ struct SharedArgs {
     const int32_t *context_lens;
     __half *out;
     DecodeTails tl;
-    float *first;  // [B][H][D + 4]: records of units' first pieces
-    float *more;   // [G][256][D + 4]: of the piece with which a CTA's range begins inside a unit
+    // Records of a unit's first piece, over rows (KV head, sequence, Q head of the
+    // KV head), and of the piece with which a CTA's range begins inside a unit, over
+    // the rows of two tiles.  Both have four columns of all rows side by side
+    // ([D / 4][rows][4], then {m, l}[rows]), so that neither the threads that write
+    // them (one a row) nor those that read them leave a line half used.
+    float *first;  // [B * H rows]
+    float *more;   // [G][256 rows]
     int32_t *status;
     float scale_log2;
     int B, H, Hk, g, maxb, num_blocks, plane_k, plane_v, G;
@@ -87,6 +92,19 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
+// A record of row `row` among `rows`: its columns 4 i .. 4 i + 3, and {m, l}.
+struct Record {
+    float *base;
+    int64_t rows, row;
+    __device__ __forceinline__ float4 *cols(int i) const {
+        return reinterpret_cast<float4 *>(base) + i * rows + row;
+    }
+    template <int D>
+    __device__ __forceinline__ float2 *stat() const {
+        return reinterpret_cast<float2 *>(base + D * rows) + row;
+    }
+};
+
 // The part of the CTA's range that lies in one unit.
 struct PrefixSegment {
     PlanGroup p;
@@ -101,23 +119,31 @@ struct PrefixSegment {
 
 // Walks a CTA's range; every role has its own.
 struct PrefixWalk {
-    int64_t pos, end;
-    int group;
+    int64_t left;  // tiles to go
+    int group, unit, t0;
     PrefixSegment seg;
+    __device__ __forceinline__ void begin(const PlanCut &c) {
+        seg.p = c.p;
+        left = c.tiles;
+        group = c.group;
+        unit = c.unit;
+        t0 = c.t0;
+    }
     __device__ __forceinline__ bool next(const SharedArgs &a) {
-        if (pos >= end) return false;
-        seg.p = a.tl.plan[group];
-        while (pos >= seg.p.start + (int64_t)seg.p.tiles * seg.p.units * a.Hk)
+        if (left <= 0) return false;
+        if (unit == seg.p.units * a.Hk) {
             seg.p = a.tl.plan[++group];
-        const int64_t off = pos - seg.p.start;
-        const int unit = (int)(off / seg.p.tiles);
+            unit = 0;
+        }
         const int mpt = kPrefixTile / a.g;
-        seg.t0 = (int)(off - (int64_t)unit * seg.p.tiles);
-        seg.tiles = (int)min((int64_t)(seg.p.tiles - seg.t0), end - pos);
+        seg.t0 = t0;
+        seg.tiles = (int)min((int64_t)(seg.p.tiles - t0), left);
         seg.kvh = unit / seg.p.units;
         seg.member0 = (unit - seg.kvh * seg.p.units) * 2 * mpt;
         seg.pair = seg.p.members - seg.member0 > mpt;
-        pos += seg.tiles;
+        left -= seg.tiles;
+        ++unit;
+        t0 = 0;
         return true;
     }
 };
@@ -168,15 +194,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     griddep_wait();
     griddep_launch_dependents();
     const uint32_t tmem = *tmem_slot;  // S_0 | S_1 | O_0 | O_1
-    const int64_t total = a.tl.head->total;
-    const int G = plan_ctas(total, a.G);
     PrefixWalk w;
-    w.pos = w.end = 0;
-    w.group = 0;
-    if ((int)blockIdx.x < G) {
-        w.pos = plan_cut(total, blockIdx.x, G);
-        w.end = plan_cut(total, blockIdx.x + 1, G);
-    }
+    w.begin(a.tl.cuts[blockIdx.x]);  // (of a CTA without a range not written: see below)
+    if ((int64_t)blockIdx.x >= *a.tl.total) w.left = 0;
     const int mpt = kPrefixTile / a.g;
     auto s_col = [](int t) { return (uint32_t)(t * kPrefixTile); };
     auto o_col = [](int t) { return (uint32_t)(2 * kPrefixTile + t * D); };
@@ -443,12 +463,16 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             }
             const int member = sg.member0 + (sg.pair ? t * mpt : 0) + r / a.g;
             const bool live = r < mpt * a.g && member < sg.p.members;
-            float *rec = sg.t0 == 0
-                             ? a.first + ((int64_t)(sg.p.s0 + member) * a.H + sg.kvh * a.g + r % a.g) *
-                                             (D + 4)
-                             : a.more + ((int64_t)blockIdx.x * 2 * kPrefixTile +
-                                         (sg.pair ? t * kPrefixTile : 0) + r) *
-                                            (D + 4);
+            Record rec;
+            if (sg.t0 == 0) {
+                rec.base = a.first;
+                rec.rows = (int64_t)a.B * a.H;
+                rec.row = ((int64_t)sg.kvh * a.B + sg.p.s0 + member) * a.g + r % a.g;
+            } else {
+                rec.base = a.more + (int64_t)blockIdx.x * 2 * kPrefixTile * (D + 4);
+                rec.rows = 2 * kPrefixTile;
+                rec.row = (sg.pair ? t * kPrefixTile : 0) + r;
+            }
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32], o1[32];
@@ -463,11 +487,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 if (live) {
 #pragma unroll
                     for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<uint4 *>(rec + c + k) =
-                            make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        *rec.cols((c + k) / 4) =
+                            make_float4(u2f(o[k]), u2f(o[k + 1]), u2f(o[k + 2]), u2f(o[k + 3]));
                 }
             }
-            if (live) *reinterpret_cast<float2 *>(rec + D) = make_float2(m - kShift, l);
+            if (live) *rec.stat<D>() = make_float2(m - kShift, l);
             tc::fence_before();
             mbar_arrive(&bar[B_OFREE + t]);
             if (both) mbar_arrive(&bar[B_OFREE + 1]);
@@ -523,54 +547,75 @@ int launch_prefix(const SharedArgs &a, const pa_cache_t *cache, cudaStream_t st)
 
 constexpr int kJoinThreads = 256;
 
-// A warp per (sequence, Q head): joins the row's records.
+// Joins a row's records: a thread has four columns of a row, the 32 threads of a
+// warp the same columns of 32 rows (in the records' order), blockIdx.y the columns.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SharedArgs a) {
     griddep_wait();
     griddep_launch_dependents();
-    constexpr int kRec = D + 4, kVec = D / 32;
     const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.B * a.H) return;
-    const int s = (int)(row / a.H), h = (int)(row % a.H);
-    const int group = a.tl.seq_group[s];
-    if (group == kLeftOut) return;
-    int tail = a.context_lens[s], pieces = 0, c0 = 0, local = 0;
-    if (group >= 0) {
-        const PlanGroup p = a.tl.plan[group];
-        const int64_t total = a.tl.head->total;
+    const int c4 = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    const int64_t at = (int64_t)blockIdx.x * 32 + lane;  // (KV head, sequence, its Q head)
+    if (at >= (int64_t)a.B * a.H) return;
+    const int j = (int)at % a.g, s = (int)at / a.g % a.B, kvh = (int)at / a.g / a.B;
+    // (the tail's record does not wait for the plan, nor the pieces for each other)
+    const int64_t row = (int64_t)s * a.H + kvh * a.g + j;  // of q and out
+    const float *r = a.tl.rec + row * (D + 4);
+    float2 st = __ldcg(reinterpret_cast<const float2 *>(r + D));
+    float4 O = __ldcg(reinterpret_cast<const float4 *>(r) + c4);
+    const SeqPlan p = a.tl.seqs[s];
+    const int64_t total = *a.tl.total;
+    if (p.state == kLeftOut) return;
+    int pieces = 0, c0 = 0;
+    if (p.state == kInGroup) {
+        const int64_t start = p.start + kvh * p.stride;
         const int G = plan_ctas(total, a.G);
-        const int mpt = kPrefixTile / a.g, kvh = h / a.g, member = s - p.s0;
-        const int u = member / (2 * mpt), in = member % (2 * mpt);
-        const int64_t start = p.start + ((int64_t)kvh * p.units + u) * p.tiles;
         c0 = plan_cta(start, total, G);
         pieces = plan_cta(start + p.tiles - 1, total, G) - c0 + 1;
-        local = in / mpt * kPrefixTile + in % mpt * a.g + h % a.g;
-        tail -= p.blocks * kBlockSize;
     }
-    // record 0: the tail's (if there is one), then the pieces'
-    const int lead = tail > 0 ? 1 : 0, n = lead + pieces;
-    auto rec = [&](int i) -> const float * {
-        if (i < lead) return a.tl.rec + row * kRec;
-        if (i == lead) return a.first + row * kRec;
-        return a.more + ((int64_t)(c0 + i - lead) * 2 * kPrefixTile + local) * kRec;
-    };
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, rec(i)[D]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f, O[kVec];
-#pragma unroll
-    for (int v = 0; v < kVec; ++v) O[v] = 0.f;
-    for (int i = 0; i < n; ++i) {
-        const float *p = rec(i);
-        const float f = p[D] == -INFINITY ? 0.f : ex2(p[D] - M);
-        L = fmaf(f, p[D + 1], L);
-#pragma unroll
-        for (int v = 0; v < kVec; ++v) O[v] = fmaf(f, p[v * 32 + lane], O[v]);
+    if (p.tail == 0) {
+        st = make_float2(-INFINITY, 0.f);
+        O = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    float M = st.x, L = st.y;
+    constexpr int kBatch = 8;
+    for (int i0 = 0; i0 < pieces; i0 += kBatch) {
+        float2 ml[kBatch];
+        float4 x[kBatch];
 #pragma unroll
-    for (int v = 0; v < kVec; ++v) a.out[row * D + v * 32 + lane] = __float2half_rn(L == 0.f ? 0.f : O[v] / L);
+        for (int i = 0; i < kBatch; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+            x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + i < pieces) {
+                const bool first = i0 + i == 0;
+                const Record rec = {
+                    first ? a.first : a.more + (int64_t)(c0 + i0 + i) * 2 * kPrefixTile * (D + 4),
+                    first ? (int64_t)a.B * a.H : 2 * kPrefixTile, first ? at : p.local + j};
+                ml[i] = __ldcg(rec.template stat<D>());
+                x[i] = __ldcg(rec.cols(c4));
+            }
+        }
+        float top = M;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+        auto factor = [&](float m) { return m == -INFINITY ? 0.f : ex2(m - top); };
+        float f = factor(M);
+        M = top;
+        L *= f;
+        O = make_float4(f * O.x, f * O.y, f * O.z, f * O.w);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            f = factor(ml[i].x);
+            L = fmaf(f, ml[i].y, L);
+            O.x = fmaf(f, x[i].x, O.x);
+            O.y = fmaf(f, x[i].y, O.y);
+            O.z = fmaf(f, x[i].z, O.z);
+            O.w = fmaf(f, x[i].w, O.w);
+        }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // (no block in range: 0)
+    *reinterpret_cast<uint2 *>(a.out + row * D + 4 * c4) =
+        make_uint2(pack_half2(O.x * inv, O.y * inv), pack_half2(O.z * inv, O.w * inv));
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -584,9 +629,9 @@ template <int D>
 int launch_shared(const SharedArgs &a, const pa_cache_t *cache, cudaStream_t st) {
     const int rc = launch_prefix<D>(a, cache, st);
     if (rc != PA_OK) return rc;
-    const int64_t rows = (int64_t)a.B * a.H, per = kJoinThreads / 32;
-    launch_dependent(join_kernel<D>, dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinThreads),
-                     0, st, a);
+    const int64_t rows = (int64_t)a.B * a.H;
+    launch_dependent(join_kernel<D>, dim3((unsigned)((rows + 31) / 32), D / 4 / (kJoinThreads / 32)),
+                     dim3(kJoinThreads), 0, st, a);
     return launch_status();
 }
 
@@ -599,8 +644,8 @@ extern "C" size_t pa_decode_shared_workspace_bytes(int num_seqs, int n_heads, in
                                                    int head_dim) {
     if (num_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0) return 0;
     return up256(mode_workspace_bytes(head_dim)) + 256 + up256((size_t)kMaxGroups * sizeof(PlanGroup)) +
-           up256((size_t)num_seqs * 4) + 2 * rows_bytes(num_seqs, n_heads, head_dim) +
-           rows_bytes(kMaxCtas, 2 * kPrefixTile, head_dim);
+           up256((size_t)num_seqs * sizeof(SeqPlan)) + 2 * rows_bytes(num_seqs, n_heads, head_dim) +
+           rows_bytes(kMaxCtas, 2 * kPrefixTile, head_dim) + up256(kMaxCtas * sizeof(PlanCut));
 }
 
 extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int layer,
@@ -631,17 +676,20 @@ extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int laye
     uint8_t *at = static_cast<uint8_t *>(workspace);
     uint8_t *p = at + up256(mode_workspace_bytes(head_dim));
     SharedArgs a = {};
-    a.tl.head = reinterpret_cast<PlanHead *>(p);
+    a.tl.total = reinterpret_cast<int64_t *>(p);
     p += 256;
     a.tl.plan = reinterpret_cast<PlanGroup *>(p);
     p += up256((size_t)kMaxGroups * sizeof(PlanGroup));
-    a.tl.seq_group = reinterpret_cast<int32_t *>(p);
-    p += up256((size_t)num_seqs * 4);
+    a.tl.seqs = reinterpret_cast<SeqPlan *>(p);
+    p += up256((size_t)num_seqs * sizeof(SeqPlan));
     a.tl.rec = reinterpret_cast<float *>(p);
     p += rows_bytes(num_seqs, n_heads, head_dim);
     a.first = reinterpret_cast<float *>(p);
     p += rows_bytes(num_seqs, n_heads, head_dim);
     a.more = reinterpret_cast<float *>(p);
+    p += rows_bytes(kMaxCtas, 2 * kPrefixTile, head_dim);
+    a.tl.cuts = reinterpret_cast<PlanCut *>(p);
+    a.tl.G = G;
     a.tl.groups = {group_starts, shared_blocks, num_groups, max_blocks_per_seq};
     a.q = static_cast<const __half *>(q);
     a.plane_k = layer;
