@@ -427,15 +427,17 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     const int cta = blockIdx.x;
 
     // -------- blocks per sequence (all KV heads) and their prefix sum
-    if constexpr (!kOut) griddep_wait();  // (the lengths may be the kernel before's)
+    // kScores: the lengths may be the kernel before's.  kTails runs beside the
+    // prefix kernel, which lets it start once the work before the call is done and
+    // the plan is written, and takes no more CTAs than find room there.
+    if constexpr (MODE == Mode::kScores) griddep_wait();
+    [[maybe_unused]] int tail_ctas = 0;
     if constexpr (MODE == Mode::kTails) {
-        const int bad = read_groups(a.tl.groups, a.context_lens, B, skip, lens, tid, kThreads);
-        if (bad && cta == 0 && tid == 0) report(a.status, PA_DEV_BAD_LENGTH);
-        if (warp == 1)
-            write_plan(a.tl, skip, lens, a.Hk, a.g, B, bad == 2, lane, cta, (int)gridDim.x);
+        tail_ctas = __ldcg(&a.tl.head->tail_ctas);
+        if (cta >= tail_ctas) return;
     }
     for (int s = tid; s < B; s += kThreads) {
-        [[maybe_unused]] const int ctx = __ldg(a.context_lens + s);
+        const int ctx = MODE == Mode::kTails ? 0 : __ldg(a.context_lens + s);
         int64_t n = 0;
         if constexpr (kOut) {
             if (ctx >= 1 && ctx <= a.maxb * kBlockSize)
@@ -447,6 +449,10 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                 const bool ok = ctx >= 1 && ctx <= a.maxb * kBlockSize && ctx <= a.sc.max_len;
                 if (!ok && cta == 0) report(a.status, PA_DEV_BAD_LENGTH);
                 lens[s] = ok ? ctx : 0;
+            } else {
+                const int2 t = __ldcg(reinterpret_cast<const int2 *>(a.tl.seqs + s));
+                lens[s] = t.x;
+                skip[s] = t.y;
             }
             n = (int64_t)((lens[s] + kBlockSize - 1) / kBlockSize + kCost) * a.Hk;
         }
@@ -497,7 +503,9 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     // With fewer blocks than CTAs only the first W CTAs get a (one-block)
     // range, so that every range is non-empty and a pair cut into pieces
     // counts exactly one arrival per CTA between its first and last.
-    const int G = (int)(W < (int64_t)gridDim.x ? W : (int64_t)gridDim.x);
+    // (kTails: no more CTAs than find room beside the prefix kernel's)
+    const int most = MODE == Mode::kTails ? min(tail_ctas, (int)gridDim.x) : (int)gridDim.x;
+    const int G = (int)(W < (int64_t)most ? W : (int64_t)most);
     if (cta >= G) return;
     const int64_t start = range_start(W, cta, G), end = range_start(W, cta + 1, G);
 
@@ -513,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
         for (int64_t pos = start; pos < end && !abort;) {
             const Segment sg = segment_at<kCost, I8, kShared>(pos, end, prefix, B, seg_lens);
             const int32_t *row = a.block_tables + (int64_t)sg.s * a.maxb + sg.b0;
-            if constexpr (MODE == Mode::kTails) row += max(skip[sg.s], 0);
+            if constexpr (MODE == Mode::kTails) row += skip[sg.s];
             for (int w0 = 0; w0 < sg.nb && !abort; w0 += 32) {
                 const int cnt = min(32, sg.nb - w0);
                 const int my_blk = lane < cnt ? __ldg(row + w0 + lane) : 0;
@@ -564,6 +572,10 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
             for (int i = max(0, gblk - NSTAGE); i < gblk; ++i)
                 mbar_wait(&full[i % NSTAGE], (i / NSTAGE) & 1);
         }
+        // What comes after this kernel waits for it alone: it must not be done
+        // before the prefix kernel is.
+        if constexpr (MODE == Mode::kTails)
+            if (cta == 0) griddep_wait();
         return;
     }
 

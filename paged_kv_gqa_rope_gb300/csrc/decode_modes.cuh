@@ -24,62 +24,59 @@ struct Groups {
     int n, maxb;
 };
 
-// The groups whose prefixes are read once, as the tails' kernel leaves them for
-// the kernels after it.  The prefixes' work lies on a line: group after group,
-// KV head after KV head, unit after unit (2 * (128 / g) sequences: two tiles of
-// 128 query rows), 128-key tile after tile; G CTAs take equal ranges of it.
-struct alignas(16) PlanGroup {
-    int64_t start;  // first tile of the group on the line
-    int tiles;      // key tiles of a unit
-    int blocks;     // blocks shared
-    int s0;         // first sequence
+// A group whose prefix is read once.  The prefixes' work lies on a line: group
+// after group, KV head after KV head, unit after unit (2 * (128 / g) sequences:
+// two tiles of 128 query rows), 128-key tile after tile; G CTAs take equal ranges
+// of it.
+struct PlanGroup {
+    int tiles;    // key tiles of a unit
+    int blocks;   // blocks shared
+    int s0;       // first sequence
     int members;
-    int lead;       // sequence whose block table is read
-    int units;      // units of a KV head
+    int lead;     // sequence whose block table is read
+    int units;    // units of a KV head
 };
-// What the join needs of a sequence.
+// Where a CTA's range begins: in tile t0 of unit `unit` (all KV heads counted) of
+// group `group`, and how many tiles it has.
+struct PlanCut {
+    PlanGroup p;
+    int group, unit, t0;
+    int64_t tiles;
+};
+// What the other two kernels need of a sequence, and of the call.
 struct alignas(16) SeqPlan {
-    int64_t start;   // line: first tile of its unit, of KV head 0
-    int64_t stride;  // tiles from a KV head's unit to the next head's
-    int tiles;       // of its unit
-    int local;       // row of its first Q head (of a KV head) in the unit
+    int tail;        // tokens behind the shared blocks, 0 for a sequence left out
+    int skip;        // shared blocks
     int state;
-    int tail;        // tokens behind the shared blocks
+    int local;       // row of its first Q head (of a KV head) in its unit
+    int64_t start;   // line: first tile of the unit, of KV head 0
+    int64_t stride;  // tiles from a KV head's unit to the next head's
+    int tiles;       // of the unit
+    int pad[3];
 };
 enum : int { kInGroup = 0, kAlone = -1, kLeftOut = -2 };  // SeqPlan::state
-// Where a CTA's range begins: in tile t0 of unit `unit` (all KV heads counted) of
-// group `group` of the plan, and how many tiles it has.  One load, instead of a
-// search and 64-bit divisions at the start of every CTA (5.1 us to the first
-// scores with those).
-struct alignas(16) PlanCut {
-    PlanGroup p;
-    int64_t tiles;
-    int group, unit, t0, pad[3];
+struct alignas(16) PlanHead {
+    int64_t total;  // tiles of the line
+    int ctas;       // CTAs with a range of it
+    int tail_ctas;  // CTAs of the tails' kernel
 };
+
 // Records in the place of the output, over the tokens behind the shared blocks
 // (pa_decode_shared): unnormalised O, then m and l of the row.
 struct DecodeTails {
     float *rec;  // [B][H][D + 4]
-    Groups groups;
-    int64_t *total;   // tiles of the line
-    PlanGroup *plan;  // [groups.n]: the groups with tiles
-    SeqPlan *seqs;    // [B]
-    PlanCut *cuts;    // [G]
-    int G;            // CTAs of the prefix kernel
+    // by the prefix kernel, ahead of its launch_dependents
+    const PlanHead *head;
+    const SeqPlan *seqs;  // [B]
 };
 
 constexpr int kPrefixTile = 128;  // keys of a tile, and query rows
 constexpr int kTileBlocks = kPrefixTile / kBlockSize;
 
-// CTAs with a range (each of one tile at least, so that a unit's pieces are those
-// of neighbouring CTAs), the first tile of CTA c's range, and the CTA whose range
-// holds tile t.
-__device__ __forceinline__ int plan_ctas(int64_t total, int grid) {
-    return (int)min(total, (int64_t)grid);
-}
+// First tile of CTA c's range, and the CTA whose range holds tile t.
 __device__ __forceinline__ int64_t plan_cut(int64_t total, int c, int G) { return total * c / G; }
 __device__ __forceinline__ int plan_cta(int64_t t, int64_t total, int G) {
-    if (total < INT32_MAX / 1024)  // (G <= 160: the sum fits 32 bits)
+    if (total < INT32_MAX / 1024)  // (G < 1024: the sum fits 32 bits)
         return (int)((((uint32_t)t + 1) * (uint32_t)G + (uint32_t)total - 1) / (uint32_t)total) - 1;
     return (int)(((t + 1) * G + total - 1) / total) - 1;
 }
@@ -173,97 +170,75 @@ __device__ __forceinline__ int read_groups(const Groups &g, const int32_t *conte
     return __syncthreads_or(bad) != 0 ? 1 : 0;
 }
 
-// The plan of the groups read_groups has gone over, by one warp of every CTA:
-// CTA 0 writes it down, CTA c the cut of the prefix kernel's CTA c.
-__device__ __forceinline__ void write_plan(const DecodeTails &tl, const int32_t *skip,
-                                           const int32_t *lens, int Hk, int g, int B, bool broken,
-                                           int lane, int cta, int ctas) {
-    const int mpt = kPrefixTile / g, per_unit = 2 * mpt;
-    const bool writes = cta == 0;
-    if (broken) {
-        if (writes) {
-            for (int s = lane; s < B; s += 32) tl.seqs[s].state = kLeftOut;
-            if (lane == 0) *tl.total = 0;
-        }
-        return;
-    }
-    // Groups r0 .. r0 + 31, one a lane, and the tiles that each has of the line.
-    auto load = [&](int r0, PlanGroup &p) -> int64_t {
-        p = PlanGroup{};
-        if (r0 + lane < tl.groups.n) {
-            p.s0 = __ldg(tl.groups.starts + r0 + lane);
-            p.members = __ldg(tl.groups.starts + r0 + lane + 1) - p.s0;
-            p.lead = p.s0;
-            while (p.lead < p.s0 + p.members && skip[p.lead] < 0) ++p.lead;
-            p.blocks = p.lead < p.s0 + p.members ? skip[p.lead] : 0;
-            p.tiles = (p.blocks + kTileBlocks - 1) / kTileBlocks;
-            p.units = (p.members + per_unit - 1) / per_unit;
-        }
-        return (int64_t)p.tiles * p.units * Hk;
-    };
-    auto scan = [&](int64_t x) {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        return x;
-    };
+// Group r's share of the line (tiles 0: none), from global memory.
+__device__ __forceinline__ PlanGroup load_group(const Groups &g, const int32_t *context_lens, int r,
+                                                int per_unit) {
     PlanGroup p;
-    int64_t line = 0;
-    int count = 0;
-    for (int r0 = 0; r0 < tl.groups.n; r0 += 32) {
-        const int64_t mine = load(r0, p), sum = scan(mine);
-        p.start = line + sum - mine;
-        if (writes) {
-            const uint32_t has = __ballot_sync(0xffffffffu, mine > 0);
-            if (mine > 0) tl.plan[count + __popc(has & ((1u << lane) - 1))] = p;
-            count += __popc(has);
-            for (int i = 0; i < min(32, tl.groups.n - r0); ++i) {
-                const int s0 = __shfl_sync(0xffffffffu, p.s0, i);
-                const int m = __shfl_sync(0xffffffffu, p.members, i);
-                SeqPlan q = {};
-                q.start = __shfl_sync(0xffffffffu, p.start, i);
-                q.tiles = __shfl_sync(0xffffffffu, p.tiles, i);
-                q.stride = (int64_t)q.tiles * __shfl_sync(0xffffffffu, p.units, i);
-                for (int s = s0 + lane; s < s0 + m; s += 32) {
-                    const int u = (s - s0) / per_unit, in = s - s0 - u * per_unit;
-                    SeqPlan x = q;
-                    x.start += (int64_t)u * x.tiles;
-                    x.local = in / mpt * kPrefixTile + in % mpt * g;
-                    x.state = skip[s] < 0 ? kLeftOut : q.tiles > 0 ? kInGroup : kAlone;
-                    x.tail = lens[s];
-                    tl.seqs[s] = x;
-                }
-            }
+    p.s0 = __ldg(g.starts + r);
+    p.members = __ldg(g.starts + r + 1) - p.s0;
+    const int named = __ldg(g.blocks + r);
+    p.blocks = named >= 0 && named <= g.maxb ? shared_of(named, p.members) : 0;
+    p.lead = p.s0;
+    if (p.blocks > 0) {
+        // the first sequence in order (as read_groups has it)
+        for (int ctx; p.lead < p.s0 + p.members; ++p.lead) {
+            ctx = __ldg(context_lens + p.lead);
+            if (ctx <= g.maxb * kBlockSize && ctx >= named * kBlockSize) break;
         }
-        line += __shfl_sync(0xffffffffu, sum, 31);
+        if (p.lead == p.s0 + p.members) p.blocks = 0;
     }
-    if (writes && lane == 0) *tl.total = line;
-    // The group that holds a cut, and where the cut lies in it.
-    const int G = plan_ctas(line, tl.G);
-    for (int c = cta; c < G; c += ctas) {
-        const int64_t at = plan_cut(line, c, G);
-        int64_t before = 0;
-        int group = 0;
-        for (int r0 = 0; r0 < tl.groups.n; r0 += 32) {
-            const int64_t mine = load(r0, p), sum = scan(mine);
-            p.start = before + sum - mine;
-            const uint32_t has = __ballot_sync(0xffffffffu, mine > 0);
-            if (p.start <= at && at < p.start + mine) {
-                PlanCut cut = {};
-                cut.p = p;
-                cut.tiles = plan_cut(line, c + 1, G) - at;
-                cut.group = group + __popc(has & ((1u << lane) - 1));
-                cut.unit = (int)((at - p.start) / p.tiles);
-                cut.t0 = (int)((at - p.start) % p.tiles);
-                tl.cuts[c] = cut;
-            }
-            group += __popc(has);
-            before += __shfl_sync(0xffffffffu, sum, 31);
-            if (before > at) break;
+    p.tiles = (p.blocks + kTileBlocks - 1) / kTileBlocks;
+    p.units = (p.members + per_unit - 1) / per_unit;
+    return p;
+}
+
+// How the SMs are divided between the prefixes and the tails, which run side by
+// side: in proportion to what each would take of one SM, in units of a tail's
+// block (8 KB at d = 128, about 0.16 us of an SM's share of the bandwidth).  A key
+// tile is 8 blocks; against two tiles of query rows it takes the tensor cores and
+// the softmax 1.75 us, 11 units.
+constexpr int kTileCost = 8, kPairTileCost = 11;
+
+// By a whole CTA of `threads` threads after read_groups; `sums` are three words of
+// shared memory.  Every CTA comes to the same.  Returns the SMs for the prefixes; total: tiles of their line.
+__device__ __forceinline__ int plan_sms(const Groups &groups, const int32_t *context_lens, int Hk,
+                                        int g, int B, const int32_t *lens, int pair_cost, int sms,
+                                        bool broken, unsigned long long *sums, int tid, int threads,
+                                        int64_t &total) {
+    const int mpt = kPrefixTile / g, per_unit = 2 * mpt;
+    if (tid < 3) sums[tid] = 0;
+    __syncthreads();
+    unsigned long long tail = 0, tiles = 0, cost = 0;
+    for (int s = tid; s < B; s += threads)
+        if (lens[s] > 0) tail += (unsigned)((lens[s] + kBlockSize - 1) / kBlockSize + pair_cost);
+    if (!broken)
+        for (int r = tid; r < groups.n; r += threads) {
+            const PlanGroup p = load_group(groups, context_lens, r, per_unit);
+            const int rest = p.members % per_unit;
+            tiles += (unsigned long long)p.tiles * p.units;
+            cost += (unsigned long long)p.tiles *
+                    (p.members / per_unit * kPairTileCost +
+                     (rest == 0 ? 0 : rest <= mpt ? kTileCost : kPairTileCost));
         }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        tail += __shfl_xor_sync(0xffffffffu, tail, o);
+        tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+        cost += __shfl_xor_sync(0xffffffffu, cost, o);
     }
+    if ((tid & 31) == 0) {
+        atomicAdd(&sums[0], tail);
+        atomicAdd(&sums[1], tiles);
+        atomicAdd(&sums[2], cost);
+    }
+    __syncthreads();
+    tail = sums[0];
+    cost = sums[2];
+    total = (int64_t)sums[1] * Hk;
+    if (cost == 0) return 0;
+    if (tail == 0) return sms;
+    const int n = (int)((double)sms * (double)cost / ((double)cost + (double)tail) + 0.5);
+    return max(1, min(sms - 1, n));
 }
 
 }  // namespace pa

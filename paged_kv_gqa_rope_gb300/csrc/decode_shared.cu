@@ -13,7 +13,10 @@ struct SharedArgs {
     const int32_t *block_tables;
     const int32_t *context_lens;
     __half *out;
-    DecodeTails tl;
+    Groups groups;
+    const float *tails;  // [B * H][D + 4]: records of the tails, in q's order
+    PlanHead *head;
+    SeqPlan *seqs;
     // Records of a unit's first piece, over rows (KV head, sequence, Q head of the
     // KV head), and of the piece with which a CTA's range begins inside a unit, over
     // the rows of two tiles.  Both have four columns of all rows side by side
@@ -36,6 +39,7 @@ constexpr int kMmaWarp = 9;
 constexpr int kPrefixThreads = 11 * 32;
 constexpr int kTmemCols = 512;
 constexpr float kRescale = 8.f;   // the maximum moves only when a tile raises it by more
+constexpr int kTailCost = 10;     // the decode kernel's units for a pair's fixed cost
 constexpr float kShift = 7.f;     // P = 2^(x - m + 7) <= 2^15
 constexpr int kValidRing = 16;    // tiles whose mask of blocks is kept
 
@@ -65,7 +69,7 @@ enum {
     B_EMPTY = 23,
     B_COUNT = 33
 };
-static_assert(B_COUNT * 8 + 4 <= 512, "barrier area");
+static_assert(B_COUNT * 8 + 4 <= 448, "barrier area");
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 
@@ -131,11 +135,13 @@ struct PrefixWalk {
     }
     __device__ __forceinline__ bool next(const SharedArgs &a) {
         if (left <= 0) return false;
+        const int mpt = kPrefixTile / a.g;
         if (unit == seg.p.units * a.Hk) {
-            seg.p = a.tl.plan[++group];
+            do {  // (tiles are left, so a group with some follows)
+                seg.p = load_group(a.groups, a.context_lens, ++group, 2 * mpt);
+            } while (seg.p.tiles == 0);
             unit = 0;
         }
-        const int mpt = kPrefixTile / a.g;
         seg.t0 = t0;
         seg.tiles = (int)min((int64_t)(seg.p.tiles - t0), left);
         seg.kvh = unit / seg.p.units;
@@ -148,6 +154,91 @@ struct PrefixWalk {
     }
 };
 
+// Groups r0 .. r0 + 31, one a lane: the group, its tiles of the line and the sum of
+// those up to it.
+__device__ __forceinline__ int64_t load_groups(const SharedArgs &a, int r0, int lane, PlanGroup &p,
+                                               int64_t &sum) {
+    p = PlanGroup{};
+    if (r0 + lane < a.groups.n)
+        p = load_group(a.groups, a.context_lens, r0 + lane, 2 * (kPrefixTile / a.g));
+    const int64_t mine = (int64_t)p.tiles * p.units * a.Hk;
+    sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+    }
+    return mine;
+}
+
+// By one warp: where this CTA's range begins.
+__device__ __forceinline__ void find_cut(const SharedArgs &a, PlanCut *cut, int64_t total, int G,
+                                         int lane) {
+    const int64_t at = plan_cut(total, blockIdx.x, G);
+    int64_t before = 0;
+    for (int r0 = 0; r0 < a.groups.n && before <= at; r0 += 32) {
+        PlanGroup p;
+        int64_t sum;
+        const int64_t mine = load_groups(a, r0, lane, p, sum);
+        const int64_t start = before + sum - mine;
+        if (start <= at && at < start + mine) {
+            cut->p = p;
+            cut->tiles = plan_cut(total, blockIdx.x + 1, G) - at;
+            cut->group = r0 + lane;
+            if (total < INT32_MAX) {
+                cut->unit = (int)((uint32_t)(at - start) / (uint32_t)p.tiles);
+                cut->t0 = (int)((uint32_t)(at - start) % (uint32_t)p.tiles);
+            } else {
+                cut->unit = (int)((at - start) / p.tiles);
+                cut->t0 = (int)((at - start) % p.tiles);
+            }
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+}
+
+// By one CTA: what the tails' kernel and the join need.
+__device__ __forceinline__ void write_plan(const SharedArgs &a, const int32_t *skip,
+                                           const int32_t *lens, bool broken, int64_t total, int sms,
+                                           int G, int tid) {
+    if (tid == 0) *a.head = {total, G, sms < a.G ? 2 * (a.G - sms) : a.G};
+    const int mpt = kPrefixTile / a.g, per_unit = 2 * mpt, lane = tid & 31;
+    if (broken) {
+        for (int s = tid; s < a.B; s += kPrefixThreads) {
+            SeqPlan x = {};
+            x.state = kLeftOut;
+            a.seqs[s] = x;
+        }
+        return;
+    }
+    int64_t line = 0;
+    for (int r0 = 0; r0 < a.groups.n; r0 += 32) {
+        PlanGroup p;
+        int64_t sum;
+        const int64_t mine = load_groups(a, r0, lane, p, sum), start = line + sum - mine;
+        // (a group a warp)
+        for (int i = tid >> 5; i < min(32, a.groups.n - r0); i += kPrefixThreads / 32) {
+            const int s0 = __shfl_sync(0xffffffffu, p.s0, i);
+            const int m = __shfl_sync(0xffffffffu, p.members, i);
+            SeqPlan q = {};
+            q.start = __shfl_sync(0xffffffffu, start, i);
+            q.tiles = __shfl_sync(0xffffffffu, p.tiles, i);
+            q.stride = (int64_t)q.tiles * __shfl_sync(0xffffffffu, p.units, i);
+            for (int s = s0 + lane; s < s0 + m; s += 32) {
+                const int u = (s - s0) / per_unit, in = s - s0 - u * per_unit;
+                SeqPlan x = q;
+                x.start += (int64_t)u * x.tiles;
+                x.local = in / mpt * kPrefixTile + in % mpt * a.g;
+                x.state = skip[s] < 0 ? kLeftOut : q.tiles > 0 ? kInGroup : kAlone;
+                x.skip = max(skip[s], 0);
+                x.tail = lens[s];
+                a.seqs[s] = x;
+            }
+        }
+        line += __shfl_sync(0xffffffffu, sum, 31);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap qmap,
@@ -159,6 +250,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + B_COUNT);
     uint32_t *valid = reinterpret_cast<uint32_t *>(smem_raw + 512);  // [kValidRing]
     float *stats = reinterpret_cast<float *>(valid + kValidRing);    // [128] m, [128] l
+    unsigned long long *plan_sums = reinterpret_cast<unsigned long long *>(smem_raw + 448);  // [3]
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + L::kMisc + 1023) & ~static_cast<uintptr_t>(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -192,12 +284,37 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     __syncthreads();
     tc::fence_after();
     griddep_wait();
-    griddep_launch_dependents();
+    // The tails' kernel may start once every CTA has come here (the work before the
+    // call is done then) and CTA 0 has written the plan.
+    if (blockIdx.x != 0) griddep_launch_dependents();
     const uint32_t tmem = *tmem_slot;  // S_0 | S_1 | O_0 | O_1
-    PrefixWalk w;
-    w.begin(a.tl.cuts[blockIdx.x]);  // (of a CTA without a range not written: see below)
-    if ((int64_t)blockIdx.x >= *a.tl.total) w.left = 0;
     const int mpt = kPrefixTile / a.g;
+    // ---- the plan, with the room of the tiles for the sequences' lengths
+    PlanCut *cut = reinterpret_cast<PlanCut *>(stats);
+    {
+        int32_t *skip = reinterpret_cast<int32_t *>(smem), *lens = skip + a.B;
+        const int bad = read_groups(a.groups, a.context_lens, a.B, skip, lens, tid, kPrefixThreads);
+        if (bad && blockIdx.x == 0 && tid == 0) report(a.status, PA_DEV_BAD_LENGTH);
+        int64_t total;
+        const int sms = plan_sms(a.groups, a.context_lens, a.Hk, a.g, a.B, lens, kTailCost, a.G,
+                                 bad == 2, plan_sums, tid, kPrefixThreads, total);
+        const int G = (int)min(total, (int64_t)sms);
+        if (tid == 0) cut->tiles = 0;
+        __syncthreads();
+        if (blockIdx.x == 0) {
+            write_plan(a, skip, lens, bad == 2, total, sms, G, tid);
+            __threadfence();
+            __syncthreads();
+            griddep_launch_dependents();
+        }
+        if (warp == 0 && (int)blockIdx.x < G) find_cut(a, cut, total, G, lane);
+        // (the tiles' room was written by the threads, and will be by TMA)
+        tc::fence_proxy_async_smem();
+        __syncthreads();
+    }
+    PrefixWalk w;
+    w.begin(*cut);
+    __syncthreads();  // (stats, where it stood, are free)
     auto s_col = [](int t) { return (uint32_t)(t * kPrefixTile); };
     auto o_col = [](int t) { return (uint32_t)(2 * kPrefixTile + t * D); };
 
@@ -560,18 +677,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SharedArgs a) 
     const int j = (int)at % a.g, s = (int)at / a.g % a.B, kvh = (int)at / a.g / a.B;
     // (the tail's record does not wait for the plan, nor the pieces for each other)
     const int64_t row = (int64_t)s * a.H + kvh * a.g + j;  // of q and out
-    const float *r = a.tl.rec + row * (D + 4);
+    const float *r = a.tails + row * (D + 4);
     float2 st = __ldcg(reinterpret_cast<const float2 *>(r + D));
     float4 O = __ldcg(reinterpret_cast<const float4 *>(r) + c4);
-    const SeqPlan p = a.tl.seqs[s];
-    const int64_t total = *a.tl.total;
+    const SeqPlan p = a.seqs[s];
+    const PlanHead head = *a.head;
     if (p.state == kLeftOut) return;
     int pieces = 0, c0 = 0;
     if (p.state == kInGroup) {
         const int64_t start = p.start + kvh * p.stride;
-        const int G = plan_ctas(total, a.G);
-        c0 = plan_cta(start, total, G);
-        pieces = plan_cta(start + p.tiles - 1, total, G) - c0 + 1;
+        c0 = plan_cta(start, head.total, head.ctas);
+        pieces = plan_cta(start + p.tiles - 1, head.total, head.ctas) - c0 + 1;
     }
     if (p.tail == 0) {
         st = make_float2(-INFINITY, 0.f);
@@ -626,9 +742,7 @@ constexpr int kMaxCtas = 160;  // (152 SMs)
 size_t rows_bytes(int B, int H, int D) { return up256((size_t)B * H * (D + 4) * sizeof(float)); }
 
 template <int D>
-int launch_shared(const SharedArgs &a, const pa_cache_t *cache, cudaStream_t st) {
-    const int rc = launch_prefix<D>(a, cache, st);
-    if (rc != PA_OK) return rc;
+int launch_join(const SharedArgs &a, cudaStream_t st) {
     const int64_t rows = (int64_t)a.B * a.H;
     launch_dependent(join_kernel<D>, dim3((unsigned)((rows + 31) / 32), D / 4 / (kJoinThreads / 32)),
                      dim3(kJoinThreads), 0, st, a);
@@ -643,9 +757,8 @@ using namespace pa;
 extern "C" size_t pa_decode_shared_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads,
                                                    int head_dim) {
     if (num_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0) return 0;
-    return up256(mode_workspace_bytes(head_dim)) + 256 + up256((size_t)kMaxGroups * sizeof(PlanGroup)) +
-           up256((size_t)num_seqs * sizeof(SeqPlan)) + 2 * rows_bytes(num_seqs, n_heads, head_dim) +
-           rows_bytes(kMaxCtas, 2 * kPrefixTile, head_dim) + up256(kMaxCtas * sizeof(PlanCut));
+    return up256(mode_workspace_bytes(head_dim)) + 256 + up256((size_t)num_seqs * sizeof(SeqPlan)) + 2 * rows_bytes(num_seqs, n_heads, head_dim) +
+           rows_bytes(kMaxCtas, 2 * kPrefixTile, head_dim);
 }
 
 extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int layer,
@@ -676,21 +789,17 @@ extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int laye
     uint8_t *at = static_cast<uint8_t *>(workspace);
     uint8_t *p = at + up256(mode_workspace_bytes(head_dim));
     SharedArgs a = {};
-    a.tl.total = reinterpret_cast<int64_t *>(p);
+    a.head = reinterpret_cast<PlanHead *>(p);
     p += 256;
-    a.tl.plan = reinterpret_cast<PlanGroup *>(p);
-    p += up256((size_t)kMaxGroups * sizeof(PlanGroup));
-    a.tl.seqs = reinterpret_cast<SeqPlan *>(p);
+    a.seqs = reinterpret_cast<SeqPlan *>(p);
     p += up256((size_t)num_seqs * sizeof(SeqPlan));
-    a.tl.rec = reinterpret_cast<float *>(p);
+    float *const tails = reinterpret_cast<float *>(p);
+    a.tails = tails;
     p += rows_bytes(num_seqs, n_heads, head_dim);
     a.first = reinterpret_cast<float *>(p);
     p += rows_bytes(num_seqs, n_heads, head_dim);
     a.more = reinterpret_cast<float *>(p);
-    p += rows_bytes(kMaxCtas, 2 * kPrefixTile, head_dim);
-    a.tl.cuts = reinterpret_cast<PlanCut *>(p);
-    a.tl.G = G;
-    a.tl.groups = {group_starts, shared_blocks, num_groups, max_blocks_per_seq};
+    a.groups = {group_starts, shared_blocks, num_groups, max_blocks_per_seq};
     a.q = static_cast<const __half *>(q);
     a.plane_k = layer;
     a.plane_v = cache->layers + layer;
@@ -710,9 +819,10 @@ extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int laye
     const DecodeCall c = {q,        cache,   layer,      block_tables, max_blocks_per_seq,
                           context_lens, num_seqs, n_heads, n_kv_heads, head_dim,
                           scale,    out,     dev_status, st};
-    const int rc2 = launch_decode_tails(c, at, a.tl);
+    int rc2 = head_dim == 128 ? launch_prefix<128>(a, cache, st) : launch_prefix<64>(a, cache, st);
+    if (rc2 == PA_OK) rc2 = launch_decode_tails(c, at, DecodeTails{tails, a.head, a.seqs});
     if (rc2 != PA_OK) return rc2;
-    return head_dim == 128 ? launch_shared<128>(a, cache, st) : launch_shared<64>(a, cache, st);
+    return head_dim == 128 ? launch_join<128>(a, st) : launch_join<64>(a, st);
 }
 
 extern "C" int pa_prepare_shared(int num_seqs, const int32_t *block_tables,
