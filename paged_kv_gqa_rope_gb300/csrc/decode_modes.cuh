@@ -26,8 +26,9 @@ struct Groups {
 
 // A group whose prefix is read once.  The prefixes' work lies on a line: group
 // after group, KV head after KV head, unit after unit (2 * (128 / g) sequences:
-// two tiles of 128 query rows), 128-key tile after tile; G CTAs take equal ranges
-// of it.
+// two tiles of 128 query rows), 128-key tile after tile and kUnitCost places for a
+// unit's fixed cost (its Q, the ring's start, its record: about 4 us, without which
+// CTAs with several short units end last); G CTAs take equal ranges of it.
 struct PlanGroup {
     int tiles;    // key tiles of a unit
     int blocks;   // blocks shared
@@ -36,12 +37,12 @@ struct PlanGroup {
     int lead;     // sequence whose block table is read
     int units;    // units of a KV head
 };
-// Where a CTA's range begins: in tile t0 of unit `unit` (all KV heads counted) of
-// group `group`, and how many tiles it has.
+// Where a CTA's range begins: at place t0 of unit `unit` (all KV heads counted) of
+// group `group`, and how many places it has.
 struct PlanCut {
     PlanGroup p;
     int group, unit, t0;
-    int64_t tiles;
+    int64_t places;
 };
 // What the other two kernels need of a sequence, and of the call.
 struct alignas(16) SeqPlan {
@@ -49,14 +50,14 @@ struct alignas(16) SeqPlan {
     int skip;        // shared blocks
     int state;
     int local;       // row of its first Q head (of a KV head) in its unit
-    int64_t start;   // line: first tile of the unit, of KV head 0
-    int64_t stride;  // tiles from a KV head's unit to the next head's
+    int64_t start;   // line: first place of the unit, of KV head 0
+    int64_t stride;  // places from a KV head's unit to the next head's
     int tiles;       // of the unit
     int pad[3];
 };
 enum : int { kInGroup = 0, kAlone = -1, kLeftOut = -2 };  // SeqPlan::state
 struct alignas(16) PlanHead {
-    int64_t total;  // tiles of the line
+    int64_t total;  // places of the line
     int ctas;       // CTAs with a range of it
     int tail_ctas;  // CTAs of the tails' kernel
 };
@@ -73,10 +74,17 @@ struct DecodeTails {
 constexpr int kPrefixTile = 128;  // keys of a tile, and query rows
 constexpr int kTileBlocks = kPrefixTile / kBlockSize;
 
-// First tile of CTA c's range, and the CTA whose range holds tile t.
-__device__ __forceinline__ int64_t plan_cut(int64_t total, int c, int G) { return total * c / G; }
+constexpr int kUnitCost = 2;
+
+// First place of CTA c's range, and the CTA whose range holds place t.  (32-bit
+// divisions for all but absurd lines: G < 1024, so their operands fit.)
+constexpr int kShortLine = INT32_MAX / 1024;
+__device__ __forceinline__ int64_t plan_cut(int64_t total, int c, int G) {
+    if (total < kShortLine) return (uint32_t)total * (uint32_t)c / (uint32_t)G;
+    return total * c / G;
+}
 __device__ __forceinline__ int plan_cta(int64_t t, int64_t total, int G) {
-    if (total < INT32_MAX / 1024)  // (G < 1024: the sum fits 32 bits)
+    if (total < kShortLine)
         return (int)((((uint32_t)t + 1) * (uint32_t)G + (uint32_t)total - 1) / (uint32_t)total) - 1;
     return (int)(((t + 1) * G + total - 1) / total) - 1;
 }
@@ -194,41 +202,44 @@ __device__ __forceinline__ PlanGroup load_group(const Groups &g, const int32_t *
 
 // How the SMs are divided between the prefixes and the tails, which run side by
 // side: in proportion to what each would take of one SM, in units of a tail's
-// block (8 KB at d = 128, about 0.16 us of an SM's share of the bandwidth).  A key
-// tile is 8 blocks; against two tiles of query rows it takes the tensor cores and
-// the softmax 1.75 us, 11 units.
-constexpr int kTileCost = 8, kPairTileCost = 11;
+// block (8 KB at d = 128, about 0.14 us with two decode CTAs an SM).  A key tile
+// (64 KB) takes 1.56 us against one tile of query rows, 2.1 against two.
+constexpr int kTileCost = 11, kPairTileCost = 15;
 
-// By a whole CTA of `threads` threads after read_groups; `sums` are three words of
-// shared memory.  Every CTA comes to the same.  Returns the SMs for the prefixes; total: tiles of their line.
+// By a whole CTA of `threads` threads after read_groups; `sums` are four words of
+// shared memory.  Every CTA comes to the same.  Returns the SMs for the prefixes; total: places of their line.
 __device__ __forceinline__ int plan_sms(const Groups &groups, const int32_t *context_lens, int Hk,
                                         int g, int B, const int32_t *lens, int pair_cost, int sms,
                                         bool broken, unsigned long long *sums, int tid, int threads,
                                         int64_t &total) {
     const int mpt = kPrefixTile / g, per_unit = 2 * mpt;
-    if (tid < 3) sums[tid] = 0;
+    if (tid < 4) sums[tid] = 0;
     __syncthreads();
-    unsigned long long tail = 0, tiles = 0, cost = 0;
+    unsigned long long tail = 0, places = 0, cost = 0, alone = 0;  // alone: units, groups
     for (int s = tid; s < B; s += threads)
         if (lens[s] > 0) tail += (unsigned)((lens[s] + kBlockSize - 1) / kBlockSize + pair_cost);
     if (!broken)
         for (int r = tid; r < groups.n; r += threads) {
             const PlanGroup p = load_group(groups, context_lens, r, per_unit);
             const int rest = p.members % per_unit;
-            tiles += (unsigned long long)p.tiles * p.units;
-            cost += (unsigned long long)p.tiles *
+            if (p.tiles == 0) continue;
+            places += (unsigned long long)(p.tiles + kUnitCost) * p.units;
+            cost += (unsigned long long)(p.tiles + kUnitCost) *
                     (p.members / per_unit * kPairTileCost +
                      (rest == 0 ? 0 : rest <= mpt ? kTileCost : kPairTileCost));
+            alone += (unsigned long long)p.units << 32 | 1;
         }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         tail += __shfl_xor_sync(0xffffffffu, tail, o);
-        tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+        places += __shfl_xor_sync(0xffffffffu, places, o);
+        alone += __shfl_xor_sync(0xffffffffu, alone, o);
         cost += __shfl_xor_sync(0xffffffffu, cost, o);
     }
     if ((tid & 31) == 0) {
         atomicAdd(&sums[0], tail);
-        atomicAdd(&sums[1], tiles);
+        atomicAdd(&sums[1], places);
+        atomicAdd(&sums[3], alone);
         atomicAdd(&sums[2], cost);
     }
     __syncthreads();
@@ -236,9 +247,21 @@ __device__ __forceinline__ int plan_sms(const Groups &groups, const int32_t *con
     cost = sums[2];
     total = (int64_t)sums[1] * Hk;
     if (cost == 0) return 0;
-    if (tail == 0) return sms;
-    const int n = (int)((double)sms * (double)cost / ((double)cost + (double)tail) + 0.5);
-    return max(1, min(sms - 1, n));
+    int n = sms, most = sms;
+    if (tail > 0) {
+        most = sms - 1;
+        n = max(1, min(most, (int)((float)sms * (float)cost / ((float)cost + (float)tail) + 0.5f)));
+    }
+    // Of one group every unit is alike: a multiple of them cuts none but at its ends.
+    alone = sums[3];
+    if ((uint32_t)alone == 1) {
+        const int64_t units = (int64_t)(alone >> 32) * Hk;
+        if (units <= most) {
+            const int u = (int)units, even = max(1, (n + u / 2) / u) * u;
+            n = even <= most ? even : even - u;
+        }
+    }
+    return n;
 }
 
 }  // namespace pa

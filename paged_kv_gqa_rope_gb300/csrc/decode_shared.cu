@@ -123,45 +123,47 @@ struct PrefixSegment {
 
 // Walks a CTA's range; every role has its own.
 struct PrefixWalk {
-    int64_t left;  // tiles to go
+    int64_t left;  // places to go
     int group, unit, t0;
     PrefixSegment seg;
     __device__ __forceinline__ void begin(const PlanCut &c) {
         seg.p = c.p;
-        left = c.tiles;
+        left = c.places;
         group = c.group;
         unit = c.unit;
         t0 = c.t0;
     }
     __device__ __forceinline__ bool next(const SharedArgs &a) {
-        if (left <= 0) return false;
         const int mpt = kPrefixTile / a.g;
-        if (unit == seg.p.units * a.Hk) {
-            do {  // (tiles are left, so a group with some follows)
-                seg.p = load_group(a.groups, a.context_lens, ++group, 2 * mpt);
-            } while (seg.p.tiles == 0);
-            unit = 0;
+        while (left > 0) {
+            if (unit == seg.p.units * a.Hk) {
+                do {  // (places are left, so a group with some follows)
+                    seg.p = load_group(a.groups, a.context_lens, ++group, 2 * mpt);
+                } while (seg.p.tiles == 0);
+                unit = 0;
+            }
+            seg.t0 = t0;
+            seg.tiles = (int)min((int64_t)(seg.p.tiles - t0), left);
+            seg.kvh = unit / seg.p.units;
+            seg.member0 = (unit - seg.kvh * seg.p.units) * 2 * mpt;
+            seg.pair = seg.p.members - seg.member0 > mpt;
+            left -= seg.p.tiles + kUnitCost - t0;  // (negative where the range ends inside)
+            ++unit;
+            t0 = 0;
+            if (seg.tiles > 0) return true;  // (else the range begins in a unit's cost)
         }
-        seg.t0 = t0;
-        seg.tiles = (int)min((int64_t)(seg.p.tiles - t0), left);
-        seg.kvh = unit / seg.p.units;
-        seg.member0 = (unit - seg.kvh * seg.p.units) * 2 * mpt;
-        seg.pair = seg.p.members - seg.member0 > mpt;
-        left -= seg.tiles;
-        ++unit;
-        t0 = 0;
-        return true;
+        return false;
     }
 };
 
-// Groups r0 .. r0 + 31, one a lane: the group, its tiles of the line and the sum of
-// those up to it.
+// Groups r0 .. r0 + 31, one a lane: the group, its places of the line and the sum
+// of those up to it.
 __device__ __forceinline__ int64_t load_groups(const SharedArgs &a, int r0, int lane, PlanGroup &p,
                                                int64_t &sum) {
     p = PlanGroup{};
     if (r0 + lane < a.groups.n)
         p = load_group(a.groups, a.context_lens, r0 + lane, 2 * (kPrefixTile / a.g));
-    const int64_t mine = (int64_t)p.tiles * p.units * a.Hk;
+    const int64_t mine = p.tiles > 0 ? (int64_t)(p.tiles + kUnitCost) * p.units * a.Hk : 0;
     sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -182,16 +184,13 @@ __device__ __forceinline__ void find_cut(const SharedArgs &a, PlanCut *cut, int6
         const int64_t mine = load_groups(a, r0, lane, p, sum);
         const int64_t start = before + sum - mine;
         if (start <= at && at < start + mine) {
+            const int span = p.tiles + kUnitCost;
             cut->p = p;
-            cut->tiles = plan_cut(total, blockIdx.x + 1, G) - at;
+            cut->places = plan_cut(total, blockIdx.x + 1, G) - at;
             cut->group = r0 + lane;
-            if (total < INT32_MAX) {
-                cut->unit = (int)((uint32_t)(at - start) / (uint32_t)p.tiles);
-                cut->t0 = (int)((uint32_t)(at - start) % (uint32_t)p.tiles);
-            } else {
-                cut->unit = (int)((at - start) / p.tiles);
-                cut->t0 = (int)((at - start) % p.tiles);
-            }
+            cut->unit = (int)(total < kShortLine ? (uint32_t)(at - start) / (uint32_t)span
+                                                 : (at - start) / span);
+            cut->t0 = (int)(at - start - (int64_t)cut->unit * span);
         }
         before += __shfl_sync(0xffffffffu, sum, 31);
     }
@@ -223,11 +222,11 @@ __device__ __forceinline__ void write_plan(const SharedArgs &a, const int32_t *s
             SeqPlan q = {};
             q.start = __shfl_sync(0xffffffffu, start, i);
             q.tiles = __shfl_sync(0xffffffffu, p.tiles, i);
-            q.stride = (int64_t)q.tiles * __shfl_sync(0xffffffffu, p.units, i);
+            q.stride = (int64_t)(q.tiles + kUnitCost) * __shfl_sync(0xffffffffu, p.units, i);
             for (int s = s0 + lane; s < s0 + m; s += 32) {
                 const int u = (s - s0) / per_unit, in = s - s0 - u * per_unit;
                 SeqPlan x = q;
-                x.start += (int64_t)u * x.tiles;
+                x.start += (int64_t)u * (x.tiles + kUnitCost);
                 x.local = in / mpt * kPrefixTile + in % mpt * a.g;
                 x.state = skip[s] < 0 ? kLeftOut : q.tiles > 0 ? kInGroup : kAlone;
                 x.skip = max(skip[s], 0);
@@ -299,7 +298,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         const int sms = plan_sms(a.groups, a.context_lens, a.Hk, a.g, a.B, lens, kTailCost, a.G,
                                  bad == 2, plan_sums, tid, kPrefixThreads, total);
         const int G = (int)min(total, (int64_t)sms);
-        if (tid == 0) cut->tiles = 0;
+        if (tid == 0) cut->places = 0;
         __syncthreads();
         if (blockIdx.x == 0) {
             write_plan(a, skip, lens, bad == 2, total, sms, G, tid);
