@@ -28,7 +28,9 @@ struct Groups {
 // after group, KV head after KV head, unit after unit (2 * (128 / g) sequences:
 // two tiles of 128 query rows), 128-key tile after tile and kUnitCost places for a
 // unit's fixed cost (its Q, the ring's start, its record: about 4 us, without which
-// CTAs with several short units end last); G CTAs take equal ranges of it.
+// CTAs with several short units end last).  A tile has `weight` places: three
+// (1.56 us) against one tile of query rows, four (2.1 us) against two.  G CTAs take
+// equal ranges of the line; a tile belongs to the range of its first place.
 struct PlanGroup {
     int tiles;    // key tiles of a unit
     int blocks;   // blocks shared
@@ -36,6 +38,8 @@ struct PlanGroup {
     int members;
     int lead;     // sequence whose block table is read
     int units;    // units of a KV head
+    int weight;
+    __device__ __forceinline__ int span() const;  // places of a unit
 };
 // Where a CTA's range begins: at place t0 of unit `unit` (all KV heads counted) of
 // group `group`, and how many places it has.
@@ -52,7 +56,7 @@ struct alignas(16) SeqPlan {
     int local;       // row of its first Q head (of a KV head) in its unit
     int64_t start;   // line: first place of the unit, of KV head 0
     int64_t stride;  // places from a KV head's unit to the next head's
-    int tiles;       // of the unit
+    int last;        // first place of the unit's last tile, from the unit's first
     int pad[3];
 };
 enum : int { kInGroup = 0, kAlone = -1, kLeftOut = -2 };  // SeqPlan::state
@@ -74,7 +78,15 @@ struct DecodeTails {
 constexpr int kPrefixTile = 128;  // keys of a tile, and query rows
 constexpr int kTileBlocks = kPrefixTile / kBlockSize;
 
-constexpr int kUnitCost = 2;
+constexpr int kUnitCost = 6, kTileWeight = 3, kPairWeight = 4;
+__device__ __forceinline__ int PlanGroup::span() const { return tiles * weight + kUnitCost; }
+
+// CTAs with a range: each of kPairWeight places at least, so that it has a tile of
+// every unit that goes on through it and a unit's pieces are those of neighbouring
+// CTAs.
+__device__ __forceinline__ int plan_ctas(int64_t total, int sms) {
+    return (int)min(total / kPairWeight, (int64_t)sms);
+}
 
 // First place of CTA c's range, and the CTA whose range holds place t.  (32-bit
 // divisions for all but absurd lines: G < 1024, so their operands fit.)
@@ -197,36 +209,32 @@ __device__ __forceinline__ PlanGroup load_group(const Groups &g, const int32_t *
     }
     p.tiles = (p.blocks + kTileBlocks - 1) / kTileBlocks;
     p.units = (p.members + per_unit - 1) / per_unit;
+    p.weight = p.members > per_unit / 2 ? kPairWeight : kTileWeight;
     return p;
 }
 
 // How the SMs are divided between the prefixes and the tails, which run side by
 // side: in proportion to what each would take of one SM, in units of a tail's
-// block (8 KB at d = 128, about 0.14 us with two decode CTAs an SM).  A key tile
-// (64 KB) takes 1.56 us against one tile of query rows, 2.1 against two.
-constexpr int kTileCost = 11, kPairTileCost = 15;
+// block (8 KB at d = 128, about 0.14 us with two decode CTAs an SM).
+constexpr int kTileCost = 11;  // of kTileWeight places
 
-// By a whole CTA of `threads` threads after read_groups; `sums` are four words of
+// By a whole CTA of `threads` threads after read_groups; `sums` are three words of
 // shared memory.  Every CTA comes to the same.  Returns the SMs for the prefixes; total: places of their line.
 __device__ __forceinline__ int plan_sms(const Groups &groups, const int32_t *context_lens, int Hk,
                                         int g, int B, const int32_t *lens, int pair_cost, int sms,
                                         bool broken, unsigned long long *sums, int tid, int threads,
                                         int64_t &total) {
-    const int mpt = kPrefixTile / g, per_unit = 2 * mpt;
-    if (tid < 4) sums[tid] = 0;
+    const int per_unit = 2 * (kPrefixTile / g);
+    if (tid < 3) sums[tid] = 0;
     __syncthreads();
-    unsigned long long tail = 0, places = 0, cost = 0, alone = 0;  // alone: units, groups
+    unsigned long long tail = 0, places = 0, alone = 0;  // alone: units, groups
     for (int s = tid; s < B; s += threads)
         if (lens[s] > 0) tail += (unsigned)((lens[s] + kBlockSize - 1) / kBlockSize + pair_cost);
     if (!broken)
         for (int r = tid; r < groups.n; r += threads) {
             const PlanGroup p = load_group(groups, context_lens, r, per_unit);
-            const int rest = p.members % per_unit;
             if (p.tiles == 0) continue;
-            places += (unsigned long long)(p.tiles + kUnitCost) * p.units;
-            cost += (unsigned long long)(p.tiles + kUnitCost) *
-                    (p.members / per_unit * kPairTileCost +
-                     (rest == 0 ? 0 : rest <= mpt ? kTileCost : kPairTileCost));
+            places += (unsigned long long)p.span() * p.units;
             alone += (unsigned long long)p.units << 32 | 1;
         }
 #pragma unroll
@@ -234,26 +242,24 @@ __device__ __forceinline__ int plan_sms(const Groups &groups, const int32_t *con
         tail += __shfl_xor_sync(0xffffffffu, tail, o);
         places += __shfl_xor_sync(0xffffffffu, places, o);
         alone += __shfl_xor_sync(0xffffffffu, alone, o);
-        cost += __shfl_xor_sync(0xffffffffu, cost, o);
     }
     if ((tid & 31) == 0) {
         atomicAdd(&sums[0], tail);
         atomicAdd(&sums[1], places);
-        atomicAdd(&sums[3], alone);
-        atomicAdd(&sums[2], cost);
+        atomicAdd(&sums[2], alone);
     }
     __syncthreads();
     tail = sums[0];
-    cost = sums[2];
     total = (int64_t)sums[1] * Hk;
-    if (cost == 0) return 0;
+    if (total == 0) return 0;
     int n = sms, most = sms;
     if (tail > 0) {
         most = sms - 1;
-        n = max(1, min(most, (int)((float)sms * (float)cost / ((float)cost + (float)tail) + 0.5f)));
+        const float cost = (float)sums[1] * ((float)kTileCost / kTileWeight);
+        n = max(1, min(most, (int)((float)sms * cost / (cost + (float)tail) + 0.5f)));
     }
     // Of one group every unit is alike: a multiple of them cuts none but at its ends.
-    alone = sums[3];
+    alone = sums[2];
     if ((uint32_t)alone == 1) {
         const int64_t units = (int64_t)(alone >> 32) * Hk;
         if (units <= most) {

@@ -142,15 +142,18 @@ struct PrefixWalk {
                 } while (seg.p.tiles == 0);
                 unit = 0;
             }
-            seg.t0 = t0;
-            seg.tiles = (int)min((int64_t)(seg.p.tiles - t0), left);
+            // the tiles whose first place is in the range
+            const int wt = seg.p.weight;
+            seg.t0 = (int)((uint32_t)(t0 + wt - 1) / (uint32_t)wt);
+            const int64_t end = t0 + left < seg.p.span() ? (t0 + left + wt - 1) / wt : seg.p.tiles;
+            seg.tiles = (int)min(end, (int64_t)seg.p.tiles) - seg.t0;
             seg.kvh = unit / seg.p.units;
             seg.member0 = (unit - seg.kvh * seg.p.units) * 2 * mpt;
             seg.pair = seg.p.members - seg.member0 > mpt;
-            left -= seg.p.tiles + kUnitCost - t0;  // (negative where the range ends inside)
+            left -= seg.p.span() - t0;  // (negative where the range ends inside)
             ++unit;
             t0 = 0;
-            if (seg.tiles > 0) return true;  // (else the range begins in a unit's cost)
+            if (seg.tiles > 0) return true;  // (else it begins behind the unit's last tile)
         }
         return false;
     }
@@ -163,7 +166,7 @@ __device__ __forceinline__ int64_t load_groups(const SharedArgs &a, int r0, int 
     p = PlanGroup{};
     if (r0 + lane < a.groups.n)
         p = load_group(a.groups, a.context_lens, r0 + lane, 2 * (kPrefixTile / a.g));
-    const int64_t mine = p.tiles > 0 ? (int64_t)(p.tiles + kUnitCost) * p.units * a.Hk : 0;
+    const int64_t mine = p.tiles > 0 ? (int64_t)p.span() * p.units * a.Hk : 0;
     sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -184,7 +187,7 @@ __device__ __forceinline__ void find_cut(const SharedArgs &a, PlanCut *cut, int6
         const int64_t mine = load_groups(a, r0, lane, p, sum);
         const int64_t start = before + sum - mine;
         if (start <= at && at < start + mine) {
-            const int span = p.tiles + kUnitCost;
+            const int span = p.span();
             cut->p = p;
             cut->places = plan_cut(total, blockIdx.x + 1, G) - at;
             cut->group = r0 + lane;
@@ -221,14 +224,16 @@ __device__ __forceinline__ void write_plan(const SharedArgs &a, const int32_t *s
             const int m = __shfl_sync(0xffffffffu, p.members, i);
             SeqPlan q = {};
             q.start = __shfl_sync(0xffffffffu, start, i);
-            q.tiles = __shfl_sync(0xffffffffu, p.tiles, i);
-            q.stride = (int64_t)(q.tiles + kUnitCost) * __shfl_sync(0xffffffffu, p.units, i);
+            const int tiles = __shfl_sync(0xffffffffu, p.tiles, i);
+            const int span = __shfl_sync(0xffffffffu, p.span(), i);
+            q.last = (tiles - 1) * __shfl_sync(0xffffffffu, p.weight, i);
+            q.stride = (int64_t)span * __shfl_sync(0xffffffffu, p.units, i);
             for (int s = s0 + lane; s < s0 + m; s += 32) {
                 const int u = (s - s0) / per_unit, in = s - s0 - u * per_unit;
                 SeqPlan x = q;
-                x.start += (int64_t)u * (x.tiles + kUnitCost);
+                x.start += (int64_t)u * span;
                 x.local = in / mpt * kPrefixTile + in % mpt * a.g;
-                x.state = skip[s] < 0 ? kLeftOut : q.tiles > 0 ? kInGroup : kAlone;
+                x.state = skip[s] < 0 ? kLeftOut : tiles > 0 ? kInGroup : kAlone;
                 x.skip = max(skip[s], 0);
                 x.tail = lens[s];
                 a.seqs[s] = x;
@@ -297,7 +302,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         int64_t total;
         const int sms = plan_sms(a.groups, a.context_lens, a.Hk, a.g, a.B, lens, kTailCost, a.G,
                                  bad == 2, plan_sums, tid, kPrefixThreads, total);
-        const int G = (int)min(total, (int64_t)sms);
+        const int G = plan_ctas(total, sms);
         if (tid == 0) cut->places = 0;
         __syncthreads();
         if (blockIdx.x == 0) {
@@ -686,7 +691,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SharedArgs a) 
     if (p.state == kInGroup) {
         const int64_t start = p.start + kvh * p.stride;
         c0 = plan_cta(start, head.total, head.ctas);
-        pieces = plan_cta(start + p.tiles - 1, head.total, head.ctas) - c0 + 1;
+        pieces = plan_cta(start + p.last, head.total, head.ctas) - c0 + 1;
     }
     if (p.tail == 0) {
         st = make_float2(-INFINITY, 0.f);
