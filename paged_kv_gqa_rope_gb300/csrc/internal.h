@@ -25,7 +25,7 @@ inline bool ranges_overlap(const void *a, uint64_t na, const void *b, uint64_t n
     return x < y ? y - x < na : x - y < nb;
 }
 
-inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+__host__ __device__ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline bool cache_ok(const pa_cache_t *c, int layer, int n_kv_heads, int head_dim) {
     return c && c->base && aligned16(c->base) && c->block_size == kBlockSize &&

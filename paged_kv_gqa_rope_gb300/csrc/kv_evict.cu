@@ -5,25 +5,29 @@
 // `sinks`, the last `recent` and, of the others, the m = k - sinks - recent of
 // the largest weight, of equal ones the first.  Two kernels:
 //
-//   select  one CTA per (sequence, KV head).  The m-th largest weight among the
-//           others is found digit by digit (11 + 11 + 10 bits of a key that
-//           orders like the weights): a histogram of the digit over the keys
-//           that agree on the digits before it, and the digit at which the count
-//           from the top passes m.  Then one pass in token order: token t is kept
-//           if its key is larger, or equal and among the first of the equal ones
-//           that still have room; the tokens kept before it give its new place i.
-//           Weights move there, and the row's move (slot of t -> slot of i) goes
-//           into the (sequence, KV head)'s list unless it stays where it is.
+//   select  one CTA per (sequence, KV head), or where there are few of them a
+//           cluster of up to eight, which keep the weights in registers (those past
+//           262144 tokens are read again).  The m-th largest weight among
+//           the others is found digit by digit (11 + 11 + 10 bits of a key that
+//           orders like the weights): a histogram of the digit over the keys that
+//           agree on the digits before it, and the digit at which the count from the
+//           top passes m.  Then one sum in token order of the larger keys and of the
+//           equal ones: token t's new place is the number of larger ones before it
+//           and of the equal ones as far as they have room.  Weights move there, and
+//           the list of the (sequence, KV head) gets the row's move, slot of t ->
+//           slot of the place (or none, where it stays).
 //   move    streams the rows of the lists, K and V, one CTA per (sequence, KV
 //           head, plane, column slice).  In place a row's new place can be
-//           another row's old one.  The list is in order and i <= t, so a store
-//           can only hit rows that moves up to its own have read: a CTA loads a
-//           round of moves, waits for all of its threads, and stores them; the
-//           next round's loads are issued ahead of the stores.  Columns are
-//           independent of each other, so slices need no order between them.
+//           another row's old one.  The list is in order and no place lies behind
+//           its token, so a store can only hit rows that moves up to its own have
+//           read: a CTA loads a round of moves, waits for all of its threads, and
+//           stores them; the next round's loads are issued ahead of the stores.
+//           Columns are independent of each other, so slices need no order between
+//           them.  Into other blocks no order is needed at all, and the rounds of a
+//           list are dealt out to several CTAs.
 //
 // Bound: HBM, 8 d bytes a kept (token, KV head) that moves; for single sequences
-// the select kernel's passes over few CTAs.
+// the latency of the select kernel's few CTAs.
 #include <algorithm>
 #include <mutex>
 
@@ -33,12 +37,15 @@
 namespace pa {
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelItems = 4;  // consecutive tokens of a thread in the ordered pass
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelItems = 4;  // consecutive tokens of a thread in a chunk
+constexpr int kChunk = kSelThreads * kSelItems;
 constexpr int kDigits = 2048;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
 constexpr int kMaxSeqs = 4096;
+constexpr int kMaxCluster = 8;
 
 struct EvictArgs {
     const int32_t *block_tables;
@@ -47,7 +54,7 @@ struct EvictArgs {
     float *weights_out;
     const int32_t *out_tables;
     int32_t *out_lens;
-    int32_t *moved;  // [B][Hk] moves of each list
+    int32_t *moved;  // [B][Hk] length of each list, ~length where some rows stay in their blocks
     int32_t *kept;   // [B] new lengths, -1: sequence left out
     int2 *moves;     // [B][Hk][cap] {from, to} slots
     __half *kplane;
@@ -64,195 +71,334 @@ __device__ __forceinline__ uint32_t key_of(float w) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Exclusive sum of v over the CTA's threads and its total (all threads call).
-__device__ __forceinline__ int block_scan(int v, int *sm, int &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+// Inclusive sum over a warp's lanes.
+template <typename T>
+__device__ __forceinline__ T warp_sums(T x, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    __syncthreads();  // sm of an earlier call is read
-    if (lane == 31) sm[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int y = sm[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += z;
-        }
-        sm[lane] = y;
-    }
-    __syncthreads();
-    total = sm[kSelThreads / 32 - 1];
-    return x - v + (warp ? sm[warp - 1] : 0);
+    return x;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
+// Larger keys in the low half, equal ones in the high half (both fit: a list has at
+// most INT32_MAX tokens).
+using Counts = unsigned long long;
+
+// The cluster's barrier (of all threads; orders shared and global memory within the
+// cluster), this CTA's place in it, and a word of another CTA's shared memory.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ int ld_cluster(const int *p, uint32_t rank) {
+    uint32_t at;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// (four words, 16-byte aligned)
+__device__ __forceinline__ int4 ld_cluster4(const int *p, uint32_t rank) {
+    uint32_t at;
+    int4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+
+// C chunks of tokens a CTA stay in registers.  `size` CTAs (a cluster) work on a
+// list, each on `slice` tokens of it; with one CTA the last chunks may go on in
+// memory.
+template <int C>
+__global__ void __launch_bounds__(kSelThreads, C > 4 ? 1 : 2)
+    evict_select_kernel(const EvictArgs a, int size) {
     griddep_launch_dependents();
     griddep_wait();
-    __shared__ int hist[kDigits];
-    __shared__ int scan[32];
-    __shared__ int found[2];
-    const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
+    __shared__ __align__(16) int hist[3][kDigits];
+    __shared__ Counts sums[C * kSelWarps];
+    __shared__ int warp_total[kSelWarps];
+    __shared__ int found[2], mine_of[2];
+    const int h = blockIdx.x / size, s = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = size > 1 ? (int)cluster_rank() : 0;
     const int64_t pair = (int64_t)s * a.Hk + h;
     const int n = a.context_lens[s];
     const int k = min(n, a.budget);
     const bool ok = n >= 0 && n <= a.maxb * kBlockSize && n <= a.stride &&
                     (int64_t)k <= (int64_t)a.out_maxb * kBlockSize;
-    if (tid == 0) {
-        if (h == 0) a.kept[s] = ok ? k : -1;
-        if (!ok) {
+    if (tid == 0 && h == 0 && rank == 0) a.kept[s] = ok ? k : -1;
+    if (!ok) {
+        if (tid == 0 && rank == 0) {
             if (h == 0) report(a.status, PA_DEV_BAD_LENGTH);
             a.moved[pair] = 0;
         }
+        return;
     }
-    if (!ok) return;
     const float *w = a.weights + pair * a.stride;
     float *w_out = a.weights_out + pair * a.stride;
-
-    // ---- the m-th largest key of tokens [lo, hi), and how many equal to it to keep
-    const bool all = n <= a.budget;
-    const int lo = all ? 0 : a.sinks, hi = all ? 0 : n - a.recent;
-    uint32_t limit = 0;
-    int equal = 0;
-    if (!all) {
-        int want = k - a.sinks - a.recent;  // of the hi - lo > want tokens
-        uint32_t mask = 0;
-        equal = want;
-        for (int shift = 21; want > 0; shift = shift == 21 ? 10 : 0) {
-            const int bits = shift == 0 ? 10 : 11;
-            for (int i = tid; i < kDigits; i += kSelThreads) hist[i] = 0;
-            __syncthreads();
-            for (unsigned t = lo + tid; t < (unsigned)hi; t += kSelThreads) {
-                const uint32_t key = key_of(w[t]);
-                if ((key & mask) == limit) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1);
-            }
-            __syncthreads();
-            // thread i holds the digits 2047 - 2i and 2046 - 2i: counts from the top
-            const int d0 = kDigits - 1 - 2 * tid;
-            const int c0 = hist[d0], c1 = hist[d0 - 1];
-            int total;
-            const int before = block_scan(c0 + c1, scan, total);
-            if (before < want && want <= before + c0) {
-                found[0] = d0;
-                found[1] = want - before;
-            } else if (before + c0 < want && want <= before + c0 + c1) {
-                found[0] = d0 - 1;
-                found[1] = want - before - c0;
-            }
-            __syncthreads();
-            limit |= (uint32_t)found[0] << shift;
-            mask |= ((1u << bits) - 1) << shift;
-            equal = want = found[1];
-            __syncthreads();
-            if (shift == 0) break;
-        }
-        if (k == a.sinks + a.recent) limit = 0xffffffffu;  // (no key is that large)
-    }
-
-    // ---- the ordered pass
     const int32_t *row = a.block_tables + (int64_t)s * a.maxb;
     const int32_t *out_row = a.out_tables + (int64_t)s * a.out_maxb;
     int2 *list = a.moves + pair * a.cap;
-    int places = 0, ties = 0, count = 0;  // so far: kept, equal ones met, moves listed
-    for (unsigned t0 = 0; t0 < (unsigned)n; t0 += kSelThreads * kSelItems) {
-        float x[kSelItems];
-        int keep[kSelItems], eq[kSelItems];
-        int nk = 0, ne = 0;
+    // this CTA's tokens: first .. last - 1
+    const unsigned slice = size > 1 ? ((n + size - 1) / size + 3) & ~3u : (unsigned)n;
+    const unsigned first = min((unsigned)n, rank * slice), last = min((unsigned)n, first + slice);
+
+    // A thread's tokens of the chunk that begins at c0.
+    const bool wide = a.stride % 4 == 0 && aligned16(a.weights);
+    auto load = [&](unsigned c0, float (&x)[kSelItems]) {
+        const unsigned t = c0 + tid * kSelItems;
+        if (wide && t + kSelItems <= last) {
+            const float4 v = *reinterpret_cast<const float4 *>(w + t);
+            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        } else {
 #pragma unroll
-        for (int j = 0; j < kSelItems; ++j) {
-            const unsigned t = t0 + tid * kSelItems + j;
-            x[j] = t < (unsigned)n ? w[t] : 0.f;
-            const uint32_t key = key_of(x[j]);
-            const bool other = t >= (unsigned)lo && t < (unsigned)hi;
-            eq[j] = other && key == limit;
-            keep[j] = t < (unsigned)n && (all || !other || key > limit);
-            nk += keep[j];
-            ne += eq[j];
+            for (int j = 0; j < kSelItems; ++j) x[j] = t + j < last ? w[t + j] : 0.f;
         }
-        // equal ones first: which of them still have room (both counts in one sum)
-        int total;
-        const int base = block_scan(ne, scan, total);
-        int e = ties + base;
-        ties += total;
+    };
+    float x[C][kSelItems];
 #pragma unroll
-        for (int j = 0; j < kSelItems; ++j) {
-            if (eq[j] && e < equal) {
-                keep[j] = 1;
-                ++nk;
-            }
-            e += eq[j];
-        }
-        int i = places + block_scan(nk, scan, total);
-        places += total;
-        int2 mv[kSelItems];
-        int nm = 0;
+    for (int c = 0; c < C; ++c) load(first + c * kChunk, x[c]);
+    for (int i = tid; i < 3 * kDigits; i += kSelThreads) (&hist[0][0])[i] = 0;
+    // (does any kept row's block stand in both tables?)
+    int same = 0;
+    for (int j = tid; j < (k + kBlockSize - 1) / kBlockSize; j += kSelThreads)
+        same |= row[j] == out_row[j];
+    same = __syncthreads_or(same);
+
+    // ---- the m-th largest key of tokens [lo, hi), and how many equal to it to keep
+    const bool all = n <= a.budget;
+    const unsigned lo = max(first, all ? 0 : a.sinks), hi = min(last, all ? 0 : n - a.recent);
+    uint32_t limit = 0xffffffffu;  // (no key is that large)
+    int equal = 0;
+    if (!all && k > a.sinks + a.recent) {
+        int want = k - a.sinks - a.recent;  // of more than that many tokens
+        uint32_t mask = 0;
+        limit = 0;
+#pragma unroll 1
+        for (int d = 0; d < 3; ++d) {
+            const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+            const uint32_t digit = d == 2 ? 1023 : 2047;
+            auto count = [&](unsigned c0, const float (&y)[kSelItems]) {
 #pragma unroll
-        for (int j = 0; j < kSelItems; ++j) {
-            const unsigned t = t0 + tid * kSelItems + j;
-            mv[j] = make_int2(-1, -1);
-            if (!keep[j]) continue;
-            // (every weight of this round has been read: the sums above wait for all)
-            w_out[i] = x[j];
-            const int src = row[t / kBlockSize], dst = out_row[i / kBlockSize];
-            if (src < 0 || src >= a.num_blocks || dst < 0 || dst >= a.num_blocks) {
-                report(a.status, PA_DEV_BAD_BLOCK);
-            } else {
-                const int from = src * kBlockSize + (int)(t % kBlockSize);
-                const int to = dst * kBlockSize + i % kBlockSize;
-                if (from != to) {
-                    mv[j] = make_int2(from, to);
-                    ++nm;
+                for (int j = 0; j < kSelItems; ++j) {
+                    const unsigned t = c0 + tid * kSelItems + j;
+                    const uint32_t key = key_of(y[j]);
+                    if (t >= lo && t < hi && (key & mask) == limit)
+                        atomicAdd(&hist[d][(key >> shift) & digit], 1);
                 }
-            }
-            ++i;
-        }
-        int c = count + block_scan(nm, scan, total);
-        count += total;
+            };
 #pragma unroll
-        for (int j = 0; j < kSelItems; ++j)
-            if (mv[j].x >= 0) list[c++] = mv[j];
+            for (int c = 0; c < C; ++c) count(first + c * kChunk, x[c]);
+            for (unsigned c0 = first + C * kChunk; c0 < hi; c0 += kChunk) {
+                float y[kSelItems];
+                load(c0, y);
+                count(c0, y);
+            }
+            // thread i holds four digits, from the top: 2047 - 4 i and down
+            constexpr int kPer = kDigits / kSelThreads;
+            static_assert(kPer == 4, "a vector of four");
+            int cnt[kPer] = {}, mine = 0;
+            if (size > 1) {
+                cluster_sync();
+                int4 all_of[kMaxCluster];
+#pragma unroll
+                for (int q = 0; q < kMaxCluster; ++q)
+                    all_of[q] = q < size ? ld_cluster4(&hist[d][kDigits - kPer * (tid + 1)], q)
+                                         : make_int4(0, 0, 0, 0);
+#pragma unroll
+                for (int q = 0; q < kMaxCluster; ++q) {
+                    cnt[0] += all_of[q].w;
+                    cnt[1] += all_of[q].z;
+                    cnt[2] += all_of[q].y;
+                    cnt[3] += all_of[q].x;
+                }
+            } else {
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) cnt[j] = hist[d][kDigits - 1 - kPer * tid - j];
+            }
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) mine += cnt[j];
+            const int upto = warp_sums(mine, lane);
+            if (lane == 31) warp_total[warp] = upto;
+            __syncthreads();
+            int before = upto - mine;
+#pragma unroll
+            for (int v = 0; v < kSelWarps; ++v) before += v < warp ? warp_total[v] : 0;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                if (before < want && want <= before + cnt[j]) {
+                    found[0] = kDigits - 1 - kPer * tid - j;
+                    found[1] = want - before;
+                }
+                before += cnt[j];
+            }
+            __syncthreads();
+            limit |= (uint32_t)found[0] << shift;
+            mask |= digit << shift;
+            equal = want = found[1];
+            // (barriers of the next digit come before found and warp_total change)
+        }
     }
-    for (unsigned t = k + tid; t < (unsigned)n; t += kSelThreads) w_out[t] = 0.f;
-    if (tid == 0) a.moved[pair] = count;
+
+    // ---- new places
+    auto counts = [&](unsigned c0, const float (&y)[kSelItems]) -> Counts {
+        Counts v = 0;
+#pragma unroll
+        for (int j = 0; j < kSelItems; ++j) {
+            const unsigned t = c0 + tid * kSelItems + j;
+            const uint32_t key = key_of(y[j]);
+            const bool other = t >= lo && t < hi;
+            if (t < last) v += other && key == limit ? (Counts)1 << 32
+                               : all || !other || key > limit ? 1 : 0;
+        }
+        return v;
+    };
+    // The chunk's kept tokens, `v` counted before this thread's.
+    auto place = [&](unsigned c0, const float (&y)[kSelItems], Counts v) {
+        unsigned larger = (unsigned)v;
+        int ties = (int)(v >> 32);
+#pragma unroll
+        for (int j = 0; j < kSelItems; ++j) {
+            const unsigned t = c0 + tid * kSelItems + j;
+            if (t >= last) break;
+            const uint32_t key = key_of(y[j]);
+            const bool other = t >= lo && t < hi;
+            const bool tie = other && key == limit;
+            const unsigned i = larger + min(ties, equal);
+            const bool keep = tie ? ties < equal : all || !other || key > limit;
+            ties += tie;
+            larger += keep && !tie;
+            if (!keep) continue;
+            w_out[i] = y[j];
+            list[i].x = (int)t;
+        }
+    };
+    Counts v[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const Counts mine = counts(first + c * kChunk, x[c]), upto = warp_sums(mine, lane);
+        if (lane == 31) sums[c * kSelWarps + warp] = upto;
+        v[c] = upto - mine;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        Counts carry = 0;
+        for (int i0 = 0; i0 < C * kSelWarps; i0 += 32) {
+            const Counts mine = i0 + lane < C * kSelWarps ? sums[i0 + lane] : 0;
+            const Counts upto = warp_sums(mine, lane);
+            if (i0 + lane < C * kSelWarps) sums[i0 + lane] = carry + upto - mine;
+            carry += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        if (lane == 0) mine_of[0] = (int)(unsigned)carry, mine_of[1] = (int)(carry >> 32);
+    }
+    // (behind this barrier every weight in registers has been read: its places in
+    // `weights` may be written)
+    Counts base = 0;
+    if (size > 1) {
+        cluster_sync();
+        for (int q = 0; q < rank; ++q)
+            base += (Counts)(unsigned)ld_cluster(&mine_of[0], q) |
+                    (Counts)(unsigned)ld_cluster(&mine_of[1], q) << 32;
+    } else {
+        __syncthreads();
+    }
+    if (tid == 0 && rank == 0) a.moved[pair] = same ? ~k : k;
+#pragma unroll
+    for (int c = 0; c < C; ++c) place(first + c * kChunk, x[c], base + sums[c * kSelWarps + warp] + v[c]);
+    Counts total = (Counts)(unsigned)mine_of[0] | (Counts)(unsigned)mine_of[1] << 32;
+    for (unsigned c0 = first + C * kChunk; c0 < last; c0 += kChunk) {  // (one CTA)
+        float y[kSelItems];
+        load(c0, y);
+        const Counts mine = counts(c0, y), upto = warp_sums(mine, lane);
+        __syncthreads();  // sums of the chunk before are read
+        if (lane == 31) sums[warp] = upto;
+        __syncthreads();  // (and this chunk's weights)
+        Counts before = total + upto - mine;
+        for (int u = 0; u < kSelWarps; ++u) {
+            before += u < warp ? sums[u] : 0;
+            total += sums[u];
+        }
+        place(c0, y, before);
+    }
+    const unsigned me = rank * kSelThreads + tid, everyone = size * kSelThreads;
+    for (unsigned t = k + me; t < (unsigned)n; t += everyone) w_out[t] = 0.f;
+
+    // ---- tokens to slots, apart from the places: so the block ids' loads do not wait
+    // for each other
+    if (size > 1)
+        cluster_sync();  // (and the last reads of another CTA's shared memory are done)
+    else
+        __syncthreads();
+#pragma unroll 4
+    for (unsigned i = me; i < (unsigned)k; i += everyone) {
+        const int t = list[i].x;
+        const int src = row[t / kBlockSize], dst = out_row[i / kBlockSize];
+        int2 mv = make_int2(-1, -1);
+        if (src < 0 || src >= a.num_blocks || dst < 0 || dst >= a.num_blocks) {
+            report(a.status, PA_DEV_BAD_BLOCK);
+        } else {
+            const int from = src * kBlockSize + t % kBlockSize;
+            const int to = dst * kBlockSize + (int)(i % kBlockSize);
+            if (from != to) mv = make_int2(from, to);
+        }
+        list[i] = mv;
+    }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int slices) {
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int slices,
+                                                                  int parts) {
     // (No launch_dependents: this kernel writes the new lengths, and pa_decode
     // reads its lengths ahead of its wait for the kernel before.)
     griddep_wait();
-    const int h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x;
+    const int h = blockIdx.y, s = blockIdx.z / parts, part = blockIdx.z % parts, tid = threadIdx.x;
     const int64_t pair = (int64_t)s * a.Hk + h;
-    if (blockIdx.x == 0 && h == 0 && tid == 0 && a.kept[s] >= 0) a.out_lens[s] = a.kept[s];
-    const unsigned n = a.moved[pair];
+    if (blockIdx.x == 0 && h == 0 && part == 0 && tid == 0 && a.kept[s] >= 0) a.out_lens[s] = a.kept[s];
+    const int moved = a.moved[pair];
+    if (moved < 0 && part > 0) return;  // in place: one CTA, in order
+    const unsigned n = moved < 0 ? ~moved : moved;
     __half *plane = blockIdx.x & 1 ? a.vplane : a.kplane;
     const int width = D / 8 / slices;  // 16-byte pieces of a slice
     const int rows = kMoveThreads / width, r = tid / width;
     uint4 *base = reinterpret_cast<uint4 *>(plane) + (blockIdx.x >> 1) * width + tid % width;
     const int2 *list = a.moves + pair * a.cap;
-    const int round = rows * kMoveUnroll;
+    const unsigned round = rows * kMoveUnroll, step = moved < 0 ? round : parts * round;
 
     auto at = [&](int slot) { return base + ((int64_t)slot * a.Hk + h) * (D / 8); };
+    int2 mv[kMoveUnroll];  // of the round after the one in x
     uint4 x[kMoveUnroll];
     int to[kMoveUnroll];
-    auto load = [&](unsigned i0) {
+    auto moves = [&](unsigned i0) {
 #pragma unroll
         for (int j = 0; j < kMoveUnroll; ++j) {
             const unsigned i = i0 + j * rows + r;
-            to[j] = -1;
-            if (i < n) {
-                const int2 mv = list[i];
-                to[j] = mv.y;
-                x[j] = *at(mv.x);
-            }
+            mv[j] = i < n ? list[i] : make_int2(-1, -1);
         }
     };
-    load(0);
-    for (unsigned i0 = 0; i0 < n; i0 += round) {
+    auto load = [&]() {
+#pragma unroll
+        for (int j = 0; j < kMoveUnroll; ++j) {
+            to[j] = mv[j].y;
+            if (mv[j].x >= 0) x[j] = *at(mv[j].x);
+        }
+    };
+    unsigned i0 = part * round;
+    moves(i0);
+    load();
+    moves(i0 + step);
+    for (; i0 < n; i0 += step) {
         uint4 y[kMoveUnroll];
         int yt[kMoveUnroll];
 #pragma unroll
@@ -261,11 +407,29 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
             yt[j] = to[j];
         }
         __syncthreads();  // this round's rows are read
-        load(i0 + round);
+        load();
+        moves(i0 + 2 * step);
 #pragma unroll
         for (int j = 0; j < kMoveUnroll; ++j)
             if (yt[j] >= 0) *at(yt[j]) = y[j];
     }
+}
+
+template <int C>
+void launch_select(const EvictArgs &a, int size, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.Hk * size, a.B);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = size;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = size > 1 ? 2 : 1;
+    cudaLaunchKernelEx(&cfg, evict_select_kernel<C>, a, size);  // (errors: launch_status)
 }
 
 size_t header_bytes(int B, int Hk) {
@@ -338,18 +502,33 @@ extern "C" int pa_kv_evict(const pa_cache_t *cache, int layer, const int32_t *bl
     a.cap = cap;
     a.num_blocks = cache->num_blocks;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    launch_dependent(evict_select_kernel, dim3(n_kv_heads, num_seqs), dim3(kSelThreads), 0, st, a);
+    // As many CTAs a list as find an SM each, of a chunk of tokens at least, and
+    // registers for the tokens that a table row can hold, as far as they go.
+    const int longest = max_blocks_per_seq * kBlockSize;
+    int size = 1;
+    while (size < kMaxCluster && size * kChunk < longest &&
+           (int64_t)2 * size * n_kv_heads * num_seqs <= sm_count())
+        size *= 2;
+    if (longest / size > 16 * kChunk - 4) size = 1;  // (a cluster keeps all in registers)
+    const int64_t each = ((int64_t)longest + size - 1) / size + 3;
+    if (each <= kChunk)
+        launch_select<1>(a, size, st);
+    else if (each <= 4 * kChunk)
+        launch_select<4>(a, size, st);
+    else
+        launch_select<16>(a, size, st);
     const int rc = launch_status();
     if (rc != PA_OK) return rc;
-    // Whole rows where that already gives a CTA to every SM, else slices down to
-    // 64 bytes (two DRAM sectors).
+    // Whole rows where that already gives several CTAs to every SM, else slices down
+    // to 64 bytes (two DRAM sectors), and parts of the lists.
+    const int64_t want = 2 * (int64_t)sm_count(), lists = 2 * (int64_t)n_kv_heads * num_seqs;
     int slices = 1;
-    while (slices < head_dim / 32 && (int64_t)2 * slices * n_kv_heads * num_seqs < 4 * sm_count())
-        slices *= 2;
-    const dim3 grid(2 * slices, n_kv_heads, num_seqs);
+    while (slices < head_dim / 32 && slices * lists < want) slices *= 2;
+    const int parts = (int)std::min<int64_t>(8, std::max<int64_t>(1, want / (slices * lists)));
+    const dim3 grid(2 * slices, n_kv_heads, num_seqs * parts);
     if (head_dim == 128)
-        launch_dependent(evict_move_kernel<128>, grid, dim3(kMoveThreads), 0, st, a, slices);
+        launch_dependent(evict_move_kernel<128>, grid, dim3(kMoveThreads), 0, st, a, slices, parts);
     else
-        launch_dependent(evict_move_kernel<64>, grid, dim3(kMoveThreads), 0, st, a, slices);
+        launch_dependent(evict_move_kernel<64>, grid, dim3(kMoveThreads), 0, st, a, slices, parts);
     return launch_status();
 }

@@ -525,7 +525,8 @@ class EvictBatch(WeightBatch):
 
 EVICT = [([1], 1, 0, 0), ([40, 0, 1, 33], 16, 2, 5), ([700, 200, 256, 257], 256, 4, 64),
          ([9000, 100], 1000, 4, 256), ([300], 299, 0, 299), ([300, 5000], 300, 300, 0),
-         ([5000], 4999, 0, 0), ([20000], 1, 0, 0), ([4096, 4097, 8192], 2048, 1, 1), ([64] * 50, 10, 0, 3)]
+         ([5000], 4999, 0, 0), ([20000], 1, 0, 0), ([4096, 4097, 8192], 2048, 1, 1), ([64] * 50, 10, 0, 3),
+         ([70000], 3000, 0, 7), ([40000] + [20] * 79, 500, 4, 64)]
 
 
 @pytest.mark.parametrize("H,Hk,d", [(2, 2, 64), (8, 8, 128), (1, 1, 128)])
