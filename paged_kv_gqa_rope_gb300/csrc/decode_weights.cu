@@ -16,7 +16,8 @@
 namespace pa {
 namespace {
 
-constexpr int kWeightThreads = 256;
+constexpr int kWeightThreads = 128;
+constexpr int kWeightTokens = 4;
 
 struct WeightArgs {
     DecodeScores sc;
@@ -27,27 +28,60 @@ struct WeightArgs {
     int H, Hk;
 };
 
-// grid (chunks of tokens, Hk, B); one thread a token at a time.
+// grid (chunks of tokens, Hk, B).  A thread has kWeightTokens tokens at a time, all
+// their loads in flight together with the statistics' (a token at a time: 12 us of
+// the serving batch of 64/8 heads and 4097 tokens).
 template <int G>
 __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightArgs a) {
     griddep_wait();
     griddep_launch_dependents();
     const int h = blockIdx.y, s = blockIdx.z;
     const int64_t first = a.sc.first[s];
-    if (first < 0) return;
     const int n = a.context_lens[s];
-    float2 st[G];
-#pragma unroll
-    for (int j = 0; j < G; ++j) st[j] = a.sc.stats[(int64_t)s * a.H + h * G + j];
+    if (first < 0) return;
+    const float2 *stats = a.sc.stats + (int64_t)s * a.H + h * G;
     const float *x =
         a.sc.scores + (first + (int64_t)((n + kBlockSize - 1) / kBlockSize) * h) * kBlockSize * G;
     const int64_t row = ((int64_t)s * a.Hk + h) * a.stride;
-    for (int64_t t = blockIdx.x * kWeightThreads + threadIdx.x; t < n;
-         t += (int64_t)gridDim.x * kWeightThreads) {
-        float w = 0.f;
+    constexpr int kStep = kWeightThreads * kWeightTokens;
+    for (int64_t t0 = (int64_t)blockIdx.x * kStep; t0 < n; t0 += (int64_t)gridDim.x * kStep) {
+        float v[kWeightTokens][G], w[kWeightTokens];
 #pragma unroll
-        for (int j = 0; j < G; ++j) w += ex2(__ldcs(x + t * G + j) - st[j].x) * st[j].y;
-        a.weights_out[row + t] = a.weights ? a.weights[row + t] + w : w;
+        for (int i = 0; i < kWeightTokens; ++i) {
+            const int64_t t = t0 + i * kWeightThreads + threadIdx.x;
+            w[i] = 0.f;
+            if (t < n) {
+                if constexpr (G % 4 == 0) {
+#pragma unroll
+                    for (int j = 0; j < G; j += 4) {
+                        const float4 y = __ldcs(reinterpret_cast<const float4 *>(x + t * G + j));
+                        v[i][j] = y.x, v[i][j + 1] = y.y, v[i][j + 2] = y.z, v[i][j + 3] = y.w;
+                    }
+                } else if constexpr (G % 2 == 0) {
+#pragma unroll
+                    for (int j = 0; j < G; j += 2) {
+                        const float2 y = __ldcs(reinterpret_cast<const float2 *>(x + t * G + j));
+                        v[i][j] = y.x, v[i][j + 1] = y.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < G; ++j) v[i][j] = __ldcs(x + t * G + j);
+                }
+                if (a.weights) w[i] = a.weights[row + t];
+            }
+        }
+        float p[kWeightTokens] = {};
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            const float2 st = stats[j];
+#pragma unroll
+            for (int i = 0; i < kWeightTokens; ++i) p[i] = fmaf(ex2(v[i][j] - st.x), st.y, p[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kWeightTokens; ++i) {
+            const int64_t t = t0 + i * kWeightThreads + threadIdx.x;
+            if (t < n) a.weights_out[row + t] = w[i] + p[i];
+        }
     }
 }
 
@@ -121,8 +155,9 @@ extern "C" int pa_decode_weights(const void *q, const pa_cache_t *cache, int lay
     // CTAs for the longest row the table allows, as long as they are few
     const int64_t pairs = (int64_t)num_seqs * n_kv_heads;
     const int64_t longest = (int64_t)max_blocks_per_seq * kBlockSize;
-    const int64_t chunks = std::min((longest + kWeightThreads - 1) / kWeightThreads,
-                                    std::max<int64_t>(1, (16 * (int64_t)sm_count() + pairs - 1) / pairs));
+    constexpr int kStep = kWeightThreads * kWeightTokens;
+    const int64_t chunks = std::min((longest + kStep - 1) / kStep,
+                                    std::max<int64_t>(1, (32 * (int64_t)sm_count() + pairs - 1) / pairs));
     const dim3 grid((unsigned)chunks, n_kv_heads, num_seqs), block_dim(kWeightThreads);
     switch (n_heads / n_kv_heads) {
 #define PA_CASE(G) \
