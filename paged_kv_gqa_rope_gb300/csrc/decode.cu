@@ -593,11 +593,18 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
             pos += sg.nu;
             continue;
         }
-        [[maybe_unused]] float *scores = nullptr;  // of the pair's first token
+        // This lane's place in the scores of the warp's block, and which of its two
+        // heads it stores: none, the first, both at once (g even) or one by one.
+        [[maybe_unused]] float *sc_at = nullptr;
+        [[maybe_unused]] int sc_heads = 0;
         if constexpr (MODE == Mode::kScores) {
             const int64_t at = scores_start<kCost>(a, prefix, lens, s, nullptr);
-            if (at >= 0)
-                scores = a.sc.scores + (at + (sg.pair_end - sg.pair_start) * kvh) * kBlockSize * a.g;
+            if (at >= 0 && h0 < a.g) {
+                sc_at = a.sc.scores +
+                        ((at + (sg.pair_end - sg.pair_start) * kvh + b0 + warp) * kBlockSize + head) * a.g +
+                        h0;
+                sc_heads = (a.g & 1) == 0 ? 2 : h0 + 1 < a.g ? 3 : 1;
+            }
         }
 
         // Q^T fragments (B operand).  fp16 cache: Q[head][16kk + 2*quad + {0,1}]
@@ -788,9 +795,10 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
             } else {
                 if constexpr (MODE == Mode::kScores) {
                     // a block out of range takes part in nothing
-                    if (bad && scores != nullptr)
-                        for (int i = lane; i < kBlockSize * a.g; i += 32)
-                            scores[(int64_t)(b0 + j) * kBlockSize * a.g + i] = -INFINITY;
+                    if (bad && sc_heads != 0) {
+                        sc_at[0] = sc_at[8 * a.g] = -INFINITY;
+                        if (sc_heads > 1) sc_at[1] = sc_at[8 * a.g + 1] = -INFINITY;
+                    }
                 }
                 if (!bad) {
                     const uint32_t vt = kt + L::kTileBytes;
@@ -808,22 +816,15 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                     if (tok + 8 >= ctx) x2 = x3 = -INFINITY;
                     if constexpr (MODE == Mode::kScores) {
                         // the block's scores [16 tokens][g heads], padding tokens' too
-                        if (scores != nullptr) {
-                            float *r = scores + (int64_t)tok * a.g + h0;
-                            if ((a.g & 1) == 0) {
-                                if (h0 < a.g) {
-                                    *reinterpret_cast<float2 *>(r) = make_float2(x0, x1);
-                                    *reinterpret_cast<float2 *>(r + 8 * a.g) = make_float2(x2, x3);
-                                }
-                            } else {
-                                if (h0 < a.g) {
-                                    r[0] = x0;
-                                    r[8 * a.g] = x2;
-                                }
-                                if (h0 + 1 < a.g) {
-                                    r[1] = x1;
-                                    r[8 * a.g + 1] = x3;
-                                }
+                        if (sc_heads == 2) {
+                            *reinterpret_cast<float2 *>(sc_at) = make_float2(x0, x1);
+                            *reinterpret_cast<float2 *>(sc_at + 8 * a.g) = make_float2(x2, x3);
+                        } else if (sc_heads != 0) {
+                            sc_at[0] = x0;
+                            sc_at[8 * a.g] = x2;
+                            if (sc_heads == 3) {
+                                sc_at[1] = x1;
+                                sc_at[8 * a.g + 1] = x3;
                             }
                         }
                     }
@@ -888,6 +889,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                     mbar_arrive(&empty[stage]);
                 }
             }
+            if constexpr (MODE == Mode::kScores) sc_at += kConsumerWarps * kBlockSize * a.g;
         }
         // A timed-out wait leaves the ring out of step: every consumer warp
         // learns of it at the barrier below and the CTA stops after this segment.
