@@ -32,11 +32,14 @@ struct SharedArgs {
 // ------------------------------------------------------------------ prefixes
 
 // Roles: warps 0-3 and 4-7 the softmax of stream 0 and 1 (thread = query row =
-// TMEM lane), warp 8 the TMA producer, warp 9 the MMA issuer (one thread) and owner
-// of the TMEM.
+// TMEM lane), warp 8 the TMA producer of the Q and K tiles, warp 11 of the V tiles
+// (a copy of 2 KB takes its thread about 70 cycles: with one producer a tile of 64 KB
+// took 2.2 us), warps 9 and 10 the MMA issuers of stream 0 and 1 (one thread each;
+// warp 9 owns the TMEM).
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
-constexpr int kPrefixThreads = 10 * 32;
+constexpr int kVProducerWarp = 11;
+constexpr int kPrefixThreads = 12 * 32;
 constexpr int kTmemCols = 512;
 constexpr float kRescale = 8.f;   // the maximum moves only when a tile raises it by more
 constexpr int kTailCost = 10;     // the decode kernel's units for a pair's fixed cost
@@ -47,9 +50,10 @@ template <int D>
 struct PrefixLayout {
     static constexpr int kHalf = kPrefixTile * 128;    // 64 columns of a tile
     static constexpr int kTileBytes = kHalf * (D / 64);
-    static constexpr int kStages = D == 128 ? 5 : 10;  // K and V tiles in turn
-    static constexpr int kRing = 2 * kTileBytes;       // behind two Q tiles
-    static constexpr int kBytes = kRing + kStages * kTileBytes;
+    static constexpr int kKStages = D == 128 ? 3 : 5, kVStages = D == 128 ? 2 : 5;
+    static constexpr int kK = 2 * kTileBytes;  // behind two Q tiles
+    static constexpr int kV = kK + kKStages * kTileBytes;
+    static constexpr int kBytes = kV + kVStages * kTileBytes;
     // barriers and small arrays, at most 1008 bytes to the 1024-byte boundary of
     // the tiles (the window starts 16-byte aligned)
     static constexpr int kMisc = 512 + kValidRing * 4 + 2 * kPrefixTile * 4;
@@ -58,16 +62,19 @@ struct PrefixLayout {
 
 enum {
     B_QFULL = 0,
-    B_QEMPTY = 1,  // the segment's last scores done
+    B_QEMPTY = 1,  // both issuers: the segment's last scores done
     B_SFULL = 2,   // per stream: a score tile written
     B_PREADY = 4,  // per stream: its P written
     B_OUNIT = 6,   // per stream: the segment's last P.V done
     B_OFREE = 8,   // per stream: O read out
     B_STATS = 10,  // stream 1's row statistics written
-    B_DRAIN = 11,
-    B_FULL = 12,   // ring stages
-    B_EMPTY = 22,
-    B_COUNT = 32
+    B_DRAIN = 11,  // per stream
+    B_TURN = 13,   // per stream: the other issuer's turn is over
+    B_KFULL = 15,  // up to 5 stages each
+    B_KEMPTY = 20,
+    B_VFULL = 25,
+    B_VEMPTY = 30,
+    B_COUNT = 35
 };
 static_assert(B_COUNT * 8 + 4 <= 448, "barrier area");
 
@@ -247,7 +254,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kvmap, const SharedArgs a) {
     using L = PrefixLayout<D>;
-    constexpr int NS = L::kStages;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem_raw);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar + B_COUNT);
@@ -260,18 +266,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 
     if (tid == 0) {
         mbar_init(&bar[B_QFULL], 1);
-        mbar_init(&bar[B_QEMPTY], 1);
+        mbar_init(&bar[B_QEMPTY], 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar[B_SFULL + i], 1);
             mbar_init(&bar[B_PREADY + i], 128);
             mbar_init(&bar[B_OUNIT + i], 1);
             mbar_init(&bar[B_OFREE + i], 128);
+            mbar_init(&bar[B_DRAIN + i], 1);
+            mbar_init(&bar[B_TURN + i], 1);
         }
         mbar_init(&bar[B_STATS], 128);
-        mbar_init(&bar[B_DRAIN], 1);
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&bar[B_FULL + i], 1);
-            mbar_init(&bar[B_EMPTY + i], 1);
+        for (int i = 0; i < L::kKStages; ++i) {
+            mbar_init(&bar[B_KFULL + i], 1);
+            mbar_init(&bar[B_KEMPTY + i], 2);
+        }
+        for (int i = 0; i < L::kVStages; ++i) {
+            mbar_init(&bar[B_VFULL + i], 1);
+            mbar_init(&bar[B_VEMPTY + i], 2);
         }
         fence_barrier_init();
     }
@@ -321,12 +332,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     auto s_col = [](int t) { return (uint32_t)(t * kPrefixTile); };
     auto o_col = [](int t) { return (uint32_t)(2 * kPrefixTile + t * D); };
 
-    if (warp == kProducerWarp) {
-        // ============ producer: a segment's K and V tiles in turn, its Q tiles behind
-        // the first two (whose stages free before the Q tiles' last reader does), the
-        // first segment's ahead of them
+    if (warp == kProducerWarp || warp == kVProducerWarp) {
+        // ============ producers: K tiles, and a segment's Q tiles behind its first
+        // (whose stage frees before the Q tiles' last reader does; the first segment's
+        // ahead of them); V tiles
+        const bool is_v = warp == kVProducerWarp;
+        const int stages = is_v ? L::kVStages : L::kKStages, plane = is_v ? a.plane_v : a.plane_k;
+        uint64_t *const full = bar + (is_v ? B_VFULL : B_KFULL);
+        uint64_t *const empty = bar + (is_v ? B_VEMPTY : B_KEMPTY);
+        uint8_t *const ring = smem + (is_v ? L::kV : L::kK);
         const uint32_t q_bytes = (uint32_t)(a.g * mpt * 128 * (D / 64));
-        int ok = 1, entry = 0, segs = 0, tile = 0;
+        int ok = 1, segs = 0, tile = 0;
         while (ok && w.next(a)) {
             const PrefixSegment &sg = w.seg;
             const int32_t *row = a.block_tables + (int64_t)sg.p.lead * a.maxb;
@@ -335,7 +351,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 if (lane >= kTileBlocks || j >= sg.tiles || b >= sg.p.blocks) return -1;
                 const int blk = __ldg(row + b);
                 if (blk >= 0 && blk < a.num_blocks) return blk;
-                report(a.status, PA_DEV_BAD_BLOCK);
+                if (!is_v) report(a.status, PA_DEV_BAD_BLOCK);
                 return -1;
             };
             auto load_q = [&]() {
@@ -346,114 +362,139 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                                     0, hf, sg.kvh * a.g, sg.p.s0 + sg.member0 + t * mpt);
             };
             int blk = block_at(0);
-            if (segs == 0 && lane == 0) load_q();
+            if (!is_v && segs == 0 && lane == 0) load_q();
             for (int j = 0; j < sg.tiles && ok; ++j, ++tile) {
+                const int st = tile % stages;
                 const uint32_t have = __ballot_sync(0xffffffffu, blk >= 0);
-                const int next_blk = block_at(j + 1);
-                if (lane == 0) valid[tile % kValidRing] = have;
-                __syncwarp();
-                for (int kv = 0; kv < 2 && ok; ++kv, ++entry) {
-                    const int st = entry % NS;
-                    ok = mbar_wait(&bar[B_EMPTY + st], ((entry / NS) & 1) ^ 1);
-                    if (lane == 0 && ok) mbar_arrive_expect_tx(&bar[B_FULL + st], L::kTileBytes);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    // (a block that is missing comes from behind the pool: zeros)
-                    const int r0 = (blk >= 0 ? blk : a.num_blocks) * kBlockSize;
-                    if (lane < kTileBlocks)
-                        for (int hf = 0; hf < D / 64; ++hf)
-                            tma_load_5d(smem + L::kRing + st * L::kTileBytes + hf * L::kHalf +
-                                            lane * kBlockSize * 128,
-                                        &kvmap, &bar[B_FULL + st], 0, hf, sg.kvh, r0,
-                                        kv ? a.plane_v : a.plane_k);
+                // (a block that is missing comes from behind the pool: zeros)
+                const int r0 = (blk >= 0 ? blk : a.num_blocks) * kBlockSize;
+                blk = block_at(j + 1);
+                ok = mbar_wait(&empty[st], ((tile / stages) & 1) ^ 1);
+                if (lane == 0 && ok) {
+                    if (!is_v) valid[tile % kValidRing] = have;
+                    mbar_arrive_expect_tx(&full[st], L::kTileBytes);
                 }
-                blk = next_blk;
-                if (j == 0 && ok) {
-                    if (segs > 0) {
-                        ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_QEMPTY], (segs - 1) & 1));
-                        if (lane == 0 && ok) load_q();
-                    }
-                    ++segs;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane < kTileBlocks)
+                    for (int hf = 0; hf < D / 64; ++hf)
+                        tma_load_5d(ring + st * L::kTileBytes + hf * L::kHalf + lane * kBlockSize * 128,
+                                    &kvmap, &full[st], 0, hf, sg.kvh, r0, plane);
+                if (!is_v && j == 0 && segs > 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bar[B_QEMPTY], (segs - 1) & 1));
+                    if (lane == 0 && ok) load_q();
                 }
             }
+            ++segs;
         }
         if (lane == 0) {
             if (!ok) report(a.status, PA_DEV_TIMEOUT);
             // Leave no copy in flight.
-            for (int i = max(0, entry - NS); i < entry; ++i)
-                mbar_wait(&bar[B_FULL + i % NS], (i / NS) & 1);
-            if (segs > 0) mbar_wait(&bar[B_QFULL], (segs - 1) & 1);
+            for (int i = max(0, tile - stages); i < tile; ++i)
+                mbar_wait(&full[i % stages], (i / stages) & 1);
+            if (!is_v && segs > 0) mbar_wait(&bar[B_QFULL], (segs - 1) & 1);
         }
-    } else if (warp == kMmaWarp) {
-        // ============ MMA issuer.  A segment's jobs take the streams in turn: job i is
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+        // ============ MMA issuers.  A segment's jobs take the streams in turn: job i is
         // stream i & 1's, against key tile i / 2 of two tiles of query rows, or tile
-        // i of one.  A job's scores S_t = Q_t K^T go in behind the last job's of its
-        // stream, O_t += P V, which reads P from where they go; operations issued by
-        // one thread execute in order.  So a stream's P V and next scores run
-        // together while the softmax works on the other's (two issuers, one a
-        // stream, ran in step: both softmaxes, then both P V's, 2.4 us a tile of two
-        // against 1.7).
+        // i of one.  Turn i of the segment is thread i & 1's: O_t += P V of job i - 2,
+        // and behind it, into the place where that P stood, the scores S_t = Q_t K^T
+        // of job i (operations issued by one thread execute in order).  Strict turns
+        // keep one stream's softmax beside the other's operations (free-running
+        // threads fell in step, both softmaxes and then both products: 2.4 us a tile
+        // of two), and while one thread issues, which holds it for the operations' run
+        // time, the other waits for its barriers (one thread for both, which waited
+        // between: 2096 cycles a job, 1370 of them issuing).
+        const int t = warp - kMmaWarp;
         if (lane == 0) {
             constexpr uint32_t kIdescQK = tc::idesc_f16(kPrefixTile, kPrefixTile, false, false);
             constexpr uint32_t kIdescPV = tc::idesc_f16(kPrefixTile, D, false, true);
             const uint64_t dq0 = tc::smem_desc_sw128(smem_u32(smem), 16, 1024);
-            const uint64_t dk0 = tc::smem_desc_sw128(smem_u32(smem + L::kRing), 16, 1024);
-            const uint64_t dv0 = tc::smem_desc_sw128(smem_u32(smem + L::kRing), L::kHalf, 1024);
+            const uint64_t dk0 = tc::smem_desc_sw128(smem_u32(smem + L::kK), 16, 1024);
+            const uint64_t dv0 = tc::smem_desc_sw128(smem_u32(smem + L::kV), L::kHalf, 1024);
             bool ok = true;
-            int entry = 0, segs = 0;             // ring entries, segments before this one
-            int g0 = 0, g1 = 0, un0 = 0, un1 = 0;  // per stream: jobs, segments with jobs
+            int tile = 0, segs = 0;  // key tiles, segments before this one
+            int turns = 0;           // turns of this thread
+            int g = 0, un = 0;       // jobs, segments with jobs of this stream
+            // Tile j has been loaded.  (Each thread waits for every tile of a ring, in
+            // order, and gives it back: so a wait by phase parity is exact.)
+            auto k_wait = [&](int j) {
+                return mbar_wait(&bar[B_KFULL + j % L::kKStages], (j / L::kKStages) & 1);
+            };
+            auto v_wait = [&](int j) {
+                return mbar_wait(&bar[B_VFULL + j % L::kVStages], (j / L::kVStages) & 1);
+            };
             while (ok && w.next(a)) {
                 const PrefixSegment &sg = w.seg;
-                const int jobs = sg.pair ? 2 * sg.tiles : sg.tiles;
+                const bool pair = sg.pair;
+                const int jobs = pair ? 2 * sg.tiles : sg.tiles;
+                const uint64_t dq = dq0 + (uint64_t)((pair && t ? L::kTileBytes : 0) >> 4);
                 ok = mbar_wait(&bar[B_QFULL], segs & 1);
                 ++segs;
-                if (!ok) break;
-                auto scores = [&](int i) -> bool {
-                    const int t = i & 1, e = entry + 2 * (sg.pair ? i >> 1 : i), st = e % NS;
-                    if (!(sg.pair && t) && !mbar_wait(&bar[B_FULL + st], (e / NS) & 1)) return false;
-                    tc::fence_after();
-                    const uint64_t dq = dq0 + (uint64_t)((sg.pair && t ? L::kTileBytes : 0) >> 4);
-                    const uint64_t dk = dk0 + (uint64_t)((st * L::kTileBytes) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t step = (uint64_t)(((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4);
-                        tc::mma_ss(tmem + s_col(t), dq + step, dk + step, kIdescQK, kk > 0);
+                if (ok && t >= jobs) mbar_arrive(&bar[B_QEMPTY]);
+                // (an even number of turns, so that thread 0 begins the next segment)
+                for (int i = t; i < ((jobs + 3) & ~1) && ok; i += 2) {
+                    const bool scores = i < jobs, values = i >= 2 && i < jobs + 2;
+                    const int kj = tile + (pair ? i >> 1 : i), vj = tile + (pair ? (i - 2) >> 1 : i - 2);
+                    if (!pair) {  // the other stream's tiles
+                        if (i >= 3 && i - 3 < jobs) {
+                            ok = v_wait(tile + i - 3);
+                            mbar_arrive(&bar[B_VEMPTY + (tile + i - 3) % L::kVStages]);
+                        }
+                        if (i >= 1 && i - 1 < jobs) {
+                            ok = ok && k_wait(tile + i - 1);
+                            mbar_arrive(&bar[B_KEMPTY + (tile + i - 1) % L::kKStages]);
+                        }
                     }
-                    tc::commit(&bar[B_SFULL + t]);
-                    if (!sg.pair || t) tc::commit(&bar[B_EMPTY + st]);
-                    if (i == jobs - 1) tc::commit(&bar[B_QEMPTY]);
-                    return true;
-                };
-                ok = scores(0);
-                for (int i = 0; i < jobs && ok; ++i) {
-                    if (i + 1 < jobs) ok = scores(i + 1);
-                    const int t = i & 1, e = entry + 2 * (sg.pair ? i >> 1 : i) + 1, st = e % NS;
-                    if (ok && !(sg.pair && t)) ok = mbar_wait(&bar[B_FULL + st], (e / NS) & 1);
-                    ok = ok && mbar_wait(&bar[B_PREADY + t], (t ? g1 : g0) & 1);
-                    // the stream's O of the segment before has to have been read
-                    const int un = t ? un1 : un0;
-                    if (ok && i < 2 && un > 0) ok = mbar_wait(&bar[B_OFREE + t], (un - 1) & 1);
+                    if (values) {
+                        ok = ok && v_wait(vj) && mbar_wait(&bar[B_PREADY + t], g & 1);
+                        // the stream's O of the segment before has to have been read
+                        if (ok && i < 4 && un > 0) ok = mbar_wait(&bar[B_OFREE + t], (un - 1) & 1);
+                    }
+                    if (scores) ok = ok && k_wait(kj);
+                    // (thread 0's first turn is free)
+                    ok = ok && mbar_wait(&bar[B_TURN + t], (turns & 1) ^ (t == 0 ? 1 : 0));
+                    ++turns;
                     if (!ok) break;
                     tc::fence_after();
-                    const uint64_t dv = dv0 + (uint64_t)((st * L::kTileBytes) >> 4);
+                    if (values) {
+                        const int st = vj % L::kVStages;
+                        const uint64_t dv = dv0 + (uint64_t)((st * L::kTileBytes) >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kPrefixTile / 16; ++kk)
-                        tc::mma_ts(tmem + o_col(t), tmem + s_col(t) + kk * 8,
-                                   dv + (uint64_t)((kk * 16 * 128) >> 4), kIdescPV,
-                                   (i > 1 || kk > 0) ? 1u : 0u);
-                    if (!sg.pair || t) tc::commit(&bar[B_EMPTY + st]);
-                    if (i >= jobs - 2) tc::commit(&bar[B_OUNIT + t]);
-                    g0 += t == 0;
-                    g1 += t;
+                        for (int kk = 0; kk < kPrefixTile / 16; ++kk)
+                            tc::mma_ts(tmem + o_col(t), tmem + s_col(t) + kk * 8,
+                                       dv + (uint64_t)((kk * 16 * 128) >> 4), kIdescPV,
+                                       (i >= 4 || kk > 0) ? 1u : 0u);
+                        tc::commit(&bar[B_VEMPTY + st]);
+                        if (i >= jobs) tc::commit(&bar[B_OUNIT + t]);
+                        ++g;
+                    }
+                    if (scores) {
+                        const int st = kj % L::kKStages;
+                        const uint64_t dk = dk0 + (uint64_t)((st * L::kTileBytes) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t step = (uint64_t)(((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4);
+                            tc::mma_ss(tmem + s_col(t), dq + step, dk + step, kIdescQK, kk > 0);
+                        }
+                        tc::commit(&bar[B_SFULL + t]);
+                        tc::commit(&bar[B_KEMPTY + st]);
+                        if (i + 2 >= jobs) tc::commit(&bar[B_QEMPTY]);
+                    }
+                    mbar_arrive(&bar[B_TURN + 1 - t]);
                 }
-                entry += 2 * sg.tiles;
-                ++un0;
-                un1 += jobs > 1;
+                // (the last V tile, if it was the other's and this thread had no turn left)
+                if (ok && !pair && ((jobs - 1) & 1) != t && jobs + 2 >= ((jobs + 3) & ~1)) {
+                    ok = v_wait(tile + jobs - 1);
+                    mbar_arrive(&bar[B_VEMPTY + (tile + jobs - 1) % L::kVStages]);
+                }
+                tile += sg.tiles;
+                un += t < jobs;
             }
             if (!ok) report(a.status, PA_DEV_TIMEOUT);
             // Nothing of ours may still be running when the CTA frees TMEM.
-            tc::commit(&bar[B_DRAIN]);
-            mbar_wait(&bar[B_DRAIN], 0);
+            tc::commit(&bar[B_DRAIN + t]);
+            mbar_wait(&bar[B_DRAIN + t], 0);
         }
         __syncwarp();
     } else {
