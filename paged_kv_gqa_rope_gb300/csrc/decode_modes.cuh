@@ -27,9 +27,9 @@ struct Groups {
 // A group whose prefix is read once.  The prefixes' work lies on a line: group
 // after group, KV head after KV head, unit after unit (2 * (128 / g) sequences:
 // two tiles of 128 query rows), 128-key tile after tile and kUnitCost places for a
-// unit's fixed cost (its Q, the ring's start, its record: about 4 us, without which
-// CTAs with several short units end last).  A tile has `weight` places: three
-// (1.56 us) against one tile of query rows, four (2.1 us) against two.  G CTAs take
+// unit's fixed cost (its Q, the ring's start, its record: about 3.5 us, without which
+// CTAs with several short units end last).  A tile has `weight` places: two
+// (1.15 us) against one tile of query rows, three (1.7 us) against two.  G CTAs take
 // equal ranges of the line; a tile belongs to the range of its first place.
 struct PlanGroup {
     int tiles;    // key tiles of a unit
@@ -78,7 +78,7 @@ struct DecodeTails {
 constexpr int kPrefixTile = 128;  // keys of a tile, and query rows
 constexpr int kTileBlocks = kPrefixTile / kBlockSize;
 
-constexpr int kUnitCost = 6, kTileWeight = 3, kPairWeight = 4;
+constexpr int kUnitCost = 6, kTileWeight = 2, kPairWeight = 3;
 __device__ __forceinline__ int PlanGroup::span() const { return tiles * weight + kUnitCost; }
 
 // CTAs with a range: each of kPairWeight places at least, so that it has a tile of
@@ -216,7 +216,7 @@ __device__ __forceinline__ PlanGroup load_group(const Groups &g, const int32_t *
 // How the SMs are divided between the prefixes and the tails, which run side by
 // side: in proportion to what each would take of one SM, in units of a tail's
 // block (8 KB at d = 128, about 0.14 us with two decode CTAs an SM).
-constexpr int kTileCost = 11;  // of kTileWeight places
+constexpr int kTileCost = 8;  // of kTileWeight places
 
 // By a whole CTA of `threads` threads after read_groups; `sums` are three words of
 // shared memory.  Every CTA comes to the same.  Returns the SMs for the prefixes; total: places of their line.

@@ -116,6 +116,12 @@ struct Record {
     }
 };
 
+// A load whose value nobody waits for.
+__device__ __forceinline__ void touch(const int32_t *p) {
+    int32_t v;
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
+}
+
 // The part of the CTA's range that lies in one unit.
 struct PrefixSegment {
     PlanGroup p;
@@ -303,7 +309,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     if (blockIdx.x != 0) griddep_launch_dependents();
     const uint32_t tmem = *tmem_slot;  // S_0 | S_1 | O_0 | O_1
     const int mpt = kPrefixTile / a.g;
-    // ---- the plan, with the room of the tiles for the sequences' lengths
+    // ---- the plan, with the room of the tiles for the sequences' lengths.  What its
+    // steps read first is asked for at once, so that they find it in L1.
+    touch(a.context_lens + min(tid, a.B - 1));
+    touch(a.groups.starts + min(tid, a.groups.n));
+    touch(a.groups.blocks + min(tid, a.groups.n - 1));
     PlanCut *cut = reinterpret_cast<PlanCut *>(stats);
     {
         int32_t *skip = reinterpret_cast<int32_t *>(smem), *lens = skip + a.B;

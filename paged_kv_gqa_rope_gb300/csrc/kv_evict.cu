@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kSelThreads, C > 4 ? 1 : 2)
     __shared__ __align__(16) int hist[3][kDigits];
     __shared__ Counts sums[C * kSelWarps];
     __shared__ int warp_total[kSelWarps];
-    __shared__ int found[2], mine_of[2];
+    __shared__ int found[3], mine_of[2];
     const int h = blockIdx.x / size, s = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = size > 1 ? (int)cluster_rank() : 0;
@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(kSelThreads, C > 4 ? 1 : 2)
                 if (before < want && want <= before + cnt[j]) {
                     found[0] = kDigits - 1 - kPer * tid - j;
                     found[1] = want - before;
+                    found[2] = cnt[j];
                 }
                 before += cnt[j];
             }
@@ -248,6 +249,13 @@ __global__ void __launch_bounds__(kSelThreads, C > 4 ? 1 : 2)
             limit |= (uint32_t)found[0] << shift;
             mask |= digit << shift;
             equal = want = found[1];
+            if (found[2] == want && limit > 0) {
+                // all keys that agree so far are kept (one key, more often than not):
+                // those are the keys above the largest one below them
+                --limit;
+                equal = 0;
+                break;
+            }
             // (barriers of the next digit come before found and warp_total change)
         }
     }
