@@ -94,6 +94,24 @@ int pa_bm_num_tokens(pa_bm_t bm, int64_t seq_id);
 int pa_bm_block_table(pa_bm_t bm, int64_t seq_id, int32_t *table, int max_blocks,
                       int *num_blocks);
 
+/*
+ * Shorten a computed sequence to num_keep tokens by pa_kv_evict.  begin
+ * switches its table to the one for the kept rows (pa_kv_evict's
+ * out_block_tables): the sequence's own blocks where no other sequence uses
+ * them, which can no longer be matched by a prompt, and free blocks in the place
+ * of shared ones.  The blocks that it leaves stay taken until end, so read the
+ * old table first, call begin for every sequence of the batch, enqueue the
+ * evictions of all layers, then call end: the blocks may then be handed out anew
+ * (whoever writes them comes later in stream order).  Afterwards the sequence
+ * has num_keep tokens and goes on with pa_bm_append (its new blocks are never
+ * matched); the caller keeps track of true positions.  With num_keep >= its
+ * tokens nothing changes.  begin fails for a sequence whose prompt is not
+ * computed or that is being evicted (PA_ERR_INVALID), or with too few free blocks
+ * (PA_ERR_WORKSPACE, nothing changed); between begin and end pa_bm_append fails.
+ */
+int pa_bm_evict_begin(pa_bm_t bm, int64_t seq_id, int num_keep);
+int pa_bm_evict_end(pa_bm_t bm, int64_t seq_id);
+
 /* Give back seq_id's blocks (finished or preempted); the id may be reused. */
 int pa_bm_free(pa_bm_t bm, int64_t seq_id);
 

@@ -43,6 +43,9 @@ struct Seq {
     int prompt = 0;
     int computed = 0;             // tokens whose K/V are in the cache
     uint64_t last_full_hash = 0;  // chained hash of the last full block
+    std::vector<int32_t> leaving; // blocks an eviction under way still reads
+    bool evicting = false;
+    bool evicted = false;         // its blocks no longer hold the rows of `tokens`
 };
 
 }  // namespace
@@ -61,12 +64,7 @@ struct pa_block_manager {
         free_list.pop_front();
         Block &k = blocks[b];
         k.in_free = false;
-        if (k.hashed) {
-            auto it = by_hash.find(k.hash);
-            if (it != by_hash.end() && it->second == b) by_hash.erase(it);
-            k.hashed = false;
-            k.tokens.clear();
-        }
+        forget(b);
         k.ref = 1;
         return b;
     }
@@ -85,6 +83,15 @@ struct pa_block_manager {
             k.in_free = true;
             k.free_it = std::prev(free_list.end());
         }
+    }
+    // Block b's contents are about to change: it can no longer be matched.
+    void forget(int b) {
+        Block &k = blocks[b];
+        if (!k.hashed) return;
+        auto it = by_hash.find(k.hash);
+        if (it != by_hash.end() && it->second == b) by_hash.erase(it);
+        k.hashed = false;
+        k.tokens.clear();
     }
     // Register full block b under hash h (a block with the same contents
     // already registered keeps the entry).
@@ -201,7 +208,7 @@ int pa_bm_can_append(pa_bm_t bm, int64_t seq_id) {
 
 int pa_bm_append(pa_bm_t bm, int64_t seq_id, int32_t token, int32_t *slot) {
     Seq *s = bm ? bm->find(seq_id) : nullptr;
-    if (!s || !slot || s->computed < (int)s->tokens.size()) return PA_ERR_INVALID;
+    if (!s || !slot || s->evicting || s->computed < (int)s->tokens.size()) return PA_ERR_INVALID;
     const int bs = bm->bs;
     const int pos = (int)s->tokens.size();
     if (pos % bs == 0) {
@@ -213,7 +220,7 @@ int pa_bm_append(pa_bm_t bm, int64_t seq_id, int32_t token, int32_t *slot) {
     s->computed = pos + 1;
     const int blk = s->blocks[pos / bs];
     *slot = blk * bs + pos % bs;
-    if ((pos + 1) % bs == 0) {  // the block just filled: it can be matched from now on
+    if ((pos + 1) % bs == 0 && !s->evicted) {  // the block just filled: it can be matched from now on
         const uint64_t h = block_hash(s->last_full_hash, s->tokens.data() + (pos + 1 - bs), bs);
         bm->set_hash(blk, h, s->tokens.data() + (pos + 1 - bs));
         s->last_full_hash = h;
@@ -237,9 +244,52 @@ int pa_bm_block_table(pa_bm_t bm, int64_t seq_id, int32_t *table, int max_blocks
     return PA_OK;
 }
 
+int pa_bm_evict_begin(pa_bm_t bm, int64_t seq_id, int num_keep) {
+    Seq *s = bm ? bm->find(seq_id) : nullptr;
+    if (!s || num_keep <= 0 || s->evicting || s->computed < (int)s->tokens.size())
+        return PA_ERR_INVALID;
+    if (num_keep >= (int)s->tokens.size()) {  // nothing goes
+        s->evicting = true;
+        return PA_OK;
+    }
+    const int keep = (num_keep + bm->bs - 1) / bm->bs;
+    int fresh = 0;
+    for (int i = 0; i < keep; ++i) fresh += bm->blocks[s->blocks[i]].ref > 1 ? 1 : 0;
+    if (fresh > (int)bm->free_list.size()) return PA_ERR_WORKSPACE;
+    try {
+        s->leaving.reserve(s->blocks.size());  // (nothing below allocates)
+    } catch (...) {
+        return PA_ERR_WORKSPACE;
+    }
+    s->leaving.assign(s->blocks.begin() + keep, s->blocks.end());
+    s->blocks.resize(keep);
+    for (int i = 0; i < keep; ++i) {
+        if (bm->blocks[s->blocks[i]].ref > 1) {
+            s->leaving.push_back(s->blocks[i]);
+            s->blocks[i] = bm->take_free();
+        } else {
+            bm->forget(s->blocks[i]);
+        }
+    }
+    s->tokens.resize(num_keep);
+    s->computed = s->prompt = num_keep;
+    s->evicting = s->evicted = true;
+    return PA_OK;
+}
+
+int pa_bm_evict_end(pa_bm_t bm, int64_t seq_id) {
+    Seq *s = bm ? bm->find(seq_id) : nullptr;
+    if (!s || !s->evicting) return PA_ERR_INVALID;
+    for (auto it = s->leaving.rbegin(); it != s->leaving.rend(); ++it) bm->release(*it);
+    s->leaving.clear();
+    s->evicting = false;
+    return PA_OK;
+}
+
 int pa_bm_free(pa_bm_t bm, int64_t seq_id) {
     Seq *s = bm ? bm->find(seq_id) : nullptr;
     if (!s) return PA_ERR_INVALID;
+    for (auto it = s->leaving.rbegin(); it != s->leaving.rend(); ++it) bm->release(*it);
     for (auto it = s->blocks.rbegin(); it != s->blocks.rend(); ++it) bm->release(*it);
     bm->seqs.erase(seq_id);
     return PA_OK;

@@ -118,7 +118,7 @@ struct Record {
 
 // A load whose value nobody waits for.
 __device__ __forceinline__ void touch(const int32_t *p) {
-    int32_t v;
+    [[maybe_unused]] int32_t v;
     asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
 }
 

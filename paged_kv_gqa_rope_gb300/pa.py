@@ -38,7 +38,7 @@ EXPORTS = (
     "pa_rope_kv_write_layout", "pa_rope_table_init_scaled", "pa_prepare_shared",
     "pa_decode_shared_workspace_bytes", "pa_decode_shared",
     "pa_decode_weights_workspace_bytes", "pa_decode_weights",
-    "pa_kv_evict_workspace_bytes", "pa_kv_evict",
+    "pa_kv_evict_workspace_bytes", "pa_kv_evict", "pa_bm_evict_begin", "pa_bm_evict_end",
 )
 
 
@@ -123,6 +123,8 @@ _SIGS = {
     "pa_bm_num_tokens": (_i32, [_vp, _i64]),
     "pa_bm_block_table": (_i32, [_vp, _i64, _vp, _i32, ctypes.POINTER(_i32)]),
     "pa_bm_free": (_i32, [_vp, _i64]),
+    "pa_bm_evict_begin": (_i32, [_vp, _i64, _i32]),
+    "pa_bm_evict_end": (_i32, [_vp, _i64]),
     "pa_selftest_wait_timeout": (_i32, [_vp, _vp]),
     "pa_cache_i8_bytes": (_sz, [_i32] * 5),
     "pa_alloc_cache_i8": (_i32, [ctypes.POINTER(PaCacheI8)] + [_i32] * 5 + [_vp]),
@@ -572,6 +574,14 @@ class BlockManager:
         _check("pa_bm_block_table", lib().pa_bm_block_table(self._h, seq_id, _p(out), out.size,
                                                              ctypes.byref(n)))
         return out[:n.value]
+
+    def evict_begin(self, seq_id, num_keep):
+        """Switch to the table of the kept rows (kv_evict's out_block_tables)."""
+        _check("pa_bm_evict_begin", lib().pa_bm_evict_begin(self._h, seq_id, int(num_keep)))
+
+    def evict_end(self, seq_id):
+        """The evictions are enqueued: the blocks left behind may be reused."""
+        _check("pa_bm_evict_end", lib().pa_bm_evict_end(self._h, seq_id))
 
     def free(self, seq_id):
         _check("pa_bm_free", lib().pa_bm_free(self._h, seq_id))

@@ -714,15 +714,11 @@ def test_serving_loop(H, Hk, d):
     true_pos = ctx.copy()
     slots = np.zeros(B, np.int32)
     ctx_d = None
-    for step in range(6):
-        if step < 4:
-            for i in range(B):
-                slots[i] = bm.append(i, step)
-                t = bm.block_table(i)
-                bt[i, :len(t)] = t
-        else:  # behind the eviction the tables are this test's own
-            for i in range(B):
-                slots[i] = bt[i, ctx[i] // 16] * 16 + ctx[i] % 16
+    for step in range(14):
+        for i in range(B):
+            slots[i] = bm.append(i, step)
+            t = bm.block_table(i)
+            bt[i, :len(t)] = t
         q, k, v = normal16(rng, B, H, d), normal16(rng, B, Hk, d), normal16(rng, B, Hk, d)
         qr, q_rot = append(q, k, v, true_pos, slots)
         true_pos += 1
@@ -739,15 +735,21 @@ def test_serving_loop(H, Hk, d):
                 want_w[s, :, :ctx[s]] += x
         assert_attention_close(out, want)
         assert np.abs(w.cpu().numpy() - want_w).max() <= 1e-4
+        assert [bm.num_tokens(i) for i in range(B)] == ctx.tolist() or step == 3
         if step == 3:
             # the weights decide: what the GPU added up goes into the oracle's eviction
             to = np.full((B, width), -1, np.int32)
-            to[:, :3] = np.setdiff1d(np.arange(NB), bt)[:3 * B].reshape(B, 3)
+            for i in range(B):
+                bm.evict_begin(i, 40)
+                to[i, :3] = bm.block_table(i)
             host_w = w.cpu().numpy()
             ctx_d = dev(ctx)
             pa.kv_evict(cache, dev(bt), ctx_d, w, 40, pa.kv_evict_workspace(B, Hk, 40), sinks=4,
                         recent=8, out_block_tables=dev(to), status=status)
             ctx = orc.evict(pool, 0, bt, ctx, host_w, 40, 4, 8, to)
+            for i in range(B):
+                bm.evict_end(i)
+            assert len(set(to[:, :3].ravel())) == 3 * B  # (nothing shared any more)
             assert ctx.tolist() == [40] * B and np.array_equal(ctx_d.cpu().numpy(), ctx)
             assert np.array_equal(w.cpu().numpy(), host_w)
             want_w = host_w.astype(np.float64)

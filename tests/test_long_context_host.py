@@ -155,6 +155,73 @@ def test_prepare_shared_refusals(libpa):
     assert (out == 7).all() and n.value == 7
 
 
+# ---------------------------------------------------------------- the block manager
+
+
+def test_block_manager_evicts(libpa):
+    bm = pa.BlockManager(20)
+    prompt = list(range(64))
+    bm.allocate(1, prompt + [1] * 20)  # 6 blocks
+    bm.allocate(2, prompt + [2] * 40)  # 7, the first 4 shared
+    for s, n in ((1, 84), (2, 40)):
+        bm.mark_computed(s, n)
+    old = {s: bm.block_table(s).tolist() for s in (1, 2)}
+    assert old[1][:4] == old[2][:4] and bm.num_free() == 20 - 9
+    bm.evict_begin(2, 70)  # 5 blocks: 4 fresh ones for the shared, its own fifth
+    new = bm.block_table(2).tolist()
+    assert new[4] == old[2][4] and not set(new[:4]) & set(old[1] + old[2])
+    assert bm.num_tokens(2) == 70 and bm.num_free() == 11 - 4  # what it leaves stays taken
+    with pytest.raises(pa.PAError):
+        bm.append(2, 7)
+    with pytest.raises(pa.PAError):
+        bm.evict_begin(2, 60)
+    bm.evict_end(2)
+    assert bm.num_free() == 7 + 2 and bm.block_table(1).tolist() == old[1]
+    with pytest.raises(pa.PAError):
+        bm.evict_end(2)
+    # on with its own slots; what fills is not matched, what it had of its own neither
+    slots = [bm.append(2, 5) for _ in range(26)]
+    assert slots[0] == new[4] * 16 + 6 and bm.num_tokens(2) == 96
+    free = bm.num_free()
+    assert bm.allocate(3, prompt + [2] * 40) == 64  # the shared prefix alone: sequence 1's
+    assert bm.block_table(3).tolist()[:4] == old[1][:4] and bm.num_free() == free - 3
+    bm.free(3)
+    # sequence 1 in place: its blocks are matched no longer
+    bm.evict_begin(1, 33)
+    assert bm.block_table(1).tolist() == old[1][:3]
+    bm.evict_end(1)
+    bm.free(1)
+    assert bm.allocate(4, prompt) == 0
+    for s in (2, 4):
+        bm.free(s)
+    assert bm.num_free() == 20
+
+
+def test_block_manager_evict_refusals(libpa):
+    bm = pa.BlockManager(8)
+    with pytest.raises(pa.PAError):
+        bm.evict_begin(1, 4)
+    bm.allocate(1, list(range(100)))
+    with pytest.raises(pa.PAError):
+        bm.evict_begin(1, 40)  # its prompt is not computed
+    bm.mark_computed(1, 100)
+    with pytest.raises(pa.PAError):
+        bm.evict_begin(1, 0)
+    bm.evict_begin(1, 100)  # nothing goes
+    bm.evict_end(1)
+    assert bm.num_tokens(1) == 100 and len(bm.block_table(1)) == 7
+    bm.allocate(2, list(range(112)))
+    bm.mark_computed(2, bm.num_tokens(2) - 96)
+    table = bm.block_table(2).tolist()
+    with pytest.raises(pa.PAError) as e:  # six shared blocks, no free one
+        bm.evict_begin(2, 90)
+    assert e.value.code == pa.PA_ERR_WORKSPACE and bm.block_table(2).tolist() == table
+    bm.free(1)  # (between begin and end: blocks left behind are given back too)
+    bm.evict_begin(2, 20)
+    bm.free(2)
+    assert bm.num_free() == 8
+
+
 # ---------------------------------------------------------------- sizes and refusals
 
 BUF = ctypes.c_void_p(1 << 24)
