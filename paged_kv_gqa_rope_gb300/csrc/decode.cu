@@ -300,13 +300,23 @@ __device__ __forceinline__ int ld_acquire_gpu(const int *p) {
 // sum), the row sum and the O of the head's D columns (lane = column within
 // each run of 32) accumulated in piece order, the O values of four pieces
 // loaded at a time (two for the int8 kernel, whose registers are capped).
+// Loads of the call's inputs.  kTails takes them from L2: it does not itself wait
+// for the work that wrote them (the prefix kernel has, before it let it start).
+template <Mode MODE, typename T>
+__device__ __forceinline__ T load_meta(const T *p) {
+    if constexpr (MODE == Mode::kTails)
+        return __ldcg(p);
+    else
+        return __ldg(p);
+}
+
 // One element (head h of the pair, value d) of a finished pair: O unnormalised,
-// M the maximum, L the sum of the row.
+// M the maximum, L the sum of the row; alone: nothing to be joined with it.
 template <int D, Mode MODE>
 __device__ __forceinline__ void emit(const DecodeArgs &a, int s, int kvh, int h, int d, float O,
-                                     float M, float L) {
+                                     float M, float L, bool alone) {
     const int64_t row = (int64_t)s * a.H + kvh * a.g + h;
-    if constexpr (MODE == Mode::kTails) {
+    if (MODE == Mode::kTails && !alone) {
         float *r = a.tl.rec + row * (D + 4);
         r[d] = O;
         if (d == 0) {
@@ -319,7 +329,7 @@ __device__ __forceinline__ void emit(const DecodeArgs &a, int s, int kvh, int h,
         } else {  // (NaN stays NaN; a row whose blocks are all out of range is 0)
             const bool none = L == 0.f;
             a.out[row * D + d] = __float2half_rn(none ? 0.f : O / L);
-            if (d == 0)
+            if (MODE == Mode::kScores && d == 0)
                 a.sc.stats[row] = none ? make_float2(0.f, 0.f) : make_float2(M - kPShift, 1.f / L);
         }
     }
@@ -327,7 +337,7 @@ __device__ __forceinline__ void emit(const DecodeArgs &a, int s, int kvh, int h,
 
 template <int D, bool I8, Mode MODE>
 __device__ void warp_merge_records(const DecodeArgs &a, const Segment &sg, int64_t W, int G,
-                                   int lane, int h0, int step) {
+                                   int lane, int h0, int step, bool alone) {
     constexpr int kRec = D + 4;
     constexpr int kRuns = D / 32;
     constexpr int kBatch = I8 ? 2 : 4;
@@ -379,15 +389,14 @@ __device__ void warp_merge_records(const DecodeArgs &a, const Segment &sg, int64
         }
 #pragma unroll
         for (int rr = 0; rr < kRuns; ++rr)
-            emit<D, MODE>(a, sg.s, sg.kvh, h, rr * 32 + lane, O[rr], M, Lsum);
+            emit<D, MODE>(a, sg.s, sg.kvh, h, rr * 32 + lane, O[rr], M, Lsum, alone);
     }
 }
 
-// The lines of the modes other than kOut: every sequence has its cost units, one
-// with no blocks (nothing behind its shared prefix, or a bad length) nothing
-// else, and `lens` in shared memory has the tokens that are the sequence's here
-// (0 for a bad length).  Blocks of all KV heads ahead of sequence s:
-// prefix[s] - s * kCost * Hk.
+// In the modes other than kOut `lens` in shared memory has the tokens that are a
+// sequence's here: 0 for a bad length, or nothing behind the shared prefix.  Such a
+// sequence has no place on the line of kTails; in kScores it has its cost units, so
+// that the blocks of all KV heads ahead of sequence s are prefix[s] - s * kCost * Hk.
 template <int D, int NSTAGE, bool I8, Mode MODE>
 __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     decode_kernel(const __grid_constant__ CUtensorMap kvmap,
@@ -455,7 +464,8 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                 lens[s] = t.x;
                 skip[s] = t.y;
             }
-            n = (int64_t)((lens[s] + kBlockSize - 1) / kBlockSize + kCost) * a.Hk;
+            if (MODE == Mode::kScores || lens[s] > 0)
+                n = (int64_t)((lens[s] + kBlockSize - 1) / kBlockSize + kCost) * a.Hk;
         }
         prefix[s + 1] = n;
     }
@@ -507,7 +517,11 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     // (kTails: no more CTAs than find room beside the prefix kernel's)
     const int most = MODE == Mode::kTails ? min(tail_ctas, (int)gridDim.x) : (int)gridDim.x;
     const int G = (int)(W < (int64_t)most ? W : (int64_t)most);
-    if (cta >= G) return;
+    if (cta >= G) {
+        if constexpr (MODE == Mode::kTails)
+            if (cta == 0) griddep_wait();  // (as below)
+        return;
+    }
     const int64_t start = range_start(W, cta, G), end = range_start(W, cta + 1, G);
 
     if (warp == kConsumerWarps) {
@@ -525,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
             if constexpr (MODE == Mode::kTails) row += skip[sg.s];
             for (int w0 = 0; w0 < sg.nb && !abort; w0 += 32) {
                 const int cnt = min(32, sg.nb - w0);
-                const int my_blk = lane < cnt ? __ldg(row + w0 + lane) : 0;
+                const int my_blk = lane < cnt ? load_meta<MODE>(row + w0 + lane) : 0;
                 for (int j = 0; j < cnt; ++j) {
                     const int blk = __shfl_sync(0xffffffffu, my_blk, j);
                     const int stage = gblk % NSTAGE;
@@ -593,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
             pos += sg.nu;
             continue;
         }
+        const bool alone = MODE != Mode::kTails || skip[s] == 0;
         // This lane's place in the scores of the warp's block, and which of its two
         // heads it stores: none, the first, both at once (g even) or one by one.
         [[maybe_unused]] float *sc_at = nullptr;
@@ -643,8 +658,8 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
             } else {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    qb[kk][0] = hv ? __ldg(qrow + kk * 8 + quad) : 0u;
-                    qb[kk][1] = hv ? __ldg(qrow + kk * 8 + 4 + quad) : 0u;
+                    qb[kk][0] = hv ? load_meta<MODE>(qrow + kk * 8 + quad) : 0u;
+                    qb[kk][1] = hv ? load_meta<MODE>(qrow + kk * 8 + 4 + quad) : 0u;
                 }
             }
         }
@@ -963,7 +978,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
 #pragma unroll
                 for (int wv = 0; wv < kConsumerWarps; ++wv)
                     O = __fmaf_rn(sm_m[wv * kGroupPad + h], sm_o[(wv * kGroupPad + h) * D + d], O);
-                emit<D, MODE>(a, s, kvh, h, d, O, sm_l[kGroupPad + h], sm_l[h]);
+                emit<D, MODE>(a, s, kvh, h, d, O, sm_l[kGroupPad + h], sm_l[h], alone);
             }
             named_barrier_sync(1, kCons);  // the smem merge area is free again
         } else {
@@ -1007,7 +1022,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                             if (last) fence_acq_rel_gpu();
                         }
                         if (__shfl_sync(0xffffffffu, last, 0)) {
-                            warp_merge_records<D, I8, MODE>(a, sg, W, G, lane, 0, 1);
+                            warp_merge_records<D, I8, MODE>(a, sg, W, G, lane, 0, 1, alone);
                             if (lane == 0) a.counters[s * a.Hk + kvh] = 0;
                         }
                     }
@@ -1092,7 +1107,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                                     if (i < nrec)
                                         O = __fmaf_rn(sm_pm[i * kGroupPad + h],
                                                       i == own ? Oown : x[i][k], O);
-                                emit<D, MODE>(a, s, kvh, h, d, O, sm_pl[kGroupPad + h], sm_pl[h]);
+                                emit<D, MODE>(a, s, kvh, h, d, O, sm_pl[kGroupPad + h], sm_pl[h], alone);
                             }
                         }
                     }
@@ -1162,7 +1177,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                                                   i == own ? oown[k]
                                                            : sm_o[(i * kGroupPad + h) * D + d],
                                                   O);
-                            emit<D, MODE>(a, s, kvh, h, d, O, sm_pl[kGroupPad + h], sm_pl[h]);
+                            emit<D, MODE>(a, s, kvh, h, d, O, sm_pl[kGroupPad + h], sm_pl[h], alone);
                         }
                     }
                 }
@@ -1171,7 +1186,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                 // More pieces (a long pair), from the records: a head per warp.
                 // (One element per thread and a piece at a time took 210 us of the
                 // 231 of one sequence of 32767 tokens over 8 KV heads.)
-                warp_merge_records<D, I8, MODE>(a, sg, W, G, lane, warp, kConsumerWarps);
+                warp_merge_records<D, I8, MODE>(a, sg, W, G, lane, warp, kConsumerWarps, alone);
                 if (tid == 0) a.counters[s * a.Hk + kvh] = 0;
             }
         }

@@ -67,7 +67,8 @@ struct alignas(16) PlanHead {
 };
 
 // Records in the place of the output, over the tokens behind the shared blocks
-// (pa_decode_shared): unnormalised O, then m and l of the row.
+// (pa_decode_shared): unnormalised O, then m and l of the row.  A sequence with no
+// shared blocks gets its output.
 struct DecodeTails {
     float *rec;  // [B][H][D + 4]
     // by the prefix kernel, ahead of its launch_dependents
@@ -134,7 +135,9 @@ int launch_decode_tails(const DecodeCall &c, void *workspace, const DecodeTails 
 
 // A prefix is read once for its group if that saves at least this many blocks
 // of a KV head, else by each sequence with the rest of its context (a single
-// sequence has nothing to share).
+// sequence has nothing to share).  Eight sequences over 128 shared tokens, 56
+// blocks: 14.8 us shared and 15.0 not with 4/2 heads of 64, 18.6 and 18.8 with 32/32
+// of 128; two over 256, 16 blocks, 64/8 of 128: 16.6 and 24.0.
 constexpr int kMinSavedBlocks = 8;
 
 __device__ __forceinline__ int shared_of(int blocks, int members) {

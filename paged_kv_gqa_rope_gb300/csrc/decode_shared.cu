@@ -737,13 +737,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SharedArgs a) 
     float4 O = __ldcg(reinterpret_cast<const float4 *>(r) + c4);
     const SeqPlan p = a.seqs[s];
     const PlanHead head = *a.head;
-    if (p.state == kLeftOut) return;
-    int pieces = 0, c0 = 0;
-    if (p.state == kInGroup) {
-        const int64_t start = p.start + kvh * p.stride;
-        c0 = plan_cta(start, head.total, head.ctas);
-        pieces = plan_cta(start + p.last, head.total, head.ctas) - c0 + 1;
-    }
+    if (p.state != kInGroup) return;  // (alone: the tails' kernel has written it)
+    const int64_t start = p.start + kvh * p.stride;
+    const int c0 = plan_cta(start, head.total, head.ctas);
+    const int pieces = plan_cta(start + p.last, head.total, head.ctas) - c0 + 1;
     if (p.tail == 0) {
         st = make_float2(-INFINITY, 0.f);
         O = make_float4(0.f, 0.f, 0.f, 0.f);

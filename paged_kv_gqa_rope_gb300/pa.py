@@ -918,9 +918,10 @@ def rope_table_scaled(max_positions, rotary_dim, theta=10000.0, scaling=None, fa
         raise ValueError("bad RoPE table shape")
     if high is None:
         high = 32.0 if scaling == "yarn" else 4.0
-    t = torch.empty((max_positions, rotary_dim // 2, 2), dtype=torch.float32, device=device)
-    if not t.is_cuda:
-        raise ValueError(f"a RoPE table cannot be on {t.device}")
+    if torch.device(device).type != "cuda":
+        raise ValueError(f"a RoPE table cannot be on {device}")
+    with torch.cuda.stream(stream):  # (None: as it is)
+        t = torch.empty((max_positions, rotary_dim // 2, 2), dtype=torch.float32, device=device)
     sc = PaRopeScaling(ROPE_SCALINGS.get(scaling, 0), original_positions, factor, low, high,
                        attention)
     _call_on(t.get_device(), "pa_rope_table_init_scaled", stream, t.data_ptr(), max_positions,
