@@ -136,8 +136,8 @@ int launch_decode_tails(const DecodeCall &c, void *workspace, const DecodeTails 
 // A prefix is read once for its group if that saves at least this many blocks
 // of a KV head, else by each sequence with the rest of its context (a single
 // sequence has nothing to share).  Eight sequences over 128 shared tokens, 56
-// blocks: 14.8 us shared and 15.0 not with 4/2 heads of 64, 18.6 and 18.8 with 32/32
-// of 128; two over 256, 16 blocks, 64/8 of 128: 16.6 and 24.0.
+// blocks: 14.7 us shared and 14.3 not with 4/2 heads of 64, 18.6 and 18.8 with 32/32
+// of 128; two over 256, 16 blocks, 64/8 of 128: 16.6 and 22.8.
 constexpr int kMinSavedBlocks = 8;
 
 __device__ __forceinline__ int shared_of(int blocks, int members) {

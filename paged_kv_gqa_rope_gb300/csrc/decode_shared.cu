@@ -1,4 +1,29 @@
 // Decode of sequences that share a prefix (pa_decode_shared).
+//
+// A group's n sequences name the same first blocks, so its n g query rows of a KV
+// head (g Q heads each) meet the same K and V: out = softmax(q K^T) V over prefix and
+// own tokens is joined from parts that each leave the row's maximum m, sum l and
+// unnormalised O,
+//     M = max m_i,   out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// Three kernels:
+//   prefix  (below) the shared blocks, read once a group, on the tensor cores:
+//           tiles of 128 query rows (128 / g sequences) x 128 keys, two tiles of rows
+//           a unit, the units' key tiles laid on one line and cut evenly between the
+//           CTAs of some of the SMs;
+//   tails   decode.cu's kernel over what each sequence has behind them, on the other
+//           SMs: it is launched as the prefix kernel's programmatic dependent and does
+//           not wait for it;
+//   join    one row's records after another, of the tail and of the pieces into which
+//           CTA ranges cut the row's unit.
+// The prefix kernel's CTAs each work out the plan (every CTA the same): which groups
+// share enough, the line, and how the SMs are divided, by the work of both sides.
+//
+// Bound: HBM for up to 128 query rows a KV head (each key tile of 64 KB serves them
+// all: 32 sequences, 32/32 heads, 65536 tokens at 6.1 TB/s), the tensor cores above
+// (128 sequences, 64/8 heads, 65536 tokens at 1100 TFLOP/s; an issuing thread is held
+// 1370 cycles a job of 128 x 128 x 128 twice, at the 1.5 GHz that the power limit
+// leaves).  Serving batches of 8192 shared tokens are bound by latencies: about 5 us
+// for the plan, 3 to the first tile, 2 a record, 5 for the join.
 #include <algorithm>
 #include <mutex>
 

@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(kSelThreads, C > 4 ? 1 : 2)
                 }
             };
 #pragma unroll
-            for (int c = 0; c < C; ++c) count(first + c * kChunk, x[c]);
+            for (int c = 0; c < C; ++c)
+                if (first + c * kChunk < hi) count(first + c * kChunk, x[c]);
             for (unsigned c0 = first + C * kChunk; c0 < hi; c0 += kChunk) {
                 float y[kSelItems];
                 load(c0, y);
@@ -233,9 +234,9 @@ __global__ void __launch_bounds__(kSelThreads, C > 4 ? 1 : 2)
             const int upto = warp_sums(mine, lane);
             if (lane == 31) warp_total[warp] = upto;
             __syncthreads();
-            int before = upto - mine;
-#pragma unroll
-            for (int v = 0; v < kSelWarps; ++v) before += v < warp ? warp_total[v] : 0;
+            const int warps = warp_sums(lane < kSelWarps ? warp_total[lane] : 0, lane);
+            const int ahead = __shfl_sync(0xffffffffu, warps, max(warp - 1, 0));
+            int before = upto - mine + (warp ? ahead : 0);
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
                 if (before < want && want <= before + cnt[j]) {
@@ -296,6 +297,9 @@ __global__ void __launch_bounds__(kSelThreads, C > 4 ? 1 : 2)
     Counts v[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
+        v[c] = 0;
+        if (lane == 31) sums[c * kSelWarps + warp] = 0;
+        if (first + c * kChunk >= last) continue;
         const Counts mine = counts(first + c * kChunk, x[c]), upto = warp_sums(mine, lane);
         if (lane == 31) sums[c * kSelWarps + warp] = upto;
         v[c] = upto - mine;
@@ -324,7 +328,9 @@ __global__ void __launch_bounds__(kSelThreads, C > 4 ? 1 : 2)
     }
     if (tid == 0 && rank == 0) a.moved[pair] = same ? ~k : k;
 #pragma unroll
-    for (int c = 0; c < C; ++c) place(first + c * kChunk, x[c], base + sums[c * kSelWarps + warp] + v[c]);
+    for (int c = 0; c < C; ++c)
+        if (first + c * kChunk < last)
+            place(first + c * kChunk, x[c], base + sums[c * kSelWarps + warp] + v[c]);
     Counts total = (Counts)(unsigned)mine_of[0] | (Counts)(unsigned)mine_of[1] << 32;
     for (unsigned c0 = first + C * kChunk; c0 < last; c0 += kChunk) {  // (one CTA)
         float y[kSelItems];
