@@ -221,6 +221,23 @@ __device__ __forceinline__ PlanGroup load_group(const Groups &g, const int32_t *
 // block (8 KB at d = 128, about 0.14 us with two decode CTAs an SM).
 constexpr int kTileCost = 8;  // of kTileWeight places
 
+__device__ __forceinline__ int divide_sms(unsigned long long places, unsigned long long tail,
+                                          int active, int64_t units, int sms) {
+    if (places == 0) return 0;
+    int n = sms, most = sms;
+    if (tail > 0) {
+        most = sms - 1;
+        const float cost = (float)places * ((float)kTileCost / kTileWeight);
+        n = max(1, min(most, (int)((float)sms * cost / (cost + (float)tail) + 0.5f)));
+    }
+    // Of one group every unit is alike: a multiple of them cuts none but at its ends.
+    if (active == 1 && units <= most) {
+        const int u = (int)units, even = max(1, (n + u / 2) / u) * u;
+        n = even <= most ? even : even - u;
+    }
+    return n;
+}
+
 // By a whole CTA of `threads` threads after read_groups; `sums` are three words of
 // shared memory.  Every CTA comes to the same.  Returns the SMs for the prefixes; total: places of their line.
 __device__ __forceinline__ int plan_sms(const Groups &groups, const int32_t *context_lens, int Hk,
@@ -252,25 +269,9 @@ __device__ __forceinline__ int plan_sms(const Groups &groups, const int32_t *con
         atomicAdd(&sums[2], alone);
     }
     __syncthreads();
-    tail = sums[0];
     total = (int64_t)sums[1] * Hk;
-    if (total == 0) return 0;
-    int n = sms, most = sms;
-    if (tail > 0) {
-        most = sms - 1;
-        const float cost = (float)sums[1] * ((float)kTileCost / kTileWeight);
-        n = max(1, min(most, (int)((float)sms * cost / (cost + (float)tail) + 0.5f)));
-    }
-    // Of one group every unit is alike: a multiple of them cuts none but at its ends.
     alone = sums[2];
-    if ((uint32_t)alone == 1) {
-        const int64_t units = (int64_t)(alone >> 32) * Hk;
-        if (units <= most) {
-            const int u = (int)units, even = max(1, (n + u / 2) / u) * u;
-            n = even <= most ? even : even - u;
-        }
-    }
-    return n;
+    return divide_sms(sums[1], sums[0], (int)(uint32_t)alone, (int64_t)(alone >> 32) * Hk, sms);
 }
 
 }  // namespace pa

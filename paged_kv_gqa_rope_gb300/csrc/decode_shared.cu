@@ -25,6 +25,7 @@
 // leaves).  Serving batches of 8192 shared tokens are bound by latencies: about 5 us
 // for the plan, 3 to the first tile, 2 a record, 5 for the join.
 #include <algorithm>
+#include <climits>
 #include <mutex>
 
 #include "decode_modes.cuh"
@@ -180,10 +181,10 @@ struct PrefixWalk {
                 unit = 0;
             }
             // the tiles whose first place is in the range
-            const int wt = seg.p.weight;
-            seg.t0 = (int)((uint32_t)(t0 + wt - 1) / (uint32_t)wt);
-            const int64_t end = t0 + left < seg.p.span() ? (t0 + left + wt - 1) / wt : seg.p.tiles;
-            seg.tiles = (int)min(end, (int64_t)seg.p.tiles) - seg.t0;
+            const uint32_t wt = seg.p.weight, span = seg.p.span();
+            const uint32_t to = t0 + left < span ? (uint32_t)(t0 + left) : span;
+            seg.t0 = (int)((t0 + wt - 1) / wt);
+            seg.tiles = min((int)((to + wt - 1) / wt), seg.p.tiles) - seg.t0;
             seg.kvh = unit / seg.p.units;
             seg.member0 = (unit - seg.kvh * seg.p.units) * 2 * mpt;
             seg.pair = seg.p.members - seg.member0 > mpt;
@@ -280,6 +281,125 @@ __device__ __forceinline__ void write_plan(const SharedArgs &a, const int32_t *s
     }
 }
 
+// The plan of up to 32 groups: every warp keeps them in its lanes, and one barrier is
+// all the CTA needs (the steps for more groups, one after another, take 4 us).
+struct FewGroups {
+    unsigned long long tail[kPrefixThreads / 32];
+    int lead[32];  // set to INT_MAX before the kernel's first barrier
+};
+
+__device__ __forceinline__ PlanCut plan_few(const SharedArgs &a, FewGroups *few, int tid) {
+    const int lane = tid & 31, n = a.groups.n, maxb = a.groups.maxb;
+    const int mpt = kPrefixTile / a.g, per_unit = 2 * mpt;
+    // ---- all that is read, at once
+    const int mine = min(lane, n - 1);
+    int ctx = __ldg(a.context_lens + min(tid, a.B - 1));
+    const int g0 = __ldg(a.groups.starts + mine), g1 = __ldg(a.groups.starts + mine + 1);
+    const int named = __ldg(a.groups.blocks + mine);
+    const bool broken = __any_sync(0xffffffffu, g0 > g1 || (lane == 0 && g0 != 0) ||
+                                                    (mine == n - 1 && g1 != a.B));
+    const bool in_range = named >= 0 && named <= maxb;
+    const int kept = in_range ? shared_of(named, g1 - g0) : -1;
+    // A sequence's group, shared blocks (-1: left out) and tokens behind them.
+    auto sequence = [&](int s, int len, int &r, int &skip, int &own) {
+        r = 0;
+        for (int i = 0; i < n - 1; ++i) r += __shfl_sync(0xffffffffu, g1, i) <= s;
+        const int want = __shfl_sync(0xffffffffu, named, r), k = __shfl_sync(0xffffffffu, kept, r);
+        const bool fine = !broken && k >= 0 && len >= 1 && len <= maxb * kBlockSize &&
+                          len >= want * kBlockSize;
+        skip = fine ? k : -1;
+        own = fine ? len - k * kBlockSize : 0;
+    };
+    unsigned long long tail = 0;
+    int bad = broken;
+    const int rounds = (a.B + kPrefixThreads - 1) / kPrefixThreads;
+    for (int i = 0; i < rounds; ++i) {
+        const int s = i * kPrefixThreads + tid;
+        if (i > 0) ctx = __ldg(a.context_lens + min(s, a.B - 1));
+        int r, skip, own;
+        sequence(min(s, a.B - 1), ctx, r, skip, own);
+        if (s >= a.B) continue;
+        bad |= skip < 0;
+        if (skip > 0) atomicMin(&few->lead[r], s);
+        if (own > 0) tail += (unsigned)((own + kBlockSize - 1) / kBlockSize + kTailCost);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) tail += __shfl_xor_sync(0xffffffffu, tail, o);
+    if (lane == 0) few->tail[tid >> 5] = tail;
+    bad = __syncthreads_or(bad);
+    if (bad && blockIdx.x == 0 && tid == 0) report(a.status, PA_DEV_BAD_LENGTH);
+    // ---- the groups' places on the line, and this CTA's
+    tail = 0;
+#pragma unroll
+    for (int i = 0; i < kPrefixThreads / 32; ++i) tail += few->tail[i];
+    PlanGroup p;
+    p.s0 = g0;
+    p.members = g1 - g0;
+    p.lead = few->lead[lane];
+    p.blocks = lane < n && p.lead != INT_MAX ? kept : 0;
+    p.tiles = (p.blocks + kTileBlocks - 1) / kTileBlocks;
+    p.units = (p.members + per_unit - 1) / per_unit;
+    p.weight = p.members > mpt ? kPairWeight : kTileWeight;
+    const int64_t places = p.tiles > 0 ? (int64_t)p.span() * p.units * a.Hk : 0;
+    int64_t end = places;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += y;
+    }
+    const int64_t start = end - places, total = __shfl_sync(0xffffffffu, end, 31);
+    const uint32_t active = __ballot_sync(0xffffffffu, places > 0);
+    const int64_t units = (int64_t)__shfl_sync(0xffffffffu, p.units, active ? __ffs(active) - 1 : 0) * a.Hk;
+    const int sms = divide_sms((unsigned long long)(total / a.Hk), tail, __popc(active), units, a.G);
+    const int G = plan_ctas(total, sms);
+
+    if (blockIdx.x == 0) {  // what the tails' kernel and the join need
+        if (tid == 0) *a.head = {total, G, sms < a.G ? 2 * (a.G - sms) : a.G};
+        for (int i = 0; i < rounds; ++i) {
+            const int s = i * kPrefixThreads + tid;
+            if (rounds > 1) ctx = __ldg(a.context_lens + min(s, a.B - 1));
+            int r, skip, own;
+            sequence(min(s, a.B - 1), ctx, r, skip, own);
+            const int in_group = s - __shfl_sync(0xffffffffu, p.s0, r);
+            const int span = __shfl_sync(0xffffffffu, p.span(), r);
+            const int tiles = __shfl_sync(0xffffffffu, p.tiles, r);
+            const int u = in_group / per_unit, in = in_group - u * per_unit;
+            SeqPlan x = {};
+            x.tail = own;
+            x.skip = max(skip, 0);
+            x.state = skip < 0 ? kLeftOut : tiles > 0 ? kInGroup : kAlone;
+            x.local = in / mpt * kPrefixTile + in % mpt * a.g;
+            x.start = __shfl_sync(0xffffffffu, start, r) + (int64_t)u * span;
+            x.stride = (int64_t)span * __shfl_sync(0xffffffffu, p.units, r);
+            x.last = (tiles - 1) * __shfl_sync(0xffffffffu, p.weight, r);
+            if (s < a.B) a.seqs[s] = x;
+        }
+        __threadfence();
+        __syncthreads();
+        griddep_launch_dependents();
+    }
+
+    PlanCut cut = {};
+    if ((int)blockIdx.x < G) {
+        const int64_t at = plan_cut(total, blockIdx.x, G);
+        cut.places = plan_cut(total, blockIdx.x + 1, G) - at;
+        const int r = __ffs(__ballot_sync(0xffffffffu, start <= at && at < end)) - 1;
+        cut.group = r;
+        cut.p.tiles = __shfl_sync(0xffffffffu, p.tiles, r);
+        cut.p.blocks = __shfl_sync(0xffffffffu, p.blocks, r);
+        cut.p.s0 = __shfl_sync(0xffffffffu, p.s0, r);
+        cut.p.members = __shfl_sync(0xffffffffu, p.members, r);
+        cut.p.lead = __shfl_sync(0xffffffffu, p.lead, r);
+        cut.p.units = __shfl_sync(0xffffffffu, p.units, r);
+        cut.p.weight = __shfl_sync(0xffffffffu, p.weight, r);
+        const int64_t off = at - __shfl_sync(0xffffffffu, start, r);
+        const int span = cut.p.span();
+        cut.unit = (int)(total < kShortLine ? (uint32_t)off / (uint32_t)span : off / span);
+        cut.t0 = (int)(off - (int64_t)cut.unit * span);
+    }
+    return cut;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap qmap,
@@ -295,6 +415,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + L::kMisc + 1023) & ~static_cast<uintptr_t>(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    if (tid < 32) reinterpret_cast<FewGroups *>(stats)->lead[tid] = INT_MAX;
     if (tid == 0) {
         mbar_init(&bar[B_QFULL], 1);
         mbar_init(&bar[B_QEMPTY], 2);
@@ -334,13 +455,18 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     if (blockIdx.x != 0) griddep_launch_dependents();
     const uint32_t tmem = *tmem_slot;  // S_0 | S_1 | O_0 | O_1
     const int mpt = kPrefixTile / a.g;
-    // ---- the plan, with the room of the tiles for the sequences' lengths.  What its
-    // steps read first is asked for at once, so that they find it in L1.
-    touch(a.context_lens + min(tid, a.B - 1));
-    touch(a.groups.starts + min(tid, a.groups.n));
-    touch(a.groups.blocks + min(tid, a.groups.n - 1));
-    PlanCut *cut = reinterpret_cast<PlanCut *>(stats);
-    {
+    // ---- the plan
+    PlanCut cut;
+    if (a.groups.n <= 32) {
+        cut = plan_few(a, reinterpret_cast<FewGroups *>(stats), tid);
+        __syncthreads();  // (stats are free)
+    } else {
+        // with the room of the tiles for the sequences' lengths; what the steps read
+        // first is asked for at once, so that they find it in L1
+        touch(a.context_lens + min(tid, a.B - 1));
+        touch(a.groups.starts + min(tid, a.groups.n));
+        touch(a.groups.blocks + min(tid, a.groups.n - 1));
+        PlanCut *shared_cut = reinterpret_cast<PlanCut *>(stats);
         int32_t *skip = reinterpret_cast<int32_t *>(smem), *lens = skip + a.B;
         const int bad = read_groups(a.groups, a.context_lens, a.B, skip, lens, tid, kPrefixThreads);
         if (bad && blockIdx.x == 0 && tid == 0) report(a.status, PA_DEV_BAD_LENGTH);
@@ -348,7 +474,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         const int sms = plan_sms(a.groups, a.context_lens, a.Hk, a.g, a.B, lens, kTailCost, a.G,
                                  bad == 2, plan_sums, tid, kPrefixThreads, total);
         const int G = plan_ctas(total, sms);
-        if (tid == 0) cut->places = 0;
+        if (tid == 0) shared_cut->places = 0;
         __syncthreads();
         if (blockIdx.x == 0) {
             write_plan(a, skip, lens, bad == 2, total, sms, G, tid);
@@ -356,14 +482,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             __syncthreads();
             griddep_launch_dependents();
         }
-        if (warp == 0 && (int)blockIdx.x < G) find_cut(a, cut, total, G, lane);
+        if (warp == 0 && (int)blockIdx.x < G) find_cut(a, shared_cut, total, G, lane);
         // (the tiles' room was written by the threads, and will be by TMA)
         tc::fence_proxy_async_smem();
         __syncthreads();
+        cut = *shared_cut;
+        __syncthreads();  // (stats are free)
     }
     PrefixWalk w;
-    w.begin(*cut);
-    __syncthreads();  // (stats, where it stood, are free)
+    w.begin(cut);
     auto s_col = [](int t) { return (uint32_t)(t * kPrefixTile); };
     auto o_col = [](int t) { return (uint32_t)(2 * kPrefixTile + t * D); };
 
