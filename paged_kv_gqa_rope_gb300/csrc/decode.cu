@@ -328,7 +328,7 @@ __device__ __forceinline__ void emit(const DecodeArgs &a, int s, int kvh, int h,
             a.out[row * D + d] = __float2half_rn(L > 0.f ? O / L : 0.f);
         } else {  // (NaN stays NaN; a row whose blocks are all out of range is 0)
             const bool none = L == 0.f;
-            a.out[row * D + d] = __float2half_rn(none ? 0.f : O / L);
+            a.out[row * D + d] = __float2half_rn(none ? 0.f : saturate16(O / L));
             if (MODE == Mode::kScores && d == 0)
                 a.sc.stats[row] = none ? make_float2(0.f, 0.f) : make_float2(M - kPShift, 1.f / L);
         }

@@ -102,6 +102,13 @@ __device__ __forceinline__ int plan_cta(int64_t t, int64_t total, int G) {
     return (int)(((t + 1) * G + total - 1) / total) - 1;
 }
 
+// The output's rounding.  P is rounded to fp16 on its way to P V and its sum is
+// not, so an average of values at the end of fp16's range can come out past it:
+// finite ones are saturated.
+__device__ __forceinline__ float saturate16(float x) {
+    return fabsf(x) < INFINITY ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
+}
+
 // A decode call as its entry point has checked it.
 struct DecodeCall {
     const void *q;

@@ -330,6 +330,26 @@ def test_shared_in_a_graph_and_on_a_stream():
     assert_attention_close(out, want)
 
 
+def test_shared_flat_history():
+    """65536 keys of equal weight and values of one sign, whose sums grow as they can."""
+    b = SharedBatch(17, 8, 1, 128, [(4096, [5, 40])])
+    b.pool[0] = 0
+    b.pool[1] = 0.5 + 0.01 * b.pool[1].astype(np.float32)
+    assert_attention_close(b.run(), b.want())
+
+
+@pytest.mark.parametrize("value", [65504, -65504])
+def test_values_at_the_end_of_the_range(value):
+    """Averages of finite values stay finite: within a rounding of P (2^-11) of V's."""
+    b = SharedBatch(16, 8, 2, 128, [(40, [9, 300, 0]), (0, [77])], std=3.0)
+    b.pool[1] = value
+    w = WeightBatch(16, 8, 2, 128, [300, 9], std=3.0)
+    w.pool[1] = value
+    for out in (b.run(), w.run()[0]):
+        out = out.float().cpu().numpy()
+        assert np.isfinite(out).all() and np.abs(out - value).max() <= 65504 * 2.0 ** -11 + 16
+
+
 def test_shared_nan_reaches_its_own_rows_alone():
     b = SharedBatch(15, 4, 2, 64, [(20, [3, 9, 1])])
     b.q[1, 3, 5] = np.nan
