@@ -696,7 +696,8 @@ int pa_rope_table_init_scaled(void *device_table, int max_positions, int rotary_
  * rise from 0 to num_seqs leave all outputs so.  Shared blocks whose id is out
  * of range set PA_DEV_BAD_BLOCK and drop out of the group's attention, as in
  * pa_decode.  Other arguments, results and limits are those of pa_decode, and
- * num_seqs * n_kv_heads <= 262144.
+ * num_seqs * n_kv_heads <= 262144.  The size is 0 for non-positive arguments and
+ * one past SIZE_MAX.
  */
 size_t pa_decode_shared_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads, int head_dim);
 int pa_decode_shared(const void *q, const pa_cache_t *cache, int layer,

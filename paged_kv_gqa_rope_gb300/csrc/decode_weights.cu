@@ -102,9 +102,11 @@ extern "C" size_t pa_decode_weights_workspace_bytes(int num_seqs, int n_heads, i
                                                     int head_dim, int64_t score_blocks) {
     if (num_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || score_blocks <= 0)
         return 0;
+    // (the parts first: each must fit by itself before it is counted in 64 bits)
     const unsigned __int128 n = (unsigned __int128)score_blocks * kBlockSize * n_heads * 4 +
-                                fixed_bytes(num_seqs, n_heads, head_dim);
-    return n > SIZE_MAX ? 0 : (size_t)n;
+                                (unsigned __int128)num_seqs * n_heads * sizeof(float2);
+    if (n > SIZE_MAX / 2) return 0;
+    return (size_t)score_blocks * kBlockSize * n_heads * 4 + fixed_bytes(num_seqs, n_heads, head_dim);
 }
 
 extern "C" int pa_decode_weights(const void *q, const pa_cache_t *cache, int layer,

@@ -245,6 +245,9 @@ def test_workspace_sizes(libpa):
     assert libpa.pa_decode_weights_workspace_bytes(4, 8, 2, 64, 11) == one + 10 * 16 * 8 * 4
     assert libpa.pa_decode_weights_workspace_bytes(4, 8, 2, 64, 0) == 0
     assert libpa.pa_decode_weights_workspace_bytes(4, 8, 2, 64, 2**60) == 0  # past 64 bits
+    assert libpa.pa_decode_weights_workspace_bytes(INT_MAX, INT_MAX, 2, 64, 1) == 0
+    assert libpa.pa_decode_shared_workspace_bytes(INT_MAX, INT_MAX, 2, 64) == 0
+    assert libpa.pa_decode_shared_workspace_bytes(INT_MAX, 8, 2, INT_MAX) == 0
     assert libpa.pa_kv_evict_workspace_bytes(3, 2, 100) >= 3 * 2 * 100 * 8
     assert libpa.pa_kv_evict_workspace_bytes(3, 2, 0) == 0
     assert libpa.pa_kv_evict_workspace_bytes(INT_MAX, INT_MAX, INT_MAX) == 0
