@@ -962,9 +962,11 @@ using namespace pa;
 extern "C" size_t pa_decode_shared_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads,
                                                    int head_dim) {
     if (num_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0) return 0;
-    if ((unsigned __int128)num_seqs * n_heads * (head_dim + (int64_t)4) * sizeof(float) > SIZE_MAX / 4)
-        return 0;
-    return up256(mode_workspace_bytes(head_dim)) + 256 + up256((size_t)num_seqs * sizeof(SeqPlan)) + 2 * rows_bytes(num_seqs, n_heads, head_dim) +
+    const unsigned __int128 row_bytes = (head_dim + (int64_t)4) * sizeof(float);
+    if (row_bytes * num_seqs * n_heads > SIZE_MAX / 4) return 0;
+    return up256(mode_workspace_bytes(head_dim)) + 256 +
+           up256((size_t)num_seqs * sizeof(SeqPlan)) +
+           2 * rows_bytes(num_seqs, n_heads, head_dim) +
            rows_bytes(kMaxCtas, 2 * kPrefixTile, head_dim);
 }
 
