@@ -59,6 +59,7 @@ constexpr int kThreads = (kConsumerWarps + 1) * 32;
 constexpr int kMaxSeqs = 4096;
 constexpr int kGroupPad = 8;   // MMA N: Q heads per KV head, padded
 constexpr int kMaxGrid = 608;  // CTAs the workspace has record slots for (4 per SM)
+static_assert(kMaxGrid == kModeCtas && kGroupPad == kModeRows, "the tails' records");
 
 struct DecodeArgs {
     const __half *q;              // [B][H][D]
@@ -310,6 +311,10 @@ __device__ __forceinline__ T load_meta(const T *p) {
         return __ldg(p);
 }
 
+__device__ __forceinline__ Record tail_record(const DecodeArgs &a, int s, int kvh, int h) {
+    return {a.tl.rec, (int64_t)a.B * a.H, ((int64_t)kvh * a.B + s) * a.g + h};
+}
+
 // One element (head h of the pair, value d) of a finished pair: O unnormalised,
 // M the maximum, L the sum of the row; alone: nothing to be joined with it.
 template <int D, Mode MODE>
@@ -317,12 +322,9 @@ __device__ __forceinline__ void emit(const DecodeArgs &a, int s, int kvh, int h,
                                      float M, float L, bool alone) {
     const int64_t row = (int64_t)s * a.H + kvh * a.g + h;
     if (MODE == Mode::kTails && !alone) {
-        float *r = a.tl.rec + row * (D + 4);
-        r[d] = O;
-        if (d == 0) {
-            r[D] = M - kPShift;
-            r[D + 1] = L;
-        }
+        const Record r = tail_record(a, s, kvh, h);
+        reinterpret_cast<float *>(r.cols(d >> 2))[d & 3] = O;
+        if (d == 0) *r.stat<D>() = make_float2(M - kPShift, L);
     } else {
         if constexpr (MODE == Mode::kOut) {
             a.out[row * D + d] = __float2half_rn(L > 0.f ? O / L : 0.f);
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     // has not consumed yet (the mbarrier parity would alias that wait onto
     // the earlier, completed phase).
     static_assert(NSTAGE % kConsumerWarps == 0, "stages must be a multiple of consumer warps");
-    constexpr int kCost = I8 ? kPairCostI8 : kPairCost;
+    constexpr int kCost = I8 ? kPairCostI8 : MODE == Mode::kTails ? kTailCost : kPairCost;
     using L = Layout<D, I8>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -956,11 +958,13 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
         // value is needed after the barrier.)
         int c_first = 0, c_last = 0, nrec = 1, arrived = -1;
         bool may_close = false;
+        [[maybe_unused]] bool left = false;  // kTails: in pieces, for the kernel that joins them
         if (!whole) {
             c_first = cta_of(sg.pair_start, W, G);
             c_last = cta_of(sg.pair_end - 1, W, G);
             nrec = c_last - c_first + 1;
-            may_close = pos + sg.nu == end && nrec <= kConsumerWarps;
+            if constexpr (MODE == Mode::kTails) left = !alone && nrec <= kTailPieces;
+            may_close = !left && pos + sg.nu == end && nrec <= kConsumerWarps;
             if (may_close && tid == 0) arrived = ld_acquire_gpu(a.counters + s * a.Hk + kvh);
         }
         named_barrier_sync(1, kCons);
@@ -971,7 +975,33 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
         const bool close = sm_flag[2] != 0;
         const bool last_seg = pos + sg.nu == end;
 
-        if (whole) {
+        if constexpr (MODE == Mode::kTails)
+            if (!alone && b0 == 0 && tid == 0)
+                a.tl.pieces[s * a.Hk + kvh] = left ? (c_first + 1) | (nrec - 1) << 16 : 0;
+        if (MODE == Mode::kTails && !alone && (whole || left)) {
+            // (four values a thread at a time)
+            for (int idx = tid; idx < a.g * (D / 4); idx += kCons) {
+                const int h = idx / (D / 4), d = (idx - h * (D / 4)) * 4;
+                const Record r =
+                    b0 == 0 ? tail_record(a, s, kvh, h)
+                            : Record{a.rec + (int64_t)cta * 2 * kGroupPad * L::kRec, kGroupPad, h};
+                float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int wv = 0; wv < kConsumerWarps; ++wv) {
+                    const float f = sm_m[wv * kGroupPad + h];
+                    const float4 x =
+                        *reinterpret_cast<const float4 *>(sm_o + (wv * kGroupPad + h) * D + d);
+                    O.x = __fmaf_rn(f, x.x, O.x);
+                    O.y = __fmaf_rn(f, x.y, O.y);
+                    O.z = __fmaf_rn(f, x.z, O.z);
+                    O.w = __fmaf_rn(f, x.w, O.w);
+                }
+                *r.cols(d / 4) = O;
+                if (d == 0)
+                    *r.template stat<D>() = make_float2(sm_l[kGroupPad + h] - kPShift, sm_l[h]);
+            }
+            named_barrier_sync(1, kCons);  // the smem merge area is free again
+        } else if (whole) {
             for (int idx = tid; idx < a.g * D; idx += kCons) {
                 const int h = idx / D, d = idx - (idx / D) * D;
                 float O = 0.f;
@@ -1318,8 +1348,7 @@ int launch_mode(const DecodeCall &c, void *workspace, const DecodeScores &sc,
     a.context_lens = c.context_lens;
     a.out = static_cast<__half *>(c.out);
     a.counters = static_cast<int32_t *>(workspace);
-    a.rec = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
-                                      (size_t)kModePairs * sizeof(int32_t));
+    a.rec = mode_records(workspace);
     a.status = c.dev_status;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.B = c.num_seqs;
@@ -1334,6 +1363,11 @@ int launch_mode(const DecodeCall &c, void *workspace, const DecodeScores &sc,
 }
 
 }  // namespace
+
+float *mode_records(void *workspace) {
+    return reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
+                                     (size_t)kModePairs * sizeof(int32_t));
+}
 
 size_t mode_workspace_bytes(int head_dim) {
     const size_t rec = cta_record_bytes(head_dim > 128 ? head_dim : 128);

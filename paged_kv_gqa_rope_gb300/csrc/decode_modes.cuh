@@ -66,11 +66,32 @@ struct alignas(16) PlanHead {
     int tail_ctas;  // CTAs of the tails' kernel
 };
 
+// Records of rows, with four columns of all of them side by side ([D / 4][rows][4],
+// then {m, l}[rows]): neither the threads that write them, one a row, nor those that
+// read them leave a line half used.
+struct Record {
+    float *base;
+    int64_t rows, row;
+    __device__ __forceinline__ float4 *cols(int i) const {  // columns 4 i .. 4 i + 3
+        return reinterpret_cast<float4 *>(base) + i * rows + row;
+    }
+    template <int D>
+    __device__ __forceinline__ float2 *stat() const {
+        return reinterpret_cast<float2 *>(base + D * rows) + row;
+    }
+};
+
 // Records in the place of the output, over the tokens behind the shared blocks
 // (pa_decode_shared): unnormalised O, then m and l of the row.  A sequence with no
-// shared blocks gets its output.
+// shared blocks gets its output.  A pair (sequence, KV head) that the CTAs' ranges cut
+// into at most kTailPieces pieces is left in them: the first in its place in rec, the
+// others in their CTAs' records, where its readers join them with what they join
+// anyway (pieces merged by the last to arrive: 3.7 us a piece, 1.5 a whole pair).
+constexpr int kTailPieces = 8;
+constexpr int kTailCost = 6;  // units of a pair's fixed cost on the tails' line (a block: 1)
 struct DecodeTails {
-    float *rec;  // [B][H][D + 4]
+    float *rec;       // rows (KV head, sequence, Q head of the KV head), as Record has them
+    int32_t *pieces;  // [B][Hk]: CTA of the second piece | pieces but the first << 16
     // by the prefix kernel, ahead of its launch_dependents
     const PlanHead *head;
     const SeqPlan *seqs;  // [B]
@@ -136,7 +157,10 @@ int check_decode_args(const void *q, const pa_cache_t *cache, int layer,
 // place and of the same size whatever the call's shape, and nothing else is
 // written there: so one workspace serves calls of several shapes.
 constexpr int kModePairs = 1 << 18;  // (sequence, KV head) pairs with a counter
+constexpr int kModeCtas = 608;          // with two records each
 size_t mode_workspace_bytes(int head_dim);
+constexpr int kModeRows = 8;             // of D + 4 floats each
+float *mode_records(void *workspace);    // [2 * CTA + slot]
 int launch_decode_scores(const DecodeCall &c, void *workspace, const DecodeScores &sc);
 int launch_decode_tails(const DecodeCall &c, void *workspace, const DecodeTails &tl);
 

@@ -40,14 +40,13 @@ struct SharedArgs {
     const int32_t *context_lens;
     __half *out;
     Groups groups;
-    const float *tails;  // [B * H][D + 4]: records of the tails, in q's order
+    float *tails;  // records of the tails (DecodeTails), and the CTAs'
+    float *tail_recs;
+    const int32_t *tail_pieces;
     PlanHead *head;
     SeqPlan *seqs;
-    // Records of a unit's first piece, over rows (KV head, sequence, Q head of the
-    // KV head), and of the piece with which a CTA's range begins inside a unit, over
-    // the rows of two tiles.  Both have four columns of all rows side by side
-    // ([D / 4][rows][4], then {m, l}[rows]), so that neither the threads that write
-    // them (one a row) nor those that read them leave a line half used.
+    // Records of a unit's first piece, over the same rows, and of the piece with which
+    // a CTA's range begins inside a unit, over the rows of two tiles.
     float *first;  // [B * H rows]
     float *more;   // [G][256 rows]
     int32_t *status;
@@ -68,7 +67,6 @@ constexpr int kVProducerWarp = 11;
 constexpr int kPrefixThreads = 12 * 32;
 constexpr int kTmemCols = 512;
 constexpr float kRescale = 8.f;   // the maximum moves only when a tile raises it by more
-constexpr int kTailCost = 10;     // the decode kernel's units for a pair's fixed cost
 constexpr float kShift = 7.f;     // P = 2^(x - m + 7) <= 2^15
 constexpr int kValidRing = 16;    // tiles whose mask of blocks is kept
 
@@ -129,18 +127,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
-// A record of row `row` among `rows`: its columns 4 i .. 4 i + 3, and {m, l}.
-struct Record {
-    float *base;
-    int64_t rows, row;
-    __device__ __forceinline__ float4 *cols(int i) const {
-        return reinterpret_cast<float4 *>(base) + i * rows + row;
-    }
-    template <int D>
-    __device__ __forceinline__ float2 *stat() const {
-        return reinterpret_cast<float2 *>(base + D * rows) + row;
-    }
-};
+// Asks L2 for a line (a hint: what an earlier kernel still writes there is seen).
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
 // A load whose value nobody waits for.
 __device__ __forceinline__ void touch(const int32_t *p) {
@@ -437,6 +427,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             mbar_init(&bar[B_VEMPTY + i], 2);
         }
         fence_barrier_init();
+    }
+    if (warp == kVProducerWarp && lane < 4) {  // what the plan reads first
+        prefetch_l2(a.context_lens + min(lane * 32, a.B - 1));
+        if (lane == 0) prefetch_l2(a.groups.starts);
+        if (lane == 1) prefetch_l2(a.groups.blocks);
     }
     if (warp == kMmaWarp) {
         tc::alloc(tmem_slot, kTmemCols);
@@ -870,6 +865,7 @@ int launch_prefix(const SharedArgs &a, const pa_cache_t *cache, cudaStream_t st)
 }
 
 constexpr int kJoinThreads = 256;
+constexpr int kJoinBatch = 4;  // records in flight
 
 // Joins a row's records: a thread has four columns of a row, the 32 threads of a
 // warp the same columns of 32 rows (in the records' order), blockIdx.y the columns.
@@ -882,49 +878,45 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SharedArgs a) 
     const int64_t at = (int64_t)blockIdx.x * 32 + lane;  // (KV head, sequence, its Q head)
     if (at >= (int64_t)a.B * a.H) return;
     const int j = (int)at % a.g, s = (int)at / a.g % a.B, kvh = (int)at / a.g / a.B;
-    // (the tail's record does not wait for the plan, nor the pieces for each other)
-    const int64_t row = (int64_t)s * a.H + kvh * a.g + j;  // of q and out
-    const float *r = a.tails + row * (D + 4);
-    float2 st = __ldcg(reinterpret_cast<const float2 *>(r + D));
-    float4 O = __ldcg(reinterpret_cast<const float4 *>(r) + c4);
+    const int64_t row = (int64_t)s * a.H + kvh * a.g + j, rows = (int64_t)a.B * a.H;
+    // Every row that is not alone has a first piece; it and the tail's record do not
+    // wait for the plan, nor the other pieces for each other.
+    float2 ml[kJoinBatch];
+    float4 x[kJoinBatch];
+    auto take = [&](int i, const Record &r) {
+        ml[i] = __ldcg(r.template stat<D>());
+        x[i] = __ldcg(r.cols(c4));
+    };
+    auto none = [&](int i) {
+        ml[i] = make_float2(-INFINITY, 0.f);
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    take(0, {a.tails, rows, at});
+    take(1, {a.first, rows, at});
+    const int cut = __ldcg(a.tail_pieces + s * a.Hk + kvh);
     const SeqPlan p = a.seqs[s];
     const PlanHead head = *a.head;
     if (p.state != kInGroup) return;  // (alone: the tails' kernel has written it)
     const int64_t start = p.start + kvh * p.stride;
     const int c0 = plan_cta(start, head.total, head.ctas);
-    const int pieces = plan_cta(start + p.last, head.total, head.ctas) - c0 + 1;
-    if (p.tail == 0) {
-        st = make_float2(-INFINITY, 0.f);
-        O = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    float M = st.x, L = st.y;
-    constexpr int kBatch = 8;
-    for (int i0 = 0; i0 < pieces; i0 += kBatch) {
-        float2 ml[kBatch];
-        float4 x[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            ml[i] = make_float2(-INFINITY, 0.f);
-            x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i0 + i < pieces) {
-                const bool first = i0 + i == 0;
-                const Record rec = {
-                    first ? a.first : a.more + (int64_t)(c0 + i0 + i) * 2 * kPrefixTile * (D + 4),
-                    first ? (int64_t)a.B * a.H : 2 * kPrefixTile, first ? at : p.local + j};
-                ml[i] = __ldcg(rec.template stat<D>());
-                x[i] = __ldcg(rec.cols(c4));
-            }
-        }
+    const int more = plan_cta(start + p.last, head.total, head.ctas) - c0;
+    // the tail's pieces behind its first (what a call that gave up has not written may
+    // be anything)
+    const int cut_cta = cut & 0xffff, left = cut >> 16;
+    const int tail_more =
+        p.tail > 0 && left > 0 && left < kTailPieces && cut_cta + left <= kModeCtas ? left : 0;
+    if (p.tail == 0) none(0);
+    float M = -INFINITY, L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto join = [&](int n) {
         float top = M;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+        for (int i = 0; i < n; ++i) top = fmaxf(top, ml[i].x);
         auto factor = [&](float m) { return m == -INFINITY ? 0.f : ex2(m - top); };
         float f = factor(M);
         M = top;
         L *= f;
         O = make_float4(f * O.x, f * O.y, f * O.z, f * O.w);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
+        for (int i = 0; i < n; ++i) {
             f = factor(ml[i].x);
             L = fmaf(f, ml[i].y, L);
             O.x = fmaf(f, x[i].x, O.x);
@@ -932,6 +924,21 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SharedArgs a) 
             O.z = fmaf(f, x[i].z, O.z);
             O.w = fmaf(f, x[i].w, O.w);
         }
+    };
+    join(2);
+    for (int i0 = 0; i0 < tail_more + more; i0 += kJoinBatch) {
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) {
+            const int n = i0 + i;
+            if (n < tail_more)
+                take(i, {a.tail_recs + (int64_t)(cut_cta + n) * 2 * kModeRows * (D + 4), kModeRows, j});
+            else if (n < tail_more + more)
+                take(i, {a.more + (int64_t)(c0 + 1 + n - tail_more) * 2 * kPrefixTile * (D + 4),
+                         2 * kPrefixTile, p.local + j});
+            else
+                none(i);
+        }
+        join(kJoinBatch);
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;  // (no block in range: 0)
     *reinterpret_cast<uint2 *>(a.out + row * D + 4 * c4) =
@@ -966,6 +973,7 @@ extern "C" size_t pa_decode_shared_workspace_bytes(int num_seqs, int n_heads, in
     if (row_bytes * num_seqs * n_heads > SIZE_MAX / 4) return 0;
     return up256(mode_workspace_bytes(head_dim)) + 256 +
            up256((size_t)num_seqs * sizeof(SeqPlan)) +
+           up256((size_t)num_seqs * n_kv_heads * sizeof(int32_t)) +
            2 * rows_bytes(num_seqs, n_heads, head_dim) +
            rows_bytes(kMaxCtas, 2 * kPrefixTile, head_dim);
 }
@@ -1002,6 +1010,10 @@ extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int laye
     p += 256;
     a.seqs = reinterpret_cast<SeqPlan *>(p);
     p += up256((size_t)num_seqs * sizeof(SeqPlan));
+    int32_t *const pieces = reinterpret_cast<int32_t *>(p);
+    a.tail_pieces = pieces;
+    a.tail_recs = mode_records(at);
+    p += up256((size_t)num_seqs * n_kv_heads * sizeof(int32_t));
     float *const tails = reinterpret_cast<float *>(p);
     a.tails = tails;
     p += rows_bytes(num_seqs, n_heads, head_dim);
@@ -1029,7 +1041,7 @@ extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int laye
                           context_lens, num_seqs, n_heads, n_kv_heads, head_dim,
                           scale,    out,     dev_status, st};
     int rc2 = head_dim == 128 ? launch_prefix<128>(a, cache, st) : launch_prefix<64>(a, cache, st);
-    if (rc2 == PA_OK) rc2 = launch_decode_tails(c, at, DecodeTails{tails, a.head, a.seqs});
+    if (rc2 == PA_OK) rc2 = launch_decode_tails(c, at, DecodeTails{tails, pieces, a.head, a.seqs});
     if (rc2 != PA_OK) return rc2;
     return head_dim == 128 ? launch_join<128>(a, st) : launch_join<64>(a, st);
 }
