@@ -108,6 +108,11 @@ __device__ __forceinline__ bool mbar_wait2(uint64_t *b1, uint32_t p1, uint64_t *
     return (d1 || mbar_wait(b1, p1)) && (d2 || mbar_wait(b2, p2));
 }
 
+// Asks L2 for a line (a hint: what an earlier kernel still writes there is seen).
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {

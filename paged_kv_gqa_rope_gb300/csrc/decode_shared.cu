@@ -127,11 +127,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
-// Asks L2 for a line (a hint: what an earlier kernel still writes there is seen).
-__device__ __forceinline__ void prefetch_l2(const void *p) {
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
 // A load whose value nobody waits for.
 __device__ __forceinline__ void touch(const int32_t *p) {
     [[maybe_unused]] int32_t v;
