@@ -212,6 +212,22 @@ def test_shared_large_batch():
         assert_attention_close(b.run(), b.want())
 
 
+@pytest.mark.parametrize("H,Hk,d", [(1, 1, 64), (8, 1, 128), (6, 2, 128)])
+@pytest.mark.parametrize("blocks", [list(range(1, 13)), [9, 8, 1], [40, 2, 70], [3] * 90, [900, 1]])
+def test_shared_tails_in_pieces(H, Hk, d, blocks):
+    """Tails cut into one piece (a block a CTA where there are few) up to many: those
+    that the join takes from the CTAs' records, and those merged before it; alone ones
+    beside them.  The workspace has held other shapes; twice the same bits."""
+    ws = pa.decode_shared_workspace(128, H, Hk, d)
+    SharedBatch(7, H, Hk, d, [(20, [1 + 37 * i % 90 for i in range(100)])]).run(ws=ws)
+    b = SharedBatch(len(blocks), H, Hk, d, [(10, [16 * n - n % 3 for n in blocks]), (0, [50, 130])])
+    status = pa.new_status()
+    out = b.run(ws=ws, status=status)
+    assert int(status.item()) == 0
+    assert_attention_close(out, b.want())
+    assert torch.equal(out, b.run(ws=ws))
+
+
 def test_shared_scale_layer_and_large_scores():
     b = SharedBatch(3, 8, 2, 128, [(40, [9, 30, 1])], layers=3, layer=2, std=8.0)
     assert_attention_close(b.run(), b.want())
