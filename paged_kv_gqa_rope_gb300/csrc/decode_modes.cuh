@@ -88,7 +88,9 @@ struct Record {
 // others in their CTAs' records, where its readers join them with what they join
 // anyway (pieces merged by the last to arrive: 3.7 us a piece, 1.5 a whole pair).
 constexpr int kTailPieces = 8;
-constexpr int kTailCost = 6;  // units of a pair's fixed cost on the tails' line (a block: 1)
+// Units of a pair's fixed cost on the tails' line (a block: 1).  With 64/8, 32/32 and
+// 32/8 heads 6 took 30.3, 34.9 and 46.5 us, 5 31.7, 35.5 and 47.4, 8 29.6, 35.8 and 47.2.
+constexpr int kTailCost = 6;
 struct DecodeTails {
     float *rec;       // rows (KV head, sequence, Q head of the KV head), as Record has them
     int32_t *pieces;  // [B][Hk]: CTA of the second piece | pieces but the first << 16
@@ -167,8 +169,8 @@ int launch_decode_tails(const DecodeCall &c, void *workspace, const DecodeTails 
 // A prefix is read once for its group if that saves at least this many blocks
 // of a KV head, else by each sequence with the rest of its context (a single
 // sequence has nothing to share).  Eight sequences over 128 shared tokens, 56
-// blocks: 14.7 us shared and 14.3 not with 4/2 heads of 64, 18.6 and 18.8 with 32/32
-// of 128; two over 256, 16 blocks, 64/8 of 128: 16.6 and 22.8.
+// blocks: 12.1 us shared and 14.5 not with 4/2 heads of 64, 14.4 and 16.7 with 32/32
+// of 128; two over 256, 16 blocks, 64/8 of 128: 12.3 and 22.6.
 constexpr int kMinSavedBlocks = 8;
 
 __device__ __forceinline__ int shared_of(int blocks, int members) {

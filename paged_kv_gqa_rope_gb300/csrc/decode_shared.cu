@@ -19,8 +19,8 @@
 // share enough, the line, and how the SMs are divided, by the work of both sides.
 //
 // Bound: HBM for up to 128 query rows a KV head (each key tile of 64 KB serves them
-// all: 32 sequences, 32/32 heads, 65536 tokens at 6.1 TB/s), the tensor cores above
-// (128 sequences, 64/8 heads, 65536 tokens at 1100 TFLOP/s; an issuing thread is held
+// all: 32 sequences, 32/32 heads, 65536 tokens at 6.2 TB/s), the tensor cores above
+// (128 sequences, 64/8 heads, 65536 tokens at 1130 TFLOP/s; an issuing thread is held
 // 1370 cycles a job of 128 x 128 x 128 twice, at the 1.5 GHz that the power limit
 // leaves).  Serving batches of 8192 shared tokens are bound by latencies: about 2 us
 // for the plan, 4 to the first tile, 2 a record, 3 for the join.
