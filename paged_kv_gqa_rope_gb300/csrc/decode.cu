@@ -311,8 +311,9 @@ __device__ __forceinline__ T load_meta(const T *p) {
         return __ldg(p);
 }
 
-__device__ __forceinline__ Record tail_record(const DecodeArgs &a, int s, int kvh, int h) {
-    return {a.tl.rec, (int64_t)a.B * a.H, ((int64_t)kvh * a.B + s) * a.g + h};
+__device__ __forceinline__ Record first_record(const Pieces &p, const DecodeArgs &a, int s, int kvh,
+                                               int h) {
+    return {p.rec, (int64_t)a.B * a.H, ((int64_t)kvh * a.B + s) * a.g + h};
 }
 
 // One element (head h of the pair, value d) of a finished pair: O unnormalised,
@@ -322,9 +323,9 @@ __device__ __forceinline__ void emit(const DecodeArgs &a, int s, int kvh, int h,
                                      float M, float L, bool alone) {
     const int64_t row = (int64_t)s * a.H + kvh * a.g + h;
     if (MODE == Mode::kTails && !alone) {
-        const Record r = tail_record(a, s, kvh, h);
+        const Record r = first_record(a.tl.pieces, a, s, kvh, h);
         reinterpret_cast<float *>(r.cols(d >> 2))[d & 3] = O;
-        if (d == 0) *r.stat<D>() = make_float2(M - kPShift, L);
+        if (d == 0) *r.stat(D) = make_float2(M - kPShift, L);
     } else {
         if constexpr (MODE == Mode::kOut) {
             a.out[row * D + d] = __float2half_rn(L > 0.f ? O / L : 0.f);
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
         // where the second kernel finds a sequence's scores
         if (cta == 0)
             for (int s = tid; s < B; s += kThreads)
-                a.sc.first[s] = lens[s] == 0 ? -1
+                a.sc.first[s] = lens[s] == 0 ? -2
                                              : scores_start<kCost>(a, prefix, lens, s, a.status);
     }
     // With fewer blocks than CTAs only the first W CTAs get a (one-block)
@@ -958,12 +959,13 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
         // value is needed after the barrier.)
         int c_first = 0, c_last = 0, nrec = 1, arrived = -1;
         bool may_close = false;
-        [[maybe_unused]] bool left = false;  // kTails: in pieces, for the kernel that joins them
+        [[maybe_unused]] bool left = false;  // in pieces, for the next kernel (not kOut)
         if (!whole) {
             c_first = cta_of(sg.pair_start, W, G);
             c_last = cta_of(sg.pair_end - 1, W, G);
             nrec = c_last - c_first + 1;
-            if constexpr (MODE == Mode::kTails) left = !alone && nrec <= kTailPieces;
+            if constexpr (MODE == Mode::kScores) left = nrec <= kPieces;
+            if constexpr (MODE == Mode::kTails) left = !alone && nrec <= kPieces;
             may_close = !left && pos + sg.nu == end && nrec <= kConsumerWarps;
             if (may_close && tid == 0) arrived = ld_acquire_gpu(a.counters + s * a.Hk + kvh);
         }
@@ -975,16 +977,16 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
         const bool close = sm_flag[2] != 0;
         const bool last_seg = pos + sg.nu == end;
 
-        if constexpr (MODE == Mode::kTails)
-            if (!alone && b0 == 0 && tid == 0)
-                a.tl.pieces[s * a.Hk + kvh] = left ? (c_first + 1) | (nrec - 1) << 16 : 0;
-        if (MODE == Mode::kTails && !alone && (whole || left)) {
+        const Pieces &to = MODE == Mode::kScores ? a.sc.pieces : a.tl.pieces;
+        if constexpr (!kOut)
+            if ((MODE == Mode::kScores || !alone) && b0 == 0 && tid == 0)
+                to.cut[s * a.Hk + kvh] = left ? (c_first + 1) | (nrec - 1) << 16 : 0;
+        if (!kOut && (left || (MODE == Mode::kTails && !alone && whole))) {
             // (four values a thread at a time)
             for (int idx = tid; idx < a.g * (D / 4); idx += kCons) {
                 const int h = idx / (D / 4), d = (idx - h * (D / 4)) * 4;
                 const Record r =
-                    b0 == 0 ? tail_record(a, s, kvh, h)
-                            : Record{a.rec + (int64_t)cta * 2 * kGroupPad * L::kRec, kGroupPad, h};
+                    b0 == 0 ? first_record(to, a, s, kvh, h) : piece_of(a.rec, cta, D, h);
                 float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int wv = 0; wv < kConsumerWarps; ++wv) {
@@ -998,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                 }
                 *r.cols(d / 4) = O;
                 if (d == 0)
-                    *r.template stat<D>() = make_float2(sm_l[kGroupPad + h] - kPShift, sm_l[h]);
+                    *r.stat(D) = make_float2(sm_l[kGroupPad + h] - kPShift, sm_l[h]);
             }
             named_barrier_sync(1, kCons);  // the smem merge area is free again
         } else if (whole) {

@@ -8,15 +8,6 @@
 
 namespace pa {
 
-// Scores and row statistics besides the output (pa_decode_weights).
-struct DecodeScores {
-    float *scores;     // [blocks of all KV heads][16 tokens][g]: log2 units
-    float2 *stats;     // [B][H]: {m, 1 / l}, a weight being 2^(score - m) / l
-    int64_t *first;    // [B]: a sequence's first block in scores, -1: none kept
-    int64_t capacity;  // blocks of all KV heads that scores holds
-    int max_len;       // longest context that the rows of weights hold
-};
-
 // Sequences starts[r] .. starts[r + 1] - 1 name the same first blocks[r] blocks.
 struct Groups {
     const int32_t *starts;
@@ -75,25 +66,40 @@ struct Record {
     __device__ __forceinline__ float4 *cols(int i) const {  // columns 4 i .. 4 i + 3
         return reinterpret_cast<float4 *>(base) + i * rows + row;
     }
-    template <int D>
-    __device__ __forceinline__ float2 *stat() const {
-        return reinterpret_cast<float2 *>(base + D * rows) + row;
+    __device__ __forceinline__ float2 *stat(int d) const {
+        return reinterpret_cast<float2 *>(base + d * rows) + row;
     }
 };
 
-// Records in the place of the output, over the tokens behind the shared blocks
-// (pa_decode_shared): unnormalised O, then m and l of the row.  A sequence with no
-// shared blocks gets its output.  A pair (sequence, KV head) that the CTAs' ranges cut
-// into at most kTailPieces pieces is left in them: the first in its place in rec, the
-// others in their CTAs' records, where its readers join them with what they join
-// anyway (pieces merged by the last to arrive: 3.7 us a piece, 1.5 a whole pair).
-constexpr int kTailPieces = 8;
+// What the decode kernel's other modes leave for the kernel after it: a row's
+// unnormalised O, m and l.  A pair (sequence, KV head) that the CTAs' ranges cut into at
+// most kPieces pieces stays in them: the first in its place in rec, the others in their
+// CTAs' records.  (Merged by the last piece to arrive, a piece took 3.7 us against a
+// whole pair's 1.5, and the last CTAs of a launch were done 4 us later.)
+constexpr int kPieces = 8;
+struct Pieces {
+    float *rec;    // rows (KV head, sequence, Q head of the KV head), as Record has them
+    int32_t *cut;  // [B][Hk]: CTA of the second piece | pieces but the first << 16
+};
+
+// pa_decode_weights: scores and row statistics besides the output.  Of a pair left in
+// pieces (of no other) there are no statistics and no output.
+struct DecodeScores {
+    Pieces pieces;
+    float *scores;     // [blocks of all KV heads][16 tokens][g]: log2 units
+    float2 *stats;     // [B][H]: {m, 1 / l}, a weight being 2^(score - m) / l
+    int64_t *first;    // [B]: a sequence's first block in scores, -1: none kept, -2: left out
+    int64_t capacity;  // blocks of all KV heads that scores holds
+    int max_len;       // longest context that the rows of weights hold
+};
+
 // Units of a pair's fixed cost on the tails' line (a block: 1).  With 64/8, 32/32 and
 // 32/8 heads 6 took 30.3, 34.9 and 46.5 us, 5 31.7, 35.5 and 47.4, 8 29.6, 35.8 and 47.2.
 constexpr int kTailCost = 6;
+// pa_decode_shared: records in the place of the output, over the tokens behind the
+// shared blocks.  A sequence with no shared blocks gets its output.
 struct DecodeTails {
-    float *rec;       // rows (KV head, sequence, Q head of the KV head), as Record has them
-    int32_t *pieces;  // [B][Hk]: CTA of the second piece | pieces but the first << 16
+    Pieces pieces;
     // by the prefix kernel, ahead of its launch_dependents
     const PlanHead *head;
     const SeqPlan *seqs;  // [B]
@@ -165,6 +171,20 @@ constexpr int kModeRows = 8;             // of D + 4 floats each
 float *mode_records(void *workspace);    // [2 * CTA + slot]
 int launch_decode_scores(const DecodeCall &c, void *workspace, const DecodeScores &sc);
 int launch_decode_tails(const DecodeCall &c, void *workspace, const DecodeTails &tl);
+
+// The pieces of a pair behind its first, `more` of them, each a CTA's first record.
+// (What a call that gave up has not written may be anything.)
+struct Cut {
+    int cta, more;
+};
+__device__ __forceinline__ Cut cut_of(int32_t x) {
+    Cut c = {x & 0xffff, x >> 16};
+    if (c.more < 0 || c.more >= kPieces || c.cta + c.more > kModeCtas) c.more = 0;
+    return c;
+}
+__device__ __forceinline__ Record piece_of(float *records, int cta, int d, int head) {
+    return {records + (int64_t)cta * 2 * kModeRows * (d + 4), kModeRows, head};
+}
 
 // A prefix is read once for its group if that saves at least this many blocks
 // of a KV head, else by each sequence with the rest of its context (a single

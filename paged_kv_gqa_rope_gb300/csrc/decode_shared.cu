@@ -42,7 +42,7 @@ struct SharedArgs {
     Groups groups;
     float *tails;  // records of the tails (DecodeTails), and the CTAs'
     float *tail_recs;
-    const int32_t *tail_pieces;
+    const int32_t *tail_cut;
     PlanHead *head;
     SeqPlan *seqs;
     // Records of a unit's first piece, over the same rows, and of the piece with which
@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                             make_float4(u2f(o[k]), u2f(o[k + 1]), u2f(o[k + 2]), u2f(o[k + 3]));
                 }
             }
-            if (live) *rec.stat<D>() = make_float2(m - kShift, l);
+            if (live) *rec.stat(D) = make_float2(m - kShift, l);
             tc::fence_before();
             mbar_arrive(&bar[B_OFREE + t]);
             if (both) mbar_arrive(&bar[B_OFREE + 1]);
@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SharedArgs a) 
     float2 ml[kJoinBatch];
     float4 x[kJoinBatch];
     auto take = [&](int i, const Record &r) {
-        ml[i] = __ldcg(r.template stat<D>());
+        ml[i] = __ldcg(r.stat(D));
         x[i] = __ldcg(r.cols(c4));
     };
     auto none = [&](int i) {
@@ -890,18 +890,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SharedArgs a) 
     };
     take(0, {a.tails, rows, at});
     take(1, {a.first, rows, at});
-    const int cut = __ldcg(a.tail_pieces + s * a.Hk + kvh);
+    const int cut = __ldcg(a.tail_cut + s * a.Hk + kvh);
     const SeqPlan p = a.seqs[s];
     const PlanHead head = *a.head;
     if (p.state != kInGroup) return;  // (alone: the tails' kernel has written it)
     const int64_t start = p.start + kvh * p.stride;
     const int c0 = plan_cta(start, head.total, head.ctas);
     const int more = plan_cta(start + p.last, head.total, head.ctas) - c0;
-    // the tail's pieces behind its first (what a call that gave up has not written may
-    // be anything)
-    const int cut_cta = cut & 0xffff, left = cut >> 16;
-    const int tail_more =
-        p.tail > 0 && left > 0 && left < kTailPieces && cut_cta + left <= kModeCtas ? left : 0;
+    const Cut behind = cut_of(cut);  // the tail's pieces behind its first
+    const int tail_more = p.tail > 0 ? behind.more : 0;
     if (p.tail == 0) none(0);
     float M = -INFINITY, L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -928,7 +925,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SharedArgs a) 
         for (int i = 0; i < kJoinBatch; ++i) {
             const int n = i0 + i;
             if (n < tail_more)
-                take(i, {a.tail_recs + (int64_t)(cut_cta + n) * 2 * kModeRows * (D + 4), kModeRows, j});
+                take(i, piece_of(a.tail_recs, behind.cta + n, D, j));
             else if (n < tail_more + more)
                 take(i, {a.more + (int64_t)(c0 + 1 + n - tail_more) * 2 * kPrefixTile * (D + 4),
                          2 * kPrefixTile, p.local + j});
@@ -1007,8 +1004,8 @@ extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int laye
     p += 256;
     a.seqs = reinterpret_cast<SeqPlan *>(p);
     p += up256((size_t)num_seqs * sizeof(SeqPlan));
-    int32_t *const pieces = reinterpret_cast<int32_t *>(p);
-    a.tail_pieces = pieces;
+    int32_t *const tail_cut = reinterpret_cast<int32_t *>(p);
+    a.tail_cut = tail_cut;
     a.tail_recs = mode_records(at);
     p += up256((size_t)num_seqs * n_kv_heads * sizeof(int32_t));
     float *const tails = reinterpret_cast<float *>(p);
@@ -1038,7 +1035,7 @@ extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int laye
                           context_lens, num_seqs, n_heads, n_kv_heads, head_dim,
                           scale,    out,     dev_status, st};
     int rc2 = head_dim == 128 ? launch_prefix<128>(a, cache, st) : launch_prefix<64>(a, cache, st);
-    if (rc2 == PA_OK) rc2 = launch_decode_tails(c, at, DecodeTails{tails, pieces, a.head, a.seqs});
+    if (rc2 == PA_OK) rc2 = launch_decode_tails(c, at, DecodeTails{{tails, tail_cut}, a.head, a.seqs});
     if (rc2 != PA_OK) return rc2;
     return head_dim == 128 ? launch_join<128>(a, st) : launch_join<64>(a, st);
 }

@@ -6,7 +6,8 @@
 // A token's p is known only once its row's last token has been seen, so the
 // decode kernel leaves the scores (fp32, 4 g bytes a (token, KV head), against
 // 4 d for its K and V row) and each row's m and 1/l behind; this kernel turns
-// them into weights.  Reading K a second time instead would cost 2 d bytes.
+// them into weights, and joins the outputs of the pairs (sequence, KV head) that the
+// decode kernel's CTAs have left in pieces.  Reading K a second time instead would cost 2 d bytes.
 //
 // Bound: L2 and HBM, 4 g + 8 bytes a (token, KV head).
 #include <algorithm>
@@ -24,22 +25,58 @@ struct WeightArgs {
     const int32_t *context_lens;
     const float *weights;  // nullptr: zeros
     float *weights_out;
+    __half *out;
+    float *recs;  // the decode kernel's CTAs'
     int64_t stride;
-    int H, Hk;
+    int B, H, Hk, d;
 };
 
 // grid (chunks of tokens, Hk, B).  A thread has kWeightTokens tokens at a time, all
 // their loads in flight together with the statistics' (a token at a time: 12 us of
-// the serving batch of 64/8 heads and 4097 tokens).
+// the serving batch of 64/8 heads and 4097 tokens).  32 CTAs an SM at most: twice as
+// many, most of them without tokens, cost a ragged batch 3.6 us.
 template <int G>
-__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightArgs a) {
+__global__ void __launch_bounds__(kWeightThreads, 8) weights_kernel(const WeightArgs a) {
     griddep_wait();
     griddep_launch_dependents();
     const int h = blockIdx.y, s = blockIdx.z;
     const int64_t first = a.sc.first[s];
-    const int n = a.context_lens[s];
-    if (first < 0) return;
-    const float2 *stats = a.sc.stats + (int64_t)s * a.H + h * G;
+    const int n = first == -1 ? 0 : a.context_lens[s];  // (-1: no scores kept)
+    const Cut cut = cut_of(a.sc.pieces.cut[s * a.Hk + h]);
+    if (first == -2) return;
+    __shared__ float2 stats[G];
+    __shared__ float factors[kPieces][G];  // of a cut pair's pieces
+    auto piece = [&](int i, int j) {
+        return i == 0 ? Record{a.sc.pieces.rec, (int64_t)a.B * a.H, ((int64_t)h * a.B + s) * G + j}
+                      : piece_of(a.recs, cut.cta + i - 1, a.d, j);
+    };
+    // The rows' statistics, by a thread each.
+    auto read_stats = [&]() {
+        const int j = threadIdx.x;
+        if (j < G) {
+            if (cut.more == 0) {
+                stats[j] = a.sc.stats[(int64_t)s * a.H + h * G + j];
+            } else {
+                float2 ml[kPieces];
+                float M = -INFINITY, L = 0.f;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i)
+                    ml[i] = i <= cut.more ? *piece(i, j).stat(a.d) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) M = fmaxf(M, ml[i].x);
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const float f = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - M);
+                    factors[i][j] = f;
+                    L = fmaf(f, ml[i].y, L);
+                }
+                const bool none = L == 0.f;  // (no block in range: weights and output 0)
+                stats[j] = none ? make_float2(0.f, 0.f) : make_float2(M, 1.f / L);
+            }
+        }
+        __syncthreads();
+    };
+    bool known = false;
     const float *x =
         a.sc.scores + (first + (int64_t)((n + kBlockSize - 1) / kBlockSize) * h) * kBlockSize * G;
     const int64_t row = ((int64_t)s * a.Hk + h) * a.stride;
@@ -70,6 +107,8 @@ __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightArg
                 if (a.weights) w[i] = a.weights[row + t];
             }
         }
+        if (!known) read_stats();
+        known = true;
         float p[kWeightTokens] = {};
 #pragma unroll
         for (int j = 0; j < G; ++j) {
@@ -83,14 +122,40 @@ __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const WeightArg
             if (t < n) a.weights_out[row + t] = w[i] + p[i];
         }
     }
+    // (the last CTA has the fewest tokens)
+    if (cut.more == 0 || blockIdx.x != gridDim.x - 1) return;
+    if (!known) read_stats();
+    for (int i0 = threadIdx.x; i0 < G * (a.d / 4); i0 += kWeightThreads) {
+        const int j = i0 / (a.d / 4), c = i0 - j * (a.d / 4);
+        float4 O[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            O[i] = i <= cut.more ? *piece(i, j).cols(c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const float f = factors[i][j];
+            y.x = fmaf(f, O[i].x, y.x);
+            y.y = fmaf(f, O[i].y, y.y);
+            y.z = fmaf(f, O[i].z, y.z);
+            y.w = fmaf(f, O[i].w, y.w);
+        }
+        const float inv = stats[j].y;
+        *reinterpret_cast<uint2 *>(a.out + ((int64_t)s * a.H + h * G + j) * a.d + 4 * c) =
+            make_uint2(pack_half2(saturate16(y.x * inv), saturate16(y.y * inv)),
+                       pack_half2(saturate16(y.z * inv), saturate16(y.w * inv)));
+    }
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Workspace: the decode kernel's, the statistics, each sequence's first block, scores.
-size_t fixed_bytes(int B, int H, int D) {
+// Workspace: the decode kernel's, the statistics, each sequence's first block, the cut
+// pairs, their first pieces, scores.
+size_t record_bytes(int B, int H, int D) { return up256((size_t)B * H * (D + 4) * sizeof(float)); }
+size_t fixed_bytes(int B, int H, int Hk, int D) {
     return up256(mode_workspace_bytes(D)) + up256((size_t)B * H * sizeof(float2)) +
-           up256((size_t)B * sizeof(int64_t));
+           up256((size_t)B * sizeof(int64_t)) + up256((size_t)B * Hk * sizeof(int32_t)) +
+           record_bytes(B, H, D);
 }
 
 }  // namespace
@@ -103,10 +168,13 @@ extern "C" size_t pa_decode_weights_workspace_bytes(int num_seqs, int n_heads, i
     if (num_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || score_blocks <= 0)
         return 0;
     // (the parts first: each must fit by itself before it is counted in 64 bits)
-    const unsigned __int128 n = (unsigned __int128)score_blocks * kBlockSize * n_heads * 4 +
-                                (unsigned __int128)num_seqs * n_heads * sizeof(float2);
+    const unsigned __int128 n =
+        (unsigned __int128)score_blocks * kBlockSize * n_heads * 4 +
+        (unsigned __int128)num_seqs * n_heads * (head_dim + (int64_t)6) * sizeof(float) +
+        (unsigned __int128)num_seqs * n_kv_heads * sizeof(int32_t);
     if (n > SIZE_MAX / 2) return 0;
-    return (size_t)score_blocks * kBlockSize * n_heads * 4 + fixed_bytes(num_seqs, n_heads, head_dim);
+    return (size_t)score_blocks * kBlockSize * n_heads * 4 +
+           fixed_bytes(num_seqs, n_heads, n_kv_heads, head_dim);
 }
 
 extern "C" int pa_decode_weights(const void *q, const pa_cache_t *cache, int layer,
@@ -130,16 +198,20 @@ extern "C" int pa_decode_weights(const void *q, const pa_cache_t *cache, int lay
     if (rows > SIZE_MAX || (weights && weights_out != weights &&
                             ranges_overlap(weights, (uint64_t)rows, weights_out, (uint64_t)rows)))
         return PA_ERR_INVALID;
-    const size_t fixed = fixed_bytes(num_seqs, n_heads, head_dim);
+    const size_t fixed = fixed_bytes(num_seqs, n_heads, n_kv_heads, head_dim);
     const size_t block = (size_t)kBlockSize * n_heads * sizeof(float);  // of all KV heads
     if (workspace_bytes < fixed + block) return PA_ERR_WORKSPACE;
 
     uint8_t *at = static_cast<uint8_t *>(workspace);
-    const size_t dec = mode_workspace_bytes(head_dim);
+    uint8_t *p = at + up256(mode_workspace_bytes(head_dim));
     WeightArgs w;
-    w.sc.stats = reinterpret_cast<float2 *>(at + up256(dec));
-    w.sc.first = reinterpret_cast<int64_t *>(at + up256(dec) +
-                                             up256((size_t)num_seqs * n_heads * sizeof(float2)));
+    w.sc.stats = reinterpret_cast<float2 *>(p);
+    p += up256((size_t)num_seqs * n_heads * sizeof(float2));
+    w.sc.first = reinterpret_cast<int64_t *>(p);
+    p += up256((size_t)num_seqs * sizeof(int64_t));
+    w.sc.pieces.cut = reinterpret_cast<int32_t *>(p);
+    p += up256((size_t)num_seqs * n_kv_heads * sizeof(int32_t));
+    w.sc.pieces.rec = reinterpret_cast<float *>(p);
     w.sc.scores = reinterpret_cast<float *>(at + fixed);
     w.sc.capacity = (int64_t)((workspace_bytes - fixed) / block) * n_kv_heads;
     w.sc.max_len = (int)std::min<int64_t>(weights_stride, INT32_MAX);
@@ -147,8 +219,12 @@ extern "C" int pa_decode_weights(const void *q, const pa_cache_t *cache, int lay
     w.weights = weights;
     w.weights_out = weights_out;
     w.stride = weights_stride;
+    w.out = static_cast<__half *>(out);
+    w.recs = mode_records(workspace);
+    w.B = num_seqs;
     w.H = n_heads;
     w.Hk = n_kv_heads;
+    w.d = head_dim;
     const DecodeCall c = {q,        cache,   layer,      block_tables, max_blocks_per_seq,
                           context_lens, num_seqs, n_heads, n_kv_heads, head_dim,
                           scale,    out,     dev_status, static_cast<cudaStream_t>(stream)};
