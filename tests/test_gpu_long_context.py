@@ -467,6 +467,22 @@ def test_weights_from_nothing_and_beside():
     assert (np.abs(apart.cpu().numpy() - want) <= tol).all()
 
 
+@pytest.mark.parametrize("g", range(1, 9))
+def test_weights_one_workspace_again(g):
+    """Batches of several shapes by turns in one workspace, whose scores' lines the
+    second kernel gives up: pairs in one to many pieces, padded blocks, odd groups."""
+    batches = [WeightBatch(g, 2 * g, 2, 64, lens)
+               for lens in ([128, 16 * 9 + 1, 7, 33], [40] * 30 + [1], [3000, 2], list(range(1, 180, 9)))]
+    ws = pa.decode_weights_workspace(31, 2 * g, 2, 64, max(b.blocks for b in batches))
+    for b in batches + batches[::-1]:
+        status = pa.new_status()
+        out, got = b.run(ws=ws, status=status)
+        assert int(status.item()) == 0
+        assert_attention_close(out, b.out())
+        want, tol = b.want()
+        assert (np.abs(got.cpu().numpy() - want) <= tol).all()
+
+
 def test_weights_sum_to_the_heads():
     """Every row's weights sum to the group's size, over lengths of all sorts."""
     b = WeightBatch(4, 32, 4, 64, [1, 2, 15, 16, 17, 1000, 4097, 31])
