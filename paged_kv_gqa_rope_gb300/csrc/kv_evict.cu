@@ -110,13 +110,13 @@ __device__ __forceinline__ int ld_cluster(const int *p, uint32_t rank) {
     return v;
 }
 
-// (four words, 16-byte aligned)
-__device__ __forceinline__ int4 ld_cluster4(const int *p, uint32_t rank) {
+// (two words, 8-byte aligned)
+__device__ __forceinline__ int2 ld_cluster2(const int *p, uint32_t rank) {
     uint32_t at;
-    int4 v;
+    int2 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+    asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+                 : "=r"(v.x), "=r"(v.y)
                  : "r"(at)
                  : "memory");
     return v;
@@ -132,8 +132,9 @@ __global__ void __launch_bounds__(kSelThreads, C > 4 ? 1 : 2)
     griddep_wait();
     __shared__ __align__(16) int hist[3][kDigits];
     __shared__ Counts sums[C * kSelWarps];
-    __shared__ int warp_total[kSelWarps];
-    __shared__ int found[3], mine_of[2];
+    __shared__ __align__(8) int groups[3][kDigits / 32];  // sums of 32 digits, from the top
+    __shared__ int found[3];
+    __shared__ __align__(8) int mine_of[2];
     const int h = blockIdx.x / size, s = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = size > 1 ? (int)cluster_rank() : 0;
@@ -212,44 +213,48 @@ __global__ void __launch_bounds__(kSelThreads, C > 4 ? 1 : 2)
                 count(c0, y);
             }
             // thread i holds four digits, from the top: 2047 - 4 i and down
-            constexpr int kPer = kDigits / kSelThreads;
-            static_assert(kPer == 4, "a vector of four");
-            int cnt[kPer] = {}, mine = 0;
-            if (size > 1) {
+            static_assert(kDigits == 4 * kSelThreads, "a vector of four");
+            __syncthreads();
+            const int4 own = *reinterpret_cast<const int4 *>(&hist[d][kDigits - 4 * (tid + 1)]);
+            int sum = own.x + own.y + own.z + own.w;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if ((tid & 7) == 0) groups[d][tid / 8] = sum;
+            if (size > 1)
                 cluster_sync();
-                int4 all_of[kMaxCluster];
+            else
+                __syncthreads();
+            // One warp looks for the group of 32 digits, then for the digit (the whole
+            // histograms of a cluster of eight, read by all, took 3 us a digit).
+            if (warp == 0) {
+                int2 g[kMaxCluster];
 #pragma unroll
                 for (int q = 0; q < kMaxCluster; ++q)
-                    all_of[q] = q < size ? ld_cluster4(&hist[d][kDigits - kPer * (tid + 1)], q)
-                                         : make_int4(0, 0, 0, 0);
+                    g[q] = q < size ? ld_cluster2(&groups[d][2 * lane], q) : make_int2(0, 0);
+                int a0 = 0, a1 = 0;
 #pragma unroll
-                for (int q = 0; q < kMaxCluster; ++q) {
-                    cnt[0] += all_of[q].w;
-                    cnt[1] += all_of[q].z;
-                    cnt[2] += all_of[q].y;
-                    cnt[3] += all_of[q].x;
-                }
-            } else {
-                __syncthreads();
+                for (int q = 0; q < kMaxCluster; ++q) a0 += g[q].x, a1 += g[q].y;
+                int before = warp_sums(a0 + a1, lane) - a0 - a1;
+                int at = -1;  // this lane's group, if it is the one
+                if (before < want && want <= before + a0) at = 2 * lane;
+                before += at < 0 ? a0 : 0;
+                if (at < 0 && before < want && want <= before + a1) at = 2 * lane + 1;
+                const int who = __ffs(__ballot_sync(0xffffffffu, at >= 0)) - 1;
+                at = __shfl_sync(0xffffffffu, at, who);
+                before = __shfl_sync(0xffffffffu, before, who);
+                const int mine = kDigits - 1 - 32 * at - lane;
+                int c[kMaxCluster], cnt = 0;
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) cnt[j] = hist[d][kDigits - 1 - kPer * tid - j];
-            }
+                for (int q = 0; q < kMaxCluster; ++q)
+                    c[q] = q < size ? ld_cluster(&hist[d][mine], q) : 0;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) mine += cnt[j];
-            const int upto = warp_sums(mine, lane);
-            if (lane == 31) warp_total[warp] = upto;
-            __syncthreads();
-            const int warps = warp_sums(lane < kSelWarps ? warp_total[lane] : 0, lane);
-            const int ahead = __shfl_sync(0xffffffffu, warps, max(warp - 1, 0));
-            int before = upto - mine + (warp ? ahead : 0);
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                if (before < want && want <= before + cnt[j]) {
-                    found[0] = kDigits - 1 - kPer * tid - j;
+                for (int q = 0; q < kMaxCluster; ++q) cnt += c[q];
+                before += warp_sums(cnt, lane) - cnt;
+                if (before < want && want <= before + cnt) {
+                    found[0] = mine;
                     found[1] = want - before;
-                    found[2] = cnt[j];
+                    found[2] = cnt;
                 }
-                before += cnt[j];
             }
             __syncthreads();
             limit |= (uint32_t)found[0] << shift;
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(kSelThreads, C > 4 ? 1 : 2)
                 equal = 0;
                 break;
             }
-            // (barriers of the next digit come before found and warp_total change)
+            // (barriers of the next digit come before found changes)
         }
     }
 
@@ -325,9 +330,10 @@ __global__ void __launch_bounds__(kSelThreads, C > 4 ? 1 : 2)
     Counts base = 0;
     if (size > 1) {
         cluster_sync();
-        for (int q = 0; q < rank; ++q)
-            base += (Counts)(unsigned)ld_cluster(&mine_of[0], q) |
-                    (Counts)(unsigned)ld_cluster(&mine_of[1], q) << 32;
+        const int2 c = lane < rank ? ld_cluster2(mine_of, lane) : make_int2(0, 0);
+        base = (Counts)(unsigned)c.x | (Counts)(unsigned)c.y << 32;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
     } else {
         __syncthreads();
     }
