@@ -440,10 +440,8 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     const int cta = blockIdx.x;
 
     // -------- blocks per sequence (all KV heads) and their prefix sum
-    // kScores: the lengths may be the kernel before's.  kTails runs beside the
-    // prefix kernel, which lets it start once the work before the call is done and
-    // the plan is written, and takes no more CTAs than find room there.
-    if constexpr (MODE == Mode::kScores) griddep_wait();
+    // kTails runs beside the prefix kernel, which lets it start once the work before the
+    // call is done and the plan is written, and takes no more CTAs than find room there.
     [[maybe_unused]] int tail_ctas = 0;
     if constexpr (MODE == Mode::kTails) {
         tail_ctas = __ldcg(&a.tl.head->tail_ctas);
@@ -500,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     __syncthreads();
     // Everything above read only call metadata; Q and the cache may still be
     // being written by the RoPE/append kernel before this one.
-    if constexpr (kOut) griddep_wait();
+    if constexpr (MODE != Mode::kTails) griddep_wait();
     // The kernel after this one (the next step's RoPE/append, the step
     // graph's output copy) may be launched now: it waits for this grid to
     // finish before it touches memory, and this grid's CTAs are all resident

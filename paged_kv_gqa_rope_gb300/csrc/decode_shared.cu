@@ -312,7 +312,6 @@ __device__ __forceinline__ PlanCut plan_few(const SharedArgs &a, FewGroups *few,
     for (int o = 16; o > 0; o >>= 1) tail += __shfl_xor_sync(0xffffffffu, tail, o);
     if (lane == 0) few->tail[tid >> 5] = tail;
     bad = __syncthreads_or(bad);
-    if (bad && blockIdx.x == 0 && tid == 0) report(a.status, PA_DEV_BAD_LENGTH);
     // ---- the groups' places on the line, and this CTA's
     tail = 0;
 #pragma unroll
@@ -338,7 +337,11 @@ __device__ __forceinline__ PlanCut plan_few(const SharedArgs &a, FewGroups *few,
     const int sms = divide_sms((unsigned long long)(total / a.Hk), tail, __popc(active), units, a.G);
     const int G = plan_ctas(total, sms);
 
-    if (blockIdx.x == 0) {  // what the tails' kernel and the join need
+    griddep_wait();
+    if (blockIdx.x != 0) {
+        griddep_launch_dependents();
+    } else {  // what the tails' kernel and the join need
+        if (bad && tid == 0) report(a.status, PA_DEV_BAD_LENGTH);
         if (tid == 0) *a.head = {total, G, sms < a.G ? 2 * (a.G - sms) : a.G};
         for (int i = 0; i < rounds; ++i) {
             const int s = i * kPrefixThreads + tid;
@@ -423,11 +426,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
         fence_barrier_init();
     }
-    if (warp == kVProducerWarp && lane < 4) {  // what the plan reads first
-        prefetch_l2(a.context_lens + min(lane * 32, a.B - 1));
-        if (lane == 0) prefetch_l2(a.groups.starts);
-        if (lane == 1) prefetch_l2(a.groups.blocks);
-    }
     if (warp == kMmaWarp) {
         tc::alloc(tmem_slot, kTmemCols);
         tc::relinquish();
@@ -439,10 +437,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    griddep_wait();
-    // The tails' kernel may start once every CTA has come here (the work before the
+    // The plan reads only the call's metadata, which is complete (as pa_decode's); Q and
+    // the cache, which may still be written, and the workspace wait for griddep_wait.
+    // The tails' kernel may start once every CTA has passed it (the work before the
     // call is done then) and CTA 0 has written the plan.
-    if (blockIdx.x != 0) griddep_launch_dependents();
     const uint32_t tmem = *tmem_slot;  // S_0 | S_1 | O_0 | O_1
     const int mpt = kPrefixTile / a.g;
     // ---- the plan
@@ -459,14 +457,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         PlanCut *shared_cut = reinterpret_cast<PlanCut *>(stats);
         int32_t *skip = reinterpret_cast<int32_t *>(smem), *lens = skip + a.B;
         const int bad = read_groups(a.groups, a.context_lens, a.B, skip, lens, tid, kPrefixThreads);
-        if (bad && blockIdx.x == 0 && tid == 0) report(a.status, PA_DEV_BAD_LENGTH);
         int64_t total;
         const int sms = plan_sms(a.groups, a.context_lens, a.Hk, a.g, a.B, lens, kTailCost, a.G,
                                  bad == 2, plan_sums, tid, kPrefixThreads, total);
         const int G = plan_ctas(total, sms);
         if (tid == 0) shared_cut->places = 0;
         __syncthreads();
-        if (blockIdx.x == 0) {
+        griddep_wait();
+        if (blockIdx.x != 0) {
+            griddep_launch_dependents();
+        } else {
+            if (bad && tid == 0) report(a.status, PA_DEV_BAD_LENGTH);
             write_plan(a, skip, lens, bad == 2, total, sms, G, tid);
             __threadfence();
             __syncthreads();
