@@ -94,8 +94,8 @@ struct DecodeScores {
 };
 
 // Units of a pair's fixed cost on the tails' line (a block: 1).  With 64/8, 32/32 and
-// 32/8 heads 6 took 30.3, 34.9 and 46.5 us, 5 31.7, 35.5 and 47.4, 8 29.6, 35.8 and 47.2.
-constexpr int kTailCost = 6;
+// 32/8 heads 8 took 26.2, 33.7 and 44.4 us, 6 27.4, 33.7 and 44.1.
+constexpr int kTailCost = 8;
 // pa_decode_shared: records in the place of the output, over the tokens behind the
 // shared blocks.  A sequence with no shared blocks gets its output.
 struct DecodeTails {

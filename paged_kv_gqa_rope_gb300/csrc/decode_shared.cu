@@ -337,6 +337,25 @@ __device__ __forceinline__ PlanCut plan_few(const SharedArgs &a, FewGroups *few,
     const int sms = divide_sms((unsigned long long)(total / a.Hk), tail, __popc(active), units, a.G);
     const int G = plan_ctas(total, sms);
 
+    PlanCut cut = {};
+    if ((int)blockIdx.x < G) {
+        const int64_t at = plan_cut(total, blockIdx.x, G);
+        cut.places = plan_cut(total, blockIdx.x + 1, G) - at;
+        const int r = __ffs(__ballot_sync(0xffffffffu, start <= at && at < end)) - 1;
+        cut.group = r;
+        cut.p.tiles = __shfl_sync(0xffffffffu, p.tiles, r);
+        cut.p.blocks = __shfl_sync(0xffffffffu, p.blocks, r);
+        cut.p.s0 = __shfl_sync(0xffffffffu, p.s0, r);
+        cut.p.members = __shfl_sync(0xffffffffu, p.members, r);
+        cut.p.lead = __shfl_sync(0xffffffffu, p.lead, r);
+        cut.p.units = __shfl_sync(0xffffffffu, p.units, r);
+        cut.p.weight = __shfl_sync(0xffffffffu, p.weight, r);
+        const int64_t off = at - __shfl_sync(0xffffffffu, start, r);
+        const int span = cut.p.span();
+        cut.unit = (int)(total < kShortLine ? (uint32_t)off / (uint32_t)span : off / span);
+        cut.t0 = (int)(off - (int64_t)cut.unit * span);
+    }
+
     griddep_wait();
     if (blockIdx.x != 0) {
         griddep_launch_dependents();
@@ -365,25 +384,6 @@ __device__ __forceinline__ PlanCut plan_few(const SharedArgs &a, FewGroups *few,
         __threadfence();
         __syncthreads();
         griddep_launch_dependents();
-    }
-
-    PlanCut cut = {};
-    if ((int)blockIdx.x < G) {
-        const int64_t at = plan_cut(total, blockIdx.x, G);
-        cut.places = plan_cut(total, blockIdx.x + 1, G) - at;
-        const int r = __ffs(__ballot_sync(0xffffffffu, start <= at && at < end)) - 1;
-        cut.group = r;
-        cut.p.tiles = __shfl_sync(0xffffffffu, p.tiles, r);
-        cut.p.blocks = __shfl_sync(0xffffffffu, p.blocks, r);
-        cut.p.s0 = __shfl_sync(0xffffffffu, p.s0, r);
-        cut.p.members = __shfl_sync(0xffffffffu, p.members, r);
-        cut.p.lead = __shfl_sync(0xffffffffu, p.lead, r);
-        cut.p.units = __shfl_sync(0xffffffffu, p.units, r);
-        cut.p.weight = __shfl_sync(0xffffffffu, p.weight, r);
-        const int64_t off = at - __shfl_sync(0xffffffffu, start, r);
-        const int span = cut.p.span();
-        cut.unit = (int)(total < kShortLine ? (uint32_t)off / (uint32_t)span : off / span);
-        cut.t0 = (int)(off - (int64_t)cut.unit * span);
     }
     return cut;
 }
