@@ -695,7 +695,9 @@ int pa_rope_table_init_scaled(void *device_table, int max_positions, int rotary_
  * sets PA_DEV_BAD_LENGTH and its output is not written; group_starts that do not
  * rise from 0 to num_seqs leave all outputs so.  Shared blocks whose id is out
  * of range set PA_DEV_BAD_BLOCK and drop out of the group's attention, as in
- * pa_decode.  Other arguments, results and limits are those of pa_decode, and
+ * pa_decode.  context_lens, group_starts and shared_blocks are read before the
+ * wait for the work ahead in the stream (pa_decode_step has what that asks of
+ * it).  Other arguments, results and limits are those of pa_decode, and
  * num_seqs * n_kv_heads <= 262144.  The size is 0 for non-positive arguments and
  * one past SIZE_MAX.
  */
@@ -745,9 +747,10 @@ int pa_prepare_shared(int num_seqs, const int32_t *block_tables, int max_blocks_
  *                weights are not.  256-byte aligned, ZEROED before its first
  *                use, left ready for the next call (of any shape that it is
  *                large enough for); one call at a time.
- * Other arguments, results, checks and limits are those of pa_decode, and
- * num_seqs * n_kv_heads <= 262144.  The size
- * is 0 for non-positive arguments and one past SIZE_MAX.
+ * context_lens are read before the wait for the work ahead in the stream
+ * (pa_decode_step has what that asks of it).  Other arguments, results, checks
+ * and limits are those of pa_decode, and num_seqs * n_kv_heads <= 262144.  The
+ * size is 0 for non-positive arguments and one past SIZE_MAX.
  */
 size_t pa_decode_weights_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads, int head_dim,
                                          int64_t score_blocks);

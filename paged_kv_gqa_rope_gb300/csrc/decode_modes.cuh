@@ -189,8 +189,8 @@ __device__ __forceinline__ Record piece_of(float *records, int cta, int d, int h
 // A prefix is read once for its group if that saves at least this many blocks
 // of a KV head, else by each sequence with the rest of its context (a single
 // sequence has nothing to share).  Eight sequences over 128 shared tokens, 56
-// blocks: 12.1 us shared and 14.5 not with 4/2 heads of 64, 14.4 and 16.7 with 32/32
-// of 128; two over 256, 16 blocks, 64/8 of 128: 12.3 and 22.6.
+// blocks: 9.9 us shared and 14.5 not with 4/2 heads of 64, 13.7 and 17.1 with 32/32
+// of 128; two over 256, 16 blocks, 64/8 of 128: 11.1 and 22.6.
 constexpr int kMinSavedBlocks = 8;
 
 __device__ __forceinline__ int shared_of(int blocks, int members) {
@@ -292,7 +292,8 @@ __device__ __forceinline__ int divide_sms(unsigned long long places, unsigned lo
 }
 
 // By a whole CTA of `threads` threads after read_groups; `sums` are three words of
-// shared memory.  Every CTA comes to the same.  Returns the SMs for the prefixes; total: places of their line.
+// shared memory.  Every CTA comes to the same.  Returns the SMs for the prefixes;
+// total: places of their line.
 __device__ __forceinline__ int plan_sms(const Groups &groups, const int32_t *context_lens, int Hk,
                                         int g, int B, const int32_t *lens, int pair_cost, int sms,
                                         bool broken, unsigned long long *sums, int tid, int threads,

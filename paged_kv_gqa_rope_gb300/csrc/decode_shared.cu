@@ -19,11 +19,11 @@
 // share enough, the line, and how the SMs are divided, by the work of both sides.
 //
 // Bound: HBM for up to 128 query rows a KV head (each key tile of 64 KB serves them
-// all: 32 sequences, 32/32 heads, 65536 tokens at 6.2 TB/s), the tensor cores above
+// all: 32 sequences, 32/32 heads, 65536 tokens at 6.3 TB/s), the tensor cores above
 // (128 sequences, 64/8 heads, 65536 tokens at 1130 TFLOP/s; an issuing thread is held
 // 1370 cycles a job of 128 x 128 x 128 twice, at the 1.5 GHz that the power limit
-// leaves).  Serving batches of 8192 shared tokens are bound by latencies: about 2 us
-// for the plan, 4 to the first tile, 2 a record, 3 for the join.
+// leaves).  Serving batches of 8192 shared tokens are bound by latencies: about 4 us
+// to the first tile, 2 a record, 3 for the join.
 #include <algorithm>
 #include <climits>
 #include <mutex>
@@ -333,8 +333,10 @@ __device__ __forceinline__ PlanCut plan_few(const SharedArgs &a, FewGroups *few,
     }
     const int64_t start = end - places, total = __shfl_sync(0xffffffffu, end, 31);
     const uint32_t active = __ballot_sync(0xffffffffu, places > 0);
-    const int64_t units = (int64_t)__shfl_sync(0xffffffffu, p.units, active ? __ffs(active) - 1 : 0) * a.Hk;
-    const int sms = divide_sms((unsigned long long)(total / a.Hk), tail, __popc(active), units, a.G);
+    const int64_t units =
+        (int64_t)__shfl_sync(0xffffffffu, p.units, active ? __ffs(active) - 1 : 0) * a.Hk;
+    const int sms =
+        divide_sms((unsigned long long)(total / a.Hk), tail, __popc(active), units, a.G);
     const int G = plan_ctas(total, sms);
 
     PlanCut cut = {};

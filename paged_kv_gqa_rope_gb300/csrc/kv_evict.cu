@@ -394,12 +394,15 @@ __global__ void __launch_bounds__(kSelThreads, C > 4 ? 1 : 2)
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int slices,
                                                                   int parts) {
-    // (No launch_dependents: this kernel writes the new lengths, and pa_decode
-    // reads its lengths ahead of its wait for the kernel before.)
+    // (No launch_dependents: this kernel writes the new lengths, and the decode calls
+    // read their lengths ahead of their wait for the kernel before.)
     griddep_wait();
     const int h = blockIdx.y, s = blockIdx.z / parts, part = blockIdx.z % parts, tid = threadIdx.x;
     const int64_t pair = (int64_t)s * a.Hk + h;
-    if (blockIdx.x == 0 && h == 0 && part == 0 && tid == 0 && a.kept[s] >= 0) a.out_lens[s] = a.kept[s];
+    if (blockIdx.x == 0 && h == 0 && part == 0 && tid == 0 && a.kept[s] >= 0) {
+        a.out_lens[s] = a.kept[s];
+        __threadfence();  // (seen by kernels that start when this one's CTAs are done)
+    }
     const int moved = a.moved[pair];
     if (moved < 0 && part > 0) return;  // in place: one CTA, in order
     const unsigned n = moved < 0 ? ~moved : moved;
