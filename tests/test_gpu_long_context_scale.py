@@ -216,3 +216,73 @@ def test_empty_batches():
     assert pa.decode_weights(none, cache, bt, i0, w, ws, 2)[0].shape == (0, 4, 64)
     pa.kv_evict(cache, bt, i0, w, 8, ws)
     pa.rope_kv_write_layout(none, kv, kv, i0, i0, pa.rope_table(4, 64), cache, "half")
+
+
+def test_lengths_written_just_before():
+    """Lengths and groups changed by a copy, by an eviction, or by either with an append
+    in between, right before the decodes that read them ahead of their wait."""
+    H, Hk, d = 8, 2, 128
+    b = SharedBatch(31, H, Hk, d, [(40, [30, 5, 70, 9]), (12, [50, 33])])
+    pool, bt, q = cache_of(b.pool), dev(b.bt), dev(b.q)
+    B = len(b.ctx)
+    variants = [(b.ctx, b.starts, b.shared), (b.ctx - 3, b.starts, np.array([25, 12], np.int32)),
+                (b.ctx - 2, np.array([0, 6, 6], np.int32), np.zeros(2, np.int32))]
+    variants = [tuple(dev(x.astype(np.int32)) for x in v) for v in variants]
+    ctx, starts, shared = (torch.empty_like(x) for x in variants[0])
+    ws = pa.decode_shared_workspace(B, H, Hk, d)
+    blocks = int(sum(-(-b.ctx // 16)))
+    ww = pa.decode_weights_workspace(B, H, Hk, d, blocks)
+    w0 = dev(np.random.default_rng(2).random((B, Hk, 16 * b.bt.shape[1])).astype(np.float32))
+    # an append elsewhere: it lets the next kernel start at once
+    other = pa.Cache(1, 2, Hk, d)
+    oq, ok = torch.zeros(3, H, d).half().cuda(), torch.zeros(3, Hk, d).half().cuda()
+    table = pa.rope_table(16, d)
+    pos = slots = torch.arange(3, dtype=torch.int32).cuda()
+
+    def step(v, wait, append):
+        for x, y in zip((ctx, starts, shared), variants[v]):
+            x.copy_(y)
+        w = w0.clone()
+        if append:
+            pa.rope_kv_write_layout(oq, ok, ok, pos, slots, table, other, "half")
+        if wait:
+            torch.cuda.synchronize()
+        out = pa.decode_shared(q, pool, bt, ctx, starts, shared, ws, Hk)
+        o, w = pa.decode_weights(q, pool, bt, ctx, w, ww, Hk)
+        return out, o, w
+
+    want = [step(v, True, False) for v in range(3)]
+    got = [(i % 3, step(i % 3, False, i % 2 == 0)) for i in range(60)]
+    torch.cuda.synchronize()
+    for v, outs in got:
+        for x, y in zip(outs, want[v]):
+            assert torch.equal(x, y)
+
+    # lengths that an eviction in place leaves
+    e = WeightBatch(33, H, Hk, d, [300, 77, 1000, 64])
+    first, n = dev(e.pool), len(e.ctx)
+    epool, ebt, eq = torch.empty_like(first), dev(e.bt), dev(e.q)
+    cache = pa.Cache(1, e.NB, Hk, d, tensor=epool)
+    ew = pa.decode_weights_workspace(n, H, Hk, d, e.blocks)
+    es = pa.kv_evict_workspace(n, Hk, 128)
+    elen, weights = dev(e.ctx), dev(e.w)
+
+    def evict(wait, append):
+        epool.copy_(first)
+        elen.copy_(dev(e.ctx))
+        weights.copy_(dev(e.w))
+        pa.kv_evict(cache, ebt, elen, weights, 128, es, sinks=4, recent=16)
+        if append:
+            pa.rope_kv_write_layout(oq, ok, ok, pos, slots, table, other, "half")
+        if wait:
+            torch.cuda.synchronize()
+        o, w = pa.decode_weights(eq, cache, ebt, elen, weights, ew, Hk)
+        return o, w.clone(), elen.clone()
+
+    want = evict(True, False)
+    assert want[2].tolist() == [128, 77, 128, 64]
+    got = [evict(False, i % 2 == 0) for i in range(20)]
+    torch.cuda.synchronize()
+    for outs in got:
+        for x, y in zip(outs, want):
+            assert torch.equal(x, y)
