@@ -962,8 +962,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
             c_first = cta_of(sg.pair_start, W, G);
             c_last = cta_of(sg.pair_end - 1, W, G);
             nrec = c_last - c_first + 1;
-            if constexpr (MODE == Mode::kScores) left = nrec <= kPieces;
-            if constexpr (MODE == Mode::kTails) left = !alone && nrec <= kPieces;
+            if constexpr (!kOut) left = nrec <= kPieces;
             may_close = !left && pos + sg.nu == end && nrec <= kConsumerWarps;
             if (may_close && tid == 0) arrived = ld_acquire_gpu(a.counters + s * a.Hk + kvh);
         }
@@ -977,7 +976,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
 
         const Pieces &to = MODE == Mode::kScores ? a.sc.pieces : a.tl.pieces;
         if constexpr (!kOut)
-            if ((MODE == Mode::kScores || !alone) && b0 == 0 && tid == 0)
+            if (b0 == 0 && tid == 0)
                 to.cut[s * a.Hk + kvh] = left ? (c_first + 1) | (nrec - 1) << 16 : 0;
         if (!kOut && (left || (MODE == Mode::kTails && !alone && whole))) {
             // (four values a thread at a time)

@@ -97,7 +97,8 @@ struct DecodeScores {
 // 32/8 heads 8 took 26.2, 33.7 and 44.4 us, 6 27.4, 33.7 and 44.1.
 constexpr int kTailCost = 8;
 // pa_decode_shared: records in the place of the output, over the tokens behind the
-// shared blocks.  A sequence with no shared blocks gets its output.
+// shared blocks.  A sequence with no shared blocks gets its output, but for the pairs
+// left in pieces.
 struct DecodeTails {
     Pieces pieces;
     // by the prefix kernel, ahead of its launch_dependents

@@ -879,8 +879,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SharedArgs a) 
     if (at >= (int64_t)a.B * a.H) return;
     const int j = (int)at % a.g, s = (int)at / a.g % a.B, kvh = (int)at / a.g / a.B;
     const int64_t row = (int64_t)s * a.H + kvh * a.g + j, rows = (int64_t)a.B * a.H;
-    // Every row that is not alone has a first piece; it and the tail's record do not
-    // wait for the plan, nor the other pieces for each other.
+    // Every row that is not alone has a first piece of its prefix; it and the tail's
+    // record do not wait for the plan, nor the other pieces for each other.
     float2 ml[kJoinBatch];
     float4 x[kJoinBatch];
     auto take = [&](int i, const Record &r) {
@@ -896,12 +896,18 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SharedArgs a) 
     const int cut = __ldcg(a.tail_cut + s * a.Hk + kvh);
     const SeqPlan p = a.seqs[s];
     const PlanHead head = *a.head;
-    if (p.state != kInGroup) return;  // (alone: the tails' kernel has written it)
-    const int64_t start = p.start + kvh * p.stride;
-    const int c0 = plan_cta(start, head.total, head.ctas);
-    const int more = plan_cta(start + p.last, head.total, head.ctas) - c0;
+    if (p.state == kLeftOut) return;
     const Cut behind = cut_of(cut);  // the tail's pieces behind its first
     const int tail_more = p.tail > 0 ? behind.more : 0;
+    int c0 = 0, more = 0;  // the prefix's
+    if (p.state == kInGroup) {
+        const int64_t start = p.start + kvh * p.stride;
+        c0 = plan_cta(start, head.total, head.ctas);
+        more = plan_cta(start + p.last, head.total, head.ctas) - c0;
+    } else {
+        if (tail_more == 0) return;  // (the tails' kernel has written it)
+        none(1);
+    }
     if (p.tail == 0) none(0);
     float M = -INFINITY, L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
