@@ -293,14 +293,6 @@ __device__ __forceinline__ int ld_acquire_gpu(const int *p) {
     return v;
 }
 
-// The pair's output rows of heads h0, h0 + step, ... from its pieces' records, by
-// one warp (the warp of the last piece to arrive, while the rest of its CTA goes
-// on; or each warp of a CTA that has reached its end).  Per head:
-// the pieces' maximum M (lanes load the pieces' maxima together), then, for
-// pieces in groups of 32 (lane j holding piece i0 + j's factor 2^(m - M) and
-// sum), the row sum and the O of the head's D columns (lane = column within
-// each run of 32) accumulated in piece order, the O values of four pieces
-// loaded at a time (two for the int8 kernel, whose registers are capped).
 // Loads of the call's inputs.  kTails takes them from L2: it does not itself wait
 // for the work that wrote them (the prefix kernel has, before it let it start).
 template <Mode MODE, typename T>
@@ -317,30 +309,32 @@ __device__ __forceinline__ Record first_record(const Pieces &p, const DecodeArgs
 }
 
 // One element (head h of the pair, value d) of a finished pair: O unnormalised,
-// M the maximum, L the sum of the row; alone: nothing to be joined with it.
+// M the maximum, L the sum of the row.
 template <int D, Mode MODE>
 __device__ __forceinline__ void emit(const DecodeArgs &a, int s, int kvh, int h, int d, float O,
-                                     float M, float L, bool alone) {
+                                     float M, float L) {
     const int64_t row = (int64_t)s * a.H + kvh * a.g + h;
-    if (MODE == Mode::kTails && !alone) {
-        const Record r = first_record(a.tl.pieces, a, s, kvh, h);
-        reinterpret_cast<float *>(r.cols(d >> 2))[d & 3] = O;
-        if (d == 0) *r.stat(D) = make_float2(M - kPShift, L);
-    } else {
-        if constexpr (MODE == Mode::kOut) {
-            a.out[row * D + d] = __float2half_rn(L > 0.f ? O / L : 0.f);
-        } else {  // (NaN stays NaN; a row whose blocks are all out of range is 0)
-            const bool none = L == 0.f;
-            a.out[row * D + d] = __float2half_rn(none ? 0.f : saturate16(O / L));
-            if (MODE == Mode::kScores && d == 0)
-                a.sc.stats[row] = none ? make_float2(0.f, 0.f) : make_float2(M - kPShift, 1.f / L);
-        }
+    if constexpr (MODE == Mode::kOut) {
+        a.out[row * D + d] = __float2half_rn(L > 0.f ? O / L : 0.f);
+    } else {  // (NaN stays NaN; a row whose blocks are all out of range is 0)
+        const bool none = L == 0.f;
+        a.out[row * D + d] = __float2half_rn(none ? 0.f : saturate16(O / L));
+        if (MODE == Mode::kScores && d == 0)
+            a.sc.stats[row] = none ? make_float2(0.f, 0.f) : make_float2(M - kPShift, 1.f / L);
     }
 }
 
-template <int D, bool I8, Mode MODE>
+// The pair's output rows of heads h0, h0 + step, ... from its pieces' records, by
+// one warp (the warp of the last piece to arrive, while the rest of its CTA goes
+// on; or each warp of a CTA that has reached its end).  Per head:
+// the pieces' maximum M (lanes load the pieces' maxima together), then, for
+// pieces in groups of 32 (lane j holding piece i0 + j's factor 2^(m - M) and
+// sum), the row sum and the O of the head's D columns (lane = column within
+// each run of 32) accumulated in piece order, the O values of four pieces
+// loaded at a time (two for the int8 kernel, whose registers are capped).
+template <int D, bool I8>
 __device__ void warp_merge_records(const DecodeArgs &a, const Segment &sg, int64_t W, int G,
-                                   int lane, int h0, int step, bool alone) {
+                                   int lane, int h0, int step) {
     constexpr int kRec = D + 4;
     constexpr int kRuns = D / 32;
     constexpr int kBatch = I8 ? 2 : 4;
@@ -392,7 +386,7 @@ __device__ void warp_merge_records(const DecodeArgs &a, const Segment &sg, int64
         }
 #pragma unroll
         for (int rr = 0; rr < kRuns; ++rr)
-            emit<D, MODE>(a, sg.s, sg.kvh, h, rr * 32 + lane, O[rr], M, Lsum, alone);
+            emit<D, Mode::kOut>(a, sg.s, sg.kvh, h, rr * 32 + lane, O[rr], M, Lsum);
     }
 }
 
@@ -957,13 +951,13 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
         // value is needed after the barrier.)
         int c_first = 0, c_last = 0, nrec = 1, arrived = -1;
         bool may_close = false;
-        [[maybe_unused]] bool left = false;  // in pieces, for the next kernel (not kOut)
+        // (the modes other than kOut leave all pieces to the next kernel)
+        [[maybe_unused]] const bool left = !kOut && !whole;
         if (!whole) {
             c_first = cta_of(sg.pair_start, W, G);
             c_last = cta_of(sg.pair_end - 1, W, G);
             nrec = c_last - c_first + 1;
-            if constexpr (!kOut) left = nrec <= kPieces;
-            may_close = !left && pos + sg.nu == end && nrec <= kConsumerWarps;
+            may_close = kOut && pos + sg.nu == end && nrec <= kConsumerWarps;
             if (may_close && tid == 0) arrived = ld_acquire_gpu(a.counters + s * a.Hk + kvh);
         }
         named_barrier_sync(1, kCons);
@@ -1007,10 +1001,10 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
 #pragma unroll
                 for (int wv = 0; wv < kConsumerWarps; ++wv)
                     O = __fmaf_rn(sm_m[wv * kGroupPad + h], sm_o[(wv * kGroupPad + h) * D + d], O);
-                emit<D, MODE>(a, s, kvh, h, d, O, sm_l[kGroupPad + h], sm_l[h], alone);
+                emit<D, MODE>(a, s, kvh, h, d, O, sm_l[kGroupPad + h], sm_l[h]);
             }
             named_barrier_sync(1, kCons);  // the smem merge area is free again
-        } else {
+        } else if constexpr (kOut) {
             // A piece of a cut pair.  Unless it closes the pair, it leaves the
             // CTA's record of it (slot 0 for the CTA's first segment, 1 for its
             // last) and arrives on the pair's counter after a release fence
@@ -1051,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                             if (last) fence_acq_rel_gpu();
                         }
                         if (__shfl_sync(0xffffffffu, last, 0)) {
-                            warp_merge_records<D, I8, MODE>(a, sg, W, G, lane, 0, 1, alone);
+                            warp_merge_records<D, I8>(a, sg, W, G, lane, 0, 1);
                             if (lane == 0) a.counters[s * a.Hk + kvh] = 0;
                         }
                     }
@@ -1136,7 +1130,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                                     if (i < nrec)
                                         O = __fmaf_rn(sm_pm[i * kGroupPad + h],
                                                       i == own ? Oown : x[i][k], O);
-                                emit<D, MODE>(a, s, kvh, h, d, O, sm_pl[kGroupPad + h], sm_pl[h], alone);
+                                emit<D, MODE>(a, s, kvh, h, d, O, sm_pl[kGroupPad + h], sm_pl[h]);
                             }
                         }
                     }
@@ -1206,7 +1200,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                                                   i == own ? oown[k]
                                                            : sm_o[(i * kGroupPad + h) * D + d],
                                                   O);
-                            emit<D, MODE>(a, s, kvh, h, d, O, sm_pl[kGroupPad + h], sm_pl[h], alone);
+                            emit<D, MODE>(a, s, kvh, h, d, O, sm_pl[kGroupPad + h], sm_pl[h]);
                         }
                     }
                 }
@@ -1215,7 +1209,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                 // More pieces (a long pair), from the records: a head per warp.
                 // (One element per thread and a piece at a time took 210 us of the
                 // 231 of one sequence of 32767 tokens over 8 KV heads.)
-                warp_merge_records<D, I8, MODE>(a, sg, W, G, lane, warp, kConsumerWarps, alone);
+                warp_merge_records<D, I8>(a, sg, W, G, lane, warp, kConsumerWarps);
                 if (tid == 0) a.counters[s * a.Hk + kvh] = 0;
             }
         }
@@ -1346,7 +1340,6 @@ int launch_mode(const DecodeCall &c, void *workspace, const DecodeScores &sc,
     a.block_tables = c.block_tables;
     a.context_lens = c.context_lens;
     a.out = static_cast<__half *>(c.out);
-    a.counters = static_cast<int32_t *>(workspace);
     a.rec = mode_records(workspace);
     a.status = c.dev_status;
     a.scale_log2 = scale * 1.4426950408889634f;
@@ -1363,14 +1356,10 @@ int launch_mode(const DecodeCall &c, void *workspace, const DecodeScores &sc,
 
 }  // namespace
 
-float *mode_records(void *workspace) {
-    return reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
-                                     (size_t)kModePairs * sizeof(int32_t));
-}
+float *mode_records(void *workspace) { return static_cast<float *>(workspace); }
 
 size_t mode_workspace_bytes(int head_dim) {
-    const size_t rec = cta_record_bytes(head_dim > 128 ? head_dim : 128);
-    return (size_t)kModePairs * sizeof(int32_t) + (size_t)kMaxGrid * rec;
+    return (size_t)kMaxGrid * cta_record_bytes(head_dim > 128 ? head_dim : 128);
 }
 
 int launch_decode_scores(const DecodeCall &c, void *workspace, const DecodeScores &sc) {
