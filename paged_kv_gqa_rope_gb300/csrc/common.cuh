@@ -241,6 +241,16 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
+// a, b += the halves of p: one operation each, the conversion among it (in the order of
+// the other volatile ones).
+__device__ __forceinline__ void add_halves(float &a, float &b, uint32_t p) {
+    asm volatile(
+        "{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.rn.f32.f16 %0, lo, %0;\n\t"
+        "add.rn.f32.f16 %1, hi, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(p));
+}
+
 // Programmatic dependent launch (PTX griddepcontrol).  A kernel launched
 // with programmatic stream serialization may start while the kernel before
 // it in the stream still runs; `griddep_wait` returns once that kernel has

@@ -58,16 +58,17 @@ struct alignas(16) PlanHead {
 };
 
 // Records of rows, with four columns of all of them side by side ([D / 4][rows][4],
-// then {m, l}[rows]): neither the threads that write them, one a row, nor those that
-// read them leave a line half used.
+// then {m, l}[rows], {m, w}[rows]): neither the threads that write them, one a row, nor
+// those that read them leave a line half used.
 struct Record {
     float *base;
     int64_t rows, row;
     __device__ __forceinline__ float4 *cols(int i) const {  // columns 4 i .. 4 i + 3
         return reinterpret_cast<float4 *>(base) + i * rows + row;
     }
-    __device__ __forceinline__ float2 *stat(int d) const {
-        return reinterpret_cast<float2 *>(base + d * rows) + row;
+    // (w, of pa_decode_weights: l before P's rounding)
+    __device__ __forceinline__ float2 *stat(int d, bool w = false) const {
+        return reinterpret_cast<float2 *>(base + (d + (w ? 2 : 0)) * rows) + row;
     }
 };
 
@@ -87,7 +88,7 @@ struct Pieces {
 struct DecodeScores {
     Pieces pieces;
     float *scores;     // [blocks of all KV heads][16 tokens][g]: log2 units
-    float2 *stats;     // [B][H]: {m, 1 / l}, a weight being 2^(score - m) / l
+    float2 *stats;     // [B][H]: {m, 1 / w}, a weight being 2^(score - m) / w
     int64_t *first;    // [B]: a sequence's first block in scores, -1: none kept, -2: left out
     int64_t capacity;  // blocks of all KV heads that scores holds
     int max_len;       // longest context that the rows of weights hold
@@ -132,9 +133,9 @@ __device__ __forceinline__ int plan_cta(int64_t t, int64_t total, int G) {
     return (int)(((t + 1) * G + total - 1) / total) - 1;
 }
 
-// The output's rounding.  P is rounded to fp16 on its way to P V and its sum is
-// not, so an average of values at the end of fp16's range can come out past it:
-// finite ones are saturated.
+// The output's rounding.  An average of values at the end of fp16's range, its two
+// sums each a fp32 chain of one step a tile or block, can come out past it where the
+// context is long: finite ones are saturated.
 __device__ __forceinline__ float saturate16(float x) {
     return fabsf(x) < INFINITY ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
 }

@@ -1,0 +1,73 @@
+"""Calls of the long-context operators that their documentation allows beside those of
+test_gpu_long_context.py: values that must come back as they are, workspaces that hold
+anything, tables far wider than the contexts."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_gqa_rope_gb300 import pa
+from tests.gpu_helpers import bits
+from tests.test_gpu_long_context import SHARED, SharedBatch, WeightBatch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(libpa):
+    assert torch.cuda.is_available()
+    assert pa.check_device() == pa.PA_OK
+    return libpa
+
+
+# An average of equal values is the value.  P is fp16 in the product with V, so that
+# holds only if the sum that it is divided by adds the same fp16 values.  Here one key of
+# score 0 stands beside keys whose P is 0.9 of half a step above a power of two: each loses
+# 0.9 * 2^-11 of itself to its rounding, while the values, 2047 / 1024 by powers of two,
+# have a half step of 2^-12 of themselves.  Beside that rounding stand fp32 ones alone: a row
+# has at most 300 blocks, 38 tiles of 8 products or 300 of one, each of which cuts its sum by
+# 2^-22 at most, 300 * 2^-22 < 2^-13 together; the sums of P add 2^-24 a value of a thread's
+# chain, at most 38 * 32 of them, less than 2^-13.
+SCALE = (1 - math.log2(1 + 0.9 * 2.0 ** -11)) / math.log2(math.e)
+
+
+def equal_values(b, seed):
+    """Every token of the batch gets the same V row a KV head; the output that then is due."""
+    rng = np.random.default_rng(seed)
+    row = (2047 / 1024 * 2.0 ** rng.integers(-2, 2, (b.Hk, b.d)) * rng.choice([-1, 1], (b.Hk, b.d)))
+    written = ~np.isnan(b.pool[1])
+    b.pool[1] = np.where(written, row.astype(np.float16), b.pool[1])
+    b.pool[0] = np.where(written, np.float16(0), b.pool[0])
+    b.pool[0, ..., 0] = np.where(written[..., 0], np.float16(-1), b.pool[0, ..., 0])
+    for s in range(len(b.ctx)):
+        b.pool[0, b.layer, b.bt[s, 0], 0] = 0
+    b.q[:] = 1
+    return np.repeat(row, b.H // b.Hk, 0).astype(np.float16) + np.zeros(b.q.shape, np.float16)
+
+
+@pytest.mark.parametrize("H,Hk,d", [(4, 2, 64), (14, 2, 64), (8, 1, 128), (12, 4, 128), (6, 6, 128)])
+@pytest.mark.parametrize("groups", range(len(SHARED)))
+def test_shared_gives_equal_values_back(H, Hk, d, groups):
+    b = SharedBatch(groups, H, Hk, d, SHARED[groups])
+    want = equal_values(b, groups)
+    assert np.array_equal(bits(b.run(scale=SCALE)), bits(want))
+
+
+@pytest.mark.parametrize("H,Hk,d", [(4, 2, 64), (14, 2, 64), (8, 1, 128), (12, 4, 128), (6, 6, 128)])
+@pytest.mark.parametrize("lens", [[1], [16, 2, 17], [300, 5, 33, 64], [4800], [3] * 70])
+def test_weights_give_equal_values_back(H, Hk, d, lens):
+    b = WeightBatch(len(lens), H, Hk, d, lens)
+    want = equal_values(b, len(lens))
+    b.w[:] = 0
+    out, got = b.run(scale=SCALE)
+    assert np.array_equal(bits(out), bits(want))
+    # The weights are those of the scores, not of P: n - 1 tokens of p beside one of 1.
+    # Off by a sum of at most 80 blocks a warp, each step 2^-24 (2^-17.6), and a handful of
+    # roundings of 2^-22.
+    g, p, got = H // Hk, 2.0 ** -(SCALE * math.log2(math.e)), got.cpu().numpy()
+    for s, n in enumerate(lens):
+        w = np.full(n, g * p / (1 + p * (n - 1)))
+        w[0] = g / (1 + p * (n - 1))
+        assert np.abs(got[s, :, :n] / w - 1).max() <= 2.0 ** -17
