@@ -683,12 +683,12 @@ int pa_rope_table_init_scaled(void *device_table, int max_positions, int rotary_
  *                  (nothing but the shared blocks is allowed); 0 or a group of
  *                  one sequence shares nothing
  *   num_groups     1 .. 4096
- *   workspace      pa_decode_shared_workspace_bytes(...) bytes, otherwise as
- *                  pa_decode's: 256-byte aligned, ZEROED before its first use,
- *                  left ready for the next call (of any shape that it is large
- *                  enough for), one call at a time (two streams, or two captured
- *                  graphs that may run together, take one each).  A smaller one
- *                  gives PA_ERR_WORKSPACE.
+ *   workspace      pa_decode_shared_workspace_bytes(...) bytes, 256-byte
+ *                  aligned, contents undefined before and after (unlike
+ *                  pa_decode's, it need not be zeroed), so for calls of any shape
+ *                  that it is large enough for; one call at a time (two streams,
+ *                  or two captured graphs that may run together, take one each).
+ *                  A smaller one gives PA_ERR_WORKSPACE.
  * The blocks are read through the table of the group's first sequence that is
  * in order.  A sequence whose length is out of range or shorter than its shared
  * blocks, and every sequence of a group whose shared_blocks is out of range,
@@ -744,9 +744,9 @@ int pa_prepare_shared(int num_seqs, const int32_t *block_tables, int max_blocks_
  *                score_blocks >= sum_s ceil(context_lens[s] / 16): the call keeps
  *                4 bytes a (Q head, token) between its kernels.  Sequences that
  *                no longer fit set PA_DEV_WORKSPACE: their out is written, their
- *                weights are not.  256-byte aligned, ZEROED before its first
- *                use, left ready for the next call (of any shape that it is
- *                large enough for); one call at a time.
+ *                weights are not.  256-byte aligned, contents undefined before
+ *                and after (unlike pa_decode's, it need not be zeroed); one call
+ *                at a time.
  * context_lens are read before the wait for the work ahead in the stream
  * (pa_decode_step has what that asks of it).  Other arguments, results, checks
  * and limits are those of pa_decode, and num_seqs * n_kv_heads <= 262144.  The

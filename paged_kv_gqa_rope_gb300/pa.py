@@ -944,11 +944,11 @@ def prepare_shared(block_tables, context_lens, block_size=16):
 
 
 def decode_shared_workspace(num_seqs, n_heads, n_kv_heads, head_dim, device="cuda"):
-    """A zeroed workspace for pa_decode_shared (its counters must start at zero)."""
+    """A workspace for pa_decode_shared."""
     n = lib().pa_decode_shared_workspace_bytes(num_seqs, n_heads, n_kv_heads, head_dim)
     if n == 0:
         raise ValueError("bad shared decode workspace shape")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def decode_shared(q, cache: Cache, block_tables, context_lens, group_starts, shared_blocks,
@@ -979,13 +979,13 @@ def decode_shared(q, cache: Cache, block_tables, context_lens, group_starts, sha
 
 def decode_weights_workspace(num_seqs, n_heads, n_kv_heads, head_dim, score_blocks,
                              device="cuda"):
-    """A zeroed workspace for pa_decode_weights batches whose contexts take at most
+    """A workspace for pa_decode_weights batches whose contexts take at most
     `score_blocks` blocks of 16 tokens together."""
     n = lib().pa_decode_weights_workspace_bytes(num_seqs, n_heads, n_kv_heads, head_dim,
                                                 score_blocks)
     if n == 0:
         raise ValueError("bad weights workspace shape")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def decode_weights(q, cache: Cache, block_tables, context_lens, weights, workspace, n_kv_heads,

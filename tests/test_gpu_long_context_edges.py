@@ -10,7 +10,7 @@ import torch
 
 from paged_kv_gqa_rope_gb300 import pa
 from tests.gpu_helpers import bits
-from tests.test_gpu_long_context import SHARED, SharedBatch, WeightBatch
+from tests.test_gpu_long_context import SHARED, SharedBatch, WeightBatch, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +71,33 @@ def test_weights_give_equal_values_back(H, Hk, d, lens):
         w = np.full(n, g * p / (1 + p * (n - 1)))
         w[0] = g / (1 + p * (n - 1))
         assert np.abs(got[s, :, :n] / w - 1).max() <= 2.0 ** -17
+
+
+# ------------------------------------------------------------------ workspaces
+
+@pytest.mark.parametrize("byte", [0xFF, 0x7F, 0x3C])
+def test_workspaces_hold_anything_before_the_first_call(byte):
+    """Bytes that read as NaN, as negative or as large numbers: the same bits come out as
+    from a cleared workspace, for sequences in order and those left out."""
+    for groups in SHARED + [[(20, [3, 9, 1]), (12, [5, 5]), (9, [2, 300, 4])]]:
+        b = SharedBatch(1, 8, 2, 128, groups)
+        if len(groups) == 3:
+            b.ctx[1] = 0  # left out
+        B, outs = len(b.ctx), []
+        for fill in (0, byte):
+            ws = pa.decode_shared_workspace(B, 8, 2, 128).fill_(fill)
+            status, out = pa.new_status(), torch.full(b.q.shape, 7.0).half().cuda()
+            b.run(ws=ws, out=out, status=status)
+            outs.append((out, int(status.item())))
+        assert torch.equal(outs[0][0], outs[1][0]) and outs[0][1] == outs[1][1]
+    for lens, blocks in (([1], 1), ([3000, 2, 77], 194), ([40] * 70, 210), ([300, 0, 9, 500], 24)):
+        w = WeightBatch(2, 8, 2, 128, lens)  # (the last: one left out, one with no room)
+        outs = []
+        for fill in (0, byte):
+            ws = pa.decode_weights_workspace(len(lens), 8, 2, 128, blocks).fill_(fill)
+            status, out = pa.new_status(), torch.full(w.q.shape, 7.0).half().cuda()
+            _, got = w.run(ws=ws, out=out, status=status)
+            outs.append((out, got, int(status.item())))
+        assert all(torch.equal(x, y) for x, y in zip(outs[0][:2], outs[1][:2]))
+        assert outs[0][2] == outs[1][2]
+        assert outs[0][2] == (pa.PA_DEV_BAD_LENGTH | pa.PA_DEV_WORKSPACE if 0 in lens else 0)
