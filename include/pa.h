@@ -698,8 +698,8 @@ int pa_rope_table_init_scaled(void *device_table, int max_positions, int rotary_
  * pa_decode.  context_lens, group_starts and shared_blocks are read before the
  * wait for the work ahead in the stream (pa_decode_step has what that asks of
  * it).  Other arguments, results and limits are those of pa_decode, and
- * num_seqs * n_kv_heads <= 262144.  The size is 0 for non-positive arguments and
- * one past SIZE_MAX.
+ * num_seqs * n_heads < 2^31 (PA_ERR_UNSUPPORTED otherwise).  The size is 0 for
+ * non-positive arguments and one past SIZE_MAX.
  */
 size_t pa_decode_shared_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads, int head_dim);
 int pa_decode_shared(const void *q, const pa_cache_t *cache, int layer,
@@ -749,8 +749,8 @@ int pa_prepare_shared(int num_seqs, const int32_t *block_tables, int max_blocks_
  *                at a time.
  * context_lens are read before the wait for the work ahead in the stream
  * (pa_decode_step has what that asks of it).  Other arguments, results, checks
- * and limits are those of pa_decode, and num_seqs * n_kv_heads <= 262144.  The
- * size is 0 for non-positive arguments and one past SIZE_MAX.
+ * and limits are those of pa_decode, and n_kv_heads <= 65535 (PA_ERR_UNSUPPORTED
+ * otherwise).  The size is 0 for non-positive arguments and one past SIZE_MAX.
  */
 size_t pa_decode_weights_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads, int head_dim,
                                          int64_t score_blocks);

@@ -164,7 +164,6 @@ int check_decode_args(const void *q, const pa_cache_t *cache, int layer,
 
 // The decode kernel in its other modes.  The CTAs' records stand at the start of the
 // workspace, which so serves calls of several shapes.
-constexpr int kModePairs = 1 << 18;  // (sequence, KV head) pairs of a call
 constexpr int kModeCtas = 608;          // with two records each
 size_t mode_workspace_bytes(int head_dim);
 constexpr int kModeRows = 8;             // of D + 4 floats each

@@ -999,7 +999,8 @@ extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int laye
                                      out);
     if (rc != PA_OK) return rc;
     if (num_groups < 0) return PA_ERR_INVALID;
-    if (num_groups > kMaxGroups || (int64_t)num_seqs * n_kv_heads > kModePairs)
+    // (rows of the records are counted in int32)
+    if (num_groups > kMaxGroups || (int64_t)num_seqs * n_heads > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
     if (num_groups == 0 || !group_starts || !shared_blocks || !workspace ||
@@ -1010,7 +1011,6 @@ extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int laye
     if (workspace_bytes < need) return PA_ERR_WORKSPACE;
     const int G = std::min(sm_count(), kMaxCtas);
     if (G < 1) return PA_ERR_CUDA;
-    if ((int64_t)num_seqs * n_heads > INT32_MAX) return PA_ERR_UNSUPPORTED;
 
     uint8_t *at = static_cast<uint8_t *>(workspace);
     uint8_t *p = at + up256(mode_workspace_bytes(head_dim));

@@ -252,8 +252,7 @@ extern "C" int pa_decode_weights(const void *q, const pa_cache_t *cache, int lay
                                      out);
     if (rc != PA_OK) return rc;
     if (weights_stride <= 0) return PA_ERR_INVALID;
-    if (n_kv_heads > 65535 || (int64_t)num_seqs * n_kv_heads > kModePairs)
-        return PA_ERR_UNSUPPORTED;
+    if (n_kv_heads > 65535) return PA_ERR_UNSUPPORTED;  // (a grid's y)
     if (num_seqs == 0) return PA_OK;
     if (!weights_out || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return PA_ERR_INVALID;

@@ -10,7 +10,7 @@ import torch
 
 from paged_kv_gqa_rope_gb300 import pa
 from tests.gpu_helpers import bits
-from tests.test_gpu_long_context import SHARED, SharedBatch, WeightBatch, dev
+from tests.test_gpu_long_context import SHARED, SharedBatch, WeightBatch, dev, ints, normal16
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +101,32 @@ def test_workspaces_hold_anything_before_the_first_call(byte):
         assert all(torch.equal(x, y) for x, y in zip(outs[0][:2], outs[1][:2]))
         assert outs[0][2] == outs[1][2]
         assert outs[0][2] == (pa.PA_DEV_BAD_LENGTH | pa.PA_DEV_WORKSPACE if 0 in lens else 0)
+
+
+def test_half_a_million_pairs():
+    """4096 sequences of 128 KV heads, 5 tokens behind 4 blocks that 64 of them share: with
+    equal values in a head every output is the value, and the weights of a KV head's only Q
+    head sum to 1."""
+    B, H, d, pre, n = 4096, 128, 64, 4, 69
+    rng = np.random.default_rng(3)
+    row = rng.uniform(0.25, 4, (H, d)).astype(np.float16)
+    cache = pa.Cache(1, 40, H, d)
+    cache.tensor[0] = dev(normal16(rng, 1, 40, 16, H, d))
+    cache.tensor[1] = dev(row)
+    bt = np.empty((B, pre + 1), np.int32)
+    for r in range(B // 64):
+        bt[64 * r:64 * r + 64, :pre] = rng.permutation(40)[:pre]
+    bt[:, pre] = rng.integers(0, 40, B)
+    q, ctx = dev(normal16(rng, B, H, d)), ints([n] * B)
+    status = pa.new_status()
+    out = pa.decode_shared(q, cache, dev(bt), ctx, ints(list(range(0, B + 1, 64))),
+                           ints([pre] * (B // 64)), pa.decode_shared_workspace(B, H, H, d), H,
+                           status=status)
+    assert int(status.item()) == 0 and torch.equal(out, dev(row).expand_as(out))
+    w = torch.zeros(B, H, 80, device="cuda")
+    out, _ = pa.decode_weights(q, cache, dev(bt), ctx, w,
+                               pa.decode_weights_workspace(B, H, H, d, B * (pre + 1)), H,
+                               status=status)
+    assert int(status.item()) == 0 and torch.equal(out, dev(row).expand_as(out))
+    # (69 weights, each with the roundings of an exponent below 16 and of a sum)
+    assert (w.sum(-1) - 1).abs().max() <= 2.0 ** -16 and not w[..., n:].any()

@@ -1,0 +1,35 @@
+"""The long-context operators' sizes, refusals and host state that test_long_context_host.py
+leaves out, without a GPU."""
+
+import ctypes
+
+import pytest
+
+from paged_kv_gqa_rope_gb300 import pa
+
+BUF = ctypes.c_void_p(1 << 24)
+INT_MAX = 2**31 - 1
+
+
+def desc_of(libpa, Hk, d=64):
+    x = pa.PaCache()
+    assert libpa.pa_alloc_cache(ctypes.byref(x), 1, 64, 16, Hk, d, ctypes.c_void_p(1 << 20)) == 0
+    return ctypes.byref(x)
+
+
+def test_limits_on_heads(libpa):
+    """More (sequence, KV head) pairs than 2^18 are in order (here the workspace alone is
+    too small); rows past int32 and KV heads past a grid's y are not."""
+    def shared(B, H, Hk):
+        return libpa.pa_decode_shared(BUF, desc_of(libpa, Hk), 0, BUF, 4, BUF, B, BUF, BUF, 1, H, Hk,
+                                      64, 0.0, BUF, 0, BUF, None, None)
+
+    def weights(B, H, Hk):
+        return libpa.pa_decode_weights(BUF, desc_of(libpa, Hk), 0, BUF, 4, BUF, B, H, Hk, 64, 0.0,
+                                       BUF, BUF, 64, BUF, 0, BUF, None, None)
+
+    assert shared(4096, 128, 128) == weights(4096, 128, 128) == pa.PA_ERR_WORKSPACE
+    assert shared(4096, 2**19 - 1, 2**19 - 1) == pa.PA_ERR_WORKSPACE
+    assert shared(4096, 2**19, 2**19) == pa.PA_ERR_UNSUPPORTED
+    assert weights(4096, 65535, 65535) == pa.PA_ERR_WORKSPACE
+    assert weights(1, 65536, 65536) == pa.PA_ERR_UNSUPPORTED
