@@ -33,3 +33,11 @@ def test_limits_on_heads(libpa):
     assert shared(4096, 2**19, 2**19) == pa.PA_ERR_UNSUPPORTED
     assert weights(4096, 65535, 65535) == pa.PA_ERR_WORKSPACE
     assert weights(1, 65536, 65536) == pa.PA_ERR_UNSUPPORTED
+
+
+def test_shared_workspace_size_does_not_wrap(libpa):
+    """4 (num_seqs n_kv_heads) bytes of cut words pass 64 bits where the rows do not."""
+    size = libpa.pa_decode_shared_workspace_bytes
+    assert size(INT_MAX, 1, INT_MAX, 128) == size(INT_MAX, 8, INT_MAX, 64) == 0
+    assert size(INT_MAX, 1, 2**30, 128) > 2**63
+    assert size(4096, 64, 8, 128) > 2 * 4096 * 64 * 132 * 4
