@@ -978,8 +978,13 @@ using namespace pa;
 extern "C" size_t pa_decode_shared_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads,
                                                    int head_dim) {
     if (num_seqs <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0) return 0;
+    // (the parts first: each must fit by itself before it is counted in 64 bits)
     const unsigned __int128 row_bytes = (head_dim + (int64_t)4) * sizeof(float);
-    if (row_bytes * num_seqs * n_heads > SIZE_MAX / 4) return 0;
+    const unsigned __int128 n =
+        row_bytes * (2 * (unsigned __int128)num_seqs * n_heads + 2 * kPrefixTile * kMaxCtas) +
+        (unsigned __int128)num_seqs * sizeof(SeqPlan) +
+        (unsigned __int128)num_seqs * n_kv_heads * sizeof(int32_t);
+    if (n > SIZE_MAX - mode_workspace_bytes(head_dim) - 8 * 256) return 0;
     return up256(mode_workspace_bytes(head_dim)) + 256 +
            up256((size_t)num_seqs * sizeof(SeqPlan)) +
            up256((size_t)num_seqs * n_kv_heads * sizeof(int32_t)) +
