@@ -1331,7 +1331,7 @@ constexpr int kStagesI8 = 8;
 size_t counters_bytes(int B, int Hk) {
     return ((size_t)B * Hk * sizeof(int32_t) + 255) & ~(size_t)255;
 }
-size_t cta_record_bytes(int D) { return (size_t)2 * kGroupPad * (D + 4) * sizeof(float); }
+size_t cta_record_bytes(int D) { return (size_t)2 * kGroupPad * ((size_t)D + 4) * sizeof(float); }
 
 }  // namespace
 }  // namespace pa

@@ -960,7 +960,7 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr int kMaxGroups = 4096;
 constexpr int kMaxCtas = 160;  // (152 SMs)
 
-size_t rows_bytes(int B, int H, int D) { return up256((size_t)B * H * (D + 4) * sizeof(float)); }
+size_t rows_bytes(int B, int H, int D) { return up256((size_t)B * H * ((size_t)D + 4) * sizeof(float)); }
 
 template <int D>
 int launch_join(const SharedArgs &a, cudaStream_t st) {

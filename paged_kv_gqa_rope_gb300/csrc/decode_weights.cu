@@ -214,7 +214,7 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Workspace: the decode kernel's, the statistics, each sequence's first block, the cut
 // pairs, their first pieces, scores.
-size_t record_bytes(int B, int H, int D) { return up256((size_t)B * H * (D + 4) * sizeof(float)); }
+size_t record_bytes(int B, int H, int D) { return up256((size_t)B * H * ((size_t)D + 4) * sizeof(float)); }
 size_t fixed_bytes(int B, int H, int Hk, int D) {
     return up256(mode_workspace_bytes(D)) + up256((size_t)B * H * sizeof(float2)) +
            up256((size_t)B * sizeof(int64_t)) + up256((size_t)B * Hk * sizeof(int32_t)) +

@@ -41,3 +41,12 @@ def test_shared_workspace_size_does_not_wrap(libpa):
     assert size(INT_MAX, 1, INT_MAX, 128) == size(INT_MAX, 8, INT_MAX, 64) == 0
     assert size(INT_MAX, 1, 2**30, 128) > 2**63
     assert size(4096, 64, 8, 128) > 2 * 4096 * 64 * 132 * 4
+
+
+def test_workspace_sizes_of_the_largest_rows(libpa):
+    """head_dim + 4 values a row, counted past int32."""
+    row = 4 * (INT_MAX + 4)
+    assert libpa.pa_decode_shared_workspace_bytes(1, 1, 1, INT_MAX) > 608 * 16 * row
+    assert libpa.pa_decode_weights_workspace_bytes(1, 1, 1, INT_MAX, 1) > 608 * 16 * row
+    assert libpa.pa_decode_workspace_bytes(1, 1, 1, INT_MAX) > 608 * 16 * row
+    assert libpa.pa_decode_workspace_bytes(1, 1, 1, INT_MAX) < 609 * 16 * row
