@@ -107,7 +107,8 @@ int pa_bm_block_table(pa_bm_t bm, int64_t seq_id, int32_t *table, int max_blocks
  * matched); the caller keeps track of true positions.  With num_keep >= its
  * tokens nothing changes.  begin fails for a sequence whose prompt is not
  * computed or that is being evicted (PA_ERR_INVALID), or with too few free blocks
- * (PA_ERR_WORKSPACE, nothing changed); between begin and end pa_bm_append fails.
+ * (PA_ERR_WORKSPACE, nothing changed); between begin and end pa_bm_append fails
+ * and pa_bm_can_append is 0.
  */
 int pa_bm_evict_begin(pa_bm_t bm, int64_t seq_id, int num_keep);
 int pa_bm_evict_end(pa_bm_t bm, int64_t seq_id);

@@ -203,6 +203,7 @@ int pa_bm_mark_computed(pa_bm_t bm, int64_t seq_id, int num_tokens) {
 int pa_bm_can_append(pa_bm_t bm, int64_t seq_id) {
     Seq *s = bm ? bm->find(seq_id) : nullptr;
     if (!s) return -PA_ERR_INVALID;
+    if (s->evicting) return 0;
     return (s->tokens.size() % bm->bs) != 0 || !bm->free_list.empty() ? 1 : 0;
 }
 

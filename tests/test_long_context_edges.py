@@ -50,3 +50,26 @@ def test_workspace_sizes_of_the_largest_rows(libpa):
     assert libpa.pa_decode_weights_workspace_bytes(1, 1, 1, INT_MAX, 1) > 608 * 16 * row
     assert libpa.pa_decode_workspace_bytes(1, 1, 1, INT_MAX) > 608 * 16 * row
     assert libpa.pa_decode_workspace_bytes(1, 1, 1, INT_MAX) < 609 * 16 * row
+
+
+def test_no_append_while_evicting(libpa):
+    """pa_bm_can_append says what pa_bm_append will do between begin and end; the count of
+    tokens is right at each step of a loop that evicts."""
+    bm = pa.BlockManager(8)
+    bm.allocate(1, list(range(40)))
+    bm.mark_computed(1, 40)
+    n = 40
+    for step in range(30):
+        assert bm.can_append(1)
+        bm.append(1, step)
+        n += 1
+        assert bm.num_tokens(1) == n
+        if step in (3, 17):
+            n = 40 if step == 3 else n  # (the second time nothing goes)
+            bm.evict_begin(1, n)
+            assert bm.num_tokens(1) == n and not bm.can_append(1)
+            with pytest.raises(pa.PAError):
+                bm.append(1, 0)
+            bm.evict_end(1)
+            assert bm.num_tokens(1) == n and bm.can_append(1)
+    assert len(bm.block_table(1)) == -(-n // 16)
