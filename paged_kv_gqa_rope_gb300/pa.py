@@ -237,6 +237,13 @@ def _bound(n):
     return min(int(n), 2**31 - 1)
 
 
+def _int32(**numbers):
+    """Refuses numbers that the library would see cut to their low 32 bits."""
+    for name, x in numbers.items():
+        if not -2**31 <= x < 2**31:
+            raise ValueError(f"{name} {x} does not fit int32")
+
+
 def _opt(t, dtype, name, shape):
     return None if t is None else _dev(t, dtype, name, shape)
 
@@ -577,7 +584,8 @@ class BlockManager:
 
     def evict_begin(self, seq_id, num_keep):
         """Switch to the table of the kept rows (kv_evict's out_block_tables)."""
-        _check("pa_bm_evict_begin", lib().pa_bm_evict_begin(self._h, seq_id, int(num_keep)))
+        _check("pa_bm_evict_begin", lib().pa_bm_evict_begin(self._h, seq_id,
+                                                            _bound(max(num_keep, 0))))
 
     def evict_end(self, seq_id):
         """The evictions are enqueued: the blocks left behind may be reused."""
@@ -914,6 +922,8 @@ def rope_table_scaled(max_positions, rotary_dim, theta=10000.0, scaling=None, fa
     unless given)."""
     if scaling is not None and scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling {scaling!r} is none of {', '.join(ROPE_SCALINGS)}")
+    _int32(max_positions=max_positions, rotary_dim=rotary_dim,
+           original_positions=original_positions)
     if lib().pa_rope_table_bytes(max_positions, rotary_dim) == 0:
         raise ValueError("bad RoPE table shape")
     if high is None:
@@ -932,6 +942,7 @@ def rope_table_scaled(max_positions, rotary_dim, theta=10000.0, scaling=None, fa
 def prepare_shared(block_tables, context_lens, block_size=16):
     """pa_prepare_shared: the groups of neighbouring sequences whose block tables begin
     alike, as group_starts [groups + 1] and shared_blocks [groups] (numpy)."""
+    _int32(block_size=block_size)
     bt = np.ascontiguousarray(block_tables, np.int32)
     ctx = np.ascontiguousarray(context_lens, np.int32)
     if bt.ndim != 2 or ctx.shape != bt.shape[:1]:
@@ -945,6 +956,7 @@ def prepare_shared(block_tables, context_lens, block_size=16):
 
 def decode_shared_workspace(num_seqs, n_heads, n_kv_heads, head_dim, device="cuda"):
     """A workspace for pa_decode_shared."""
+    _int32(num_seqs=num_seqs, n_heads=n_heads, n_kv_heads=n_kv_heads, head_dim=head_dim)
     n = lib().pa_decode_shared_workspace_bytes(num_seqs, n_heads, n_kv_heads, head_dim)
     if n == 0:
         raise ValueError("bad shared decode workspace shape")
@@ -981,6 +993,7 @@ def decode_weights_workspace(num_seqs, n_heads, n_kv_heads, head_dim, score_bloc
                              device="cuda"):
     """A workspace for pa_decode_weights batches whose contexts take at most
     `score_blocks` blocks of 16 tokens together."""
+    _int32(num_seqs=num_seqs, n_heads=n_heads, n_kv_heads=n_kv_heads, head_dim=head_dim)
     n = lib().pa_decode_weights_workspace_bytes(num_seqs, n_heads, n_kv_heads, head_dim,
                                                 score_blocks)
     if n == 0:
@@ -1022,6 +1035,7 @@ def decode_weights(q, cache: Cache, block_tables, context_lens, weights, workspa
 
 def kv_evict_workspace(num_seqs, n_kv_heads, budget, device="cuda"):
     """A workspace for pa_kv_evict."""
+    _int32(num_seqs=num_seqs, n_kv_heads=n_kv_heads, budget=budget)
     n = lib().pa_kv_evict_workspace_bytes(num_seqs, n_kv_heads, budget)
     if n == 0:
         raise ValueError("bad eviction workspace shape")
@@ -1053,9 +1067,7 @@ def kv_evict(cache: Cache, block_tables, context_lens, weights, budget, workspac
         _refuse_rank((block_tables, 2, "block_tables"), (out_block_tables, 2, "out_block_tables"),
                      (workspace, 1, "workspace"), (weights, 3, "weights"))
     desc = _cache_f16(dev, cache)
-    for name, x in (("budget", budget), ("sinks", sinks), ("recent", recent)):
-        if not -2**31 <= x < 2**31:
-            raise ValueError(f"{name} {x} does not fit int32")
+    _int32(budget=budget, sinks=sinks, recent=recent)
     _call_on(dev, "pa_kv_evict", stream, desc, _layer_i4(layer),
              _on(dev, block_tables, torch.int32, "block_tables", B, width),
              _table_width(block_tables), _on(dev, context_lens, torch.int32, "context_lens", B), B,

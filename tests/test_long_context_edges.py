@@ -2,7 +2,9 @@
 leaves out, without a GPU."""
 
 import ctypes
+import sys
 
+import numpy as np
 import pytest
 
 from paged_kv_gqa_rope_gb300 import pa
@@ -73,3 +75,37 @@ def test_no_append_while_evicting(libpa):
             bm.evict_end(1)
             assert bm.num_tokens(1) == n and bm.can_append(1)
     assert len(bm.block_table(1)) == -(-n // 16)
+
+
+def test_binding_does_not_cut_to_32_bits(libpa):
+    """Numbers past int32 reach the library as themselves, bounds, or not at all; cut to
+    their low 32 bits they would be another call's."""
+    far = 2**32
+    bm = pa.BlockManager(8)
+    bm.allocate(1, list(range(60)))
+    bm.mark_computed(1, 60)
+    for keep in (far + 16, 2**31 + 16, sys.maxsize):
+        bm.evict_begin(1, keep)  # more than it has: nothing goes
+        bm.evict_end(1)
+        assert bm.num_tokens(1) == 60 and len(bm.block_table(1)) == 4
+    for keep in (-far + 16, 0):
+        with pytest.raises(pa.PAError):
+            bm.evict_begin(1, keep)
+    yarn = dict(scaling="yarn", factor=2.0, original_positions=64)
+    for bad in (dict(original_positions=far + 64), dict(original_positions=-far + 64)):
+        with pytest.raises(ValueError):
+            pa.rope_table_scaled(8, 64, **{**yarn, **bad})
+    for shape in ((far + 8, 64), (8, far + 64)):
+        with pytest.raises(ValueError):
+            pa.rope_table_scaled(*shape, **yarn)
+    with pytest.raises(ValueError):
+        pa.prepare_shared(np.zeros((1, 2), np.int32), np.zeros(1, np.int32), block_size=far + 16)
+    for make, sizes in ((pa.decode_shared_workspace, (2, 8, 2, 64)),
+                        (pa.decode_weights_workspace, (2, 8, 2, 64, 3)),
+                        (pa.kv_evict_workspace, (2, 2, 8))):
+        for i in range(len(sizes)):
+            if i == 4:
+                continue  # (blocks of scores: int64)
+            with pytest.raises(ValueError):
+                make(*(x + far * (i == j) for j, x in enumerate(sizes)), device="cpu")
+        assert make(*sizes, device="cpu").numel() > 0
