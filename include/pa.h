@@ -23,7 +23,7 @@
  *  - fp16 is IEEE binary16 (stored as uint16_t bits); metadata is int32.
  *  - Device work is enqueued on `stream` (a cudaStream_t; NULL = the legacy
  *    default stream) and is asynchronous: no entry point synchronises the
- *    stream except pa_rope_table_init.
+ *    stream except pa_rope_table_init and pa_rope_table_init_scaled.
  *  - The return value is a pa_status code.  Arguments are checked on the
  *    host before anything is enqueued; an invalid call returns
  *    PA_ERR_INVALID / PA_ERR_UNSUPPORTED and touches no memory.
@@ -644,9 +644,11 @@ int pa_rope_kv_write_layout(const void *q, void *q_out, const void *k, const voi
  *                     (high - low), 0, 1), turns_i = original_positions f_i / (2 pi)
  * Entries are {a cos, a sin} of m f_i, computed in double precision on the host
  * and rounded once to float; a = attention, or, where that is 0, 1, and for
- * PA_ROPE_YARN 0.1 ln(factor) + 1.  factor >= 1; 0 < low < high and
- * original_positions > 0 for the last two kinds; scaling NULL is
- * PA_ROPE_UNSCALED.  rotary_dim: a multiple of 16 up to 128
+ * PA_ROPE_YARN 0.1 ln(factor) + 1.  theta is finite and above 1 whatever the kind
+ * (frequencies fall from pair to pair), and so is the base that PA_ROPE_NTK makes
+ * of it; factor >= 1; 0 < low < high and original_positions > 0 for the last two
+ * kinds; attention 0 or finite and positive (PA_ERR_INVALID otherwise); scaling
+ * NULL is PA_ROPE_UNSCALED.  rotary_dim: a multiple of 16 up to 128
  * (PA_ERR_UNSUPPORTED otherwise).  device_table holds
  * pa_rope_table_bytes(max_positions, rotary_dim) bytes, 16-byte aligned.
  * Synchronises `stream`.

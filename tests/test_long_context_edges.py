@@ -2,6 +2,7 @@
 leaves out, without a GPU."""
 
 import ctypes
+import math
 import sys
 
 import numpy as np
@@ -109,3 +110,16 @@ def test_binding_does_not_cut_to_32_bits(libpa):
             with pytest.raises(ValueError):
                 make(*(x + far * (i == j) for j, x in enumerate(sizes)), device="cpu")
         assert make(*sizes, device="cpu").numel() > 0
+
+
+def test_scaled_tables_take_a_base_above_one(libpa):
+    def call(theta, sc=None):
+        return libpa.pa_rope_table_init_scaled(BUF, 8, 64, theta,
+                                               None if sc is None else ctypes.byref(sc), None)
+
+    kinds = [None] + [pa.PaRopeScaling(k, 64, 2.0, 1.0, 4.0, 0.0) for k in range(5)]
+    for sc in kinds:
+        for theta in (1.0, 0.5, 0.0, -2.0, math.inf, math.nan):
+            assert call(theta, sc) == pa.PA_ERR_INVALID
+    # the base that NTK makes of it
+    assert call(1e300, pa.PaRopeScaling(2, 0, 1e30, 0.0, 0.0, 0.0)) == pa.PA_ERR_INVALID
