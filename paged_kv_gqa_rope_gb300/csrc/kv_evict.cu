@@ -6,8 +6,10 @@
 // the largest weight, of equal ones the first.  Two kernels:
 //
 //   select  one CTA per (sequence, KV head), or where there are few of them a
-//           cluster of up to eight, which keep the weights in registers (those past
-//           262144 tokens are read again).  The m-th largest weight among
+//           cluster of up to eight, which keep the weights in registers, 32768 tokens
+//           a CTA.  Where the tables allow rows past what the cluster then holds
+//           (262112 tokens of eight CTAs) it is one CTA that reads those past 32768
+//           again, once a digit and once for the places.  The m-th largest weight among
 //           the others is found digit by digit (11 + 11 + 10 bits of a key that
 //           orders like the weights): a histogram of the digit over the keys that
 //           agree on the digits before it, and the digit at which the count from the
@@ -543,7 +545,10 @@ extern "C" int pa_kv_evict(const pa_cache_t *cache, int layer, const int32_t *bl
         cap, kAheadBytes / ((int64_t)num_seqs * n_kv_heads * 4 * head_dim));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // As many CTAs a list as find an SM each, of a chunk of tokens at least, and
-    // registers for the tokens that a table row can hold, as far as they go.
+    // registers for the tokens that a table row can hold, as far as they go.  (The
+    // lengths are on the device.  One sequence of 32767 tokens cut to 4096, 8 KV heads,
+    // in a graph: 20.4 us with a table of 32768 tokens, 26.6 of 131072 to 262112, 51.6
+    // past that; 32 of 1000 to 5000 cut to 1024: 55 of 5008, 72 of 8192 and more.)
     const int longest = max_blocks_per_seq * kBlockSize;
     int size = 1;
     while (size < kMaxCluster && size * kChunk < longest &&

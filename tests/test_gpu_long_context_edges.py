@@ -8,9 +8,11 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import reference as orc
 from paged_kv_gqa_rope_gb300 import pa
-from tests.gpu_helpers import bits
-from tests.test_gpu_long_context import SHARED, SharedBatch, WeightBatch, dev, ints, normal16
+from tests.gpu_helpers import assert_attention_close, bits
+from tests.test_gpu_long_context import (SHARED, EvictBatch, SharedBatch, WeightBatch, dev, ints,
+                                         normal16)
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +132,46 @@ def test_half_a_million_pairs():
     assert int(status.item()) == 0 and torch.equal(out, dev(row).expand_as(out))
     # (69 weights, each with the roundings of an exponent below 16 and of a sum)
     assert (w.sum(-1) - 1).abs().max() <= 2.0 ** -16 and not w[..., n:].any()
+
+
+# ------------------------------------------------------------------ wide tables
+
+@pytest.mark.parametrize("width", [16383, 16384, 17000, 70000])
+@pytest.mark.parametrize("lens", [[33000, 700], [70000, 20, 100, 5000, 3]])
+def test_evict_with_tables_far_wider_than_the_contexts(width, lens):
+    """Tables of 262128 tokens and more: clusters give way to one CTA a list, which reads
+    what is past its registers again.  In place, weights beside, and into other blocks."""
+    def widen(b):
+        b.bt = np.concatenate([b.bt, np.full((len(lens), width - b.bt.shape[1]), -1, np.int32)], 1)
+        return b
+
+    for budget, sinks, recent in ((3000, 4, 256), (200, 0, 0)):
+        widen(EvictBatch(1, 2, 2, 64, lens)).check(budget, sinks, recent)
+    b = widen(EvictBatch(2, 2, 2, 64, lens, layers=2, layer=1))
+    b.w[0, 0, :lens[0]] = 0.5  # (ties among what is read again)
+    pool, want = b.pool.copy(), b.w.copy()
+    n = orc.evict(pool, 1, b.bt, b.ctx, want, 1500, 4, 64, b.bt)
+    for s, k in enumerate(lens):
+        want[s, :, k:] = 5
+    beside, status = torch.full(b.w.shape, 5.0, device="cuda"), pa.new_status()
+    got, lens_out = b.run(1500, 4, 64, weights_out=beside, status=status)
+    assert int(status.item()) == 0 and np.array_equal(lens_out.cpu().numpy(), n)
+    assert np.array_equal(got.cpu().numpy(), want) and np.array_equal(bits(b.cache.tensor), bits(pool))
+    b = widen(EvictBatch(3, 2, 2, 64, lens))
+    more = -(-1500 // 16) * len(lens)
+    b.pool = np.concatenate([b.pool, np.full_like(b.pool[:, :, :more], 7)], 2)
+    to = np.arange(b.NB, b.NB + more, dtype=np.int32).reshape(len(lens), -1)
+    b.NB += more
+    b.check(1500, 4, 64, to)
+
+
+def test_decodes_with_tables_far_wider_than_the_contexts():
+    b = SharedBatch(4, 8, 2, 64, [(20, [3, 40]), (0, [17])])
+    w = WeightBatch(5, 8, 2, 64, [300, 2, 64])
+    for x in (b, w):
+        x.bt = np.concatenate([x.bt, np.full((3, 70000), -1, np.int32)], 1)
+    assert_attention_close(b.run(), b.want())
+    out, got = w.run()
+    assert_attention_close(out, w.out())
+    want, tol = w.want()
+    assert (np.abs(got.cpu().numpy() - want) <= tol).all()
