@@ -75,7 +75,7 @@ struct DecodeArgs {
     DecodeTails tl;               // Mode::kTails
 };
 
-// What a launch leaves besides, or in the place of, the output (internal.h).
+// What a launch leaves besides, or in the place of, the output (decode_modes.cuh).
 enum class Mode { kOut, kScores, kTails };
 
 // P enters the tensor core as 2^(x - max + kPShift) in the modes other than

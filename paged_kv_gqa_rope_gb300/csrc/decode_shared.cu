@@ -1092,7 +1092,6 @@ extern "C" int pa_prepare_shared(int num_seqs, const int32_t *block_tables,
                 shared_blocks[n - 1] = c;
                 continue;
             }
-            if (members == 1) shared_blocks[n - 1] = 0;
         }
         group_starts[n] = s;
         shared_blocks[n] = 0;

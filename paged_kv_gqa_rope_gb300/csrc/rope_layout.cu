@@ -76,8 +76,8 @@ __device__ __forceinline__ void turn_halves(uint4 &lo, uint4 &hi, const float4 *
     }
 }
 
-// Work item i of a token: item u of row `row`, its pieces p0 and p1.
-template <int D, bool HALF>
+// The pieces p0 and p1 of a row's work item u; the first nrot items are rotated.
+template <bool HALF>
 __device__ __forceinline__ void pieces_of(int u, int nrot, int &p0, int &p1) {
     if (HALF && u < nrot) {
         p0 = u;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kTokenThreads) rope_layout_kernel(const Layout
         src = reinterpret_cast<const uint4 *>(a.k + ((int64_t)t * Hk + h) * D);
         dst = reinterpret_cast<uint4 *>(a.kcache + ((int64_t)slot * Hk + h) * D);
     }
-    pieces_of<D, HALF>(u, nrot, p0, p1);
+    pieces_of<HALF>(u, nrot, p0, p1);
     uint4 x0 = __ldcs(src + p0), x1 = __ldcs(src + p1);
     if (u < nrot) {
         const float4 *cs =
