@@ -83,13 +83,20 @@ struct Pieces {
     int32_t *cut;  // [B][Hk]: CTA of the second piece | pieces but the first << 16
 };
 
+// A sequence in pa_decode_weights: its first block in the scores (-1: none kept, -2: left
+// out), and its tokens, as the decode kernel has checked and counted them.
+struct alignas(16) SeqScores {
+    int64_t first;
+    int32_t len, pad;
+};
+
 // pa_decode_weights: scores and row statistics besides the output.  Of a pair left in
 // pieces (of no other) there are no statistics and no output.
 struct DecodeScores {
     Pieces pieces;
     float *scores;     // [blocks of all KV heads][16 tokens][g]: log2 units
     float2 *stats;     // [B][H]: {m, 1 / w}, a weight being 2^(score - m) / w
-    int64_t *first;    // [B]: a sequence's first block in scores, -1: none kept, -2: left out
+    SeqScores *seqs;   // [B]
     int64_t capacity;  // blocks of all KV heads that scores holds
     int max_len;       // longest context that the rows of weights hold
 };

@@ -25,7 +25,6 @@ constexpr int kFewPieces = 8;  // that a thread reads at once
 
 struct WeightArgs {
     DecodeScores sc;
-    const int32_t *context_lens;
     const float *weights;  // nullptr: zeros
     float *weights_out;
     __half *out;
@@ -48,8 +47,11 @@ __global__ void __launch_bounds__(kWeightThreads, 8) weights_kernel(const Weight
     griddep_wait();
     griddep_launch_dependents();
     const int h = blockIdx.y, s = blockIdx.z;
-    const int64_t first = a.sc.first[s];
-    const int n = first == -1 ? 0 : a.context_lens[s];  // (-1: no scores kept)
+    // (The length is the one that the decode kernel read: context_lens, should they have
+    // changed since, could lead past the scores and the rows of weights.)
+    const SeqScores q = a.sc.seqs[s];
+    const int64_t first = q.first;
+    const int n = first == -1 ? 0 : q.len;  // (-1: no scores kept)
     const Cut cut = cut_of(a.sc.pieces.cut[s * a.Hk + h]);
     if (first == -2) return;
     __shared__ float2 stats[G];
@@ -217,7 +219,7 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t record_bytes(int B, int H, int D) { return up256((size_t)B * H * ((size_t)D + 4) * sizeof(float)); }
 size_t fixed_bytes(int B, int H, int Hk, int D) {
     return up256(mode_workspace_bytes(D)) + up256((size_t)B * H * sizeof(float2)) +
-           up256((size_t)B * sizeof(int64_t)) + up256((size_t)B * Hk * sizeof(int32_t)) +
+           up256((size_t)B * sizeof(SeqScores)) + up256((size_t)B * Hk * sizeof(int32_t)) +
            record_bytes(B, H, D);
 }
 
@@ -269,15 +271,14 @@ extern "C" int pa_decode_weights(const void *q, const pa_cache_t *cache, int lay
     WeightArgs w;
     w.sc.stats = reinterpret_cast<float2 *>(p);
     p += up256((size_t)num_seqs * n_heads * sizeof(float2));
-    w.sc.first = reinterpret_cast<int64_t *>(p);
-    p += up256((size_t)num_seqs * sizeof(int64_t));
+    w.sc.seqs = reinterpret_cast<SeqScores *>(p);
+    p += up256((size_t)num_seqs * sizeof(SeqScores));
     w.sc.pieces.cut = reinterpret_cast<int32_t *>(p);
     p += up256((size_t)num_seqs * n_kv_heads * sizeof(int32_t));
     w.sc.pieces.rec = reinterpret_cast<float *>(p);
     w.sc.scores = reinterpret_cast<float *>(at + fixed);
     w.sc.capacity = (int64_t)((workspace_bytes - fixed) / block) * n_kv_heads;
     w.sc.max_len = (int)std::min<int64_t>(weights_stride, INT32_MAX);
-    w.context_lens = context_lens;
     w.weights = weights;
     w.weights_out = weights_out;
     w.stride = weights_stride;
