@@ -12,7 +12,7 @@ namespace pa {
 struct Groups {
     const int32_t *starts;
     const int32_t *blocks;
-    int n, maxb;
+    int n, maxb, seqs;
 };
 
 // A group whose prefix is read once.  The prefixes' work lies on a line: group
@@ -252,14 +252,18 @@ __device__ __forceinline__ int read_groups(const Groups &g, const int32_t *conte
     return __syncthreads_or(bad) != 0 ? 1 : 0;
 }
 
-// Group r's share of the line (tiles 0: none), from global memory.
+// Group r's share of the line (tiles 0: none), from global memory.  (Whoever asks has
+// seen that the groups are a partition; a group that by now is none of the sequences'
+// has no share, so that no read leaves the arrays.)
 __device__ __forceinline__ PlanGroup load_group(const Groups &g, const int32_t *context_lens, int r,
                                                 int per_unit) {
     PlanGroup p;
     p.s0 = __ldg(g.starts + r);
     p.members = __ldg(g.starts + r + 1) - p.s0;
     const int named = __ldg(g.blocks + r);
-    p.blocks = named >= 0 && named <= g.maxb ? shared_of(named, p.members) : 0;
+    const bool in_range = named >= 0 && named <= g.maxb && p.s0 >= 0 && p.members >= 0 &&
+                          p.members <= g.seqs - p.s0;
+    p.blocks = in_range ? shared_of(named, p.members) : 0;
     p.lead = p.s0;
     if (p.blocks > 0) {
         // the first sequence in order (as read_groups has it)

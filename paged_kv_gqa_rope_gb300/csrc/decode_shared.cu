@@ -160,8 +160,9 @@ struct PrefixWalk {
         const int mpt = kPrefixTile / a.g;
         while (left > 0) {
             if (unit == seg.p.units * a.Hk) {
-                do {  // (places are left, so a group with some follows)
-                    seg.p = load_group(a.groups, a.context_lens, ++group, 2 * mpt);
+                do {  // (places are left, so a group with some follows; to the last at most)
+                    if (++group >= a.groups.n) return false;
+                    seg.p = load_group(a.groups, a.context_lens, group, 2 * mpt);
                 } while (seg.p.tiles == 0);
                 unit = 0;
             }
@@ -1034,7 +1035,7 @@ extern "C" int pa_decode_shared(const void *q, const pa_cache_t *cache, int laye
     a.first = reinterpret_cast<float *>(p);
     p += rows_bytes(num_seqs, n_heads, head_dim);
     a.more = reinterpret_cast<float *>(p);
-    a.groups = {group_starts, shared_blocks, num_groups, max_blocks_per_seq};
+    a.groups = {group_starts, shared_blocks, num_groups, max_blocks_per_seq, num_seqs};
     a.q = static_cast<const __half *>(q);
     a.plane_k = layer;
     a.plane_v = cache->layers + layer;
