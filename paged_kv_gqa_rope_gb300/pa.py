@@ -966,7 +966,12 @@ def decode_shared_workspace(num_seqs, n_heads, n_kv_heads, head_dim, device="cud
 def decode_shared(q, cache: Cache, block_tables, context_lens, group_starts, shared_blocks,
                   workspace, n_kv_heads, layer=0, scale=0.0, out=None, status=None, stream=None):
     """pa_decode_shared: decode of sequences group_starts[r] .. group_starts[r + 1] - 1
-    that share their first shared_blocks[r] blocks, read once for the group."""
+    that share their first shared_blocks[r] blocks, read once for the group.
+    `context_lens`, `group_starts` and `shared_blocks` are read before the wait for the
+    work ahead in the stream: torch operations, copies and this library's calls may write
+    them directly before, a kernel that lets its dependents launch early
+    (griddepcontrol.launch_dependents, programmatic launches of compiled kernels) may
+    not."""
     try:
         (B, H, d), (_, width), (nbytes,) = q.shape, block_tables.shape, workspace.shape
         (groups,) = shared_blocks.shape
@@ -1006,7 +1011,9 @@ def decode_weights(q, cache: Cache, block_tables, context_lens, weights, workspa
     """pa_decode_weights: decode, and weights_out[s, kv head, t] = weights + the attention
     weight of token t in the KV head's Q heads.  `weights` fp32 [B, n_kv_heads, stride]
     is updated in place unless `weights_out` is given; None stands for zeros (weights_out
-    is then needed).  Returns (out, weights_out)."""
+    is then needed).  `context_lens` are read before the wait for the work ahead in the
+    stream, as decode_shared's.  The weights stand by batch row: a sequence that changes
+    its row takes them along.  Returns (out, weights_out)."""
     if weights_out is None:
         weights_out = weights
     try:
@@ -1048,8 +1055,9 @@ def kv_evict(cache: Cache, block_tables, context_lens, weights, budget, workspac
     """pa_kv_evict: every KV head keeps `budget` of a sequence's tokens, the first `sinks`,
     the last `recent` and those of the largest weights, K and V rows and weights [B,
     n_kv_heads, stride] moved to the first places.  Tables, lengths and weights are
-    worked on in place unless their `out` is given.  Returns (weights_out,
-    out_context_lens)."""
+    worked on in place unless their `out` is given.  One call is one layer's: with more
+    layers give `out_context_lens`, since every layer starts from the old lengths.
+    Returns (weights_out, out_context_lens)."""
     if out_block_tables is None:
         out_block_tables = block_tables
     if out_context_lens is None:

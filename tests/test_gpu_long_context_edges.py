@@ -175,3 +175,36 @@ def test_decodes_with_tables_far_wider_than_the_contexts():
     assert_attention_close(out, w.out())
     want, tol = w.want()
     assert (np.abs(got.cpu().numpy() - want) <= tol).all()
+
+
+# ------------------------------------------------------------------ layers
+
+@pytest.mark.parametrize("inplace", [True, False])
+def test_evict_every_layer_from_the_old_lengths(inplace):
+    """Layers one after another, each with its own weights, through one workspace; then
+    decode with weights over each, with the lengths that the last call wrote."""
+    L, H, Hk, d = 3, 8, 2, 64
+    b = EvictBatch(4, H, Hk, d, [500, 30, 129], layers=L)
+    rng = np.random.default_rng(5)
+    more = 7 * 3
+    b.pool = normal16(rng, 2, L, b.NB + more, 16, Hk, d)
+    to = b.bt if inplace else np.arange(b.NB, b.NB + more, dtype=np.int32).reshape(3, 7)
+    w = np.stack([rng.random(b.w.shape, dtype=np.float32) for _ in range(L)])
+    for s, n in enumerate(b.ctx):
+        w[:, s, :, n:] = 0
+    cache = pa.Cache(L, b.NB + more, Hk, d, tensor=dev(b.pool))
+    bt, tod, ctx, wd = dev(b.bt), dev(to), dev(b.ctx), dev(w)
+    new, ws, status = torch.zeros_like(ctx), pa.kv_evict_workspace(3, Hk, 100), pa.new_status()
+    for layer in range(L):
+        pa.kv_evict(cache, bt, ctx, wd[layer], 100, ws, sinks=4, recent=20, out_block_tables=tod,
+                    out_context_lens=new, layer=layer, status=status)
+    lens = [orc.evict(b.pool, layer, b.bt, b.ctx, w[layer], 100, 4, 20, to) for layer in range(L)][0]
+    assert int(status.item()) == 0 and new.tolist() == lens.tolist() == [100, 30, 100]
+    assert np.array_equal(wd.cpu().numpy(), w) and np.array_equal(bits(cache.tensor), bits(b.pool))
+    q = normal16(rng, 3, H, d)
+    for layer in range(L):
+        out, _ = pa.decode_weights(dev(q), cache, tod, new, wd[layer],
+                                   pa.decode_weights_workspace(3, H, Hk, d, 7 * 3), Hk, layer=layer,
+                                   status=status)
+        assert_attention_close(out, orc.attention_decode(q, b.pool, layer, to, lens, H, Hk))
+    assert int(status.item()) == 0
