@@ -196,7 +196,12 @@ __device__ __forceinline__ Record piece_of(float *records, int cta, int d, int h
 // of a KV head, else by each sequence with the rest of its context (a single
 // sequence has nothing to share).  Eight sequences over 128 shared tokens, 56
 // blocks: 9.9 us shared and 14.5 not with 4/2 heads of 64, 13.7 and 17.1 with 32/32
-// of 128; two over 256, 16 blocks, 64/8 of 128: 11.1 and 22.6.
+// of 128; two over 256, 16 blocks, 64/8 of 128: 11.1 and 22.6.  It holds for few groups
+// and large ones.  Of many small ones the fixed cost of a unit a group and KV head, which
+// the rule does not weigh, is more than they save: 64 sequences with up to 512 tokens of
+// their own, 32/8 heads of 128, in 32 groups over 128 tokens 30.2 us shared and 25.6 not,
+// over 256 30.6 and 27.1, over 1024 46.5 and 50.7; in 16 groups over 128 26.0 and 25.1,
+// over 256 27.2 and 28.5.
 constexpr int kMinSavedBlocks = 8;
 
 __device__ __forceinline__ int shared_of(int blocks, int members) {

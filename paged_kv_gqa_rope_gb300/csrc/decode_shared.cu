@@ -20,9 +20,9 @@
 //
 // Bound: HBM for up to 128 query rows a KV head (each key tile of 64 KB serves them
 // all: 32 sequences, 32/32 heads, 65536 tokens at 6.3 TB/s), the tensor cores above
-// (128 sequences, 64/8 heads, 65536 tokens at 1130 TFLOP/s; an issuing thread is held
-// 1370 cycles a job of 128 x 128 x 128 twice, at the 1.5 GHz that the power limit
-// leaves).  Serving batches of 8192 shared tokens are bound by latencies: about 4 us
+// (128 sequences, 64/8 heads, 65536 tokens at 1080 TFLOP/s, 5 % of the time the row sums'
+// operations beside the other stream's exponentials; an issuing thread is held 1370
+// cycles a job of 128 x 128 x 128 twice, at the 1.5 GHz that the power limit leaves).  Serving batches of 8192 shared tokens are bound by latencies: about 4 us
 // to the first tile, 2 a record, 3 for the join.
 #include <algorithm>
 #include <climits>
@@ -720,8 +720,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 // product, not the two of a value in two halves.  The row sum adds the
                 // rounded P, so that the output is an average of V by the weights that
                 // multiplied it, as pa_decode's; it does so once the tile's P is given
-                // away, beside the product (64/8 heads, 8192 shared tokens: 25.7 us; ahead
-                // of that 25.8, of P before its rounding 25.3).
+                // away, beside the product (64/8 heads, 32 sequences over 8192 shared tokens:
+                // 25.6 us, 128 over 65536: 254; summed ahead of that 25.7 and 257, P before
+                // its rounding 25.4 and 243).
                 uint32_t p[4][16];
                 auto exps = [&](const uint32_t (&s)[32], int c, uint32_t (&p)[16]) {
 #pragma unroll

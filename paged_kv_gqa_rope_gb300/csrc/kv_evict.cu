@@ -25,7 +25,10 @@
 //           read: a CTA loads a round of moves, waits for all of its threads, and
 //           stores them; the next round's loads are issued ahead of the stores.
 //           Columns are independent of each other, so slices need no order between
-//           them.  Into other blocks no order is needed at all, and the rounds of a
+//           them.  The order costs a long list its parts (one of 32767 tokens cut to
+//           4096, 8 KV heads: 25.6 us in place, 20.4 into other blocks, both kernels, in
+//           a graph) and many lists nothing (32 x 8 of 1000 to 5000 cut to 1024: 54.8
+//           and 55.4).  Into other blocks no order is needed at all, and the rounds of a
 //           list are dealt out to several CTAs.
 //
 // Bound: HBM, 8 d bytes a kept (token, KV head) that moves; for single sequences

@@ -42,7 +42,7 @@ struct LayoutArgs {
 
 // Rows are read once, with the evict-first policy; batches that write more than
 // this (half of L2) also store with it, since nobody finds their rows in L2 anyway
-// (16 prompts, 64/8 heads, 352 MB: 55.7 us, 94 % of the copy bandwidth, against 61.7
+// (16 prompts, 64/8 heads, 352 MB: 54.6 us, 96 % of the copy bandwidth, against 61.7
 // with the policy on neither side and 62 with it on one).  Smaller ones leave Q, K
 // and V where the attention that follows reads them.
 constexpr int64_t kStreamBytes = 64 << 20;
