@@ -308,11 +308,18 @@ __device__ __forceinline__ Record first_record(const Pieces &p, const DecodeArgs
     return {p.rec, (int64_t)a.B * a.H, ((int64_t)kvh * a.B + s) * a.g + h};
 }
 
+// Two fp16 values, infinite ones brought to the end of the range.
+__device__ __forceinline__ uint32_t finite2(uint32_t x) {
+    const __half2 top = __half2half2(__ushort_as_half(0x7bff));
+    const __half2 y = __hmax2(__hmin2(*reinterpret_cast<const __half2 *>(&x), top), __hneg2(top));
+    return *reinterpret_cast<const uint32_t *>(&y);
+}
+
 // One element (head h of the pair, value d) of a finished pair: O unnormalised,
-// M the maximum, L the sum of the row, W that before P's rounding (kScores).
+// M the maximum, L the sum of the row.
 template <int D, Mode MODE>
 __device__ __forceinline__ void emit(const DecodeArgs &a, int s, int kvh, int h, int d, float O,
-                                     float M, float L, float W = 0.f) {
+                                     float M, float L) {
     const int64_t row = (int64_t)s * a.H + kvh * a.g + h;
     if constexpr (MODE == Mode::kOut) {
         a.out[row * D + d] = __float2half_rn(L > 0.f ? O / L : 0.f);
@@ -320,7 +327,7 @@ __device__ __forceinline__ void emit(const DecodeArgs &a, int s, int kvh, int h,
         const bool none = L == 0.f;
         a.out[row * D + d] = __float2half_rn(none ? 0.f : saturate16(O / L));
         if (MODE == Mode::kScores && d == 0)
-            a.sc.stats[row] = none ? make_float2(0.f, 0.f) : make_float2(M - kPShift, 1.f / W);
+            a.sc.stats[row] = none ? make_float2(0.f, 0.f) : make_float2(M - kPShift, 1.f / L);
     }
 }
 
@@ -420,8 +427,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
     float *sm_m = sm_o + kConsumerWarps * kGroupPad * D;           // [4][8]
     float *sm_l = sm_m + kConsumerWarps * kGroupPad;               // [4][8]
     float *sm_pm = sm_l + kConsumerWarps * kGroupPad;              // [4][8] pieces' (max,
-    float *sm_pl = sm_pm + kConsumerWarps * kGroupPad;             // [4][8]  sum) per head;
-                                                                   // kScores: warps' sums
+    float *sm_pl = sm_pm + kConsumerWarps * kGroupPad;             // [4][8]  sum) per head
     int *sm_flag = reinterpret_cast<int *>(sm_pl + kConsumerWarps * kGroupPad);  // [4]
     int64_t *prefix = reinterpret_cast<int64_t *>(sm_flag + 4);    // [B + 1]
     constexpr bool kOut = MODE == Mode::kOut;
@@ -660,7 +666,6 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
             }
         }
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-        [[maybe_unused]] float w0 = 0.f, w1 = 0.f;  // kScores: the sums before P's rounding
         float o[D / 16][4];
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
@@ -850,11 +855,17 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                     const float al0 = ex2(m0 - mn0), al1 = ex2(m1 - mn1);
                     m0 = mn0;
                     m1 = mn1;
-                    // P is rounded to fp16, by 2^-11 of a value at most, for one MMA
-                    // instead of the two of a value in two halves.  The row sum adds
-                    // the rounded P, so that the output is an average of V by the
-                    // weights that multiplied it.
+                    // P is rounded to fp16, by 2^-11 of a value at most, and the row
+                    // sum adds the rounded P, so that the output is an average of V
+                    // by the weights that multiplied it.  kScores multiplies what the
+                    // rounding leaves (to 2^-22) as well, in a second MMA for which
+                    // the time is there (64/8 heads, 32 x 4097 tokens: 93.1 us with
+                    // and without; errors against 64 bits 2.1e-4, the output's own
+                    // rounding, and 2.6e-4), so that output and weights go by the same
+                    // fp32 sum.  kTails, beside the tensor cores' prefix, does not
+                    // (32/32 heads: 31.4 us, with it 32.2).
                     __half2 p01, p23;
+                    [[maybe_unused]] __half2 q01, q23;
                     if constexpr (kOut) {
                         p01 = __floats2half2_rn(ex2(x0 - mn0), ex2(x1 - mn1));
                         p23 = __floats2half2_rn(ex2(x2 - mn0), ex2(x3 - mn1));
@@ -864,10 +875,10 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                         p01 = __floats2half2_rn(e0, e1);
                         p23 = __floats2half2_rn(e2, e3);
                         if constexpr (MODE == Mode::kScores) {
-                            // a weight is divided by the sum before the rounding: it
-                            // comes from its own fp32 score, not from P
-                            w0 = w0 * al0 + (e0 + e2);
-                            w1 = w1 * al1 + (e1 + e3);
+                            l0 = l0 * al0 + (e0 + e2);
+                            l1 = l1 * al1 + (e1 + e3);
+                            q01 = __floats2half2_rn(e0 - __low2float(p01), e1 - __high2float(p01));
+                            q23 = __floats2half2_rn(e2 - __low2float(p23), e3 - __high2float(p23));
                         }
                     }
                     if constexpr (kOut) {
@@ -876,7 +887,13 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                     }
                     const uint32_t pb0 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&p01));
                     const uint32_t pb1 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&p23));
-                    if constexpr (!kOut) {  // a product with ones: P's columns are the rows
+                    [[maybe_unused]] uint32_t qb0 = 0, qb1 = 0;
+                    if constexpr (MODE == Mode::kScores) {
+                        qb0 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&q01));
+                        qb1 = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&q23));
+                    }
+                    if constexpr (MODE == Mode::kTails) {
+                        // (a product with ones: P's columns are the rows)
                         const uint32_t one = 0x3c003c00u, ones[4] = {one, one, one, one};
                         float ls[4] = {l0 * al0, l1 * al1, 0.f, 0.f};
                         mma_16816(ls, ones, pb0, pb1);
@@ -908,6 +925,13 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                         af[2] &= keep89;
                         af[3] &= keep89;
                         mma_16816(o[mt], af, pb0, pb1);
+                        if constexpr (MODE == Mode::kScores) {
+                            // (an infinite V is the first product's alone: times a rest
+                            // of 0 or of the other sign it would be NaN)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) af[i] = finite2(af[i]);
+                            mma_16816(o[mt], af, qb0, qb1);
+                        }
                     }
                 }
                 __syncwarp();
@@ -925,20 +949,12 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
 
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
-            if constexpr (kOut) {  // (else every lane has them)
+            if constexpr (MODE != Mode::kTails) {  // (there every lane has them)
                 l0 += __shfl_xor_sync(0xffffffffu, l0, off);
                 l1 += __shfl_xor_sync(0xffffffffu, l1, off);
             }
-            if constexpr (MODE == Mode::kScores) {
-                w0 += __shfl_xor_sync(0xffffffffu, w0, off);
-                w1 += __shfl_xor_sync(0xffffffffu, w1, off);
-            }
         }
         if (lane < 4) {
-            if constexpr (MODE == Mode::kScores) {
-                sm_pl[warp * kGroupPad + h0] = w0;
-                sm_pl[warp * kGroupPad + h0 + 1] = w1;
-            }
             sm_m[warp * kGroupPad + h0] = m0;
             sm_m[warp * kGroupPad + h0 + 1] = m1;
             sm_l[warp * kGroupPad + h0] = l0;
@@ -989,16 +1005,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
         }
         named_barrier_sync(1, kCons);
         abort = sm_flag[1] != 0;
-        if (tid < a.g) {
-            merge_factors(sm_m, sm_l, tid, kConsumerWarps);
-            if constexpr (MODE == Mode::kScores) {  // (sm_m: the factors)
-                float W = 0.f;
-#pragma unroll
-                for (int wv = 0; wv < kConsumerWarps; ++wv)
-                    W = __fmaf_rn(sm_m[wv * kGroupPad + tid], sm_pl[wv * kGroupPad + tid], W);
-                sm_pl[tid] = W;
-            }
-        }
+        if (tid < a.g) merge_factors(sm_m, sm_l, tid, kConsumerWarps);
         if (tid == 0) sm_flag[2] = may_close && arrived == nrec - 1;
         named_barrier_sync(1, kCons);
         const bool close = sm_flag[2] != 0;
@@ -1026,11 +1033,8 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
                     O.w = __fmaf_rn(f, x.w, O.w);
                 }
                 *r.cols(d / 4) = O;
-                if (d == 0) {
-                    const float m = sm_l[kGroupPad + h] - kPShift;
-                    *r.stat(D) = make_float2(m, sm_l[h]);
-                    if constexpr (MODE == Mode::kScores) *r.stat(D, true) = make_float2(m, sm_pl[h]);
-                }
+                if (d == 0)
+                    *r.stat(D) = make_float2(sm_l[kGroupPad + h] - kPShift, sm_l[h]);
             }
             named_barrier_sync(1, kCons);  // the smem merge area is free again
         } else if (whole) {
@@ -1040,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
 #pragma unroll
                 for (int wv = 0; wv < kConsumerWarps; ++wv)
                     O = __fmaf_rn(sm_m[wv * kGroupPad + h], sm_o[(wv * kGroupPad + h) * D + d], O);
-                emit<D, MODE>(a, s, kvh, h, d, O, sm_l[kGroupPad + h], sm_l[h], sm_pl[h]);
+                emit<D, MODE>(a, s, kvh, h, d, O, sm_l[kGroupPad + h], sm_l[h]);
             }
             named_barrier_sync(1, kCons);  // the smem merge area is free again
         } else if constexpr (kOut) {

@@ -58,17 +58,16 @@ struct alignas(16) PlanHead {
 };
 
 // Records of rows, with four columns of all of them side by side ([D / 4][rows][4],
-// then {m, l}[rows], {m, w}[rows]): neither the threads that write them, one a row, nor
-// those that read them leave a line half used.
+// then {m, l}[rows]): neither the threads that write them, one a row, nor those that
+// read them leave a line half used.
 struct Record {
     float *base;
     int64_t rows, row;
     __device__ __forceinline__ float4 *cols(int i) const {  // columns 4 i .. 4 i + 3
         return reinterpret_cast<float4 *>(base) + i * rows + row;
     }
-    // (w, of pa_decode_weights: l before P's rounding)
-    __device__ __forceinline__ float2 *stat(int d, bool w = false) const {
-        return reinterpret_cast<float2 *>(base + (d + (w ? 2 : 0)) * rows) + row;
+    __device__ __forceinline__ float2 *stat(int d) const {
+        return reinterpret_cast<float2 *>(base + d * rows) + row;
     }
 };
 
@@ -95,7 +94,7 @@ struct alignas(16) SeqScores {
 struct DecodeScores {
     Pieces pieces;
     float *scores;     // [blocks of all KV heads][16 tokens][g]: log2 units
-    float2 *stats;     // [B][H]: {m, 1 / w}, a weight being 2^(score - m) / w
+    float2 *stats;     // [B][H]: {m, 1 / l}, a weight being 2^(score - m) / l
     SeqScores *seqs;   // [B]
     int64_t capacity;  // blocks of all KV heads that scores holds
     int max_len;       // longest context that the rows of weights hold

@@ -1,15 +1,13 @@
 // Decode that accumulates attention weights (pa_decode_weights).
 //
 // With x[h][t] the scaled score of Q head h and token t in log2 units,
-//     out[h]  = sum_t p[h][t] v[t],   p[h][t] = 2^(x[h][t] - m_h) / w_h,
+//     out[h]  = sum_t p[h][t] v[t],   p[h][t] = 2^(x[h][t] - m_h) / l_h,
 //     weights_out[kv head][t] = weights[kv head][t] + sum over its Q heads of p[h][t].
 // A token's p is known only once its row's last token has been seen, so the
 // decode kernel leaves the scores (fp32, 4 g bytes a (token, KV head), against
-// 4 d for its K and V row) and each row's m and 1/w behind; this kernel turns
+// 4 d for its K and V row) and each row's m and 1/l behind; this kernel turns
 // them into weights, and joins the outputs of the pairs (sequence, KV head) that the
-// decode kernel's CTAs have left in pieces.  (In the output P is fp16, and so is what
-// its sum l adds; w adds the same values before their rounding.)  Reading K a second
-// time instead would cost 2 d bytes.
+// decode kernel's CTAs have left in pieces.  Reading K a second time instead would cost 2 d bytes.
 //
 // Bound: L2 and HBM, 4 g + 8 bytes a (token, KV head).
 #include <algorithm>
@@ -72,8 +70,7 @@ __global__ void __launch_bounds__(kWeightThreads, 8) weights_kernel(const Weight
                 float M = -INFINITY, L = 0.f;
 #pragma unroll
                 for (int i = 0; i < kFewPieces; ++i)
-                    ml[i] = i <= cut.more ? *piece(i, tid).stat(a.d, true)
-                                          : make_float2(-INFINITY, 0.f);
+                    ml[i] = i <= cut.more ? *piece(i, tid).stat(a.d) : make_float2(-INFINITY, 0.f);
 #pragma unroll
                 for (int i = 0; i < kFewPieces; ++i) M = fmaxf(M, ml[i].x);
 #pragma unroll
@@ -89,7 +86,7 @@ __global__ void __launch_bounds__(kWeightThreads, 8) weights_kernel(const Weight
             for (int j = tid / 32; j < G; j += kWeightThreads / 32) {
                 float M = -INFINITY, L = 0.f;
                 for (int i0 = 0; i0 <= cut.more; i0 += 32) {
-                    const float2 ml = i0 + lane <= cut.more ? *piece(i0 + lane, j).stat(a.d, true)
+                    const float2 ml = i0 + lane <= cut.more ? *piece(i0 + lane, j).stat(a.d)
                                                             : make_float2(-INFINITY, 0.f);
                     float top = ml.x;
 #pragma unroll
@@ -167,15 +164,12 @@ __global__ void __launch_bounds__(kWeightThreads, 8) weights_kernel(const Weight
             }
         }
     }
-    // The output, divided by l.  (Added up here, where few CTAs come: every CTA's
-    // read_stats would spill registers for it, weights_gqa +1.8 us.)  The last CTA has the
-    // fewest tokens.
+    // (the last CTA has the fewest tokens)
     if (cut.more == 0 || blockIdx.x != gridDim.x - 1) return;
     if (!known) read_stats();
     for (int i0 = threadIdx.x; i0 < G * (a.d / 4); i0 += kWeightThreads) {
         const int j = i0 / (a.d / 4), c = i0 - j * (a.d / 4);
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        float L = 0.f;
         auto add = [&](float f, const float4 &O) {
             y.x = fmaf(f, O.x, y.x);
             y.y = fmaf(f, O.y, y.y);
@@ -184,28 +178,20 @@ __global__ void __launch_bounds__(kWeightThreads, 8) weights_kernel(const Weight
         };
         if (cut.more < kFewPieces) {
             float4 O[kFewPieces];
-            float l[kFewPieces];
 #pragma unroll
-            for (int i = 0; i < kFewPieces; ++i) {
+            for (int i = 0; i < kFewPieces; ++i)
                 O[i] = i <= cut.more ? *piece(i, j).cols(c) : make_float4(0.f, 0.f, 0.f, 0.f);
-                l[i] = i <= cut.more ? piece(i, j).stat(a.d)->y : 0.f;
-            }
 #pragma unroll
-            for (int i = 0; i < kFewPieces; ++i) {
-                add(factors[i][j], O[i]);
-                L = fmaf(factors[i][j], l[i], L);
-            }
+            for (int i = 0; i < kFewPieces; ++i) add(factors[i][j], O[i]);
         } else {
             const float M = stats[j].x;
 #pragma unroll 8
             for (int i = 0; i <= cut.more; ++i) {
-                const float2 ml = *piece(i, j).stat(a.d);
-                const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-                add(f, *piece(i, j).cols(c));
-                L = fmaf(f, ml.y, L);
+                const float m = piece(i, j).stat(a.d)->x;
+                add(m == -INFINITY ? 0.f : ex2(m - M), *piece(i, j).cols(c));
             }
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;  // (no block in range: 0)
+        const float inv = stats[j].y;
         *reinterpret_cast<uint2 *>(a.out + ((int64_t)s * a.H + h * G + j) * a.d + 4 * c) =
             make_uint2(pack_half2(saturate16(y.x * inv), saturate16(y.y * inv)),
                        pack_half2(saturate16(y.z * inv), saturate16(y.w * inv)));

@@ -10,7 +10,7 @@ import torch
 
 from oracle import reference as orc
 from paged_kv_gqa_rope_gb300 import pa
-from tests.gpu_helpers import assert_attention_close, bits
+from tests.gpu_helpers import assert_attention_close, bits, half_ulp16
 from tests.test_gpu_long_context import (SHARED, EvictBatch, SharedBatch, WeightBatch, dev, ints,
                                          normal16)
 
@@ -24,8 +24,9 @@ def _lib(libpa):
     return libpa
 
 
-# An average of equal values is the value.  P is fp16 in the product with V, so that
-# holds only if the sum that it is divided by adds the same fp16 values.  Here one key of
+# An average of equal values is the value.  P is fp16 in the product with V (of the
+# shared prefixes), so that holds only if the sum that it is divided by adds the same fp16
+# values.  Here one key of
 # score 0 stands beside keys whose P is 0.9 of half a step above a power of two: each loses
 # 0.9 * 2^-11 of itself to its rounding, while the values, 2047 / 1024 by powers of two,
 # have a half step of 2^-12 of themselves.  Beside that rounding stand fp32 ones alone: a row
@@ -73,6 +74,42 @@ def test_weights_give_equal_values_back(H, Hk, d, lens):
         w = np.full(n, g * p / (1 + p * (n - 1)))
         w[0] = g / (1 + p * (n - 1))
         assert np.abs(got[s, :, :n] / w - 1).max() <= 2.0 ** -17
+
+
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+def test_infinite_values_stay_in_their_columns(value):
+    """An infinite V of one token makes its column infinite, whatever P's rounding leaves for
+    a second product; a NaN makes it NaN.  The other columns and heads are as before."""
+    lens = [300, 5, 64, 2000]
+    w = WeightBatch(9, 8, 2, 64, lens)
+    b = SharedBatch(9, 8, 2, 64, [(20, [3, 40, 1]), (0, [77])])
+    for x, run in ((w, lambda: w.run()[0]), (b, b.run)):
+        want = x.want() if x is b else x.out()
+        x.pool[1, 0, x.bt[0, 0], 0, 1, 7] = value  # the first sequence's, KV head 1, column 7
+        got = run().float().cpu().numpy()
+        hit = np.zeros(got.shape, bool)
+        hit[:3 if x is b else 1, 4:, 7] = True  # (a shared block's: all who share it)
+        assert np.isnan(got[hit]).all() if np.isnan(value) else (got[hit] == value).all()
+        got[hit] = want[hit] = 0
+        assert_attention_close(got.astype(np.float64), want)
+
+
+@pytest.mark.parametrize("H,Hk,d", [(8, 1, 128), (32, 4, 64), (6, 6, 128)])
+def test_weights_output_keeps_what_the_rounding_of_p_leaves(H, Hk, d):
+    """The first key's P is 1 and its V -(n - 1) / 2, the n - 1 others' P is 0.9 * 2^-11 of
+    itself above 1 / 2 and their V 1: what a single fp16 half keeps of P cancels."""
+    b = WeightBatch(11, H, Hk, d, [3, 65, 1001, 3001])
+    equal_values(b, 0)
+    b.pool[1] = np.where(np.isnan(b.pool[1]), b.pool[1], np.float16(1))
+    for s, n in enumerate(b.ctx):
+        b.pool[1, 0, b.bt[s, 0], 0] = -(n - 1) / 2
+    out = b.run(scale=SCALE)[0].double().cpu().numpy()
+    p = 2.0 ** -(SCALE * math.log2(math.e))
+    for s, n in enumerate(b.ctx):
+        want = np.full((H, d), (n - 1) * (p - 0.5) / (1 + (n - 1) * p))  # 2.2e-4 to 4.4e-4
+        # at most 47 blocks a warp, each cutting the sums of products of size n / 2 by 2^-22
+        # of them, which are divided by more than n / 2; an exponent's roundings, 2^-21 of P
+        assert (np.abs(out[s] - want) <= half_ulp16(want) + 50 * 2.0 ** -22).all()
 
 
 # ------------------------------------------------------------------ workspaces
