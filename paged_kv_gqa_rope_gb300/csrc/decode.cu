@@ -511,7 +511,8 @@ __global__ void __launch_bounds__(kThreads, I8 ? 4 : 2)
         if (cta == 0)
             for (int s = tid; s < B; s += kThreads)
                 a.sc.seqs[s] = {
-                    lens[s] == 0 ? -2 : scores_start<kCost>(a, prefix, lens, s, a.status), lens[s], 0};
+                    lens[s] == 0 ? -2 : scores_start<kCost>(a, prefix, lens, s, a.status),
+                    lens[s], 0};
     }
     // With fewer blocks than CTAs only the first W CTAs get a (one-block)
     // range, so that every range is non-empty and a pair cut into pieces

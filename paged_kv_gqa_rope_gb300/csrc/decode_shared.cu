@@ -22,8 +22,9 @@
 // all: 32 sequences, 32/32 heads, 65536 tokens at 6.3 TB/s), the tensor cores above
 // (128 sequences, 64/8 heads, 65536 tokens at 1080 TFLOP/s, 5 % of the time the row sums'
 // operations beside the other stream's exponentials; an issuing thread is held 1370
-// cycles a job of 128 x 128 x 128 twice, at the 1.5 GHz that the power limit leaves).  Serving batches of 8192 shared tokens are bound by latencies: about 4 us
-// to the first tile, 2 a record, 3 for the join.
+// cycles a job of 128 x 128 x 128 twice, at the 1.5 GHz that the power limit leaves).
+// Serving batches of 8192 shared tokens are bound by latencies: about 4 us to the first
+// tile, 2 a record, 3 for the join.
 #include <algorithm>
 #include <climits>
 #include <mutex>
@@ -965,7 +966,9 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr int kMaxGroups = 4096;
 constexpr int kMaxCtas = 160;  // (152 SMs)
 
-size_t rows_bytes(int B, int H, int D) { return up256((size_t)B * H * ((size_t)D + 4) * sizeof(float)); }
+size_t rows_bytes(int B, int H, int D) {
+    return up256((size_t)B * H * ((size_t)D + 4) * sizeof(float));
+}
 
 template <int D>
 int launch_join(const SharedArgs &a, cudaStream_t st) {

@@ -7,7 +7,8 @@
 // decode kernel leaves the scores (fp32, 4 g bytes a (token, KV head), against
 // 4 d for its K and V row) and each row's m and 1/l behind; this kernel turns
 // them into weights, and joins the outputs of the pairs (sequence, KV head) that the
-// decode kernel's CTAs have left in pieces.  Reading K a second time instead would cost 2 d bytes.
+// decode kernel's CTAs have left in pieces.  Reading K a second time instead would cost
+// 2 d bytes.
 //
 // Bound: L2 and HBM, 4 g + 8 bytes a (token, KV head).
 #include <algorithm>
@@ -200,9 +201,11 @@ __global__ void __launch_bounds__(kWeightThreads, 8) weights_kernel(const Weight
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Workspace: the decode kernel's, the statistics, each sequence's first block, the cut
+// Workspace: the decode kernel's, the statistics, the sequences' places and lengths, the cut
 // pairs, their first pieces, scores.
-size_t record_bytes(int B, int H, int D) { return up256((size_t)B * H * ((size_t)D + 4) * sizeof(float)); }
+size_t record_bytes(int B, int H, int D) {
+    return up256((size_t)B * H * ((size_t)D + 4) * sizeof(float));
+}
 size_t fixed_bytes(int B, int H, int Hk, int D) {
     return up256(mode_workspace_bytes(D)) + up256((size_t)B * H * sizeof(float2)) +
            up256((size_t)B * sizeof(SeqScores)) + up256((size_t)B * Hk * sizeof(int32_t)) +
