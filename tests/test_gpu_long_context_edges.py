@@ -245,3 +245,79 @@ def test_evict_every_layer_from_the_old_lengths(inplace):
                                    status=status)
         assert_attention_close(out, orc.attention_decode(q, b.pool, layer, to, lens, H, Hk))
     assert int(status.item()) == 0
+
+
+# ------------------------------------------------------------------ largest sizes
+
+@pytest.mark.parametrize("half", [False, True])
+def test_append_of_more_tokens_than_a_grid_has_rows(half):
+    """70000 tokens: past 65535, and past what is stored to stay in L2."""
+    T, H, Hk, d, rotary = 70000, 4, 2, 128, 96
+    rng = np.random.default_rng(6)
+    q, k, v = (normal16(rng, 64, n, d) for n in (H, Hk, Hk))
+    pos = rng.integers(0, 500, T).astype(np.int32)
+    table = orc.rope_scaled_table(500, rotary)
+    pick = np.arange(T) % 64  # (rows again and again, at other positions)
+    NB = T // 16 + 2
+    slots = rng.permutation(NB * 16)[:T].astype(np.int32)
+    cache, status = pa.Cache(1, NB, Hk, d), pa.new_status()
+    cache.tensor.zero_()
+    out = pa.rope_kv_write_layout(dev(q[pick]), dev(k[pick]), dev(v[pick]), dev(pos), dev(slots),
+                                  dev(table), cache, "half" if half else "interleaved",
+                                  status=status)
+    assert int(status.item()) == 0
+    assert np.array_equal(bits(out), bits(orc.rope_layout_pinned(q[pick], pos, table, half)))
+    pool = np.zeros((2, 1, NB, 16, Hk, d), np.float16)
+    orc.kv_write(pool, 0, orc.rope_layout_pinned(k[pick], pos, table, half), v[pick], slots)
+    assert np.array_equal(bits(cache.tensor), bits(pool))
+
+
+def test_a_line_of_more_places_than_32_bits_plan():
+    """4096 KV heads over 32768 shared tokens: 2.1 million places, which the plan divides in
+    64 bits; against pa_decode, whose own rounding of P stands beside."""
+    H, d, pre, B = 4096, 64, 2048, 2
+    cache = pa.Cache(1, pre + 2 * B, H, d)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    for part in cache.tensor.view(-1).split(2**30):
+        part.normal_(generator=gen)
+    bt = torch.arange(pre + 2, dtype=torch.int32).repeat(B, 1)
+    bt[1, pre:] += 2
+    ctx = ints([16 * pre + 9, 16 * pre + 32])
+    q = torch.randn(B, H, d, device="cuda", generator=gen).half()
+    status = pa.new_status()
+    out = pa.decode_shared(q, cache, bt.cuda(), ctx, ints([0, B]), ints([pre]),
+                           pa.decode_shared_workspace(B, H, H, d), H, status=status)
+    want = pa.decode(q, cache, bt.cuda(), ctx, pa.decode_workspace(B, H, H, d), H)
+    assert int(status.item()) == 0
+    # (each within the library's 1e-3 of the exact output)
+    assert torch.linalg.norm(out.float() - want.float()) <= 2e-3 * torch.linalg.norm(want.float())
+    assert (out.float() - want.float()).abs().max() <= 2e-3
+
+
+def test_most_kv_heads():
+    """65535 KV heads, as many as a grid has rows: weights and an eviction by them."""
+    H, d, n, budget = 65535, 64, 20, 10
+    cache = pa.Cache(1, 2, H, d)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    cache.tensor.normal_(generator=gen)
+    before = cache.tensor.clone()
+    bt, ctx = ints([[1, 0]]), ints([n])
+    q = torch.randn(1, H, d, device="cuda", generator=gen).half()
+    w = torch.zeros(1, H, 32, device="cuda")
+    status = pa.new_status()
+    out, _ = pa.decode_weights(q, cache, bt, ctx, w, pa.decode_weights_workspace(1, H, H, d, 2), H,
+                               status=status)
+    K, V = (before[i, 0, [1, 0]].reshape(32, H, d)[:n].float() for i in range(2))
+    p = torch.softmax(torch.einsum("hd,thd->ht", q[0].float(), K) / d ** 0.5, -1)
+    assert int(status.item()) == 0
+    assert (w[0, :, :n] - p).abs().max() <= 1e-5 and not w[..., n:].any()
+    want = torch.einsum("ht,thd->hd", p, V)
+    assert (out[0].float() - want).abs().max() <= 2e-3
+    kept = w[0, :, :n].topk(budget).indices.sort().values.T  # [budget, H]
+    old = w.clone()
+    pa.kv_evict(cache, bt, ctx, w, budget, pa.kv_evict_workspace(1, H, budget), status=status)
+    assert int(status.item()) == 0 and ctx.tolist() == [budget]
+    for i, rows in enumerate((K, V)):
+        got = cache.tensor[i, 0, 1, :budget].float()
+        assert torch.equal(got, rows.gather(0, kept[..., None].expand(-1, -1, d)))
+    assert torch.equal(w[0, :, :budget], old[0].gather(1, kept.T)) and not w[..., budget:].any()
